@@ -8,6 +8,7 @@ the shared library is missing or CUDA is unavailable, the calls raise.
 
 Entry points (same names as the C ABI, without the ``exl3_`` prefix):
   rotate, encode_tiles, decode_tiles, mse, quantize, gss_scale
+  linear, linear_backward, expert_linear (products with coded matrices)
 plus the workspace queries.
 """
 from __future__ import annotations
@@ -21,11 +22,14 @@ __all__ = [
     "encode_rows", "decode_rows",
     "quantize", "gss_scale", "scale_search", "scale_search_workspace_bytes", "encode_workspace_bytes", "encode_workspace_min_bytes",
     "quantize_workspace_bytes", "gss_workspace_bytes", "mse_workspace_bytes",
-    "supports_k", "rotate_last_kernel", "profile_enable", "profile_read", "wait_timeouts", "EXL3_F32", "EXL3_BF16",
+    "linear", "linear_backward", "expert_linear", "linear_workspace_bytes",
+    "linear_backward_workspace_bytes", "expert_linear_workspace_bytes",
+    "supports_k", "rotate_last_kernel", "profile_enable", "profile_read", "wait_timeouts", "EXL3_F32", "EXL3_BF16", "EXL3_F16",
 ]
 
 EXL3_F32 = 0
 EXL3_BF16 = 1
+EXL3_F16 = 2
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libexl3.so")
@@ -98,7 +102,19 @@ def lib():
         L.exl3_wait_timeouts.argtypes = [P]
         L.exl3_rotate_last_kernel.argtypes = []
         L.exl3_rotate_last_kernel.restype = i32
-        for name in ("exl3_regularize", "exl3_block_ldl", "exl3_ldlq", "exl3_scale_search", "exl3_encode_rows", "exl3_decode_rows", "exl3_profile_read", "exl3_wait_timeouts", "exl3_rotate", "exl3_encode_tiles", "exl3_decode_tiles", "exl3_mse",
+        L.exl3_linear_workspace_bytes.argtypes = [i64, i64, i64, i32, i32, i32]
+        L.exl3_linear_workspace_bytes.restype = sz
+        L.exl3_linear.argtypes = [P, i32, i64, i64, P, i64, i64, i32, P, P, P, i32, P, P, P, P, P,
+                                  i32, i32, P, i64, P, sz, P]
+        L.exl3_linear_backward_workspace_bytes.argtypes = [i64, i64, i64, i32, i32, i32]
+        L.exl3_linear_backward_workspace_bytes.restype = sz
+        L.exl3_linear_backward.argtypes = [P, i64, P, i64, i32, i64, P, i64, i64, i32, P, P, P, i32,
+                                           P, P, P, P, P, i32, i32, P, i64, P, P, P, sz, P]
+        L.exl3_expert_linear_workspace_bytes.argtypes = [i64, i64, i64, i32]
+        L.exl3_expert_linear_workspace_bytes.restype = sz
+        L.exl3_expert_linear.argtypes = [P, i32, i64, i64, P, i32, P, i64, i64, i32, P, P, P, i32,
+                                         P, i64, P, sz, P]
+        for name in ("exl3_linear", "exl3_linear_backward", "exl3_expert_linear", "exl3_regularize", "exl3_block_ldl", "exl3_ldlq", "exl3_scale_search", "exl3_encode_rows", "exl3_decode_rows", "exl3_profile_read", "exl3_wait_timeouts", "exl3_rotate", "exl3_encode_tiles", "exl3_decode_tiles", "exl3_mse",
                      "exl3_quantize", "exl3_gss_scale"):
             getattr(L, name).restype = i32
         _lib = L
@@ -426,3 +442,17 @@ def gss_scale(W, su, sv, K: int, lo: float = 0.5, hi: float = 2.0, n_eval: int =
                                 _ptr(best_codes), _ptr(scale), _ptr(g), _ptr(m), _ptr(hist),
                                 _ptr(ws), ws.numel() * ws.element_size(), _stream(dev)))
     return dict(codes=best_codes, scale=scale, g=g, mse=m, history=hist)
+
+
+_PRODUCTS = ("linear", "linear_backward", "expert_linear", "linear_workspace_bytes",
+             "linear_backward_workspace_bytes", "expert_linear_workspace_bytes")
+
+
+def __getattr__(name):
+    """The products with coded matrices load with their first use: they need torch
+    at import, which the rest of the package takes only when it is called."""
+    if name in _PRODUCTS:
+        from . import products
+        value = globals()[name] = getattr(products, name)
+        return value
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

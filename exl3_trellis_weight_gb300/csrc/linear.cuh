@@ -1,0 +1,141 @@
+// linear.cuh -- launch parameters shared by the kernels that multiply by
+// trellis-coded matrices (linear_act.cu, linear_product.cu, linear_adapt.cu)
+// and their entry points (linear_abi.cu).
+//
+// With V the codebook levels of a coded matrix, H the blockwise Sylvester
+// matrix and s its scale, the decoded matrix is
+//     W^ = 2^-7 s diag(su) (H V H) diag(sv),
+// so a product with it needs no decoded weights in memory:
+//     x W^   = ((x . su) H) V   H . sv . 2^-7 s
+//     x W^^T = ((x . sv) H) V^T H . su . 2^-7 s.
+// linear_act.cu makes z = (x . left) H once per token, linear_product.cu
+// multiplies by V straight from the codes and rotates the result.
+#pragma once
+
+#include "common.cuh"
+
+namespace exl3 {
+
+constexpr int kMaxExperts = 1024;
+constexpr int kMaxAdapters = 1024;
+constexpr int kMaxRank = 128;
+
+// Rotated activations z in binary16, in the order the product kernel loads
+// them: for each block of 64 inputs, NP token rows of 128 bytes whose 16-byte
+// chunks c sit at c ^ (row & 7) (the 128-byte swizzle of a shared-memory
+// operand), so that any tile of token rows starting at a multiple of 8 is one
+// contiguous copy.  NP leaves 16 rows behind the last token: tiles are rounded
+// up to 16 tokens.
+__host__ __device__ inline int64_t act_rows(int64_t T) { return (T + 7) / 8 * 8 + 16; }
+__host__ __device__ inline int64_t act_offset(int64_t NP, int64_t t, int k) {
+    return ((int64_t)(k >> 6) * NP + t) * 128 + ((((k >> 3) & 7) ^ (int)(t & 7)) << 4) + (k & 7) * 2;
+}
+
+struct ActLaunch {
+    const void *x;            // [T, n] activations, row stride in elements
+    int dt;                   // EXL3_BF16 / EXL3_F16
+    int64_t T, stride;
+    int n;                    // inputs, a multiple of 128
+    const float *left;        // [E or 1][n]
+    const int32_t *offsets;   // [E + 1] or nullptr (one matrix)
+    int E;
+    unsigned char *image;     // act_rows(T) * n * 2 bytes
+    float *rscale;            // [T]: z = image * rscale
+    void *y;                  // rows outside of every expert are set to 0
+    int64_t y_stride;
+    int y_cols;
+};
+exl3_status launch_act(const ActLaunch &p, cudaStream_t s);
+
+struct ProductLaunch {
+    const unsigned char *image;
+    const float *rscale;
+    int64_t T;
+    const uint32_t *codes;    // [E][rows/16][cols/16][8 K]
+    int64_t rows, cols;
+    int K;
+    const float *right;       // [E or 1][outputs]
+    const float *scale;       // [E or 1]
+    int transposed;
+    const int32_t *offsets;   // [E + 1] or nullptr
+    int E;                    // 1 when offsets == nullptr
+    // adapters added in the epilogue: y_t += sum_j h[t][j] B[slot_t][j]
+    const void *B;            // nullable, [n_adapters][rank][outputs], dtype dt
+    const float *h;           // [T][rank]
+    const int32_t *slots;     // [T]
+    const int32_t *ranks;     // nullable, [n_adapters]
+    int n_adapters, rank;
+    void *y;
+    int dt;
+    int64_t y_stride;
+};
+exl3_status launch_product(const ProductLaunch &p, cudaStream_t s);
+
+// h[t][j] = gain_i sum_k M[i][j][k] x[t][k], i = slots[t], j < ranks[i] (0 otherwise)
+struct ShrinkLaunch {
+    const void *x;
+    int dt;
+    int64_t T, stride;
+    int n;
+    const void *M;            // [n_adapters][rank][n]
+    const float *gain;
+    const int32_t *slots, *ranks;
+    int n_adapters, rank;
+    float *h;                 // [T][rank]
+};
+exl3_status launch_shrink(const ShrinkLaunch &p, cudaStream_t s);
+
+// dM[i][j][k] = sum over tokens t of adapter i of h[t][j] x[t][k]
+struct OuterLaunch {
+    const float *h;
+    const void *x;
+    int dt;
+    int64_t T, stride;
+    int n;
+    const int32_t *slots, *ranks;
+    int n_adapters, rank;
+    void *dM;                 // [n_adapters][rank][n]
+};
+exl3_status launch_outer(const OuterLaunch &p, cudaStream_t s);
+
+template <typename T> __device__ __forceinline__ float to_f32(T v);
+template <> __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <> __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+template <typename T> __device__ __forceinline__ T from_f32(float v);
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32(float v) { return __float2bfloat16_rn(v); }
+template <> __device__ __forceinline__ __half from_f32(float v) { return __float2half_rn(v); }
+
+// two values of a packed pair
+template <typename T> __device__ __forceinline__ float2 unpack2(uint32_t w);
+template <> __device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+template <> __device__ __forceinline__ float2 unpack2<__half>(uint32_t w) {
+    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+template <typename T> __device__ __forceinline__ uint32_t pack2(float a, float b);
+template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// Expert of token t: the e with offsets[e] <= t < offsets[e + 1], or -1.
+// The offsets are expected to ascend; whatever they hold, the result is a
+// valid index or -1.
+__device__ __forceinline__ int expert_of(const int32_t *off, int E, int64_t t) {
+    int lo = 0, hi = E;                  // first e with off[e + 1] > t lies in [lo, hi]
+    while (lo < hi) {
+        const int m = (lo + hi) >> 1;
+        if (off[m + 1] > t)
+            hi = m;
+        else
+            lo = m + 1;
+    }
+    return lo < E && off[lo] <= t ? lo : -1;
+}
+
+}  // namespace exl3

@@ -1,0 +1,206 @@
+"""Products with trellis-coded matrices: one shared projection with the low-rank
+adapters of many requests (``linear``, ``linear_backward``) and products grouped
+by expert (``expert_linear``).  The same thin binding as the package's other
+entry points; a call that decodes a single token is a few microseconds of GPU
+work, so the checks here stay few and cheap."""
+from __future__ import annotations
+
+import torch
+
+from . import EXL3_BF16, EXL3_F16, Exl3Error, lib
+
+_DT = {torch.bfloat16: EXL3_BF16, torch.float16: EXL3_F16}
+_fn = None
+
+
+def _lib():
+    global _fn
+    if _fn is None:
+        _fn = lib()
+    return _fn
+
+
+def _fail(status: int):
+    L = _lib()
+    raise Exl3Error(status, f"{L.exl3_status_str(status).decode()}: {L.exl3_last_error().decode()}")
+
+
+def linear_workspace_bytes(T: int, rows: int, cols: int, transposed: bool = False, n_adapters: int = 0,
+                           rank: int = 0) -> int:
+    return int(_lib().exl3_linear_workspace_bytes(T, rows, cols, int(transposed), n_adapters, rank))
+
+
+def linear_backward_workspace_bytes(T: int, rows: int, cols: int, transposed: bool = False, n_adapters: int = 0,
+                                    rank: int = 0) -> int:
+    return int(_lib().exl3_linear_backward_workspace_bytes(T, rows, cols, int(transposed), n_adapters, rank))
+
+
+def expert_linear_workspace_bytes(T: int, rows: int, cols: int, transposed: bool = False) -> int:
+    return int(_lib().exl3_expert_linear_workspace_bytes(T, rows, cols, int(transposed)))
+
+
+def _activations(t, name, columns, device=None, like=None):
+    """Row stride of a [T, columns] tensor, in elements."""
+    if not t.is_cuda:
+        raise ValueError("all tensors must be CUDA tensors (no CPU fallback)")
+    if t.dim() != 2 or t.shape[1] != columns:
+        raise ValueError(f"{name} must be [tokens, {columns}], got {tuple(t.shape)}")
+    if t.dtype not in _DT:
+        raise ValueError(f"unsupported dtype {t.dtype} of {name} (bfloat16 or float16)")
+    if like is not None and (t.dtype != like.dtype or t.shape[0] != like.shape[0] or t.device != like.device):
+        raise ValueError(f"{name} must have the dtype, tokens and device of the activations")
+    if t.shape[0] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}'s columns must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else columns
+
+
+def _dense(t, name, dtype, shape, device):
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device} (no CPU fallback)")
+    if not t.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    return t.data_ptr()
+
+
+def _coded(codes, su, sv, K, scale, lead, device):
+    """Pointers of a coded matrix (or a stack of them) and its two sizes."""
+    if codes.dim() != len(lead) + 3:
+        raise ValueError(f"codes must have {len(lead) + 3} dimensions, got {tuple(codes.shape)}")
+    rows, cols = codes.shape[-3] * 16, codes.shape[-2] * 16
+    dt = codes.dtype
+    if dt is not torch.int16:
+        raise ValueError(f"codes must be int16, got {dt}")
+    c = _dense(codes, "codes", dt, (*lead, rows // 16, cols // 16, 16 * K), device)
+    if not isinstance(scale, torch.Tensor):
+        scale = torch.full(lead, float(scale), dtype=torch.float32, device=device)
+    u = _dense(su, "su", torch.float32, (*lead, rows), device)
+    v = _dense(sv, "sv", torch.float32, (*lead, cols), device)
+    # the scale's tensor is returned too: one made here must live until the launch
+    return rows, cols, c, u, v, _dense(scale, "scale", torch.float32, lead, device), scale
+
+
+_NO_ADAPTERS = (None, None, None, None, None, 0, 0)
+
+
+def _adapters(A, B, gain, slots, ranks, n_in, n_out, x):
+    if A is None:
+        if B is not None or gain is not None or slots is not None or ranks is not None:
+            raise ValueError("B, gain, slots and ranks need A")
+        return _NO_ADAPTERS
+    if B is None or gain is None or slots is None:
+        raise ValueError("A needs B, gain and slots")
+    dev = x.device
+    n, r = A.shape[0], A.shape[1]
+    return (_dense(A, "A", x.dtype, (n, r, n_in), dev), _dense(B, "B", x.dtype, (n, r, n_out), dev),
+            _dense(gain, "gain", torch.float32, (n,), dev),
+            _dense(slots, "slots", torch.int32, (x.shape[0],), dev),
+            None if ranks is None else _dense(ranks, "ranks", torch.int32, (n,), dev), n, r)
+
+
+def _ws(need, device, ws):
+    if ws is None:
+        return torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+    if not ws.is_cuda or not ws.is_contiguous():
+        raise ValueError("the workspace must be a contiguous CUDA tensor")
+    return ws
+
+
+def linear(x, codes, su, sv, K: int, scale, transposed: bool = False, A=None, B=None, gain=None, slots=None,
+           ranks=None, out=None, ws=None):
+    """exl3_linear: y = x W^ (transposed: x W^^T) for the matrix coded in ``codes``
+    [rows/16, cols/16, 16K], plus each token's low-rank adapter.
+
+    x [T, inputs] bfloat16 or float16 (rows may be strided); su [rows], sv [cols]
+    float32; scale a float32 device scalar (as ``quantize`` returns it) or a number.
+    A [n, r, inputs], B [n, r, outputs] of x's dtype, gain [n] float32, slots [T]
+    int32 (the adapter of each token; out of [0, n): none), ranks [n] int32 or None.
+    Returns y [T, outputs] of x's dtype."""
+    dev = x.device
+    rows, cols, pc, pu, pv, ps, _keep = _coded(codes, su, sv, K, scale, (), dev)
+    n_in, n_out = (cols, rows) if transposed else (rows, cols)
+    xs = _activations(x, "x", n_in)
+    T = x.shape[0]
+    pA, pB, pg, pslots, pranks, n, r = _adapters(A, B, gain, slots, ranks, n_in, n_out, x)
+    if out is None:
+        out = torch.empty(T, n_out, dtype=x.dtype, device=dev)
+        ys = n_out
+    else:
+        ys = _activations(out, "out", n_out, like=x)
+    L = _lib()
+    tr = 1 if transposed else 0
+    ws = _ws(L.exl3_linear_workspace_bytes(T, rows, cols, tr, n, r), dev, ws)
+    st = L.exl3_linear(x.data_ptr(), _DT[x.dtype], T, xs, pc, rows, cols, K, pu, pv, ps, tr, pA, pB, pg, pslots,
+                       pranks, n, r, out.data_ptr(), ys, ws.data_ptr(), ws.numel() * ws.element_size(),
+                       torch.cuda.current_stream(dev).cuda_stream)
+    if st:
+        _fail(st)
+    return out
+
+
+def linear_backward(dy, x, codes, su, sv, K: int, scale, transposed: bool = False, A=None, B=None, gain=None,
+                    slots=None, ranks=None, dx=None, ws=None):
+    """exl3_linear_backward: gradients of ``linear`` for dy [T, outputs], with the
+    arguments of the forward call.  Returns dict(dx, dA, dB) (dA, dB None without
+    adapters; x is then not needed and may be None)."""
+    dev = dy.device
+    rows, cols, pc, pu, pv, ps, _keep = _coded(codes, su, sv, K, scale, (), dev)
+    n_in, n_out = (cols, rows) if transposed else (rows, cols)
+    dys = _activations(dy, "dy", n_out)
+    T = dy.shape[0]
+    pA, pB, pg, pslots, pranks, n, r = _adapters(A, B, gain, slots, ranks, n_in, n_out, dy)
+    px, xs = None, n_in
+    if n:
+        if x is None:
+            raise ValueError("the adapters' gradients need x")
+        xs = _activations(x, "x", n_in, like=dy)
+        px = x.data_ptr()
+    dA = torch.empty_like(A) if n else None
+    dB = torch.empty_like(B) if n else None
+    if dx is None:
+        dx = torch.empty(T, n_in, dtype=dy.dtype, device=dev)
+        dxs = n_in
+    else:
+        dxs = _activations(dx, "dx", n_in, like=dy)
+    L = _lib()
+    tr = 1 if transposed else 0
+    ws = _ws(L.exl3_linear_backward_workspace_bytes(T, rows, cols, tr, n, r), dev, ws)
+    st = L.exl3_linear_backward(dy.data_ptr(), dys, px, xs, _DT[dy.dtype], T, pc, rows, cols, K, pu, pv, ps, tr, pA,
+                                pB, pg, pslots, pranks, n, r, dx.data_ptr(), dxs, dA.data_ptr() if n else None,
+                                dB.data_ptr() if n else None, ws.data_ptr(), ws.numel() * ws.element_size(),
+                                torch.cuda.current_stream(dev).cuda_stream)
+    if st:
+        _fail(st)
+    return dict(dx=dx, dA=dA, dB=dB)
+
+
+def expert_linear(x, offsets, codes, su, sv, K: int, scale, transposed: bool = False, out=None, ws=None):
+    """exl3_expert_linear: rows offsets[e]..offsets[e+1]-1 of x [T, inputs] times the
+    matrix of expert e, coded in codes [E, rows/16, cols/16, 16K] with su [E, rows],
+    sv [E, cols] and scale [E] (float32 tensors).  offsets: int32 [E + 1] on the
+    device, ascending; rows of no expert give 0.  The input gradient is the same
+    call with ``transposed`` flipped.  Returns y [T, outputs] of x's dtype."""
+    dev = x.device
+    if codes.dim() != 4:
+        raise ValueError(f"codes must be [experts, rows/16, cols/16, 16K], got {tuple(codes.shape)}")
+    E = codes.shape[0]
+    rows, cols, pc, pu, pv, ps, _keep = _coded(codes, su, sv, K, scale, (E,), dev)
+    n_in, n_out = (cols, rows) if transposed else (rows, cols)
+    xs = _activations(x, "x", n_in)
+    T = x.shape[0]
+    po = _dense(offsets, "offsets", torch.int32, (E + 1,), dev)
+    if out is None:
+        out = torch.empty(T, n_out, dtype=x.dtype, device=dev)
+        ys = n_out
+    else:
+        ys = _activations(out, "out", n_out, like=x)
+    L = _lib()
+    tr = 1 if transposed else 0
+    ws = _ws(L.exl3_expert_linear_workspace_bytes(T, rows, cols, tr), dev, ws)
+    st = L.exl3_expert_linear(x.data_ptr(), _DT[x.dtype], T, xs, po, E, pc, rows, cols, K, pu, pv, ps, tr,
+                              out.data_ptr(), ys, ws.data_ptr(), ws.numel() * ws.element_size(),
+                              torch.cuda.current_stream(dev).cuda_stream)
+    if st:
+        _fail(st)
+    return out

@@ -70,7 +70,9 @@ typedef enum {
     EXL3_ERR_NUMERIC = 6       /* the input has no factorisation (exl3_block_ldl) */
 } exl3_status;
 
-typedef enum { EXL3_F32 = 0, EXL3_BF16 = 1 } exl3_dtype;
+/* EXL3_F16 is a type of activations and adapters (exl3_linear and the entry
+ * points beside it); weights are EXL3_F32 or EXL3_BF16. */
+typedef enum { EXL3_F32 = 0, EXL3_BF16 = 1, EXL3_F16 = 2 } exl3_dtype;
 
 /* Static string for a status code (never NULL). */
 EXL3_API const char *exl3_status_str(int status);
@@ -368,6 +370,96 @@ EXL3_API exl3_status exl3_regularize(const void *W, int dt, int64_t rows, int64_
                                      const float *h, const float *sv, int apply_out,
                                      float *W_out, float *sv_out, double *info_out, void *ws,
                                      size_t ws_bytes, void *stream);
+
+/*
+ * Products with a trellis-coded matrix (no counterpart on the pages, which
+ * leave the use of the codes to another program).  W^ is the matrix that
+ * exl3_decode_tiles and the inverse exl3_rotate give for `codes`, `su`, `sv`
+ * and `scale`:  W^ = 2^-7 scale diag(su) (H V H) diag(sv), V the mul1 levels.
+ *   transposed = 0:  y = x W^     (x has `rows` columns, y has `cols`)
+ *   transposed = 1:  y = x W^^T   (x has `cols` columns, y has `rows`: a
+ *                                  weight stored [out, in])
+ * plus, for the low-rank adapter i = slots[t] of each token t (none when it is
+ * negative or >= n_adapters),
+ *   y_t += gain_i * sum_{j < ranks_i} (A_i[j] . x_t) B_i[j].
+ *   x (device) [T, inputs] of dtype dt (EXL3_BF16 or EXL3_F16), rows x_stride
+ *     elements apart; y (device) [T, outputs] of the same type, rows y_stride
+ *     apart; any 2-byte alignment (16-byte aligned rows are read and written
+ *     in wide accesses).  y overlaps neither x nor the workspace.  T >= 0.
+ *   codes (device, 16-byte aligned) uint16 [rows/16][cols/16][16 K]; su, sv
+ *     (device, 16-byte aligned) fp32, multiplied as given (they may carry
+ *     channel scales, a zero included); scale (device) one float.  rows, cols
+ *     multiples of 128 up to 65536; K in {1, 2, 3, 4}.
+ *   A (device, 16-byte aligned) [n_adapters, rank, inputs], B [n_adapters,
+ *     rank, outputs], dtype dt; gain (device) fp32 [n_adapters]; slots
+ *     (device) int32 [T]; ranks (device) int32 [n_adapters] or NULL (all of
+ *     them `rank`; values are clamped to [0, rank], rows behind them are not
+ *     read).  n_adapters in [0, 1024] (0: no adapters, the other arguments are
+ *     ignored), rank in [1, 128].
+ *   ws: exl3_linear_workspace_bytes(...); 0 for sizes that are not supported.
+ * Arithmetic: the activations are rotated in binary32 and rounded to binary16
+ * under an exact power-of-two scale for each row; products with the levels
+ * are summed in binary32 (tensor cores, in any order within a sum), rotated
+ * and scaled in binary32 and rounded to dt once, with the adapters added
+ * before.  Results are the same from run to run.  A row of x that holds an
+ * infinity or a NaN gives no numbers in its own row of y and touches no other.
+ */
+EXL3_API size_t exl3_linear_workspace_bytes(int64_t T, int64_t rows, int64_t cols, int transposed,
+                                            int n_adapters, int rank);
+EXL3_API exl3_status exl3_linear(const void *x, int dt, int64_t T, int64_t x_stride,
+                                 const uint16_t *codes, int64_t rows, int64_t cols, int K,
+                                 const float *su, const float *sv, const float *scale,
+                                 int transposed, const void *A, const void *B, const float *gain,
+                                 const int32_t *slots, const int32_t *ranks, int n_adapters,
+                                 int rank, void *y, int64_t y_stride, void *ws, size_t ws_bytes,
+                                 void *stream);
+
+/*
+ * Gradients of exl3_linear with respect to x, A and B (the codes are frozen;
+ * gain is a constant of the adapter).  With h_t = gain_i A_i x_t and
+ * g_t = gain_i B_i dy_t for i = slots[t]:
+ *   dx_t = dy_t W^^T + sum_j g_t[j] A_i[j]   (W^ for transposed = 1)
+ *   dA_i[j] = sum_{t of i} g_t[j] x_t,   dB_i[j] = sum_{t of i} h_t[j] dy_t,
+ * rows j >= ranks_i and adapters without tokens get 0.
+ *   dy (device) [T, outputs], x, dx [T, inputs] of dtype dt with row strides;
+ *   x, dA and dB are used only when n_adapters > 0 (dA, dB 16-byte aligned,
+ *   shapes and type of A and B).  dx overlaps neither dy, x nor ws.  The sums
+ *   over tokens are binary32 in a fixed order, rounded to dt once.  The other
+ *   arguments are those of exl3_linear.
+ */
+EXL3_API size_t exl3_linear_backward_workspace_bytes(int64_t T, int64_t rows, int64_t cols,
+                                                     int transposed, int n_adapters, int rank);
+EXL3_API exl3_status exl3_linear_backward(const void *dy, int64_t dy_stride, const void *x,
+                                          int64_t x_stride, int dt, int64_t T,
+                                          const uint16_t *codes, int64_t rows, int64_t cols, int K,
+                                          const float *su, const float *sv, const float *scale,
+                                          int transposed, const void *A, const void *B,
+                                          const float *gain, const int32_t *slots,
+                                          const int32_t *ranks, int n_adapters, int rank, void *dx,
+                                          int64_t dx_stride, void *dA, void *dB, void *ws,
+                                          size_t ws_bytes, void *stream);
+
+/*
+ * Products grouped by expert: rows offsets[e] .. offsets[e+1]-1 of x times the
+ * coded matrix of expert e (transposed as in exl3_linear; the gradient of x is
+ * the same call with the other transposition).
+ *   offsets (device) int32 [n_experts + 1], ascending, within [0, T]; experts
+ *     may be empty; rows of no expert (before offsets[0], from
+ *     offsets[n_experts] on) get 0.  Offsets that break this give unspecified
+ *     rows of y, but nothing out of bounds.  The host never reads them.
+ *   codes (device, 16-byte aligned) uint16 [n_experts][rows/16][cols/16][16 K],
+ *     su fp32 [n_experts][rows], sv [n_experts][cols], scale [n_experts].
+ *   n_experts in [1, 1024].  Everything else as in exl3_linear.
+ *   ws: exl3_expert_linear_workspace_bytes(...).
+ */
+EXL3_API size_t exl3_expert_linear_workspace_bytes(int64_t T, int64_t rows, int64_t cols,
+                                                   int transposed);
+EXL3_API exl3_status exl3_expert_linear(const void *x, int dt, int64_t T, int64_t x_stride,
+                                        const int32_t *offsets, int n_experts,
+                                        const uint16_t *codes, int64_t rows, int64_t cols, int K,
+                                        const float *su, const float *sv, const float *scale,
+                                        int transposed, void *y, int64_t y_stride, void *ws,
+                                        size_t ws_bytes, void *stream);
 
 /*
  * exl3_encode_tiles without a workspace, for callers that cannot allocate
