@@ -972,6 +972,8 @@ exl3_status exl3_wait_timeouts(unsigned int *count_out) {
     if (st == EXL3_OK)
         st = exl3::rot_take_wait_timeouts(&r);
     n += r;
+    if (st == EXL3_OK)
+        st = exl3::product_take_wait_timeouts(&r), n += r;
     if (count_out)
         *count_out = n;
     if (st != EXL3_OK)

@@ -207,6 +207,8 @@ bool rotate_fwd_tma_eligible(const RotateLaunch &p);
 exl3_status launch_rotate_fwd_tma(const RotateLaunch &p, cudaStream_t s);
 // reads and clears the TMA rotation's expired-wait count (no synchronisation)
 exl3_status rot_take_wait_timeouts(unsigned int *n);
+// the same of the products with coded matrices (linear_product.cu)
+exl3_status product_take_wait_timeouts(unsigned int *n);
 
 // grid-and-parabola scale search (scale_search.cu)
 struct GridSearchLaunch {

@@ -64,6 +64,10 @@ __global__ void act_kernel(const ActLaunch a) {
     __shared__ float wmax[32];
     const int tid = threadIdx.x;
     const int64_t NP = act_rows(a.T);
+    // the product kernel behind this one may start on the codes; it waits for this
+    // kernel's end before it reads z.  (This kernel itself starts after everything
+    // before it, so the codes are complete.)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (a.offsets) {
         for (int i = tid; i <= a.E; i += blockDim.x)
             off[i] = a.offsets[i];

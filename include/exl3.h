@@ -518,11 +518,13 @@ EXL3_API exl3_status exl3_profile_read(double *encode_ms, int64_t *encode_launch
                               int64_t *kernel_launches);
 
 /*
- * Device-side wait accounting (no counterpart on the pages).  One kernel waits
+ * Device-side wait accounting (no counterpart on the pages).  Two kernels wait
  * on asynchronous arrivals: the forward rotation of bf16 weights waits for its
- * TMA tile loads.  Each such wait gives up after one second, after which the
- * block issues no further loads, waits (bounded) for the loads it already
- * issued, and the launch's results are void.  exl3_wait_timeouts synchronises the device,
+ * TMA tile loads, and the products with coded matrices (exl3_linear and the
+ * entry points beside it) for their copies, operands and tensor-core results.
+ * Each such wait gives up after one second, after which the block issues
+ * nothing further, waits (bounded) for what it already issued, and the
+ * launch's results are void.  exl3_wait_timeouts synchronises the device,
  * stores in *count_out (may be NULL) the number of expired waits since the
  * previous call and resets it; it returns EXL3_ERR_TIMEOUT when that number is
  * nonzero, EXL3_ERR_CUDA when the device could not be read, else EXL3_OK.  The
