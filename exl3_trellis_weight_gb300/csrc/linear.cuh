@@ -24,9 +24,9 @@ constexpr int kMaxRank = 128;
 // them: for each block of 64 inputs, NP token rows of 128 bytes whose 16-byte
 // chunks c sit at c ^ (row & 7) (the 128-byte swizzle of a shared-memory
 // operand), so that any tile of token rows starting at a multiple of 8 is one
-// contiguous copy.  NP leaves 16 rows behind the last token: tiles are rounded
-// up to 16 tokens.
-__host__ __device__ inline int64_t act_rows(int64_t T) { return (T + 7) / 8 * 8 + 16; }
+// contiguous copy.  NP leaves 32 rows behind the last token: tiles are rounded
+// up to 16 or 32 tokens.
+__host__ __device__ inline int64_t act_rows(int64_t T) { return (T + 7) / 8 * 8 + 32; }
 __host__ __device__ inline int64_t act_offset(int64_t NP, int64_t t, int k) {
     return ((int64_t)(k >> 6) * NP + t) * 128 + ((((k >> 3) & 7) ^ (int)(t & 7)) << 4) + (k & 7) * 2;
 }

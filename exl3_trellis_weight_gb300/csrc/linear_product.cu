@@ -2,27 +2,29 @@
 // from the codes on the way into the tensor cores.
 //
 // The product runs transposed: a block owns 128 outputs (the lanes of its
-// accumulator) and up to 256 tokens (its columns), so that a weight is decoded
-// once for 256 tokens and a single token still fills every lane.  Warps have
+// accumulators) and the tokens are the columns, so that a weight is decoded
+// once for many tokens and a single token still fills every lane.  Warps have
 // roles:
-//   0-7    decode: 32 weights of every 128 x 64 step each, from registers that
-//          were loaded kAhead steps before, to a swizzled operand stage.  The
-//          weights of a tile row run along the outputs (x W^) or along the sum
-//          (x W^^T): the first is stored as an operand whose rows run along M,
-//          the second along K, and only the descriptor differs;
-//   8-11   results: accumulator -> shared memory (one token per row) -> H over
+//   0-15   decode, eight warps to a 128 x 64 step and taking turns: 32 weights a
+//          thread to a swizzled operand stage.  The weights of a tile row run
+//          along the outputs (x W^) or along the sum (x W^^T): the first is
+//          stored as an operand whose rows run along M, the second along K, and
+//          only the descriptor differs;
+//   16-19  results: accumulator -> shared memory (one token per row) -> H over
 //          the 128 outputs (16 to a thread) -> scales, adapters, one rounding;
-//   12     bulk copies of the rotated activations, one contiguous block a step;
-//   13     issues the matrix instructions (128 x N x 16, binary16 in, binary32 out).
-// Two accumulators let the results of one tile overlap the sums of the next.
+//   20     bulk copies of the rotated activations, one contiguous block a step;
+//   21     issues the matrix instructions (binary16 in, binary32 out).
+//
+// Two forms.  Alone, a block multiplies by up to 256 tokens and two
+// accumulators let the results of one tile overlap the sums of the next.  In
+// pairs (PAIR, a cluster of two), one instruction multiplies the 256 outputs of
+// both blocks by up to 256 tokens of which each block holds half, and a tile
+// has up to 512 tokens in two accumulators: each weight is decoded for twice
+// the tokens, and each copy of activations feeds twice the outputs.
 //
 // With few tiles (decode), the sum is split over the `split` blocks of a
 // cluster; each leaves its partial sums in its shared memory and block r adds
 // up, in block order, and finishes tokens r, r + split, ...
-//
-// Bound by the integer and half-precision pipes of the decode (about 6
-// instructions a weight) for few tokens, by the tensor cores and shared memory
-// for many.
 //
 // Every wait is bounded (tc.cuh); after one gives up the block stops issuing,
 // waits for what it has in flight, and its results are void (counted in
@@ -36,15 +38,16 @@ namespace {
 
 using namespace tc;
 
-constexpr int kDecWarps = 8, kOutWarps = 4;
-constexpr int kThreadsP = (kDecWarps + kOutWarps + 2) * 32;
-constexpr int kN = 256;                    // tokens of a tile, at most
+constexpr int kGroups = 2, kDecWarps = 8 * kGroups, kOutWarps = 4;
+constexpr int kWarpB = kDecWarps + kOutWarps, kWarpMma = kWarpB + 1;
+constexpr int kThreadsP = (kWarpB + 2) * 32;
+constexpr int kN = 256;                    // columns of an accumulator
 constexpr int kStep = 64;                  // inputs of a step
-constexpr int kStages = 4;
-constexpr int kAhead = 4;                  // steps whose codes are in flight
-constexpr uint32_t kABytes = 128 * kStep * 2, kBBytes = kN * kStep * 2;
-constexpr uint32_t kStageB = kStages * kABytes;             // B stages behind the A stages
-constexpr uint32_t kOutOff = kStageB + kStages * kBBytes;   // 32 tokens x 128 outputs, fp32
+constexpr int kAStages = 4, kBStages = 16; // operand stages (of B at most)
+constexpr uint32_t kABytes = 128 * kStep * 2, kBArea = 104 * 1024, kCArea = 32 * 1024;
+constexpr uint32_t kBOff = kAStages * kABytes;              // B stages behind the A stages,
+constexpr uint32_t kCOff = kBOff + kBArea;                  // then a ring of codes for each decode warp,
+constexpr uint32_t kOutOff = kCOff + kCArea;                // then 32 tokens x 128 outputs, fp32
 constexpr uint32_t kSmem = kOutOff + 32 * 128 * 4 + 1024;   // + alignment slack
 
 __device__ unsigned int g_product_timeouts;
@@ -66,10 +69,6 @@ __device__ __forceinline__ uint32_t levels2(uint32_t s0, uint32_t s1) {
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// A tile row of 16 weights ends with the last bit of r[NR - 1]; its windows need
-// 15 bits before it: 15 + 16 K bits in NR words.
-template <int K> struct RowBits { static constexpr int NR = (15 + 16 * K + 31) / 32; };
-
 // 16-bit window `sh` bits before the end of r.  Byte-aligned picks share one
 // funnel shift for each bit offset.
 template <int NR> __device__ __forceinline__ uint32_t window(const uint32_t (&r)[NR], int sh) {
@@ -82,61 +81,34 @@ template <int NR> __device__ __forceinline__ uint32_t window(const uint32_t (&r)
     return __funnelshift_r(r[a], hi, b) & 0xFFFFu;
 }
 
-template <int K> __device__ __forceinline__ void load_codes(const uint32_t *p, uint32_t (&w)[K]) {
-    if constexpr (K == 4) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p));
-        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-    } else if constexpr (K == 2) {
-        const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
-        w[0] = v.x, w[1] = v.y;
-    } else {
+// Row R (16 weights) of the tile whose codes start at `tile`, to the 32 bytes of
+// an operand row at `to` (the second 16 at to ^ 16).  The row's windows need the
+// 15 + 16 K bits up to its last one: NR words that end with it.
+template <int K> __device__ __forceinline__ void decode_row(uint32_t tile, int R, uint32_t to) {
+    constexpr int NR = (15 + 16 * K + 31) / 32;
+    constexpr int NL = (K & 1) ? NR + 1 : NR;              // odd K: half the rows end inside a word
+    const int end = 16 * K * (R + 1), last = (end - 1) >> 5;
+    uint32_t l[NL], r[NR];
 #pragma unroll
-        for (int i = 0; i < K; i++)
-            w[i] = __ldg(p + i);
+    for (int j = 0; j < NL; j++) {
+        int at = last - (NL - 1 - j);
+        at += at < 0 ? 8 * K : 0;                          // the stream is a ring
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(l[j]) : "r"(tile + 4u * at));
     }
-}
-
-// 32 weights (two tile rows) of this thread to the operand stage.  Threads of
-// odd q store their second row first, so that the eight lanes of a store phase
-// cover all banks.
-template <int K>
-__device__ __forceinline__ void decode32(const uint32_t (&w)[K], int lane, uint32_t first, uint32_t second) {
-    constexpr int NR = RowBits<K>::NR;
-    const uint32_t prev = __shfl_sync(0xffffffffu, w[K - 1], (lane + 28) & 31);   // the eight q of a tile in a ring
-    uint32_t r0[NR], r1[NR];
-    if constexpr (K == 1) {
-        r0[0] = __funnelshift_r(w[0], prev, 16);
-        r1[0] = w[0];
-    } else if constexpr (K == 2) {
-        r0[0] = prev, r0[1] = w[0];
-        r1[0] = w[0], r1[1] = w[1];
-    } else if constexpr (K == 3) {
-        r0[0] = __funnelshift_r(w[0], prev, 16), r0[1] = __funnelshift_r(w[1], w[0], 16);
-        r1[0] = w[1], r1[1] = w[2];
-    } else {
-        r0[0] = prev, r0[1] = w[0], r0[2] = w[1];
-        r1[0] = w[1], r1[1] = w[2], r1[2] = w[3];
-    }
-    const bool odd = (lane & 4) != 0;
 #pragma unroll
-    for (int i = 0; i < 2; i++) {
-        uint32_t r[NR];
+    for (int j = 0; j < NR; j++)
+        r[j] = (K & 1) ? __funnelshift_r(l[j + NL - NR], l[j + NL - NR - (K & 1)], end & 16) : l[j];
 #pragma unroll
-        for (int j = 0; j < NR; j++)
-            r[j] = (i == 0) == odd ? r1[j] : r0[j];
-        const uint32_t at = i ? second : first;
+    for (int h = 0; h < 2; h++) {
+        uint32_t v[4];
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-            uint32_t v[4];
-#pragma unroll
-            for (int p = 0; p < 4; p++) {
-                const int c = 8 * h + 2 * p;
-                v[p] = levels2(window<NR>(r, (15 - c) * K), window<NR>(r, (14 - c) * K));
-            }
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at ^ (h << 4)), "r"(v[0]), "r"(v[1]),
-                         "r"(v[2]), "r"(v[3])
-                         : "memory");
+        for (int p = 0; p < 4; p++) {
+            const int c = 8 * h + 2 * p;
+            v[p] = levels2(window<NR>(r, (15 - c) * K), window<NR>(r, (14 - c) * K));
         }
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to ^ (h << 4)), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                     "r"(v[3])
+                     : "memory");
     }
 }
 
@@ -145,7 +117,7 @@ struct Tile {
     int f0;           // first output
     int64_t t0;       // first token column, a multiple of 8 (columns before lo are not stored)
     int64_t lo, hi;   // tokens of the expert inside [t0, t0 + n)
-    int n;            // columns, a multiple of 16
+    int n;            // columns, a multiple of 16 (PAIR: 32)
 };
 
 // Shared list of token tiles: expert e has first[e + 1] - first[e] of them
@@ -157,7 +129,9 @@ struct Plan {
 struct Args {
     ProductLaunch p;
     int n_in, n_out;
-    int tile_n;          // tokens of a tile (a multiple of 16 up to kN)
+    int tile_n;          // tokens of a tile (a multiple of 16 up to 256, PAIR: of 32 up to 512)
+    int b_steps;         // steps of a B stage: the fewer the tokens, the more
+    int b_stages;        // B stages of b_steps steps of tile_n tokens (PAIR: of half of them)
     int split;           // blocks of a cluster, each with its share of the steps
 };
 
@@ -167,12 +141,13 @@ __device__ __forceinline__ int tiles_of(int lo, int hi, int tile_n) {
     return hi > lo ? (hi - (lo & ~7) + tile_n - 1) / tile_n : 0;
 }
 
-// tile `it`: outputs fastest, so that blocks running side by side share their tokens
-__device__ __forceinline__ Tile make_tile(const Args &a, const Plan *plan, int64_t it) {
+// tile `it`: outputs fastest, so that blocks running side by side share their
+// tokens.  The second block of the last pair may have no outputs (f0 == n_out).
+template <bool PAIR> __device__ __forceinline__ Tile make_tile(const Args &a, const Plan *plan, int64_t it, int rank) {
     Tile t;
-    const int nf = a.n_out / 128;
+    const int nf = PAIR ? (a.n_out / 128 + 1) / 2 : a.n_out / 128;
     int j = (int)(it / nf);
-    t.f0 = (int)(it % nf) * 128;
+    t.f0 = (int)(it % nf) * (PAIR ? 256 : 128) + (PAIR ? rank * 128 : 0);
     int64_t lo = 0, hi = a.p.T;
     t.e = 0;
     if (a.p.offsets) {
@@ -192,11 +167,17 @@ __device__ __forceinline__ Tile make_tile(const Args &a, const Plan *plan, int64
     t.t0 = (lo & ~7ll) + (int64_t)j * a.tile_n;
     t.lo = lo > t.t0 ? lo : t.t0;
     t.hi = hi < t.t0 + a.tile_n ? hi : t.t0 + a.tile_n;
-    t.n = (int)((t.hi - t.t0 + 15) / 16 * 16);
+    t.n = PAIR ? (int)((t.hi - t.t0 + 31) / 32 * 32) : (int)((t.hi - t.t0 + 15) / 16 * 16);
     return t;
 }
 
-// outputs 4u + 32m + i (m, i < 4) of one token to v[4m + i]: H over the 128, eight threads to a token
+// One token's results pass through shared memory as 32 float4; float4 f of a row
+// sits at f ^ (f / 8 & 1), so that a warp's columns (32 consecutive outputs of one
+// token) and eight threads' reads (outputs 8u + 64m + i of it, u < 8) both cover
+// all banks.
+__device__ __forceinline__ int out_at(int f4) { return f4 ^ ((f4 >> 3) & 1); }
+
+// v[8m + i] is output 8u + 64m + i of a token (m < 2, i < 8), u = lane % 8: H over the 128
 __device__ __forceinline__ void rotate_out(float (&v)[16], int lane) {
 #pragma unroll
     for (int h = 1; h < 16; h <<= 1)
@@ -216,98 +197,130 @@ __device__ __forceinline__ void rotate_out(float (&v)[16], int lane) {
     }
 }
 
-template <typename TY>
-__device__ __forceinline__ void finish_token(const Args &a, const Tile &tl, int64_t t, float (&v)[16], int u) {
+// right . 2^-7 s of output f < 128 of the tile
+__device__ __forceinline__ float right_of(const Args &a, const Tile &tl, int f) {
+    const int f0 = min(tl.f0, a.n_out - 128);
+    return __fmul_rn(__ldg(a.p.right + (size_t)tl.e * a.n_out + f0 + f), __fmul_rn(__ldg(a.p.scale + tl.e), 0x1p-7f));
+}
+
+template <typename TY> __device__ __forceinline__ void fma8(float *v, float h, const uint4 &w) {
+    const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const float2 f = unpack2<TY>(q[i]);
+        v[2 * i] = __fmaf_rn(h, f.x, v[2 * i]);
+        v[2 * i + 1] = __fmaf_rn(h, f.y, v[2 * i + 1]);
+    }
+}
+
+// token t's 16 outputs of this thread: scales, adapter, one rounding.  With SHARED,
+// the four groups of eight threads of a warp hold the same token and a quarter of
+// the adapter's rows each.
+template <typename TY, bool SHARED>
+__device__ __forceinline__ void finish(const Args &a, const Tile &tl, int64_t t, float rs, float (&v)[16],
+                                       const float *right, int lane) {
+    rotate_out(v, lane);
+    if (t < tl.lo || t >= tl.hi || tl.f0 >= a.n_out)
+        return;
     const ProductLaunch &p = a.p;
-    const float s = __fmul_rn(p.rscale[t], __fmul_rn(p.scale[tl.e], 0x1p-7f));
-    const float *right = p.right + (size_t)tl.e * a.n_out + tl.f0 + 4 * u;
+    const int u = lane & 7;
 #pragma unroll
     for (int m = 0; m < 4; m++) {
-        const float4 r = __ldg(reinterpret_cast<const float4 *>(right + 32 * m));
-        v[4 * m] = __fmul_rn(__fmul_rn(v[4 * m], s), r.x);
-        v[4 * m + 1] = __fmul_rn(__fmul_rn(v[4 * m + 1], s), r.y);
-        v[4 * m + 2] = __fmul_rn(__fmul_rn(v[4 * m + 2], s), r.z);
-        v[4 * m + 3] = __fmul_rn(__fmul_rn(v[4 * m + 3], s), r.w);
+        const float4 f = reinterpret_cast<const float4 *>(right)[2 * u + (m & 1) + 16 * (m >> 1)];
+        v[4 * m] = __fmul_rn(__fmul_rn(v[4 * m], rs), f.x);
+        v[4 * m + 1] = __fmul_rn(__fmul_rn(v[4 * m + 1], rs), f.y);
+        v[4 * m + 2] = __fmul_rn(__fmul_rn(v[4 * m + 2], rs), f.z);
+        v[4 * m + 3] = __fmul_rn(__fmul_rn(v[4 * m + 3], rs), f.w);
     }
     if (p.B) {
         const int ad = p.slots[t];
         if (ad >= 0 && ad < p.n_adapters) {
             const int r = p.ranks ? min(max(p.ranks[ad], 0), p.rank) : p.rank;
-            const TY *b = reinterpret_cast<const TY *>(p.B) + (size_t)ad * p.rank * a.n_out + tl.f0 + 4 * u;
+            const TY *b = reinterpret_cast<const TY *>(p.B) + (size_t)ad * p.rank * a.n_out + tl.f0 + 8 * u;
             const float *h = p.h + t * p.rank;
-            for (int j = 0; j < r; j++, b += a.n_out) {
-                const float hj = h[j];
+            if (SHARED && lane >= 8) {
 #pragma unroll
-                for (int m = 0; m < 4; m++) {
-                    const uint2 w = __ldg(reinterpret_cast<const uint2 *>(b + 32 * m));
-                    const float2 x = unpack2<TY>(w.x), y = unpack2<TY>(w.y);
-                    v[4 * m] = __fmaf_rn(hj, x.x, v[4 * m]);
-                    v[4 * m + 1] = __fmaf_rn(hj, x.y, v[4 * m + 1]);
-                    v[4 * m + 2] = __fmaf_rn(hj, y.x, v[4 * m + 2]);
-                    v[4 * m + 3] = __fmaf_rn(hj, y.y, v[4 * m + 3]);
+                for (int i = 0; i < 16; i++)
+                    v[i] = 0.0f;
+            }
+#pragma unroll 2
+            for (int j = SHARED ? lane >> 3 : 0; j < r; j += SHARED ? 4 : 1) {
+                const float hj = h[j];
+                const uint4 x = __ldg(reinterpret_cast<const uint4 *>(b + (size_t)j * a.n_out));
+                const uint4 y = __ldg(reinterpret_cast<const uint4 *>(b + (size_t)j * a.n_out + 64));
+                fma8<TY>(v, hj, x);
+                fma8<TY>(v + 8, hj, y);
+            }
+            if (SHARED) {
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 16; i++) {
+                    v[i] = __fadd_rn(v[i], __shfl_xor_sync(0xffffffffu, v[i], 8));
+                    v[i] = __fadd_rn(v[i], __shfl_xor_sync(0xffffffffu, v[i], 16));
                 }
             }
         }
+        if (SHARED && lane >= 8)
+            return;
     }
-    TY *y = reinterpret_cast<TY *>(p.y) + t * p.y_stride + tl.f0 + 4 * u;
-    if ((((uintptr_t)p.y | (uintptr_t)(p.y_stride * 2)) & 7u) == 0) {
+    TY *y = reinterpret_cast<TY *>(p.y) + t * p.y_stride + tl.f0 + 8 * u;
+    const bool wide = (((uintptr_t)p.y | (uintptr_t)(p.y_stride * 2)) & 15u) == 0;
 #pragma unroll
-        for (int m = 0; m < 4; m++)
-            *reinterpret_cast<uint2 *>(y + 32 * m) =
-                make_uint2(pack2<TY>(v[4 * m], v[4 * m + 1]), pack2<TY>(v[4 * m + 2], v[4 * m + 3]));
-    } else {
+    for (int m = 0; m < 2; m++) {
+        if (wide) {
+            *reinterpret_cast<uint4 *>(y + 64 * m) =
+                make_uint4(pack2<TY>(v[8 * m], v[8 * m + 1]), pack2<TY>(v[8 * m + 2], v[8 * m + 3]),
+                           pack2<TY>(v[8 * m + 4], v[8 * m + 5]), pack2<TY>(v[8 * m + 6], v[8 * m + 7]));
+        } else {
 #pragma unroll
-        for (int m = 0; m < 4; m++)
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-                y[32 * m + i] = from_f32<TY>(v[4 * m + i]);
+            for (int i = 0; i < 8; i++)
+                y[64 * m + i] = from_f32<TY>(v[8 * m + i]);
+        }
     }
 }
 
-__device__ __forceinline__ void finish(const Args &a, const Tile &tl, int64_t t, float (&v)[16], int lane) {
-    rotate_out(v, lane);
-    if (t < tl.lo || t >= tl.hi)
-        return;
-    if (a.p.dt == EXL3_BF16)
-        finish_token<__nv_bfloat16>(a, tl, t, v, lane & 7);
-    else
-        finish_token<__half>(a, tl, t, v, lane & 7);
-}
-
-template <int K>
+template <int K, bool PAIR, typename TY>
 __global__ void __launch_bounds__(kThreadsP, 1) product_kernel(const __grid_constant__ Args a) {
     extern __shared__ unsigned char smem_raw[];
-    __shared__ __align__(8) unsigned long long bars[3 * kStages + 5];
+    __shared__ __align__(8) unsigned long long bars[2 * kAStages + 2 * kBStages + 5];
     __shared__ Plan plan;
+    __shared__ __align__(16) float right[128];
     __shared__ uint32_t tmem_at;
     __shared__ int gave_up;
     const uint32_t base = (saddr(smem_raw) + 1023u) & ~1023u;
     unsigned char *const sb = smem_raw + (base - saddr(smem_raw));
-    const uint32_t bar0 = saddr(bars);
-    auto full_a = [&](int s) { return bar0 + 8u * s; };
-    auto full_b = [&](int s) { return bar0 + 8u * (kStages + s); };
-    auto empty = [&](int s) { return bar0 + 8u * (2 * kStages + s); };
-    auto acc_full = [&](int i) { return bar0 + 8u * (3 * kStages + i); };
-    auto acc_empty = [&](int i) { return bar0 + 8u * (3 * kStages + 2 + i); };
-    const uint32_t drained = bar0 + 8u * (3 * kStages + 4);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t bar_a = saddr(bars), bar_b = bar_a + 16u * kAStages;
+    const uint32_t bar_d = bar_b + 16u * kBStages;
+    auto full_a = [&](uint32_t s) { return bar_a + 8u * s; };
+    auto empty_a = [&](uint32_t s) { return bar_a + 8u * (kAStages + s); };
+    auto full_b = [&](uint32_t s) { return bar_b + 8u * s; };
+    auto empty_b = [&](uint32_t s) { return bar_b + 8u * (kBStages + s); };
+    auto acc_full = [&](uint32_t i) { return bar_d + 8u * i; };
+    auto acc_empty = [&](uint32_t i) { return bar_d + 8u * (2 + i); };
+    const uint32_t drained = bar_d + 32u;
+    // (through a shuffle the compiler knows the warp's number, and what follows from it, as uniform)
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    const int rank = PAIR ? (int)(blockIdx.x & 1) : a.split > 1 ? (int)(blockIdx.x % a.split) : 0;
 
     if (tid == 0) {
-        for (int s = 0; s < kStages; s++) {
-            bar_init(full_a(s), kDecWarps);
+        for (int s = 0; s < kAStages; s++) {
+            bar_init(full_a(s), PAIR ? 16 : 8);
+            bar_init(empty_a(s), 1);
+        }
+        for (int s = 0; s < kBStages; s++) {
             bar_init(full_b(s), 1);
-            bar_init(empty(s), 1);
+            bar_init(empty_b(s), 1);
         }
         for (int i = 0; i < 2; i++) {
             bar_init(acc_full(i), 1);
-            bar_init(acc_empty(i), kOutWarps);
+            bar_init(acc_empty(i), PAIR ? 2 * kOutWarps : kOutWarps);
         }
         bar_init(drained, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         gave_up = 0;
     }
     if (warp == kDecWarps)
-        tmem_alloc<512>(saddr(&tmem_at));
+        tmem_alloc_all<PAIR>(saddr(&tmem_at));
     // token tiles of each expert
     if (a.p.offsets) {
         for (int i = tid; i <= a.p.E; i += kThreadsP)
@@ -334,230 +347,335 @@ __global__ void __launch_bounds__(kThreadsP, 1) product_kernel(const __grid_cons
     }
     fence_before();
     __syncthreads();
+    if (PAIR)
+        cluster_sync();                    // the other block's barriers are ready
     fence_after();
     const uint32_t tmem = tmem_at;
     const int64_t n_tok = a.p.offsets ? plan.first[a.p.E] : (a.p.T + a.tile_n - 1) / a.tile_n;
-    const int64_t n_tiles = n_tok * (a.n_out / 128);
-    const int rank = a.split > 1 ? (int)(blockIdx.x % a.split) : 0;
-    const int64_t it0 = blockIdx.x / a.split, dit = a.split > 1 ? n_tiles : gridDim.x;   // one tile a cluster
+    const int64_t n_tiles = n_tok * (PAIR ? (a.n_out / 128 + 1) / 2 : a.n_out / 128);
+    const int blocks = PAIR ? 2 : a.split;                                             // of a cluster
+    const int64_t it0 = blockIdx.x / blocks, dit = !PAIR && a.split > 1 ? n_tiles : gridDim.x / blocks;
     const int steps = a.n_in / kStep;
-    const int k_lo = (int)((int64_t)steps * rank / a.split), k_hi = (int)((int64_t)steps * (rank + 1) / a.split);
+    const int k_lo = PAIR ? 0 : (int)((int64_t)steps * rank / a.split);
+    const int k_hi = PAIR ? steps : (int)((int64_t)steps * (rank + 1) / a.split);
     const int64_t NP = act_rows(a.p.T);
+    const uint32_t nb = (uint32_t)a.b_stages, b_step = (uint32_t)a.tile_n * (PAIR ? 64u : 128u);   // bytes of a step
+    const uint32_t b_bytes = b_step * (uint32_t)a.b_steps;
     unsigned int *const count = &g_product_timeouts;
+    const uint32_t n_mine = it0 < n_tiles ? (uint32_t)((n_tiles - 1 - it0) / dit + 1) : 0u;
+    uint32_t issued = 0;                   // B stages copied (of the thread that copies)
 
-    uint32_t issued = 0;                   // bulk copies (of the thread that makes them)
     if (warp < kDecWarps) {
-        // ---- decode ----
-        const int q = lane >> 2, tc = lane & 3;
+        // ---- decode: groups of eight warps take turns at the steps ----
+        const int q = lane >> 2, tc = lane & 3, dw = warp & 7, group = warp >> 3, odd = q & 1;
+        const uint32_t panel = a.p.transposed ? (uint32_t)dw * 16u * 128u
+                                              : (uint32_t)(dw & 1) * 8192u + (uint32_t)(dw >> 1) * 16u * 128u;
+        const uint32_t n = (uint32_t)(k_hi - k_lo), total = n_mine * n;
+        // This warp's codes of a step are those of four neighbouring tiles, 128 K
+        // bytes in a row.  They are copied kRing of its steps ahead, across tiles.
+        constexpr uint32_t kRing = 16 / K, kSlot = 128 * K;
+        static_assert(kRing * kSlot * kDecWarps <= kCArea, "code rings");
+        const uint32_t ring = base + kCOff + (uint32_t)warp * (kRing * kSlot);
         const int64_t tiles_c = a.p.cols / 16;
-        // tile of this thread inside a step, and its rows in the operand stage
-        const int tr = a.p.transposed ? warp : warp >> 1, tcol = a.p.transposed ? tc : (warp & 1) * 4 + tc;
-        const int64_t hop = (a.p.transposed ? 4 : 4 * tiles_c) * (8 * K);
-        const uint32_t panel = a.p.transposed ? (uint32_t)warp * 16u * 128u
-                                              : (uint32_t)(warp & 1) * 8192u + (uint32_t)(warp >> 1) * 16u * 128u;
-        const int odd = q & 1, ra = 2 * q + odd, rb = 2 * q + 1 - odd;
-        const uint32_t offa = panel + ra * 128 + (((2 * tc) ^ (ra & 7)) << 4);
-        const uint32_t offb = panel + rb * 128 + (((2 * tc) ^ (rb & 7)) << 4);
-        uint32_t it_step = 0;
-        bool ok = true;
-        for (int64_t it = it0; ok && it < n_tiles; it += dit) {
-            const Tile tl = make_tile(a, &plan, it);
-            const int64_t r0 = a.p.transposed ? tl.f0 / 16 + tr : (int64_t)k_lo * 4 + tr;
-            const int64_t c0 = a.p.transposed ? (int64_t)k_lo * 4 + tcol : tl.f0 / 16 + tcol;
-            const uint32_t *p = a.p.codes + (size_t)tl.e * (a.p.rows / 16) * tiles_c * (8 * K) +
-                                (size_t)(r0 * tiles_c + c0) * (8 * K) + q * K;
-            uint32_t w[kAhead][K];
-#pragma unroll
-            for (int i = 0; i < kAhead; i++)
-                if (k_lo + i < k_hi)
-                    load_codes<K>(p + i * hop, w[i]);
-            for (int k = k_lo; ok && k < k_hi; k += kAhead) {
-#pragma unroll
-                for (int i = 0; i < kAhead; i++) {
-                    if (k + i < k_hi && ok) {
-                        const int s = it_step % kStages;
-                        const uint32_t round = it_step / kStages;
-                        if (round && !bar_wait(empty(s), (round - 1) & 1, &gave_up, count))
-                            ok = false;
-                        // every lane of the warp goes on or none: a lane that gave up takes the others along
-                        ok = __all_sync(0xffffffffu, ok);
-                        if (ok) {
-                            const uint32_t st = base + s * kABytes;
-                            decode32<K>(w[i], lane, st + offa, st + offb);
-                            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                            __syncwarp();
-                            if (lane == 0)
-                                bar_arrive(full_a(s));
-                            if (k + i + kAhead < k_hi)
-                                load_codes<K>(p + (int64_t)(k + i + kAhead - k_lo) * hop, w[i]);
-                            it_step++;
-                        }
-                    }
+        const int tr = a.p.transposed ? dw : dw >> 1, tcol = a.p.transposed ? 0 : (dw & 1) * 4;
+        const int64_t hop = (a.p.transposed ? 4 : 4 * tiles_c) * (32 * K);       // bytes from step to step
+        uint32_t s_load = group, k_load = group, slot_load = 0;
+        int64_t it_load = it0;
+        const char *p_load = nullptr;
+        auto next_codes = [&]() {
+            if (s_load < total) {
+                while (!p_load || k_load >= n) {
+                    if (p_load)
+                        k_load -= n, it_load += dit;
+                    const Tile tl = make_tile<PAIR>(a, &plan, it_load, rank);
+                    const int f0 = PAIR ? min(tl.f0, a.n_out - 128) : tl.f0;
+                    const int64_t r0 = a.p.transposed ? f0 / 16 + tr : (int64_t)k_lo * 4 + tr;
+                    const int64_t c0 = a.p.transposed ? (int64_t)k_lo * 4 + tcol : f0 / 16 + tcol;
+                    p_load = reinterpret_cast<const char *>(a.p.codes) +
+                             ((int64_t)tl.e * (a.p.rows / 16) * tiles_c + r0 * tiles_c + c0) * (32 * K) + lane * 16;
                 }
+                if (lane < 8 * K)
+                    copy16(ring + slot_load * kSlot + lane * 16, p_load + k_load * hop);
             }
+            copy_group();
+            s_load += kGroups;
+            k_load += kGroups;
+            slot_load = slot_load + 1 == kRing ? 0 : slot_load + 1;
+        };
+#pragma unroll 1
+        for (uint32_t i = 0; i < kRing; i++)
+            next_codes();
+        uint32_t slot = 0, s_b = group % nb, round_b = group / nb;
+        bool ready = true;                 // the stage is known to be free
+#pragma unroll 1
+        for (uint32_t step = group; step < total; step += kGroups) {
+            const uint32_t s = step % kAStages, round = step / kAStages;
+            if (!__all_sync(0xffffffffu, ready || bar_wait(empty_a(s), (round - 1) & 1, &gave_up, count)))
+                break;                     // the warp goes on as a whole or not at all
+            copy_wait<kRing - 1>();
+            __syncwarp();
+            // whether the next stage is free, asked for before it is needed
+            const uint32_t s2 = (step + kGroups) % kAStages, round2 = (step + kGroups) / kAStages;
+            ready = round2 == 0 || bar_peek(empty_a(s2), (round2 - 1) & 1);
+            const uint32_t st = base + s * kABytes + panel, tile = ring + slot * kSlot + tc * (32u * K);
+            // Threads of odd q take their second row first: the eight lanes of a
+            // store phase then cover all banks.  The loop stays one: unrolled over
+            // rows and steps the code outgrew the instruction cache.
+#pragma unroll 1
+            for (int i = 0; i < 2; i++) {
+                const int R = 2 * q + (i ^ odd);
+                decode_row<K>(tile, R, st + R * 128 + (((2 * tc) ^ (R & 7)) << 4));
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (PAIR && rank == 1 && dw == 0) {
+                // block 0 issues for both: this block's arrival also says that its activations have landed
+                if (!__all_sync(0xffffffffu, bar_wait(full_b(s_b), round_b & 1, &gave_up, count)))
+                    break;
+                for (int i = 0; i < kGroups; i++)
+                    if (++s_b == nb)
+                        s_b = 0, round_b++;
+            }
+            if (lane == 0) {
+                if (PAIR)
+                    bar_arrive_at(at_block(full_a(s), 0));
+                else
+                    bar_arrive(full_a(s));
+            }
+            next_codes();
+            slot = slot + 1 == kRing ? 0 : slot + 1;
         }
     } else if (warp < kDecWarps + kOutWarps) {
         // ---- results ----
         const int ow = warp - kDecWarps;
-        float *const buf = reinterpret_cast<float *>(sb + (a.split > 1 ? 0 : kOutOff));
+        const bool keep = !PAIR && a.split > 1;             // partial sums stay in shared memory
+        float *const buf = reinterpret_cast<float *>(sb + (keep ? 0 : kOutOff));
+        const int col = 4 * out_at(8 * ow + (lane >> 2)) + (lane & 3);
         asm volatile("griddepcontrol.wait;" ::: "memory");
-        uint32_t i_acc = 0;
-        for (int64_t it = it0; it < n_tiles; it += dit, i_acc++) {
-            const Tile tl = make_tile(a, &plan, it);
-            const int d = i_acc & 1;
-            bool ok = bar_wait(acc_full(d), (i_acc >> 1) & 1, &gave_up, count);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok)
-                break;
-            fence_after();
-            for (int c0 = 0; c0 < tl.n; c0 += 32) {
-                float v[32];
-                tmem_load32(tmem + (uint32_t)(ow * 32) * 65536u + d * kN + c0, v);
-                float *const dst = buf + (a.split > 1 ? c0 * 128 : 0) + ow * 32 + lane;
+        uint32_t acc = 0;
+        bool ok = true;
+        for (int64_t it = it0; ok && it < n_tiles; it += dit) {
+            const Tile tl = make_tile<PAIR>(a, &plan, it, rank);
+            // read after the barriers of the first chunk; the last chunk's protect the previous tile's
+            right[ow * 32 + lane] = right_of(a, tl, ow * 32 + lane);
+            for (int n0 = 0; ok && n0 < tl.n; n0 += kN, acc++) {
+                const int d = acc & 1;
+                ok = bar_wait(acc_full(d), (acc >> 1) & 1, &gave_up, count);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok)
+                    break;
+                fence_after();
+                const int n1 = min(tl.n - n0, kN);
+                for (int c0 = 0; c0 < n1; c0 += 32) {
+                    // 16 tokens at a time, eight threads to a token
+                    const int64_t t = tl.t0 + n0 + c0 + ow * 4 + (lane >> 3);
+                    const float rs0 = !keep && t < tl.hi ? a.p.rscale[t] : 0.0f;
+                    const float rs1 = !keep && t + 16 < tl.hi ? a.p.rscale[t + 16] : 0.0f;
+                    float *const dst = buf + (keep ? c0 * 128 : 0) + col;
 #pragma unroll
-                for (int i = 0; i < 32; i++)
-                    dst[i * 128] = v[i];
-                if (a.split > 1)
-                    continue;
-                asm volatile("bar.sync 1, 128;" ::: "memory");
-                // 16 tokens at a time, eight threads to a token
+                    for (int g = 0; g < 2; g++) {
+                        float v[16];
+                        tmem_load16(tmem + (uint32_t)(ow * 32) * 65536u + d * kN + c0 + 16 * g, v);
 #pragma unroll
-                for (int g = 0; g < 2; g++) {
-                    const int row = g * 16 + ow * 4 + (lane >> 3);
-                    const float4 *src = reinterpret_cast<const float4 *>(buf + row * 128) + (lane & 7);
-                    float x[16];
-#pragma unroll
-                    for (int m = 0; m < 4; m++) {
-                        const float4 f = src[8 * m];
-                        x[4 * m] = f.x, x[4 * m + 1] = f.y, x[4 * m + 2] = f.z, x[4 * m + 3] = f.w;
+                        for (int i = 0; i < 16; i++)
+                            dst[(16 * g + i) * 128] = v[i];
                     }
-                    finish(a, tl, tl.t0 + c0 + row, x, lane);
+                    if (keep)
+                        continue;
+                    asm volatile("bar.sync 1, 128;" ::: "memory");
+#pragma unroll 1
+                    for (int g = 0; g < 2; g++) {
+                        const float4 *src = reinterpret_cast<const float4 *>(buf) + (g * 16 + ow * 4 + (lane >> 3)) * 32;
+                        float x[16];
+#pragma unroll
+                        for (int m = 0; m < 4; m++) {
+                            const float4 f = src[out_at(2 * (lane & 7) + (m & 1) + 16 * (m >> 1))];
+                            x[4 * m] = f.x, x[4 * m + 1] = f.y, x[4 * m + 2] = f.z, x[4 * m + 3] = f.w;
+                        }
+                        finish<TY, false>(a, tl, t + 16 * g, g ? rs1 : rs0, x, right, lane);
+                    }
+                    asm volatile("bar.sync 1, 128;" ::: "memory");
                 }
-                asm volatile("bar.sync 1, 128;" ::: "memory");
+                fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (PAIR)
+                        bar_arrive_at(at_block(acc_empty(d), 0));
+                    else
+                        bar_arrive(acc_empty(d));
+                }
             }
-            fence_before();
-            __syncwarp();
-            if (lane == 0)
-                bar_arrive(acc_empty(d));
         }
-    } else if (warp == kDecWarps + kOutWarps) {
+    } else if (warp == kWarpB) {
         // ---- activations ----
         asm volatile("griddepcontrol.wait;" ::: "memory");
         if (lane == 0) {
-            uint32_t it_step = 0;
             bool ok = true;
+            uint32_t s = 0, round = 0;
             for (int64_t it = it0; ok && it < n_tiles; it += dit) {
-                const Tile tl = make_tile(a, &plan, it);
+                const Tile tl = make_tile<PAIR>(a, &plan, it, rank);
                 const unsigned char *src = a.p.image + ((int64_t)k_lo * NP + tl.t0) * 128;
-                for (int k = k_lo; k < k_hi; k++, src += NP * 128) {
-                    const int s = it_step % kStages;
-                    const uint32_t round = it_step / kStages;
-                    if (round && !bar_wait(empty(s), (round - 1) & 1, &gave_up, count)) {
+                for (int k = k_lo; k < k_hi; k += a.b_steps) {
+                    if (round && !bar_wait(empty_b(s), (round - 1) & 1, &gave_up, count)) {
                         ok = false;
                         break;
                     }
-                    bar_expect(full_b(s), (uint32_t)tl.n * 128u);
-                    bulk_load(base + kStageB + s * kBBytes, src, (uint32_t)tl.n * 128u, full_b(s));
-                    it_step++;
+                    const int steps_here = min(a.b_steps, k_hi - k);
+                    bar_expect(full_b(s), (uint32_t)(steps_here * tl.n) * (PAIR ? 64u : 128u));
+                    for (int j = 0; j < steps_here; j++, src += NP * 128) {
+                        const uint32_t dst = base + kBOff + s * b_bytes + j * b_step;
+                        if (PAIR) {
+                            // this block's half of the columns of each accumulator
+                            for (int n0 = 0; n0 < tl.n; n0 += kN) {
+                                const int half = min(tl.n - n0, kN) / 2;
+                                bulk_load(dst + n0 * 64, src + (int64_t)(n0 + rank * half) * 128, (uint32_t)half * 128u,
+                                          full_b(s));
+                            }
+                        } else {
+                            bulk_load(dst, src, (uint32_t)tl.n * 128u, full_b(s));
+                        }
+                    }
+                    issued++;
+                    if (++s == nb)
+                        s = 0, round++;
                 }
             }
-            issued = it_step;
         }
-    } else {
+    } else if (!PAIR || rank == 0) {
         // ---- matrix instructions ----
-        if (lane == 0) {
-            uint32_t it_step = 0, i_acc = 0;
-            bool ok = true;
-            for (int64_t it = it0; ok && it < n_tiles; it += dit, i_acc++) {
-                const Tile tl = make_tile(a, &plan, it);
-                const int d = i_acc & 1;
-                const uint32_t shape = shape_f16(128, tl.n, !a.p.transposed);
-                if (i_acc >= 2 && !bar_wait(acc_empty(d), ((i_acc >> 1) - 1) & 1, &gave_up, count))
-                    break;
-                fence_after();
-                for (int k = k_lo; k < k_hi; k++, it_step++) {
-                    const int s = it_step % kStages;
-                    const uint32_t par = (it_step / kStages) & 1;
-                    if (!bar_wait(full_b(s), par, &gave_up, count) || !bar_wait(full_a(s), par, &gave_up, count)) {
-                        ok = false;
+        // The warp stays together and elects the thread that issues at each step: a
+        // branch on the lane took 780 cycles a step for what takes 100 this way.
+        // What follows from the tile is kept out of the loop over the steps, which has
+        // to stay shorter than a step's decode.
+        uint32_t acc = 0, s = 0, s_phase = 0, sa = 0, sa_phase = 0;
+        bool ok = true;
+        // 16 inputs on: 32 bytes of a row along K, two groups of 8 rows along M
+        const uint64_t a0 = a.p.transposed ? operand(base, 16, 1024) : operand(base, 8192, 1024);
+        const uint64_t b0 = operand(base + kBOff, 16, 1024);
+        const uint32_t hop_a = a.p.transposed ? 32 >> 4 : 2048 >> 4;
+        for (int64_t it = it0; ok && it < n_tiles; it += dit) {
+            const Tile tl = make_tile<PAIR>(a, &plan, it, rank);
+            const bool two = PAIR && tl.n > kN;
+            ok = acc < 2 || bar_wait<PAIR>(acc_empty(acc & 1), ((acc >> 1) - 1) & 1, &gave_up, count);
+            if (two && acc + 1 >= 2)
+                ok = bar_wait<PAIR>(acc_empty((acc + 1) & 1), (((acc + 1) >> 1) - 1) & 1, &gave_up, count) && ok;
+            ok = __all_sync(0xffffffffu, ok);
+            const uint32_t shape = shape_f16(PAIR ? 256 : 128, two ? kN : tl.n, !a.p.transposed);
+            const uint32_t shape2 = shape_f16(256, tl.n - kN, !a.p.transposed);
+            const uint32_t d = tmem + (acc & 1) * kN, d2 = tmem + ((acc + 1) & 1) * kN;
+            for (int k = k_lo; ok && k < k_hi;) {
+                ok = __all_sync(0xffffffffu, bar_wait(full_b(s), s_phase, &gave_up, count));
+                const int k_end = min(k + a.b_steps, k_hi);
+                uint64_t db = b0 + (s * b_bytes >> 4);
+                for (; ok && k < k_end; k++, db += b_step >> 4) {
+                    ok = __all_sync(0xffffffffu, bar_wait<PAIR>(full_a(sa), sa_phase, &gave_up, count));
+                    if (!ok)
                         break;
-                    }
                     fence_after();
-                    const uint32_t sa = base + s * kABytes, sB = base + kStageB + s * kBBytes;
+                    if (elect()) {
+                        const uint64_t da = a0 + sa * (kABytes >> 4);
+                        const bool add = k > k_lo;
 #pragma unroll
-                    for (int j = 0; j < kStep / 16; j++) {
-                        // 16 inputs on: 32 bytes of a row along K, two groups of 8 rows along M
-                        const uint64_t da = a.p.transposed ? operand(sa + 32 * j, 16, 1024)
-                                                           : operand(sa + 2048 * j, 8192, 1024);
-                        mma_f16(tmem + d * kN, da, operand(sB + 32 * j, 16, 1024), shape, k > k_lo || j > 0);
+                        for (int j = 0; j < kStep / 16; j++)
+                            mma_f16<PAIR>(d, da + j * hop_a, db + j * 2, shape, add || j > 0);
+                        if (two) {
+#pragma unroll
+                            for (int j = 0; j < kStep / 16; j++)
+                                mma_f16<PAIR>(d2, da + j * hop_a, db + (kN * 64 >> 4) + j * 2, shape2, add || j > 0);
+                        }
+                        commit<PAIR>(empty_a(sa));
+                        if (k + 1 == k_end)
+                            commit<PAIR>(empty_b(s));
                     }
-                    commit(empty(s));
+                    __syncwarp();
+                    if (++sa == kAStages)
+                        sa = 0, sa_phase ^= 1;
                 }
-                if (ok)
-                    commit(acc_full(d));
+                if (++s == nb)
+                    s = 0, s_phase ^= 1;
             }
+            if (ok && elect()) {
+                commit<PAIR>(acc_full(acc & 1));
+                if (two)
+                    commit<PAIR>(acc_full((acc + 1) & 1));
+            }
+            __syncwarp();
+            acc += two ? 2 : 1;
         }
     }
     __syncwarp();
 
-    if (a.split > 1) {
+    if (!PAIR && a.split > 1) {
         // partial sums of the cluster, added in block order
-        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+        cluster_sync();
         if (it0 < n_tiles && warp < kDecWarps + kOutWarps) {
-            // (decode warps read what the result warps' `griddepcontrol.wait` has waited for)
-            const Tile tl = make_tile(a, &plan, it0);
-            const int groups = (kDecWarps + kOutWarps) * 4;
+            const Tile tl = make_tile<PAIR>(a, &plan, it0, rank);
+            // a warp takes four tokens at a time, with adapters one
+            const bool shared = a.p.B != nullptr;
+            const int each = shared ? 1 : 4, sub = shared ? 0 : lane >> 3;
             const int mine = (tl.n + a.split - 1 - rank) / a.split;          // tokens rank, rank + split, ...
-            for (int i = warp * 4; i < mine; i += groups) {
-                const int row = rank + (i + (lane >> 3)) * a.split;
+            for (int i = warp * each; i < mine; i += (kDecWarps + kOutWarps) * each) {
+                const int row = rank + (i + sub) * a.split;
                 const bool in = row < tl.n;
                 float x[16];
 #pragma unroll
                 for (int j = 0; j < 16; j++)
                     x[j] = 0.0f;
+                const int64_t t = in ? tl.t0 + row : tl.hi;
+                const float rs = t < tl.hi ? a.p.rscale[t] : 0.0f;
                 if (in)
+#pragma unroll 1
                     for (int b = 0; b < a.split; b++) {
-                        uint32_t from;
-                        asm("mapa.shared::cluster.u32 %0, %1, %2;"
-                            : "=r"(from) : "r"(base + (uint32_t)row * 512u + (uint32_t)(lane & 7) * 16u), "r"(b));
+                        const uint32_t from = at_block(base + (uint32_t)row * 512u, b);
 #pragma unroll
                         for (int m = 0; m < 4; m++) {
                             float4 f;
                             asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                                         : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w) : "r"(from + 128u * m) : "memory");
+                                         : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w)
+                                         : "r"(from + 16u * out_at(2 * (lane & 7) + (m & 1) + 16 * (m >> 1)))
+                                         : "memory");
                             x[4 * m] = __fadd_rn(x[4 * m], f.x);
                             x[4 * m + 1] = __fadd_rn(x[4 * m + 1], f.y);
                             x[4 * m + 2] = __fadd_rn(x[4 * m + 2], f.z);
                             x[4 * m + 3] = __fadd_rn(x[4 * m + 3], f.w);
                         }
                     }
-                finish(a, tl, in ? tl.t0 + row : tl.hi, x, lane);
+                if (shared)
+                    finish<TY, true>(a, tl, t, rs, x, right, lane);
+                else
+                    finish<TY, false>(a, tl, t, rs, x, right, lane);
             }
         }
-        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+        cluster_sync();
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     fence_before();
     __syncthreads();
     if (gave_up) {
         // nothing may be in flight when the block ends: its last copies and matrix instructions
-        if (warp == kDecWarps + kOutWarps && lane == 0)
-            for (uint32_t back = 1; back <= kStages && back <= issued; back++)
-                bar_drain(full_b((issued - back) % kStages), ((issued - back) / kStages) & 1);
-        if (warp == kDecWarps + kOutWarps + 1 && lane == 0) {
-            commit(drained);
+        if (warp == kWarpB && lane == 0)
+            for (uint32_t back = 1; back <= nb && back <= issued; back++)
+                bar_drain(full_b((issued - back) % nb), ((issued - back) / nb) & 1);
+        if (warp == kWarpMma && !(PAIR && rank == 1)) {
+            if (elect())
+                commit<PAIR>(drained);
+            __syncwarp();
             bar_drain(drained, 0);
         }
         __syncthreads();
     }
+    if (PAIR)
+        cluster_sync();                    // neither block ends while the other may still reach into it
     if (warp == kDecWarps) {
         fence_after();
-        tmem_free<512>(tmem);
+        tmem_free_all<PAIR>(tmem);
     }
 }
 
-template <int K> exl3_status launch_k(const Args &a, unsigned grid, cudaStream_t s) {
-    static_assert(kSmem <= 227 * 1024, "shared memory of one block");
-    cudaError_t e = cudaFuncSetAttribute(product_kernel<K>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+template <int K, bool PAIR, typename TY> exl3_status launch_form(const Args &a, unsigned grid, unsigned cluster, cudaStream_t s) {
+    static_assert(kSmem <= 227 * 1024 - 10 * 1024, "shared memory of one block");
+    cudaError_t e =
+        cudaFuncSetAttribute(product_kernel<K, PAIR, TY>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e != cudaSuccess)
         return cuda_check(e, "cudaFuncSetAttribute(coded product)");
     cudaLaunchConfig_t cfg = {};
@@ -569,16 +687,43 @@ template <int K> exl3_status launch_k(const Args &a, unsigned grid, cudaStream_t
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)a.split;
+    attr[1].val.clusterDim.x = cluster;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, product_kernel<K>, a);
+    e = cudaLaunchKernelEx(&cfg, product_kernel<K, PAIR, TY>, a);
     if (e != cudaSuccess)
         return cuda_check(e, "coded product launch");
     note_launch();
     return cuda_check(cudaGetLastError(), "coded product launch");
+}
+
+template <bool PAIR, typename TY> exl3_status launch_k(const Args &a, unsigned grid, unsigned cluster, cudaStream_t s) {
+    switch (a.p.K) {
+    case 1: return launch_form<1, PAIR, TY>(a, grid, cluster, s);
+    case 2: return launch_form<2, PAIR, TY>(a, grid, cluster, s);
+    case 3: return launch_form<3, PAIR, TY>(a, grid, cluster, s);
+    default: return launch_form<4, PAIR, TY>(a, grid, cluster, s);
+    }
+}
+template <bool PAIR> exl3_status launch_t(const Args &a, unsigned grid, unsigned cluster, cudaStream_t s) {
+    return a.p.dt == EXL3_BF16 ? launch_k<PAIR, __nv_bfloat16>(a, grid, cluster, s)
+                               : launch_k<PAIR, __half>(a, grid, cluster, s);
+}
+
+// token tiles, at most: experts' sizes are not known to the host
+int64_t token_tiles(const ProductLaunch &p, int tile_n) {
+    const int64_t used = p.T < p.E ? p.T : p.E;
+    return p.offsets ? used + (p.T + 7 * used) / tile_n + 1 : (p.T + tile_n - 1) / tile_n;
+}
+
+// B stages of `rows` tokens: several steps to a stage when a step is small, so
+// that a wait and an arrival serve all of them
+void set_b(Args &a, int rows) {
+    a.b_steps = rows <= 64 ? 4 : rows <= 128 ? 2 : 1;
+    a.b_stages = (int)(kBArea / ((unsigned)(rows * 128) * a.b_steps));
+    a.b_stages = a.b_stages > kBStages ? kBStages : a.b_stages;
 }
 
 }  // namespace
@@ -589,24 +734,39 @@ exl3_status launch_product(const ProductLaunch &p, cudaStream_t s) {
     a.n_in = (int)(p.transposed ? p.cols : p.rows);
     a.n_out = (int)(p.transposed ? p.rows : p.cols);
     const int64_t sms = device_sm_count();
-    // token tiles of even size, at most kN; experts' sizes are not known here
+    const int nf = a.n_out / 128;
+    if (p.T > 512 * (p.offsets ? p.E : 1)) {
+        const int64_t pairs = sms / 2, np = (nf + 1) / 2;
+        // even tiles of up to 512 tokens, of the size whose rounds of the pairs take the fewest columns
+        int best = 512;
+        int64_t cost = INT64_MAX;
+        for (int n = 512; n > 256 && !p.offsets; n -= 32) {
+            const int64_t c = ((token_tiles(p, n) * np + pairs - 1) / pairs) * n;
+            if (c < cost)
+                cost = c, best = n;
+        }
+        a.tile_n = best;
+        a.b_steps = 1;                     // (block 1's decode warps count stages as steps)
+        a.b_stages = (int)(kBArea / (a.tile_n * 64u));
+        a.b_stages = a.b_stages > kBStages ? kBStages : a.b_stages;
+        a.split = 1;
+        const int64_t tiles = token_tiles(p, a.tile_n) * np;
+        return launch_t<true>(a, (unsigned)(2 * (tiles < pairs ? tiles : pairs)), 2, s);
+    }
+    // token tiles of even size, at most kN
     const int64_t n = (p.T + kN - 1) / kN;
-    a.tile_n = p.offsets ? kN : (int)(((p.T + n - 1) / n + 15) / 16 * 16);
-    const int64_t used = p.T < p.E ? p.T : p.E;
-    const int64_t tok = p.offsets ? used + (p.T + 7 * used) / kN + 1 : n;
-    const int64_t tiles = tok * (a.n_out / 128);
+    a.tile_n = p.offsets && p.T > 16 ? kN : (int)(((p.T + n - 1) / n + 15) / 16 * 16);
+    if (p.offsets && p.T <= 16)
+        a.tile_n = 32;
+    set_b(a, a.tile_n);
+    const int64_t tiles = token_tiles(p, a.tile_n) * nf;
     // blocks that would idle share the sums of the tiles, at least 4 steps each
     const int steps = a.n_in / kStep;
     a.split = 1;
     while (a.split < 8 && tiles * a.split * 2 <= sms && steps >= a.split * 2 * 4)
         a.split *= 2;
     const unsigned grid = (unsigned)(a.split > 1 ? tiles * a.split : tiles < sms ? tiles : sms);
-    switch (p.K) {
-    case 1: return launch_k<1>(a, grid, s);
-    case 2: return launch_k<2>(a, grid, s);
-    case 3: return launch_k<3>(a, grid, s);
-    default: return launch_k<4>(a, grid, s);
-    }
+    return launch_t<false>(a, grid, (unsigned)a.split, s);
 }
 
 exl3_status product_take_wait_timeouts(unsigned int *n) {

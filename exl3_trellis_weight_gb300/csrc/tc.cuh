@@ -8,8 +8,6 @@
 namespace exl3 {
 namespace tc {
 
-constexpr unsigned long long kWaitLimitNs = 1000000000ull;
-
 __device__ __forceinline__ uint32_t saddr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
 __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
@@ -21,28 +19,44 @@ __device__ __forceinline__ void bar_arrive(uint32_t bar) {
 __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
+// CLUSTER: arrivals may come from the other block
+template <bool CLUSTER = false> __device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
     uint32_t ok;
-    asm volatile("{\n\t.reg .pred p;\n\t"
+    if constexpr (CLUSTER)
+        asm volatile("{\n\t.reg .pred p;\n\t"
+                     "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                     "selp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    else
+        asm volatile("{\n\t.reg .pred p;\n\t"
                  "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
                  "selp.u32 %0, 1, 0, p;\n\t}"
                  : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     return ok != 0u;
 }
-__device__ __forceinline__ unsigned long long now_ns() {
-    unsigned long long t;
-    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-    return t;
+// whether a phase is over, without the wait that a try may do
+__device__ __forceinline__ bool bar_peek(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0u;
 }
 
-// Waits for a phase, one second at most.  False when it gave up, or when
-// another wait of the block had: the caller then leaves its loop.
+// Waits for a phase, about a second at most (2^31 cycles of the SM's clock, read
+// once in 64 tries).  False when it gave up, or when another wait of the block
+// had: the caller then leaves its loop.
+constexpr long long kWaitCycles = 1ll << 31;
+template <bool CLUSTER>
 __device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, volatile int *gave_up, unsigned int *count) {
-    const unsigned long long t0 = now_ns();
-    while (!bar_test(bar, parity)) {
+    const long long t0 = clock64();
+    for (uint32_t i = 1; !bar_test<CLUSTER>(bar, parity); i++) {
+        if ((i & 63u) != 0u)
+            continue;
         if (*gave_up)
             return false;
-        if (now_ns() - t0 > kWaitLimitNs) {
+        if (clock64() - t0 > kWaitCycles) {
             *gave_up = 1;
             atomicAdd(count, 1u);
             return false;
@@ -50,15 +64,29 @@ __device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, volati
     }
     return true;
 }
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *gave_up, unsigned int *count) {
-    return bar_test(bar, parity) || bar_wait_slow(bar, parity, gave_up, count);
+    return bar_test<CLUSTER>(bar, parity) || bar_wait_slow<CLUSTER>(bar, parity, gave_up, count);
 }
-// Waits for a phase, one second at most, whatever other waits did (the way out
+// Waits for a phase, as long at most, whatever other waits did (the way out
 // after one gave up: nothing may be in flight when the block ends).
 __device__ __forceinline__ void bar_drain(uint32_t bar, uint32_t parity) {
-    const unsigned long long t0 = now_ns();
-    while (!bar_test(bar, parity) && now_ns() - t0 < kWaitLimitNs) {
+    const long long t0 = clock64();
+    while (!bar_test(bar, parity) && clock64() - t0 < kWaitCycles) {
     }
+}
+
+// the same barrier of another block of the cluster
+__device__ __forceinline__ uint32_t at_block(uint32_t addr, uint32_t block) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(block));
+    return r;
+}
+__device__ __forceinline__ void bar_arrive_at(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // contiguous global -> shared copy; both 16-byte aligned, bytes a multiple of 16
@@ -68,32 +96,47 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
                  : "memory");
 }
 
-// ---- tensor memory ------------------------------------------------------------
-template <int COLS> __device__ __forceinline__ void tmem_alloc(uint32_t dst) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "n"(COLS) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+// 16 bytes global -> shared by this thread; groups complete in order
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"((uint64_t)__cvta_generic_to_global(src))
+                 : "memory");
 }
-template <int COLS> __device__ __forceinline__ void tmem_free(uint32_t addr) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "n"(COLS));
+__device__ __forceinline__ void copy_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT> __device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
+// ---- tensor memory (PAIR: of the two blocks of a cluster that share their products) ----
+template <bool PAIR> __device__ __forceinline__ void tmem_alloc_all(uint32_t dst) {
+    if constexpr (PAIR) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(dst) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(dst) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+}
+template <bool PAIR> __device__ __forceinline__ void tmem_free_all(uint32_t addr) {
+    if constexpr (PAIR)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(addr));
+    else
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(addr));
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// 32 columns of this warp's 32 lanes (lane l holds row l)
-__device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32]) {
-    uint32_t r[32];
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+// 16 columns of this warp's 32 lanes (lane l holds row l)
+__device__ __forceinline__ void tmem_load16(uint32_t addr, float (&v)[16]) {
+    uint32_t r[16];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
                    "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
-                   "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
-                   "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
-                   "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+                   "=r"(r[15])
                  : "r"(addr));
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-    for (int i = 0; i < 32; i++)
+    for (int i = 0; i < 16; i++)
         v[i] = __uint_as_float(r[i]);
 }
 
@@ -109,18 +152,35 @@ __device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lbo, uint32_
 __device__ __forceinline__ uint32_t shape_f16(int m, int n, bool a_mn) {
     return 1u << 4 | (a_mn ? 1u << 15 : 0u) | (uint32_t)(n >> 3) << 17 | (uint32_t)(m >> 4) << 24;
 }
+template <bool PAIR>
 __device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t shape, bool add) {
-    asm volatile("{\n\t.reg .pred p;\n\t"
-                 "setp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-                 "l"(a), "l"(b), "r"(shape), "r"((uint32_t)add)
-                 : "memory");
+    if constexpr (PAIR)
+        asm volatile("{\n\t.reg .pred p;\n\t"
+                     "setp.ne.b32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                     "l"(a), "l"(b), "r"(shape), "r"((uint32_t)add)
+                     : "memory");
+    else
+        asm volatile("{\n\t.reg .pred p;\n\t"
+                     "setp.ne.b32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                     "l"(a), "l"(b), "r"(shape), "r"((uint32_t)add)
+                     : "memory");
 }
-// arrives on the barrier when every matrix instruction issued so far by this thread is done
-__device__ __forceinline__ void commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+// arrives on the barrier (PAIR: of both blocks) when every matrix instruction
+// issued so far by this thread is done
+template <bool PAIR> __device__ __forceinline__ void commit(uint32_t bar) {
+    if constexpr (PAIR)
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                         bar),
+                     "h"((uint16_t)3)
+                     : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+                     : "memory");
 }
 
+// one thread of a converged warp, the same one each time
 __device__ __forceinline__ bool elect() {
     uint32_t ok;
     asm volatile("{\n\t.reg .pred p;\n\t"
