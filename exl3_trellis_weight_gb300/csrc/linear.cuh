@@ -44,6 +44,9 @@ struct ActLaunch {
     void *y;                  // rows outside of every expert are set to 0
     int64_t y_stride;
     int y_cols;
+    // order of 16 neighbouring inputs: place 4j + i holds input 4j + i (0), j + 4i (1)
+    // or 2j + i % 2 + 8 (i / 2) (2)
+    int order;
 };
 exl3_status launch_act(const ActLaunch &p, cudaStream_t s);
 
@@ -70,6 +73,11 @@ struct ProductLaunch {
     int64_t y_stride;
 };
 exl3_status launch_product(const ProductLaunch &p, cudaStream_t s);
+// the same for few tokens (linear_few.cu)
+bool few_eligible(const ProductLaunch &p);
+int few_order(const ProductLaunch &p);     // ActLaunch::order that it reads
+exl3_status launch_product_few(const ProductLaunch &p, cudaStream_t s);
+exl3_status few_take_wait_timeouts(unsigned int *n);
 
 // h[t][j] = gain_i sum_k M[i][j][k] x[t][k], i = slots[t], j < ranks[i] (0 otherwise)
 struct ShrinkLaunch {

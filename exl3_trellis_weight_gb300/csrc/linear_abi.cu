@@ -152,7 +152,6 @@ exl3_status run_linear(const LinearWs &m, const void *x, int dt, int64_t T, int6
     a.y = y;
     a.y_stride = y_stride;
     a.y_cols = (int)w.outputs();
-    if ((st = launch_act(a, s)) != EXL3_OK) return st;
     ProductLaunch p = {};
     p.image = m.image;
     p.rscale = m.rscale;
@@ -175,7 +174,10 @@ exl3_status run_linear(const LinearWs &m, const void *x, int dt, int64_t T, int6
     p.y = y;
     p.dt = dt;
     p.y_stride = y_stride;
-    return launch_product(p, s);
+    const bool few = few_eligible(p);
+    a.order = few ? few_order(p) : 0;
+    if ((st = launch_act(a, s)) != EXL3_OK) return st;
+    return few ? launch_product_few(p, s) : launch_product(p, s);
 }
 
 exl3_status run_shrink(const void *x, int dt, int64_t T, int64_t stride, int64_t n, const void *M, const Adapters &ad,

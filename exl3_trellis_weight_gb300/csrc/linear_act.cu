@@ -143,9 +143,19 @@ __global__ void act_kernel(const ActLaunch a) {
             }
             if (in) {
                 uint32_t w[8];
+                if (a.order == 0) {
 #pragma unroll
-                for (int i = 0; i < 8; i++)
-                    w[i] = pack2<__half>(v[2 * i], v[2 * i + 1]);
+                    for (int i = 0; i < 8; i++)
+                        w[i] = pack2<__half>(v[2 * i], v[2 * i + 1]);
+                } else if (a.order == 1) {
+#pragma unroll
+                    for (int i = 0; i < 8; i++)
+                        w[i] = pack2<__half>(v[(i >> 1) + 8 * (i & 1)], v[(i >> 1) + 8 * (i & 1) + 4]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; i++)
+                        w[i] = pack2<__half>(v[2 * (i >> 1) + 8 * (i & 1)], v[2 * (i >> 1) + 8 * (i & 1) + 1]);
+                }
                 *reinterpret_cast<uint4 *>(a.image + act_offset(NP, t, k)) = make_uint4(w[0], w[1], w[2], w[3]);
                 *reinterpret_cast<uint4 *>(a.image + act_offset(NP, t, k + 8)) = make_uint4(w[4], w[5], w[6], w[7]);
             }

@@ -1,0 +1,207 @@
+// linear_decode.cuh -- what the kernels that multiply by coded matrices share:
+// levels of the codes, the list of token tiles, the way from sums to results.
+#pragma once
+
+#include "linear.cuh"
+
+namespace exl3 {
+
+// Codebook levels of two windows, fl16(fl32(n c)) with n = bytesum - 510 (the
+// definition): the byte sum lands in the low bits of 2^23, one packed difference
+// gives n, one packed product and one conversion round it.  The multiply, the byte
+// sum and the packed operations share a pipe that starts a warp every second cycle:
+// 6 of its cycles a weight, and as many instructions (packed half operations, which
+// need a correction for the 24-bit c, take 7).
+__device__ __forceinline__ uint32_t levels2(uint32_t s0, uint32_t s1) {
+    const uint32_t a = __dp4a(s0 * kMul1Mult, 0x01010101u, 0x4B000000u);
+    const uint32_t b = __dp4a(s1 * kMul1Mult, 0x01010101u, 0x4B000000u);
+    uint32_t v;
+    asm("{\n\t.reg .b64 x, y;\n\t.reg .f32 p, q;\n\t"
+        "mov.b64 x, {%1, %2};\n\t"
+        "mov.b64 y, {%3, %3};\n\t"
+        "add.rn.f32x2 x, x, y;\n\t"
+        "mov.b64 y, {%4, %4};\n\t"
+        "mul.rn.f32x2 x, x, y;\n\t"
+        "mov.b64 {p, q}, x;\n\t"
+        "cvt.rn.f16x2.f32 %0, q, p;\n\t}"
+        : "=r"(v) : "r"(a), "r"(b), "f"(-8389118.0f), "f"(kMul1C));
+    return v;
+}
+
+// ---- tiles of outputs and tokens ----------------------------------------------
+struct OutTile {
+    int e;            // expert
+    int f0;           // first output
+    int64_t t0;       // first token column, a multiple of 8 (columns before lo are not stored)
+    int64_t lo, hi;   // tokens of the expert inside the tile
+};
+
+// Shared list of token tiles: expert e has first[e + 1] - first[e] of them
+struct Plan {
+    int32_t off[kMaxExperts + 1];
+    int32_t first[kMaxExperts + 1];
+};
+
+__device__ __forceinline__ int clamp_off(int32_t v, int64_t T) { return v < 0 ? 0 : (int64_t)v > T ? (int)T : v; }
+
+__device__ __forceinline__ int tiles_of(int lo, int hi, int tile_n) {
+    return hi > lo ? (hi - (lo & ~7) + tile_n - 1) / tile_n : 0;
+}
+
+// by all `threads` threads of a block; a barrier must follow
+__device__ __forceinline__ void make_plan(Plan &plan, const int32_t *offsets, int E, int64_t T, int tile_n, int tid,
+                                          int threads) {
+    for (int i = tid; i <= E; i += threads)
+        plan.off[i] = clamp_off(offsets[i], T);
+    __syncthreads();
+    if (tid >= 32)
+        return;
+    int at = 0;
+    for (int e0 = 0; e0 < E; e0 += 32) {
+        const int e = e0 + tid;
+        const int n = e < E ? tiles_of(plan.off[e], plan.off[e + 1], tile_n) : 0;
+        int sum = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, sum, d);
+            sum += tid >= d ? o : 0;
+        }
+        if (e < E)
+            plan.first[e] = at + sum - n;
+        at += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    if (tid == 0)
+        plan.first[E] = at;
+}
+
+// tile `it` of nf x (token tiles): outputs fastest, so that blocks running side by
+// side share their tokens.  f0 counts in units of `width` outputs.
+__device__ __forceinline__ OutTile out_tile(const Plan *plan, int E, int64_t T, int tile_n, int nf, int width, int64_t it) {
+    OutTile t;
+    int j = (int)(it / nf);
+    t.f0 = (int)(it % nf) * width;
+    int64_t lo = 0, hi = T;
+    t.e = 0;
+    if (plan) {
+        int l = 0, h = E - 1;            // last e with first[e] <= j
+        while (l < h) {
+            const int m = (l + h + 1) >> 1;
+            if (plan->first[m] <= j)
+                l = m;
+            else
+                h = m - 1;
+        }
+        t.e = l;
+        j -= plan->first[l];
+        lo = plan->off[l];
+        hi = max(lo, (int64_t)plan->off[l + 1]);
+    }
+    t.t0 = (lo & ~7ll) + (int64_t)j * tile_n;
+    t.lo = lo > t.t0 ? lo : t.t0;
+    t.hi = hi < t.t0 + tile_n ? hi : t.t0 + tile_n;
+    return t;
+}
+
+// ---- from sums to results -------------------------------------------------------
+// One token's results pass through shared memory as 32 float4; float4 f of a row
+// sits at f ^ (f / 8 & 1), so that a warp's columns (32 consecutive outputs of one
+// token) and eight threads' reads (outputs 8u + 64m + i of it, u < 8) both cover
+// all banks.
+__device__ __forceinline__ int out_at(int f4) { return f4 ^ ((f4 >> 3) & 1); }
+
+// v[8m + i] is output 8u + 64m + i of a token (m < 2, i < 8), u = lane % 8: H over the 128
+__device__ __forceinline__ void rotate_out(float (&v)[16], int lane) {
+#pragma unroll
+    for (int h = 1; h < 16; h <<= 1)
+#pragma unroll
+        for (int i = 0; i < 16; i++)
+            if ((i & h) == 0) {
+                const float p = v[i], q = v[i + h];
+                v[i] = __fadd_rn(p, q);
+                v[i + h] = __fsub_rn(p, q);
+            }
+#pragma unroll
+    for (int h = 1; h < 8; h <<= 1) {
+        const float sg = (lane & h) ? -1.0f : 1.0f;
+#pragma unroll
+        for (int i = 0; i < 16; i++)
+            v[i] = __fmaf_rn(sg, v[i], __shfl_xor_sync(0xffffffffu, v[i], h));
+    }
+}
+
+template <typename TY> __device__ __forceinline__ void fma8(float *v, float h, const uint4 &w) {
+    const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const float2 f = unpack2<TY>(q[i]);
+        v[2 * i] = __fmaf_rn(h, f.x, v[2 * i]);
+        v[2 * i + 1] = __fmaf_rn(h, f.y, v[2 * i + 1]);
+    }
+}
+
+// token t's 16 outputs of this thread: scales, adapter, one rounding.  With SHARED,
+// the four groups of eight threads of a warp hold the same token and a quarter of
+// the adapter's rows each.
+template <typename TY, bool SHARED>
+__device__ __forceinline__ void finish(const ProductLaunch &p, int n_out, const OutTile &tl, int64_t t, float rs, float (&v)[16],
+                                       const float *right, int lane) {
+    rotate_out(v, lane);
+    if (t < tl.lo || t >= tl.hi || tl.f0 >= n_out)
+        return;
+    const int u = lane & 7;
+#pragma unroll
+    for (int m = 0; m < 4; m++) {
+        const float4 f = reinterpret_cast<const float4 *>(right)[2 * u + (m & 1) + 16 * (m >> 1)];
+        v[4 * m] = __fmul_rn(__fmul_rn(v[4 * m], rs), f.x);
+        v[4 * m + 1] = __fmul_rn(__fmul_rn(v[4 * m + 1], rs), f.y);
+        v[4 * m + 2] = __fmul_rn(__fmul_rn(v[4 * m + 2], rs), f.z);
+        v[4 * m + 3] = __fmul_rn(__fmul_rn(v[4 * m + 3], rs), f.w);
+    }
+    if (p.B) {
+        const int ad = p.slots[t];
+        if (ad >= 0 && ad < p.n_adapters) {
+            const int r = p.ranks ? min(max(p.ranks[ad], 0), p.rank) : p.rank;
+            const TY *b = reinterpret_cast<const TY *>(p.B) + (size_t)ad * p.rank * n_out + tl.f0 + 8 * u;
+            const float *h = p.h + t * p.rank;
+            if (SHARED && lane >= 8) {
+#pragma unroll
+                for (int i = 0; i < 16; i++)
+                    v[i] = 0.0f;
+            }
+#pragma unroll 2
+            for (int j = SHARED ? lane >> 3 : 0; j < r; j += SHARED ? 4 : 1) {
+                const float hj = h[j];
+                const uint4 x = __ldg(reinterpret_cast<const uint4 *>(b + (size_t)j * n_out));
+                const uint4 y = __ldg(reinterpret_cast<const uint4 *>(b + (size_t)j * n_out + 64));
+                fma8<TY>(v, hj, x);
+                fma8<TY>(v + 8, hj, y);
+            }
+            if (SHARED) {
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 16; i++) {
+                    v[i] = __fadd_rn(v[i], __shfl_xor_sync(0xffffffffu, v[i], 8));
+                    v[i] = __fadd_rn(v[i], __shfl_xor_sync(0xffffffffu, v[i], 16));
+                }
+            }
+        }
+        if (SHARED && lane >= 8)
+            return;
+    }
+    TY *y = reinterpret_cast<TY *>(p.y) + t * p.y_stride + tl.f0 + 8 * u;
+    const bool wide = (((uintptr_t)p.y | (uintptr_t)(p.y_stride * 2)) & 15u) == 0;
+#pragma unroll
+    for (int m = 0; m < 2; m++) {
+        if (wide) {
+            *reinterpret_cast<uint4 *>(y + 64 * m) =
+                make_uint4(pack2<TY>(v[8 * m], v[8 * m + 1]), pack2<TY>(v[8 * m + 2], v[8 * m + 3]),
+                           pack2<TY>(v[8 * m + 4], v[8 * m + 5]), pack2<TY>(v[8 * m + 6], v[8 * m + 7]));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                y[64 * m + i] = from_f32<TY>(v[8 * m + i]);
+        }
+    }
+}
+
+}  // namespace exl3

@@ -29,7 +29,7 @@
 // Every wait is bounded (tc.cuh); after one gives up the block stops issuing,
 // waits for what it has in flight, and its results are void (counted in
 // exl3_wait_timeouts).
-#include "linear.cuh"
+#include "linear_decode.cuh"
 #include "tc.cuh"
 
 namespace exl3 {
@@ -51,23 +51,6 @@ constexpr uint32_t kOutOff = kCOff + kCArea;                // then 32 tokens x 
 constexpr uint32_t kSmem = kOutOff + 32 * 128 * 4 + 1024;   // + alignment slack
 
 __device__ unsigned int g_product_timeouts;
-
-// Codebook levels of two windows: fl16(fl32(n c)), n = bytesum - 510.  n is exact
-// in binary16 (1024 + bytesum is the half with these bits), and
-// fma(n, ch, fl16(n cl)) rounds to the same level for each of the 1021 sums.
-constexpr uint32_t kLevelHi = 0x1EED1EEDu;      // ch = 0x1.bb4p-8
-constexpr uint32_t kLevelLo = 0x802F802Fu;      // cl = -47 x 2^-24
-__device__ __forceinline__ uint32_t levels2(uint32_t s0, uint32_t s1) {
-    const uint32_t a = __dp4a(s0 * kMul1Mult, 0x01010101u, 0x6400u);
-    const uint32_t b = __dp4a(s1 * kMul1Mult, 0x01010101u, 0x6400u);
-    const uint32_t m = __byte_perm(a, b, 0x5410);
-    const uint32_t off = 0xE5FEE5FEu;           // -1534
-    const __half2 n = __hadd2_rn(*reinterpret_cast<const __half2 *>(&m), *reinterpret_cast<const __half2 *>(&off));
-    const uint32_t hi = kLevelHi, lo = kLevelLo;
-    const __half2 t = __hmul2_rn(n, *reinterpret_cast<const __half2 *>(&lo));
-    const __half2 v = __hfma2(n, *reinterpret_cast<const __half2 *>(&hi), t);
-    return *reinterpret_cast<const uint32_t *>(&v);
-}
 
 // 16-bit window `sh` bits before the end of r.  Byte-aligned picks share one
 // funnel shift for each bit offset.
@@ -112,18 +95,8 @@ template <int K> __device__ __forceinline__ void decode_row(uint32_t tile, int R
     }
 }
 
-struct Tile {
-    int e;            // expert
-    int f0;           // first output
-    int64_t t0;       // first token column, a multiple of 8 (columns before lo are not stored)
-    int64_t lo, hi;   // tokens of the expert inside [t0, t0 + n)
+struct Tile : OutTile {
     int n;            // columns, a multiple of 16 (PAIR: 32)
-};
-
-// Shared list of token tiles: expert e has first[e + 1] - first[e] of them
-struct Plan {
-    int32_t off[kMaxExperts + 1];
-    int32_t first[kMaxExperts + 1];
 };
 
 struct Args {
@@ -135,148 +108,22 @@ struct Args {
     int split;           // blocks of a cluster, each with its share of the steps
 };
 
-__device__ __forceinline__ int clamp_off(int32_t v, int64_t T) { return v < 0 ? 0 : (int64_t)v > T ? (int)T : v; }
-
-__device__ __forceinline__ int tiles_of(int lo, int hi, int tile_n) {
-    return hi > lo ? (hi - (lo & ~7) + tile_n - 1) / tile_n : 0;
-}
-
-// tile `it`: outputs fastest, so that blocks running side by side share their
-// tokens.  The second block of the last pair may have no outputs (f0 == n_out).
+// The second block of the last pair may have no outputs (f0 == n_out).
 template <bool PAIR> __device__ __forceinline__ Tile make_tile(const Args &a, const Plan *plan, int64_t it, int rank) {
     Tile t;
-    const int nf = PAIR ? (a.n_out / 128 + 1) / 2 : a.n_out / 128;
-    int j = (int)(it / nf);
-    t.f0 = (int)(it % nf) * (PAIR ? 256 : 128) + (PAIR ? rank * 128 : 0);
-    int64_t lo = 0, hi = a.p.T;
-    t.e = 0;
-    if (a.p.offsets) {
-        int l = 0, h = a.p.E - 1;        // last e with first[e] <= j
-        while (l < h) {
-            const int m = (l + h + 1) >> 1;
-            if (plan->first[m] <= j)
-                l = m;
-            else
-                h = m - 1;
-        }
-        t.e = l;
-        j -= plan->first[l];
-        lo = plan->off[l];
-        hi = max(lo, (int64_t)plan->off[l + 1]);
-    }
-    t.t0 = (lo & ~7ll) + (int64_t)j * a.tile_n;
-    t.lo = lo > t.t0 ? lo : t.t0;
-    t.hi = hi < t.t0 + a.tile_n ? hi : t.t0 + a.tile_n;
+    static_cast<OutTile &>(t) =
+        out_tile(a.p.offsets ? plan : nullptr, a.p.E, a.p.T, a.tile_n, PAIR ? (a.n_out / 128 + 1) / 2 : a.n_out / 128,
+                 PAIR ? 256 : 128, it);
+    if (PAIR)
+        t.f0 += rank * 128;
     t.n = PAIR ? (int)((t.hi - t.t0 + 31) / 32 * 32) : (int)((t.hi - t.t0 + 15) / 16 * 16);
     return t;
-}
-
-// One token's results pass through shared memory as 32 float4; float4 f of a row
-// sits at f ^ (f / 8 & 1), so that a warp's columns (32 consecutive outputs of one
-// token) and eight threads' reads (outputs 8u + 64m + i of it, u < 8) both cover
-// all banks.
-__device__ __forceinline__ int out_at(int f4) { return f4 ^ ((f4 >> 3) & 1); }
-
-// v[8m + i] is output 8u + 64m + i of a token (m < 2, i < 8), u = lane % 8: H over the 128
-__device__ __forceinline__ void rotate_out(float (&v)[16], int lane) {
-#pragma unroll
-    for (int h = 1; h < 16; h <<= 1)
-#pragma unroll
-        for (int i = 0; i < 16; i++)
-            if ((i & h) == 0) {
-                const float p = v[i], q = v[i + h];
-                v[i] = __fadd_rn(p, q);
-                v[i + h] = __fsub_rn(p, q);
-            }
-#pragma unroll
-    for (int h = 1; h < 8; h <<= 1) {
-        const float sg = (lane & h) ? -1.0f : 1.0f;
-#pragma unroll
-        for (int i = 0; i < 16; i++)
-            v[i] = __fmaf_rn(sg, v[i], __shfl_xor_sync(0xffffffffu, v[i], h));
-    }
 }
 
 // right . 2^-7 s of output f < 128 of the tile
 __device__ __forceinline__ float right_of(const Args &a, const Tile &tl, int f) {
     const int f0 = min(tl.f0, a.n_out - 128);
     return __fmul_rn(__ldg(a.p.right + (size_t)tl.e * a.n_out + f0 + f), __fmul_rn(__ldg(a.p.scale + tl.e), 0x1p-7f));
-}
-
-template <typename TY> __device__ __forceinline__ void fma8(float *v, float h, const uint4 &w) {
-    const uint32_t q[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const float2 f = unpack2<TY>(q[i]);
-        v[2 * i] = __fmaf_rn(h, f.x, v[2 * i]);
-        v[2 * i + 1] = __fmaf_rn(h, f.y, v[2 * i + 1]);
-    }
-}
-
-// token t's 16 outputs of this thread: scales, adapter, one rounding.  With SHARED,
-// the four groups of eight threads of a warp hold the same token and a quarter of
-// the adapter's rows each.
-template <typename TY, bool SHARED>
-__device__ __forceinline__ void finish(const Args &a, const Tile &tl, int64_t t, float rs, float (&v)[16],
-                                       const float *right, int lane) {
-    rotate_out(v, lane);
-    if (t < tl.lo || t >= tl.hi || tl.f0 >= a.n_out)
-        return;
-    const ProductLaunch &p = a.p;
-    const int u = lane & 7;
-#pragma unroll
-    for (int m = 0; m < 4; m++) {
-        const float4 f = reinterpret_cast<const float4 *>(right)[2 * u + (m & 1) + 16 * (m >> 1)];
-        v[4 * m] = __fmul_rn(__fmul_rn(v[4 * m], rs), f.x);
-        v[4 * m + 1] = __fmul_rn(__fmul_rn(v[4 * m + 1], rs), f.y);
-        v[4 * m + 2] = __fmul_rn(__fmul_rn(v[4 * m + 2], rs), f.z);
-        v[4 * m + 3] = __fmul_rn(__fmul_rn(v[4 * m + 3], rs), f.w);
-    }
-    if (p.B) {
-        const int ad = p.slots[t];
-        if (ad >= 0 && ad < p.n_adapters) {
-            const int r = p.ranks ? min(max(p.ranks[ad], 0), p.rank) : p.rank;
-            const TY *b = reinterpret_cast<const TY *>(p.B) + (size_t)ad * p.rank * a.n_out + tl.f0 + 8 * u;
-            const float *h = p.h + t * p.rank;
-            if (SHARED && lane >= 8) {
-#pragma unroll
-                for (int i = 0; i < 16; i++)
-                    v[i] = 0.0f;
-            }
-#pragma unroll 2
-            for (int j = SHARED ? lane >> 3 : 0; j < r; j += SHARED ? 4 : 1) {
-                const float hj = h[j];
-                const uint4 x = __ldg(reinterpret_cast<const uint4 *>(b + (size_t)j * a.n_out));
-                const uint4 y = __ldg(reinterpret_cast<const uint4 *>(b + (size_t)j * a.n_out + 64));
-                fma8<TY>(v, hj, x);
-                fma8<TY>(v + 8, hj, y);
-            }
-            if (SHARED) {
-                __syncwarp();
-#pragma unroll
-                for (int i = 0; i < 16; i++) {
-                    v[i] = __fadd_rn(v[i], __shfl_xor_sync(0xffffffffu, v[i], 8));
-                    v[i] = __fadd_rn(v[i], __shfl_xor_sync(0xffffffffu, v[i], 16));
-                }
-            }
-        }
-        if (SHARED && lane >= 8)
-            return;
-    }
-    TY *y = reinterpret_cast<TY *>(p.y) + t * p.y_stride + tl.f0 + 8 * u;
-    const bool wide = (((uintptr_t)p.y | (uintptr_t)(p.y_stride * 2)) & 15u) == 0;
-#pragma unroll
-    for (int m = 0; m < 2; m++) {
-        if (wide) {
-            *reinterpret_cast<uint4 *>(y + 64 * m) =
-                make_uint4(pack2<TY>(v[8 * m], v[8 * m + 1]), pack2<TY>(v[8 * m + 2], v[8 * m + 3]),
-                           pack2<TY>(v[8 * m + 4], v[8 * m + 5]), pack2<TY>(v[8 * m + 6], v[8 * m + 7]));
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; i++)
-                y[64 * m + i] = from_f32<TY>(v[8 * m + i]);
-        }
-    }
 }
 
 template <int K, bool PAIR, typename TY>
@@ -321,30 +168,8 @@ __global__ void __launch_bounds__(kThreadsP, 1) product_kernel(const __grid_cons
     }
     if (warp == kDecWarps)
         tmem_alloc_all<PAIR>(saddr(&tmem_at));
-    // token tiles of each expert
-    if (a.p.offsets) {
-        for (int i = tid; i <= a.p.E; i += kThreadsP)
-            plan.off[i] = clamp_off(a.p.offsets[i], a.p.T);
-        __syncthreads();
-        if (warp == 0) {
-            int at = 0;
-            for (int e0 = 0; e0 < a.p.E; e0 += 32) {
-                const int e = e0 + lane;
-                int n = e < a.p.E ? tiles_of(plan.off[e], plan.off[e + 1], a.tile_n) : 0;
-                int sum = n;
-#pragma unroll
-                for (int d = 1; d < 32; d <<= 1) {
-                    const int o = __shfl_up_sync(0xffffffffu, sum, d);
-                    sum += lane >= d ? o : 0;
-                }
-                if (e < a.p.E)
-                    plan.first[e] = at + sum - n;
-                at += __shfl_sync(0xffffffffu, sum, 31);
-            }
-            if (lane == 0)
-                plan.first[a.p.E] = at;
-        }
-    }
+    if (a.p.offsets)
+        make_plan(plan, a.p.offsets, a.p.E, a.p.T, a.tile_n, tid, kThreadsP);
     fence_before();
     __syncthreads();
     if (PAIR)
@@ -492,7 +317,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) product_kernel(const __grid_cons
                             const float4 f = src[out_at(2 * (lane & 7) + (m & 1) + 16 * (m >> 1))];
                             x[4 * m] = f.x, x[4 * m + 1] = f.y, x[4 * m + 2] = f.z, x[4 * m + 3] = f.w;
                         }
-                        finish<TY, false>(a, tl, t + 16 * g, g ? rs1 : rs0, x, right, lane);
+                        finish<TY, false>(a.p, a.n_out, tl, t + 16 * g, g ? rs1 : rs0, x, right, lane);
                     }
                     asm volatile("bar.sync 1, 128;" ::: "memory");
                 }
@@ -641,9 +466,9 @@ __global__ void __launch_bounds__(kThreadsP, 1) product_kernel(const __grid_cons
                         }
                     }
                 if (shared)
-                    finish<TY, true>(a, tl, t, rs, x, right, lane);
+                    finish<TY, true>(a.p, a.n_out, tl, t, rs, x, right, lane);
                 else
-                    finish<TY, false>(a, tl, t, rs, x, right, lane);
+                    finish<TY, false>(a.p, a.n_out, tl, t, rs, x, right, lane);
             }
         }
         cluster_sync();
@@ -778,8 +603,9 @@ exl3_status product_take_wait_timeouts(unsigned int *n) {
         e = cudaMemcpyToSymbol(g_product_timeouts, &zero, sizeof zero);
     if (e != cudaSuccess)
         return cuda_check(e, "wait timeout count");
-    *n = v;
-    return EXL3_OK;
+    const exl3_status st = few_take_wait_timeouts(n);
+    *n += v;
+    return st;
 }
 
 }  // namespace exl3
