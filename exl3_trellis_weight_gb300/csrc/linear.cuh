@@ -31,7 +31,7 @@ __host__ __device__ inline int64_t act_offset(int64_t NP, int64_t t, int k) {
     return ((int64_t)(k >> 6) * NP + t) * 128 + ((((k >> 3) & 7) ^ (int)(t & 7)) << 4) + (k & 7) * 2;
 }
 
-struct ActLaunch {
+struct PrepLaunch {
     const void *x;            // [T, n] activations, row stride in elements
     int dt;                   // EXL3_BF16 / EXL3_F16
     int64_t T, stride;
@@ -47,11 +47,18 @@ struct ActLaunch {
     // order of 16 neighbouring inputs: place 4j + i holds input 4j + i (0), j + 4i (1)
     // or 2j + i % 2 + 8 (i / 2) (2)
     int order;
+    // beside it, in the same launch (n_adapters > 0):
+    // h[t][r] = gain_i sum_k M[i][r][k] x[t][k], i = slots[t], r < ranks[i] (0 otherwise)
+    const void *M;            // [n_adapters][rank][n]
+    const float *gain;
+    const int32_t *slots, *ranks;
+    int n_adapters, rank;
+    float *h;                 // [T][rank]
 };
-exl3_status launch_act(const ActLaunch &p, cudaStream_t s);
+exl3_status launch_prep(const PrepLaunch &p, cudaStream_t s);
 
 struct ProductLaunch {
-    const unsigned char *image;
+    const unsigned char *image;   // rotated activations (PrepLaunch)
     const float *rscale;
     int64_t T;
     const uint32_t *codes;    // [E][rows/16][cols/16][8 K]
@@ -75,9 +82,9 @@ struct ProductLaunch {
 exl3_status launch_product(const ProductLaunch &p, cudaStream_t s);
 // the same for few tokens (linear_few.cu)
 bool few_eligible(const ProductLaunch &p);
-int few_order(const ProductLaunch &p);     // ActLaunch::order that it reads
-exl3_status launch_product_few(const ProductLaunch &p, cudaStream_t s);
+int few_order(const ProductLaunch &p);     // PrepLaunch::order that it reads
 exl3_status few_take_wait_timeouts(unsigned int *n);
+exl3_status launch_product_few(const ProductLaunch &p, cudaStream_t s);
 
 // h[t][j] = gain_i sum_k M[i][j][k] x[t][k], i = slots[t], j < ranks[i] (0 otherwise)
 struct ShrinkLaunch {

@@ -135,10 +135,10 @@ struct LinearWs {
 
 // y = x W^ (or its transpose), adapters' rank-sided products in h added with B
 exl3_status run_linear(const LinearWs &m, const void *x, int dt, int64_t T, int64_t x_stride, const Coded &w, int E,
-                       const int32_t *offsets, const void *B, const float *h, const Adapters &ad, void *y,
+                       const int32_t *offsets, const void *A, const void *B, float *h, const Adapters &ad, void *y,
                        int64_t y_stride, cudaStream_t s) {
     exl3_status st;
-    ActLaunch a = {};
+    PrepLaunch a = {};
     a.x = x;
     a.dt = dt;
     a.T = T;
@@ -152,6 +152,13 @@ exl3_status run_linear(const LinearWs &m, const void *x, int dt, int64_t T, int6
     a.y = y;
     a.y_stride = y_stride;
     a.y_cols = (int)w.outputs();
+    a.M = A;
+    a.gain = ad.gain;
+    a.slots = ad.slots;
+    a.ranks = ad.ranks;
+    a.n_adapters = ad.n;
+    a.rank = ad.rank;
+    a.h = h;
     ProductLaunch p = {};
     p.image = m.image;
     p.rscale = m.rscale;
@@ -176,7 +183,7 @@ exl3_status run_linear(const LinearWs &m, const void *x, int dt, int64_t T, int6
     p.y_stride = y_stride;
     const bool few = few_eligible(p);
     a.order = few ? few_order(p) : 0;
-    if ((st = launch_act(a, s)) != EXL3_OK) return st;
+    if ((st = launch_prep(a, s)) != EXL3_OK) return st;
     return few ? launch_product_few(p, s) : launch_product(p, s);
 }
 
@@ -248,8 +255,7 @@ exl3_status exl3_linear(const void *x, int dt, int64_t T, int64_t x_stride, cons
     if ((st = check_ws(ws, ws_bytes, m.bytes)) != EXL3_OK) return st;
     if ((st = check_apart(yr, "y", ws, m.bytes, "the workspace")) != EXL3_OK) return st;
     const cudaStream_t s = (cudaStream_t)stream;
-    if (n_adapters && (st = run_shrink(x, dt, T, x_stride, w.inputs(), A, ad, m.h, s)) != EXL3_OK) return st;
-    return run_linear(m, x, dt, T, x_stride, w, 1, nullptr, n_adapters ? B : nullptr, m.h, ad, y, y_stride, s);
+    return run_linear(m, x, dt, T, x_stride, w, 1, nullptr, A, n_adapters ? B : nullptr, m.h, ad, y, y_stride, s);
 }
 
 size_t exl3_linear_backward_workspace_bytes(int64_t T, int64_t rows, int64_t cols, int transposed, int n_adapters,
@@ -288,11 +294,8 @@ exl3_status exl3_linear_backward(const void *dy, int64_t dy_stride, const void *
     if ((st = check_ws(ws, ws_bytes, m.bytes)) != EXL3_OK) return st;
     if ((st = check_apart(dxr, "dx", ws, m.bytes, "the workspace")) != EXL3_OK) return st;
     const cudaStream_t s = (cudaStream_t)stream;
-    if (n_adapters && T) {
-        if ((st = run_shrink(dy, dt, T, dy_stride, n_out, B, ad, m.g, s)) != EXL3_OK) return st;
-        if ((st = run_shrink(x, dt, T, x_stride, n_in, A, ad, m.h, s)) != EXL3_OK) return st;
-    }
-    if (T && (st = run_linear(m, dy, dt, T, dy_stride, w, 1, nullptr, n_adapters ? A : nullptr, m.g, ad, dx, dx_stride,
+    if (n_adapters && T && (st = run_shrink(x, dt, T, x_stride, n_in, A, ad, m.h, s)) != EXL3_OK) return st;
+    if (T && (st = run_linear(m, dy, dt, T, dy_stride, w, 1, nullptr, B, n_adapters ? A : nullptr, m.g, ad, dx, dx_stride,
                               s)) != EXL3_OK)
         return st;
     if (n_adapters) {
@@ -325,7 +328,7 @@ exl3_status exl3_expert_linear(const void *x, int dt, int64_t T, int64_t x_strid
     const LinearWs m(ws, T, w.inputs(), 0, 0, false);
     if ((st = check_ws(ws, ws_bytes, m.bytes)) != EXL3_OK) return st;
     if ((st = check_apart(yr, "y", ws, m.bytes, "the workspace")) != EXL3_OK) return st;
-    return run_linear(m, x, dt, T, x_stride, w, n_experts, offsets, nullptr, nullptr, Adapters{}, y, y_stride,
+    return run_linear(m, x, dt, T, x_stride, w, n_experts, offsets, nullptr, nullptr, nullptr, Adapters{}, y, y_stride,
                       (cudaStream_t)stream);
 }
 

@@ -1,65 +1,59 @@
 // linear_act.cu -- rotated activations: z = (x . left) H per block of 128
 // inputs, one row scale per token, written in binary16 in the order in which
-// linear_product.cu loads its token operand.
-//
-// A row is scaled by a power of two before it is rotated, so that the largest
-// possible element of z (128 times the row's largest product) stays below
-// 2^15: binary16 then holds every element down to 2^-29 of that bound at its
-// full 11 bits, whatever the range of the activations; the scale is exact and
-// leaves again with the row's result.
+// linear_product.cu loads its token operand (linear_few.cu makes its own).
 //
 // Bound by memory: 2 bytes read and 2 written per element.  A thread owns 16
 // consecutive elements (four butterfly spans in registers) and eight threads a
 // block of 128 (three spans by shuffles): 3 shuffles per element instead of the
 // 5 of one element per lane and span.
-#include "linear.cuh"
+#include "linear_rotate.cuh"
 
 namespace exl3 {
 
 namespace {
 
-template <typename TX, bool VEC>
-__device__ __forceinline__ void load16(const TX *p, float (&v)[16]) {
-    if constexpr (VEC) {
-        const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p));
-        const uint4 b = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
-        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+// Adapters' sums beside the rotation: one warp for a row of the token's adapter,
+// 16 products a lane and round, four rounds of loads in flight
+template <typename TX, bool VEC> __device__ __forceinline__ void shrink_rows(const PrepLaunch &a) {
+    const int lane = threadIdx.x & 31;
+    const int r = (blockIdx.y - 1) * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    if (r >= a.rank)
+        return;
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+        const int i = a.slots[t];
+        float s = 0.0f;
+        if (i >= 0 && i < a.n_adapters && r < (a.ranks ? min(max(a.ranks[i], 0), a.rank) : a.rank)) {
+            const TX *x = reinterpret_cast<const TX *>(a.x) + t * a.stride + lane * 8;
+            const TX *m = reinterpret_cast<const TX *>(a.M) + ((size_t)i * a.rank + r) * a.n + lane * 8;
+#pragma unroll 4
+            for (int k = 0; k < a.n; k += 256) {
+                if (k + lane * 8 < a.n) {              // (n is a multiple of 128)
+                    float v[8];
+                    load8<TX, VEC>(x + k, v);
+                    const uint4 w = __ldg(reinterpret_cast<const uint4 *>(m + k));
+                    const uint32_t q[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-            const float2 f = unpack2<TX>(w[i]);
-            v[2 * i] = f.x;
-            v[2 * i + 1] = f.y;
+                    for (int e = 0; e < 4; e++) {
+                        const float2 f = unpack2<TX>(q[e]);
+                        s = __fmaf_rn(v[2 * e], f.x, s);
+                        s = __fmaf_rn(v[2 * e + 1], f.y, s);
+                    }
+                }
+            }
+#pragma unroll
+            for (int d = 16; d; d >>= 1)
+                s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, d));
+            s = __fmul_rn(s, a.gain[i]);
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 16; i++)
-            v[i] = to_f32(p[i]);
+        if (lane == 0)
+            a.h[t * a.rank + r] = s;
     }
 }
 
-__device__ __forceinline__ void mul16(const float *s, float (&v)[16]) {
-    const float4 *q = reinterpret_cast<const float4 *>(s);
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const float4 f = __ldg(q + i);
-        v[4 * i] = __fmul_rn(v[4 * i], f.x);
-        v[4 * i + 1] = __fmul_rn(v[4 * i + 1], f.y);
-        v[4 * i + 2] = __fmul_rn(v[4 * i + 2], f.z);
-        v[4 * i + 3] = __fmul_rn(v[4 * i + 3], f.w);
-    }
-}
-
-__device__ __forceinline__ float max16(const float (&v)[16], float m) {
-#pragma unroll
-    for (int i = 0; i < 16; i++)
-        m = fmaxf(m, fabsf(v[i]));
-    return m;
-}
-
-// grid: rows, one block at a time; block: a multiple of 32 threads, 16 inputs
+// grid: (rows, 1 + adapters' rows), one row at a time; block: a multiple of 32 threads, 16 inputs
 // each.  ONE: the row fits one round of the block and stays in registers.
 template <typename TX, bool VEC, bool ONE>
-__global__ void act_kernel(const ActLaunch a) {
+__global__ void prep_kernel(const PrepLaunch a) {
     __shared__ int32_t off[kMaxExperts + 1];
     __shared__ float wmax[32];
     const int tid = threadIdx.x;
@@ -68,6 +62,10 @@ __global__ void act_kernel(const ActLaunch a) {
     // kernel's end before it reads z.  (This kernel itself starts after everything
     // before it, so the codes are complete.)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (blockIdx.y > 0) {
+        shrink_rows<TX, VEC>(a);
+        return;
+    }
     if (a.offsets) {
         for (int i = tid; i <= a.E; i += blockDim.x)
             off[i] = a.offsets[i];
@@ -103,13 +101,10 @@ __global__ void act_kernel(const ActLaunch a) {
         m = 0.0f;
         for (int w = 0; w < (int)(blockDim.x >> 5); w++)
             m = fmaxf(m, wmax[w]);
-        // 2^(7 - floor(log2 m)): 128 m 2^.. < 2^15; tiny rows stop at 2^107, and an
-        // infinite one (its results are not numbers anyway) is left to overflow
-        int ex = (int)((__float_as_uint(m) >> 23) & 255u) - 127;
-        ex = ex < -100 ? -100 : ex;
-        const float up = __uint_as_float((uint32_t)(127 + 7 - ex) << 23);
+        float up, down;
+        row_scale(m, up, down);
         if (tid == 0)
-            a.rscale[t] = __uint_as_float((uint32_t)(127 + ex - 7) << 23);
+            a.rscale[t] = down;
         for (int k0 = 0; k0 < a.n; k0 += blockDim.x * 16) {
             const int k = k0 + tid * 16;
             const bool in = k < a.n;
@@ -125,22 +120,7 @@ __global__ void act_kernel(const ActLaunch a) {
 #pragma unroll
             for (int i = 0; i < 16; i++)
                 v[i] = __fmul_rn(v[i], up);
-#pragma unroll
-            for (int h = 1; h < 16; h <<= 1)
-#pragma unroll
-                for (int i = 0; i < 16; i++)
-                    if ((i & h) == 0) {
-                        const float p = v[i], q = v[i + h];
-                        v[i] = __fadd_rn(p, q);
-                        v[i + h] = __fsub_rn(p, q);
-                    }
-#pragma unroll
-            for (int h = 1; h < 8; h <<= 1) {
-                const float sg = (tid & h) ? -1.0f : 1.0f;
-#pragma unroll
-                for (int i = 0; i < 16; i++)
-                    v[i] = __fmaf_rn(sg, v[i], __shfl_xor_sync(0xffffffffu, v[i], h));
-            }
+            rotate128(v, tid);
             if (in) {
                 uint32_t w[8];
                 if (a.order == 0) {
@@ -164,27 +144,28 @@ __global__ void act_kernel(const ActLaunch a) {
 }
 
 template <typename TX, bool VEC>
-void launch_act_t(const ActLaunch &p, unsigned grid, unsigned block, bool one, cudaStream_t s) {
+void launch_prep_t(const PrepLaunch &p, dim3 grid, unsigned block, bool one, cudaStream_t s) {
     if (one)
-        act_kernel<TX, VEC, true><<<grid, block, 0, s>>>(p);
+        prep_kernel<TX, VEC, true><<<grid, block, 0, s>>>(p);
     else
-        act_kernel<TX, VEC, false><<<grid, block, 0, s>>>(p);
+        prep_kernel<TX, VEC, false><<<grid, block, 0, s>>>(p);
 }
 
 }  // namespace
 
-exl3_status launch_act(const ActLaunch &p, cudaStream_t s) {
+exl3_status launch_prep(const PrepLaunch &p, cudaStream_t s) {
     const bool vec = ((uintptr_t)p.x & 15u) == 0 && p.stride % 8 == 0;
     unsigned block = (unsigned)((p.n / 16 + 31) / 32 * 32);
     block = block > 1024 ? 1024 : block;
     const bool one = (int64_t)block * 16 >= p.n;
     const int64_t most = (int64_t)device_sm_count() * (2048 / block);
-    const unsigned grid = (unsigned)(p.T < most ? p.T : most);
+    const dim3 grid((unsigned)(p.T < most ? p.T : most),
+                    1 + (p.n_adapters ? (unsigned)((p.rank + block / 32 - 1) / (block / 32)) : 0u));
     if (p.dt == EXL3_BF16)
-        vec ? launch_act_t<__nv_bfloat16, true>(p, grid, block, one, s)
-            : launch_act_t<__nv_bfloat16, false>(p, grid, block, one, s);
+        vec ? launch_prep_t<__nv_bfloat16, true>(p, grid, block, one, s)
+            : launch_prep_t<__nv_bfloat16, false>(p, grid, block, one, s);
     else
-        vec ? launch_act_t<__half, true>(p, grid, block, one, s) : launch_act_t<__half, false>(p, grid, block, one, s);
+        vec ? launch_prep_t<__half, true>(p, grid, block, one, s) : launch_prep_t<__half, false>(p, grid, block, one, s);
     note_launch();
     return cuda_check(cudaGetLastError(), "activation rotation launch");
 }

@@ -14,6 +14,7 @@ __device__ __forceinline__ int rank_of(const int32_t *ranks, int i, int rank) {
 // grid (T, ceil(rank / 8)): one warp per row of the token's adapter
 template <typename TX>
 __global__ void __launch_bounds__(256) shrink_kernel(const ShrinkLaunch a) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int64_t t = blockIdx.x;
     const int j = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (j >= a.rank)

@@ -2,7 +2,7 @@
 // levels of the codes, the list of token tiles, the way from sums to results.
 #pragma once
 
-#include "linear.cuh"
+#include "linear_rotate.cuh"
 
 namespace exl3 {
 
@@ -109,26 +109,6 @@ __device__ __forceinline__ OutTile out_tile(const Plan *plan, int E, int64_t T, 
 // all banks.
 __device__ __forceinline__ int out_at(int f4) { return f4 ^ ((f4 >> 3) & 1); }
 
-// v[8m + i] is output 8u + 64m + i of a token (m < 2, i < 8), u = lane % 8: H over the 128
-__device__ __forceinline__ void rotate_out(float (&v)[16], int lane) {
-#pragma unroll
-    for (int h = 1; h < 16; h <<= 1)
-#pragma unroll
-        for (int i = 0; i < 16; i++)
-            if ((i & h) == 0) {
-                const float p = v[i], q = v[i + h];
-                v[i] = __fadd_rn(p, q);
-                v[i + h] = __fsub_rn(p, q);
-            }
-#pragma unroll
-    for (int h = 1; h < 8; h <<= 1) {
-        const float sg = (lane & h) ? -1.0f : 1.0f;
-#pragma unroll
-        for (int i = 0; i < 16; i++)
-            v[i] = __fmaf_rn(sg, v[i], __shfl_xor_sync(0xffffffffu, v[i], h));
-    }
-}
-
 template <typename TY> __device__ __forceinline__ void fma8(float *v, float h, const uint4 &w) {
     const uint32_t q[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -139,15 +119,46 @@ template <typename TY> __device__ __forceinline__ void fma8(float *v, float h, c
     }
 }
 
-// token t's 16 outputs of this thread: scales, adapter, one rounding.  With SHARED,
-// the four groups of eight threads of a warp hold the same token and a quarter of
-// the adapter's rows each.
-template <typename TY, bool SHARED>
-__device__ __forceinline__ void finish(const ProductLaunch &p, int n_out, const OutTile &tl, int64_t t, float rs, float (&v)[16],
-                                       const float *right, int lane) {
-    rotate_out(v, lane);
-    if (t < tl.lo || t >= tl.hi || tl.f0 >= n_out)
+// v += the adapter term of token t, outputs f0 + 8u + 64m + i (m < 2, i < 8): rows
+// first, first + every, ... of the token's adapter
+template <typename TY>
+__device__ __forceinline__ void add_adapter(const ProductLaunch &p, int n_out, int f0, int64_t t, float (&v)[16], int u,
+                                            int first, int every) {
+    const int ad = p.slots[t];
+    if (ad < 0 || ad >= p.n_adapters)
         return;
+    const int r = p.ranks ? min(max(p.ranks[ad], 0), p.rank) : p.rank;
+    const TY *b = reinterpret_cast<const TY *>(p.B) + (size_t)ad * p.rank * n_out + f0 + 8 * u;
+    const float *h = p.h + t * p.rank;
+    int j = first;
+    for (; j + 3 * every < r; j += 4 * every) {            // four rows in flight
+        float hj[4];
+        uint4 x[4];
+#pragma unroll
+        for (int m = 0; m < 2; m++) {
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                hj[i] = h[j + i * every];
+                x[i] = __ldg(reinterpret_cast<const uint4 *>(b + (size_t)(j + i * every) * n_out + 64 * m));
+            }
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                fma8<TY>(v + 8 * m, hj[i], x[i]);
+        }
+    }
+    for (; j < r; j += every) {
+        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(b + (size_t)j * n_out));
+        const uint4 y = __ldg(reinterpret_cast<const uint4 *>(b + (size_t)j * n_out + 64));
+        fma8<TY>(v, h[j], x);
+        fma8<TY>(v + 8, h[j], y);
+    }
+}
+
+// sums of a token (float4 m of the thread: outputs 8u + 64 (m / 2) + 4 (m % 2) ..) to
+// results in the same places: H over the 128, the row's scale, right . 2^-7 s
+__device__ __forceinline__ void scale_out(float (&v)[16], float rs, const float *right, int lane) {
+    // (the places are those of rotate128 up to the order of the spans)
+    rotate128(v, lane);
     const int u = lane & 7;
 #pragma unroll
     for (int m = 0; m < 4; m++) {
@@ -157,38 +168,12 @@ __device__ __forceinline__ void finish(const ProductLaunch &p, int n_out, const 
         v[4 * m + 2] = __fmul_rn(__fmul_rn(v[4 * m + 2], rs), f.z);
         v[4 * m + 3] = __fmul_rn(__fmul_rn(v[4 * m + 3], rs), f.w);
     }
-    if (p.B) {
-        const int ad = p.slots[t];
-        if (ad >= 0 && ad < p.n_adapters) {
-            const int r = p.ranks ? min(max(p.ranks[ad], 0), p.rank) : p.rank;
-            const TY *b = reinterpret_cast<const TY *>(p.B) + (size_t)ad * p.rank * n_out + tl.f0 + 8 * u;
-            const float *h = p.h + t * p.rank;
-            if (SHARED && lane >= 8) {
-#pragma unroll
-                for (int i = 0; i < 16; i++)
-                    v[i] = 0.0f;
-            }
-#pragma unroll 2
-            for (int j = SHARED ? lane >> 3 : 0; j < r; j += SHARED ? 4 : 1) {
-                const float hj = h[j];
-                const uint4 x = __ldg(reinterpret_cast<const uint4 *>(b + (size_t)j * n_out));
-                const uint4 y = __ldg(reinterpret_cast<const uint4 *>(b + (size_t)j * n_out + 64));
-                fma8<TY>(v, hj, x);
-                fma8<TY>(v + 8, hj, y);
-            }
-            if (SHARED) {
-                __syncwarp();
-#pragma unroll
-                for (int i = 0; i < 16; i++) {
-                    v[i] = __fadd_rn(v[i], __shfl_xor_sync(0xffffffffu, v[i], 8));
-                    v[i] = __fadd_rn(v[i], __shfl_xor_sync(0xffffffffu, v[i], 16));
-                }
-            }
-        }
-        if (SHARED && lane >= 8)
-            return;
-    }
-    TY *y = reinterpret_cast<TY *>(p.y) + t * p.y_stride + tl.f0 + 8 * u;
+}
+
+// one rounding, and out
+template <typename TY>
+__device__ __forceinline__ void store_out(const ProductLaunch &p, int f0, int64_t t, const float (&v)[16], int u) {
+    TY *y = reinterpret_cast<TY *>(p.y) + t * p.y_stride + f0 + 8 * u;
     const bool wide = (((uintptr_t)p.y | (uintptr_t)(p.y_stride * 2)) & 15u) == 0;
 #pragma unroll
     for (int m = 0; m < 2; m++) {
@@ -201,6 +186,21 @@ __device__ __forceinline__ void finish(const ProductLaunch &p, int n_out, const 
             for (int i = 0; i < 8; i++)
                 y[64 * m + i] = from_f32<TY>(v[8 * m + i]);
         }
+    }
+}
+
+// x[4m + i] += sums[from + 16 * out_at(..)] of another block's (or this one's) shared memory
+__device__ __forceinline__ void add_sums(float (&x)[16], uint32_t from, int u) {
+#pragma unroll
+    for (int m = 0; m < 4; m++) {
+        float4 f;
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w)
+                     : "r"(from + 16u * out_at(2 * u + (m & 1) + 16 * (m >> 1))));
+        x[4 * m] = __fadd_rn(x[4 * m], f.x);
+        x[4 * m + 1] = __fadd_rn(x[4 * m + 1], f.y);
+        x[4 * m + 2] = __fadd_rn(x[4 * m + 2], f.z);
+        x[4 * m + 3] = __fadd_rn(x[4 * m + 3], f.w);
     }
 }
 

@@ -12,8 +12,11 @@
 //
 // A block is 8 warps (128 outputs) times kSlices of the inputs; the blocks of a
 // cluster split the inputs further.  Codes arrive in a ring for each warp, the
-// activations of the block's inputs in one go.  Partial sums meet in shared
-// memory, block r of the cluster adds up and finishes tokens r, r + split, ...
+// rotated activations of the block's inputs in one go (rotating them in here took
+// longer, 26 against 22 us at 7 x 12288 x 4096: every block of outputs repeats it,
+// while linear_act.cu overlaps this kernel's start).  Partial sums meet in shared
+// memory, block r of the cluster adds up and finishes tokens r, r + split, ...; the
+// adapters' terms are made before that meeting.
 //
 // Bound by the decode (linear_decode.cuh): 6 cycles of a quarter of an SM for 32
 // weights, against 8 of its matrix pipe for 256 weights and 8 tokens.
@@ -59,7 +62,7 @@ template <int B> __device__ __forceinline__ uint32_t cut(uint32_t t) {
 // distance is a whole number of bytes come out of one shifted word in one
 // instruction each (x W^^T; in x W^ a lane takes rows 4j .. 4j + 3, and outputs
 // g and g + 8 where eight weights are one or two bytes).  The activations are
-// stored in that order (act_order).
+// stored in that order (few_order).
 struct Lane {
     uint32_t last, before, sh;             // byte offsets of the first row's word and of the one before it
     uint32_t last1, sh1;                   // x W^ at K = 3: of the second row
@@ -142,9 +145,9 @@ __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uin
 template <int K, bool TR, int NB, typename TY>
 __global__ void __launch_bounds__(kThreadsF, 2) few_kernel(const __grid_constant__ FewArgs a) {
     extern __shared__ unsigned char smem_raw[];
-    __shared__ __align__(8) unsigned long long bar_z;
     __shared__ Plan plan;
     __shared__ __align__(16) float right[128];
+    __shared__ __align__(8) unsigned long long bar_z;
     __shared__ int gave_up;
     const uint32_t base = (saddr(smem_raw) + 1023u) & ~1023u;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -167,13 +170,14 @@ __global__ void __launch_bounds__(kThreadsF, 2) few_kernel(const __grid_constant
         return;
     }
     const OutTile tl = out_tile(p.offsets ? &plan : nullptr, p.E, p.T, a.tile_n, a.n_out / 128, 128, it);
-    // inputs of this block in blocks of 64, of this warp in tiles of 16
-    const int steps = a.n_in / 64;
-    const int k_lo = (int)((int64_t)steps * rank / a.split), k_hi = (int)((int64_t)steps * (rank + 1) / a.split);
+    // inputs of this block in blocks of 64 (an even number), of this warp in tiles of 16
+    const int steps = a.n_in / 128;
+    const int k_lo = steps * rank / a.split * 2, k_hi = steps * (rank + 1) / a.split * 2;
     const int fw = warp & 7, slice = warp >> 3;
     const int q_lo = (k_hi - k_lo) * slice / kSlices * 4, q_hi = (k_hi - k_lo) * (slice + 1) / kSlices * 4;
+    const int n = (int)(tl.hi - tl.t0);                       // tokens
+    const int rows_z = (n + 7) / 8 * 8;                       // token rows to load
     const int64_t NP = act_rows(p.T);
-    const int rows_z = min(NB * 8, (int)((tl.hi - tl.t0 + 7) / 8 * 8));       // token rows to load
 
     // codes: a warp's tiles follow each other along a tile row (TR) or down a tile column
     const int64_t tiles_c = p.cols / 16;
@@ -215,10 +219,8 @@ __global__ void __launch_bounds__(kThreadsF, 2) few_kernel(const __grid_constant
 #pragma unroll
         for (int i = 0; i < 4; i++)
             acc[b][i] = 0.0f;
-    bool ok = bar_wait(full, 0, &gave_up, &g_few_timeouts);
-    ok = __all_sync(0xffffffffu, ok);
-    // blocks of 8 tokens that hold any
-    const int blocks = (rows_z + 7) / 8;
+    const int blocks = rows_z / 8;         // blocks of 8 tokens that hold any
+    const bool ok = __all_sync(0xffffffffu, bar_wait(full, 0, &gave_up, &g_few_timeouts));
     const Lane l = lane_of<K, TR>(g, j);
     uint32_t tiles = ring;
     // token g's four inputs of tile i: 8 bytes of chunk 2 i + j / 2 of its row
@@ -259,44 +261,60 @@ __global__ void __launch_bounds__(kThreadsF, 2) few_kernel(const __grid_constant
             const int o = fw * 16 + (TR || K <= 2 ? g + 8 * (i >> 1) : 2 * g + (i >> 1)), t = b * 8 + 2 * j + (i & 1);
             sums[(slice * NB * 8 + t) * 128 + 4 * out_at(o >> 2) + (o & 3)] = acc[b][i];
         }
+    // a warp takes four tokens at a time, with adapters one (its four groups of eight
+    // lanes a quarter of the adapter's rows each, in the first round before the sums)
+    const bool shared = p.B != nullptr;
+    const int each = shared ? 1 : 4, sub = shared ? 0 : lane >> 3, u = lane & 7;
+    const int mine = (n + a.split - 1 - rank) / a.split;
+    float v[16];
+    auto adapter = [&](int i) {
+#pragma unroll
+        for (int m = 0; m < 16; m++)
+            v[m] = 0.0f;
+        const int64_t t = tl.t0 + rank + i * a.split;
+        if (i >= mine || t < tl.lo)
+            return;
+        add_adapter<TY>(p, a.n_out, tl.f0, t, v, u, lane >> 3, 4);
+        __syncwarp();
+#pragma unroll
+        for (int m = 0; m < 16; m++) {
+            v[m] = __fadd_rn(v[m], __shfl_xor_sync(0xffffffffu, v[m], 8));
+            v[m] = __fadd_rn(v[m], __shfl_xor_sync(0xffffffffu, v[m], 16));
+        }
+    };
+    if (shared)
+        adapter(warp);
     if (a.split > 1)
         cluster_sync();
     else
         __syncthreads();
-    const int n = (int)(tl.hi - tl.t0);
-    // a warp takes four tokens at a time, with adapters one
-    const bool shared = p.B != nullptr;
-    const int each = shared ? 1 : 4, sub = shared ? 0 : lane >> 3;
-    const int mine = (n + a.split - 1 - rank) / a.split;
     for (int i = warp * each; i < mine; i += kWarps * each) {
         const int row = rank + (i + sub) * a.split;
         const int64_t t = row < n ? tl.t0 + row : tl.hi;
         const float rs = t < tl.hi ? p.rscale[t] : 0.0f;
+        if (shared && i != warp)
+            adapter(i);
         float x[16];
 #pragma unroll
         for (int m = 0; m < 16; m++)
             x[m] = 0.0f;
         if (row < n)
-            for (int b = 0; b < a.split * kSlices; b++) {
-                const uint32_t at = base + (uint32_t)(((b % kSlices) * NB * 8 + row) * 512);
-                const uint32_t from = at_block(at, b / kSlices);
+#pragma unroll 1
+            for (int b = 0; b < a.split; b++) {
+                const uint32_t from = at_block(base + (uint32_t)row * 512u, b);
 #pragma unroll
-                for (int m = 0; m < 4; m++) {
-                    float4 f;
-                    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                                 : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w)
-                                 : "r"(from + 16u * out_at(2 * (lane & 7) + (m & 1) + 16 * (m >> 1)))
-                                 : "memory");
-                    x[4 * m] = __fadd_rn(x[4 * m], f.x);
-                    x[4 * m + 1] = __fadd_rn(x[4 * m + 1], f.y);
-                    x[4 * m + 2] = __fadd_rn(x[4 * m + 2], f.z);
-                    x[4 * m + 3] = __fadd_rn(x[4 * m + 3], f.w);
-                }
+                for (int s = 0; s < kSlices; s++)
+                    add_sums(x, from + (uint32_t)(s * NB * 8 * 512), u);
             }
-        if (shared)
-            finish<TY, true>(p, a.n_out, tl, t, rs, x, right, lane);
-        else
-            finish<TY, false>(p, a.n_out, tl, t, rs, x, right, lane);
+        scale_out(x, rs, right, lane);
+        if (t >= tl.lo && t < tl.hi && (!shared || lane < 8)) {
+            if (shared) {
+#pragma unroll
+                for (int m = 0; m < 16; m++)
+                    x[m] = __fadd_rn(x[m], v[m]);
+            }
+            store_out<TY>(p, tl.f0, t, x, u);
+        }
     }
     if (gave_up && warp == 1)
         bar_drain(full, 0);                // nothing may be in flight when the block ends
@@ -352,6 +370,7 @@ template <typename TY> exl3_status launch_few_k(const FewArgs &a, unsigned grid,
 
 }  // namespace
 
+// lane j's four inputs are places 4j .. 4j + 3 of 16
 int few_order(const ProductLaunch &p) { return !p.transposed || p.K == 3 ? 0 : p.K == 1 ? 2 : 1; }
 
 namespace {
@@ -372,15 +391,15 @@ bool plan_few(const ProductLaunch &p, FewArgs &a, unsigned &grid, uint32_t &smem
     const int64_t used = p.T < p.E ? p.T : p.E;
     const int64_t tok = p.offsets ? used + (p.T + 7 * used) / a.tile_n + 1 : (p.T + a.tile_n - 1) / a.tile_n;
     const int64_t tiles = tok * (a.n_out / 128);
-    // blocks that would idle share the inputs of the tiles, at least 2 blocks of 64 each
-    const int steps = a.n_in / 64;
+    // blocks that would idle share the inputs of the tiles, at least a block of 128 each
+    const int steps = a.n_in / 128;
     const uint32_t sums = (uint32_t)(kSlices * a.tile_n * 512), ring = kWarps * kTilesAhead * 32u * p.K;
     auto z_bytes = [&](int split) {
-        const uint32_t z = (uint32_t)((steps + split - 1) / split) * (uint32_t)a.tile_n * 128u;
+        const uint32_t z = (uint32_t)((steps + split - 1) / split) * (uint32_t)a.tile_n * 256u;
         return z > sums ? z : sums;
     };
     a.split = 1;
-    while (a.split < 8 && ((tiles * a.split * 2 <= 2 * sms && steps >= a.split * 2 * 2) ||
+    while (a.split < 8 && ((tiles * a.split * 2 <= 2 * sms && steps >= a.split * 2) ||
                            z_bytes(a.split) + ring > 200u * 1024u))
         a.split *= 2;
     a.ring_off = z_bytes(a.split);

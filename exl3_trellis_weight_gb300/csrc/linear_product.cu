@@ -317,7 +317,12 @@ __global__ void __launch_bounds__(kThreadsP, 1) product_kernel(const __grid_cons
                             const float4 f = src[out_at(2 * (lane & 7) + (m & 1) + 16 * (m >> 1))];
                             x[4 * m] = f.x, x[4 * m + 1] = f.y, x[4 * m + 2] = f.z, x[4 * m + 3] = f.w;
                         }
-                        finish<TY, false>(a.p, a.n_out, tl, t + 16 * g, g ? rs1 : rs0, x, right, lane);
+                        scale_out(x, g ? rs1 : rs0, right, lane);
+                        if (t + 16 * g >= tl.lo && t + 16 * g < tl.hi && tl.f0 < a.n_out) {
+                            if (a.p.B)
+                                add_adapter<TY>(a.p, a.n_out, tl.f0, t + 16 * g, x, lane & 7, 0, 1);
+                            store_out<TY>(a.p, tl.f0, t + 16 * g, x, lane & 7);
+                        }
                     }
                     asm volatile("bar.sync 1, 128;" ::: "memory");
                 }
@@ -435,40 +440,27 @@ __global__ void __launch_bounds__(kThreadsP, 1) product_kernel(const __grid_cons
         cluster_sync();
         if (it0 < n_tiles && warp < kDecWarps + kOutWarps) {
             const Tile tl = make_tile<PAIR>(a, &plan, it0, rank);
-            // a warp takes four tokens at a time, with adapters one
-            const bool shared = a.p.B != nullptr;
-            const int each = shared ? 1 : 4, sub = shared ? 0 : lane >> 3;
+            // a warp takes four tokens at a time
             const int mine = (tl.n + a.split - 1 - rank) / a.split;          // tokens rank, rank + split, ...
-            for (int i = warp * each; i < mine; i += (kDecWarps + kOutWarps) * each) {
-                const int row = rank + (i + sub) * a.split;
+            for (int i = warp * 4; i < mine; i += (kDecWarps + kOutWarps) * 4) {
+                const int row = rank + (i + (lane >> 3)) * a.split;
                 const bool in = row < tl.n;
+                const int64_t t = in ? tl.t0 + row : tl.hi;
+                const float rs = t < tl.hi ? a.p.rscale[t] : 0.0f;
                 float x[16];
 #pragma unroll
                 for (int j = 0; j < 16; j++)
                     x[j] = 0.0f;
-                const int64_t t = in ? tl.t0 + row : tl.hi;
-                const float rs = t < tl.hi ? a.p.rscale[t] : 0.0f;
                 if (in)
-#pragma unroll 1
-                    for (int b = 0; b < a.split; b++) {
-                        const uint32_t from = at_block(base + (uint32_t)row * 512u, b);
-#pragma unroll
-                        for (int m = 0; m < 4; m++) {
-                            float4 f;
-                            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                                         : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w)
-                                         : "r"(from + 16u * out_at(2 * (lane & 7) + (m & 1) + 16 * (m >> 1)))
-                                         : "memory");
-                            x[4 * m] = __fadd_rn(x[4 * m], f.x);
-                            x[4 * m + 1] = __fadd_rn(x[4 * m + 1], f.y);
-                            x[4 * m + 2] = __fadd_rn(x[4 * m + 2], f.z);
-                            x[4 * m + 3] = __fadd_rn(x[4 * m + 3], f.w);
-                        }
-                    }
-                if (shared)
-                    finish<TY, true>(a.p, a.n_out, tl, t, rs, x, right, lane);
-                else
-                    finish<TY, false>(a.p, a.n_out, tl, t, rs, x, right, lane);
+#pragma unroll 2
+                    for (int b = 0; b < a.split; b++)
+                        add_sums(x, at_block(base + (uint32_t)row * 512u, b), lane & 7);
+                scale_out(x, rs, right, lane);
+                if (t >= tl.lo && t < tl.hi) {
+                    if (a.p.B)
+                        add_adapter<TY>(a.p, a.n_out, tl.f0, t, x, lane & 7, 0, 1);
+                    store_out<TY>(a.p, tl.f0, t, x, lane & 7);
+                }
             }
         }
         cluster_sync();
