@@ -69,9 +69,10 @@ struct ProductLaunch {
     int transposed;
     const int32_t *offsets;   // [E + 1] or nullptr
     int E;                    // 1 when offsets == nullptr
-    // adapters added in the epilogue: y_t += sum_j h[t][j] B[slot_t][j]
+    // adapters: h != nullptr adds sum_j h[t][j] B[slot_t][j] to the result; h == nullptr
+    // adds what y holds of tokens with an adapter (launch_expand)
     const void *B;            // nullable, [n_adapters][rank][outputs], dtype dt
-    const float *h;           // [T][rank]
+    const float *h;           // nullable, [T][rank]
     const int32_t *slots;     // [T]
     const int32_t *ranks;     // nullable, [n_adapters]
     int n_adapters, rank;
@@ -86,32 +87,41 @@ int few_order(const ProductLaunch &p);     // PrepLaunch::order that it reads
 exl3_status few_take_wait_timeouts(unsigned int *n);
 exl3_status launch_product_few(const ProductLaunch &p, cudaStream_t s);
 
-// h[t][j] = gain_i sum_k M[i][j][k] x[t][k], i = slots[t], j < ranks[i] (0 otherwise)
-struct ShrinkLaunch {
-    const void *x;
-    int dt;
-    int64_t T, stride;
+// Adapters of more than a few tokens (linear_adapt.cu), tokens sorted by adapter
+struct AdaptPlan {
+    int32_t *perm;            // [T] tokens by adapter (those without one left out)
+    int32_t *seg, *first;     // [n + 1] where an adapter's tokens and its tiles of 32 begin
+    uint32_t *largest;        // [2][n]
+};
+size_t adapt_plan_ints(int64_t T, int n);
+AdaptPlan adapt_plan(int32_t *ints, int64_t T, int n);
+
+struct AdaptSide {
+    const void *x;            // [T, n] activations
+    int64_t stride;
     int n;
     const void *M;            // [n_adapters][rank][n]
+    float *h;                 // [T][rank]; only rows of tokens with an adapter are written
+    uint32_t *largest;        // [n_adapters] bits of the largest |h|
+    void *dM;                 // like M
+};
+struct AdaptLaunch {
+    AdaptPlan plan;
+    int dt;
+    int64_t T;
+    int n, rank;              // adapters, and their rows
     const float *gain;
     const int32_t *slots, *ranks;
-    int n_adapters, rank;
-    float *h;                 // [T][rank]
+    AdaptSide side[2];
+    int split;                // (set by the launchers)
 };
-exl3_status launch_shrink(const ShrinkLaunch &p, cudaStream_t s);
-
-// dM[i][j][k] = sum over tokens t of adapter i of h[t][j] x[t][k]
-struct OuterLaunch {
-    const float *h;
-    const void *x;
-    int dt;
-    int64_t T, stride;
-    int n;
-    const int32_t *slots, *ranks;
-    int n_adapters, rank;
-    void *dM;                 // [n_adapters][rank][n]
-};
-exl3_status launch_outer(const OuterLaunch &p, cudaStream_t s);
+exl3_status launch_adapt_plan(const AdaptLaunch &p, cudaStream_t s);
+// sides 0 .. sides - 1: h[t] = gain_i M_i x_t
+exl3_status launch_shrink(const AdaptLaunch &p, int sides, cudaStream_t s);
+// y[t] = sum_r h[t][r] M_i[r] with side 0's h and M (n outputs); rows without an adapter stay
+exl3_status launch_expand(const AdaptLaunch &p, void *y, int64_t y_stride, cudaStream_t s);
+// both sides: dM_i[r] = sum_{t of i} h[t][r] x_t
+exl3_status launch_outer(const AdaptLaunch &p, cudaStream_t s);
 
 template <typename T> __device__ __forceinline__ float to_f32(T v);
 template <> __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }

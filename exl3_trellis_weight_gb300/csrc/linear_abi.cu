@@ -122,6 +122,7 @@ struct LinearWs {
     unsigned char *image;     // rotated activations
     float *rscale;            // [T]
     float *h, *g;             // [T][rank]: x A^T and, for the gradient, dy B^T
+    int32_t *plan;            // tokens by adapter
     size_t bytes;
     LinearWs(void *ws, int64_t T, int64_t inputs, int n, int rank, bool grad) {
         Carve c{(unsigned char *)ws};
@@ -129,6 +130,7 @@ struct LinearWs {
         rscale = c.take<float>((size_t)T);
         h = n ? c.take<float>((size_t)T * rank) : nullptr;
         g = n && grad ? c.take<float>((size_t)T * rank) : nullptr;
+        plan = n ? c.take<int32_t>(adapt_plan_ints(T, n)) : nullptr;
         bytes = c.used;
     }
 };
@@ -156,7 +158,7 @@ exl3_status run_linear(const LinearWs &m, const void *x, int dt, int64_t T, int6
     a.gain = ad.gain;
     a.slots = ad.slots;
     a.ranks = ad.ranks;
-    a.n_adapters = ad.n;
+    a.n_adapters = A ? ad.n : 0;
     a.rank = ad.rank;
     a.h = h;
     ProductLaunch p = {};
@@ -187,40 +189,22 @@ exl3_status run_linear(const LinearWs &m, const void *x, int dt, int64_t T, int6
     return few ? launch_product_few(p, s) : launch_product(p, s);
 }
 
-exl3_status run_shrink(const void *x, int dt, int64_t T, int64_t stride, int64_t n, const void *M, const Adapters &ad,
-                       float *h, cudaStream_t s) {
-    ShrinkLaunch p = {};
-    p.x = x;
+AdaptLaunch adapt_of(const LinearWs &m, int dt, int64_t T, const Adapters &ad) {
+    AdaptLaunch p = {};
+    p.plan = adapt_plan(m.plan, T, ad.n);
     p.dt = dt;
     p.T = T;
-    p.stride = stride;
-    p.n = (int)n;
-    p.M = M;
+    p.n = ad.n;
+    p.rank = ad.rank;
     p.gain = ad.gain;
     p.slots = ad.slots;
     p.ranks = ad.ranks;
-    p.n_adapters = ad.n;
-    p.rank = ad.rank;
-    p.h = h;
-    return launch_shrink(p, s);
+    return p;
 }
 
-exl3_status run_outer(const float *h, const void *x, int dt, int64_t T, int64_t stride, int64_t n, const Adapters &ad,
-                      void *dM, cudaStream_t s) {
-    OuterLaunch p = {};
-    p.h = h;
-    p.x = x;
-    p.dt = dt;
-    p.T = T;
-    p.stride = stride;
-    p.n = (int)n;
-    p.slots = ad.slots;
-    p.ranks = ad.ranks;
-    p.n_adapters = ad.n;
-    p.rank = ad.rank;
-    p.dM = dM;
-    return launch_outer(p, s);
-}
+// up to here each token's adapter is multiplied on its own (rotation and coded product
+// carry it along); with more the tokens are sorted by adapter and multiplied in tiles
+constexpr int64_t kFewTokens = 64;
 
 bool sizes_ok(int64_t T, int64_t rows, int64_t cols, int n, int rank) {
     return T >= 0 && T <= kMaxTokens && side_ok(rows) && side_ok(cols) && adapters_ok(n, rank);
@@ -255,6 +239,16 @@ exl3_status exl3_linear(const void *x, int dt, int64_t T, int64_t x_stride, cons
     if ((st = check_ws(ws, ws_bytes, m.bytes)) != EXL3_OK) return st;
     if ((st = check_apart(yr, "y", ws, m.bytes, "the workspace")) != EXL3_OK) return st;
     const cudaStream_t s = (cudaStream_t)stream;
+    if (n_adapters && T > kFewTokens) {
+        AdaptLaunch p = adapt_of(m, dt, T, ad);
+        p.side[0] = {x, x_stride, (int)w.inputs(), A, m.h, p.plan.largest, nullptr};
+        if ((st = launch_adapt_plan(p, s)) != EXL3_OK) return st;
+        if ((st = launch_shrink(p, 1, s)) != EXL3_OK) return st;
+        p.side[0].M = B;
+        p.side[0].n = (int)w.outputs();
+        if ((st = launch_expand(p, y, y_stride, s)) != EXL3_OK) return st;
+        return run_linear(m, x, dt, T, x_stride, w, 1, nullptr, nullptr, B, nullptr, ad, y, y_stride, s);
+    }
     return run_linear(m, x, dt, T, x_stride, w, 1, nullptr, A, n_adapters ? B : nullptr, m.h, ad, y, y_stride, s);
 }
 
@@ -294,15 +288,28 @@ exl3_status exl3_linear_backward(const void *dy, int64_t dy_stride, const void *
     if ((st = check_ws(ws, ws_bytes, m.bytes)) != EXL3_OK) return st;
     if ((st = check_apart(dxr, "dx", ws, m.bytes, "the workspace")) != EXL3_OK) return st;
     const cudaStream_t s = (cudaStream_t)stream;
-    if (n_adapters && T && (st = run_shrink(x, dt, T, x_stride, n_in, A, ad, m.h, s)) != EXL3_OK) return st;
-    if (T && (st = run_linear(m, dy, dt, T, dy_stride, w, 1, nullptr, B, n_adapters ? A : nullptr, m.g, ad, dx, dx_stride,
-                              s)) != EXL3_OK)
-        return st;
-    if (n_adapters) {
-        if ((st = run_outer(m.g, x, dt, T, x_stride, n_in, ad, dA, s)) != EXL3_OK) return st;
-        if ((st = run_outer(m.h, dy, dt, T, dy_stride, n_out, ad, dB, s)) != EXL3_OK) return st;
+    if (n_adapters == 0)
+        return run_linear(m, dy, dt, T, dy_stride, w, 1, nullptr, nullptr, nullptr, nullptr, ad, dx, dx_stride, s);
+    AdaptLaunch p = adapt_of(m, dt, T, ad);
+    p.side[0] = {x, x_stride, (int)n_in, A, m.h, p.plan.largest, dA};
+    p.side[1] = {dy, dy_stride, (int)n_out, B, m.g, p.plan.largest + ad.n, dB};
+    if ((st = launch_adapt_plan(p, s)) != EXL3_OK) return st;
+    if (T) {
+        if ((st = launch_shrink(p, 2, s)) != EXL3_OK) return st;
+        AdaptLaunch q = p;
+        q.side[0] = {nullptr, 0, (int)n_in, A, m.g, nullptr, nullptr};
+        const bool few = T <= kFewTokens;                 // the coded product adds the adapters' terms itself
+        if (!few && (st = launch_expand(q, dx, dx_stride, s)) != EXL3_OK) return st;
+        if ((st = run_linear(m, dy, dt, T, dy_stride, w, 1, nullptr, nullptr, A, few ? m.g : nullptr, ad, dx, dx_stride,
+                             s)) != EXL3_OK)
+            return st;
     }
-    return EXL3_OK;
+    // dA = sum g x^T, dB = sum h dy^T
+    p.side[0].h = m.g;
+    p.side[0].largest = p.plan.largest + ad.n;
+    p.side[1].h = m.h;
+    p.side[1].largest = p.plan.largest;
+    return launch_outer(p, s);
 }
 
 size_t exl3_expert_linear_workspace_bytes(int64_t T, int64_t rows, int64_t cols, int transposed) {

@@ -1,72 +1,598 @@
-// linear_adapt.cu -- low-rank adapters of many requests: the products with the
-// rank-sized side (shrink) and the sums of outer products that are their
-// gradients (outer).  Simple form.
+// linear_adapt.cu -- low-rank adapters of many requests when there are more than a
+// few tokens: the sums with the rank-sided factor (shrink), the way back (expand)
+// and the sums of outer products that are the factors' gradients (outer).
+//
+// A plan sorts the tokens by adapter (in their order inside one) and cuts each
+// adapter's into tiles of 32, so that a tile multiplies by one factor; the host
+// never learns the sizes.  The products are a few per cent of the coded product's
+// and bound by reading the activations once: m16n8k16 instructions from shared
+// memory, fed by asynchronous copies of gathered rows, are far from the limit.
+//
+// h = gain A x is kept in binary32.  Where it becomes an operand again it is
+// rounded once to the activations' type; binary16 gets a power of two for each
+// tile (expand) or adapter (outer) first, so that its range does not matter.
 #include "linear.cuh"
+#include "tc.cuh"
 
 namespace exl3 {
 
 namespace {
 
+using namespace tc;
+
+constexpr int kTile = 32;                  // tokens of a tile
+constexpr int kPad = 8;                    // elements behind a shared-memory row: conflict-free fragments
+
 __device__ __forceinline__ int rank_of(const int32_t *ranks, int i, int rank) {
     return ranks ? min(max(ranks[i], 0), rank) : rank;
 }
 
-// grid (T, ceil(rank / 8)): one warp per row of the token's adapter
-template <typename TX>
-__global__ void __launch_bounds__(256) shrink_kernel(const ShrinkLaunch a) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int64_t t = blockIdx.x;
-    const int j = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (j >= a.rank)
-        return;
-    const int i = a.slots[t];
-    float s = 0.0f;
-    if (i >= 0 && i < a.n_adapters && j < rank_of(a.ranks, i, a.rank)) {
-        const TX *x = reinterpret_cast<const TX *>(a.x) + t * a.stride;
-        const TX *m = reinterpret_cast<const TX *>(a.M) + ((size_t)i * a.rank + j) * a.n;
-        for (int k = lane; k < a.n; k += 32)
-            s = __fmaf_rn(to_f32(x[k]), to_f32(m[k]), s);
-#pragma unroll
-        for (int d = 16; d; d >>= 1)
-            s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, d));
-        s = __fmul_rn(s, a.gain[i]);
-    }
-    if (lane == 0)
-        a.h[t * a.rank + j] = s;
+// 16 bytes, or zeros
+__device__ __forceinline__ void copy16z(uint32_t dst, const void *src, bool real) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"((uint64_t)__cvta_generic_to_global(src)),
+                 "r"(real ? 16 : 0)
+                 : "memory");
 }
 
-// grid (n / 128, rank, n_adapters)
-template <typename TX>
-__global__ void __launch_bounds__(128) outer_kernel(const OuterLaunch a) {
-    const int k = blockIdx.x * 128 + threadIdx.x, j = blockIdx.y, i = blockIdx.z;
-    float s = 0.0f;
-    if (j < rank_of(a.ranks, i, a.rank))
-        for (int64_t t = 0; t < a.T; t++)
-            if (a.slots[t] == i)
-                s = __fmaf_rn(a.h[t * a.rank + j], to_f32(reinterpret_cast<const TX *>(a.x)[t * a.stride + k]), s);
-    reinterpret_cast<TX *>(a.dM)[((size_t)i * a.rank + j) * a.n + k] = from_f32<TX>(s);
+// eight neighbouring elements of a row to shared memory, asynchronously where the
+// rows are aligned
+template <bool VEC> __device__ __forceinline__ void row8(uint32_t dst, const uint16_t *src, bool real) {
+    if constexpr (VEC) {
+        copy16z(dst, src, real);
+    } else {
+        uint32_t w[4] = {0, 0, 0, 0};
+        if (real)
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                w[i] = (uint32_t)src[2 * i] | (uint32_t)src[2 * i + 1] << 16;
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                     : "memory");
+    }
 }
+
+template <typename TX> __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
+template <>
+__device__ __forceinline__ void mma<__half>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma<__nv_bfloat16>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// four 8 x 8 blocks, transposed; lane l names row l % 8 of block l / 8
+__device__ __forceinline__ void load_t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
+}
+
+// the power of two that takes m to [2^7, 2^8); none for bfloat16, whose range is binary32's
+template <typename TX> __device__ __forceinline__ void operand_scale(float m, float &up, float &down) {
+    up = down = 1.0f;
+    if (__is_same(TX, __half) && m > 0.0f && m < 3.0e38f) {
+        const int e = max((int)(__float_as_uint(m) >> 23) - 127, -100);
+        up = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
+        down = __uint_as_float((uint32_t)(127 - 7 + e) << 23);
+    }
+}
+
+// ---- plan --------------------------------------------------------------------
+// grid: 32 adapters a block, one a warp.  perm: tokens by adapter, seg: where each
+// adapter's begin, first: its tiles.
+__global__ void __launch_bounds__(1024) plan_kernel(const AdaptLaunch a) {
+    __shared__ int count[kMaxAdapters], sums[2][32];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    count[tid] = 0;
+    __syncthreads();
+    for (int64_t t = tid; t < a.T; t += 1024) {
+        const int s = a.slots[t];
+        if (s >= 0 && s < a.n)
+            atomicAdd(&count[s], 1);
+    }
+    __syncthreads();
+    // exclusive sums over the adapters, of tokens and of tiles
+    const int c = count[tid];
+    int own[2] = {c, (c + kTile - 1) / kTile}, sum[2] = {own[0], own[1]};
+#pragma unroll
+    for (int k = 0; k < 2; k++) {
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, sum[k], d);
+            sum[k] += lane >= d ? o : 0;
+        }
+        if (lane == 31)
+            sums[k][warp] = sum[k];
+    }
+    __syncthreads();
+    int at[2];
+#pragma unroll
+    for (int k = 0; k < 2; k++) {
+        const int s = sums[k][lane];
+        int before = lane < warp ? s : 0;
+#pragma unroll
+        for (int d = 16; d; d >>= 1)
+            before += __shfl_xor_sync(0xffffffffu, before, d);
+        at[k] = before + sum[k] - own[k];
+    }
+    if (blockIdx.x == 0 && tid < a.n) {
+        a.plan.seg[tid] = at[0];
+        a.plan.first[tid] = at[1];
+        a.plan.largest[tid] = a.plan.largest[a.n + tid] = 0u;
+        if (tid == a.n - 1) {
+            a.plan.seg[a.n] = at[0] + own[0];
+            a.plan.first[a.n] = at[1] + own[1];
+        }
+    }
+    __syncthreads();
+    count[tid] = at[0];
+    __syncthreads();
+    const int i = blockIdx.x * 32 + warp;
+    if (i >= a.n)
+        return;
+    int32_t *to = a.plan.perm + count[i];
+#pragma unroll 4
+    for (int64_t t0 = 0; t0 < a.T; t0 += 32) {
+        const int64_t t = t0 + lane;
+        const bool mine = t < a.T && a.slots[t] == i;
+        const unsigned b = __ballot_sync(0xffffffffu, mine);
+        if (mine)
+            to[__popc(b & ((1u << lane) - 1u))] = (int32_t)t;
+        to += __popc(b);
+    }
+}
+
+// tile -> adapter and its tokens [lo, lo + n) of perm; false when there is no such tile
+__device__ __forceinline__ bool find_tile(const AdaptLaunch &a, int tile, int &i, int &lo, int &n) {
+    if (tile >= a.plan.first[a.n])
+        return false;
+    int l = 0, h = a.n - 1;                // last adapter with first <= tile
+    while (l < h) {
+        const int m = (l + h + 1) >> 1;
+        if (a.plan.first[m] <= tile)
+            l = m;
+        else
+            h = m - 1;
+    }
+    i = l;
+    lo = a.plan.seg[l] + (tile - a.plan.first[l]) * kTile;
+    n = min(kTile, a.plan.seg[l + 1] - lo);
+    return true;
+}
+
+// ---- shrink: h[t][r] = gain_i sum_k M_i[r][k] x[t][k] ---------------------------
+// A block takes one tile and a share of the sum (the blocks of a cluster split it);
+// warp w the tokens 16 (w % 2) .. and the sixteenth w / 2 of every step of 64.
+constexpr int kShrinkStages = 4;
+constexpr int kRow = 64 + kPad;
+
+template <typename TX, bool VEC> __global__ void __launch_bounds__(256) shrink_kernel(const AdaptLaunch a) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    const AdaptSide &sd = a.side[blockIdx.y];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, j = lane & 3;
+    const int rank = (int)(blockIdx.x % a.split);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    int i, lo, n;
+    if (!find_tile(a, (int)(blockIdx.x / a.split), i, lo, n))
+        return;                            // (the whole cluster)
+    const int r = rank_of(a.ranks, i, a.rank), R8 = (a.rank + 7) / 8 * 8, nb = (r + 7) / 8;
+    const int steps = sd.n / 64, k_lo = steps * rank / a.split, k_hi = steps * (rank + 1) / a.split;
+    const uint32_t base = saddr(smem), stage = (uint32_t)(kTile + R8) * kRow * 2;
+    const uint16_t *x = reinterpret_cast<const uint16_t *>(sd.x);
+    const uint16_t *M = reinterpret_cast<const uint16_t *>(sd.M) + (size_t)i * a.rank * sd.n;
+    // copies of a step: token tid / 8 and rows tid / 8 + 32 m of the factor, 8 elements each
+    const int row = tid >> 3, c8 = (tid & 7) * 8;
+    const bool real = row < n;
+    const uint16_t *xr = x + (int64_t)(real ? a.plan.perm[lo + row] : 0) * sd.stride + c8;
+    auto load = [&](int k) {
+        if (k < k_hi) {
+            const uint32_t st = base + (uint32_t)((k - k_lo) % kShrinkStages) * stage;
+            row8<VEC>(st + (uint32_t)(row * kRow + c8) * 2, xr + (int64_t)k * 64, real);
+            for (int q = row; q < nb * 8; q += 32)
+                copy16z(st + (uint32_t)((kTile + q) * kRow + c8) * 2, M + (size_t)min(q, a.rank - 1) * sd.n + k * 64 + c8, q < r);
+        }
+        copy_group();
+    };
+#pragma unroll
+    for (int s = 0; s < kShrinkStages - 1; s++)
+        load(k_lo + s);
+    float acc[16][4];
+#pragma unroll
+    for (int b = 0; b < 16; b++)
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+            acc[b][e] = 0.0f;
+    const uint32_t at = (uint32_t)(((warp & 1) * 16 + g) * kRow + (warp >> 1) * 16 + 2 * j) * 2;
+    const uint32_t bt = (uint32_t)((kTile + g) * kRow + (warp >> 1) * 16 + 2 * j) * 2;
+    for (int k = k_lo; k < k_hi; k++) {
+        copy_wait<kShrinkStages - 2>();
+        __syncthreads();
+        load(k + kShrinkStages - 1);
+        const uint32_t st = base + (uint32_t)((k - k_lo) % kShrinkStages) * stage;
+        uint32_t f[4] = {lds32(st + at), lds32(st + at + 16 * kRow), lds32(st + at + 16), lds32(st + at + 16 * kRow + 16)};
+#pragma unroll
+        for (int b = 0; b < 16; b++)
+            if (b < nb)
+                mma<TX>(acc[b], f, lds32(st + bt + b * 16 * kRow), lds32(st + bt + b * 16 * kRow + 16));
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    // partial sums [4][token][R8] meet in shared memory
+    float *const part = reinterpret_cast<float *>(smem);
+#pragma unroll
+    for (int b = 0; b < 16; b++)
+        if (b < nb)
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+                part[((warp >> 1) * kTile + (warp & 1) * 16 + g + 8 * (e >> 1)) * R8 + b * 8 + 2 * j + (e & 1)] = acc[b][e];
+    if (a.split > 1)
+        cluster_sync();
+    else
+        __syncthreads();
+    const float gain = a.gain[i];
+    float m = 0.0f;
+    for (int e = tid; e < kTile * a.rank; e += 256) {
+        const int t = e / a.rank, q = e % a.rank;
+        if (t % a.split != rank || t >= n)
+            continue;
+        float s = 0.0f;
+        if (q < r) {
+            for (int b = 0; b < a.split; b++) {
+                const uint32_t from = at_block(base + (uint32_t)(t * R8 + q) * 4u, b);
+#pragma unroll
+                for (int w = 0; w < 4; w++) {
+                    float v;
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(from + (uint32_t)(w * kTile * R8) * 4u) : "memory");
+                    s = __fadd_rn(s, v);
+                }
+            }
+            s = __fmul_rn(s, gain);
+        }
+        sd.h[(int64_t)a.plan.perm[lo + t] * a.rank + q] = s;
+        m = fmaxf(m, fabsf(s));
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1)
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    if (lane == 0 && m > 0.0f)
+        atomicMax(sd.largest + i, __float_as_uint(m));   // a maximum: any order gives the same
+    if (a.split > 1)
+        cluster_sync();
+}
+
+// ---- expand: y[t] = sum_r h[t][r] M_i[r] (one rounding; the coded product adds to it) --------
+// A block takes one tile and 512 outputs, 128 at a time; warp w the tokens 16 (w % 2) ..
+// and 32 of the outputs.
+template <typename TX> __global__ void __launch_bounds__(256) expand_kernel(const AdaptLaunch a, void *y, int64_t y_stride) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ float wmax[8];
+    const AdaptSide &sd = a.side[0];       // h and its way back: M is [rank][n], n outputs
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, j = lane & 3;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    int i, lo, n;
+    if (!find_tile(a, (int)blockIdx.x, i, lo, n))
+        return;
+    const int r = rank_of(a.ranks, i, a.rank), R16 = (a.rank + 15) / 16 * 16, kb = (r + 15) / 16;
+    constexpr int kF = 128 + kPad;
+    const int hrow = R16 + kPad;
+    TX *const sh = reinterpret_cast<TX *>(smem);                                 // [32][R16]
+    const uint32_t sB = saddr(smem) + (uint32_t)(kTile * hrow) * 2, bbytes = (uint32_t)(R16 * kF) * 2;   // two [R16][128]
+    TX *const so = reinterpret_cast<TX *>(smem + kTile * hrow * 2 + 2 * bbytes); // [32][128]
+    const uint16_t *M = reinterpret_cast<const uint16_t *>(sd.M) + (size_t)i * a.rank * sd.n;
+    const int f_lo = blockIdx.y * 512, f_hi = min(f_lo + 512, sd.n);
+    auto load = [&](int f0, int buf) {
+        if (f0 < f_hi)
+            for (int e = tid; e < kb * 16 * 16; e += 256) {
+                const int q = e >> 4, c = (e & 15) * 8;
+                copy16z(sB + buf * bbytes + (uint32_t)(q * kF + c) * 2, M + (size_t)min(q, a.rank - 1) * sd.n + f0 + c, q < r);
+            }
+        copy_group();
+    };
+    load(f_lo, 0);
+    // h of the tile in the operand's type, scaled by a power of two
+    float m = 0.0f;
+    for (int e = tid; e < kTile * R16; e += 256) {
+        const int t = e / R16, q = e % R16;
+        if (t < n && q < r)
+            m = fmaxf(m, fabsf(sd.h[(int64_t)a.plan.perm[lo + t] * a.rank + q]));
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1)
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    if (lane == 0)
+        wmax[warp] = m;
+    __syncthreads();
+    m = wmax[lane & 7];
+#pragma unroll
+    for (int d = 4; d; d >>= 1)
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    float up, down;
+    operand_scale<TX>(m, up, down);
+    for (int e = tid; e < kTile * R16; e += 256) {
+        const int t = e / R16, q = e % R16;
+        const float v = t < n && q < r ? sd.h[(int64_t)a.plan.perm[lo + t] * a.rank + q] : 0.0f;
+        sh[t * hrow + q] = from_f32<TX>(__fmul_rn(v, up));
+    }
+    const uint32_t ha = saddr(smem) + (uint32_t)(((warp & 1) * 16 + g) * hrow + 2 * j) * 2;
+    for (int f0 = f_lo, buf = 0; f0 < f_hi; f0 += 128, buf ^= 1) {
+        load(f0 + 128, buf ^ 1);
+        copy_wait<1>();
+        __syncthreads();
+        float acc[4][4];
+#pragma unroll
+        for (int b = 0; b < 4; b++)
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+                acc[b][e] = 0.0f;
+        for (int k = 0; k < kb; k++) {
+            const uint32_t at = ha + k * 32;
+            const uint32_t f[4] = {lds32(at), lds32(at + 16 * hrow), lds32(at + 16), lds32(at + 16 * hrow + 16)};
+#pragma unroll
+            for (int b = 0; b < 2; b++) {
+                uint32_t t[4];
+                load_t(sB + buf * bbytes + (uint32_t)((k * 16 + (lane & 15)) * kF + (warp >> 1) * 32 + b * 16 + (lane >> 4) * 8) * 2, t);
+                mma<TX>(acc[2 * b], f, t[0], t[1]);
+                mma<TX>(acc[2 * b + 1], f, t[2], t[3]);
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < 4; b++)
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+                so[((warp & 1) * 16 + g + 8 * (e >> 1)) * kF + (warp >> 1) * 32 + b * 8 + 2 * j + (e & 1)] =
+                    from_f32<TX>(__fmul_rn(acc[b][e], down));
+        __syncthreads();
+        const bool wide = (((uintptr_t)y | (uintptr_t)(y_stride * 2)) & 15u) == 0;
+        for (int e = tid; e < kTile * 16; e += 256) {
+            const int t = e >> 4, c = (e & 15) * 8;
+            if (t >= n)
+                continue;
+            TX *to = reinterpret_cast<TX *>(y) + (int64_t)a.plan.perm[lo + t] * y_stride + f0 + c;
+            const TX *from = so + t * kF + c;
+            if (wide) {
+                *reinterpret_cast<uint4 *>(to) = *reinterpret_cast<const uint4 *>(from);
+            } else {
+                for (int q = 0; q < 8; q++)
+                    to[q] = from[q];
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// ---- outer: dM_i[r][k] = sum_{t of i} h[t][r] x[t][k] ------------------------------
+// A block takes one adapter, 128 of k (16 a warp) and a share of the adapter's tokens
+// (the blocks of a cluster take turns at its tiles of 32).
+constexpr int kOuterStages = 4;
+constexpr int kXRow = 128 + kPad;
+
+template <typename TX, bool VEC> __global__ void __launch_bounds__(256) outer_kernel(const AdaptLaunch a) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, j = lane & 3;
+    const int rank = (int)(blockIdx.x % a.split), i = blockIdx.y;
+    int chunk = (int)(blockIdx.x / a.split);
+    const int side = chunk < a.side[0].n / 128 ? 0 : 1;
+    chunk -= side ? a.side[0].n / 128 : 0;
+    const AdaptSide &sd = a.side[side];
+    const int r = rank_of(a.ranks, i, a.rank), R16 = (a.rank + 15) / 16 * 16, mb = (r + 15) / 16;
+    const int lo = a.plan.seg[i], n = a.plan.seg[i + 1] - lo;
+    const int hrow = R16 + kPad;
+    const uint32_t base = saddr(smem), xbytes = kTile * kXRow * 2, hbytes = (uint32_t)(kTile * hrow) * 2;
+    const uint32_t hbase = base + kOuterStages * xbytes;
+    float up, down;
+    operand_scale<TX>(__uint_as_float(sd.largest[i]), up, down);
+    const int tiles = (n + kTile - 1) / kTile;
+    const int mine = r > 0 && tiles > rank ? (tiles - 1 - rank) / a.split + 1 : 0;
+    const uint16_t *x = reinterpret_cast<const uint16_t *>(sd.x) + chunk * 128;
+    // copies of a tile: tokens tid / 16 and tid / 16 + 16, 8 elements each
+    const int row = tid >> 4, c8 = (tid & 15) * 8;
+    auto load = [&](int s) {
+        if (s < mine) {
+            const int t0 = (rank + s * a.split) * kTile;
+#pragma unroll
+            for (int b = 0; b < 2; b++) {
+                const int t = t0 + row + 16 * b;
+                const bool real = t < n;
+                row8<VEC>(base + (uint32_t)(s % kOuterStages) * xbytes + (uint32_t)((row + 16 * b) * kXRow + c8) * 2,
+                          x + (int64_t)(real ? a.plan.perm[lo + t] : 0) * sd.stride + c8, real);
+            }
+        }
+        copy_group();
+    };
+    // h of a tile: token tid / 8, elements tid % 8 + 8 q
+    const int ht = tid >> 3, hq = tid & 7;
+    float hv[16];
+    auto fetch = [&](int s) {
+        const int t = (rank + s * a.split) * kTile + ht;
+        const bool real = s < mine && t < n;
+        const float *from = sd.h + (real ? (int64_t)a.plan.perm[lo + t] * a.rank : 0);
+#pragma unroll
+        for (int q = 0; q < 16; q++)
+            if (q < 2 * mb)
+                hv[q] = real && hq + 8 * q < r ? __fmul_rn(from[hq + 8 * q], up) : 0.0f;
+    };
+#pragma unroll
+    for (int s = 0; s < kOuterStages - 1; s++)
+        load(s);
+    fetch(0);
+    float acc[8][2][4];
+#pragma unroll
+    for (int m = 0; m < 8; m++)
+#pragma unroll
+        for (int b = 0; b < 2; b++)
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+                acc[m][b][e] = 0.0f;
+    for (int s = 0; s < mine; s++) {
+        TX *const sh = reinterpret_cast<TX *>(smem + kOuterStages * xbytes + (s & 1) * hbytes);
+#pragma unroll
+        for (int q = 0; q < 16; q++)
+            if (q < 2 * mb)
+                sh[ht * hrow + hq + 8 * q] = from_f32<TX>(hv[q]);
+        copy_wait<kOuterStages - 2>();
+        __syncthreads();
+        load(s + kOuterStages - 1);
+        fetch(s + 1);
+        const uint32_t xs = base + (uint32_t)(s % kOuterStages) * xbytes, hs = hbase + (s & 1) * hbytes;
+#pragma unroll
+        for (int k = 0; k < kTile / 16; k++) {
+            uint32_t b[4];
+            load_t(xs + (uint32_t)((k * 16 + (lane & 15)) * kXRow + warp * 16 + (lane >> 4) * 8) * 2, b);
+#pragma unroll
+            for (int m = 0; m < 8; m++)
+                if (m < mb) {
+                    uint32_t f[4];         // blocks (tokens 0-7 | 8-15) x (rows 0-7 | 8-15): rows first
+                    load_t(hs + (uint32_t)((k * 16 + (lane & 7) + (lane >> 4) * 8) * hrow + m * 16 + ((lane >> 3) & 1) * 8) * 2, f);
+                    mma<TX>(acc[m][0], f, b[0], b[1]);
+                    mma<TX>(acc[m][1], f, b[2], b[3]);
+                }
+        }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    // partial sums [R16][128] meet in shared memory; block `rank` finishes rows rank, rank + split, ...
+    float *const part = reinterpret_cast<float *>(smem);
+#pragma unroll
+    for (int m = 0; m < 8; m++)
+        if (m < mb)
+#pragma unroll
+            for (int b = 0; b < 2; b++)
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+                    part[(m * 16 + g + 8 * (e >> 1)) * 132 + warp * 16 + b * 8 + 2 * j + (e & 1)] = acc[m][b][e];
+    if (a.split > 1)
+        cluster_sync();
+    else
+        __syncthreads();
+    TX *const out = reinterpret_cast<TX *>(sd.dM) + (size_t)i * a.rank * sd.n + chunk * 128;
+    for (int q = rank + (tid >> 5) * a.split; q < a.rank; q += 8 * a.split) {
+        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (q < r)
+            for (int b = 0; b < a.split; b++) {
+                float4 f;
+                asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                             : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w)
+                             : "r"(at_block(base + (uint32_t)(q * 132 + lane * 4) * 4u, b)) : "memory");
+                v[0] = __fadd_rn(v[0], f.x), v[1] = __fadd_rn(v[1], f.y), v[2] = __fadd_rn(v[2], f.z), v[3] = __fadd_rn(v[3], f.w);
+            }
+        *reinterpret_cast<uint2 *>(out + (size_t)q * sd.n + lane * 4) =
+            make_uint2(pack2<TX>(__fmul_rn(v[0], down), __fmul_rn(v[1], down)),
+                       pack2<TX>(__fmul_rn(v[2], down), __fmul_rn(v[3], down)));
+    }
+    if (a.split > 1)
+        cluster_sync();
+}
+
+// early: the launch may overlap the end of the one before it, whose results the kernel
+// waits for (shrink and expand behind the plan, which starts after everything before)
+template <typename... P, typename... A>
+exl3_status launch(const char *what, void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, unsigned cluster,
+                   bool early, cudaStream_t s, A... args) {
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess)
+            return cuda_check(e, what);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = early;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    if (e != cudaSuccess)
+        return cuda_check(e, what);
+    note_launch();
+    return cuda_check(cudaGetLastError(), what);
+}
+
+// rows that are read 16 bytes at a time
+bool wide_rows(const AdaptSide &s) { return ((uintptr_t)s.x & 15u) == 0 && s.stride % 8 == 0; }
 
 }  // namespace
 
-exl3_status launch_shrink(const ShrinkLaunch &p, cudaStream_t s) {
-    const dim3 grid((unsigned)p.T, (unsigned)((p.rank + 7) / 8));
-    if (p.dt == EXL3_BF16)
-        shrink_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(p);
-    else
-        shrink_kernel<__half><<<grid, 256, 0, s>>>(p);
-    note_launch();
-    return cuda_check(cudaGetLastError(), "adapter shrink launch");
+size_t adapt_plan_ints(int64_t T, int n) { return (size_t)T + 4 * (size_t)n + 2; }
+
+AdaptPlan adapt_plan(int32_t *ints, int64_t T, int n) {
+    AdaptPlan p;
+    p.perm = ints;
+    p.seg = ints + T;
+    p.first = p.seg + n + 1;
+    p.largest = reinterpret_cast<uint32_t *>(p.first + n + 1);
+    return p;
 }
 
-exl3_status launch_outer(const OuterLaunch &p, cudaStream_t s) {
-    const dim3 grid((unsigned)(p.n / 128), (unsigned)p.rank, (unsigned)p.n_adapters);
+exl3_status launch_adapt_plan(const AdaptLaunch &p, cudaStream_t s) {
+    return launch("adapter plan launch", plan_kernel, dim3((unsigned)((p.n + 31) / 32)), 1024, 0, 1, false, s, p);
+}
+
+exl3_status launch_shrink(const AdaptLaunch &p0, int sides, cudaStream_t s) {
+    AdaptLaunch p = p0;
+    const int64_t tiles = (p.T + kTile - 1) / kTile + (p.n < p.T ? p.n : p.T);    // at most
+    // blocks that would idle share the sums, at least 4 steps of 64 each
+    const int64_t sms = device_sm_count();
+    int least = p.side[0].n;
+    if (sides > 1 && p.side[1].n < least)
+        least = p.side[1].n;
+    p.split = 1;
+    while (p.split < 8 && tiles * sides * p.split * 2 <= 2 * sms && least / 64 >= p.split * 2 * 4)
+        p.split *= 2;
+    const int R8 = (p.rank + 7) / 8 * 8;
+    const size_t stages = (size_t)kShrinkStages * (kTile + R8) * kRow * 2, part = (size_t)4 * kTile * R8 * 4;
+    const size_t smem = stages > part ? stages : part;
+    const dim3 grid((unsigned)(tiles * p.split), (unsigned)sides);
+    const bool vec = wide_rows(p.side[0]) && (sides < 2 || wide_rows(p.side[1]));
+    auto go = [&](auto k) { return launch("adapter shrink launch", k, grid, 256, smem, (unsigned)p.split, true, s, p); };
     if (p.dt == EXL3_BF16)
-        outer_kernel<__nv_bfloat16><<<grid, 128, 0, s>>>(p);
-    else
-        outer_kernel<__half><<<grid, 128, 0, s>>>(p);
-    note_launch();
-    return cuda_check(cudaGetLastError(), "adapter gradient launch");
+        return vec ? go(shrink_kernel<__nv_bfloat16, true>) : go(shrink_kernel<__nv_bfloat16, false>);
+    return vec ? go(shrink_kernel<__half, true>) : go(shrink_kernel<__half, false>);
+}
+
+exl3_status launch_expand(const AdaptLaunch &p, void *y, int64_t y_stride, cudaStream_t s) {
+    const int64_t tiles = (p.T + kTile - 1) / kTile + (p.n < p.T ? p.n : p.T);
+    const int R16 = (p.rank + 15) / 16 * 16;
+    const size_t smem = (size_t)kTile * (R16 + kPad) * 2 + (size_t)2 * R16 * (128 + kPad) * 2 + (size_t)kTile * (128 + kPad) * 2;
+    const dim3 grid((unsigned)tiles, (unsigned)((p.side[0].n + 511) / 512));
+    if (p.dt == EXL3_BF16)
+        return launch("adapter expand launch", expand_kernel<__nv_bfloat16>, grid, 256, smem, 1, true, s, p, y, y_stride);
+    return launch("adapter expand launch", expand_kernel<__half>, grid, 256, smem, 1, true, s, p, y, y_stride);
+}
+
+exl3_status launch_outer(const AdaptLaunch &p0, cudaStream_t s) {
+    AdaptLaunch p = p0;
+    const int64_t blocks = (int64_t)(p.side[0].n + p.side[1].n) / 128 * p.n, sms = device_sm_count();
+    p.split = 1;
+    while (p.split < 8 && blocks * p.split * 2 <= 2 * sms && p.T >= (int64_t)p.split * 2 * kTile * p.n)
+        p.split *= 2;
+    const int R16 = (p.rank + 15) / 16 * 16;
+    const size_t stages = (size_t)kOuterStages * kTile * kXRow * 2 + (size_t)2 * kTile * (R16 + kPad) * 2;
+    const size_t part = (size_t)R16 * 132 * 4, smem = stages > part ? stages : part;
+    const dim3 grid((unsigned)((p.side[0].n + p.side[1].n) / 128 * p.split), (unsigned)p.n);
+    const bool vec = wide_rows(p.side[0]) && wide_rows(p.side[1]);
+    auto go = [&](auto k) { return launch("adapter gradient launch", k, grid, 256, smem, (unsigned)p.split, false, s, p); };
+    if (p.dt == EXL3_BF16)
+        return vec ? go(outer_kernel<__nv_bfloat16, true>) : go(outer_kernel<__nv_bfloat16, false>);
+    return vec ? go(outer_kernel<__half, true>) : go(outer_kernel<__half, false>);
 }
 
 }  // namespace exl3

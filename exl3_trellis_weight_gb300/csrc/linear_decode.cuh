@@ -127,6 +127,22 @@ __device__ __forceinline__ void add_adapter(const ProductLaunch &p, int n_out, i
     const int ad = p.slots[t];
     if (ad < 0 || ad >= p.n_adapters)
         return;
+    if (!p.h) {                            // made before: y holds it
+        const TY *y = reinterpret_cast<const TY *>(p.y) + t * p.y_stride + f0 + 8 * u;
+        const bool wide = (((uintptr_t)p.y | (uintptr_t)(p.y_stride * 2)) & 15u) == 0;
+#pragma unroll
+        for (int m = 0; m < 2; m++) {
+            if (wide) {
+                const uint4 w = *reinterpret_cast<const uint4 *>(y + 64 * m);
+                fma8<TY>(v + 8 * m, 1.0f, w);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; i++)
+                    v[8 * m + i] = __fadd_rn(v[8 * m + i], to_f32(y[64 * m + i]));
+            }
+        }
+        return;
+    }
     const int r = p.ranks ? min(max(p.ranks[ad], 0), p.rank) : p.rank;
     const TY *b = reinterpret_cast<const TY *>(p.B) + (size_t)ad * p.rank * n_out + f0 + 8 * u;
     const float *h = p.h + t * p.rank;
