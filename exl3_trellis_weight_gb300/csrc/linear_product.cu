@@ -44,11 +44,12 @@ constexpr int kThreadsP = (kWarpB + 2) * 32;
 constexpr int kN = 256;                    // columns of an accumulator
 constexpr int kStep = 64;                  // inputs of a step
 constexpr int kAStages = 4, kBStages = 16; // operand stages (of B at most)
-constexpr uint32_t kABytes = 128 * kStep * 2, kBArea = 104 * 1024, kCArea = 32 * 1024;
+constexpr uint32_t kABytes = 128 * kStep * 2, kBArea = 96 * 1024, kCArea = 32 * 1024;
 constexpr uint32_t kBOff = kAStages * kABytes;              // B stages behind the A stages,
 constexpr uint32_t kCOff = kBOff + kBArea;                  // then a ring of codes for each decode warp,
 constexpr uint32_t kOutOff = kCOff + kCArea;                // then 32 tokens x 128 outputs, fp32
-constexpr uint32_t kSmem = kOutOff + 32 * 128 * 4 + 1024;   // + alignment slack
+constexpr uint32_t kAddOff = kOutOff + 32 * 128 * 4;        // then 64 bytes for each thread of the result warps
+constexpr uint32_t kSmem = kAddOff + 128 * 64 + 1024;       // + alignment slack
 
 __device__ unsigned int g_product_timeouts;
 
@@ -262,7 +263,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) product_kernel(const __grid_cons
                         s_b = 0, round_b++;
             }
             if (lane == 0) {
-                if (PAIR)
+                if (PAIR && rank == 1)
                     bar_arrive_at(at_block(full_a(s), 0));
                 else
                     bar_arrive(full_a(s));
@@ -279,10 +280,35 @@ __global__ void __launch_bounds__(kThreadsP, 1) product_kernel(const __grid_cons
         asm volatile("griddepcontrol.wait;" ::: "memory");
         uint32_t acc = 0;
         bool ok = true;
+        const bool wide_y = (((uintptr_t)a.p.y | (uintptr_t)(a.p.y_stride * 2)) & 15u) == 0;
+        const int u = lane & 7;
         for (int64_t it = it0; ok && it < n_tiles; it += dit) {
             const Tile tl = make_tile<PAIR>(a, &plan, it, rank);
+            const bool live = !PAIR || tl.f0 < a.n_out;
             // read after the barriers of the first chunk; the last chunk's protect the previous tile's
             right[ow * 32 + lane] = right_of(a, tl, ow * 32 + lane);
+            // A thread finishes two tokens of every 32, eight threads to a token.  What it
+            // needs of them from memory is asked for a chunk before: the row's scale, and
+            // what y holds of a token with an adapter (to its own place in shared memory).
+            float rs[2];
+            bool has[2];
+            const uint32_t mine = base + kAddOff + (uint32_t)(ow * 32 + lane) * 16u;
+            auto fetch = [&](int g, int64_t t) {
+                const bool in = !keep && live && t >= tl.lo && t < tl.hi;
+                rs[g] = in ? a.p.rscale[t] : 0.0f;
+                has[g] = false;
+                if (a.p.B && !a.p.h && wide_y && in) {
+                    const TY *y = reinterpret_cast<const TY *>(a.p.y) + t * a.p.y_stride + tl.f0 + 8 * u;
+                    copy16(mine + g * 4096u, y);
+                    copy16(mine + g * 4096u + 2048u, y + 64);
+                    const int ad = a.p.slots[t];
+                    has[g] = ad >= 0 && ad < a.p.n_adapters;
+                }
+                copy_group();
+            };
+            const int64_t t_mine = tl.t0 + ow * 4 + (lane >> 3);
+            fetch(0, t_mine);
+            fetch(1, t_mine + 16);
             for (int n0 = 0; ok && n0 < tl.n; n0 += kN, acc++) {
                 const int d = acc & 1;
                 ok = bar_wait(acc_full(d), (acc >> 1) & 1, &gave_up, count);
@@ -292,10 +318,6 @@ __global__ void __launch_bounds__(kThreadsP, 1) product_kernel(const __grid_cons
                 fence_after();
                 const int n1 = min(tl.n - n0, kN);
                 for (int c0 = 0; c0 < n1; c0 += 32) {
-                    // 16 tokens at a time, eight threads to a token
-                    const int64_t t = tl.t0 + n0 + c0 + ow * 4 + (lane >> 3);
-                    const float rs0 = !keep && t < tl.hi ? a.p.rscale[t] : 0.0f;
-                    const float rs1 = !keep && t + 16 < tl.hi ? a.p.rscale[t + 16] : 0.0f;
                     float *const dst = buf + (keep ? c0 * 128 : 0) + col;
 #pragma unroll
                     for (int g = 0; g < 2; g++) {
@@ -308,28 +330,36 @@ __global__ void __launch_bounds__(kThreadsP, 1) product_kernel(const __grid_cons
                     if (keep)
                         continue;
                     asm volatile("bar.sync 1, 128;" ::: "memory");
-#pragma unroll 1
+#pragma unroll
                     for (int g = 0; g < 2; g++) {
+                        const int64_t t = t_mine + n0 + c0 + 16 * g;
                         const float4 *src = reinterpret_cast<const float4 *>(buf) + (g * 16 + ow * 4 + (lane >> 3)) * 32;
                         float x[16];
 #pragma unroll
                         for (int m = 0; m < 4; m++) {
-                            const float4 f = src[out_at(2 * (lane & 7) + (m & 1) + 16 * (m >> 1))];
+                            const float4 f = src[out_at(2 * u + (m & 1) + 16 * (m >> 1))];
                             x[4 * m] = f.x, x[4 * m + 1] = f.y, x[4 * m + 2] = f.z, x[4 * m + 3] = f.w;
                         }
-                        scale_out(x, g ? rs1 : rs0, right, lane);
-                        if (t + 16 * g >= tl.lo && t + 16 * g < tl.hi && tl.f0 < a.n_out) {
-                            if (a.p.B)
-                                add_adapter<TY>(a.p, a.n_out, tl.f0, t + 16 * g, x, lane & 7, 0, 1);
-                            store_out<TY>(a.p, tl.f0, t + 16 * g, x, lane & 7);
+                        scale_out(x, rs[g], right, lane);
+                        const bool in = live && t >= tl.lo && t < tl.hi;
+                        copy_wait<1>();
+                        if (has[g]) {
+                            const unsigned char *from = sb + (mine - base) + g * 4096;
+                            fma8<TY>(x, 1.0f, *reinterpret_cast<const uint4 *>(from));
+                            fma8<TY>(x + 8, 1.0f, *reinterpret_cast<const uint4 *>(from + 2048));
+                        } else if (a.p.B && (a.p.h || !wide_y) && in) {
+                            add_adapter<TY>(a.p, a.n_out, tl.f0, t, x, u, 0, 1);
                         }
+                        fetch(g, t + 32);
+                        if (in)
+                            store_out<TY>(a.p, tl.f0, t, x, u);
                     }
                     asm volatile("bar.sync 1, 128;" ::: "memory");
                 }
                 fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    if (PAIR)
+                    if (PAIR && rank == 1)
                         bar_arrive_at(at_block(acc_empty(d), 0));
                     else
                         bar_arrive(acc_empty(d));
@@ -386,9 +416,9 @@ __global__ void __launch_bounds__(kThreadsP, 1) product_kernel(const __grid_cons
         for (int64_t it = it0; ok && it < n_tiles; it += dit) {
             const Tile tl = make_tile<PAIR>(a, &plan, it, rank);
             const bool two = PAIR && tl.n > kN;
-            ok = acc < 2 || bar_wait<PAIR>(acc_empty(acc & 1), ((acc >> 1) - 1) & 1, &gave_up, count);
+            ok = acc < 2 || bar_wait(acc_empty(acc & 1), ((acc >> 1) - 1) & 1, &gave_up, count);
             if (two && acc + 1 >= 2)
-                ok = bar_wait<PAIR>(acc_empty((acc + 1) & 1), (((acc + 1) >> 1) - 1) & 1, &gave_up, count) && ok;
+                ok = bar_wait(acc_empty((acc + 1) & 1), (((acc + 1) >> 1) - 1) & 1, &gave_up, count) && ok;
             ok = __all_sync(0xffffffffu, ok);
             const uint32_t shape = shape_f16(PAIR ? 256 : 128, two ? kN : tl.n, !a.p.transposed);
             const uint32_t shape2 = shape_f16(256, tl.n - kN, !a.p.transposed);
@@ -398,7 +428,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) product_kernel(const __grid_cons
                 const int k_end = min(k + a.b_steps, k_hi);
                 uint64_t db = b0 + (s * b_bytes >> 4);
                 for (; ok && k < k_end; k++, db += b_step >> 4) {
-                    ok = __all_sync(0xffffffffu, bar_wait<PAIR>(full_a(sa), sa_phase, &gave_up, count));
+                    ok = __all_sync(0xffffffffu, bar_wait(full_a(sa), sa_phase, &gave_up, count));
                     if (!ok)
                         break;
                     fence_after();

@@ -19,16 +19,9 @@ __device__ __forceinline__ void bar_arrive(uint32_t bar) {
 __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
-// CLUSTER: arrivals may come from the other block
-template <bool CLUSTER = false> __device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
     uint32_t ok;
-    if constexpr (CLUSTER)
-        asm volatile("{\n\t.reg .pred p;\n\t"
-                     "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-                     "selp.u32 %0, 1, 0, p;\n\t}"
-                     : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-    else
-        asm volatile("{\n\t.reg .pred p;\n\t"
+    asm volatile("{\n\t.reg .pred p;\n\t"
                  "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
                  "selp.u32 %0, 1, 0, p;\n\t}"
                  : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
@@ -48,10 +41,9 @@ __device__ __forceinline__ bool bar_peek(uint32_t bar, uint32_t parity) {
 // once in 64 tries).  False when it gave up, or when another wait of the block
 // had: the caller then leaves its loop.
 constexpr long long kWaitCycles = 1ll << 31;
-template <bool CLUSTER>
-__device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, volatile int *gave_up, unsigned int *count) {
+static __device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, volatile int *gave_up, unsigned int *count) {
     const long long t0 = clock64();
-    for (uint32_t i = 1; !bar_test<CLUSTER>(bar, parity); i++) {
+    for (uint32_t i = 1; !bar_test(bar, parity); i++) {
         if ((i & 63u) != 0u)
             continue;
         if (*gave_up)
@@ -64,9 +56,8 @@ __device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, volati
     }
     return true;
 }
-template <bool CLUSTER = false>
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *gave_up, unsigned int *count) {
-    return bar_test<CLUSTER>(bar, parity) || bar_wait_slow<CLUSTER>(bar, parity, gave_up, count);
+    return bar_test(bar, parity) || bar_wait_slow(bar, parity, gave_up, count);
 }
 // Waits for a phase, as long at most, whatever other waits did (the way out
 // after one gave up: nothing may be in flight when the block ends).
@@ -82,8 +73,11 @@ __device__ __forceinline__ uint32_t at_block(uint32_t addr, uint32_t block) {
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(block));
     return r;
 }
+// What the arrival announces has been handed to the asynchronous proxy by a fence (or
+// is a finished read of tensor memory): a release at cluster scope on top of that
+// took 1200 cycles an arrival.
 __device__ __forceinline__ void bar_arrive_at(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
