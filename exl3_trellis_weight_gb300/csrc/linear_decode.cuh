@@ -119,6 +119,73 @@ template <typename TY> __device__ __forceinline__ void fma8(float *v, float h, c
     }
 }
 
+// ---- the same from shared memory with many tokens: H in two passes -----------------
+// 32 tokens of 32 float4; float4 f of token t sits at swz(f, t): a warp writing one
+// token's 32 neighbouring outputs, and the eight lanes of each 16-byte access below,
+// cover all banks.
+__device__ __forceinline__ int swz(int f, int t) { return f ^ ((f >> 3) & 1) ^ ((f >> 3) & 2) ^ ((t & 1) << 2); }
+
+__device__ __forceinline__ void add2(float &a0, float &a1, float b0, float b1, float &d0, float &d1) {
+    // (a, b) -> (a + b, a - b) of two neighbours at a time
+    asm("{\n\t.reg .b64 a, b, s, d;\n\t"
+        "mov.b64 a, {%0, %1};\n\t"
+        "mov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 s, a, b;\n\t"
+        "sub.rn.f32x2 d, a, b;\n\t"
+        "mov.b64 {%0, %1}, s;\n\t"
+        "mov.b64 {%2, %3}, d;\n\t}"
+        : "+f"(a0), "+f"(a1), "=f"(d0), "=f"(d1) : "f"(b0), "f"(b1));
+}
+// butterflies of span SPAN (>= 2) over N values
+template <int SPAN, int N> __device__ __forceinline__ void span2(float (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2)
+        if ((i & SPAN) == 0)
+            add2(v[i], v[i + 1], v[i + SPAN], v[i + SPAN + 1], v[i + SPAN], v[i + SPAN + 1]);
+}
+
+// first pass, in place: thread `tid` of 128 takes token tid / 4, outputs with bits 2 and 6
+// equal to tid's two: spans 1, 2, 8, 16, 32
+__device__ __forceinline__ void rotate_first(float *buf, int tid) {
+    const int t = tid >> 2, f0 = (tid & 1) + 16 * ((tid >> 1) & 1);
+    float4 *row = reinterpret_cast<float4 *>(buf) + t * 32;
+    float v[32];
+#pragma unroll
+    for (int b = 0; b < 8; b++) {
+        const float4 f = row[swz(f0 + 2 * b, t)];
+        v[4 * b] = __fadd_rn(f.x, f.y), v[4 * b + 1] = __fsub_rn(f.x, f.y);
+        v[4 * b + 2] = __fadd_rn(f.z, f.w), v[4 * b + 3] = __fsub_rn(f.z, f.w);
+    }
+    span2<2>(v);
+    span2<4>(v);
+    span2<8>(v);
+    span2<16>(v);
+#pragma unroll
+    for (int b = 0; b < 8; b++)
+        row[swz(f0 + 2 * b, t)] = make_float4(v[4 * b], v[4 * b + 1], v[4 * b + 2], v[4 * b + 3]);
+}
+
+// second pass: outputs 8u + 64m + i of token t (m < 2, i < 8) to v[8m + i]: spans 4 and 64,
+// the row's scale and right . 2^-7 s
+__device__ __forceinline__ void rotate_second(const float *buf, int t, int u, float rs, const float *right, float (&v)[16]) {
+    const float4 *row = reinterpret_cast<const float4 *>(buf) + t * 32;
+#pragma unroll
+    for (int m = 0; m < 4; m++) {
+        const float4 f = row[swz(2 * u + (m & 1) + 16 * (m >> 1), t)];
+        v[4 * m] = f.x, v[4 * m + 1] = f.y, v[4 * m + 2] = f.z, v[4 * m + 3] = f.w;
+    }
+    span2<4>(v);
+    span2<8>(v);
+#pragma unroll
+    for (int m = 0; m < 4; m++) {
+        const float4 f = reinterpret_cast<const float4 *>(right)[2 * u + (m & 1) + 16 * (m >> 1)];
+        v[4 * m] = __fmul_rn(__fmul_rn(v[4 * m], rs), f.x);
+        v[4 * m + 1] = __fmul_rn(__fmul_rn(v[4 * m + 1], rs), f.y);
+        v[4 * m + 2] = __fmul_rn(__fmul_rn(v[4 * m + 2], rs), f.z);
+        v[4 * m + 3] = __fmul_rn(__fmul_rn(v[4 * m + 3], rs), f.w);
+    }
+}
+
 // v += the adapter term of token t, outputs f0 + 8u + 64m + i (m < 2, i < 8): rows
 // first, first + every, ... of the token's adapter
 template <typename TY>

@@ -11,7 +11,7 @@
 //          stored as an operand whose rows run along M, the second along K, and
 //          only the descriptor differs;
 //   16-19  results: accumulator -> shared memory (one token per row) -> H over
-//          the 128 outputs (16 to a thread) -> scales, adapters, one rounding;
+//          the 128 outputs in two passes -> scales, adapters, one rounding;
 //   20     bulk copies of the rotated activations, one contiguous block a step;
 //   21     issues the matrix instructions (binary16 in, binary32 out).
 //
@@ -65,23 +65,34 @@ template <int NR> __device__ __forceinline__ uint32_t window(const uint32_t (&r)
     return __funnelshift_r(r[a], hi, b) & 0xFFFFu;
 }
 
-// Row R (16 weights) of the tile whose codes start at `tile`, to the 32 bytes of
-// an operand row at `to` (the second 16 at to ^ 16).  The row's windows need the
-// 15 + 16 K bits up to its last one: NR words that end with it.
-template <int K> __device__ __forceinline__ void decode_row(uint32_t tile, int R, uint32_t to) {
-    constexpr int NR = (15 + 16 * K + 31) / 32;
-    constexpr int NL = (K & 1) ? NR + 1 : NR;              // odd K: half the rows end inside a word
-    const int end = 16 * K * (R + 1), last = (end - 1) >> 5;
+// A row of 16 weights, to the 32 bytes of an operand row at `to` (the second 16 at
+// to ^ 16).  The row's windows need the 15 + 16 K bits up to its last one: NR words that
+// end with it, from NL words of the tile, the last at `last`, the first at `first` (the
+// stream is a ring; only the first can be around it).  `half`: 16 where the row ends in
+// the middle of a word (odd K).
+template <int K> struct Row {
+    static constexpr int NR = (15 + 16 * K + 31) / 32, NL = (K & 1) ? NR + 1 : NR;
+    uint32_t last, first, half, to;
+    // row R of a tile at offset `tile` of the codes, column 16 tc of an operand panel at `panel`
+    __device__ __forceinline__ Row(uint32_t tile, uint32_t panel, int R, int tc) {
+        const int end = 16 * K * (R + 1), w = (end - 1) >> 5, f = w - (NL - 1);
+        last = tile + 4u * w;
+        first = tile + 4u * (f < 0 ? f + 8 * K : f);
+        half = end & 16;
+        to = panel + R * 128 + (((2 * tc) ^ (R & 7)) << 4);
+    }
+};
+template <int K> __device__ __forceinline__ void decode_row(const Row<K> &row, uint32_t codes, uint32_t stage) {
+    constexpr int NR = Row<K>::NR, NL = Row<K>::NL;
     uint32_t l[NL], r[NR];
 #pragma unroll
-    for (int j = 0; j < NL; j++) {
-        int at = last - (NL - 1 - j);
-        at += at < 0 ? 8 * K : 0;                          // the stream is a ring
-        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(l[j]) : "r"(tile + 4u * at));
-    }
+    for (int j = 0; j < NL; j++)
+        asm volatile("ld.shared.b32 %0, [%1];"
+                     : "=r"(l[j]) : "r"(j == 0 ? codes + row.first : codes + row.last - 4u * (NL - 1 - j)));
 #pragma unroll
     for (int j = 0; j < NR; j++)
-        r[j] = (K & 1) ? __funnelshift_r(l[j + NL - NR], l[j + NL - NR - (K & 1)], end & 16) : l[j];
+        r[j] = (K & 1) ? __funnelshift_r(l[j + NL - NR], l[j + NL - NR - (K & 1)], row.half) : l[j];
+    const uint32_t to = stage + row.to;
 #pragma unroll
     for (int h = 0; h < 2; h++) {
         uint32_t v[4];
@@ -199,84 +210,91 @@ __global__ void __launch_bounds__(kThreadsP, 1) product_kernel(const __grid_cons
         const uint32_t n = (uint32_t)(k_hi - k_lo), total = n_mine * n;
         // This warp's codes of a step are those of four neighbouring tiles, 128 K
         // bytes in a row.  They are copied kRing of its steps ahead, across tiles.
-        constexpr uint32_t kRing = 16 / K, kSlot = 128 * K;
+        constexpr uint32_t kSlot = 128 * K, kRing = kCArea / (kDecWarps * kSlot);
         static_assert(kRing * kSlot * kDecWarps <= kCArea, "code rings");
         const uint32_t ring = base + kCOff + (uint32_t)warp * (kRing * kSlot);
         const int64_t tiles_c = a.p.cols / 16;
         const int tr = a.p.transposed ? dw : dw >> 1, tcol = a.p.transposed ? 0 : (dw & 1) * 4;
         const int64_t hop = (a.p.transposed ? 4 : 4 * tiles_c) * (32 * K);       // bytes from step to step
-        uint32_t s_load = group, k_load = group, slot_load = 0;
+        uint32_t k_load = group, left = total > (uint32_t)group ? (total - group + kGroups - 1) / kGroups : 0u, slot_load = 0;
         int64_t it_load = it0;
-        const char *p_load = nullptr;
+        const char *p_load = nullptr;      // codes of step k_load
         auto next_codes = [&]() {
-            if (s_load < total) {
-                while (!p_load || k_load >= n) {
+            if (left) {
+                left--;
+                if (!p_load || k_load >= n) {
+                    // another tile
                     if (p_load)
-                        k_load -= n, it_load += dit;
+                        do
+                            k_load -= n, it_load += dit;
+                        while (k_load >= n);
+                    else
+                        for (; k_load >= n; k_load -= n)
+                            it_load += dit;
                     const Tile tl = make_tile<PAIR>(a, &plan, it_load, rank);
                     const int f0 = PAIR ? min(tl.f0, a.n_out - 128) : tl.f0;
                     const int64_t r0 = a.p.transposed ? f0 / 16 + tr : (int64_t)k_lo * 4 + tr;
                     const int64_t c0 = a.p.transposed ? (int64_t)k_lo * 4 + tcol : f0 / 16 + tcol;
                     p_load = reinterpret_cast<const char *>(a.p.codes) +
-                             ((int64_t)tl.e * (a.p.rows / 16) * tiles_c + r0 * tiles_c + c0) * (32 * K) + lane * 16;
+                             ((int64_t)tl.e * (a.p.rows / 16) * tiles_c + r0 * tiles_c + c0) * (32 * K) + lane * 16 +
+                             k_load * hop;
                 }
                 if (lane < 8 * K)
-                    copy16(ring + slot_load * kSlot + lane * 16, p_load + k_load * hop);
+                    copy16(ring + slot_load * kSlot + lane * 16, p_load);
+                p_load += kGroups * hop;
+                k_load += kGroups;
             }
             copy_group();
-            s_load += kGroups;
-            k_load += kGroups;
             slot_load = slot_load + 1 == kRing ? 0 : slot_load + 1;
         };
 #pragma unroll 1
         for (uint32_t i = 0; i < kRing; i++)
             next_codes();
-        uint32_t slot = 0, s_b = group % nb, round_b = group / nb;
-        bool ready = true;                 // the stage is known to be free
+        // This lane's rows 2q and 2q + 1 of tile tc.  Lanes of odd q take their second row
+        // first: the eight lanes of a store phase then cover all banks.
+        const Row<K> row0(tc * (32u * K), panel, 2 * q + odd, tc), row1(tc * (32u * K), panel, 2 * q + 1 - odd, tc);
+        uint32_t codes = ring, stage = base + (uint32_t)(group % kAStages) * kABytes, s_b = group % nb, round_b = group / nb;
+        uint32_t bar = full_a(group % kAStages), round = 0;       // (the stage's full barrier; the empty one lies kAStages behind)
 #pragma unroll 1
-        for (uint32_t step = group; step < total; step += kGroups) {
-            const uint32_t s = step % kAStages, round = step / kAStages;
-            if (!__all_sync(0xffffffffu, ready || bar_wait(empty_a(s), (round - 1) & 1, &gave_up, count)))
+        for (uint32_t i = total > (uint32_t)group ? (total - group + kGroups - 1) / kGroups : 0u; i; i--) {
+            if (!__all_sync(0xffffffffu, round == 0 || bar_wait(bar + 8u * kAStages, (round - 1) & 1, &gave_up, count)))
                 break;                     // the warp goes on as a whole or not at all
             copy_wait<kRing - 1>();
             __syncwarp();
-            // whether the next stage is free, asked for before it is needed
-            const uint32_t s2 = (step + kGroups) % kAStages, round2 = (step + kGroups) / kAStages;
-            ready = round2 == 0 || bar_peek(empty_a(s2), (round2 - 1) & 1);
-            const uint32_t st = base + s * kABytes + panel, tile = ring + slot * kSlot + tc * (32u * K);
-            // Threads of odd q take their second row first: the eight lanes of a
-            // store phase then cover all banks.  The loop stays one: unrolled over
-            // rows and steps the code outgrew the instruction cache.
-#pragma unroll 1
-            for (int i = 0; i < 2; i++) {
-                const int R = 2 * q + (i ^ odd);
-                decode_row<K>(tile, R, st + R * 128 + (((2 * tc) ^ (R & 7)) << 4));
-            }
+            decode_row<K>(row0, codes, stage);
+            decode_row<K>(row1, codes, stage);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (PAIR && rank == 1 && dw == 0) {
                 // block 0 issues for both: this block's arrival also says that its activations have landed
                 if (!__all_sync(0xffffffffu, bar_wait(full_b(s_b), round_b & 1, &gave_up, count)))
                     break;
-                for (int i = 0; i < kGroups; i++)
+                for (int j = 0; j < kGroups; j++)
                     if (++s_b == nb)
                         s_b = 0, round_b++;
             }
             if (lane == 0) {
                 if (PAIR && rank == 1)
-                    bar_arrive_at(at_block(full_a(s), 0));
+                    bar_arrive_at(at_block(bar, 0));
                 else
-                    bar_arrive(full_a(s));
+                    bar_arrive(bar);
             }
             next_codes();
-            slot = slot + 1 == kRing ? 0 : slot + 1;
+            codes += kSlot;
+            if (codes == ring + kRing * kSlot)
+                codes = ring;
+            stage += kGroups * kABytes;
+            bar += kGroups * 8u;
+            if (stage >= base + kAStages * kABytes)
+                stage -= kAStages * kABytes, bar -= kAStages * 8u, round++;
         }
     } else if (warp < kDecWarps + kOutWarps) {
         // ---- results ----
         const int ow = warp - kDecWarps;
         const bool keep = !PAIR && a.split > 1;             // partial sums stay in shared memory
         float *const buf = reinterpret_cast<float *>(sb + (keep ? 0 : kOutOff));
-        const int col = 4 * out_at(8 * ow + (lane >> 2)) + (lane & 3);
+        const int f4 = 8 * ow + (lane >> 2), col = 4 * out_at(f4) + (lane & 3);
+        const int col0 = 4 * swz(f4, 0) + (lane & 3), col1 = 4 * swz(f4, 1) + (lane & 3);
         asm volatile("griddepcontrol.wait;" ::: "memory");
         uint32_t acc = 0;
         bool ok = true;
@@ -291,18 +309,17 @@ __global__ void __launch_bounds__(kThreadsP, 1) product_kernel(const __grid_cons
             // needs of them from memory is asked for a chunk before: the row's scale, and
             // what y holds of a token with an adapter (to its own place in shared memory).
             float rs[2];
-            bool has[2];
+            int slot[2];                   // -1: nothing in y
             const uint32_t mine = base + kAddOff + (uint32_t)(ow * 32 + lane) * 16u;
             auto fetch = [&](int g, int64_t t) {
                 const bool in = !keep && live && t >= tl.lo && t < tl.hi;
                 rs[g] = in ? a.p.rscale[t] : 0.0f;
-                has[g] = false;
+                slot[g] = -1;
                 if (a.p.B && !a.p.h && wide_y && in) {
                     const TY *y = reinterpret_cast<const TY *>(a.p.y) + t * a.p.y_stride + tl.f0 + 8 * u;
                     copy16(mine + g * 4096u, y);
                     copy16(mine + g * 4096u + 2048u, y + 64);
-                    const int ad = a.p.slots[t];
-                    has[g] = ad >= 0 && ad < a.p.n_adapters;
+                    slot[g] = a.p.slots[t];
                 }
                 copy_group();
             };
@@ -318,32 +335,33 @@ __global__ void __launch_bounds__(kThreadsP, 1) product_kernel(const __grid_cons
                 fence_after();
                 const int n1 = min(tl.n - n0, kN);
                 for (int c0 = 0; c0 < n1; c0 += 32) {
-                    float *const dst = buf + (keep ? c0 * 128 : 0) + col;
 #pragma unroll
                     for (int g = 0; g < 2; g++) {
                         float v[16];
                         tmem_load16(tmem + (uint32_t)(ow * 32) * 65536u + d * kN + c0 + 16 * g, v);
+                        if (keep) {
 #pragma unroll
-                        for (int i = 0; i < 16; i++)
-                            dst[(16 * g + i) * 128] = v[i];
+                            for (int i = 0; i < 16; i++)
+                                buf[(c0 + 16 * g + i) * 128 + col] = v[i];
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 16; i++)
+                                buf[(16 * g + i) * 128 + (i & 1 ? col1 : col0)] = v[i];
+                        }
                     }
                     if (keep)
                         continue;
                     asm volatile("bar.sync 1, 128;" ::: "memory");
+                    rotate_first(buf, ow * 32 + lane);
+                    asm volatile("bar.sync 1, 128;" ::: "memory");
 #pragma unroll
                     for (int g = 0; g < 2; g++) {
                         const int64_t t = t_mine + n0 + c0 + 16 * g;
-                        const float4 *src = reinterpret_cast<const float4 *>(buf) + (g * 16 + ow * 4 + (lane >> 3)) * 32;
                         float x[16];
-#pragma unroll
-                        for (int m = 0; m < 4; m++) {
-                            const float4 f = src[out_at(2 * u + (m & 1) + 16 * (m >> 1))];
-                            x[4 * m] = f.x, x[4 * m + 1] = f.y, x[4 * m + 2] = f.z, x[4 * m + 3] = f.w;
-                        }
-                        scale_out(x, rs[g], right, lane);
+                        rotate_second(buf, g * 16 + ow * 4 + (lane >> 3), u, rs[g], right, x);
                         const bool in = live && t >= tl.lo && t < tl.hi;
                         copy_wait<1>();
-                        if (has[g]) {
+                        if (slot[g] >= 0 && slot[g] < a.p.n_adapters) {
                             const unsigned char *from = sb + (mine - base) + g * 4096;
                             fma8<TY>(x, 1.0f, *reinterpret_cast<const uint4 *>(from));
                             fma8<TY>(x + 8, 1.0f, *reinterpret_cast<const uint4 *>(from + 2048));
