@@ -387,98 +387,102 @@ __global__ void __launch_bounds__(kThreadsP, 1) product_kernel(const __grid_cons
     } else if (warp == kWarpB) {
         // ---- activations ----
         asm volatile("griddepcontrol.wait;" ::: "memory");
-        if (lane == 0) {
-            bool ok = true;
-            uint32_t s = 0, round = 0;
-            for (int64_t it = it0; ok && it < n_tiles; it += dit) {
-                const Tile tl = make_tile<PAIR>(a, &plan, it, rank);
-                const unsigned char *src = a.p.image + ((int64_t)k_lo * NP + tl.t0) * 128;
-                for (int k = k_lo; k < k_hi; k += a.b_steps) {
-                    if (round && !bar_wait(empty_b(s), (round - 1) & 1, &gave_up, count)) {
-                        ok = false;
-                        break;
-                    }
-                    const int steps_here = min(a.b_steps, k_hi - k);
-                    bar_expect(full_b(s), (uint32_t)(steps_here * tl.n) * (PAIR ? 64u : 128u));
-                    for (int j = 0; j < steps_here; j++, src += NP * 128) {
-                        const uint32_t dst = base + kBOff + s * b_bytes + j * b_step;
-                        if (PAIR) {
-                            // this block's half of the columns of each accumulator
-                            for (int n0 = 0; n0 < tl.n; n0 += kN) {
-                                const int half = min(tl.n - n0, kN) / 2;
-                                bulk_load(dst + n0 * 64, src + (int64_t)(n0 + rank * half) * 128, (uint32_t)half * 128u,
-                                          full_b(s));
-                            }
-                        } else {
-                            bulk_load(dst, src, (uint32_t)tl.n * 128u, full_b(s));
-                        }
-                    }
-                    issued++;
-                    if (++s == nb)
-                        s = 0, round++;
+        bool ok = true;
+        uint32_t s = 0, phase = 1;         // (the phase before the first is over)
+        for (int64_t it = it0; ok && it < n_tiles; it += dit) {
+            const Tile tl = make_tile<PAIR>(a, &plan, it, rank);
+            const unsigned char *src = a.p.image + ((int64_t)k_lo * NP + tl.t0) * 128;
+            const int64_t hop = NP * 128;
+            // PAIR: this block's half of the columns of each accumulator
+            const uint32_t n1 = PAIR ? (uint32_t)min(tl.n, kN) * 64u : (uint32_t)tl.n * 128u;
+            const uint32_t n2 = PAIR && tl.n > kN ? (uint32_t)(tl.n - kN) * 64u : 0u;
+            const unsigned char *src1 = src + (PAIR ? (uint32_t)rank * n1 : 0u);
+            const unsigned char *src2 = src + kN * 128 + (uint32_t)rank * n2;
+            for (int k = k_lo; k < k_hi; k += a.b_steps) {
+                if (!__all_sync(0xffffffffu, bar_wait(empty_b(s), phase, &gave_up, count))) {
+                    ok = false;
+                    break;
                 }
+                const int steps_here = min(a.b_steps, k_hi - k);
+                if (elect()) {
+                    uint32_t dst = base + kBOff + s * b_bytes;
+                    bar_expect(full_b(s), (uint32_t)steps_here * (n1 + n2));
+                    for (int j = 0; j < steps_here; j++, dst += b_step) {
+                        bulk_load(dst, src1 + j * hop, n1, full_b(s));
+                        if (PAIR && n2)
+                            bulk_load(dst + kN * 64, src2 + j * hop, n2, full_b(s));
+                    }
+                }
+                __syncwarp();
+                src1 += steps_here * hop;
+                src2 += steps_here * hop;
+                issued++;
+                if (++s == nb)
+                    s = 0, phase ^= 1;
             }
         }
     } else if (!PAIR || rank == 0) {
-        // ---- matrix instructions ----
-        // The warp stays together and elects the thread that issues at each step: a
-        // branch on the lane took 780 cycles a step for what takes 100 this way.
-        // What follows from the tile is kept out of the loop over the steps, which has
-        // to stay shorter than a step's decode.
-        uint32_t acc = 0, s = 0, s_phase = 0, sa = 0, sa_phase = 0;
-        bool ok = true;
-        // 16 inputs on: 32 bytes of a row along K, two groups of 8 rows along M
-        const uint64_t a0 = a.p.transposed ? operand(base, 16, 1024) : operand(base, 8192, 1024);
-        const uint64_t b0 = operand(base + kBOff, 16, 1024);
-        const uint32_t hop_a = a.p.transposed ? 32 >> 4 : 2048 >> 4;
-        for (int64_t it = it0; ok && it < n_tiles; it += dit) {
-            const Tile tl = make_tile<PAIR>(a, &plan, it, rank);
-            const bool two = PAIR && tl.n > kN;
-            ok = acc < 2 || bar_wait(acc_empty(acc & 1), ((acc >> 1) - 1) & 1, &gave_up, count);
-            if (two && acc + 1 >= 2)
-                ok = bar_wait(acc_empty((acc + 1) & 1), (((acc + 1) >> 1) - 1) & 1, &gave_up, count) && ok;
-            ok = __all_sync(0xffffffffu, ok);
-            const uint32_t shape = shape_f16(PAIR ? 256 : 128, two ? kN : tl.n, !a.p.transposed);
-            const uint32_t shape2 = shape_f16(256, tl.n - kN, !a.p.transposed);
-            const uint32_t d = tmem + (acc & 1) * kN, d2 = tmem + ((acc + 1) & 1) * kN;
-            for (int k = k_lo; ok && k < k_hi;) {
-                ok = __all_sync(0xffffffffu, bar_wait(full_b(s), s_phase, &gave_up, count));
-                const int k_end = min(k + a.b_steps, k_hi);
-                uint64_t db = b0 + (s * b_bytes >> 4);
-                for (; ok && k < k_end; k++, db += b_step >> 4) {
-                    ok = __all_sync(0xffffffffu, bar_wait(full_a(sa), sa_phase, &gave_up, count));
-                    if (!ok)
+        // ---- matrix instructions: one thread, as little around them as there can be ----
+        if (elect()) {
+            uint32_t acc = 0, s = 0, s_phase = 0, sa = 0, sa_phase = 0;
+            // 16 inputs on: 32 bytes of a row along K, two groups of 8 rows along M
+            const uint64_t a0 = a.p.transposed ? operand(base, 16, 1024) : operand(base, 8192, 1024);
+            const uint64_t b0 = operand(base + kBOff, 16, 1024);
+            const uint32_t hop_a = a.p.transposed ? 32 >> 4 : 2048 >> 4;
+            const int b_steps = a.b_steps;
+            uint64_t da = a0, db0 = b0;
+            for (int64_t it = it0; it < n_tiles; it += dit) {
+                const Tile tl = make_tile<PAIR>(a, &plan, it, rank);
+                const bool two = PAIR && tl.n > kN;
+                if (acc >= 2 && !bar_wait(acc_empty(acc & 1), ((acc >> 1) - 1) & 1, &gave_up, count))
+                    break;
+                if (two && acc + 1 >= 2 && !bar_wait(acc_empty((acc + 1) & 1), (((acc + 1) >> 1) - 1) & 1, &gave_up, count))
+                    break;
+                const uint32_t shape = shape_f16(PAIR ? 256 : 128, two ? kN : tl.n, !a.p.transposed);
+                const uint32_t shape2 = shape_f16(256, tl.n - kN, !a.p.transposed);
+                const uint32_t d = tmem + (acc & 1) * kN, d2 = tmem + ((acc + 1) & 1) * kN;
+                int left = k_hi - k_lo;
+                bool add = false;
+                while (left > 0) {
+                    if (!bar_wait(full_b(s), s_phase, &gave_up, count))
                         break;
-                    fence_after();
-                    if (elect()) {
-                        const uint64_t da = a0 + sa * (kABytes >> 4);
-                        const bool add = k > k_lo;
+                    int j = left < b_steps ? left : b_steps;
+                    left -= j;
+                    uint64_t db = db0;
+                    for (; j; j--, db += b_step >> 4) {
+                        if (!bar_wait(full_a(sa), sa_phase, &gave_up, count)) {
+                            left = -1;
+                            break;
+                        }
+                        fence_after();
 #pragma unroll
-                        for (int j = 0; j < kStep / 16; j++)
-                            mma_f16<PAIR>(d, da + j * hop_a, db + j * 2, shape, add || j > 0);
+                        for (int i = 0; i < kStep / 16; i++)
+                            mma_f16<PAIR>(d, da + i * hop_a, db + i * 2, shape, add || i > 0);
                         if (two) {
 #pragma unroll
-                            for (int j = 0; j < kStep / 16; j++)
-                                mma_f16<PAIR>(d2, da + j * hop_a, db + (kN * 64 >> 4) + j * 2, shape2, add || j > 0);
+                            for (int i = 0; i < kStep / 16; i++)
+                                mma_f16<PAIR>(d2, da + i * hop_a, db + (kN * 64 >> 4) + i * 2, shape2, add || i > 0);
                         }
+                        add = true;
                         commit<PAIR>(empty_a(sa));
-                        if (k + 1 == k_end)
-                            commit<PAIR>(empty_b(s));
+                        da += kABytes >> 4;
+                        if (++sa == kAStages)
+                            sa = 0, sa_phase ^= 1, da = a0;
                     }
-                    __syncwarp();
-                    if (++sa == kAStages)
-                        sa = 0, sa_phase ^= 1;
+                    if (left < 0)
+                        break;
+                    commit<PAIR>(empty_b(s));
+                    db0 += b_bytes >> 4;
+                    if (++s == nb)
+                        s = 0, s_phase ^= 1, db0 = b0;
                 }
-                if (++s == nb)
-                    s = 0, s_phase ^= 1;
-            }
-            if (ok && elect()) {
+                if (gave_up)
+                    break;
                 commit<PAIR>(acc_full(acc & 1));
                 if (two)
                     commit<PAIR>(acc_full((acc + 1) & 1));
+                acc += two ? 2 : 1;
             }
-            __syncwarp();
-            acc += two ? 2 : 1;
         }
     }
     __syncwarp();
