@@ -89,8 +89,10 @@ exl3_status launch_product_few(const ProductLaunch &p, cudaStream_t s);
 
 // Adapters of more than a few tokens (linear_adapt.cu), tokens sorted by adapter
 struct AdaptPlan {
+    int4 *tiles;              // adapter, first place in perm and tokens of each tile of 32
     int32_t *perm;            // [T] tokens by adapter (those without one left out)
-    int32_t *seg, *first;     // [n + 1] where an adapter's tokens and its tiles of 32 begin
+    int32_t *seg;             // [n + 1] where an adapter's tokens begin
+    int32_t *n_tiles;
     uint32_t *largest;        // [2][n]
 };
 size_t adapt_plan_ints(int64_t T, int n);

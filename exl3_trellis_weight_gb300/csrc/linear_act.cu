@@ -50,13 +50,14 @@ template <typename TX, bool VEC> __device__ __forceinline__ void shrink_rows(con
     }
 }
 
-// grid: (rows, 1 + adapters' rows), one row at a time; block: a multiple of 32 threads, 16 inputs
-// each.  ONE: the row fits one round of the block and stays in registers.
+// grid: (blocks of neighbouring rows, 1 + adapters' rows); block: a multiple of 32
+// threads, 16 inputs each.  ONE: a row fits one round of the block and stays in
+// registers, `left` too while the expert stays the same, and the next row is on its way.
 template <typename TX, bool VEC, bool ONE>
 __global__ void prep_kernel(const PrepLaunch a) {
     __shared__ int32_t off[kMaxExperts + 1];
-    __shared__ float wmax[32];
-    const int tid = threadIdx.x;
+    __shared__ float wmax[2][32];
+    const int tid = threadIdx.x, warps = (int)(blockDim.x >> 5);
     const int64_t NP = act_rows(a.T);
     // the product kernel behind this one may start on the codes; it waits for this
     // kernel's end before it reads z.  (This kernel itself starts after everything
@@ -71,36 +72,68 @@ __global__ void prep_kernel(const PrepLaunch a) {
             off[i] = a.offsets[i];
         __syncthreads();
     }
-    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+    const int64_t t_lo = a.T * blockIdx.x / gridDim.x, t_hi = a.T * (blockIdx.x + 1) / gridDim.x;
+    const TX *x = reinterpret_cast<const TX *>(a.x) + tid * 16;
+    const bool in0 = tid * 16 < a.n;
+    uint4 raw[2];
+    float lf[16];
+    int e_left = -1, turn = 0;
+    if (ONE && VEC && in0 && t_lo < t_hi)
+        load16_raw(x + t_lo * a.stride, raw);
+    for (int64_t t = t_lo; t < t_hi; t++) {
         int e = 0;
-        if (a.offsets) {
+        if (a.offsets)
             e = expert_of(off, a.E, t);
-            if (e < 0) {                 // no expert: no product, the result row is 0
-                uint16_t *y = reinterpret_cast<uint16_t *>(a.y) + t * a.y_stride;
-                for (int c = tid; c < a.y_cols; c += blockDim.x)
-                    y[c] = 0;
-                continue;
+        float v[16];
+        if (ONE) {
+            if (VEC) {
+                unpack16<TX>(raw, v);
+                if (in0 && t + 1 < t_hi)
+                    load16_raw(x + (t + 1) * a.stride, raw);
+            } else if (in0) {
+                load16<TX, false>(x + t * a.stride, v);
             }
         }
-        const TX *x = reinterpret_cast<const TX *>(a.x) + t * a.stride;
+        if (e < 0) {                       // no expert: no product, the result row is 0
+            uint16_t *y = reinterpret_cast<uint16_t *>(a.y) + t * a.y_stride;
+            for (int c = tid; c < a.y_cols; c += blockDim.x)
+                y[c] = 0;
+            continue;
+        }
         const float *left = a.left + (size_t)e * a.n;
-        float v[16];
         float m = 0.0f;
-        for (int k = tid * 16; k < a.n; k += blockDim.x * 16) {
-            load16<TX, VEC>(x + k, v);
-            mul16(left + k, v);
+        if (ONE) {
+            if (e != e_left && in0) {
+#pragma unroll
+                for (int i = 0; i < 16; i++)
+                    lf[i] = 1.0f;
+                mul16(left + tid * 16, lf);
+                e_left = e;
+            }
+#pragma unroll
+            for (int i = 0; i < 16; i++)
+                v[i] = in0 ? __fmul_rn(v[i], lf[i]) : 0.0f;
             m = max16(v, m);
+        } else {
+            for (int k = 0; k + tid * 16 < a.n; k += blockDim.x * 16) {
+                load16<TX, VEC>(x + t * a.stride + k, v);
+                mul16(left + k + tid * 16, v);
+                m = max16(v, m);
+            }
         }
 #pragma unroll
         for (int d = 16; d; d >>= 1)
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-        __syncthreads();                 // the previous row's reads of wmax are done
+        // (two places in turn: a row's reads are done before the barrier of the next)
+        float *const w = wmax[turn];
+        turn ^= 1;
         if ((tid & 31) == 0)
-            wmax[tid >> 5] = m;
+            w[tid >> 5] = m;
         __syncthreads();
-        m = 0.0f;
-        for (int w = 0; w < (int)(blockDim.x >> 5); w++)
-            m = fmaxf(m, wmax[w]);
+        m = (tid & 31) < warps ? w[tid & 31] : 0.0f;
+#pragma unroll
+        for (int d = 16; d; d >>= 1)
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
         float up, down;
         row_scale(m, up, down);
         if (tid == 0)
@@ -109,7 +142,7 @@ __global__ void prep_kernel(const PrepLaunch a) {
             const int k = k0 + tid * 16;
             const bool in = k < a.n;
             if (!ONE && in) {
-                load16<TX, VEC>(x + k, v);
+                load16<TX, VEC>(x + t * a.stride + k0, v);
                 mul16(left + k, v);
             }
             if (!in) {
@@ -122,22 +155,22 @@ __global__ void prep_kernel(const PrepLaunch a) {
                 v[i] = __fmul_rn(v[i], up);
             rotate128(v, tid);
             if (in) {
-                uint32_t w[8];
+                uint32_t w8[8];
                 if (a.order == 0) {
 #pragma unroll
                     for (int i = 0; i < 8; i++)
-                        w[i] = pack2<__half>(v[2 * i], v[2 * i + 1]);
+                        w8[i] = pack2<__half>(v[2 * i], v[2 * i + 1]);
                 } else if (a.order == 1) {
 #pragma unroll
                     for (int i = 0; i < 8; i++)
-                        w[i] = pack2<__half>(v[(i >> 1) + 8 * (i & 1)], v[(i >> 1) + 8 * (i & 1) + 4]);
+                        w8[i] = pack2<__half>(v[(i >> 1) + 8 * (i & 1)], v[(i >> 1) + 8 * (i & 1) + 4]);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 8; i++)
-                        w[i] = pack2<__half>(v[2 * (i >> 1) + 8 * (i & 1)], v[2 * (i >> 1) + 8 * (i & 1) + 1]);
+                        w8[i] = pack2<__half>(v[2 * (i >> 1) + 8 * (i & 1)], v[2 * (i >> 1) + 8 * (i & 1) + 1]);
                 }
-                *reinterpret_cast<uint4 *>(a.image + act_offset(NP, t, k)) = make_uint4(w[0], w[1], w[2], w[3]);
-                *reinterpret_cast<uint4 *>(a.image + act_offset(NP, t, k + 8)) = make_uint4(w[4], w[5], w[6], w[7]);
+                *reinterpret_cast<uint4 *>(a.image + act_offset(NP, t, k)) = make_uint4(w8[0], w8[1], w8[2], w8[3]);
+                *reinterpret_cast<uint4 *>(a.image + act_offset(NP, t, k + 8)) = make_uint4(w8[4], w8[5], w8[6], w8[7]);
             }
         }
     }
@@ -158,7 +191,7 @@ exl3_status launch_prep(const PrepLaunch &p, cudaStream_t s) {
     unsigned block = (unsigned)((p.n / 16 + 31) / 32 * 32);
     block = block > 1024 ? 1024 : block;
     const bool one = (int64_t)block * 16 >= p.n;
-    const int64_t most = (int64_t)device_sm_count() * (2048 / block);
+    const int64_t most = (int64_t)device_sm_count() * (1024 / block);
     const dim3 grid((unsigned)(p.T < most ? p.T : most),
                     1 + (p.n_adapters ? (unsigned)((p.rank + block / 32 - 1) / (block / 32)) : 0u));
     if (p.dt == EXL3_BF16)

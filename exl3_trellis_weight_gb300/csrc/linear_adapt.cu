@@ -88,17 +88,23 @@ template <typename TX> __device__ __forceinline__ void operand_scale(float m, fl
 
 // ---- plan --------------------------------------------------------------------
 // grid: 32 adapters a block, one a warp.  perm: tokens by adapter, seg: where each
-// adapter's begin, first: its tiles.
+// adapter's begin, tiles: the adapter, first place in perm and tokens of each tile.
+constexpr int kScan = 4096;                // tokens looked at at a time
+
 __global__ void __launch_bounds__(1024) plan_kernel(const AdaptLaunch a) {
-    __shared__ int count[kMaxAdapters], sums[2][32];
+    __shared__ int32_t slot[kScan];
+    __shared__ int count[kMaxAdapters], tile0[kMaxAdapters], sums[2][32];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     count[tid] = 0;
     __syncthreads();
-    for (int64_t t = tid; t < a.T; t += 1024) {
-        const int s = a.slots[t];
-        if (s >= 0 && s < a.n)
-            atomicAdd(&count[s], 1);
+    for (int64_t t0 = 0; t0 < a.T; t0 += 1024) {
+        // a count for each adapter of a warp's tokens, added once
+        const int64_t t = t0 + tid;
+        const int s = t < a.T ? a.slots[t] : -1;
+        const unsigned same = __match_any_sync(0xffffffffu, s);
+        if (s >= 0 && s < a.n && lane == __ffs(same) - 1)
+            atomicAdd(&count[s], __popc(same));
     }
     __syncthreads();
     // exclusive sums over the adapters, of tokens and of tiles
@@ -127,47 +133,46 @@ __global__ void __launch_bounds__(1024) plan_kernel(const AdaptLaunch a) {
     }
     if (blockIdx.x == 0 && tid < a.n) {
         a.plan.seg[tid] = at[0];
-        a.plan.first[tid] = at[1];
         a.plan.largest[tid] = a.plan.largest[a.n + tid] = 0u;
         if (tid == a.n - 1) {
             a.plan.seg[a.n] = at[0] + own[0];
-            a.plan.first[a.n] = at[1] + own[1];
+            *a.plan.n_tiles = at[1] + own[1];
         }
     }
-    __syncthreads();
-    count[tid] = at[0];
+    count[tid] = at[0];                    // (each thread its own)
+    tile0[tid] = at[1];
     __syncthreads();
     const int i = blockIdx.x * 32 + warp;
-    if (i >= a.n)
-        return;
-    int32_t *to = a.plan.perm + count[i];
+    int to = i < a.n ? count[i] : 0;
+    const int from = to;
+    for (int64_t t0 = 0; t0 < a.T; t0 += kScan) {
+        const int n = (int)(a.T - t0 < kScan ? a.T - t0 : kScan);
+        __syncthreads();
+        for (int t = tid; t < kScan; t += 1024)
+            slot[t] = t < n ? a.slots[t0 + t] : -1;
+        __syncthreads();
+        if (i < a.n)
 #pragma unroll 4
-    for (int64_t t0 = 0; t0 < a.T; t0 += 32) {
-        const int64_t t = t0 + lane;
-        const bool mine = t < a.T && a.slots[t] == i;
-        const unsigned b = __ballot_sync(0xffffffffu, mine);
-        if (mine)
-            to[__popc(b & ((1u << lane) - 1u))] = (int32_t)t;
-        to += __popc(b);
+            for (int t = lane; t < kScan; t += 32) {
+                if (t - lane >= n)
+                    break;
+                const bool mine = slot[t] == i;
+                const unsigned b = __ballot_sync(0xffffffffu, mine);
+                if (mine)
+                    a.plan.perm[to + __popc(b & ((1u << lane) - 1u))] = (int32_t)(t0 + t);
+                to += __popc(b);
+            }
     }
+    if (i < a.n)
+        for (int k = lane; from + k * kTile < to; k += 32)
+            a.plan.tiles[tile0[i] + k] = make_int4(i, from + k * kTile, min(kTile, to - from - k * kTile), 0);
 }
 
-// tile -> adapter and its tokens [lo, lo + n) of perm; false when there is no such tile
+// a tile's adapter and its tokens [lo, lo + n) of perm; false when there is no such tile
 __device__ __forceinline__ bool find_tile(const AdaptLaunch &a, int tile, int &i, int &lo, int &n) {
-    if (tile >= a.plan.first[a.n])
-        return false;
-    int l = 0, h = a.n - 1;                // last adapter with first <= tile
-    while (l < h) {
-        const int m = (l + h + 1) >> 1;
-        if (a.plan.first[m] <= tile)
-            l = m;
-        else
-            h = m - 1;
-    }
-    i = l;
-    lo = a.plan.seg[l] + (tile - a.plan.first[l]) * kTile;
-    n = min(kTile, a.plan.seg[l + 1] - lo);
-    return true;
+    const int4 t = a.plan.tiles[tile];     // (behind the last one it is not used)
+    i = t.x, lo = t.y, n = t.z;
+    return tile < *a.plan.n_tiles;
 }
 
 // ---- shrink: h[t][r] = gain_i sum_k M_i[r][k] x[t][k] ---------------------------
@@ -301,12 +306,17 @@ template <typename TX> __global__ void __launch_bounds__(256) expand_kernel(cons
         copy_group();
     };
     load(f_lo, 0);
-    // h of the tile in the operand's type, scaled by a power of two
-    float m = 0.0f;
-    for (int e = tid; e < kTile * R16; e += 256) {
-        const int t = e / R16, q = e % R16;
-        if (t < n && q < r)
-            m = fmaxf(m, fabsf(sd.h[(int64_t)a.plan.perm[lo + t] * a.rank + q]));
+    // h of the tile in the operand's type, scaled by a power of two: token tid / 8,
+    // elements tid % 8 + 8 q
+    float hv[16], m = 0.0f;
+    {
+        const int t = tid >> 3, hq = tid & 7;
+        const float *from = sd.h + (t < n ? (int64_t)a.plan.perm[lo + t] * a.rank : 0);
+#pragma unroll
+        for (int q = 0; q < 16; q++) {
+            hv[q] = t < n && q < 2 * kb && hq + 8 * q < r ? from[hq + 8 * q] : 0.0f;
+            m = fmaxf(m, fabsf(hv[q]));
+        }
     }
 #pragma unroll
     for (int d = 16; d; d >>= 1)
@@ -320,11 +330,10 @@ template <typename TX> __global__ void __launch_bounds__(256) expand_kernel(cons
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
     float up, down;
     operand_scale<TX>(m, up, down);
-    for (int e = tid; e < kTile * R16; e += 256) {
-        const int t = e / R16, q = e % R16;
-        const float v = t < n && q < r ? sd.h[(int64_t)a.plan.perm[lo + t] * a.rank + q] : 0.0f;
-        sh[t * hrow + q] = from_f32<TX>(__fmul_rn(v, up));
-    }
+#pragma unroll
+    for (int q = 0; q < 16; q++)
+        if (q < 2 * kb)
+            sh[(tid >> 3) * hrow + (tid & 7) + 8 * q] = from_f32<TX>(__fmul_rn(hv[q], up));
     const uint32_t ha = saddr(smem) + (uint32_t)(((warp & 1) * 16 + g) * hrow + 2 * j) * 2;
     for (int f0 = f_lo, buf = 0; f0 < f_hi; f0 += 128, buf ^= 1) {
         load(f0 + 128, buf ^ 1);
@@ -396,37 +405,48 @@ template <typename TX, bool VEC> __global__ void __launch_bounds__(256) outer_ke
     const int tiles = (n + kTile - 1) / kTile;
     const int mine = r > 0 && tiles > rank ? (tiles - 1 - rank) / a.split + 1 : 0;
     const uint16_t *x = reinterpret_cast<const uint16_t *>(sd.x) + chunk * 128;
-    // copies of a tile: tokens tid / 16 and tid / 16 + 16, 8 elements each
+    // copies of a tile: tokens tid / 16 and tid / 16 + 16, 8 elements each.  The tokens'
+    // rows are looked up a tile before they are copied.
     const int row = tid >> 4, c8 = (tid & 15) * 8;
-    auto load = [&](int s) {
-        if (s < mine) {
-            const int t0 = (rank + s * a.split) * kTile;
+    int next[2];
+    auto lookup = [&](int s) {
 #pragma unroll
-            for (int b = 0; b < 2; b++) {
-                const int t = t0 + row + 16 * b;
-                const bool real = t < n;
-                row8<VEC>(base + (uint32_t)(s % kOuterStages) * xbytes + (uint32_t)((row + 16 * b) * kXRow + c8) * 2,
-                          x + (int64_t)(real ? a.plan.perm[lo + t] : 0) * sd.stride + c8, real);
-            }
+        for (int b = 0; b < 2; b++) {
+            const int t = (rank + s * a.split) * kTile + row + 16 * b;
+            next[b] = s < mine && t < n ? a.plan.perm[lo + t] : -1;
         }
-        copy_group();
     };
-    // h of a tile: token tid / 8, elements tid % 8 + 8 q
+    auto load = [&](int s) {
+        if (s < mine)
+#pragma unroll
+            for (int b = 0; b < 2; b++)
+                row8<VEC>(base + (uint32_t)(s % kOuterStages) * xbytes + (uint32_t)((row + 16 * b) * kXRow + c8) * 2,
+                          x + (int64_t)max(next[b], 0) * sd.stride + c8, next[b] >= 0);
+        copy_group();
+        lookup(s + 1);
+    };
+    // h of a tile: token tid / 8, elements tid % 8 + 8 q, in the same way
     const int ht = tid >> 3, hq = tid & 7;
     float hv[16];
-    auto fetch = [&](int s) {
+    int hnext;
+    auto hlookup = [&](int s) {
         const int t = (rank + s * a.split) * kTile + ht;
-        const bool real = s < mine && t < n;
-        const float *from = sd.h + (real ? (int64_t)a.plan.perm[lo + t] * a.rank : 0);
+        hnext = s < mine && t < n ? a.plan.perm[lo + t] : -1;
+    };
+    auto fetch = [&](int s) {
+        const float *from = sd.h + (int64_t)max(hnext, 0) * a.rank;
 #pragma unroll
         for (int q = 0; q < 16; q++)
             if (q < 2 * mb)
-                hv[q] = real && hq + 8 * q < r ? __fmul_rn(from[hq + 8 * q], up) : 0.0f;
+                hv[q] = hnext >= 0 && hq + 8 * q < r ? from[hq + 8 * q] : 0.0f;
+        hlookup(s + 1);
     };
+    hlookup(0);
+    lookup(0);
+    fetch(0);
 #pragma unroll
     for (int s = 0; s < kOuterStages - 1; s++)
         load(s);
-    fetch(0);
     float acc[8][2][4];
 #pragma unroll
     for (int m = 0; m < 8; m++)
@@ -440,7 +460,7 @@ template <typename TX, bool VEC> __global__ void __launch_bounds__(256) outer_ke
 #pragma unroll
         for (int q = 0; q < 16; q++)
             if (q < 2 * mb)
-                sh[ht * hrow + hq + 8 * q] = from_f32<TX>(hv[q]);
+                sh[ht * hrow + hq + 8 * q] = from_f32<TX>(__fmul_rn(hv[q], up));
         copy_wait<kOuterStages - 2>();
         __syncthreads();
         load(s + kOuterStages - 1);
@@ -531,14 +551,17 @@ bool wide_rows(const AdaptSide &s) { return ((uintptr_t)s.x & 15u) == 0 && s.str
 
 }  // namespace
 
-size_t adapt_plan_ints(int64_t T, int n) { return (size_t)T + 4 * (size_t)n + 2; }
+size_t adapt_plan_ints(int64_t T, int n) {
+    return 4 * ((size_t)T / kTile + n + 1) + (size_t)T + 3 * (size_t)n + 2;
+}
 
 AdaptPlan adapt_plan(int32_t *ints, int64_t T, int n) {
     AdaptPlan p;
-    p.perm = ints;
-    p.seg = ints + T;
-    p.first = p.seg + n + 1;
-    p.largest = reinterpret_cast<uint32_t *>(p.first + n + 1);
+    p.tiles = reinterpret_cast<int4 *>(ints);
+    p.perm = ints + 4 * (T / kTile + n + 1);
+    p.seg = p.perm + T;
+    p.n_tiles = p.seg + n + 1;
+    p.largest = reinterpret_cast<uint32_t *>(p.n_tiles + 1);
     return p;
 }
 
@@ -548,7 +571,7 @@ exl3_status launch_adapt_plan(const AdaptLaunch &p, cudaStream_t s) {
 
 exl3_status launch_shrink(const AdaptLaunch &p0, int sides, cudaStream_t s) {
     AdaptLaunch p = p0;
-    const int64_t tiles = (p.T + kTile - 1) / kTile + (p.n < p.T ? p.n : p.T);    // at most
+    const int64_t tiles = p.T / kTile + (p.n < p.T ? p.n : p.T);    // at most
     // blocks that would idle share the sums, at least 4 steps of 64 each
     const int64_t sms = device_sm_count();
     int least = p.side[0].n;
@@ -569,7 +592,7 @@ exl3_status launch_shrink(const AdaptLaunch &p0, int sides, cudaStream_t s) {
 }
 
 exl3_status launch_expand(const AdaptLaunch &p, void *y, int64_t y_stride, cudaStream_t s) {
-    const int64_t tiles = (p.T + kTile - 1) / kTile + (p.n < p.T ? p.n : p.T);
+    const int64_t tiles = p.T / kTile + (p.n < p.T ? p.n : p.T);
     const int R16 = (p.rank + 15) / 16 * 16;
     const size_t smem = (size_t)kTile * (R16 + kPad) * 2 + (size_t)2 * R16 * (128 + kPad) * 2 + (size_t)kTile * (128 + kPad) * 2;
     const dim3 grid((unsigned)tiles, (unsigned)((p.side[0].n + 511) / 512));

@@ -11,6 +11,20 @@
 
 namespace exl3 {
 
+template <typename TX> __device__ __forceinline__ void load16_raw(const TX *p, uint4 (&r)[2]) {
+    r[0] = __ldg(reinterpret_cast<const uint4 *>(p));
+    r[1] = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
+}
+template <typename TX> __device__ __forceinline__ void unpack16(const uint4 (&r)[2], float (&v)[16]) {
+    const uint32_t w[8] = {r[0].x, r[0].y, r[0].z, r[0].w, r[1].x, r[1].y, r[1].z, r[1].w};
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        const float2 f = unpack2<TX>(w[i]);
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+    }
+}
+
 template <typename TX, bool VEC>
 __device__ __forceinline__ void load16(const TX *p, float (&v)[16]) {
     if constexpr (VEC) {
