@@ -30,13 +30,36 @@ exl3_status cuda_check(cudaError_t e, const char *what) {
 }
 
 int device_sm_count() {
+    // a device's count does not change: looked up once for each
+    static std::atomic<int> known[64];
     int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
+    if (cudaGetDevice(&dev) != cudaSuccess) {
         (void)cudaGetLastError();
         return 152;   // GB300 (two dies x 76 SMs) when no device can be queried
     }
+    if (dev >= 0 && dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0)
+        return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
+        (void)cudaGetLastError();
+        return 152;
+    }
+    if (dev >= 0 && dev < 64)
+        known[dev].store(n, std::memory_order_relaxed);
     return n;
+}
+
+cudaError_t allow_smem(const void *kernel, size_t bytes, SmemAllowed &allowed) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    const bool slot = dev >= 0 && dev < 64;
+    if (slot && allowed.bytes[dev].load(std::memory_order_relaxed) >= (int)bytes)
+        return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess && slot)
+        allowed.bytes[dev].store((int)bytes, std::memory_order_relaxed);
+    return e;
 }
 
 // ---- profiling ----------------------------------------------------------------

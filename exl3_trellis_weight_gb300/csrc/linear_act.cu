@@ -154,23 +154,35 @@ __global__ void prep_kernel(const PrepLaunch a) {
             for (int i = 0; i < 16; i++)
                 v[i] = __fmul_rn(v[i], up);
             rotate128(v, tid);
+            uint32_t w8[8];
+            if (a.order == 0) {
+#pragma unroll
+                for (int i = 0; i < 8; i++)
+                    w8[i] = pack2<__half>(v[2 * i], v[2 * i + 1]);
+            } else if (a.order == 1) {
+#pragma unroll
+                for (int i = 0; i < 8; i++)
+                    w8[i] = pack2<__half>(v[(i >> 1) + 8 * (i & 1)], v[(i >> 1) + 8 * (i & 1) + 4]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; i++)
+                    w8[i] = pack2<__half>(v[2 * (i >> 1) + 8 * (i & 1)], v[2 * (i >> 1) + 8 * (i & 1) + 1]);
+            }
+            // Lanes l and l + 4 (the same places of two blocks of 64) swap a half, so that
+            // eight lanes write one block's whole 128 bytes at a time
+            const bool high = (tid & 4) != 0;
+            uint32_t first[4], second[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? w8[i] : w8[4 + i], 4);
+                first[i] = high ? got : w8[i];
+                second[i] = high ? w8[4 + i] : got;
+            }
             if (in) {
-                uint32_t w8[8];
-                if (a.order == 0) {
-#pragma unroll
-                    for (int i = 0; i < 8; i++)
-                        w8[i] = pack2<__half>(v[2 * i], v[2 * i + 1]);
-                } else if (a.order == 1) {
-#pragma unroll
-                    for (int i = 0; i < 8; i++)
-                        w8[i] = pack2<__half>(v[(i >> 1) + 8 * (i & 1)], v[(i >> 1) + 8 * (i & 1) + 4]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; i++)
-                        w8[i] = pack2<__half>(v[2 * (i >> 1) + 8 * (i & 1)], v[2 * (i >> 1) + 8 * (i & 1) + 1]);
-                }
-                *reinterpret_cast<uint4 *>(a.image + act_offset(NP, t, k)) = make_uint4(w8[0], w8[1], w8[2], w8[3]);
-                *reinterpret_cast<uint4 *>(a.image + act_offset(NP, t, k + 8)) = make_uint4(w8[4], w8[5], w8[6], w8[7]);
+                // elements 8 high .. of the pair's 16, of the lower and of the upper block
+                const int k1 = (k & ~127) + (k & 48) + (high ? 8 : 0);
+                *reinterpret_cast<uint4 *>(a.image + act_offset(NP, t, k1)) = make_uint4(first[0], first[1], first[2], first[3]);
+                *reinterpret_cast<uint4 *>(a.image + act_offset(NP, t, k1 + 64)) = make_uint4(second[0], second[1], second[2], second[3]);
             }
         }
     }

@@ -98,13 +98,20 @@ __global__ void __launch_bounds__(1024) plan_kernel(const AdaptLaunch a) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     count[tid] = 0;
     __syncthreads();
-    for (int64_t t0 = 0; t0 < a.T; t0 += 1024) {
+    for (int64_t t0 = 0; t0 < a.T; t0 += 4096) {
+        int s[4];
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            const int64_t t = t0 + k * 1024 + tid;
+            s[k] = t < a.T ? a.slots[t] : -1;
+        }
         // a count for each adapter of a warp's tokens, added once
-        const int64_t t = t0 + tid;
-        const int s = t < a.T ? a.slots[t] : -1;
-        const unsigned same = __match_any_sync(0xffffffffu, s);
-        if (s >= 0 && s < a.n && lane == __ffs(same) - 1)
-            atomicAdd(&count[s], __popc(same));
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            const unsigned same = __match_any_sync(0xffffffffu, s[k]);
+            if (s[k] >= 0 && s[k] < a.n && lane == __ffs(same) - 1)
+                atomicAdd(&count[s[k]], __popc(same));
+        }
     }
     __syncthreads();
     // exclusive sums over the adapters, of tokens and of tiles
@@ -152,15 +159,17 @@ __global__ void __launch_bounds__(1024) plan_kernel(const AdaptLaunch a) {
             slot[t] = t < n ? a.slots[t0 + t] : -1;
         __syncthreads();
         if (i < a.n)
-#pragma unroll 4
-            for (int t = lane; t < kScan; t += 32) {
-                if (t - lane >= n)
-                    break;
-                const bool mine = slot[t] == i;
-                const unsigned b = __ballot_sync(0xffffffffu, mine);
-                if (mine)
-                    a.plan.perm[to + __popc(b & ((1u << lane) - 1u))] = (int32_t)(t0 + t);
-                to += __popc(b);
+            for (int t = lane; t - lane < n; t += 256) {
+                unsigned b[8];
+#pragma unroll
+                for (int k = 0; k < 8; k++)
+                    b[k] = __ballot_sync(0xffffffffu, slot[t + 32 * k] == i);
+#pragma unroll
+                for (int k = 0; k < 8; k++) {
+                    if (b[k] >> lane & 1u)
+                        a.plan.perm[to + __popc(b[k] & ((1u << lane) - 1u))] = (int32_t)(t0 + t + 32 * k);
+                    to += __popc(b[k]);
+                }
             }
     }
     if (i < a.n)
@@ -177,9 +186,9 @@ __device__ __forceinline__ bool find_tile(const AdaptLaunch &a, int tile, int &i
 
 // ---- shrink: h[t][r] = gain_i sum_k M_i[r][k] x[t][k] ---------------------------
 // A block takes one tile and a share of the sum (the blocks of a cluster split it);
-// warp w the tokens 16 (w % 2) .. and the sixteenth w / 2 of every step of 64.
-constexpr int kShrinkStages = 4;
-constexpr int kRow = 64 + kPad;
+// warp w the tokens 16 (w % 2) .. and two sixteenths of every step of 128.
+constexpr int kShrinkStages = 3;
+constexpr int kRow = 128 + kPad;
 
 template <typename TX, bool VEC> __global__ void __launch_bounds__(256) shrink_kernel(const AdaptLaunch a) {
     extern __shared__ __align__(16) unsigned char smem[];
@@ -192,20 +201,24 @@ template <typename TX, bool VEC> __global__ void __launch_bounds__(256) shrink_k
     if (!find_tile(a, (int)(blockIdx.x / a.split), i, lo, n))
         return;                            // (the whole cluster)
     const int r = rank_of(a.ranks, i, a.rank), R8 = (a.rank + 7) / 8 * 8, nb = (r + 7) / 8;
-    const int steps = sd.n / 64, k_lo = steps * rank / a.split, k_hi = steps * (rank + 1) / a.split;
+    const int steps = sd.n / 128, k_lo = steps * rank / a.split, k_hi = steps * (rank + 1) / a.split;
     const uint32_t base = saddr(smem), stage = (uint32_t)(kTile + R8) * kRow * 2;
     const uint16_t *x = reinterpret_cast<const uint16_t *>(sd.x);
     const uint16_t *M = reinterpret_cast<const uint16_t *>(sd.M) + (size_t)i * a.rank * sd.n;
-    // copies of a step: token tid / 8 and rows tid / 8 + 32 m of the factor, 8 elements each
-    const int row = tid >> 3, c8 = (tid & 7) * 8;
-    const bool real = row < n;
-    const uint16_t *xr = x + (int64_t)(real ? a.plan.perm[lo + row] : 0) * sd.stride + c8;
+    // copies of a step: tokens tid / 16 and tid / 16 + 16, rows tid / 16 + 16 m of the factor, 8 elements each
+    const int row = tid >> 4, c8 = (tid & 15) * 8;
+    const uint16_t *xr[2];
+#pragma unroll
+    for (int b = 0; b < 2; b++)
+        xr[b] = x + (int64_t)(row + 16 * b < n ? a.plan.perm[lo + row + 16 * b] : 0) * sd.stride + c8;
     auto load = [&](int k) {
         if (k < k_hi) {
             const uint32_t st = base + (uint32_t)((k - k_lo) % kShrinkStages) * stage;
-            row8<VEC>(st + (uint32_t)(row * kRow + c8) * 2, xr + (int64_t)k * 64, real);
-            for (int q = row; q < nb * 8; q += 32)
-                copy16z(st + (uint32_t)((kTile + q) * kRow + c8) * 2, M + (size_t)min(q, a.rank - 1) * sd.n + k * 64 + c8, q < r);
+#pragma unroll
+            for (int b = 0; b < 2; b++)
+                row8<VEC>(st + (uint32_t)((row + 16 * b) * kRow + c8) * 2, xr[b] + (int64_t)k * 128, row + 16 * b < n);
+            for (int q = row; q < nb * 8; q += 16)
+                copy16z(st + (uint32_t)((kTile + q) * kRow + c8) * 2, M + (size_t)min(q, a.rank - 1) * sd.n + k * 128 + c8, q < r);
         }
         copy_group();
     };
@@ -218,18 +231,22 @@ template <typename TX, bool VEC> __global__ void __launch_bounds__(256) shrink_k
 #pragma unroll
         for (int e = 0; e < 4; e++)
             acc[b][e] = 0.0f;
-    const uint32_t at = (uint32_t)(((warp & 1) * 16 + g) * kRow + (warp >> 1) * 16 + 2 * j) * 2;
-    const uint32_t bt = (uint32_t)((kTile + g) * kRow + (warp >> 1) * 16 + 2 * j) * 2;
+    const uint32_t at = (uint32_t)(((warp & 1) * 16 + g) * kRow + (warp >> 1) * 32 + 2 * j) * 2;
+    const uint32_t bt = (uint32_t)((kTile + g) * kRow + (warp >> 1) * 32 + 2 * j) * 2;
     for (int k = k_lo; k < k_hi; k++) {
         copy_wait<kShrinkStages - 2>();
         __syncthreads();
         load(k + kShrinkStages - 1);
         const uint32_t st = base + (uint32_t)((k - k_lo) % kShrinkStages) * stage;
-        uint32_t f[4] = {lds32(st + at), lds32(st + at + 16 * kRow), lds32(st + at + 16), lds32(st + at + 16 * kRow + 16)};
 #pragma unroll
-        for (int b = 0; b < 16; b++)
-            if (b < nb)
-                mma<TX>(acc[b], f, lds32(st + bt + b * 16 * kRow), lds32(st + bt + b * 16 * kRow + 16));
+        for (int h = 0; h < 64; h += 32) {
+            const uint32_t f[4] = {lds32(st + at + h), lds32(st + at + h + 16 * kRow), lds32(st + at + h + 16),
+                                   lds32(st + at + h + 16 * kRow + 16)};
+#pragma unroll
+            for (int b = 0; b < 16; b++)
+                if (b < nb)
+                    mma<TX>(acc[b], f, lds32(st + bt + h + b * 16 * kRow), lds32(st + bt + h + b * 16 * kRow + 16));
+        }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
@@ -572,13 +589,13 @@ exl3_status launch_adapt_plan(const AdaptLaunch &p, cudaStream_t s) {
 exl3_status launch_shrink(const AdaptLaunch &p0, int sides, cudaStream_t s) {
     AdaptLaunch p = p0;
     const int64_t tiles = p.T / kTile + (p.n < p.T ? p.n : p.T);    // at most
-    // blocks that would idle share the sums, at least 4 steps of 64 each
+    // blocks that would idle share the sums, at least 4 steps of 128 each
     const int64_t sms = device_sm_count();
     int least = p.side[0].n;
     if (sides > 1 && p.side[1].n < least)
         least = p.side[1].n;
     p.split = 1;
-    while (p.split < 8 && tiles * sides * p.split * 2 <= 2 * sms && least / 64 >= p.split * 2 * 4)
+    while (p.split < 8 && tiles * sides * p.split * 2 <= 2 * sms && least / 128 >= p.split * 2 * 4)
         p.split *= 2;
     const int R8 = (p.rank + 7) / 8 * 8;
     const size_t stages = (size_t)kShrinkStages * (kTile + R8) * kRow * 2, part = (size_t)4 * kTile * R8 * 4;
