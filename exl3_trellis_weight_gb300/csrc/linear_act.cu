@@ -50,6 +50,21 @@ template <typename TX, bool VEC> __device__ __forceinline__ void shrink_rows(con
     }
 }
 
+// the largest of the block's m, in every thread; one barrier
+__device__ __forceinline__ float block_max(float m, float *place, int warps) {
+#pragma unroll
+    for (int d = 16; d; d >>= 1)
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    if ((threadIdx.x & 31) == 0)
+        place[threadIdx.x >> 5] = m;
+    __syncthreads();
+    m = (int)(threadIdx.x & 31) < warps ? place[threadIdx.x & 31] : 0.0f;
+#pragma unroll
+    for (int d = 16; d; d >>= 1)
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    return m;
+}
+
 // grid: (blocks of neighbouring rows, 1 + adapters' rows); block: a multiple of 32
 // threads, 16 inputs each.  ONE: a row fits one round of the block and stays in
 // registers, `left` too while the expert stays the same, and the next row is on its way.
@@ -77,6 +92,7 @@ __global__ void prep_kernel(const PrepLaunch a) {
     const bool in0 = tid * 16 < a.n;
     uint4 raw[2];
     float lf[16];
+    float left_max = 0.0f;
     int e_left = -1, turn = 0;
     if (ONE && VEC && in0 && t_lo < t_hi)
         load16_raw(x + t_lo * a.stride, raw);
@@ -85,13 +101,17 @@ __global__ void prep_kernel(const PrepLaunch a) {
         if (a.offsets)
             e = expert_of(off, a.E, t);
         float v[16];
+        float m = 0.0f;
         if (ONE) {
             if (VEC) {
+                if (in0)
+                    m = max16_raw<TX>(raw);
                 unpack16<TX>(raw, v);
                 if (in0 && t + 1 < t_hi)
                     load16_raw(x + (t + 1) * a.stride, raw);
             } else if (in0) {
                 load16<TX, false>(x + t * a.stride, v);
+                m = max16(v, m);
             }
         }
         if (e < 0) {                       // no expert: no product, the result row is 0
@@ -101,19 +121,24 @@ __global__ void prep_kernel(const PrepLaunch a) {
             continue;
         }
         const float *left = a.left + (size_t)e * a.n;
-        float m = 0.0f;
         if (ONE) {
-            if (e != e_left && in0) {
-#pragma unroll
-                for (int i = 0; i < 16; i++)
-                    lf[i] = 1.0f;
-                mul16(left + tid * 16, lf);
+            if (e != e_left) {
+                // this thread's factors, and the largest of the row's
                 e_left = e;
+                float f = 0.0f;
+                if (in0) {
+#pragma unroll
+                    for (int i = 0; i < 16; i++)
+                        lf[i] = 1.0f;
+                    mul16(left + tid * 16, lf);
+                    f = max16(lf, f);
+                }
+                left_max = block_max(f, wmax[turn], warps);
+                turn ^= 1;
             }
 #pragma unroll
-            for (int i = 0; i < 16; i++)
-                v[i] = in0 ? __fmul_rn(v[i], lf[i]) : 0.0f;
-            m = max16(v, m);
+            for (int i = 0; i < 16; i += 2)
+                mul2(v[i], v[i + 1], lf[i], lf[i + 1]);
         } else {
             for (int k = 0; k + tid * 16 < a.n; k += blockDim.x * 16) {
                 load16<TX, VEC>(x + t * a.stride + k, v);
@@ -121,19 +146,11 @@ __global__ void prep_kernel(const PrepLaunch a) {
                 m = max16(v, m);
             }
         }
-#pragma unroll
-        for (int d = 16; d; d >>= 1)
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
         // (two places in turn: a row's reads are done before the barrier of the next)
-        float *const w = wmax[turn];
+        m = block_max(m, wmax[turn], warps);
         turn ^= 1;
-        if ((tid & 31) == 0)
-            w[tid >> 5] = m;
-        __syncthreads();
-        m = (tid & 31) < warps ? w[tid & 31] : 0.0f;
-#pragma unroll
-        for (int d = 16; d; d >>= 1)
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        if (ONE)
+            m = __fmul_rn(m, left_max);    // a bound of the row's products
         float up, down;
         row_scale(m, up, down);
         if (tid == 0)
@@ -151,8 +168,8 @@ __global__ void prep_kernel(const PrepLaunch a) {
                     v[i] = 0.0f;
             }
 #pragma unroll
-            for (int i = 0; i < 16; i++)
-                v[i] = __fmul_rn(v[i], up);
+            for (int i = 0; i < 16; i += 2)
+                mul2(v[i], v[i + 1], up, up);
             rotate128(v, tid);
             uint32_t w8[8];
             if (a.order == 0) {

@@ -125,25 +125,6 @@ template <typename TY> __device__ __forceinline__ void fma8(float *v, float h, c
 // cover all banks.
 __device__ __forceinline__ int swz(int f, int t) { return f ^ ((f >> 3) & 1) ^ ((f >> 3) & 2) ^ ((t & 1) << 2); }
 
-__device__ __forceinline__ void add2(float &a0, float &a1, float b0, float b1, float &d0, float &d1) {
-    // (a, b) -> (a + b, a - b) of two neighbours at a time
-    asm("{\n\t.reg .b64 a, b, s, d;\n\t"
-        "mov.b64 a, {%0, %1};\n\t"
-        "mov.b64 b, {%4, %5};\n\t"
-        "add.rn.f32x2 s, a, b;\n\t"
-        "sub.rn.f32x2 d, a, b;\n\t"
-        "mov.b64 {%0, %1}, s;\n\t"
-        "mov.b64 {%2, %3}, d;\n\t}"
-        : "+f"(a0), "+f"(a1), "=f"(d0), "=f"(d1) : "f"(b0), "f"(b1));
-}
-// butterflies of span SPAN (>= 2) over N values
-template <int SPAN, int N> __device__ __forceinline__ void span2(float (&v)[N]) {
-#pragma unroll
-    for (int i = 0; i < N; i += 2)
-        if ((i & SPAN) == 0)
-            add2(v[i], v[i + 1], v[i + SPAN], v[i + SPAN + 1], v[i + SPAN], v[i + SPAN + 1]);
-}
-
 // first pass, in place: thread `tid` of 128 takes token tid / 4, outputs with bits 2 and 6
 // equal to tid's two: spans 1, 2, 8, 16, 32
 __device__ __forceinline__ void rotate_first(float *buf, int tid) {

@@ -7,6 +7,8 @@
 // leaves again with the row's result.
 #pragma once
 
+#include <type_traits>
+
 #include "linear.cuh"
 
 namespace exl3 {
@@ -74,6 +76,18 @@ __device__ __forceinline__ void mul16(const float *s, float (&v)[16]) {
     }
 }
 
+// largest magnitude of 16 raw elements (a NaN is passed over)
+template <typename TX> __device__ __forceinline__ float max16_raw(const uint4 (&r)[2]) {
+    using T2 = typename std::conditional<std::is_same<TX, __half>::value, __half2, __nv_bfloat162>::type;
+    const uint32_t w[8] = {r[0].x, r[0].y, r[0].z, r[0].w, r[1].x, r[1].y, r[1].z, r[1].w};
+    T2 m = __habs2(*reinterpret_cast<const T2 *>(&w[0]));
+#pragma unroll
+    for (int i = 1; i < 8; i++)
+        m = __hmax2(m, __habs2(*reinterpret_cast<const T2 *>(&w[i])));
+    const float2 f = unpack2<TX>(*reinterpret_cast<const uint32_t *>(&m));
+    return fmaxf(f.x, f.y);
+}
+
 __device__ __forceinline__ float max16(const float (&v)[16], float m) {
 #pragma unroll
     for (int i = 0; i < 16; i++)
@@ -91,23 +105,62 @@ __device__ __forceinline__ void row_scale(float m, float &up, float &down) {
     down = __uint_as_float((uint32_t)(127 + ex - 7) << 23);
 }
 
+// ---- binary32 in pairs: each half rounds as the single operation would ----------------
+__device__ __forceinline__ void add2(float &a0, float &a1, float b0, float b1, float &d0, float &d1) {
+    // (a, b) -> (a + b, a - b) of two neighbours at a time
+    asm("{\n\t.reg .b64 a, b, s, d;\n\t"
+        "mov.b64 a, {%0, %1};\n\t"
+        "mov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 s, a, b;\n\t"
+        "sub.rn.f32x2 d, a, b;\n\t"
+        "mov.b64 {%0, %1}, s;\n\t"
+        "mov.b64 {%2, %3}, d;\n\t}"
+        : "+f"(a0), "+f"(a1), "=f"(d0), "=f"(d1) : "f"(b0), "f"(b1));
+}
+// butterflies of span SPAN (>= 2) over N values
+template <int SPAN, int N> __device__ __forceinline__ void span2(float (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2)
+        if ((i & SPAN) == 0)
+            add2(v[i], v[i + 1], v[i + SPAN], v[i + SPAN + 1], v[i + SPAN], v[i + SPAN + 1]);
+}
+
+__device__ __forceinline__ void mul2(float &a0, float &a1, float b0, float b1) {
+    asm("{\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%0, %1};\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "mul.rn.f32x2 a, a, b;\n\t"
+        "mov.b64 {%0, %1}, a;\n\t}"
+        : "+f"(a0), "+f"(a1) : "f"(b0), "f"(b1));
+}
+// a <- s a + b
+__device__ __forceinline__ void fma2(float &a0, float &a1, float s, float b0, float b1) {
+    asm("{\n\t.reg .b64 a, b, s;\n\t"
+        "mov.b64 a, {%0, %1};\n\t"
+        "mov.b64 b, {%3, %4};\n\t"
+        "mov.b64 s, {%2, %2};\n\t"
+        "fma.rn.f32x2 a, s, a, b;\n\t"
+        "mov.b64 {%0, %1}, a;\n\t}"
+        : "+f"(a0), "+f"(a1) : "f"(s), "f"(b0), "f"(b1));
+}
+
 // v: elements 16 s + i of a block of 128, s = lane % 8; v <- v H
 __device__ __forceinline__ void rotate128(float (&v)[16], int lane) {
 #pragma unroll
-    for (int h = 1; h < 16; h <<= 1)
-#pragma unroll
-        for (int i = 0; i < 16; i++)
-            if ((i & h) == 0) {
-                const float p = v[i], q = v[i + h];
-                v[i] = __fadd_rn(p, q);
-                v[i + h] = __fsub_rn(p, q);
-            }
+    for (int i = 0; i < 16; i += 2) {
+        const float p = v[i], q = v[i + 1];
+        v[i] = __fadd_rn(p, q);
+        v[i + 1] = __fsub_rn(p, q);
+    }
+    span2<2>(v);
+    span2<4>(v);
+    span2<8>(v);
 #pragma unroll
     for (int h = 1; h < 8; h <<= 1) {
         const float sg = (lane & h) ? -1.0f : 1.0f;
 #pragma unroll
-        for (int i = 0; i < 16; i++)
-            v[i] = __fmaf_rn(sg, v[i], __shfl_xor_sync(0xffffffffu, v[i], h));
+        for (int i = 0; i < 16; i += 2)
+            fma2(v[i], v[i + 1], sg, __shfl_xor_sync(0xffffffffu, v[i], h), __shfl_xor_sync(0xffffffffu, v[i + 1], h));
     }
 }
 
