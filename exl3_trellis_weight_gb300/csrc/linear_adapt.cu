@@ -8,9 +8,11 @@
 // and bound by reading the activations once: m16n8k16 instructions from shared
 // memory, fed by asynchronous copies of gathered rows, are far from the limit.
 //
-// h = gain A x is kept in binary32.  Where it becomes an operand again it is
-// rounded once to the activations' type; binary16 gets a power of two for each
-// tile (expand) or adapter (outer) first, so that its range does not matter.
+// h = gain A x is kept in binary32.  Where it becomes an operand again it is split
+// into two of the activations' type, the second the rounding error of the first, and
+// both are multiplied (one alone cost half as much again in the results' error);
+// binary16 gets a power of two for each tile (expand) or adapter (outer) first, so
+// that its range does not matter.
 #include "linear.cuh"
 #include "tc.cuh"
 
@@ -84,6 +86,13 @@ template <typename TX> __device__ __forceinline__ void operand_scale(float m, fl
         up = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
         down = __uint_as_float((uint32_t)(127 - 7 + e) << 23);
     }
+}
+
+// v as the sum of two values of the type, `apart` elements apart
+template <typename TX> __device__ __forceinline__ void split(float v, TX *to, int apart) {
+    const TX high = from_f32<TX>(v);
+    to[0] = high;
+    to[apart] = from_f32<TX>(__fsub_rn(v, to_f32(high)));
 }
 
 // ---- plan --------------------------------------------------------------------
@@ -309,9 +318,10 @@ template <typename TX> __global__ void __launch_bounds__(256) expand_kernel(cons
     const int r = rank_of(a.ranks, i, a.rank), R16 = (a.rank + 15) / 16 * 16, kb = (r + 15) / 16;
     constexpr int kF = 128 + kPad;
     const int hrow = R16 + kPad;
-    TX *const sh = reinterpret_cast<TX *>(smem);                                 // [32][R16]
-    const uint32_t sB = saddr(smem) + (uint32_t)(kTile * hrow) * 2, bbytes = (uint32_t)(R16 * kF) * 2;   // two [R16][128]
-    TX *const so = reinterpret_cast<TX *>(smem + kTile * hrow * 2 + 2 * bbytes); // [32][128]
+    TX *const sh = reinterpret_cast<TX *>(smem);                                 // h, twice [32][R16]
+    const uint32_t hlow = (uint32_t)(kTile * hrow) * 2;                          // bytes to the second
+    const uint32_t sB = saddr(smem) + 2 * hlow, bbytes = (uint32_t)(R16 * kF) * 2;   // two [R16][128]
+    TX *const so = reinterpret_cast<TX *>(smem + 2 * hlow + 2 * bbytes);         // [32][128]
     const uint16_t *M = reinterpret_cast<const uint16_t *>(sd.M) + (size_t)i * a.rank * sd.n;
     const int f_lo = blockIdx.y * 512, f_hi = min(f_lo + 512, sd.n);
     auto load = [&](int f0, int buf) {
@@ -350,7 +360,7 @@ template <typename TX> __global__ void __launch_bounds__(256) expand_kernel(cons
 #pragma unroll
     for (int q = 0; q < 16; q++)
         if (q < 2 * kb)
-            sh[(tid >> 3) * hrow + (tid & 7) + 8 * q] = from_f32<TX>(__fmul_rn(hv[q], up));
+            split<TX>(__fmul_rn(hv[q], up), sh + (tid >> 3) * hrow + (tid & 7) + 8 * q, kTile * hrow);
     const uint32_t ha = saddr(smem) + (uint32_t)(((warp & 1) * 16 + g) * hrow + 2 * j) * 2;
     for (int f0 = f_lo, buf = 0; f0 < f_hi; f0 += 128, buf ^= 1) {
         load(f0 + 128, buf ^ 1);
@@ -365,12 +375,16 @@ template <typename TX> __global__ void __launch_bounds__(256) expand_kernel(cons
         for (int k = 0; k < kb; k++) {
             const uint32_t at = ha + k * 32;
             const uint32_t f[4] = {lds32(at), lds32(at + 16 * hrow), lds32(at + 16), lds32(at + 16 * hrow + 16)};
+            const uint32_t at2 = at + hlow;
+            const uint32_t f2[4] = {lds32(at2), lds32(at2 + 16 * hrow), lds32(at2 + 16), lds32(at2 + 16 * hrow + 16)};
 #pragma unroll
             for (int b = 0; b < 2; b++) {
                 uint32_t t[4];
                 load_t(sB + buf * bbytes + (uint32_t)((k * 16 + (lane & 15)) * kF + (warp >> 1) * 32 + b * 16 + (lane >> 4) * 8) * 2, t);
                 mma<TX>(acc[2 * b], f, t[0], t[1]);
                 mma<TX>(acc[2 * b + 1], f, t[2], t[3]);
+                mma<TX>(acc[2 * b], f2, t[0], t[1]);
+                mma<TX>(acc[2 * b + 1], f2, t[2], t[3]);
             }
         }
 #pragma unroll
@@ -415,7 +429,7 @@ template <typename TX, bool VEC> __global__ void __launch_bounds__(256) outer_ke
     const int r = rank_of(a.ranks, i, a.rank), R16 = (a.rank + 15) / 16 * 16, mb = (r + 15) / 16;
     const int lo = a.plan.seg[i], n = a.plan.seg[i + 1] - lo;
     const int hrow = R16 + kPad;
-    const uint32_t base = saddr(smem), xbytes = kTile * kXRow * 2, hbytes = (uint32_t)(kTile * hrow) * 2;
+    const uint32_t base = saddr(smem), xbytes = kTile * kXRow * 2, hlow = (uint32_t)(kTile * hrow) * 2, hbytes = 2 * hlow;
     const uint32_t hbase = base + kOuterStages * xbytes;
     float up, down;
     operand_scale<TX>(__uint_as_float(sd.largest[i]), up, down);
@@ -477,7 +491,7 @@ template <typename TX, bool VEC> __global__ void __launch_bounds__(256) outer_ke
 #pragma unroll
         for (int q = 0; q < 16; q++)
             if (q < 2 * mb)
-                sh[ht * hrow + hq + 8 * q] = from_f32<TX>(__fmul_rn(hv[q], up));
+                split<TX>(__fmul_rn(hv[q], up), sh + ht * hrow + hq + 8 * q, kTile * hrow);
         copy_wait<kOuterStages - 2>();
         __syncthreads();
         load(s + kOuterStages - 1);
@@ -491,7 +505,11 @@ template <typename TX, bool VEC> __global__ void __launch_bounds__(256) outer_ke
             for (int m = 0; m < 8; m++)
                 if (m < mb) {
                     uint32_t f[4];         // blocks (tokens 0-7 | 8-15) x (rows 0-7 | 8-15): rows first
-                    load_t(hs + (uint32_t)((k * 16 + (lane & 7) + (lane >> 4) * 8) * hrow + m * 16 + ((lane >> 3) & 1) * 8) * 2, f);
+                    const uint32_t at = hs + (uint32_t)((k * 16 + (lane & 7) + (lane >> 4) * 8) * hrow + m * 16 + ((lane >> 3) & 1) * 8) * 2;
+                    load_t(at, f);
+                    mma<TX>(acc[m][0], f, b[0], b[1]);
+                    mma<TX>(acc[m][1], f, b[2], b[3]);
+                    load_t(at + hlow, f);
                     mma<TX>(acc[m][0], f, b[0], b[1]);
                     mma<TX>(acc[m][1], f, b[2], b[3]);
                 }
@@ -611,7 +629,7 @@ exl3_status launch_shrink(const AdaptLaunch &p0, int sides, cudaStream_t s) {
 exl3_status launch_expand(const AdaptLaunch &p, void *y, int64_t y_stride, cudaStream_t s) {
     const int64_t tiles = p.T / kTile + (p.n < p.T ? p.n : p.T);
     const int R16 = (p.rank + 15) / 16 * 16;
-    const size_t smem = (size_t)kTile * (R16 + kPad) * 2 + (size_t)2 * R16 * (128 + kPad) * 2 + (size_t)kTile * (128 + kPad) * 2;
+    const size_t smem = (size_t)2 * kTile * (R16 + kPad) * 2 + (size_t)2 * R16 * (128 + kPad) * 2 + (size_t)kTile * (128 + kPad) * 2;
     const dim3 grid((unsigned)tiles, (unsigned)((p.side[0].n + 511) / 512));
     if (p.dt == EXL3_BF16)
         return launch("adapter expand launch", expand_kernel<__nv_bfloat16>, grid, 256, smem, 1, true, s, p, y, y_stride);
@@ -625,7 +643,7 @@ exl3_status launch_outer(const AdaptLaunch &p0, cudaStream_t s) {
     while (p.split < 8 && blocks * p.split * 2 <= 2 * sms && p.T >= (int64_t)p.split * 2 * kTile * p.n)
         p.split *= 2;
     const int R16 = (p.rank + 15) / 16 * 16;
-    const size_t stages = (size_t)kOuterStages * kTile * kXRow * 2 + (size_t)2 * kTile * (R16 + kPad) * 2;
+    const size_t stages = (size_t)kOuterStages * kTile * kXRow * 2 + (size_t)4 * kTile * (R16 + kPad) * 2;
     const size_t part = (size_t)R16 * 132 * 4, smem = stages > part ? stages : part;
     const dim3 grid((unsigned)((p.side[0].n + p.side[1].n) / 128 * p.split), (unsigned)p.n);
     const bool vec = wide_rows(p.side[0]) && wide_rows(p.side[1]);

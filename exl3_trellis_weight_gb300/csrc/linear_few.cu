@@ -31,7 +31,7 @@ using namespace tc;
 
 constexpr int kSlices = 2;
 constexpr int kWarps = 8 * kSlices, kThreadsF = kWarps * 32;
-constexpr int kTok = 64;                   // tokens of a block, at most
+constexpr int kTok = 32;                   // tokens of a block, at most
 constexpr int kTilesAhead = 16;            // tiles in a warp's ring
 
 __device__ unsigned int g_few_timeouts;
@@ -39,7 +39,7 @@ __device__ unsigned int g_few_timeouts;
 struct FewArgs {
     ProductLaunch p;
     int n_in, n_out;
-    int tile_n;          // tokens of a block: 8, 16, 32 or 64
+    int tile_n;          // tokens of a block: 8, 16 or 32
     int split;           // blocks of a cluster
     uint32_t ring_off;   // shared memory: activations, in their place the sums later, then the rings
 };
@@ -353,8 +353,7 @@ template <int K, bool TR, typename TY> exl3_status launch_few_n(const FewArgs &a
     switch (a.tile_n) {
     case 8: return launch_few_form<K, TR, 1, TY>(a, grid, smem, s);
     case 16: return launch_few_form<K, TR, 2, TY>(a, grid, smem, s);
-    case 32: return launch_few_form<K, TR, 4, TY>(a, grid, smem, s);
-    default: return launch_few_form<K, TR, 8, TY>(a, grid, smem, s);
+    default: return launch_few_form<K, TR, 4, TY>(a, grid, smem, s);
     }
 }
 template <int K, typename TY> exl3_status launch_few_t(const FewArgs &a, unsigned grid, uint32_t smem, cudaStream_t s) {
@@ -388,7 +387,7 @@ bool plan_few(const ProductLaunch &p, FewArgs &a, unsigned &grid, uint32_t &smem
     // all tokens; experts' sizes are not known here (their tiles start at a multiple
     // of 8 and may carry up to 7 columns of others)
     const int64_t want = p.offsets ? (p.T <= 1 ? 8 : p.T <= 9 ? 16 : 32) : p.T;
-    a.tile_n = want <= 8 ? 8 : want <= 16 ? 16 : want <= 32 ? 32 : 64;
+    a.tile_n = want <= 8 ? 8 : want <= 16 ? 16 : 32;
     const int64_t used = p.T < p.E ? p.T : p.E;
     const int64_t tok = p.offsets ? used + (p.T + 7 * used) / a.tile_n + 1 : (p.T + a.tile_n - 1) / a.tile_n;
     const int64_t tiles = tok * (a.n_out / 128);

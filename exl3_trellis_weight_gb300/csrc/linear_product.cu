@@ -492,26 +492,43 @@ __global__ void __launch_bounds__(kThreadsP, 1) product_kernel(const __grid_cons
         cluster_sync();
         if (it0 < n_tiles && warp < kDecWarps + kOutWarps) {
             const Tile tl = make_tile<PAIR>(a, &plan, it0, rank);
-            // a warp takes four tokens at a time
+            // a warp takes four tokens at a time, with adapters one (its four groups of eight
+            // lanes a quarter of the adapter's rows each)
+            const bool shared = a.p.B && a.p.h;
+            const int each = shared ? 1 : 4, sub = shared ? 0 : lane >> 3, u = lane & 7;
             const int mine = (tl.n + a.split - 1 - rank) / a.split;          // tokens rank, rank + split, ...
-            for (int i = warp * 4; i < mine; i += (kDecWarps + kOutWarps) * 4) {
-                const int row = rank + (i + (lane >> 3)) * a.split;
+            for (int i = warp * each; i < mine; i += (kDecWarps + kOutWarps) * each) {
+                const int row = rank + (i + sub) * a.split;
                 const bool in = row < tl.n;
                 const int64_t t = in ? tl.t0 + row : tl.hi;
                 const float rs = t < tl.hi ? a.p.rscale[t] : 0.0f;
-                float x[16];
+                float v[16], x[16];
 #pragma unroll
                 for (int j = 0; j < 16; j++)
-                    x[j] = 0.0f;
+                    v[j] = x[j] = 0.0f;
+                if (shared && t >= tl.lo && t < tl.hi) {
+                    add_adapter<TY>(a.p, a.n_out, tl.f0, t, v, u, lane >> 3, 4);
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 16; j++) {
+                        v[j] = __fadd_rn(v[j], __shfl_xor_sync(0xffffffffu, v[j], 8));
+                        v[j] = __fadd_rn(v[j], __shfl_xor_sync(0xffffffffu, v[j], 16));
+                    }
+                }
                 if (in)
 #pragma unroll 2
                     for (int b = 0; b < a.split; b++)
-                        add_sums(x, at_block(base + (uint32_t)row * 512u, b), lane & 7);
+                        add_sums(x, at_block(base + (uint32_t)row * 512u, b), u);
                 scale_out(x, rs, right, lane);
-                if (t >= tl.lo && t < tl.hi) {
-                    if (a.p.B)
-                        add_adapter<TY>(a.p, a.n_out, tl.f0, t, x, lane & 7, 0, 1);
-                    store_out<TY>(a.p, tl.f0, t, x, lane & 7);
+                if (t >= tl.lo && t < tl.hi && (!shared || lane < 8)) {
+                    if (shared) {
+#pragma unroll
+                        for (int j = 0; j < 16; j++)
+                            x[j] = __fadd_rn(x[j], v[j]);
+                    } else if (a.p.B) {
+                        add_adapter<TY>(a.p, a.n_out, tl.f0, t, x, u, 0, 1);
+                    }
+                    store_out<TY>(a.p, tl.f0, t, x, u);
                 }
             }
         }

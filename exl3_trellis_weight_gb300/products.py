@@ -13,6 +13,11 @@ _DT = {torch.bfloat16: EXL3_BF16, torch.float16: EXL3_F16}
 _fn = None
 
 
+# the current stream's handle, without a Stream object around it (a microsecond)
+_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _lib():
     global _fn
     if _fn is None:
@@ -39,26 +44,29 @@ def expert_linear_workspace_bytes(T: int, rows: int, cols: int, transposed: bool
     return int(_lib().exl3_expert_linear_workspace_bytes(T, rows, cols, int(transposed)))
 
 
-def _activations(t, name, columns, device=None, like=None):
+def _activations(t, name, columns, like=None):
     """Row stride of a [T, columns] tensor, in elements."""
+    shape = t.shape
     if not t.is_cuda:
         raise ValueError("all tensors must be CUDA tensors (no CPU fallback)")
-    if t.dim() != 2 or t.shape[1] != columns:
-        raise ValueError(f"{name} must be [tokens, {columns}], got {tuple(t.shape)}")
+    if len(shape) != 2 or shape[1] != columns:
+        raise ValueError(f"{name} must be [tokens, {columns}], got {tuple(shape)}")
     if t.dtype not in _DT:
         raise ValueError(f"unsupported dtype {t.dtype} of {name} (bfloat16 or float16)")
-    if like is not None and (t.dtype != like.dtype or t.shape[0] != like.shape[0] or t.device != like.device):
+    if like is not None and (t.dtype != like.dtype or shape[0] != like.shape[0] or t.device != like.device):
         raise ValueError(f"{name} must have the dtype, tokens and device of the activations")
-    if t.shape[0] > 1 and t.stride(1) != 1:
+    row, column = t.stride()
+    if column != 1 and shape[0]:
         raise ValueError(f"{name}'s columns must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else columns
+    return row if shape[0] > 1 else columns
 
 
-def _dense(t, name, dtype, shape, device):
-    if t.dtype != dtype or t.shape != shape:
+def _dense(t, name, dtype, shape, index):
+    """Address of a contiguous tensor of this type and shape on CUDA device `index`."""
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device} (no CPU fallback)")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on CUDA device {index} (no CPU fallback)")
     if not t.is_contiguous():
         raise ValueError("tensors must be contiguous")
     return t.data_ptr()
@@ -66,19 +74,19 @@ def _dense(t, name, dtype, shape, device):
 
 def _coded(codes, su, sv, K, scale, lead, device):
     """Pointers of a coded matrix (or a stack of them) and its two sizes."""
-    if codes.dim() != len(lead) + 3:
-        raise ValueError(f"codes must have {len(lead) + 3} dimensions, got {tuple(codes.shape)}")
-    rows, cols = codes.shape[-3] * 16, codes.shape[-2] * 16
-    dt = codes.dtype
-    if dt is not torch.int16:
-        raise ValueError(f"codes must be int16, got {dt}")
-    c = _dense(codes, "codes", dt, (*lead, rows // 16, cols // 16, 16 * K), device)
+    shape, index = codes.shape, device.index if device.type == "cuda" else -1
+    if len(shape) != len(lead) + 3:
+        raise ValueError(f"codes must have {len(lead) + 3} dimensions, got {tuple(shape)}")
+    if codes.dtype is not torch.int16:
+        raise ValueError(f"codes must be int16, got {codes.dtype}")
+    rows, cols = shape[-3] * 16, shape[-2] * 16
+    c = _dense(codes, "codes", torch.int16, (*lead, shape[-3], shape[-2], 16 * K), index)
     if not isinstance(scale, torch.Tensor):
         scale = torch.full(lead, float(scale), dtype=torch.float32, device=device)
-    u = _dense(su, "su", torch.float32, (*lead, rows), device)
-    v = _dense(sv, "sv", torch.float32, (*lead, cols), device)
+    u = _dense(su, "su", torch.float32, (*lead, rows), index)
+    v = _dense(sv, "sv", torch.float32, (*lead, cols), index)
     # the scale's tensor is returned too: one made here must live until the launch
-    return rows, cols, c, u, v, _dense(scale, "scale", torch.float32, lead, device), scale
+    return rows, cols, c, u, v, _dense(scale, "scale", torch.float32, lead, index), scale
 
 
 _NO_ADAPTERS = (None, None, None, None, None, 0, 0)
@@ -91,9 +99,11 @@ def _adapters(A, B, gain, slots, ranks, n_in, n_out, x):
         return _NO_ADAPTERS
     if B is None or gain is None or slots is None:
         raise ValueError("A needs B, gain and slots")
-    dev = x.device
-    n, r = A.shape[0], A.shape[1]
-    return (_dense(A, "A", x.dtype, (n, r, n_in), dev), _dense(B, "B", x.dtype, (n, r, n_out), dev),
+    if A.dim() != 3:
+        raise ValueError(f"A must be [adapters, rank, {n_in}], got {tuple(A.shape)}")
+    dev, dt = x.get_device(), x.dtype
+    n, r, _ = A.shape
+    return (_dense(A, "A", dt, (n, r, n_in), dev), _dense(B, "B", dt, (n, r, n_out), dev),
             _dense(gain, "gain", torch.float32, (n,), dev),
             _dense(slots, "slots", torch.int32, (x.shape[0],), dev),
             None if ranks is None else _dense(ranks, "ranks", torch.int32, (n,), dev), n, r)
@@ -133,7 +143,7 @@ def linear(x, codes, su, sv, K: int, scale, transposed: bool = False, A=None, B=
     ws = _ws(L.exl3_linear_workspace_bytes(T, rows, cols, tr, n, r), dev, ws)
     st = L.exl3_linear(x.data_ptr(), _DT[x.dtype], T, xs, pc, rows, cols, K, pu, pv, ps, tr, pA, pB, pg, pslots,
                        pranks, n, r, out.data_ptr(), ys, ws.data_ptr(), ws.numel() * ws.element_size(),
-                       torch.cuda.current_stream(dev).cuda_stream)
+                       _stream(dev.index))
     if st:
         _fail(st)
     return out
@@ -169,7 +179,7 @@ def linear_backward(dy, x, codes, su, sv, K: int, scale, transposed: bool = Fals
     st = L.exl3_linear_backward(dy.data_ptr(), dys, px, xs, _DT[dy.dtype], T, pc, rows, cols, K, pu, pv, ps, tr, pA,
                                 pB, pg, pslots, pranks, n, r, dx.data_ptr(), dxs, dA.data_ptr() if n else None,
                                 dB.data_ptr() if n else None, ws.data_ptr(), ws.numel() * ws.element_size(),
-                                torch.cuda.current_stream(dev).cuda_stream)
+                                _stream(dev.index))
     if st:
         _fail(st)
     return dict(dx=dx, dA=dA, dB=dB)
@@ -189,7 +199,7 @@ def expert_linear(x, offsets, codes, su, sv, K: int, scale, transposed: bool = F
     n_in, n_out = (cols, rows) if transposed else (rows, cols)
     xs = _activations(x, "x", n_in)
     T = x.shape[0]
-    po = _dense(offsets, "offsets", torch.int32, (E + 1,), dev)
+    po = _dense(offsets, "offsets", torch.int32, (E + 1,), x.get_device())
     if out is None:
         out = torch.empty(T, n_out, dtype=x.dtype, device=dev)
         ys = n_out
@@ -200,7 +210,7 @@ def expert_linear(x, offsets, codes, su, sv, K: int, scale, transposed: bool = F
     ws = _ws(L.exl3_expert_linear_workspace_bytes(T, rows, cols, tr), dev, ws)
     st = L.exl3_expert_linear(x.data_ptr(), _DT[x.dtype], T, xs, po, E, pc, rows, cols, K, pu, pv, ps, tr,
                               out.data_ptr(), ys, ws.data_ptr(), ws.numel() * ws.element_size(),
-                              torch.cuda.current_stream(dev).cuda_stream)
+                              _stream(dev.index))
     if st:
         _fail(st)
     return out

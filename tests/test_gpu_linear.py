@@ -187,6 +187,36 @@ def test_linear_strided_and_unaligned_rows(ex):
             assert (whole[:, :off] == 7.0).all() and (whole[:, off + 384:] == 7.0).all()
 
 
+def test_python_refusals(ex):
+    g = gen(8)
+    codes, su, sv, scale = coded(g, 256, 128, 2)
+    x = acts(g, 3, 256, "bf16")
+    A, B, gain, ranks = adapters(g, 2, 4, 256, 128, "bf16")
+    slots = torch.zeros(3, dtype=torch.int32, device=DEV)
+    ok = dict(A=A, B=B, gain=gain, slots=slots, ranks=ranks)
+    ex.linear(x, codes, su, sv, 2, scale, **ok)
+    for bad in (dict(x=x.float()), dict(x=x[:, :128]), dict(x=x.t().contiguous().t()), dict(x=x[:1].t().repeat(1, 2)[:, :1].t()),
+                dict(x=x.cpu()), dict(su=su.cpu()), dict(sv=sv.double()), dict(scale=scale.double()),
+                dict(A=A.half()), dict(A=A[0]), dict(B=B[:, :2]), dict(B=None), dict(gain=gain[:1]), dict(slots=slots.long()),
+                dict(slots=slots[:2]), dict(ranks=ranks.float()), dict(A=None), dict(out=torch.empty(3, 128, device=DEV)),
+                dict(out=torch.empty(2, 128, dtype=torch.bfloat16, device=DEV))):
+        kw = dict(x=x, codes=codes, su=su, sv=sv, K=2, scale=scale, **ok)
+        kw.update(bad)
+        with pytest.raises(ValueError):
+            ex.linear(**kw)
+    with pytest.raises(ex.Exl3Error) as e:
+        ex.linear(x, codes, su, sv, 2, scale, ws=torch.empty(256, dtype=torch.uint8, device=DEV))
+    assert e.value.status == 3
+    with pytest.raises(ex.Exl3Error) as e:
+        buf = torch.zeros(3, 256, dtype=torch.bfloat16, device=DEV)
+        ex.linear(buf, codes, su, sv, 2, scale, out=buf[:, :128])
+    assert e.value.status == 1
+    with pytest.raises(ValueError):
+        ex.linear_backward(acts(g, 3, 128, "bf16"), None, codes, su, sv, 2, scale, **ok)
+    with pytest.raises(ValueError):
+        ex.expert_linear(x, torch.zeros(3, dtype=torch.int32, device=DEV), codes[None], su[None], sv[None], 2, scale[None])
+
+
 def test_linear_row_ranges_and_special_values(ex):
     """Rows of zeros, of very large and very small values; rows that are not numbers stay alone."""
     g = gen(10)

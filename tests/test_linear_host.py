@@ -110,6 +110,8 @@ def test_python_checks_need_no_gpu(ex):
     su, sv, s = torch.zeros(256), torch.zeros(128), torch.ones(())
     with pytest.raises(ValueError, match="CUDA"):
         ex.linear(x, codes, su, sv, 2, s)
+    with pytest.raises(ValueError, match="codes must be"):
+        ex.linear(x, codes, su, sv, 4, s)
     with pytest.raises(ValueError, match="dimensions"):
         ex.linear(x, codes[0], su, sv, 2, s)
     with pytest.raises(ValueError, match="int16"):
