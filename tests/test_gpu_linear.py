@@ -462,3 +462,13 @@ def test_capture_in_a_graph(ex):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(kw["out"], want)
+
+
+def test_the_example_runs():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "coded_layer.py")
+    spec = importlib.util.spec_from_file_location("coded_layer", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    mod.main()
