@@ -10,10 +10,10 @@
 //          along the outputs (x W^) or along the sum (x W^^T): the first is
 //          stored as an operand whose rows run along M, the second along K, and
 //          only the descriptor differs;
-//   16-19  results: accumulator -> shared memory (one token per row) -> H over
+//   16-23  results: accumulator -> shared memory (one token per row) -> H over
 //          the 128 outputs in two passes -> scales, adapters, one rounding;
-//   20     bulk copies of the rotated activations, one contiguous block a step;
-//   21     issues the matrix instructions (binary16 in, binary32 out).
+//   24     bulk copies of the rotated activations, one contiguous block a step;
+//   25     issues the matrix instructions (binary16 in, binary32 out).
 //
 // Two forms.  Alone, a block multiplies by up to 256 tokens and two
 // accumulators let the results of one tile overlap the sums of the next.  In
@@ -38,18 +38,20 @@ namespace {
 
 using namespace tc;
 
-constexpr int kGroups = 2, kDecWarps = 8 * kGroups, kOutWarps = 4;
+constexpr int kGroups = 2, kDecWarps = 8 * kGroups, kOutWarps = 8;
 constexpr int kWarpB = kDecWarps + kOutWarps, kWarpMma = kWarpB + 1;
 constexpr int kThreadsP = (kWarpB + 2) * 32;
 constexpr int kN = 256;                    // columns of an accumulator
 constexpr int kStep = 64;                  // inputs of a step
 constexpr int kAStages = 4, kBStages = 16; // operand stages (of B at most)
-constexpr uint32_t kABytes = 128 * kStep * 2, kBArea = 96 * 1024, kCArea = 32 * 1024;
+constexpr uint32_t kABytes = 128 * kStep * 2, kBArea = 96 * 1024, kCArea = 16 * 1024;
 constexpr uint32_t kBOff = kAStages * kABytes;              // B stages behind the A stages,
 constexpr uint32_t kCOff = kBOff + kBArea;                  // then a ring of codes for each decode warp,
-constexpr uint32_t kOutOff = kCOff + kCArea;                // then 32 tokens x 128 outputs, fp32
-constexpr uint32_t kAddOff = kOutOff + 32 * 128 * 4;        // then 64 bytes for each thread of the result warps
-constexpr uint32_t kSmem = kAddOff + 128 * 64 + 1024;       // + alignment slack
+constexpr uint32_t kOutOff = kCOff + kCArea;                // then 32 tokens x 128 outputs, fp32, for four result warps each,
+constexpr uint32_t kAddOff = kOutOff + 2 * 32 * 128 * 4;    // then 64 bytes for each of their threads,
+constexpr uint32_t kPlanOff = kAddOff;                      // or the experts' tiles (which have no adapters)
+constexpr uint32_t kSmem = kAddOff + 256 * 64 + 1024;       // + alignment slack
+static_assert(sizeof(Plan) <= 256 * 64, "the plan fits where the adapters' terms would be");
 
 __device__ unsigned int g_product_timeouts;
 
@@ -142,12 +144,12 @@ template <int K, bool PAIR, typename TY>
 __global__ void __launch_bounds__(kThreadsP, 1) product_kernel(const __grid_constant__ Args a) {
     extern __shared__ unsigned char smem_raw[];
     __shared__ __align__(8) unsigned long long bars[2 * kAStages + 2 * kBStages + 5];
-    __shared__ Plan plan;
-    __shared__ __align__(16) float right[128];
+    __shared__ __align__(16) float rights[2][128];
     __shared__ uint32_t tmem_at;
     __shared__ int gave_up;
     const uint32_t base = (saddr(smem_raw) + 1023u) & ~1023u;
     unsigned char *const sb = smem_raw + (base - saddr(smem_raw));
+    Plan &plan = *reinterpret_cast<Plan *>(sb + kPlanOff);
     const uint32_t bar_a = saddr(bars), bar_b = bar_a + 16u * kAStages;
     const uint32_t bar_d = bar_b + 16u * kBStages;
     auto full_a = [&](uint32_t s) { return bar_a + 8u * s; };
@@ -290,9 +292,11 @@ __global__ void __launch_bounds__(kThreadsP, 1) product_kernel(const __grid_cons
         }
     } else if (warp < kDecWarps + kOutWarps) {
         // ---- results ----
-        const int ow = warp - kDecWarps;
+        // two groups of four warps take turns at the chunks of 32 tokens
+        const int ow = warp & 3, og = (warp - kDecWarps) >> 2;
+        float *const right = rights[og];
         const bool keep = !PAIR && a.split > 1;             // partial sums stay in shared memory
-        float *const buf = reinterpret_cast<float *>(sb + (keep ? 0 : kOutOff));
+        float *const buf = reinterpret_cast<float *>(sb + (keep ? 0u : kOutOff + og * (32u * 128u * 4u)));
         const int f4 = 8 * ow + (lane >> 2), col = 4 * out_at(f4) + (lane & 3);
         const int col0 = 4 * swz(f4, 0) + (lane & 3), col1 = 4 * swz(f4, 1) + (lane & 3);
         asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -310,7 +314,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) product_kernel(const __grid_cons
             // what y holds of a token with an adapter (to its own place in shared memory).
             float rs[2];
             int slot[2];                   // -1: nothing in y
-            const uint32_t mine = base + kAddOff + (uint32_t)(ow * 32 + lane) * 16u;
+            const uint32_t mine = base + kAddOff + (uint32_t)og * 8192u + (uint32_t)(ow * 32 + lane) * 16u;
             auto fetch = [&](int g, int64_t t) {
                 const bool in = !keep && live && t >= tl.lo && t < tl.hi;
                 rs[g] = in ? a.p.rscale[t] : 0.0f;
@@ -324,8 +328,8 @@ __global__ void __launch_bounds__(kThreadsP, 1) product_kernel(const __grid_cons
                 copy_group();
             };
             const int64_t t_mine = tl.t0 + ow * 4 + (lane >> 3);
-            fetch(0, t_mine);
-            fetch(1, t_mine + 16);
+            fetch(0, t_mine + 32 * og);
+            fetch(1, t_mine + 32 * og + 16);
             for (int n0 = 0; ok && n0 < tl.n; n0 += kN, acc++) {
                 const int d = acc & 1;
                 ok = bar_wait(acc_full(d), (acc >> 1) & 1, &gave_up, count);
@@ -334,7 +338,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) product_kernel(const __grid_cons
                     break;
                 fence_after();
                 const int n1 = min(tl.n - n0, kN);
-                for (int c0 = 0; c0 < n1; c0 += 32) {
+                for (int c0 = 32 * og; c0 < n1; c0 += 64) {
 #pragma unroll
                     for (int g = 0; g < 2; g++) {
                         float v[16];
@@ -351,9 +355,9 @@ __global__ void __launch_bounds__(kThreadsP, 1) product_kernel(const __grid_cons
                     }
                     if (keep)
                         continue;
-                    asm volatile("bar.sync 1, 128;" ::: "memory");
+                    asm volatile("bar.sync %0, 128;" ::"r"(1 + og) : "memory");
                     rotate_first(buf, ow * 32 + lane);
-                    asm volatile("bar.sync 1, 128;" ::: "memory");
+                    asm volatile("bar.sync %0, 128;" ::"r"(1 + og) : "memory");
 #pragma unroll
                     for (int g = 0; g < 2; g++) {
                         const int64_t t = t_mine + n0 + c0 + 16 * g;
@@ -368,11 +372,11 @@ __global__ void __launch_bounds__(kThreadsP, 1) product_kernel(const __grid_cons
                         } else if (a.p.B && (a.p.h || !wide_y) && in) {
                             add_adapter<TY>(a.p, a.n_out, tl.f0, t, x, u, 0, 1);
                         }
-                        fetch(g, t + 32);
+                        fetch(g, t + 64);
                         if (in)
                             store_out<TY>(a.p, tl.f0, t, x, u);
                     }
-                    asm volatile("bar.sync 1, 128;" ::: "memory");
+                    asm volatile("bar.sync %0, 128;" ::"r"(1 + og) : "memory");
                 }
                 fence_before();
                 __syncwarp();
@@ -519,7 +523,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) product_kernel(const __grid_cons
 #pragma unroll 2
                     for (int b = 0; b < a.split; b++)
                         add_sums(x, at_block(base + (uint32_t)row * 512u, b), u);
-                scale_out(x, rs, right, lane);
+                scale_out(x, rs, rights[0], lane);
                 if (t >= tl.lo && t < tl.hi && (!shared || lane < 8)) {
                     if (shared) {
 #pragma unroll
@@ -559,7 +563,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) product_kernel(const __grid_cons
 }
 
 template <int K, bool PAIR, typename TY> exl3_status launch_form(const Args &a, unsigned grid, unsigned cluster, cudaStream_t s) {
-    static_assert(kSmem <= 227 * 1024 - 10 * 1024, "shared memory of one block");
+    static_assert(kSmem <= 227 * 1024 - 1536, "shared memory of one block");
     static SmemAllowed allowed;
     cudaError_t e = allow_smem((const void *)product_kernel<K, PAIR, TY>, kSmem, allowed);
     if (e != cudaSuccess)
