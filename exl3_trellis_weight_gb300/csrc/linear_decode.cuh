@@ -29,11 +29,13 @@ __device__ __forceinline__ uint32_t levels2(uint32_t s0, uint32_t s1) {
 }
 
 // ---- tiles of outputs and tokens ----------------------------------------------
-struct OutTile {
+// (I: the type of token numbers, of which there are at most 2^24; the few-token kernel
+// keeps 64 bits, with which the compiler spills nothing, the other one 32)
+template <typename I> struct OutTile {
     int e;            // expert
     int f0;           // first output
-    int64_t t0;       // first token column, a multiple of 8 (columns before lo are not stored)
-    int64_t lo, hi;   // tokens of the expert inside the tile
+    I t0;             // first token column, a multiple of 8 (columns before lo are not stored)
+    I lo, hi;         // tokens of the expert inside the tile
 };
 
 // Shared list of token tiles: expert e has first[e + 1] - first[e] of them
@@ -76,11 +78,12 @@ __device__ __forceinline__ void make_plan(Plan &plan, const int32_t *offsets, in
 
 // tile `it` of nf x (token tiles): outputs fastest, so that blocks running side by
 // side share their tokens.  f0 counts in units of `width` outputs.
-__device__ __forceinline__ OutTile out_tile(const Plan *plan, int E, int64_t T, int tile_n, int nf, int width, int64_t it) {
-    OutTile t;
+template <typename I>
+__device__ __forceinline__ OutTile<I> out_tile(const Plan *plan, int E, I T, int tile_n, int nf, int width, int64_t it) {
+    OutTile<I> t;
     int j = (int)(it / nf);
     t.f0 = (int)(it % nf) * width;
-    int64_t lo = 0, hi = T;
+    I lo = 0, hi = T;
     t.e = 0;
     if (plan) {
         int l = 0, h = E - 1;            // last e with first[e] <= j
@@ -94,9 +97,9 @@ __device__ __forceinline__ OutTile out_tile(const Plan *plan, int E, int64_t T, 
         t.e = l;
         j -= plan->first[l];
         lo = plan->off[l];
-        hi = max(lo, (int64_t)plan->off[l + 1]);
+        hi = max(lo, (I)plan->off[l + 1]);
     }
-    t.t0 = (lo & ~7ll) + (int64_t)j * tile_n;
+    t.t0 = (lo & ~(I)7) + (I)j * tile_n;
     t.lo = lo > t.t0 ? lo : t.t0;
     t.hi = hi < t.t0 + tile_n ? hi : t.t0 + tile_n;
     return t;
@@ -176,7 +179,7 @@ __device__ __forceinline__ void add_adapter(const ProductLaunch &p, int n_out, i
     if (ad < 0 || ad >= p.n_adapters)
         return;
     if (!p.h) {                            // made before: y holds it
-        const TY *y = reinterpret_cast<const TY *>(p.y) + t * p.y_stride + f0 + 8 * u;
+        const TY *y = reinterpret_cast<const TY *>(p.y) + (int64_t)t * p.y_stride + f0 + 8 * u;
         const bool wide = (((uintptr_t)p.y | (uintptr_t)(p.y_stride * 2)) & 15u) == 0;
 #pragma unroll
         for (int m = 0; m < 2; m++) {
@@ -193,7 +196,7 @@ __device__ __forceinline__ void add_adapter(const ProductLaunch &p, int n_out, i
     }
     const int r = p.ranks ? min(max(p.ranks[ad], 0), p.rank) : p.rank;
     const TY *b = reinterpret_cast<const TY *>(p.B) + (size_t)ad * p.rank * n_out + f0 + 8 * u;
-    const float *h = p.h + t * p.rank;
+    const float *h = p.h + (int64_t)t * p.rank;
     int j = first;
     for (; j + 3 * every < r; j += 4 * every) {            // four rows in flight
         float hj[4];
@@ -237,7 +240,7 @@ __device__ __forceinline__ void scale_out(float (&v)[16], float rs, const float 
 // one rounding, and out
 template <typename TY>
 __device__ __forceinline__ void store_out(const ProductLaunch &p, int f0, int64_t t, const float (&v)[16], int u) {
-    TY *y = reinterpret_cast<TY *>(p.y) + t * p.y_stride + f0 + 8 * u;
+    TY *y = reinterpret_cast<TY *>(p.y) + (int64_t)t * p.y_stride + f0 + 8 * u;
     const bool wide = (((uintptr_t)p.y | (uintptr_t)(p.y_stride * 2)) & 15u) == 0;
 #pragma unroll
     for (int m = 0; m < 2; m++) {

@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kThreadsF, 2) few_kernel(const __grid_constant
         asm volatile("griddepcontrol.wait;" ::: "memory");    // no block ends before what this kernel follows
         return;
     }
-    const OutTile tl = out_tile(p.offsets ? &plan : nullptr, p.E, p.T, a.tile_n, a.n_out / 128, 128, it);
+    const OutTile<int64_t> tl = out_tile<int64_t>(p.offsets ? &plan : nullptr, p.E, p.T, a.tile_n, a.n_out / 128, 128, it);
     // inputs of this block in blocks of 64 (an even number), of this warp in tiles of 16
     const int steps = a.n_in / 128;
     const int k_lo = steps * rank / a.split * 2, k_hi = steps * (rank + 1) / a.split * 2;

@@ -109,7 +109,7 @@ template <int K> __device__ __forceinline__ void decode_row(const Row<K> &row, u
     }
 }
 
-struct Tile : OutTile {
+struct Tile : OutTile<int> {
     int n;            // columns, a multiple of 16 (PAIR: 32)
 };
 
@@ -125,12 +125,12 @@ struct Args {
 // The second block of the last pair may have no outputs (f0 == n_out).
 template <bool PAIR> __device__ __forceinline__ Tile make_tile(const Args &a, const Plan *plan, int64_t it, int rank) {
     Tile t;
-    static_cast<OutTile &>(t) =
-        out_tile(a.p.offsets ? plan : nullptr, a.p.E, a.p.T, a.tile_n, PAIR ? (a.n_out / 128 + 1) / 2 : a.n_out / 128,
+    static_cast<OutTile<int> &>(t) =
+        out_tile<int>(a.p.offsets ? plan : nullptr, a.p.E, (int)a.p.T, a.tile_n, PAIR ? (a.n_out / 128 + 1) / 2 : a.n_out / 128,
                  PAIR ? 256 : 128, it);
     if (PAIR)
         t.f0 += rank * 128;
-    t.n = PAIR ? (int)((t.hi - t.t0 + 31) / 32 * 32) : (int)((t.hi - t.t0 + 15) / 16 * 16);
+    t.n = PAIR ? (t.hi - t.t0 + 31) / 32 * 32 : (t.hi - t.t0 + 15) / 16 * 16;
     return t;
 }
 
@@ -315,19 +315,19 @@ __global__ void __launch_bounds__(kThreadsP, 1) product_kernel(const __grid_cons
             float rs[2];
             int slot[2];                   // -1: nothing in y
             const uint32_t mine = base + kAddOff + (uint32_t)og * 8192u + (uint32_t)(ow * 32 + lane) * 16u;
-            auto fetch = [&](int g, int64_t t) {
+            auto fetch = [&](int g, int t) {
                 const bool in = !keep && live && t >= tl.lo && t < tl.hi;
                 rs[g] = in ? a.p.rscale[t] : 0.0f;
                 slot[g] = -1;
                 if (a.p.B && !a.p.h && wide_y && in) {
-                    const TY *y = reinterpret_cast<const TY *>(a.p.y) + t * a.p.y_stride + tl.f0 + 8 * u;
+                    const TY *y = reinterpret_cast<const TY *>(a.p.y) + (int64_t)t * a.p.y_stride + tl.f0 + 8 * u;
                     copy16(mine + g * 4096u, y);
                     copy16(mine + g * 4096u + 2048u, y + 64);
                     slot[g] = a.p.slots[t];
                 }
                 copy_group();
             };
-            const int64_t t_mine = tl.t0 + ow * 4 + (lane >> 3);
+            const int t_mine = tl.t0 + ow * 4 + (lane >> 3);
             fetch(0, t_mine + 32 * og);
             fetch(1, t_mine + 32 * og + 16);
             for (int n0 = 0; ok && n0 < tl.n; n0 += kN, acc++) {
@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) product_kernel(const __grid_cons
                     asm volatile("bar.sync %0, 128;" ::"r"(1 + og) : "memory");
 #pragma unroll
                     for (int g = 0; g < 2; g++) {
-                        const int64_t t = t_mine + n0 + c0 + 16 * g;
+                        const int t = t_mine + n0 + c0 + 16 * g;
                         float x[16];
                         rotate_second(buf, g * 16 + ow * 4 + (lane >> 3), u, rs[g], right, x);
                         const bool in = live && t >= tl.lo && t < tl.hi;
@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) product_kernel(const __grid_cons
             for (int i = warp * each; i < mine; i += (kDecWarps + kOutWarps) * each) {
                 const int row = rank + (i + sub) * a.split;
                 const bool in = row < tl.n;
-                const int64_t t = in ? tl.t0 + row : tl.hi;
+                const int t = in ? tl.t0 + row : tl.hi;
                 const float rs = t < tl.hi ? a.p.rscale[t] : 0.0f;
                 float v[16], x[16];
 #pragma unroll
