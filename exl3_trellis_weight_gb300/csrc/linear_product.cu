@@ -623,38 +623,49 @@ exl3_status launch_product(const ProductLaunch &p, cudaStream_t s) {
     a.p = p;
     a.n_in = (int)(p.transposed ? p.cols : p.rows);
     a.n_out = (int)(p.transposed ? p.rows : p.cols);
-    const int64_t sms = device_sm_count();
-    const int nf = a.n_out / 128;
-    if (p.T > 512 * (p.offsets ? p.E : 1)) {
-        const int64_t pairs = sms / 2, np = (nf + 1) / 2;
-        // even tiles of up to 512 tokens, of the size whose rounds of the pairs take the fewest columns
-        int best = 512;
-        int64_t cost = INT64_MAX;
-        for (int n = 512; n > 256 && !p.offsets; n -= 32) {
-            const int64_t c = ((token_tiles(p, n) * np + pairs - 1) / pairs) * n;
-            if (c < cost)
-                cost = c, best = n;
+    const int64_t sms = device_sm_count(), pairs = sms / 2;
+    const int nf = a.n_out / 128, np = (nf + 1) / 2, steps = a.n_in / kStep;
+
+    // Alone: token tiles of even size, at most kN; blocks that would idle share the sums
+    // of the tiles, at least 4 steps each.
+    const int64_t n = (p.T + kN - 1) / kN;
+    a.tile_n = p.offsets ? (p.T > 16 ? kN : 32) : (int)(((p.T + n - 1) / n + 15) / 16 * 16);
+    const int64_t tiles = token_tiles(p, a.tile_n) * nf;
+    a.split = 1;
+    while (a.split < 8 && tiles * a.split * 2 <= sms && steps >= a.split * 2 * 4)
+        a.split *= 2;
+
+    // In pairs, with tiles of up to 512 tokens.  Both forms are estimated in cycles, as
+    // measured: a step takes about 1000 (shared memory and the handovers bound it; from
+    // 480 columns of a pair on its products do), the results of 64 columns 3000, which
+    // pass behind the next tile's sums unless that needs both accumulators.  (333 tokens,
+    // 4096 x 12288: 70 us alone in two rounds, 48 in pairs; 4096 tokens of 4096 x 4096 in
+    // tiles of 480: 116 us, of 256: 153.)  The experts' tokens are not known here: pairs
+    // when an expert has more than 512 on average.
+    int pair_n = 0;
+    if (p.offsets) {
+        pair_n = p.T > 512 * (int64_t)p.E ? 512 : 0;
+    } else if (p.T > kN) {
+        auto rounds = [](int64_t work, int64_t at_once) { return (work + at_once - 1) / at_once; };
+        int64_t best = (a.split > 1 ? 1 : rounds(tiles, sms)) * (steps / a.split) * 1000 + a.tile_n / 64 * 3000;
+        for (int t = 512; t >= 256; t -= 32) {
+            const int64_t step = t > 480 ? 1000 * t / 480 : 1000, out = t * 3000 / 64;
+            const int64_t r = rounds(token_tiles(p, t) * np, pairs);
+            const int64_t c = t > kN ? r * (steps * step + out) : r * steps * step + out;
+            if (c <= best)
+                best = c, pair_n = t;
         }
-        a.tile_n = best;
+    }
+    if (pair_n) {
+        a.tile_n = pair_n;
         a.b_steps = 1;                     // (block 1's decode warps count stages as steps)
         a.b_stages = (int)(kBArea / (a.tile_n * 64u));
         a.b_stages = a.b_stages > kBStages ? kBStages : a.b_stages;
         a.split = 1;
-        const int64_t tiles = token_tiles(p, a.tile_n) * np;
-        return launch_t<true>(a, (unsigned)(2 * (tiles < pairs ? tiles : pairs)), 2, s);
+        const int64_t t = token_tiles(p, a.tile_n) * np;
+        return launch_t<true>(a, (unsigned)(2 * (t < pairs ? t : pairs)), 2, s);
     }
-    // token tiles of even size, at most kN
-    const int64_t n = (p.T + kN - 1) / kN;
-    a.tile_n = p.offsets && p.T > 16 ? kN : (int)(((p.T + n - 1) / n + 15) / 16 * 16);
-    if (p.offsets && p.T <= 16)
-        a.tile_n = 32;
     set_b(a, a.tile_n);
-    const int64_t tiles = token_tiles(p, a.tile_n) * nf;
-    // blocks that would idle share the sums of the tiles, at least 4 steps each
-    const int steps = a.n_in / kStep;
-    a.split = 1;
-    while (a.split < 8 && tiles * a.split * 2 <= sms && steps >= a.split * 2 * 4)
-        a.split *= 2;
     const unsigned grid = (unsigned)(a.split > 1 ? tiles * a.split : tiles < sms ? tiles : sms);
     return launch_t<false>(a, grid, (unsigned)a.split, s);
 }
