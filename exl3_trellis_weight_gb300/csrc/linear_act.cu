@@ -1,11 +1,13 @@
 // linear_act.cu -- rotated activations: z = (x . left) H per block of 128
 // inputs, one row scale per token, written in binary16 in the order in which
-// linear_product.cu loads its token operand (linear_few.cu makes its own).
+// linear_product.cu and linear_few.cu load their token operand.
 //
-// Bound by memory: 2 bytes read and 2 written per element.  A thread owns 16
-// consecutive elements (four butterfly spans in registers) and eight threads a
-// block of 128 (three spans by shuffles): 3 shuffles per element instead of the
-// 5 of one element per lane and span.
+// 2 bytes read and 2 written per element, but bound by the issue of instructions:
+// unpacking, scaling, seven spans and packing are 20 and more an element.  A thread
+// owns 16 consecutive elements and eight threads a block of 128; four spans in
+// registers, an exchange through shared memory, three more in registers.  The two
+// rounds of packed binary32 additions make two elements an instruction.  4096 x 4096
+// bf16: 20.5 us, 3.3 TB/s; 16384 x 2048 of 64 experts: 46 us, 2.9 TB/s.
 #include "linear_rotate.cuh"
 
 namespace exl3 {
@@ -65,6 +67,57 @@ __device__ __forceinline__ float block_max(float m, float *place, int warps) {
     return m;
 }
 
+// v: elements 16 s + i of a block of 128, s = lane % 8; writes v H in binary16.  Four
+// spans in registers, three after an exchange through the warp's part of shared memory
+// (shuffles, 48 a thread, made 4096 x 4096 22 us instead of 20.5): then lane s has, of each sixteen, the two
+// that stand at places 2s and 2s + 1.
+constexpr int kUnit = 144;                 // floats from one block of 128 to the next: other banks
+__device__ __forceinline__ void rotate_out128(float (&v)[16], const PrepLaunch &a, int64_t NP, int64_t t, int k, bool in,
+                                              float *part, int lane) {
+    const int s = lane & 7;
+    float *const unit = part + (lane >> 3) * kUnit;
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+        const float p = v[i], q = v[i + 1];
+        v[i] = __fadd_rn(p, q);
+        v[i + 1] = __fsub_rn(p, q);
+    }
+    span2<2>(v);
+    span2<4>(v);
+    span2<8>(v);
+    // float4 f of sixteen b at (4 b + f) ^ (b / 2): eight lanes cover all banks
+#pragma unroll
+    for (int f = 0; f < 4; f++)
+        *reinterpret_cast<float4 *>(unit + 4 * ((4 * s + f) ^ (s >> 1))) = make_float4(v[4 * f], v[4 * f + 1], v[4 * f + 2], v[4 * f + 3]);
+    __syncwarp();
+    if (a.order == 0) {
+#pragma unroll
+        for (int b = 0; b < 8; b++) {
+            const float2 w = *reinterpret_cast<const float2 *>(unit + 4 * ((4 * b + (s >> 1)) ^ (b >> 1)) + 2 * (s & 1));
+            v[2 * b] = w.x, v[2 * b + 1] = w.y;
+        }
+    } else {
+        // the inputs at places 2s and 2s + 1
+        const int j = s >> 1, h = s & 1;
+        const int i0 = a.order == 1 ? j + 8 * h : 2 * j + 8 * h, i1 = a.order == 1 ? i0 + 4 : i0 + 1;
+#pragma unroll
+        for (int b = 0; b < 8; b++) {
+            v[2 * b] = unit[4 * ((4 * b + (i0 >> 2)) ^ (b >> 1)) + (i0 & 3)];
+            v[2 * b + 1] = unit[4 * ((4 * b + (i1 >> 2)) ^ (b >> 1)) + (i1 & 3)];
+        }
+    }
+    __syncwarp();
+    span2<2>(v);
+    span2<4>(v);
+    span2<8>(v);
+    if (!in)
+        return;
+    const int k0 = k & ~127;
+#pragma unroll
+    for (int b = 0; b < 8; b++)
+        *reinterpret_cast<uint32_t *>(a.image + act_offset(NP, t, k0 + 16 * b + 2 * s)) = pack2<__half>(v[2 * b], v[2 * b + 1]);
+}
+
 // grid: (blocks of neighbouring rows, 1 + adapters' rows); block: a multiple of 32
 // threads, 16 inputs each.  ONE: a row fits one round of the block and stays in
 // registers, `left` too while the expert stays the same, and the next row is on its way.
@@ -72,7 +125,9 @@ template <typename TX, bool VEC, bool ONE>
 __global__ void prep_kernel(const PrepLaunch a) {
     __shared__ int32_t off[kMaxExperts + 1];
     __shared__ float wmax[2][32];
-    const int tid = threadIdx.x, warps = (int)(blockDim.x >> 5);
+    extern __shared__ __align__(16) float parts[];
+    const int tid = threadIdx.x, warps = (int)(blockDim.x >> 5), lane = tid & 31;
+    float *const part = parts + (tid >> 5) * (4 * kUnit);
     const int64_t NP = act_rows(a.T);
     // the product kernel behind this one may start on the codes; it waits for this
     // kernel's end before it reads z.  (This kernel itself starts after everything
@@ -170,47 +225,28 @@ __global__ void prep_kernel(const PrepLaunch a) {
 #pragma unroll
             for (int i = 0; i < 16; i += 2)
                 mul2(v[i], v[i + 1], up, up);
-            rotate128(v, tid);
-            uint32_t w8[8];
-            if (a.order == 0) {
-#pragma unroll
-                for (int i = 0; i < 8; i++)
-                    w8[i] = pack2<__half>(v[2 * i], v[2 * i + 1]);
-            } else if (a.order == 1) {
-#pragma unroll
-                for (int i = 0; i < 8; i++)
-                    w8[i] = pack2<__half>(v[(i >> 1) + 8 * (i & 1)], v[(i >> 1) + 8 * (i & 1) + 4]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; i++)
-                    w8[i] = pack2<__half>(v[2 * (i >> 1) + 8 * (i & 1)], v[2 * (i >> 1) + 8 * (i & 1) + 1]);
-            }
-            // Lanes l and l + 4 (the same places of two blocks of 64) swap a half, so that
-            // eight lanes write one block's whole 128 bytes at a time
-            const bool high = (tid & 4) != 0;
-            uint32_t first[4], second[4];
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? w8[i] : w8[4 + i], 4);
-                first[i] = high ? got : w8[i];
-                second[i] = high ? w8[4 + i] : got;
-            }
-            if (in) {
-                // elements 8 high .. of the pair's 16, of the lower and of the upper block
-                const int k1 = (k & ~127) + (k & 48) + (high ? 8 : 0);
-                *reinterpret_cast<uint4 *>(a.image + act_offset(NP, t, k1)) = make_uint4(first[0], first[1], first[2], first[3]);
-                *reinterpret_cast<uint4 *>(a.image + act_offset(NP, t, k1 + 64)) = make_uint4(second[0], second[1], second[2], second[3]);
-            }
+            rotate_out128(v, a, NP, t, k, in, part, lane);
         }
     }
 }
 
-template <typename TX, bool VEC>
-void launch_prep_t(const PrepLaunch &p, dim3 grid, unsigned block, bool one, cudaStream_t s) {
-    if (one)
-        prep_kernel<TX, VEC, true><<<grid, block, 0, s>>>(p);
-    else
-        prep_kernel<TX, VEC, false><<<grid, block, 0, s>>>(p);
+template <typename TX, bool VEC, bool ONE>
+exl3_status launch_prep_t(const PrepLaunch &p, dim3 grid, unsigned block, cudaStream_t s) {
+    const size_t smem = (size_t)(block / 32) * 4 * kUnit * sizeof(float);
+    static SmemAllowed allowed;
+    if (smem > 40 * 1024) {
+        const cudaError_t e = allow_smem((const void *)prep_kernel<TX, VEC, ONE>, smem, allowed);
+        if (e != cudaSuccess)
+            return cuda_check(e, "cudaFuncSetAttribute(activation rotation)");
+    }
+    prep_kernel<TX, VEC, ONE><<<grid, block, smem, s>>>(p);
+    note_launch();
+    return cuda_check(cudaGetLastError(), "activation rotation launch");
+}
+template <typename TX> exl3_status launch_prep_x(const PrepLaunch &p, dim3 grid, unsigned block, bool vec, bool one, cudaStream_t s) {
+    if (vec)
+        return one ? launch_prep_t<TX, true, true>(p, grid, block, s) : launch_prep_t<TX, true, false>(p, grid, block, s);
+    return one ? launch_prep_t<TX, false, true>(p, grid, block, s) : launch_prep_t<TX, false, false>(p, grid, block, s);
 }
 
 }  // namespace
@@ -223,13 +259,8 @@ exl3_status launch_prep(const PrepLaunch &p, cudaStream_t s) {
     const int64_t most = (int64_t)device_sm_count() * (1024 / block);
     const dim3 grid((unsigned)(p.T < most ? p.T : most),
                     1 + (p.n_adapters ? (unsigned)((p.rank + block / 32 - 1) / (block / 32)) : 0u));
-    if (p.dt == EXL3_BF16)
-        vec ? launch_prep_t<__nv_bfloat16, true>(p, grid, block, one, s)
-            : launch_prep_t<__nv_bfloat16, false>(p, grid, block, one, s);
-    else
-        vec ? launch_prep_t<__half, true>(p, grid, block, one, s) : launch_prep_t<__half, false>(p, grid, block, one, s);
-    note_launch();
-    return cuda_check(cudaGetLastError(), "activation rotation launch");
+    return p.dt == EXL3_BF16 ? launch_prep_x<__nv_bfloat16>(p, grid, block, vec, one, s)
+                             : launch_prep_x<__half>(p, grid, block, vec, one, s);
 }
 
 }  // namespace exl3
