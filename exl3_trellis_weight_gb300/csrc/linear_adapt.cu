@@ -414,11 +414,16 @@ template <typename TX> __global__ void __launch_bounds__(256) expand_kernel(cons
 
 // ---- outer: dM_i[r][k] = sum_{t of i} h[t][r] x[t][k] ------------------------------
 // A block takes one adapter, 128 of k (16 a warp) and a share of the adapter's tokens
-// (the blocks of a cluster take turns at its tiles of 32).
+// (the blocks of a cluster take turns at its tiles of 32).  Bound by latency: a tile is
+// 8 KB of x and a dozen instructions a warp between two barriers, so that blocks in
+// flight count; three to a SM up to rank 64 (112 registers, where 16 rows more a warp
+// took 122 and two blocks) and twice the split made 4096 tokens x (4096 + 4096), four
+// adapters of rank 64, 42 us instead of 60, and 1001 tokens 8 us instead of 14.
 constexpr int kOuterStages = 4;
 constexpr int kXRow = 128 + kPad;
 
-template <typename TX, bool VEC> __global__ void __launch_bounds__(256) outer_kernel(const AdaptLaunch a) {
+// MB: sixteens of rows at most (4 up to rank 64: fewer registers, three blocks a SM)
+template <typename TX, bool VEC, int MB> __global__ void __launch_bounds__(256, MB == 4 ? 3 : 2) outer_kernel(const AdaptLaunch a) {
     extern __shared__ __align__(16) unsigned char smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, j = lane & 3;
     const int rank = (int)(blockIdx.x % a.split), i = blockIdx.y;
@@ -458,7 +463,7 @@ template <typename TX, bool VEC> __global__ void __launch_bounds__(256) outer_ke
     };
     // h of a tile: token tid / 8, elements tid % 8 + 8 q, in the same way
     const int ht = tid >> 3, hq = tid & 7;
-    float hv[16];
+    float hv[2 * MB];
     int hnext;
     auto hlookup = [&](int s) {
         const int t = (rank + s * a.split) * kTile + ht;
@@ -467,7 +472,7 @@ template <typename TX, bool VEC> __global__ void __launch_bounds__(256) outer_ke
     auto fetch = [&](int s) {
         const float *from = sd.h + (int64_t)max(hnext, 0) * a.rank;
 #pragma unroll
-        for (int q = 0; q < 16; q++)
+        for (int q = 0; q < 2 * MB; q++)
             if (q < 2 * mb)
                 hv[q] = hnext >= 0 && hq + 8 * q < r ? from[hq + 8 * q] : 0.0f;
         hlookup(s + 1);
@@ -478,9 +483,9 @@ template <typename TX, bool VEC> __global__ void __launch_bounds__(256) outer_ke
 #pragma unroll
     for (int s = 0; s < kOuterStages - 1; s++)
         load(s);
-    float acc[8][2][4];
+    float acc[MB][2][4];
 #pragma unroll
-    for (int m = 0; m < 8; m++)
+    for (int m = 0; m < MB; m++)
 #pragma unroll
         for (int b = 0; b < 2; b++)
 #pragma unroll
@@ -489,7 +494,7 @@ template <typename TX, bool VEC> __global__ void __launch_bounds__(256) outer_ke
     for (int s = 0; s < mine; s++) {
         TX *const sh = reinterpret_cast<TX *>(smem + kOuterStages * xbytes + (s & 1) * hbytes);
 #pragma unroll
-        for (int q = 0; q < 16; q++)
+        for (int q = 0; q < 2 * MB; q++)
             if (q < 2 * mb)
                 split<TX>(__fmul_rn(hv[q], up), sh + ht * hrow + hq + 8 * q, kTile * hrow);
         copy_wait<kOuterStages - 2>();
@@ -502,7 +507,7 @@ template <typename TX, bool VEC> __global__ void __launch_bounds__(256) outer_ke
             uint32_t b[4];
             load_t(xs + (uint32_t)((k * 16 + (lane & 15)) * kXRow + warp * 16 + (lane >> 4) * 8) * 2, b);
 #pragma unroll
-            for (int m = 0; m < 8; m++)
+            for (int m = 0; m < MB; m++)
                 if (m < mb) {
                     uint32_t f[4];         // blocks (tokens 0-7 | 8-15) x (rows 0-7 | 8-15): rows first
                     const uint32_t at = hs + (uint32_t)((k * 16 + (lane & 7) + (lane >> 4) * 8) * hrow + m * 16 + ((lane >> 3) & 1) * 8) * 2;
@@ -520,7 +525,7 @@ template <typename TX, bool VEC> __global__ void __launch_bounds__(256) outer_ke
     // partial sums [R16][128] meet in shared memory; block `rank` finishes rows rank, rank + split, ...
     float *const part = reinterpret_cast<float *>(smem);
 #pragma unroll
-    for (int m = 0; m < 8; m++)
+    for (int m = 0; m < MB; m++)
         if (m < mb)
 #pragma unroll
             for (int b = 0; b < 2; b++)
@@ -638,9 +643,10 @@ exl3_status launch_expand(const AdaptLaunch &p, void *y, int64_t y_stride, cudaS
 
 exl3_status launch_outer(const AdaptLaunch &p0, cudaStream_t s) {
     AdaptLaunch p = p0;
+    // four blocks a SM (they are short) while each has two tiles of an even share
     const int64_t blocks = (int64_t)(p.side[0].n + p.side[1].n) / 128 * p.n, sms = device_sm_count();
     p.split = 1;
-    while (p.split < 8 && blocks * p.split * 2 <= 2 * sms && p.T >= (int64_t)p.split * 2 * kTile * p.n)
+    while (p.split < 8 && blocks * p.split * 2 <= 4 * sms && p.T >= (int64_t)p.split * 2 * kTile * p.n)
         p.split *= 2;
     const int R16 = (p.rank + 15) / 16 * 16;
     const size_t stages = (size_t)kOuterStages * kTile * kXRow * 2 + (size_t)4 * kTile * (R16 + kPad) * 2;
@@ -648,9 +654,14 @@ exl3_status launch_outer(const AdaptLaunch &p0, cudaStream_t s) {
     const dim3 grid((unsigned)((p.side[0].n + p.side[1].n) / 128 * p.split), (unsigned)p.n);
     const bool vec = wide_rows(p.side[0]) && wide_rows(p.side[1]);
     auto go = [&](auto k) { return launch("adapter gradient launch", k, grid, 256, smem, (unsigned)p.split, false, s, p); };
+    if (p.rank > 64) {
+        if (p.dt == EXL3_BF16)
+            return vec ? go(outer_kernel<__nv_bfloat16, true, 8>) : go(outer_kernel<__nv_bfloat16, false, 8>);
+        return vec ? go(outer_kernel<__half, true, 8>) : go(outer_kernel<__half, false, 8>);
+    }
     if (p.dt == EXL3_BF16)
-        return vec ? go(outer_kernel<__nv_bfloat16, true>) : go(outer_kernel<__nv_bfloat16, false>);
-    return vec ? go(outer_kernel<__half, true>) : go(outer_kernel<__half, false>);
+        return vec ? go(outer_kernel<__nv_bfloat16, true, 4>) : go(outer_kernel<__nv_bfloat16, false, 4>);
+    return vec ? go(outer_kernel<__half, true, 4>) : go(outer_kernel<__half, false, 4>);
 }
 
 }  // namespace exl3
