@@ -416,9 +416,10 @@ template <typename TX> __global__ void __launch_bounds__(256) expand_kernel(cons
 // A block takes one adapter, 128 of k (16 a warp) and a share of the adapter's tokens
 // (the blocks of a cluster take turns at its tiles of 32).  Bound by latency: a tile is
 // 8 KB of x and a dozen instructions a warp between two barriers, so that blocks in
-// flight count; three to a SM up to rank 64 (112 registers, where 16 rows more a warp
-// took 122 and two blocks) and twice the split made 4096 tokens x (4096 + 4096), four
-// adapters of rank 64, 42 us instead of 60, and 1001 tokens 8 us instead of 14.
+// flight count: room for rank 64 only where that is enough lets three blocks share a
+// SM instead of two, and with twice the split 4096 tokens x (4096 + 4096), four adapters
+// of rank 64, take 42 us instead of 60 (1.6 TB/s of activations read), 1001 tokens 8 us
+// instead of 14.
 constexpr int kOuterStages = 4;
 constexpr int kXRow = 128 + kPad;
 

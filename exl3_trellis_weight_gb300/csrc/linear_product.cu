@@ -10,8 +10,10 @@
 //          along the outputs (x W^) or along the sum (x W^^T): the first is
 //          stored as an operand whose rows run along M, the second along K, and
 //          only the descriptor differs;
-//   16-23  results: accumulator -> shared memory (one token per row) -> H over
-//          the 128 outputs in two passes -> scales, adapters, one rounding;
+//   16-23  results, two groups that take turns at chunks of 32 tokens: accumulator ->
+//          shared memory (one token per row) -> H over the 128 outputs in two passes ->
+//          scales, adapters, one rounding (3000 cycles a chunk; with one group of four
+//          the last tile's results stood alone twice as long);
 //   24     bulk copies of the rotated activations, one contiguous block a step;
 //   25     issues the matrix instructions (binary16 in, binary32 out).
 //
@@ -21,6 +23,13 @@
 // both blocks by up to 256 tokens of which each block holds half, and a tile
 // has up to 512 tokens in two accumulators: each weight is decoded for twice
 // the tokens, and each copy of activations feeds twice the outputs.
+//
+// Bound: of a step's cycles the decode takes 384 of each quarter's arithmetic pipes,
+// the matrix instructions 512 for 256 tokens (1024 for a pair's 512), and shared memory
+// about 900 in a pair (writing and reading both operands); measured are 1000 a step, up
+// to 480 tokens in a pair, because the roles share the issue slots and the shared
+// memory.  4096 x 4096 x 4096, K = 2, in pairs: 110 us, 1.25 PFLOP/s; 333 tokens x 4096
+// x 12288, K = 4, in pairs: 48 us.
 //
 // With few tiles (decode), the sum is split over the `split` blocks of a
 // cluster; each leaves its partial sums in its shared memory and block r adds
