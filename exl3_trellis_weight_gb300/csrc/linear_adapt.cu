@@ -72,10 +72,9 @@ __device__ __forceinline__ void load_t(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
 }
-__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
-    uint32_t v;
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
-    return v;
+__device__ __forceinline__ void load_n(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
 }
 
 // the power of two that takes m to [2^7, 2^8); none for bfloat16, whose range is binary32's
@@ -199,7 +198,8 @@ __device__ __forceinline__ bool find_tile(const AdaptLaunch &a, int tile, int &i
 constexpr int kShrinkStages = 3;
 constexpr int kRow = 128 + kPad;
 
-template <typename TX, bool VEC> __global__ void __launch_bounds__(256) shrink_kernel(const AdaptLaunch a) {
+// MB: sixteens of rows at most (4 up to rank 64)
+template <typename TX, bool VEC, int MB> __global__ void __launch_bounds__(256, MB == 4 ? 3 : 2) shrink_kernel(const AdaptLaunch a) {
     extern __shared__ __align__(16) unsigned char smem[];
     const AdaptSide &sd = a.side[blockIdx.y];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, j = lane & 3;
@@ -209,9 +209,9 @@ template <typename TX, bool VEC> __global__ void __launch_bounds__(256) shrink_k
     int i, lo, n;
     if (!find_tile(a, (int)(blockIdx.x / a.split), i, lo, n))
         return;                            // (the whole cluster)
-    const int r = rank_of(a.ranks, i, a.rank), R8 = (a.rank + 7) / 8 * 8, nb = (r + 7) / 8;
+    const int r = rank_of(a.ranks, i, a.rank), R16 = (a.rank + 15) / 16 * 16, mb = (r + 15) / 16;
     const int steps = sd.n / 128, k_lo = steps * rank / a.split, k_hi = steps * (rank + 1) / a.split;
-    const uint32_t base = saddr(smem), stage = (uint32_t)(kTile + R8) * kRow * 2;
+    const uint32_t base = saddr(smem), stage = (uint32_t)(kTile + R16) * kRow * 2;
     const uint16_t *x = reinterpret_cast<const uint16_t *>(sd.x);
     const uint16_t *M = reinterpret_cast<const uint16_t *>(sd.M) + (size_t)i * a.rank * sd.n;
     // copies of a step: tokens tid / 16 and tid / 16 + 16, rows tid / 16 + 16 m of the factor, 8 elements each
@@ -226,22 +226,28 @@ template <typename TX, bool VEC> __global__ void __launch_bounds__(256) shrink_k
 #pragma unroll
             for (int b = 0; b < 2; b++)
                 row8<VEC>(st + (uint32_t)((row + 16 * b) * kRow + c8) * 2, xr[b] + (int64_t)k * 128, row + 16 * b < n);
-            for (int q = row; q < nb * 8; q += 16)
-                copy16z(st + (uint32_t)((kTile + q) * kRow + c8) * 2, M + (size_t)min(q, a.rank - 1) * sd.n + k * 128 + c8, q < r);
+#pragma unroll
+            for (int m = 0; m < MB; m++)
+                if (m < mb) {
+                    const bool real = row + 16 * m < r;
+                    copy16z(st + (uint32_t)((kTile + row + 16 * m) * kRow + c8) * 2,
+                            M + (size_t)(real ? row + 16 * m : 0) * sd.n + k * 128 + c8, real);
+                }
         }
         copy_group();
     };
 #pragma unroll
     for (int s = 0; s < kShrinkStages - 1; s++)
         load(k_lo + s);
-    float acc[16][4];
+    float acc[2 * MB][4];
 #pragma unroll
-    for (int b = 0; b < 16; b++)
+    for (int b = 0; b < 2 * MB; b++)
 #pragma unroll
         for (int e = 0; e < 4; e++)
             acc[b][e] = 0.0f;
-    const uint32_t at = (uint32_t)(((warp & 1) * 16 + g) * kRow + (warp >> 1) * 32 + 2 * j) * 2;
-    const uint32_t bt = (uint32_t)((kTile + g) * kRow + (warp >> 1) * 32 + 2 * j) * 2;
+    // blocks of 8 x 8: tokens (0-7 | 8-15) x inputs (0-7 | 8-15), rows (0-7 | 8-15) x inputs the other way round
+    const uint32_t at = (uint32_t)(((warp & 1) * 16 + (lane & 15)) * kRow + (warp >> 1) * 32 + (lane >> 4) * 8) * 2;
+    const uint32_t bt = (uint32_t)((kTile + (lane & 7) + (lane >> 4) * 8) * kRow + (warp >> 1) * 32 + (lane & 8)) * 2;
     for (int k = k_lo; k < k_hi; k++) {
         copy_wait<kShrinkStages - 2>();
         __syncthreads();
@@ -249,24 +255,29 @@ template <typename TX, bool VEC> __global__ void __launch_bounds__(256) shrink_k
         const uint32_t st = base + (uint32_t)((k - k_lo) % kShrinkStages) * stage;
 #pragma unroll
         for (int h = 0; h < 64; h += 32) {
-            const uint32_t f[4] = {lds32(st + at + h), lds32(st + at + h + 16 * kRow), lds32(st + at + h + 16),
-                                   lds32(st + at + h + 16 * kRow + 16)};
+            uint32_t f[4];
+            load_n(st + at + h, f);
 #pragma unroll
-            for (int b = 0; b < 16; b++)
-                if (b < nb)
-                    mma<TX>(acc[b], f, lds32(st + bt + h + b * 16 * kRow), lds32(st + bt + h + b * 16 * kRow + 16));
+            for (int m = 0; m < MB; m++)
+                if (m < mb) {
+                    uint32_t b[4];
+                    load_n(st + bt + h + m * 32 * kRow, b);
+                    mma<TX>(acc[2 * m], f, b[0], b[1]);
+                    mma<TX>(acc[2 * m + 1], f, b[2], b[3]);
+                }
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
-    // partial sums [4][token][R8] meet in shared memory
+    // partial sums [4][token][R16] meet in shared memory
     float *const part = reinterpret_cast<float *>(smem);
 #pragma unroll
-    for (int b = 0; b < 16; b++)
-        if (b < nb)
+    for (int b = 0; b < 2 * MB; b++)
+        if (b < 2 * mb)
 #pragma unroll
-            for (int e = 0; e < 4; e++)
-                part[((warp >> 1) * kTile + (warp & 1) * 16 + g + 8 * (e >> 1)) * R8 + b * 8 + 2 * j + (e & 1)] = acc[b][e];
+            for (int e = 0; e < 4; e += 2)
+                *reinterpret_cast<float2 *>(part + ((warp >> 1) * kTile + (warp & 1) * 16 + g + 4 * e) * R16 + b * 8 + 2 * j) =
+                    make_float2(acc[b][e], acc[b][e + 1]);
     if (a.split > 1)
         cluster_sync();
     else
@@ -280,11 +291,11 @@ template <typename TX, bool VEC> __global__ void __launch_bounds__(256) shrink_k
         float s = 0.0f;
         if (q < r) {
             for (int b = 0; b < a.split; b++) {
-                const uint32_t from = at_block(base + (uint32_t)(t * R8 + q) * 4u, b);
+                const uint32_t from = at_block(base + (uint32_t)(t * R16 + q) * 4u, b);
 #pragma unroll
                 for (int w = 0; w < 4; w++) {
                     float v;
-                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(from + (uint32_t)(w * kTile * R8) * 4u) : "memory");
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(from + (uint32_t)(w * kTile * R16) * 4u) : "memory");
                     s = __fadd_rn(s, v);
                 }
             }
@@ -361,7 +372,16 @@ template <typename TX> __global__ void __launch_bounds__(256) expand_kernel(cons
     for (int q = 0; q < 16; q++)
         if (q < 2 * kb)
             split<TX>(__fmul_rn(hv[q], up), sh + (tid >> 3) * hrow + (tid & 7) + 8 * q, kTile * hrow);
-    const uint32_t ha = saddr(smem) + (uint32_t)(((warp & 1) * 16 + g) * hrow + 2 * j) * 2;
+    const uint32_t ha = saddr(smem) + (uint32_t)(((warp & 1) * 16 + (lane & 15)) * hrow + (lane >> 4) * 8) * 2;
+    const uint32_t ba = sB + (uint32_t)((lane & 15) * kF + (warp >> 1) * 32 + (lane >> 4) * 8) * 2;
+    const bool wide = (((uintptr_t)y | (uintptr_t)(y_stride * 2)) & 15u) == 0;
+    // results: tokens tid / 16 and tid / 16 + 16, 8 outputs each
+    TX *to[2];
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+        const int t = (tid >> 4) + 16 * h;
+        to[h] = t < n ? reinterpret_cast<TX *>(y) + (int64_t)a.plan.perm[lo + t] * y_stride + (tid & 15) * 8 : nullptr;
+    }
     for (int f0 = f_lo, buf = 0; f0 < f_hi; f0 += 128, buf ^= 1) {
         load(f0 + 128, buf ^ 1);
         copy_wait<1>();
@@ -373,14 +393,13 @@ template <typename TX> __global__ void __launch_bounds__(256) expand_kernel(cons
             for (int e = 0; e < 4; e++)
                 acc[b][e] = 0.0f;
         for (int k = 0; k < kb; k++) {
-            const uint32_t at = ha + k * 32;
-            const uint32_t f[4] = {lds32(at), lds32(at + 16 * hrow), lds32(at + 16), lds32(at + 16 * hrow + 16)};
-            const uint32_t at2 = at + hlow;
-            const uint32_t f2[4] = {lds32(at2), lds32(at2 + 16 * hrow), lds32(at2 + 16), lds32(at2 + 16 * hrow + 16)};
+            uint32_t f[4], f2[4];
+            load_n(ha + k * 32, f);
+            load_n(ha + k * 32 + hlow, f2);
 #pragma unroll
             for (int b = 0; b < 2; b++) {
                 uint32_t t[4];
-                load_t(sB + buf * bbytes + (uint32_t)((k * 16 + (lane & 15)) * kF + (warp >> 1) * 32 + b * 16 + (lane >> 4) * 8) * 2, t);
+                load_t(ba + buf * bbytes + (uint32_t)(k * 16 * kF + b * 16) * 2, t);
                 mma<TX>(acc[2 * b], f, t[0], t[1]);
                 mma<TX>(acc[2 * b + 1], f, t[2], t[3]);
                 mma<TX>(acc[2 * b], f2, t[0], t[1]);
@@ -390,22 +409,20 @@ template <typename TX> __global__ void __launch_bounds__(256) expand_kernel(cons
 #pragma unroll
         for (int b = 0; b < 4; b++)
 #pragma unroll
-            for (int e = 0; e < 4; e++)
-                so[((warp & 1) * 16 + g + 8 * (e >> 1)) * kF + (warp >> 1) * 32 + b * 8 + 2 * j + (e & 1)] =
-                    from_f32<TX>(__fmul_rn(acc[b][e], down));
+            for (int e = 0; e < 4; e += 2)
+                *reinterpret_cast<uint32_t *>(so + ((warp & 1) * 16 + g + 4 * e) * kF + (warp >> 1) * 32 + b * 8 + 2 * j) =
+                    pack2<TX>(__fmul_rn(acc[b][e], down), __fmul_rn(acc[b][e + 1], down));
         __syncthreads();
-        const bool wide = (((uintptr_t)y | (uintptr_t)(y_stride * 2)) & 15u) == 0;
-        for (int e = tid; e < kTile * 16; e += 256) {
-            const int t = e >> 4, c = (e & 15) * 8;
-            if (t >= n)
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            const TX *from = so + ((tid >> 4) + 16 * h) * kF + (tid & 15) * 8;
+            if (!to[h])
                 continue;
-            TX *to = reinterpret_cast<TX *>(y) + (int64_t)a.plan.perm[lo + t] * y_stride + f0 + c;
-            const TX *from = so + t * kF + c;
             if (wide) {
-                *reinterpret_cast<uint4 *>(to) = *reinterpret_cast<const uint4 *>(from);
+                *reinterpret_cast<uint4 *>(to[h] + f0) = *reinterpret_cast<const uint4 *>(from);
             } else {
                 for (int q = 0; q < 8; q++)
-                    to[q] = from[q];
+                    to[h][f0 + q] = from[q];
             }
         }
         __syncthreads();
@@ -621,15 +638,20 @@ exl3_status launch_shrink(const AdaptLaunch &p0, int sides, cudaStream_t s) {
     p.split = 1;
     while (p.split < 8 && tiles * sides * p.split * 2 <= 2 * sms && least / 128 >= p.split * 2 * 4)
         p.split *= 2;
-    const int R8 = (p.rank + 7) / 8 * 8;
-    const size_t stages = (size_t)kShrinkStages * (kTile + R8) * kRow * 2, part = (size_t)4 * kTile * R8 * 4;
+    const int R16 = (p.rank + 15) / 16 * 16;
+    const size_t stages = (size_t)kShrinkStages * (kTile + R16) * kRow * 2, part = (size_t)4 * kTile * R16 * 4;
     const size_t smem = stages > part ? stages : part;
     const dim3 grid((unsigned)(tiles * p.split), (unsigned)sides);
     const bool vec = wide_rows(p.side[0]) && (sides < 2 || wide_rows(p.side[1]));
     auto go = [&](auto k) { return launch("adapter shrink launch", k, grid, 256, smem, (unsigned)p.split, true, s, p); };
+    if (p.rank > 64) {
+        if (p.dt == EXL3_BF16)
+            return vec ? go(shrink_kernel<__nv_bfloat16, true, 8>) : go(shrink_kernel<__nv_bfloat16, false, 8>);
+        return vec ? go(shrink_kernel<__half, true, 8>) : go(shrink_kernel<__half, false, 8>);
+    }
     if (p.dt == EXL3_BF16)
-        return vec ? go(shrink_kernel<__nv_bfloat16, true>) : go(shrink_kernel<__nv_bfloat16, false>);
-    return vec ? go(shrink_kernel<__half, true>) : go(shrink_kernel<__half, false>);
+        return vec ? go(shrink_kernel<__nv_bfloat16, true, 4>) : go(shrink_kernel<__nv_bfloat16, false, 4>);
+    return vec ? go(shrink_kernel<__half, true, 4>) : go(shrink_kernel<__half, false, 4>);
 }
 
 exl3_status launch_expand(const AdaptLaunch &p, void *y, int64_t y_stride, cudaStream_t s) {
