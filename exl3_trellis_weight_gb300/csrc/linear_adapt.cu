@@ -87,11 +87,12 @@ template <typename TX> __device__ __forceinline__ void operand_scale(float m, fl
     }
 }
 
-// v as the sum of two values of the type, `apart` elements apart
-template <typename TX> __device__ __forceinline__ void split(float v, TX *to, int apart) {
-    const TX high = from_f32<TX>(v);
-    to[0] = high;
-    to[apart] = from_f32<TX>(__fsub_rn(v, to_f32(high)));
+// v and w, each as the sum of two values of the type, `apart` elements apart
+template <typename TX> __device__ __forceinline__ void split2(float v, float w, TX *to, int apart) {
+    const uint32_t high = pack2<TX>(v, w);
+    const float2 f = unpack2<TX>(high);
+    *reinterpret_cast<uint32_t *>(to) = high;
+    *reinterpret_cast<uint32_t *>(to + apart) = pack2<TX>(__fsub_rn(v, f.x), __fsub_rn(w, f.y));
 }
 
 // ---- plan --------------------------------------------------------------------
@@ -194,7 +195,10 @@ __device__ __forceinline__ bool find_tile(const AdaptLaunch &a, int tile, int &i
 
 // ---- shrink: h[t][r] = gain_i sum_k M_i[r][k] x[t][k] ---------------------------
 // A block takes one tile and a share of the sum (the blocks of a cluster split it);
-// warp w the tokens 16 (w % 2) .. and two sixteenths of every step of 128.
+// warp w the tokens 16 (w % 2) .. and two sixteenths of every step of 128.  Bound by the
+// hand-over of steps (a fourth stage changed nothing, twice the split cost a third more):
+// 4096 tokens of 4096, rank 16: 15 us, 2.2 TB/s of activations read; twice 4096 x 4096,
+// rank 64: 31 us.
 constexpr int kShrinkStages = 3;
 constexpr int kRow = 128 + kPad;
 
@@ -315,7 +319,8 @@ template <typename TX, bool VEC, int MB> __global__ void __launch_bounds__(256, 
 
 // ---- expand: y[t] = sum_r h[t][r] M_i[r] (one rounding; the coded product adds to it) --------
 // A block takes one tile and 512 outputs, 128 at a time; warp w the tokens 16 (w % 2) ..
-// and 32 of the outputs.
+// and 32 of the outputs.  Bound by instructions (2.6 of 4 a cycle): 4096 x 4096, rank
+// 16: 15 us, 2.2 TB/s written.
 template <typename TX> __global__ void __launch_bounds__(256) expand_kernel(const AdaptLaunch a, void *y, int64_t y_stride) {
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ float wmax[8];
@@ -345,14 +350,15 @@ template <typename TX> __global__ void __launch_bounds__(256) expand_kernel(cons
     };
     load(f_lo, 0);
     // h of the tile in the operand's type, scaled by a power of two: token tid / 8,
-    // elements tid % 8 + 8 q
+    // elements 2 (tid % 8) + 16 q and the next
     float hv[16], m = 0.0f;
     {
-        const int t = tid >> 3, hq = tid & 7;
+        const int t = tid >> 3, hq = 2 * (tid & 7);
         const float *from = sd.h + (t < n ? (int64_t)a.plan.perm[lo + t] * a.rank : 0);
 #pragma unroll
         for (int q = 0; q < 16; q++) {
-            hv[q] = t < n && q < 2 * kb && hq + 8 * q < r ? from[hq + 8 * q] : 0.0f;
+            const int at = hq + 16 * (q >> 1) + (q & 1);
+            hv[q] = t < n && at < r ? from[at] : 0.0f;
             m = fmaxf(m, fabsf(hv[q]));
         }
     }
@@ -369,9 +375,10 @@ template <typename TX> __global__ void __launch_bounds__(256) expand_kernel(cons
     float up, down;
     operand_scale<TX>(m, up, down);
 #pragma unroll
-    for (int q = 0; q < 16; q++)
-        if (q < 2 * kb)
-            split<TX>(__fmul_rn(hv[q], up), sh + (tid >> 3) * hrow + (tid & 7) + 8 * q, kTile * hrow);
+    for (int q = 0; q < 8; q++)
+        if (q < kb)
+            split2<TX>(__fmul_rn(hv[2 * q], up), __fmul_rn(hv[2 * q + 1], up), sh + (tid >> 3) * hrow + 2 * (tid & 7) + 16 * q,
+                       kTile * hrow);
     const uint32_t ha = saddr(smem) + (uint32_t)(((warp & 1) * 16 + (lane & 15)) * hrow + (lane >> 4) * 8) * 2;
     const uint32_t ba = sB + (uint32_t)((lane & 15) * kF + (warp >> 1) * 32 + (lane >> 4) * 8) * 2;
     const bool wide = (((uintptr_t)y | (uintptr_t)(y_stride * 2)) & 15u) == 0;
@@ -431,12 +438,12 @@ template <typename TX> __global__ void __launch_bounds__(256) expand_kernel(cons
 
 // ---- outer: dM_i[r][k] = sum_{t of i} h[t][r] x[t][k] ------------------------------
 // A block takes one adapter, 128 of k (16 a warp) and a share of the adapter's tokens
-// (the blocks of a cluster take turns at its tiles of 32).  Bound by latency: a tile is
-// 8 KB of x and a dozen instructions a warp between two barriers, so that blocks in
-// flight count: room for rank 64 only where that is enough lets three blocks share a
-// SM instead of two, and with twice the split 4096 tokens x (4096 + 4096), four adapters
-// of rank 64, take 42 us instead of 60 (1.6 TB/s of activations read), 1001 tokens 8 us
-// instead of 14.
+// (the blocks of a cluster take turns at its tiles of 32).  Bound by latency (a tile is
+// 8 KB of x and a hundred instructions a warp between two barriers) and by the adapter
+// with the most tokens: blocks in flight count.  Room for rank 64 only, where that is
+// enough, lets three blocks share a SM instead of two; with twice the split, 4096 tokens
+// x (4096 + 4096), four adapters of rank 64, take 38 us instead of 60, 1001 tokens 8
+// instead of 14 (twice the split again: 47 and 13).
 constexpr int kOuterStages = 4;
 constexpr int kXRow = 128 + kPad;
 
@@ -479,8 +486,8 @@ template <typename TX, bool VEC, int MB> __global__ void __launch_bounds__(256, 
         copy_group();
         lookup(s + 1);
     };
-    // h of a tile: token tid / 8, elements tid % 8 + 8 q, in the same way
-    const int ht = tid >> 3, hq = tid & 7;
+    // h of a tile: token tid / 8, elements 2 (tid % 8) + 16 q and the next, in the same way
+    const int ht = tid >> 3, hq = 2 * (tid & 7);
     float hv[2 * MB];
     int hnext;
     auto hlookup = [&](int s) {
@@ -490,9 +497,10 @@ template <typename TX, bool VEC, int MB> __global__ void __launch_bounds__(256, 
     auto fetch = [&](int s) {
         const float *from = sd.h + (int64_t)max(hnext, 0) * a.rank;
 #pragma unroll
-        for (int q = 0; q < 2 * MB; q++)
-            if (q < 2 * mb)
-                hv[q] = hnext >= 0 && hq + 8 * q < r ? from[hq + 8 * q] : 0.0f;
+        for (int q = 0; q < 2 * MB; q++) {
+            const int at = hq + 16 * (q >> 1) + (q & 1);
+            hv[q] = hnext >= 0 && at < r ? from[at] : 0.0f;
+        }
         hlookup(s + 1);
     };
     hlookup(0);
@@ -512,9 +520,9 @@ template <typename TX, bool VEC, int MB> __global__ void __launch_bounds__(256, 
     for (int s = 0; s < mine; s++) {
         TX *const sh = reinterpret_cast<TX *>(smem + kOuterStages * xbytes + (s & 1) * hbytes);
 #pragma unroll
-        for (int q = 0; q < 2 * MB; q++)
-            if (q < 2 * mb)
-                split<TX>(__fmul_rn(hv[q], up), sh + ht * hrow + hq + 8 * q, kTile * hrow);
+        for (int q = 0; q < MB; q++)
+            if (q < mb)
+                split2<TX>(__fmul_rn(hv[2 * q], up), __fmul_rn(hv[2 * q + 1], up), sh + ht * hrow + hq + 16 * q, kTile * hrow);
         copy_wait<kOuterStages - 2>();
         __syncthreads();
         load(s + kOuterStages - 1);
