@@ -400,8 +400,10 @@ EXL3_API exl3_status exl3_regularize(const void *W, int dt, int64_t rows, int64_
  * Arithmetic: the activations are rotated in binary32 and rounded to binary16
  * under an exact power-of-two scale for each row; products with the levels
  * are summed in binary32 (tensor cores, in any order within a sum), rotated
- * and scaled in binary32 and rounded to dt once, with the adapters added
- * before.  Results are the same from run to run.  A row of x that holds an
+ * and scaled in binary32 and rounded to dt once, with the adapters' terms
+ * (binary32 sums) added before; with more than 64 tokens, and in
+ * exl3_linear_backward, these wait in y for that and are rounded to dt, too.
+ * Results are the same from run to run.  A row of x that holds an
  * infinity or a NaN gives no numbers in its own row of y and touches no other.
  */
 EXL3_API size_t exl3_linear_workspace_bytes(int64_t T, int64_t rows, int64_t cols, int transposed,
