@@ -54,6 +54,9 @@ struct PrepLaunch {
     const int32_t *slots, *ranks;
     int n_adapters, rank;
     float *h;                 // [T][rank]
+    // runs beside the kernels launched before it, which neither write what it reads nor
+    // use what it writes, and ends after them (n_adapters == 0)
+    bool beside;
 };
 exl3_status launch_prep(const PrepLaunch &p, cudaStream_t s);
 

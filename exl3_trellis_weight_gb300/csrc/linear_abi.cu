@@ -135,10 +135,13 @@ struct LinearWs {
     }
 };
 
-// y = x W^ (or its transpose), adapters' rank-sided products in h added with B
+// y = x W^ (or its transpose), adapters' rank-sided products in h added with B.
+// beside: kernels of the same call run already (plan and shrink), the rotation runs
+// beside them (they are latency, it is instructions); back: the adapters' way back to y
+// comes between it and the product.
 exl3_status run_linear(const LinearWs &m, const void *x, int dt, int64_t T, int64_t x_stride, const Coded &w, int E,
                        const int32_t *offsets, const void *A, const void *B, float *h, const Adapters &ad, void *y,
-                       int64_t y_stride, cudaStream_t s) {
+                       int64_t y_stride, cudaStream_t s, bool beside = false, const AdaptLaunch *back = nullptr) {
     exl3_status st;
     PrepLaunch a = {};
     a.x = x;
@@ -161,6 +164,7 @@ exl3_status run_linear(const LinearWs &m, const void *x, int dt, int64_t T, int6
     a.n_adapters = A ? ad.n : 0;
     a.rank = ad.rank;
     a.h = h;
+    a.beside = beside;
     ProductLaunch p = {};
     p.image = m.image;
     p.rscale = m.rscale;
@@ -186,6 +190,7 @@ exl3_status run_linear(const LinearWs &m, const void *x, int dt, int64_t T, int6
     const bool few = few_eligible(p);
     a.order = few ? few_order(p) : 0;
     if ((st = launch_prep(a, s)) != EXL3_OK) return st;
+    if (back && (st = launch_expand(*back, y, y_stride, s)) != EXL3_OK) return st;
     return few ? launch_product_few(p, s) : launch_product(p, s);
 }
 
@@ -246,8 +251,7 @@ exl3_status exl3_linear(const void *x, int dt, int64_t T, int64_t x_stride, cons
         if ((st = launch_shrink(p, 1, s)) != EXL3_OK) return st;
         p.side[0].M = B;
         p.side[0].n = (int)w.outputs();
-        if ((st = launch_expand(p, y, y_stride, s)) != EXL3_OK) return st;
-        return run_linear(m, x, dt, T, x_stride, w, 1, nullptr, nullptr, B, nullptr, ad, y, y_stride, s);
+        return run_linear(m, x, dt, T, x_stride, w, 1, nullptr, nullptr, B, nullptr, ad, y, y_stride, s, true, &p);
     }
     return run_linear(m, x, dt, T, x_stride, w, 1, nullptr, A, n_adapters ? B : nullptr, m.h, ad, y, y_stride, s);
 }
@@ -299,9 +303,8 @@ exl3_status exl3_linear_backward(const void *dy, int64_t dy_stride, const void *
         AdaptLaunch q = p;
         q.side[0] = {nullptr, 0, (int)n_in, A, m.g, nullptr, nullptr};
         const bool few = T <= kFewTokens;                 // the coded product adds the adapters' terms itself
-        if (!few && (st = launch_expand(q, dx, dx_stride, s)) != EXL3_OK) return st;
         if ((st = run_linear(m, dy, dt, T, dy_stride, w, 1, nullptr, nullptr, A, few ? m.g : nullptr, ad, dx, dx_stride,
-                             s)) != EXL3_OK)
+                             s, true, few ? nullptr : &q)) != EXL3_OK)
             return st;
     }
     // dA = sum g x^T, dB = sum h dy^T

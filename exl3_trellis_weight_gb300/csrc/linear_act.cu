@@ -130,8 +130,8 @@ __global__ void prep_kernel(const PrepLaunch a) {
     float *const part = parts + (tid >> 5) * (4 * kUnit);
     const int64_t NP = act_rows(a.T);
     // the product kernel behind this one may start on the codes; it waits for this
-    // kernel's end before it reads z.  (This kernel itself starts after everything
-    // before it, so the codes are complete.)
+    // kernel's end before it reads z.  (This kernel itself, or the first of those that it
+    // runs beside, starts after everything before it, so the codes are complete.)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (blockIdx.y > 0) {
         shrink_rows<TX, VEC>(a);
@@ -228,6 +228,10 @@ __global__ void prep_kernel(const PrepLaunch a) {
             rotate_out128(v, a, NP, t, k, in, part, lane);
         }
     }
+    // what follows waits for this kernel only: it may not end before those it runs beside.
+    // One block, the last to start, is enough and keeps no other from its place.
+    if (blockIdx.x == gridDim.x - 1)
+        asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 template <typename TX, bool VEC, bool ONE>
@@ -239,7 +243,19 @@ exl3_status launch_prep_t(const PrepLaunch &p, dim3 grid, unsigned block, cudaSt
         if (e != cudaSuccess)
             return cuda_check(e, "cudaFuncSetAttribute(activation rotation)");
     }
-    prep_kernel<TX, VEC, ONE><<<grid, block, smem, s>>>(p);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = p.beside ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, prep_kernel<TX, VEC, ONE>, p);
+    if (e != cudaSuccess)
+        return cuda_check(e, "activation rotation launch");
     note_launch();
     return cuda_check(cudaGetLastError(), "activation rotation launch");
 }

@@ -401,8 +401,8 @@ EXL3_API exl3_status exl3_regularize(const void *W, int dt, int64_t rows, int64_
  * under an exact power-of-two scale for each row; products with the levels
  * are summed in binary32 (tensor cores, in any order within a sum), rotated
  * and scaled in binary32 and rounded to dt once, with the adapters' terms
- * (binary32 sums) added before; with more than 64 tokens, and in
- * exl3_linear_backward, these wait in y for that and are rounded to dt, too.
+ * (binary32 sums) added before; with more than 64 tokens these wait in y for
+ * that and are rounded to dt, too.
  * Results are the same from run to run.  A row of x that holds an
  * infinity or a NaN gives no numbers in its own row of y and touches no other.
  */
