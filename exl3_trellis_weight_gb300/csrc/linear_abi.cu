@@ -307,7 +307,7 @@ exl3_status exl3_linear_backward(const void *dy, int64_t dy_stride, const void *
                              s, true, few ? nullptr : &q)) != EXL3_OK)
             return st;
     }
-    // dA = sum g x^T, dB = sum h dy^T
+    // dA = sum g x^T, dB = sum h dy^T, beside the product's end
     p.side[0].h = m.g;
     p.side[0].largest = p.plan.largest + ad.n;
     p.side[1].h = m.h;

@@ -449,6 +449,10 @@ template <typename TX> __global__ void __launch_bounds__(256) expand_kernel(cons
 constexpr int kOuterStages = 4;
 constexpr int kXRow = 128 + kPad;
 
+// It needs nothing of the coded product before it and starts on the SMs that the product
+// leaves (1001 tokens in all: 70 us instead of 79; where the product fills the GPU it
+// makes no difference): the product lets it go once its own wait has passed, so that h and the plan are
+// complete (and are read past L1, which a kernel that has not waited may find stale).
 // MB: sixteens of rows at most (4 up to rank 64: fewer registers, three blocks a SM)
 template <typename TX, bool VEC, int MB> __global__ void __launch_bounds__(256, MB == 4 ? 3 : 2) outer_kernel(const AdaptLaunch a) {
     extern __shared__ __align__(16) unsigned char smem[];
@@ -459,12 +463,12 @@ template <typename TX, bool VEC, int MB> __global__ void __launch_bounds__(256, 
     chunk -= side ? a.side[0].n / 128 : 0;
     const AdaptSide &sd = a.side[side];
     const int r = rank_of(a.ranks, i, a.rank), R16 = (a.rank + 15) / 16 * 16, mb = (r + 15) / 16;
-    const int lo = a.plan.seg[i], n = a.plan.seg[i + 1] - lo;
+    const int lo = __ldcg(a.plan.seg + i), n = __ldcg(a.plan.seg + i + 1) - lo;
     const int hrow = R16 + kPad;
     const uint32_t base = saddr(smem), xbytes = kTile * kXRow * 2, hlow = (uint32_t)(kTile * hrow) * 2, hbytes = 2 * hlow;
     const uint32_t hbase = base + kOuterStages * xbytes;
     float up, down;
-    operand_scale<TX>(__uint_as_float(sd.largest[i]), up, down);
+    operand_scale<TX>(__uint_as_float(__ldcg(sd.largest + i)), up, down);
     const int tiles = (n + kTile - 1) / kTile;
     const int mine = r > 0 && tiles > rank ? (tiles - 1 - rank) / a.split + 1 : 0;
     const uint16_t *x = reinterpret_cast<const uint16_t *>(sd.x) + chunk * 128;
@@ -476,7 +480,7 @@ template <typename TX, bool VEC, int MB> __global__ void __launch_bounds__(256, 
 #pragma unroll
         for (int b = 0; b < 2; b++) {
             const int t = (rank + s * a.split) * kTile + row + 16 * b;
-            next[b] = s < mine && t < n ? a.plan.perm[lo + t] : -1;
+            next[b] = s < mine && t < n ? __ldcg(a.plan.perm + lo + t) : -1;
         }
     };
     auto load = [&](int s) {
@@ -490,18 +494,25 @@ template <typename TX, bool VEC, int MB> __global__ void __launch_bounds__(256, 
     };
     // h of a tile: token tid / 8, elements 2 (tid % 8) + 16 q and the next, in the same way
     const int ht = tid >> 3, hq = 2 * (tid & 7);
+    const bool pairs = a.rank % 2 == 0;
     float hv[2 * MB];
     int hnext;
     auto hlookup = [&](int s) {
         const int t = (rank + s * a.split) * kTile + ht;
-        hnext = s < mine && t < n ? a.plan.perm[lo + t] : -1;
+        hnext = s < mine && t < n ? __ldcg(a.plan.perm + lo + t) : -1;
     };
     auto fetch = [&](int s) {
         const float *from = sd.h + (int64_t)max(hnext, 0) * a.rank;
 #pragma unroll
-        for (int q = 0; q < 2 * MB; q++) {
-            const int at = hq + 16 * (q >> 1) + (q & 1);
-            hv[q] = hnext >= 0 && at < r ? from[at] : 0.0f;
+        for (int q = 0; q < MB; q++) {
+            const int at = hq + 16 * q;
+            if (pairs) {                   // (rows behind r hold zeros)
+                const float2 f = hnext >= 0 && at < r ? __ldcg(reinterpret_cast<const float2 *>(from + at)) : make_float2(0.0f, 0.0f);
+                hv[2 * q] = f.x, hv[2 * q + 1] = f.y;
+            } else {
+                hv[2 * q] = hnext >= 0 && at < r ? __ldcg(from + at) : 0.0f;
+                hv[2 * q + 1] = hnext >= 0 && at + 1 < r ? __ldcg(from + at + 1) : 0.0f;
+            }
         }
         hlookup(s + 1);
     };
@@ -581,6 +592,9 @@ template <typename TX, bool VEC, int MB> __global__ void __launch_bounds__(256, 
     }
     if (a.split > 1)
         cluster_sync();
+    // the last block to start keeps the grid from ending before the product
+    if (blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1)
+        asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // early: the launch may overlap the end of the one before it, whose results the kernel
@@ -686,7 +700,7 @@ exl3_status launch_outer(const AdaptLaunch &p0, cudaStream_t s) {
     const size_t part = (size_t)R16 * 132 * 4, smem = stages > part ? stages : part;
     const dim3 grid((unsigned)((p.side[0].n + p.side[1].n) / 128 * p.split), (unsigned)p.n);
     const bool vec = wide_rows(p.side[0]) && wide_rows(p.side[1]);
-    auto go = [&](auto k) { return launch("adapter gradient launch", k, grid, 256, smem, (unsigned)p.split, false, s, p); };
+    auto go = [&](auto k) { return launch("adapter gradient launch", k, grid, 256, smem, (unsigned)p.split, p.T > 0, s, p); };
     if (p.rank > 64) {
         if (p.dt == EXL3_BF16)
             return vec ? go(outer_kernel<__nv_bfloat16, true, 8>) : go(outer_kernel<__nv_bfloat16, false, 8>);

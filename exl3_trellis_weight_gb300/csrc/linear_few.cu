@@ -205,6 +205,7 @@ __global__ void __launch_bounds__(kThreadsF, 2) few_kernel(const __grid_constant
         for (int i = lane; i < 128; i += 32)
             right[i] = __fmul_rn(__ldg(p.right + (size_t)tl.e * a.n_out + tl.f0 + i), __fmul_rn(__ldg(p.scale + tl.e), 0x1p-7f));
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");       // (the adapters' gradients)
     if (warp == 1) {
         // activations of the block's inputs: NB * 8 token rows of each block of 64
         if (lane == 0)

@@ -309,6 +309,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) product_kernel(const __grid_cons
         const int f4 = 8 * ow + (lane >> 2), col = 4 * out_at(f4) + (lane & 3);
         const int col0 = 4 * swz(f4, 0) + (lane & 3), col1 = 4 * swz(f4, 1) + (lane & 3);
         asm volatile("griddepcontrol.wait;" ::: "memory");
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // (the adapters' gradients)
         uint32_t acc = 0;
         bool ok = true;
         const bool wide_y = (((uintptr_t)a.p.y | (uintptr_t)(a.p.y_stride * 2)) & 15u) == 0;
