@@ -319,7 +319,8 @@ template <typename TX, bool VEC, int MB> __global__ void __launch_bounds__(256, 
 
 // ---- expand: y[t] = sum_r h[t][r] M_i[r], which the coded product adds to ------------
 // (rounded to y's type on the way: in 32 bits it would need a buffer twice as large, read
-// and written once more, for half a last place of a term of the sum).
+// and written once more, for half a last place of a term of the sum: 0.0020 instead of
+// 0.0017 relative error in bf16 where the adapters make a large part of the result).
 // A block takes one tile and 512 outputs, 128 at a time; warp w the tokens 16 (w % 2) ..
 // and 32 of the outputs.  Bound by instructions (2.6 of 4 a cycle): 4096 x 4096, rank
 // 16: 15 us, 2.2 TB/s written.
