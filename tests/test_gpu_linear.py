@@ -464,6 +464,54 @@ def test_capture_in_a_graph(ex):
     assert torch.equal(kw["out"], want)
 
 
+def test_calls_back_to_back_in_one_workspace(ex):
+    """A call's kernels overlap one another, not those of the calls around it."""
+    g = gen(45)
+    codes, su, sv, scale = coded(g, 512, 1024, 3)
+    A, B, gain, ranks = adapters(g, 5, 48, 512, 1024, "bf16")
+    T = 700
+    sets = []
+    for _ in range(3):
+        x, dy = acts(g, T, 512, "bf16"), acts(g, T, 1024, "bf16")
+        slots = torch.randint(-1, 5, (T,), generator=g, device=DEV, dtype=torch.int32)
+        sets.append((x, dy, dict(A=A, B=B, gain=gain, slots=slots, ranks=ranks)))
+    ws = torch.empty(ex.linear_backward_workspace_bytes(T, 512, 1024, False, 5, 48), dtype=torch.uint8, device=DEV)
+
+    def call(x, dy, kw):
+        return [ex.linear(x, codes, su, sv, 3, scale, ws=ws, **kw),
+                *ex.linear_backward(dy, x, codes, su, sv, 3, scale, ws=ws, **kw).values()]
+
+    want = []
+    for s in sets:
+        want.append(call(*s))
+        torch.cuda.synchronize()
+    got = [call(*sets[i % 3]) for i in range(30)]
+    for i, outs in enumerate(got):
+        for p, q in zip(outs, want[i % 3]):
+            assert torch.equal(p, q)
+
+
+def test_backward_capture_in_a_graph(ex):
+    g = gen(46)
+    codes, su, sv, scale = coded(g, 256, 384, 2)
+    A, B, gain, ranks = adapters(g, 4, 16, 256, 384, "fp16")
+    for T in (20, 200):
+        x, dy = acts(g, T, 256, "fp16"), acts(g, T, 384, "fp16")
+        slots = torch.randint(-1, 4, (T,), generator=g, device=DEV, dtype=torch.int32)
+        kw = dict(A=A, B=B, gain=gain, slots=slots, ranks=ranks)
+        want = ex.linear_backward(dy, x, codes, su, sv, 2, scale, **kw)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = ex.linear_backward(dy, x, codes, su, sv, 2, scale, **kw)
+        for _ in range(3):
+            for t in got.values():
+                t.fill_(7.0)
+            graph.replay()
+            torch.cuda.synchronize()
+            for k in want:
+                assert torch.equal(got[k], want[k])
+
+
 def test_the_example_runs():
     import importlib.util
     import os
