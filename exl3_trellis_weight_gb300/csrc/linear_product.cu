@@ -343,7 +343,9 @@ __global__ void __launch_bounds__(kThreadsP, 1) product_kernel(const __grid_cons
             for (int n0 = 0; ok && n0 < tl.n; n0 += kN, acc++) {
                 const int d = acc & 1;
                 ok = bar_wait(acc_full(d), (acc >> 1) & 1, &gave_up, count);
-                ok = __all_sync(0xffffffffu, ok);
+                // the group goes on as a whole or not at all: another wait of the block may have
+                // given up while this phase ended, and a warp that left would be missing below
+                ok = bar_all(1 + og, 128, __all_sync(0xffffffffu, ok));
                 if (!ok)
                     break;
                 fence_after();

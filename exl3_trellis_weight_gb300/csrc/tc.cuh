@@ -59,6 +59,16 @@ static __device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity,
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *gave_up, unsigned int *count) {
     return bar_test(bar, parity) || bar_wait_slow(bar, parity, gave_up, count);
 }
+// whether `ok` holds in all `threads` threads that meet at named barrier `name`
+__device__ __forceinline__ bool bar_all(int name, int threads, bool ok) {
+    uint32_t all;
+    asm volatile("{\n\t.reg .pred p, q;\n\t"
+                 "setp.ne.b32 p, %1, 0;\n\t"
+                 "barrier.cta.red.and.aligned.pred q, %2, %3, p;\n\t"
+                 "selp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(all) : "r"((uint32_t)ok), "r"(name), "r"(threads) : "memory");
+    return all != 0u;
+}
 // Waits for a phase, as long at most, whatever other waits did (the way out
 // after one gave up: nothing may be in flight when the block ends).
 __device__ __forceinline__ void bar_drain(uint32_t bar, uint32_t parity) {
