@@ -10,6 +10,7 @@
 #include <vector>
 
 #include "common.cuh"
+#include "smem_limit.cuh"
 
 namespace exl3 {
 
@@ -48,18 +49,15 @@ int device_sm_count() {
     return n;
 }
 
-cudaError_t allow_smem(const void *kernel, size_t bytes, SmemAllowed &allowed) {
+cudaError_t allow_smem(const void *kernel, size_t bytes) {
+    static SmemLimits &limits = *new SmemLimits;   // (kept to the end: threads may still launch then)
     int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    const cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
         return e;
-    const bool slot = dev >= 0 && dev < 64;
-    if (slot && allowed.bytes[dev].load(std::memory_order_relaxed) >= (int)bytes)
-        return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e == cudaSuccess && slot)
-        allowed.bytes[dev].store((int)bytes, std::memory_order_relaxed);
-    return e;
+    return (cudaError_t)limits.raise(kernel, dev, (int)bytes, [&] {
+        return (int)cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    });
 }
 
 // ---- profiling ----------------------------------------------------------------

@@ -10,8 +10,6 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
-#include <atomic>
-
 #include "../../include/exl3.h"
 
 namespace exl3 {
@@ -142,12 +140,8 @@ constexpr size_t kEncodeBlockScratchBytes =
 exl3_status set_error(exl3_status st, const char *fmt, ...);
 exl3_status cuda_check(cudaError_t e, const char *what);
 int device_sm_count();
-// lets `kernel` use `bytes` of dynamic shared memory, set once for each device and size
-// (a static SmemAllowed for each kernel): the call takes a microsecond
-struct SmemAllowed {
-    std::atomic<int> bytes[64];
-};
-cudaError_t allow_smem(const void *kernel, size_t bytes, SmemAllowed &allowed);
+// lets `kernel` use at least `bytes` of dynamic shared memory on the current device
+cudaError_t allow_smem(const void *kernel, size_t bytes);
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 

@@ -237,9 +237,8 @@ __global__ void prep_kernel(const PrepLaunch a) {
 template <typename TX, bool VEC, bool ONE>
 exl3_status launch_prep_t(const PrepLaunch &p, dim3 grid, unsigned block, cudaStream_t s) {
     const size_t smem = (size_t)(block / 32) * 4 * kUnit * sizeof(float);
-    static SmemAllowed allowed;
     if (smem > 40 * 1024) {
-        const cudaError_t e = allow_smem((const void *)prep_kernel<TX, VEC, ONE>, smem, allowed);
+        const cudaError_t e = allow_smem((const void *)prep_kernel<TX, VEC, ONE>, smem);
         if (e != cudaSuccess)
             return cuda_check(e, "cudaFuncSetAttribute(activation rotation)");
     }

@@ -604,7 +604,7 @@ template <typename... P, typename... A>
 exl3_status launch(const char *what, void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, unsigned cluster,
                    bool early, cudaStream_t s, A... args) {
     if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        const cudaError_t e = allow_smem((const void *)kernel, smem);
         if (e != cudaSuccess)
             return cuda_check(e, what);
     }

@@ -327,8 +327,7 @@ __global__ void __launch_bounds__(kThreadsF, 2) few_kernel(const __grid_constant
 
 template <int K, bool TR, int NB, typename TY>
 exl3_status launch_few_form(const FewArgs &a, unsigned grid, uint32_t smem, cudaStream_t s) {
-    static SmemAllowed allowed;
-    cudaError_t e = allow_smem((const void *)few_kernel<K, TR, NB, TY>, smem, allowed);
+    cudaError_t e = allow_smem((const void *)few_kernel<K, TR, NB, TY>, smem);
     if (e != cudaSuccess)
         return cuda_check(e, "cudaFuncSetAttribute(coded product, few tokens)");
     cudaLaunchConfig_t cfg = {};

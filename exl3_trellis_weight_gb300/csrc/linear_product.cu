@@ -576,8 +576,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) product_kernel(const __grid_cons
 
 template <int K, bool PAIR, typename TY> exl3_status launch_form(const Args &a, unsigned grid, unsigned cluster, cudaStream_t s) {
     static_assert(kSmem <= 227 * 1024 - 1536, "shared memory of one block");
-    static SmemAllowed allowed;
-    cudaError_t e = allow_smem((const void *)product_kernel<K, PAIR, TY>, kSmem, allowed);
+    cudaError_t e = allow_smem((const void *)product_kernel<K, PAIR, TY>, kSmem);
     if (e != cudaSuccess)
         return cuda_check(e, "cudaFuncSetAttribute(coded product)");
     cudaLaunchConfig_t cfg = {};
