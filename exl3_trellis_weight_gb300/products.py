@@ -16,6 +16,7 @@ _fn = None
 # the current stream's handle, without a Stream object around it (a microsecond)
 _stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _lib():
@@ -28,6 +29,18 @@ def _lib():
 def _fail(status: int):
     L = _lib()
     raise Exl3Error(status, f"{L.exl3_status_str(status).decode()}: {L.exl3_last_error().decode()}")
+
+
+def _call(entry, index, *args):
+    """The entry point with CUDA device ``index`` current: the library launches on the
+    current device, which need not be the tensors'."""
+    if _current_device() == index:
+        st = entry(*args)
+    else:
+        with torch.cuda.device(index):
+            st = entry(*args)
+    if st:
+        _fail(st)
 
 
 def linear_workspace_bytes(T: int, rows: int, cols: int, transposed: bool = False, n_adapters: int = 0,
@@ -114,6 +127,8 @@ def _ws(need, device, ws):
         return torch.empty(max(need, 256), dtype=torch.uint8, device=device)
     if not ws.is_cuda or not ws.is_contiguous():
         raise ValueError("the workspace must be a contiguous CUDA tensor")
+    if ws.get_device() != device.index:
+        raise ValueError(f"the workspace must be on CUDA device {device.index}, as the other tensors")
     return ws
 
 
@@ -141,11 +156,8 @@ def linear(x, codes, su, sv, K: int, scale, transposed: bool = False, A=None, B=
     L = _lib()
     tr = 1 if transposed else 0
     ws = _ws(L.exl3_linear_workspace_bytes(T, rows, cols, tr, n, r), dev, ws)
-    st = L.exl3_linear(x.data_ptr(), _DT[x.dtype], T, xs, pc, rows, cols, K, pu, pv, ps, tr, pA, pB, pg, pslots,
-                       pranks, n, r, out.data_ptr(), ys, ws.data_ptr(), ws.numel() * ws.element_size(),
-                       _stream(dev.index))
-    if st:
-        _fail(st)
+    _call(L.exl3_linear, dev.index, x.data_ptr(), _DT[x.dtype], T, xs, pc, rows, cols, K, pu, pv, ps, tr, pA, pB, pg,
+          pslots, pranks, n, r, out.data_ptr(), ys, ws.data_ptr(), ws.numel() * ws.element_size(), _stream(dev.index))
     return out
 
 
@@ -176,12 +188,9 @@ def linear_backward(dy, x, codes, su, sv, K: int, scale, transposed: bool = Fals
     L = _lib()
     tr = 1 if transposed else 0
     ws = _ws(L.exl3_linear_backward_workspace_bytes(T, rows, cols, tr, n, r), dev, ws)
-    st = L.exl3_linear_backward(dy.data_ptr(), dys, px, xs, _DT[dy.dtype], T, pc, rows, cols, K, pu, pv, ps, tr, pA,
-                                pB, pg, pslots, pranks, n, r, dx.data_ptr(), dxs, dA.data_ptr() if n else None,
-                                dB.data_ptr() if n else None, ws.data_ptr(), ws.numel() * ws.element_size(),
-                                _stream(dev.index))
-    if st:
-        _fail(st)
+    _call(L.exl3_linear_backward, dev.index, dy.data_ptr(), dys, px, xs, _DT[dy.dtype], T, pc, rows, cols, K, pu, pv,
+          ps, tr, pA, pB, pg, pslots, pranks, n, r, dx.data_ptr(), dxs, dA.data_ptr() if n else None,
+          dB.data_ptr() if n else None, ws.data_ptr(), ws.numel() * ws.element_size(), _stream(dev.index))
     return dict(dx=dx, dA=dA, dB=dB)
 
 
@@ -208,9 +217,6 @@ def expert_linear(x, offsets, codes, su, sv, K: int, scale, transposed: bool = F
     L = _lib()
     tr = 1 if transposed else 0
     ws = _ws(L.exl3_expert_linear_workspace_bytes(T, rows, cols, tr), dev, ws)
-    st = L.exl3_expert_linear(x.data_ptr(), _DT[x.dtype], T, xs, po, E, pc, rows, cols, K, pu, pv, ps, tr,
-                              out.data_ptr(), ys, ws.data_ptr(), ws.numel() * ws.element_size(),
-                              _stream(dev.index))
-    if st:
-        _fail(st)
+    _call(L.exl3_expert_linear, dev.index, x.data_ptr(), _DT[x.dtype], T, xs, po, E, pc, rows, cols, K, pu, pv, ps, tr,
+          out.data_ptr(), ys, ws.data_ptr(), ws.numel() * ws.element_size(), _stream(dev.index))
     return out
