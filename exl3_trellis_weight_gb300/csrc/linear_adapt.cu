@@ -11,8 +11,9 @@
 // h = gain A x is kept in binary32.  Where it becomes an operand again it is split
 // into two of the activations' type, the second the rounding error of the first, and
 // both are multiplied (one alone cost half as much again in the results' error);
-// binary16 gets a power of two for each tile (expand) or adapter (outer) first, so
-// that its range does not matter.
+// binary16 gets a power of two first, for each token where a token has its own sums
+// (expand: nothing of one token touches another's), for each adapter where its tokens
+// are summed up (outer), so that its range does not matter.
 #include "linear.cuh"
 #include "tc.cuh"
 
@@ -77,7 +78,8 @@ __device__ __forceinline__ void load_n(uint32_t addr, uint32_t (&r)[4]) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
 }
 
-// the power of two that takes m to [2^7, 2^8); none for bfloat16, whose range is binary32's
+// the power of two that takes m to [2^7, 2^8); none for bfloat16, whose range is binary32's,
+// nor for an infinite m (its results are not numbers anyway)
 template <typename TX> __device__ __forceinline__ void operand_scale(float m, float &up, float &down) {
     up = down = 1.0f;
     if (__is_same(TX, __half) && m > 0.0f && m < 3.0e38f) {
@@ -326,7 +328,7 @@ template <typename TX, bool VEC, int MB> __global__ void __launch_bounds__(256, 
 // 16: 15 us, 2.2 TB/s written.
 template <typename TX> __global__ void __launch_bounds__(256) expand_kernel(const AdaptLaunch a, void *y, int64_t y_stride) {
     extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ float wmax[8];
+    __shared__ float downs[kTile];
     const AdaptSide &sd = a.side[0];       // h and its way back: M is [rank][n], n outputs
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, j = lane & 3;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -352,7 +354,7 @@ template <typename TX> __global__ void __launch_bounds__(256) expand_kernel(cons
         copy_group();
     };
     load(f_lo, 0);
-    // h of the tile in the operand's type, scaled by a power of two: token tid / 8,
+    // h of the tile in the operand's type, each token under its power of two: token tid / 8,
     // elements 2 (tid % 8) + 16 q and the next
     float hv[16], m = 0.0f;
     {
@@ -366,17 +368,12 @@ template <typename TX> __global__ void __launch_bounds__(256) expand_kernel(cons
         }
     }
 #pragma unroll
-    for (int d = 16; d; d >>= 1)
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    if (lane == 0)
-        wmax[warp] = m;
-    __syncthreads();
-    m = wmax[lane & 7];
-#pragma unroll
     for (int d = 4; d; d >>= 1)
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
     float up, down;
     operand_scale<TX>(m, up, down);
+    if ((tid & 7) == 0)
+        downs[tid >> 3] = down;            // (read behind the barriers of the first outputs)
 #pragma unroll
     for (int q = 0; q < 8; q++)
         if (q < kb)
@@ -419,9 +416,11 @@ template <typename TX> __global__ void __launch_bounds__(256) expand_kernel(cons
 #pragma unroll
         for (int b = 0; b < 4; b++)
 #pragma unroll
-            for (int e = 0; e < 4; e += 2)
-                *reinterpret_cast<uint32_t *>(so + ((warp & 1) * 16 + g + 4 * e) * kF + (warp >> 1) * 32 + b * 8 + 2 * j) =
-                    pack2<TX>(__fmul_rn(acc[b][e], down), __fmul_rn(acc[b][e + 1], down));
+            for (int e = 0; e < 4; e += 2) {
+                const int t = (warp & 1) * 16 + g + 4 * e;
+                *reinterpret_cast<uint32_t *>(so + t * kF + (warp >> 1) * 32 + b * 8 + 2 * j) =
+                    pack2<TX>(__fmul_rn(acc[b][e], downs[t]), __fmul_rn(acc[b][e + 1], downs[t]));
+            }
         __syncthreads();
 #pragma unroll
         for (int h = 0; h < 2; h++) {
