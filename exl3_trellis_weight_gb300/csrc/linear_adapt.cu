@@ -78,14 +78,15 @@ __device__ __forceinline__ void load_n(uint32_t addr, uint32_t (&r)[4]) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
 }
 
-// the power of two that takes m to [2^7, 2^8); none for bfloat16, whose range is binary32's,
-// nor for an infinite m (its results are not numbers anyway)
+// the power of two that takes m to [2^14, 2^15), from where binary16 holds values down to
+// 2^-29 of m at its full 11 bits; none for bfloat16, whose range is binary32's, nor for an
+// infinite m (its results are not numbers anyway)
 template <typename TX> __device__ __forceinline__ void operand_scale(float m, float &up, float &down) {
     up = down = 1.0f;
     if (__is_same(TX, __half) && m > 0.0f && m < 3.0e38f) {
         const int e = max((int)(__float_as_uint(m) >> 23) - 127, -100);
-        up = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
-        down = __uint_as_float((uint32_t)(127 - 7 + e) << 23);
+        up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+        down = __uint_as_float((uint32_t)(127 - 14 + e) << 23);
     }
 }
 

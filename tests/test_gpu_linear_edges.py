@@ -45,3 +45,25 @@ def test_adapters_of_a_token_do_not_depend_on_its_neighbours(ex):
         rest[[5, 33]] = False
         assert torch.equal(z[rest], y[rest])
         assert not torch.isfinite(z[~rest]).any()
+
+
+def test_gradients_of_small_sums_beside_large_ones(ex):
+    """float16: an adapter's token with sums ten million times those of its others, and a
+    gradient that is 0 in half of the columns: there the others are all there is."""
+    g = gen(55)
+    T = 90
+    codes, su, sv, scale = coded(g, 256, 384, 2)
+    x, dy = torch.randn(T, 256, generator=g, device=DEV) * 1e-3, torch.randn(T, 384, generator=g, device=DEV)
+    x[4] *= 1e7
+    dy[4, ::2] = 0
+    x, dy = x.half(), dy.half()
+    A = torch.randn(1, 6, 256, generator=g, device=DEV).half()
+    B = (0.1 * torch.randn(1, 6, 384, generator=g, device=DEV)).half()
+    slots = torch.zeros(T, dtype=torch.int32, device=DEV)
+    got = ex.linear_backward(dy, x, codes, su, sv, 2, scale, A=A, B=B, gain=torch.ones(1, device=DEV), slots=slots)
+    h = x.double() @ A[0].double().t()
+    ref, e = h.t() @ dy.double(), (h.pow(2).t() @ dy.double().pow(2)).sqrt()
+    tol = U["fp16"] * ref.abs() + 2.0 ** -25 + 6 * U["fp16"] / math.sqrt(3) * e
+    live = torch.arange(384, device=DEV) % 2 == 0
+    assert (ref[:, live].abs() < 10).all()
+    assert ((got["dB"][0].double() - ref).abs() <= tol)[:, live].all()
