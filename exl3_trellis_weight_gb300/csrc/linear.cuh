@@ -72,10 +72,11 @@ struct ProductLaunch {
     int transposed;
     const int32_t *offsets;   // [E + 1] or nullptr
     int E;                    // 1 when offsets == nullptr
-    // adapters: h != nullptr adds sum_j h[t][j] B[slot_t][j] to the result; h == nullptr
-    // adds what y holds of tokens with an adapter (launch_expand)
+    // adapters: B != nullptr adds sum_j h[t][j] B[slot_t][j] to the result; term != nullptr
+    // adds its rows of tokens with an adapter (launch_expand)
     const void *B;            // nullable, [n_adapters][rank][outputs], dtype dt
-    const float *h;           // nullable, [T][rank]
+    const float *h;           // [T][rank]
+    const float *term;        // nullable, [T][outputs], 16-byte aligned
     const int32_t *slots;     // [T]
     const int32_t *ranks;     // nullable, [n_adapters]
     int n_adapters, rank;
@@ -123,8 +124,8 @@ struct AdaptLaunch {
 exl3_status launch_adapt_plan(const AdaptLaunch &p, cudaStream_t s);
 // sides 0 .. sides - 1: h[t] = gain_i M_i x_t
 exl3_status launch_shrink(const AdaptLaunch &p, int sides, cudaStream_t s);
-// y[t] = sum_r h[t][r] M_i[r] with side 0's h and M (n outputs); rows without an adapter stay
-exl3_status launch_expand(const AdaptLaunch &p, void *y, int64_t y_stride, cudaStream_t s);
+// term[t] = sum_r h[t][r] M_i[r] with side 0's h and M (n outputs); rows without an adapter stay
+exl3_status launch_expand(const AdaptLaunch &p, float *term, cudaStream_t s);
 // both sides: dM_i[r] = sum_{t of i} h[t][r] x_t
 exl3_status launch_outer(const AdaptLaunch &p, cudaStream_t s);
 

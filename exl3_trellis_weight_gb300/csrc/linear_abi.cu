@@ -118,27 +118,38 @@ exl3_status check_ws(const void *ws, size_t have, size_t want) {
     return EXL3_OK;
 }
 
+// up to here each token's adapter is multiplied on its own (rotation and coded product
+// carry it along); with more the tokens are sorted by adapter and multiplied in tiles
+constexpr int64_t kFewTokens = 64;
+
 struct LinearWs {
     unsigned char *image;     // rotated activations
     float *rscale;            // [T]
     float *h, *g;             // [T][rank]: x A^T and, for the gradient, dy B^T
     int32_t *plan;            // tokens by adapter
+    float *term;              // [T][outputs]: the adapters' part of the result
     size_t bytes;
-    LinearWs(void *ws, int64_t T, int64_t inputs, int n, int rank, bool grad) {
+    LinearWs(void *ws, int64_t T, int64_t inputs, int64_t outputs, int n, int rank, bool grad) {
         Carve c{(unsigned char *)ws};
         image = c.take<unsigned char>((size_t)act_rows(T) * inputs * 2);
         rscale = c.take<float>((size_t)T);
         h = n ? c.take<float>((size_t)T * rank) : nullptr;
         g = n && grad ? c.take<float>((size_t)T * rank) : nullptr;
         plan = n ? c.take<int32_t>(adapt_plan_ints(T, n)) : nullptr;
+        term = n && T > kFewTokens ? c.take<float>((size_t)T * outputs) : nullptr;
         bytes = c.used;
+        // one workspace of the gradients' size serves both directions of a layer
+        if (grad) {
+            const size_t forward = LinearWs(nullptr, T, outputs, inputs, n, rank, false).bytes;
+            bytes = bytes > forward ? bytes : forward;
+        }
     }
 };
 
 // y = x W^ (or its transpose), adapters' rank-sided products in h added with B.
 // beside: kernels of the same call run already (plan and shrink), the rotation runs
-// beside them (they are latency, it is instructions); back: the adapters' way back to y
-// comes between it and the product.
+// beside them (they are latency, it is instructions); back: the adapters' way back, to
+// m.term, comes between it and the product.
 exl3_status run_linear(const LinearWs &m, const void *x, int dt, int64_t T, int64_t x_stride, const Coded &w, int E,
                        const int32_t *offsets, const void *A, const void *B, float *h, const Adapters &ad, void *y,
                        int64_t y_stride, cudaStream_t s, bool beside = false, const AdaptLaunch *back = nullptr) {
@@ -180,6 +191,7 @@ exl3_status run_linear(const LinearWs &m, const void *x, int dt, int64_t T, int6
     p.E = E;
     p.B = B;
     p.h = h;
+    p.term = back ? m.term : nullptr;
     p.slots = ad.slots;
     p.ranks = ad.ranks;
     p.n_adapters = ad.n;
@@ -190,7 +202,7 @@ exl3_status run_linear(const LinearWs &m, const void *x, int dt, int64_t T, int6
     const bool few = few_eligible(p);
     a.order = few ? few_order(p) : 0;
     if ((st = launch_prep(a, s)) != EXL3_OK) return st;
-    if (back && (st = launch_expand(*back, y, y_stride, s)) != EXL3_OK) return st;
+    if (back && (st = launch_expand(*back, m.term, s)) != EXL3_OK) return st;
     return few ? launch_product_few(p, s) : launch_product(p, s);
 }
 
@@ -207,10 +219,6 @@ AdaptLaunch adapt_of(const LinearWs &m, int dt, int64_t T, const Adapters &ad) {
     return p;
 }
 
-// up to here each token's adapter is multiplied on its own (rotation and coded product
-// carry it along); with more the tokens are sorted by adapter and multiplied in tiles
-constexpr int64_t kFewTokens = 64;
-
 bool sizes_ok(int64_t T, int64_t rows, int64_t cols, int n, int rank) {
     return T >= 0 && T <= kMaxTokens && side_ok(rows) && side_ok(cols) && adapters_ok(n, rank);
 }
@@ -222,7 +230,7 @@ extern "C" {
 size_t exl3_linear_workspace_bytes(int64_t T, int64_t rows, int64_t cols, int transposed, int n_adapters, int rank) {
     if (!sizes_ok(T, rows, cols, n_adapters, rank))
         return 0;
-    return LinearWs(nullptr, T, transposed ? cols : rows, n_adapters, rank, false).bytes;
+    return LinearWs(nullptr, T, transposed ? cols : rows, transposed ? rows : cols, n_adapters, rank, false).bytes;
 }
 
 exl3_status exl3_linear(const void *x, int dt, int64_t T, int64_t x_stride, const uint16_t *codes, int64_t rows,
@@ -240,7 +248,7 @@ exl3_status exl3_linear(const void *x, int dt, int64_t T, int64_t x_stride, cons
     if ((st = check_apart(yr, "y", x, xr.bytes(), "x")) != EXL3_OK) return st;
     if (T == 0)
         return EXL3_OK;
-    const LinearWs m(ws, T, w.inputs(), n_adapters, rank, false);
+    const LinearWs m(ws, T, w.inputs(), w.outputs(), n_adapters, rank, false);
     if ((st = check_ws(ws, ws_bytes, m.bytes)) != EXL3_OK) return st;
     if ((st = check_apart(yr, "y", ws, m.bytes, "the workspace")) != EXL3_OK) return st;
     const cudaStream_t s = (cudaStream_t)stream;
@@ -251,7 +259,7 @@ exl3_status exl3_linear(const void *x, int dt, int64_t T, int64_t x_stride, cons
         if ((st = launch_shrink(p, 1, s)) != EXL3_OK) return st;
         p.side[0].M = B;
         p.side[0].n = (int)w.outputs();
-        return run_linear(m, x, dt, T, x_stride, w, 1, nullptr, nullptr, B, nullptr, ad, y, y_stride, s, true, &p);
+        return run_linear(m, x, dt, T, x_stride, w, 1, nullptr, nullptr, nullptr, nullptr, ad, y, y_stride, s, true, &p);
     }
     return run_linear(m, x, dt, T, x_stride, w, 1, nullptr, A, n_adapters ? B : nullptr, m.h, ad, y, y_stride, s);
 }
@@ -260,7 +268,7 @@ size_t exl3_linear_backward_workspace_bytes(int64_t T, int64_t rows, int64_t col
                                             int rank) {
     if (!sizes_ok(T, rows, cols, n_adapters, rank))
         return 0;
-    return LinearWs(nullptr, T, transposed ? rows : cols, n_adapters, rank, true).bytes;
+    return LinearWs(nullptr, T, transposed ? rows : cols, transposed ? cols : rows, n_adapters, rank, true).bytes;
 }
 
 exl3_status exl3_linear_backward(const void *dy, int64_t dy_stride, const void *x, int64_t x_stride, int dt, int64_t T,
@@ -288,7 +296,7 @@ exl3_status exl3_linear_backward(const void *dy, int64_t dy_stride, const void *
     if ((st = check_apart(dxr, "dx", dy, dyr.bytes(), "dy")) != EXL3_OK) return st;
     if (T == 0 && n_adapters == 0)
         return EXL3_OK;
-    const LinearWs m(ws, T, n_out, n_adapters, rank, true);
+    const LinearWs m(ws, T, n_out, n_in, n_adapters, rank, true);
     if ((st = check_ws(ws, ws_bytes, m.bytes)) != EXL3_OK) return st;
     if ((st = check_apart(dxr, "dx", ws, m.bytes, "the workspace")) != EXL3_OK) return st;
     const cudaStream_t s = (cudaStream_t)stream;
@@ -303,8 +311,8 @@ exl3_status exl3_linear_backward(const void *dy, int64_t dy_stride, const void *
         AdaptLaunch q = p;
         q.side[0] = {nullptr, 0, (int)n_in, A, m.g, nullptr, nullptr};
         const bool few = T <= kFewTokens;                 // the coded product adds the adapters' terms itself
-        if ((st = run_linear(m, dy, dt, T, dy_stride, w, 1, nullptr, nullptr, A, few ? m.g : nullptr, ad, dx, dx_stride,
-                             s, true, few ? nullptr : &q)) != EXL3_OK)
+        if ((st = run_linear(m, dy, dt, T, dy_stride, w, 1, nullptr, nullptr, few ? A : nullptr, few ? m.g : nullptr, ad,
+                             dx, dx_stride, s, true, few ? nullptr : &q)) != EXL3_OK)
             return st;
     }
     // dA = sum g x^T, dB = sum h dy^T, beside the product's end
@@ -335,7 +343,7 @@ exl3_status exl3_expert_linear(const void *x, int dt, int64_t T, int64_t x_strid
     if ((st = check_apart(yr, "y", x, xr.bytes(), "x")) != EXL3_OK) return st;
     if (T == 0)
         return EXL3_OK;
-    const LinearWs m(ws, T, w.inputs(), 0, 0, false);
+    const LinearWs m(ws, T, w.inputs(), w.outputs(), 0, 0, false);
     if ((st = check_ws(ws, ws_bytes, m.bytes)) != EXL3_OK) return st;
     if ((st = check_apart(yr, "y", ws, m.bytes, "the workspace")) != EXL3_OK) return st;
     return run_linear(m, x, dt, T, x_stride, w, n_experts, offsets, nullptr, nullptr, nullptr, Adapters{}, y, y_stride,

@@ -320,14 +320,14 @@ template <typename TX, bool VEC, int MB> __global__ void __launch_bounds__(256, 
         cluster_sync();
 }
 
-// ---- expand: y[t] = sum_r h[t][r] M_i[r], which the coded product adds to ------------
-// (rounded to y's type on the way: in 32 bits it would need a buffer twice as large, read
-// and written once more, for half a last place of a term of the sum: 0.0020 instead of
-// 0.0017 relative error in bf16 where the adapters make a large part of the result).
+// ---- expand: term[t] = sum_r h[t][r] M_i[r], which the coded product adds to its own --
+// (in binary32: rounded to the results' type it would leave that rounding where it cancels
+// the coded part, and a binary16 term can be out of range where the sum is not.  It costs
+// what it moves: 4096 tokens forward take 176 us so, 161 with the term in 16 bits in y.)
 // A block takes one tile and 512 outputs, 128 at a time; warp w the tokens 16 (w % 2) ..
-// and 32 of the outputs.  Bound by instructions (2.6 of 4 a cycle): 4096 x 4096, rank
-// 16: 15 us, 2.2 TB/s written.
-template <typename TX> __global__ void __launch_bounds__(256) expand_kernel(const AdaptLaunch a, void *y, int64_t y_stride) {
+// and 32 of the outputs, whose sums go out in whole 32-byte sectors as they stand in the
+// registers.
+template <typename TX> __global__ void __launch_bounds__(256) expand_kernel(const AdaptLaunch a, float *term) {
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ float downs[kTile];
     const AdaptSide &sd = a.side[0];       // h and its way back: M is [rank][n], n outputs
@@ -343,7 +343,6 @@ template <typename TX> __global__ void __launch_bounds__(256) expand_kernel(cons
     TX *const sh = reinterpret_cast<TX *>(smem);                                 // h, twice [32][R16]
     const uint32_t hlow = (uint32_t)(kTile * hrow) * 2;                          // bytes to the second
     const uint32_t sB = saddr(smem) + 2 * hlow, bbytes = (uint32_t)(R16 * kF) * 2;   // two [R16][128]
-    TX *const so = reinterpret_cast<TX *>(smem + 2 * hlow + 2 * bbytes);         // [32][128]
     const uint16_t *M = reinterpret_cast<const uint16_t *>(sd.M) + (size_t)i * a.rank * sd.n;
     const int f_lo = blockIdx.y * 512, f_hi = min(f_lo + 512, sd.n);
     auto load = [&](int f0, int buf) {
@@ -382,18 +381,17 @@ template <typename TX> __global__ void __launch_bounds__(256) expand_kernel(cons
                        kTile * hrow);
     const uint32_t ha = saddr(smem) + (uint32_t)(((warp & 1) * 16 + (lane & 15)) * hrow + (lane >> 4) * 8) * 2;
     const uint32_t ba = sB + (uint32_t)((lane & 15) * kF + (warp >> 1) * 32 + (lane >> 4) * 8) * 2;
-    const bool wide = (((uintptr_t)y | (uintptr_t)(y_stride * 2)) & 15u) == 0;
-    // results: tokens tid / 16 and tid / 16 + 16, 8 outputs each
-    TX *to[2];
+    // results: tokens 16 (w % 2) + g and 8 on, outputs 32 (w / 2) + 2 j .. of each eight
+    float *to[2];
 #pragma unroll
     for (int h = 0; h < 2; h++) {
-        const int t = (tid >> 4) + 16 * h;
-        to[h] = t < n ? reinterpret_cast<TX *>(y) + (int64_t)a.plan.perm[lo + t] * y_stride + (tid & 15) * 8 : nullptr;
+        const int t = (warp & 1) * 16 + g + 8 * h;
+        to[h] = t < n ? term + (int64_t)a.plan.perm[lo + t] * sd.n + (warp >> 1) * 32 + 2 * j : nullptr;
     }
     for (int f0 = f_lo, buf = 0; f0 < f_hi; f0 += 128, buf ^= 1) {
+        copy_wait<0>();
+        __syncthreads();                   // (the other buffer is read, too)
         load(f0 + 128, buf ^ 1);
-        copy_wait<1>();
-        __syncthreads();
         float acc[4][4];
 #pragma unroll
         for (int b = 0; b < 4; b++)
@@ -415,27 +413,14 @@ template <typename TX> __global__ void __launch_bounds__(256) expand_kernel(cons
             }
         }
 #pragma unroll
-        for (int b = 0; b < 4; b++)
-#pragma unroll
-            for (int e = 0; e < 4; e += 2) {
-                const int t = (warp & 1) * 16 + g + 4 * e;
-                *reinterpret_cast<uint32_t *>(so + t * kF + (warp >> 1) * 32 + b * 8 + 2 * j) =
-                    pack2<TX>(__fmul_rn(acc[b][e], downs[t]), __fmul_rn(acc[b][e + 1], downs[t]));
-            }
-        __syncthreads();
-#pragma unroll
         for (int h = 0; h < 2; h++) {
-            const TX *from = so + ((tid >> 4) + 16 * h) * kF + (tid & 15) * 8;
             if (!to[h])
                 continue;
-            if (wide) {
-                *reinterpret_cast<uint4 *>(to[h] + f0) = *reinterpret_cast<const uint4 *>(from);
-            } else {
-                for (int q = 0; q < 8; q++)
-                    to[h][f0 + q] = from[q];
-            }
+            const float d = downs[(warp & 1) * 16 + g + 8 * h];
+#pragma unroll
+            for (int b = 0; b < 4; b++)
+                *reinterpret_cast<float2 *>(to[h] + f0 + 8 * b) = make_float2(__fmul_rn(acc[b][2 * h], d), __fmul_rn(acc[b][2 * h + 1], d));
         }
-        __syncthreads();
     }
 }
 
@@ -679,14 +664,14 @@ exl3_status launch_shrink(const AdaptLaunch &p0, int sides, cudaStream_t s) {
     return vec ? go(shrink_kernel<__half, true, 4>) : go(shrink_kernel<__half, false, 4>);
 }
 
-exl3_status launch_expand(const AdaptLaunch &p, void *y, int64_t y_stride, cudaStream_t s) {
+exl3_status launch_expand(const AdaptLaunch &p, float *term, cudaStream_t s) {
     const int64_t tiles = p.T / kTile + (p.n < p.T ? p.n : p.T);
     const int R16 = (p.rank + 15) / 16 * 16;
-    const size_t smem = (size_t)2 * kTile * (R16 + kPad) * 2 + (size_t)2 * R16 * (128 + kPad) * 2 + (size_t)kTile * (128 + kPad) * 2;
+    const size_t smem = (size_t)2 * kTile * (R16 + kPad) * 2 + (size_t)2 * R16 * (128 + kPad) * 2;
     const dim3 grid((unsigned)tiles, (unsigned)((p.side[0].n + 511) / 512));
     if (p.dt == EXL3_BF16)
-        return launch("adapter expand launch", expand_kernel<__nv_bfloat16>, grid, 256, smem, 1, true, s, p, y, y_stride);
-    return launch("adapter expand launch", expand_kernel<__half>, grid, 256, smem, 1, true, s, p, y, y_stride);
+        return launch("adapter expand launch", expand_kernel<__nv_bfloat16>, grid, 256, smem, 1, true, s, p, term);
+    return launch("adapter expand launch", expand_kernel<__half>, grid, 256, smem, 1, true, s, p, term);
 }
 
 exl3_status launch_outer(const AdaptLaunch &p0, cudaStream_t s) {

@@ -178,22 +178,6 @@ __device__ __forceinline__ void add_adapter(const ProductLaunch &p, int n_out, i
     const int ad = p.slots[t];
     if (ad < 0 || ad >= p.n_adapters)
         return;
-    if (!p.h) {                            // made before: y holds it
-        const TY *y = reinterpret_cast<const TY *>(p.y) + (int64_t)t * p.y_stride + f0 + 8 * u;
-        const bool wide = (((uintptr_t)p.y | (uintptr_t)(p.y_stride * 2)) & 15u) == 0;
-#pragma unroll
-        for (int m = 0; m < 2; m++) {
-            if (wide) {
-                const uint4 w = *reinterpret_cast<const uint4 *>(y + 64 * m);
-                fma8<TY>(v + 8 * m, 1.0f, w);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; i++)
-                    v[8 * m + i] = __fadd_rn(v[8 * m + i], to_f32(y[64 * m + i]));
-            }
-        }
-        return;
-    }
     const int r = p.ranks ? min(max(p.ranks[ad], 0), p.rank) : p.rank;
     const TY *b = reinterpret_cast<const TY *>(p.B) + (size_t)ad * p.rank * n_out + f0 + 8 * u;
     const float *h = p.h + (int64_t)t * p.rank;
@@ -218,6 +202,27 @@ __device__ __forceinline__ void add_adapter(const ProductLaunch &p, int n_out, i
         const uint4 y = __ldg(reinterpret_cast<const uint4 *>(b + (size_t)j * n_out + 64));
         fma8<TY>(v, h[j], x);
         fma8<TY>(v + 8, h[j], y);
+    }
+}
+
+// the token's row of the adapters' part, outputs f0 + 8u + 64m + i: float4 q (q < 4) of the
+// thread's (read past L1: the kernel started before the row was written)
+__device__ __forceinline__ const float4 *term_at(const ProductLaunch &p, int n_out, int f0, int64_t t, int u) {
+    return reinterpret_cast<const float4 *>(p.term + t * n_out + f0 + 8 * u);
+}
+__device__ __forceinline__ bool has_term(const ProductLaunch &p, int64_t t) {
+    const int ad = p.slots[t];
+    return ad >= 0 && ad < p.n_adapters;
+}
+__device__ __forceinline__ void add_term(const ProductLaunch &p, int n_out, int f0, int64_t t, float (&v)[16], int u) {
+    if (!has_term(p, t))
+        return;
+    const float4 *from = term_at(p, n_out, f0, t, u);
+#pragma unroll
+    for (int q = 0; q < 4; q++) {
+        const float4 f = __ldcg(from + (q & 1) + 16 * (q >> 1));
+        v[4 * q] = __fadd_rn(v[4 * q], f.x), v[4 * q + 1] = __fadd_rn(v[4 * q + 1], f.y);
+        v[4 * q + 2] = __fadd_rn(v[4 * q + 2], f.z), v[4 * q + 3] = __fadd_rn(v[4 * q + 3], f.w);
     }
 }
 

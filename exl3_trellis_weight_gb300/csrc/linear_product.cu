@@ -52,15 +52,15 @@ constexpr int kWarpB = kDecWarps + kOutWarps, kWarpMma = kWarpB + 1;
 constexpr int kThreadsP = (kWarpB + 2) * 32;
 constexpr int kN = 256;                    // columns of an accumulator
 constexpr int kStep = 64;                  // inputs of a step
-constexpr int kAStages = 4, kBStages = 16; // operand stages (of B at most)
+constexpr int kAStages = 3, kBStages = 16; // operand stages (of B at most; a fourth of A changed no time)
 constexpr uint32_t kABytes = 128 * kStep * 2, kBArea = 96 * 1024, kCArea = 16 * 1024;
 constexpr uint32_t kBOff = kAStages * kABytes;              // B stages behind the A stages,
 constexpr uint32_t kCOff = kBOff + kBArea;                  // then a ring of codes for each decode warp,
 constexpr uint32_t kOutOff = kCOff + kCArea;                // then 32 tokens x 128 outputs, fp32, for four result warps each,
-constexpr uint32_t kAddOff = kOutOff + 2 * 32 * 128 * 4;    // then 64 bytes for each of their threads,
+constexpr uint32_t kAddOff = kOutOff + 2 * 32 * 128 * 4;    // then 128 bytes for each of their threads,
 constexpr uint32_t kPlanOff = kAddOff;                      // or the experts' tiles (which have no adapters)
-constexpr uint32_t kSmem = kAddOff + 256 * 64 + 1024;       // + alignment slack
-static_assert(sizeof(Plan) <= 256 * 64, "the plan fits where the adapters' terms would be");
+constexpr uint32_t kSmem = kAddOff + 256 * 128 + 1024;      // + alignment slack
+static_assert(sizeof(Plan) <= 256 * 128, "the plan fits where the adapters' terms would be");
 
 __device__ unsigned int g_product_timeouts;
 
@@ -312,7 +312,6 @@ __global__ void __launch_bounds__(kThreadsP, 1) product_kernel(const __grid_cons
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // (the adapters' gradients)
         uint32_t acc = 0;
         bool ok = true;
-        const bool wide_y = (((uintptr_t)a.p.y | (uintptr_t)(a.p.y_stride * 2)) & 15u) == 0;
         const int u = lane & 7;
         for (int64_t it = it0; ok && it < n_tiles; it += dit) {
             const Tile tl = make_tile<PAIR>(a, &plan, it, rank);
@@ -320,20 +319,20 @@ __global__ void __launch_bounds__(kThreadsP, 1) product_kernel(const __grid_cons
             // read after the barriers of the first chunk; the last chunk's protect the previous tile's
             right[ow * 32 + lane] = right_of(a, tl, ow * 32 + lane);
             // A thread finishes two tokens of every 32, eight threads to a token.  What it
-            // needs of them from memory is asked for a chunk before: the row's scale, and
-            // what y holds of a token with an adapter (to its own place in shared memory).
+            // needs of them from memory is asked for a chunk before: the row's scale, and of a
+            // token with an adapter its part of the result (to its own place in shared memory).
             float rs[2];
-            int slot[2];                   // -1: nothing in y
-            const uint32_t mine = base + kAddOff + (uint32_t)og * 8192u + (uint32_t)(ow * 32 + lane) * 16u;
+            bool more[2];
+            const uint32_t mine = base + kAddOff + (uint32_t)og * 16384u + (uint32_t)(ow * 32 + lane) * 16u;
             auto fetch = [&](int g, int t) {
                 const bool in = !keep && live && t >= tl.lo && t < tl.hi;
                 rs[g] = in ? a.p.rscale[t] : 0.0f;
-                slot[g] = -1;
-                if (a.p.B && !a.p.h && wide_y && in) {
-                    const TY *y = reinterpret_cast<const TY *>(a.p.y) + (int64_t)t * a.p.y_stride + tl.f0 + 8 * u;
-                    copy16(mine + g * 4096u, y);
-                    copy16(mine + g * 4096u + 2048u, y + 64);
-                    slot[g] = a.p.slots[t];
+                more[g] = a.p.term && in && has_term(a.p, t);
+                if (a.p.term && in) {
+                    const float4 *from = term_at(a.p, a.n_out, tl.f0, t, u);
+#pragma unroll
+                    for (int q = 0; q < 4; q++)
+                        copy16(mine + (4 * g + q) * 2048u, from + (q & 1) + 16 * (q >> 1));
                 }
                 copy_group();
             };
@@ -377,11 +376,14 @@ __global__ void __launch_bounds__(kThreadsP, 1) product_kernel(const __grid_cons
                         rotate_second(buf, g * 16 + ow * 4 + (lane >> 3), u, rs[g], right, x);
                         const bool in = live && t >= tl.lo && t < tl.hi;
                         copy_wait<1>();
-                        if (slot[g] >= 0 && slot[g] < a.p.n_adapters) {
-                            const unsigned char *from = sb + (mine - base) + g * 4096;
-                            fma8<TY>(x, 1.0f, *reinterpret_cast<const uint4 *>(from));
-                            fma8<TY>(x + 8, 1.0f, *reinterpret_cast<const uint4 *>(from + 2048));
-                        } else if (a.p.B && (a.p.h || !wide_y) && in) {
+                        if (more[g]) {     // (the thread's own copies: no barrier)
+#pragma unroll
+                            for (int q = 0; q < 4; q++) {
+                                const float4 f = *reinterpret_cast<const float4 *>(sb + (mine - base) + (4 * g + q) * 2048);
+                                x[4 * q] = __fadd_rn(x[4 * q], f.x), x[4 * q + 1] = __fadd_rn(x[4 * q + 1], f.y);
+                                x[4 * q + 2] = __fadd_rn(x[4 * q + 2], f.z), x[4 * q + 3] = __fadd_rn(x[4 * q + 3], f.w);
+                            }
+                        } else if (a.p.B && in) {
                             add_adapter<TY>(a.p, a.n_out, tl.f0, t, x, u, 0, 1);
                         }
                         fetch(g, t + 64);
@@ -510,7 +512,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) product_kernel(const __grid_cons
             const Tile tl = make_tile<PAIR>(a, &plan, it0, rank);
             // a warp takes four tokens at a time, with adapters one (its four groups of eight
             // lanes a quarter of the adapter's rows each)
-            const bool shared = a.p.B && a.p.h;
+            const bool shared = a.p.B != nullptr;
             const int each = shared ? 1 : 4, sub = shared ? 0 : lane >> 3, u = lane & 7;
             const int mine = (tl.n + a.split - 1 - rank) / a.split;          // tokens rank, rank + split, ...
             for (int i = warp * each; i < mine; i += (kDecWarps + kOutWarps) * each) {
@@ -541,8 +543,8 @@ __global__ void __launch_bounds__(kThreadsP, 1) product_kernel(const __grid_cons
 #pragma unroll
                         for (int j = 0; j < 16; j++)
                             x[j] = __fadd_rn(x[j], v[j]);
-                    } else if (a.p.B) {
-                        add_adapter<TY>(a.p, a.n_out, tl.f0, t, x, u, 0, 1);
+                    } else if (a.p.term) {
+                        add_term(a.p, a.n_out, tl.f0, t, x, u);
                     }
                     store_out<TY>(a.p, tl.f0, t, x, u);
                 }

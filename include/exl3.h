@@ -401,8 +401,7 @@ EXL3_API exl3_status exl3_regularize(const void *W, int dt, int64_t rows, int64_
  * under an exact power-of-two scale for each row; products with the levels
  * are summed in binary32 (tensor cores, in any order within a sum), rotated
  * and scaled in binary32 and rounded to dt once, with the adapters' terms
- * (binary32 sums) added before; with more than 64 tokens these wait in y for
- * that and are rounded to dt, too.
+ * (binary32 sums) added before.
  * Results are the same from run to run.  A row of x that holds an
  * infinity or a NaN gives no numbers in its own row of y and touches no other.
  */
@@ -427,7 +426,7 @@ EXL3_API exl3_status exl3_linear(const void *x, int dt, int64_t T, int64_t x_str
  *   x, dA and dB are used only when n_adapters > 0 (dA, dB 16-byte aligned,
  *   shapes and type of A and B).  dx overlaps neither dy, x nor ws.  The sums
  *   over tokens are binary32 in a fixed order, rounded to dt once.  The other
- *   arguments are those of exl3_linear.
+ *   arguments are those of exl3_linear, for which the workspace is large enough, too.
  */
 EXL3_API size_t exl3_linear_backward_workspace_bytes(int64_t T, int64_t rows, int64_t cols,
                                                      int transposed, int n_adapters, int rank);

@@ -67,3 +67,56 @@ def test_gradients_of_small_sums_beside_large_ones(ex):
     live = torch.arange(384, device=DEV) % 2 == 0
     assert (ref[:, live].abs() < 10).all()
     assert ((got["dB"][0].double() - ref).abs() <= tol)[:, live].all()
+
+
+@pytest.mark.parametrize("T", [3, 64, 65, 300])
+def test_adapter_term_beyond_the_range_of_the_results(ex, T):
+    """float16: the term alone is out of range where its sum with the coded part is not."""
+    g = gen(52)
+    codes, su, sv, scale = coded(g, 256, 384, 2)
+    x = torch.randn(T, 256, generator=g, device=DEV).half()
+    scale = scale * 3e4 / float((x.double() @ weight64(codes, su, sv, 2, scale)).std())
+    W = weight64(codes, su, sv, 2, scale)
+    base = x.double() @ W
+    A = torch.randn(1, 1, 256, generator=g, device=DEV).half()
+    slots = torch.full((T,), -1, dtype=torch.int32, device=DEV)
+    slots[1] = 0
+    h = float(x[1].double() @ A[0, 0].double())
+    B = (-2.5 * base[1] / h).half()[None, None]
+    gain = torch.ones(1, device=DEV)
+    term, err = adapter64(x, A, B, gain, slots, None)
+    ref = base + term
+    over = (term[1].abs() > 65520) & (ref[1].abs() < 65000)
+    assert over.sum() > 10
+    y = ex.linear(x, codes, su, sv, 2, scale, A=A, B=B, gain=gain, slots=slots)
+    close(y[1:2, over], ref[1:2, over], sv.double()[over], "fp16", base[1:2, over], 6 * U["fp16"] / math.sqrt(3) * err[1:2, over])
+    # the gradient of x is the same with the other transposition
+    got = ex.linear_backward(x, torch.zeros(T, 384, dtype=torch.float16, device=DEV), codes.transpose(0, 1).contiguous(),
+                             sv, su, 2, scale, A=B, B=A, gain=gain, slots=slots)["dx"]
+    V = weight64(codes.transpose(0, 1).contiguous(), sv, su, 2, scale).t()
+    base = x.double() @ V
+    ref = base + term
+    keep = ref.abs() < 65000
+    assert torch.isfinite(got[keep]).all()
+
+
+@pytest.mark.parametrize("T", [40, 64, 65, 700])
+def test_adapter_term_that_cancels(ex, T):
+    """bfloat16: the term takes most of the coded part away.  What stays has the rounding of
+    the rotated activations (at most 2^-11 of each, 2^-11 / sqrt(3) as a root mean square; half
+    as much again is allowed) and its own, not that of a term rounded before the sum."""
+    g = gen(53)
+    codes, su, sv, scale = coded(g, 512, 384, 4)
+    W = weight64(codes, su, sv, 4, scale)
+    x = torch.randn(T, 512, generator=g, device=DEV).bfloat16()
+    base = x.double() @ W
+    A = torch.randn(1, 1, 512, generator=g, device=DEV).bfloat16()
+    for t in (0, T // 2, T - 1):
+        slots = torch.full((T,), -1, dtype=torch.int32, device=DEV)
+        slots[t] = 0
+        h = float(x[t].double() @ A[0, 0].double())
+        B = (-base[t] / h).bfloat16()[None, None]
+        ref = base[t] + h * B[0, 0].double()
+        y = ex.linear(x, codes, su, sv, 4, scale, A=A, B=B, gain=torch.ones(1, device=DEV), slots=slots)
+        rms = lambda v: float(v.pow(2).mean().sqrt())  # noqa: E731
+        assert rms(y[t].double() - ref) <= 1.5 * 2.0 ** -11 / math.sqrt(3) * rms(base[t]) + U["bf16"] * rms(ref)
