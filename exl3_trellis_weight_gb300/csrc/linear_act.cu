@@ -147,7 +147,6 @@ __global__ void prep_kernel(const PrepLaunch a) {
     const bool in0 = tid * 16 < a.n;
     uint4 raw[2];
     float lf[16];
-    float left_max = 0.0f;
     int e_left = -1, turn = 0;
     if (ONE && VEC && in0 && t_lo < t_hi)
         load16_raw(x + t_lo * a.stride, raw);
@@ -159,14 +158,11 @@ __global__ void prep_kernel(const PrepLaunch a) {
         float m = 0.0f;
         if (ONE) {
             if (VEC) {
-                if (in0)
-                    m = max16_raw<TX>(raw);
                 unpack16<TX>(raw, v);
                 if (in0 && t + 1 < t_hi)
                     load16_raw(x + (t + 1) * a.stride, raw);
             } else if (in0) {
                 load16<TX, false>(x + t * a.stride, v);
-                m = max16(v, m);
             }
         }
         if (e < 0) {                       // no expert: no product, the result row is 0
@@ -178,22 +174,19 @@ __global__ void prep_kernel(const PrepLaunch a) {
         const float *left = a.left + (size_t)e * a.n;
         if (ONE) {
             if (e != e_left) {
-                // this thread's factors, and the largest of the row's
-                e_left = e;
-                float f = 0.0f;
+                e_left = e;                // this thread's factors
                 if (in0) {
 #pragma unroll
                     for (int i = 0; i < 16; i++)
                         lf[i] = 1.0f;
                     mul16(left + tid * 16, lf);
-                    f = max16(lf, f);
                 }
-                left_max = block_max(f, wmax[turn], warps);
-                turn ^= 1;
             }
 #pragma unroll
             for (int i = 0; i < 16; i += 2)
                 mul2(v[i], v[i + 1], lf[i], lf[i + 1]);
+            if (in0)
+                m = max16(v, m);
         } else {
             for (int k = 0; k + tid * 16 < a.n; k += blockDim.x * 16) {
                 load16<TX, VEC>(x + t * a.stride + k, v);
@@ -204,8 +197,6 @@ __global__ void prep_kernel(const PrepLaunch a) {
         // (two places in turn: a row's reads are done before the barrier of the next)
         m = block_max(m, wmax[turn], warps);
         turn ^= 1;
-        if (ONE)
-            m = __fmul_rn(m, left_max);    // a bound of the row's products
         float up, down;
         row_scale(m, up, down);
         if (tid == 0)

@@ -7,8 +7,6 @@
 // leaves again with the row's result.
 #pragma once
 
-#include <type_traits>
-
 #include "linear.cuh"
 
 namespace exl3 {
@@ -76,18 +74,7 @@ __device__ __forceinline__ void mul16(const float *s, float (&v)[16]) {
     }
 }
 
-// largest magnitude of 16 raw elements (a NaN is passed over)
-template <typename TX> __device__ __forceinline__ float max16_raw(const uint4 (&r)[2]) {
-    using T2 = typename std::conditional<std::is_same<TX, __half>::value, __half2, __nv_bfloat162>::type;
-    const uint32_t w[8] = {r[0].x, r[0].y, r[0].z, r[0].w, r[1].x, r[1].y, r[1].z, r[1].w};
-    T2 m = __habs2(*reinterpret_cast<const T2 *>(&w[0]));
-#pragma unroll
-    for (int i = 1; i < 8; i++)
-        m = __hmax2(m, __habs2(*reinterpret_cast<const T2 *>(&w[i])));
-    const float2 f = unpack2<TX>(*reinterpret_cast<const uint32_t *>(&m));
-    return fmaxf(f.x, f.y);
-}
-
+// the largest magnitude of m and 16 values (a NaN is passed over)
 __device__ __forceinline__ float max16(const float (&v)[16], float m) {
 #pragma unroll
     for (int i = 0; i < 16; i++)

@@ -120,3 +120,26 @@ def test_adapter_term_that_cancels(ex, T):
         y = ex.linear(x, codes, su, sv, 4, scale, A=A, B=B, gain=torch.ones(1, device=DEV), slots=slots)
         rms = lambda v: float(v.pow(2).mean().sqrt())  # noqa: E731
         assert rms(y[t].double() - ref) <= 1.5 * 2.0 ** -11 / math.sqrt(3) * rms(base[t]) + U["bf16"] * rms(ref)
+
+
+@pytest.mark.parametrize("n", [256, 16512])
+@pytest.mark.parametrize("T", [3, 70])
+def test_row_scale_follows_the_products(ex, n, T):
+    """A row's scale comes from its products with the channel factors: neither a value in a
+    dead channel nor factors opposite to the activations take the rest's bits."""
+    g = gen(54)
+    codes, su, sv, scale = coded(g, 128, n, 2)
+    sv = torch.where(torch.rand(n, generator=g, device=DEV) < 0.5, 1.0, -1.0)
+    sv[7], sv[n - 1] = 0.0, 0.0
+    x = torch.randn(T, n, generator=g, device=DEV)
+    x[:, 7], x[:, n - 1] = 1e30, -1e25
+    x = x.bfloat16()
+    W = weight64(codes, su, sv, 2, scale).t()
+    y = ex.linear(x, codes, su, sv, 2, scale, transposed=True)
+    close(y, x.double() @ W, su.double(), "bf16")
+    half = torch.arange(n, device=DEV) % 2 == 0
+    f = torch.where(half, 2.0 ** 16, 2.0 ** -16)
+    x = (torch.randn(T, n, generator=g, device=DEV) * f).bfloat16()
+    sv = torch.where(torch.rand(n, generator=g, device=DEV) < 0.5, 1.0, -1.0) / f
+    W = weight64(codes, su, sv, 2, scale).t()
+    close(ex.linear(x, codes, su, sv, 2, scale, transposed=True), x.double() @ W, su.double(), "bf16")
