@@ -79,6 +79,7 @@ struct Adapters {
     const float *gain;
     const int32_t *slots, *ranks;
     int n, rank;
+    int64_t inputs, outputs;  // columns of A and B
 };
 
 bool adapters_ok(int n, int rank) { return n >= 0 && n <= kMaxAdapters && (n == 0 || (rank > 0 && rank <= kMaxRank)); }
@@ -97,6 +98,18 @@ exl3_status check_adapters(const Adapters &a, int64_t T) {
     if (a.ranks && !aligned(a.ranks, 4))
         return set_error(EXL3_ERR_INVALID_ARG, "ranks is not 4-byte aligned");
     return EXL3_OK;
+}
+
+// a result is apart from what the kernels read beside the activations: the codes of E
+// matrices and the adapters' factors
+exl3_status check_read(const Rows &out, const char *name, const Coded &w, int E, const Adapters &ad) {
+    exl3_status st;
+    const size_t factors = (size_t)ad.n * ad.rank * 2;
+    if ((st = check_apart(out, name, w.codes, (size_t)E * w.rows * w.cols * w.K / 8, "codes")) != EXL3_OK) return st;
+    if (ad.n == 0)
+        return EXL3_OK;
+    if ((st = check_apart(out, name, ad.A, factors * ad.inputs, "A")) != EXL3_OK) return st;
+    return check_apart(out, name, ad.B, factors * ad.outputs, "B");
 }
 
 // workspace: bump allocation at 256-byte boundaries; with a null base it counts
@@ -239,13 +252,14 @@ exl3_status exl3_linear(const void *x, int dt, int64_t T, int64_t x_stride, cons
                         int n_adapters, int rank, void *y, int64_t y_stride, void *ws, size_t ws_bytes, void *stream) {
     exl3_status st;
     const Coded w{codes, rows, cols, K, su, sv, scale, transposed ? 1 : 0};
-    const Adapters ad{A, B, gain, slots, ranks, n_adapters, rank};
+    const Adapters ad{A, B, gain, slots, ranks, n_adapters, rank, w.inputs(), w.outputs()};
     if ((st = check_coded(w, T, dt)) != EXL3_OK) return st;
     if ((st = check_adapters(ad, T)) != EXL3_OK) return st;
     const Rows xr{x, T, w.inputs(), x_stride}, yr{y, T, w.outputs(), y_stride};
     if ((st = check_rows(xr, "x")) != EXL3_OK) return st;
     if ((st = check_rows(yr, "y")) != EXL3_OK) return st;
     if ((st = check_apart(yr, "y", x, xr.bytes(), "x")) != EXL3_OK) return st;
+    if ((st = check_read(yr, "y", w, 1, ad)) != EXL3_OK) return st;
     if (T == 0)
         return EXL3_OK;
     const LinearWs m(ws, T, w.inputs(), w.outputs(), n_adapters, rank, false);
@@ -280,7 +294,8 @@ exl3_status exl3_linear_backward(const void *dy, int64_t dy_stride, const void *
     exl3_status st;
     // the gradient of x is a product with the other transposition
     const Coded w{codes, rows, cols, K, su, sv, scale, transposed ? 0 : 1};
-    const Adapters ad{A, B, gain, slots, ranks, n_adapters, rank};
+    // (w's outputs are the forward product's inputs)
+    const Adapters ad{A, B, gain, slots, ranks, n_adapters, rank, w.outputs(), w.inputs()};
     if ((st = check_coded(w, T, dt)) != EXL3_OK) return st;
     if ((st = check_adapters(ad, T)) != EXL3_OK) return st;
     const int64_t n_in = w.outputs(), n_out = w.inputs();      // of the forward product
@@ -294,11 +309,26 @@ exl3_status exl3_linear_backward(const void *dy, int64_t dy_stride, const void *
         if ((st = check_apart(dxr, "dx", x, xr.bytes(), "x")) != EXL3_OK) return st;
     }
     if ((st = check_apart(dxr, "dx", dy, dyr.bytes(), "dy")) != EXL3_OK) return st;
+    if ((st = check_read(dxr, "dx", w, 1, ad)) != EXL3_OK) return st;
+    // dA and dB are written beside the product, while x and dy are read
+    const int64_t factors = (int64_t)n_adapters * rank;
+    const Rows dAr{dA, n_adapters ? 1 : 0, factors * n_in, factors * n_in}, dBr{dB, n_adapters ? 1 : 0, factors * n_out, factors * n_out};
+    for (int k = 0; k < 2; k++) {
+        const Rows &d = k ? dBr : dAr;
+        const char *name = k ? "dB" : "dA";
+        if ((st = check_read(d, name, w, 1, ad)) != EXL3_OK) return st;
+        if ((st = check_apart(d, name, x, xr.bytes(), "x")) != EXL3_OK) return st;
+        if ((st = check_apart(d, name, dy, dyr.bytes(), "dy")) != EXL3_OK) return st;
+        if ((st = check_apart(d, name, dx, dxr.bytes(), "dx")) != EXL3_OK) return st;
+    }
+    if ((st = check_apart(dAr, "dA", dB, dBr.bytes(), "dB")) != EXL3_OK) return st;
     if (T == 0 && n_adapters == 0)
         return EXL3_OK;
     const LinearWs m(ws, T, n_out, n_in, n_adapters, rank, true);
     if ((st = check_ws(ws, ws_bytes, m.bytes)) != EXL3_OK) return st;
     if ((st = check_apart(dxr, "dx", ws, m.bytes, "the workspace")) != EXL3_OK) return st;
+    if ((st = check_apart(dAr, "dA", ws, m.bytes, "the workspace")) != EXL3_OK) return st;
+    if ((st = check_apart(dBr, "dB", ws, m.bytes, "the workspace")) != EXL3_OK) return st;
     const cudaStream_t s = (cudaStream_t)stream;
     if (n_adapters == 0)
         return run_linear(m, dy, dt, T, dy_stride, w, 1, nullptr, nullptr, nullptr, nullptr, ad, dx, dx_stride, s);
@@ -341,6 +371,7 @@ exl3_status exl3_expert_linear(const void *x, int dt, int64_t T, int64_t x_strid
     if ((st = check_rows(xr, "x")) != EXL3_OK) return st;
     if ((st = check_rows(yr, "y")) != EXL3_OK) return st;
     if ((st = check_apart(yr, "y", x, xr.bytes(), "x")) != EXL3_OK) return st;
+    if ((st = check_read(yr, "y", w, n_experts, Adapters{})) != EXL3_OK) return st;
     if (T == 0)
         return EXL3_OK;
     const LinearWs m(ws, T, w.inputs(), w.outputs(), 0, 0, false);

@@ -385,7 +385,8 @@ EXL3_API exl3_status exl3_regularize(const void *W, int dt, int64_t rows, int64_
  *   x (device) [T, inputs] of dtype dt (EXL3_BF16 or EXL3_F16), rows x_stride
  *     elements apart; y (device) [T, outputs] of the same type, rows y_stride
  *     apart; any 2-byte alignment (16-byte aligned rows are read and written
- *     in wide accesses).  y overlaps neither x nor the workspace.  T >= 0.
+ *     in wide accesses).  y overlaps neither x, codes, A, B nor the workspace.
+ *     T >= 0.
  *   codes (device, 16-byte aligned) uint16 [rows/16][cols/16][16 K]; su, sv
  *     (device, 16-byte aligned) fp32, multiplied as given (they may carry
  *     channel scales, a zero included); scale (device) one float.  rows, cols
@@ -424,7 +425,8 @@ EXL3_API exl3_status exl3_linear(const void *x, int dt, int64_t T, int64_t x_str
  * rows j >= ranks_i and adapters without tokens get 0.
  *   dy (device) [T, outputs], x, dx [T, inputs] of dtype dt with row strides;
  *   x, dA and dB are used only when n_adapters > 0 (dA, dB 16-byte aligned,
- *   shapes and type of A and B).  dx overlaps neither dy, x nor ws.  The sums
+ *   shapes and type of A and B).  dx, dA and dB overlap neither dy, x, codes, A,
+ *   B, ws nor one another.  The sums
  *   over tokens are binary32 in a fixed order, rounded to dt once.  The other
  *   arguments are those of exl3_linear, for which the workspace is large enough, too.
  */
