@@ -45,6 +45,18 @@ exl3_status check_apart(const Rows &out, const char *name, const void *p, size_t
     return EXL3_OK;
 }
 
+// the same for rows that may stand side by side with the result's: with one stride, rows
+// whose columns share no place modulo the stride never meet
+exl3_status check_apart(const Rows &out, const char *name, const Rows &r, const char *other) {
+    if (out.T > 1 && r.T > 1 && out.stride == r.stride) {
+        const int64_t step = out.stride * 2, between = (int64_t)((uintptr_t)r.p - (uintptr_t)out.p) % step;
+        const int64_t at = between < 0 ? between + step : between;
+        if (at >= out.n * 2 && at + r.n * 2 <= step)
+            return EXL3_OK;
+    }
+    return check_apart(out, name, r.p, r.bytes(), other);
+}
+
 struct Coded {
     const uint16_t *codes;
     int64_t rows, cols;
@@ -258,7 +270,7 @@ exl3_status exl3_linear(const void *x, int dt, int64_t T, int64_t x_stride, cons
     const Rows xr{x, T, w.inputs(), x_stride}, yr{y, T, w.outputs(), y_stride};
     if ((st = check_rows(xr, "x")) != EXL3_OK) return st;
     if ((st = check_rows(yr, "y")) != EXL3_OK) return st;
-    if ((st = check_apart(yr, "y", x, xr.bytes(), "x")) != EXL3_OK) return st;
+    if ((st = check_apart(yr, "y", xr, "x")) != EXL3_OK) return st;
     if ((st = check_read(yr, "y", w, 1, ad)) != EXL3_OK) return st;
     if (T == 0)
         return EXL3_OK;
@@ -306,9 +318,9 @@ exl3_status exl3_linear_backward(const void *dy, int64_t dy_stride, const void *
         if ((st = check_rows(xr, "x")) != EXL3_OK) return st;
         if ((st = need(dA, "dA", 16)) != EXL3_OK) return st;
         if ((st = need(dB, "dB", 16)) != EXL3_OK) return st;
-        if ((st = check_apart(dxr, "dx", x, xr.bytes(), "x")) != EXL3_OK) return st;
+        if ((st = check_apart(dxr, "dx", xr, "x")) != EXL3_OK) return st;
     }
-    if ((st = check_apart(dxr, "dx", dy, dyr.bytes(), "dy")) != EXL3_OK) return st;
+    if ((st = check_apart(dxr, "dx", dyr, "dy")) != EXL3_OK) return st;
     if ((st = check_read(dxr, "dx", w, 1, ad)) != EXL3_OK) return st;
     // dA and dB are written beside the product, while x and dy are read
     const int64_t factors = (int64_t)n_adapters * rank;
@@ -370,7 +382,7 @@ exl3_status exl3_expert_linear(const void *x, int dt, int64_t T, int64_t x_strid
     const Rows xr{x, T, w.inputs(), x_stride}, yr{y, T, w.outputs(), y_stride};
     if ((st = check_rows(xr, "x")) != EXL3_OK) return st;
     if ((st = check_rows(yr, "y")) != EXL3_OK) return st;
-    if ((st = check_apart(yr, "y", x, xr.bytes(), "x")) != EXL3_OK) return st;
+    if ((st = check_apart(yr, "y", xr, "x")) != EXL3_OK) return st;
     if ((st = check_read(yr, "y", w, n_experts, Adapters{})) != EXL3_OK) return st;
     if (T == 0)
         return EXL3_OK;

@@ -385,8 +385,8 @@ EXL3_API exl3_status exl3_regularize(const void *W, int dt, int64_t rows, int64_
  *   x (device) [T, inputs] of dtype dt (EXL3_BF16 or EXL3_F16), rows x_stride
  *     elements apart; y (device) [T, outputs] of the same type, rows y_stride
  *     apart; any 2-byte alignment (16-byte aligned rows are read and written
- *     in wide accesses).  y overlaps neither x, codes, A, B nor the workspace.
- *     T >= 0.
+ *     in wide accesses).  y overlaps neither x, codes, A, B nor the workspace;
+ *     x and y may be different columns of one buffer.  T >= 0.
  *   codes (device, 16-byte aligned) uint16 [rows/16][cols/16][16 K]; su, sv
  *     (device, 16-byte aligned) fp32, multiplied as given (they may carry
  *     channel scales, a zero included); scale (device) one float.  rows, cols

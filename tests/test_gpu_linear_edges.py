@@ -143,3 +143,26 @@ def test_row_scale_follows_the_products(ex, n, T):
     sv = torch.where(torch.rand(n, generator=g, device=DEV) < 0.5, 1.0, -1.0) / f
     W = weight64(codes, su, sv, 2, scale).t()
     close(ex.linear(x, codes, su, sv, 2, scale, transposed=True), x.double() @ W, su.double(), "bf16")
+
+
+@pytest.mark.parametrize("T", [3, 40, 70, 400])
+def test_columns_of_one_buffer(ex, T):
+    """Activations and results side by side in one buffer, as around a fused projection."""
+    g = gen(56)
+    codes, su, sv, scale = coded(g, 256, 384, 3)
+    A, B, gain, ranks = adapters(g, 3, 8, 256, 384, "bf16")
+    slots = torch.randint(-1, 3, (T,), generator=g, device=DEV, dtype=torch.int32)
+    kw = dict(A=A, B=B, gain=gain, slots=slots, ranks=ranks)
+    x, dy = acts(g, T, 256, "bf16"), acts(g, T, 384, "bf16")
+    y, grad = ex.linear(x, codes, su, sv, 3, scale, **kw), ex.linear_backward(dy, x, codes, su, sv, 3, scale, **kw)
+    buf = torch.full((T, 1408), 7.0, dtype=torch.bfloat16, device=DEV)
+    bx, by, bd, bg = buf[:, 8:264], buf[:, 264:648], buf[:, 656:1040], buf[:, 1040:1296]
+    bx.copy_(x), bd.copy_(dy)
+    ex.linear(bx, codes, su, sv, 3, scale, out=by, **kw)
+    got = ex.linear_backward(bd, bx, codes, su, sv, 3, scale, dx=bg, **kw)
+    for p, q in ((bx, x), (by, y), (bd, dy), (bg, grad["dx"]), (got["dA"], grad["dA"]), (got["dB"], grad["dB"])):
+        assert torch.equal(p, q)
+    assert (buf[:, :8] == 7.0).all() and (buf[:, 648:656] == 7.0).all() and (buf[:, 1296:] == 7.0).all()
+    off = torch.tensor([0, T], dtype=torch.int32, device=DEV)
+    ex.expert_linear(bx, off, codes[None], su[None], sv[None], 3, scale[None], out=by)
+    assert torch.equal(by, ex.expert_linear(x, off, codes[None], su[None], sv[None], 3, scale[None]))

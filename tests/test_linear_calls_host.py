@@ -71,3 +71,31 @@ def test_experts_refuse_results_over_the_codes(ex):
     for y, want in ((CODES, 1), (CODES + E * size - 2, 1), (CODES + E * size, 3)):
         assert ex.lib().exl3_expert_linear(X, 1, T, ROWS, SLOTS, E, CODES, ROWS, COLS, 2, SU, SV, SCALE, 0, y, COLS, WS, 0,
                                            None) == want
+
+
+@pytest.mark.parametrize("at,want", [
+    # y's columns in a buffer whose rows of 1024 begin with x's 256: beside them, up to their end,
+    # touching their last or (a row on) their first element
+    (256, 3), (640, 3), (255, 1), (641, 1), (0, 1), (-384, 3), (-385, 3), (-383, 1), (1024 + 256, 3), (1024 + 255, 1),
+])
+def test_columns_of_one_buffer_may_stand_side_by_side(ex, at, want):
+    assert _linear(ex, xs=1024, ys=1024, y=X + 2 * at, n=0) == want
+    assert ex.lib().exl3_expert_linear(X, 1, T, 1024, SLOTS, 1, CODES, ROWS, COLS, 2, SU, SV, SCALE, 0, X + 2 * at, 1024,
+                                       WS, 0, None) == want
+
+
+def test_columns_of_different_strides_are_compared_whole(ex):
+    assert _linear(ex, xs=1024, ys=1032, y=X + 2 * 256, n=0) == 1
+    assert _linear(ex, xs=1024, ys=1032, y=X + 2 * (3 * 1024 + 256), n=0) == 3
+    # a single row has no stride
+    assert _linear(ex, T=1, xs=256, ys=384, y=X + 2 * 256, n=0) == 3
+    assert _linear(ex, T=1, xs=256, ys=384, y=X + 2 * 255, n=0) == 1
+    assert _linear(ex, T=1, xs=300, ys=300 + 84, y=X + 2 * 128, n=0) == 1
+
+
+def test_gradient_beside_its_input(ex):
+    # dx (256 columns) behind dy's 384 and x's 256 in rows of 1024
+    def at(dx, x):
+        return _backward(ex, dys=1024, xs=1024, dxs=1024, x=DY + 2 * x, dx=DY + 2 * dx, wb=0)
+    assert at(640, 384) == 3 and at(768, 384) == 3
+    assert at(639, 384) == 1 and at(383, 640) == 1 and at(769, 384) == 1
