@@ -132,6 +132,58 @@ def _ws(need, device, ws):
     return ws
 
 
+_grad_on = torch.is_grad_enabled
+
+
+def _refuse_lost(out, **constants):
+    """For a call that goes through autograd: raises where a gradient would be lost."""
+    for name, t in constants.items():
+        if t is not None and t.requires_grad:
+            raise ValueError(f"there is no gradient with respect to {name} (detach it)")
+    if out is not None:
+        raise ValueError("out does not go with inputs that want a gradient (torch.no_grad() lets it)")
+
+
+def _rows(t):
+    """t with rows as the library takes them (an expanded gradient has none)."""
+    return t if t.shape[0] == 0 or (t.stride(1) == 1 and t.stride(0) >= t.shape[1]) else t.contiguous()
+
+
+class _Linear(torch.autograd.Function):
+    """``linear`` with ``linear_backward`` as its gradient."""
+
+    @staticmethod
+    def forward(ctx, x, A, B, codes, su, sv, K, scale, transposed, gain, slots, ranks, ws):
+        ctx.save_for_backward(None if A is None else x, A, B, codes, su, sv, scale, gain, slots, ranks)
+        ctx.coded = K, transposed
+        return linear(x, codes, su, sv, K, scale, transposed, A, B, gain, slots, ranks, ws=ws)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        x, A, B, codes, su, sv, scale, gain, slots, ranks = ctx.saved_tensors
+        K, transposed = ctx.coded
+        g = linear_backward(_rows(dy), x, codes, su, sv, K, scale, transposed, A, B, gain, slots, ranks)
+        return g["dx"], g["dA"], g["dB"], *(None,) * 10
+
+
+class _ExpertLinear(torch.autograd.Function):
+    """``expert_linear`` with the call of the other transposition as its gradient."""
+
+    @staticmethod
+    def forward(ctx, x, offsets, codes, su, sv, K, scale, transposed, ws):
+        ctx.save_for_backward(offsets, codes, su, sv, scale)
+        ctx.coded = K, transposed
+        return expert_linear(x, offsets, codes, su, sv, K, scale, transposed, ws=ws)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        offsets, codes, su, sv, scale = ctx.saved_tensors
+        K, transposed = ctx.coded
+        return expert_linear(_rows(dy), offsets, codes, su, sv, K, scale, not transposed), *(None,) * 8
+
+
 def linear(x, codes, su, sv, K: int, scale, transposed: bool = False, A=None, B=None, gain=None, slots=None,
            ranks=None, out=None, ws=None):
     """exl3_linear: y = x W^ (transposed: x W^^T) for the matrix coded in ``codes``
@@ -141,13 +193,18 @@ def linear(x, codes, su, sv, K: int, scale, transposed: bool = False, A=None, B=
     float32; scale a float32 device scalar (as ``quantize`` returns it) or a number.
     A [n, r, inputs], B [n, r, outputs] of x's dtype, gain [n] float32, slots [T]
     int32 (the adapter of each token; out of [0, n): none), ranks [n] int32 or None.
-    Returns y [T, outputs] of x's dtype."""
+    Returns y [T, outputs] of x's dtype, through which x, A and B get their gradients
+    where they want them."""
     dev = x.device
-    rows, cols, pc, pu, pv, ps, _keep = _coded(codes, su, sv, K, scale, (), dev)
+    rows, cols, pc, pu, pv, ps, scale_ = _coded(codes, su, sv, K, scale, (), dev)
     n_in, n_out = (cols, rows) if transposed else (rows, cols)
     xs = _activations(x, "x", n_in)
     T = x.shape[0]
     pA, pB, pg, pslots, pranks, n, r = _adapters(A, B, gain, slots, ranks, n_in, n_out, x)
+    if _grad_on() and (x.requires_grad or su.requires_grad or sv.requires_grad or scale_.requires_grad or
+                       (n and (A.requires_grad or B.requires_grad or gain.requires_grad))):
+        _refuse_lost(out, su=su, sv=sv, scale=scale_, gain=gain)
+        return _Linear.apply(x, A, B, codes, su, sv, K, scale_, transposed, gain, slots, ranks, ws)
     if out is None:
         out = torch.empty(T, n_out, dtype=x.dtype, device=dev)
         ys = n_out
@@ -199,16 +256,20 @@ def expert_linear(x, offsets, codes, su, sv, K: int, scale, transposed: bool = F
     matrix of expert e, coded in codes [E, rows/16, cols/16, 16K] with su [E, rows],
     sv [E, cols] and scale [E] (float32 tensors).  offsets: int32 [E + 1] on the
     device, ascending; rows of no expert give 0.  The input gradient is the same
-    call with ``transposed`` flipped.  Returns y [T, outputs] of x's dtype."""
+    call with ``transposed`` flipped, and what x gets through autograd.  Returns y
+    [T, outputs] of x's dtype."""
     dev = x.device
     if codes.dim() != 4:
         raise ValueError(f"codes must be [experts, rows/16, cols/16, 16K], got {tuple(codes.shape)}")
     E = codes.shape[0]
-    rows, cols, pc, pu, pv, ps, _keep = _coded(codes, su, sv, K, scale, (E,), dev)
+    rows, cols, pc, pu, pv, ps, scale_ = _coded(codes, su, sv, K, scale, (E,), dev)
     n_in, n_out = (cols, rows) if transposed else (rows, cols)
     xs = _activations(x, "x", n_in)
     T = x.shape[0]
     po = _dense(offsets, "offsets", torch.int32, (E + 1,), x.get_device())
+    if _grad_on() and (x.requires_grad or su.requires_grad or sv.requires_grad or scale_.requires_grad):
+        _refuse_lost(out, su=su, sv=sv, scale=scale_)
+        return _ExpertLinear.apply(x, offsets, codes, su, sv, K, scale_, transposed, ws)
     if out is None:
         out = torch.empty(T, n_out, dtype=x.dtype, device=dev)
         ys = n_out

@@ -166,3 +166,46 @@ def test_columns_of_one_buffer(ex, T):
     off = torch.tensor([0, T], dtype=torch.int32, device=DEV)
     ex.expert_linear(bx, off, codes[None], su[None], sv[None], 3, scale[None], out=by)
     assert torch.equal(by, ex.expert_linear(x, off, codes[None], su[None], sv[None], 3, scale[None]))
+
+
+@pytest.mark.parametrize("tr", [False, True])
+@pytest.mark.parametrize("T", [1, 40, 200])
+def test_gradients_flow_through_the_calls(ex, T, tr):
+    """x, A and B that want gradients get those of linear_backward, through whatever is
+    around the call."""
+    g = gen(57)
+    codes, su, sv, scale = coded(g, 256, 384, 2)
+    n_in, n_out = (384, 256) if tr else (256, 384)
+    A, B, gain, ranks = adapters(g, 3, 8, n_in, n_out, "bf16")
+    slots = torch.randint(-1, 3, (T,), generator=g, device=DEV, dtype=torch.int32)
+    kw = dict(transposed=tr, gain=gain, slots=slots, ranks=ranks)
+    x, c = acts(g, T, n_in, "bf16"), acts(g, T, n_out, "bf16")
+    want = ex.linear_backward(c, x, codes, su, sv, 2, scale, A=A, B=B, **kw)
+    plain = ex.linear(x, codes, su, sv, 2, scale, A=A, B=B, **kw)
+    for wanted in ("x", "A", "B", "xAB"):
+        t = dict(x=x.clone(), A=A.clone(), B=B.clone())
+        for k in wanted:
+            t[k].requires_grad_()
+        y = ex.linear(t["x"], codes, su, sv, 2, scale, A=t["A"], B=t["B"], **kw)
+        assert torch.equal(y, plain) and y.requires_grad
+        y.backward(c)
+        for k, v in t.items():
+            assert (v.grad is not None) == (k in wanted)
+            if k in wanted:
+                assert torch.equal(v.grad, want["d" + k])
+    # without adapters, and a gradient without strides of its own
+    u = x.clone().requires_grad_()
+    ex.linear(u, codes, su, sv, 2, scale, transposed=tr).sum().backward()
+    ones = torch.ones(T, n_out, dtype=torch.bfloat16, device=DEV)
+    assert torch.equal(u.grad, ex.linear_backward(ones, None, codes, su, sv, 2, scale, transposed=tr)["dx"])
+    with torch.no_grad():
+        assert not ex.linear(u, codes, su, sv, 2, scale, transposed=tr).requires_grad
+    # experts
+    off = torch.tensor([0, T // 3, T // 3, max(T - 1, 1)], dtype=torch.int32, device=DEV)
+    stack = [torch.stack([v] * 3) for v in (codes, su, sv)]
+    scales = torch.stack([scale] * 3)
+    u = x.clone().requires_grad_()
+    z = ex.expert_linear(u, off, *stack, 2, scales, transposed=tr)
+    z.backward(c)
+    assert torch.equal(z, ex.expert_linear(x, off, *stack, 2, scales, transposed=tr))
+    assert torch.equal(u.grad, ex.expert_linear(c, off, *stack, 2, scales, transposed=not tr))

@@ -82,3 +82,33 @@ def test_refuses_a_workspace_of_another_device(products, name):
     with pytest.raises(ValueError, match="workspace"):
         calls(products, Placed)[name](placed(256, dtype=torch.uint8, cls=Elsewhere))
     assert not products._fn.seen
+
+
+def test_refuses_what_would_lose_a_gradient(products):
+    """A result written to `out`, and factors whose gradients nobody computes."""
+    bf16 = torch.bfloat16
+    x, y, ws = placed(2, 256, dtype=bf16), placed(2, 128, dtype=bf16), placed(256, dtype=torch.uint8)
+    codes, su, sv, s = placed(16, 8, 32, dtype=torch.int16), placed(256), placed(128), placed()
+    ad = dict(A=placed(1, 4, 256, dtype=bf16), B=placed(1, 4, 128, dtype=bf16), gain=placed(1), slots=placed(2, dtype=torch.int32))
+    e = dict(offsets=placed(2, dtype=torch.int32), codes=codes[None], su=su[None], sv=sv[None], scale=s[None])
+
+    def wants(t):
+        return t.detach().clone().as_subclass(Placed).requires_grad_()
+
+    def linear(**kw):
+        return products.linear(**{**dict(x=x, codes=codes, su=su, sv=sv, K=2, scale=s, out=y, ws=ws), **ad, **kw})
+
+    def experts(**kw):
+        return products.expert_linear(**{**dict(x=x, K=2, out=y, ws=ws), **e, **kw})
+
+    linear(), experts()
+    assert len(products._fn.seen) == 2
+    for call, bad in ((linear, dict(x=wants(x))), (linear, dict(A=wants(ad["A"]))), (linear, dict(B=wants(ad["B"]))),
+                      (linear, dict(gain=wants(ad["gain"]))), (linear, dict(su=wants(su))), (linear, dict(sv=wants(sv))),
+                      (linear, dict(scale=wants(s))), (experts, dict(x=wants(x))), (experts, dict(su=wants(e["su"]))),
+                      (experts, dict(sv=wants(e["sv"]))), (experts, dict(scale=wants(e["scale"])))):
+        with pytest.raises(ValueError, match="gradient"):
+            call(**bad)
+        with torch.no_grad():
+            call(**bad)
+    assert len(products._fn.seen) == 2 + 11
