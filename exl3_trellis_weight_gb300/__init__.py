@@ -14,6 +14,7 @@ plus the workspace queries.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 
@@ -22,10 +23,15 @@ __all__ = [
     "encode_rows", "decode_rows",
     "quantize", "gss_scale", "scale_search", "scale_search_workspace_bytes", "encode_workspace_bytes", "encode_workspace_min_bytes",
     "quantize_workspace_bytes", "gss_workspace_bytes", "mse_workspace_bytes",
-    "linear", "linear_backward", "expert_linear", "linear_workspace_bytes",
-    "linear_backward_workspace_bytes", "expert_linear_workspace_bytes",
     "supports_k", "rotate_last_kernel", "profile_enable", "profile_read", "wait_timeouts", "EXL3_F32", "EXL3_BF16", "EXL3_F16",
 ]
+
+# loaded with their first use (__getattr__): they need torch at import, which the rest
+# takes when it is called, so without torch they are no part of a star import
+_PRODUCTS = ("linear", "linear_backward", "expert_linear", "linear_workspace_bytes",
+             "linear_backward_workspace_bytes", "expert_linear_workspace_bytes")
+if importlib.util.find_spec("torch") is not None:
+    __all__ += _PRODUCTS
 
 EXL3_F32 = 0
 EXL3_BF16 = 1
@@ -444,13 +450,8 @@ def gss_scale(W, su, sv, K: int, lo: float = 0.5, hi: float = 2.0, n_eval: int =
     return dict(codes=best_codes, scale=scale, g=g, mse=m, history=hist)
 
 
-_PRODUCTS = ("linear", "linear_backward", "expert_linear", "linear_workspace_bytes",
-             "linear_backward_workspace_bytes", "expert_linear_workspace_bytes")
-
-
 def __getattr__(name):
-    """The products with coded matrices load with their first use: they need torch
-    at import, which the rest of the package takes only when it is called."""
+    """The products with coded matrices load with their first use."""
     if name in _PRODUCTS:
         from . import products
         value = globals()[name] = getattr(products, name)
