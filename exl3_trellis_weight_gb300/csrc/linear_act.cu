@@ -122,7 +122,7 @@ __device__ __forceinline__ void rotate_out128(float (&v)[16], const PrepLaunch &
 // threads, 16 inputs each.  ONE: a row fits one round of the block and stays in
 // registers, `left` too while the expert stays the same, and the next row is on its way.
 template <typename TX, bool VEC, bool ONE>
-__global__ void prep_kernel(const PrepLaunch a) {
+__global__ void __launch_bounds__(1024) prep_kernel(const PrepLaunch a) {
     __shared__ int32_t off[kMaxExperts + 1];
     __shared__ float wmax[2][32];
     extern __shared__ __align__(16) float parts[];

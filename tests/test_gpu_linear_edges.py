@@ -209,3 +209,21 @@ def test_gradients_flow_through_the_calls(ex, T, tr):
     z.backward(c)
     assert torch.equal(z, ex.expert_linear(x, off, *stack, 2, scales, transposed=tr))
     assert torch.equal(u.grad, ex.expert_linear(c, off, *stack, 2, scales, transposed=not tr))
+
+
+# ---- forms that only large sizes reach ------------------------------------------------
+
+@pytest.mark.parametrize("n", [16384, 16512, 28672])
+@pytest.mark.parametrize("tr", [False, True])
+def test_many_inputs(ex, n, tr):
+    """Rows longer than one round of the rotation's block, aligned and not."""
+    g = gen(n)
+    rows, cols = (128, n) if tr else (n, 128)
+    codes, su, sv, scale = coded(g, rows, cols, 2)
+    W = weight64(codes, su, sv, 2, scale)
+    W = W.t() if tr else W
+    for T in (3, 70):
+        for off in (8, 1):
+            x = torch.full((T, n + 16), float("nan"), dtype=torch.bfloat16, device=DEV)[:, off:off + n]
+            x.copy_(acts(g, T, n, "bf16"))
+            close(ex.linear(x, codes, su, sv, 2, scale, transposed=tr), x.double() @ W, (su if tr else sv).double(), "bf16")
