@@ -27,15 +27,6 @@ __device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
                  : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     return ok != 0u;
 }
-// whether a phase is over, without the wait that a try may do
-__device__ __forceinline__ bool bar_peek(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile("{\n\t.reg .pred p;\n\t"
-                 "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-                 "selp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-    return ok != 0u;
-}
 
 // Waits for a phase, about a second at most (2^31 cycles of the SM's clock, read
 // once in 64 tries).  False when it gave up, or when another wait of the block
