@@ -227,3 +227,132 @@ def test_many_inputs(ex, n, tr):
             x = torch.full((T, n + 16), float("nan"), dtype=torch.bfloat16, device=DEV)[:, off:off + n]
             x.copy_(acts(g, T, n, "bf16"))
             close(ex.linear(x, codes, su, sv, 2, scale, transposed=tr), x.double() @ W, (su if tr else sv).double(), "bf16")
+
+
+@pytest.mark.parametrize("K,dt,tr", [(1, "bf16", False), (4, "fp16", True), (2, "bf16", True), (3, "fp16", False)])
+def test_pairs_with_two_accumulators(ex, K, dt, tr):
+    """Tiles of more than 256 tokens, and more tiles than pairs of blocks."""
+    g = gen(60 + K)
+    codes, su, sv, scale = coded(g, 4096, 4096, K)
+    W = weight64(codes, su, sv, K, scale)
+    W = W.t() if tr else W
+    A, B, gain, ranks = adapters(g, 3, 8, 4096, 4096, dt)
+    for T in (333, 2100):
+        x = acts(g, T, 4096, dt)
+        slots = torch.randint(-1, 3, (T,), generator=g, device=DEV, dtype=torch.int32)
+        y = ex.linear(x, codes, su, sv, K, scale, transposed=tr, A=A, B=B, gain=gain, slots=slots, ranks=ranks)
+        term, err = adapter64(x, A, B, gain, slots, ranks)
+        base = x.double() @ W
+        close(y, base + term, (su if tr else sv).double(), dt, base, 6 * U[dt] / math.sqrt(3) * err)
+        bad = x.clone()
+        bad[1, 5], bad[T - 2, 9] = float("inf"), float("nan")
+        z = ex.linear(bad, codes, su, sv, K, scale, transposed=tr, A=A, B=B, gain=gain, slots=slots, ranks=ranks)
+        rest = torch.ones(T, dtype=torch.bool, device=DEV)
+        rest[[1, T - 2]] = False
+        assert torch.equal(z[rest], y[rest])
+        assert not torch.isfinite(z[~rest][:, (su if tr else sv) != 0]).any()
+
+
+@pytest.mark.parametrize("K", [1, 2, 3, 4])
+@pytest.mark.parametrize("tr", [False, True])
+def test_blocks_with_several_tiles(ex, K, tr):
+    """More tiles of 128 outputs than blocks: accumulators alternate, code rings go on."""
+    g = gen(70 + K)
+    rows, cols = (32768, 256) if tr else (256, 32768)
+    codes, su, sv, scale = coded(g, rows, cols, K)
+    W = weight64(codes, su, sv, K, scale)
+    W = W.t() if tr else W
+    for T in (65, 150, 256):
+        x = acts(g, T, 256, "bf16")
+        close(ex.linear(x, codes, su, sv, K, scale, transposed=tr), x.double() @ W, (su if tr else sv).double(), "bf16")
+
+
+@pytest.mark.parametrize("tr", [False, True])
+@pytest.mark.parametrize("K,counts", [(2, [1100, 0, 700]), (3, [13, 1027, 1480]), (4, [2000]), (1, [600] * 9)])
+def test_experts_in_pairs_and_many_tiles(ex, K, counts, tr):
+    """More than 512 rows an expert on average: pairs of blocks; odd and empty groups,
+    an odd number of output blocks."""
+    g = gen(80 + K)
+    E, rows, cols = len(counts), 384, 640
+    codes, su, sv, scale = coded(g, rows, cols, K, (E,))
+    off = torch.tensor([0] + list(np.cumsum(counts)), dtype=torch.int32, device=DEV)
+    T = int(off[-1])
+    x = acts(g, T, cols if tr else rows, "fp16")
+    x[3, 1], x[T - 1, 2] = float("inf"), float("nan")
+    y = ex.expert_linear(x, off, codes, su, sv, K, scale, transposed=tr)
+    ok = torch.isfinite(x.float()).all(1)
+    for e, m in enumerate(counts):
+        if m:
+            r = slice(int(off[e]), int(off[e + 1]))
+            W = weight64(codes[e], su[e], sv[e], K, scale[e])
+            right = (su if tr else sv)[e].double()
+            close(y[r][ok[r]], x[r][ok[r]].double() @ (W.t() if tr else W), right, "fp16")
+            assert not torch.isfinite(y[r][~ok[r]][:, right != 0]).any()
+
+
+def test_experts_with_many_tiles_alone(ex):
+    g = gen(90)
+    E, rows, cols, K = 64, 128, 1024, 3
+    codes, su, sv, scale = coded(g, rows, cols, K, (E,))
+    p = torch.rand(E, generator=g, device=DEV) ** 3
+    counts = torch.bincount(torch.multinomial(p, 1500, replacement=True, generator=g), minlength=E).tolist()
+    off = torch.tensor([0] + list(np.cumsum(counts)), dtype=torch.int32, device=DEV)
+    x = acts(g, 1500, rows, "bf16")
+    y = ex.expert_linear(x, off, codes, su, sv, K, scale)
+    for e, m in enumerate(counts):
+        r = slice(int(off[e]), int(off[e + 1]))
+        if m:
+            close(y[r], x[r].double() @ weight64(codes[e], su[e], sv[e], K, scale[e]), sv[e].double(), "bf16")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("T,n", [(4097, 3), (9001, 40)])
+def test_adapters_of_more_tokens_than_a_round_of_the_plan(ex, dt, T, n):
+    g = gen(T)
+    codes, su, sv, scale = coded(g, 128, 256, 2)
+    W = weight64(codes, su, sv, 2, scale)
+    A, B, gain, ranks = adapters(g, n, 8, 128, 256, dt)
+    slots = torch.randint(-1, n, (T,), generator=g, device=DEV, dtype=torch.int32)
+    x, dy = acts(g, T, 128, dt), acts(g, T, 256, dt, 0.1)
+    kw = dict(A=A, B=B, gain=gain, slots=slots, ranks=ranks)
+    y = ex.linear(x, codes, su, sv, 2, scale, **kw)
+    term, err = adapter64(x, A, B, gain, slots, ranks)
+    base = x.double() @ W
+    close(y, base + term, sv.double(), dt, base, 6 * U[dt] / math.sqrt(3) * err)
+    got = ex.linear_backward(dy, x, codes, su, sv, 2, scale, **kw)
+    term, err = adapter64(dy, B, A, gain, slots, ranks)
+    base = dy.double() @ W.t()
+    close(got["dx"], base + term, su.double(), dt, base, 6 * U[dt] / math.sqrt(3) * err)
+    for i in range(n):
+        t, k = torch.nonzero(slots == i).flatten(), int(ranks[i])
+        X, D = x[t].double(), dy[t].double()
+        gg, h = float(gain[i]) * (D @ B[i, :k].double().t()), float(gain[i]) * (X @ A[i, :k].double().t())
+        for name, p, q in (("dA", gg, X), ("dB", h, D)):
+            ref, e = p.t() @ q, (p.pow(2).t() @ q.pow(2)).sqrt()
+            tol = U[dt] * ref.abs() + 2.0 ** -25 + 6 * U[dt] / math.sqrt(3) * e
+            assert ((got[name][i, :k].double() - ref).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_rows_that_are_not_numbers_stay_alone(ex, dt):
+    """With adapters, in gradients and in few-row experts."""
+    g = gen(91)
+    codes, su, sv, scale = coded(g, 256, 384, 3)
+    for T in (4, 33, 64, 90):
+        A, B, gain, ranks = adapters(g, 2, 8, 256, 384, dt)
+        slots = (torch.arange(T, device=DEV) % 3 - 1).int()
+        x, dy = acts(g, T, 256, dt), acts(g, T, 384, dt)
+        bad, dbad = x.clone(), dy.clone()
+        bad[1, 7], bad[T - 1, 130] = float("-inf"), float("nan")
+        dbad[1, 7], dbad[T - 1, 130] = float("nan"), float("inf")
+        rest = torch.ones(T, dtype=torch.bool, device=DEV)
+        rest[[1, T - 1]] = False
+        kw = dict(A=A, B=B, gain=gain, slots=slots, ranks=ranks)
+        y, z = (ex.linear(v, codes, su, sv, 3, scale, **kw) for v in (x, bad))
+        assert torch.equal(y[rest], z[rest]) and not torch.isfinite(z[~rest][:, sv != 0]).any()
+        y, z = (ex.linear_backward(v, x, codes, su, sv, 3, scale, **kw)["dx"] for v in (dy, dbad))
+        assert torch.equal(y[rest], z[rest]) and not torch.isfinite(z[~rest]).any()
+        off = torch.tensor([0, 2, 2, T - 1, T], dtype=torch.int32, device=DEV)
+        stack = [torch.stack([v] * 4) for v in (codes, su, sv)]
+        y, z = (ex.expert_linear(v, off, *stack, 3, torch.stack([scale] * 4)) for v in (x, bad))
+        assert torch.equal(y[rest], z[rest]) and not torch.isfinite(z[~rest][:, sv != 0]).any()
