@@ -148,6 +148,18 @@ def _stream(device):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
+def _run(name, device, *args):
+    """The entry point on the current stream of the tensors' device, with that device
+    current: the library launches on the current one, which need not be theirs."""
+    torch = _torch()
+    entry, stream = getattr(lib(), name), _stream(device)
+    if torch.cuda.current_device() == device.index:
+        _check(entry(*args, stream))
+    else:
+        with torch.cuda.device(device):
+            _check(entry(*args, stream))
+
+
 def _need_cuda(*ts):
     for t in ts:
         if t is not None and not t.is_cuda:
@@ -193,8 +205,8 @@ def profile_read():
 
 def wait_timeouts() -> int:
     """exl3_wait_timeouts -> number of bounded device waits that expired since
-    the last call (the TMA forward rotation's waits on its tile loads);
-    synchronises the device and resets the count.  A nonzero count means the
+    the last call (of the TMA forward rotation and of the products with coded
+    matrices); synchronises the device and resets the count.  A nonzero count means the
     launches concerned produced void results."""
     n = ctypes.c_uint(0)
     st = lib().exl3_wait_timeouts(ctypes.byref(n))
@@ -240,8 +252,8 @@ def rotate(W, su, sv, inverse: bool = False, out=None):
     rows, cols = W.shape
     if out is None:
         out = torch.empty(rows, cols, dtype=torch.float32, device=W.device)
-    _check(lib().exl3_rotate(_ptr(W), _dt(W), rows, cols, _ptr(su), _ptr(sv), int(bool(inverse)),
-                             _ptr(out), _stream(W.device)))
+    _run("exl3_rotate", W.device, _ptr(W), _dt(W), rows, cols, _ptr(su), _ptr(sv), int(bool(inverse)),
+         _ptr(out))
     return out
 
 
@@ -257,9 +269,8 @@ def encode_tiles(Y, K: int, scale: float = 1.0, codes=None, tile_cost=None,
     if want_cost and tile_cost is None:
         tile_cost = torch.empty(n, dtype=torch.float32, device=Y.device)
     ws = _workspace(encode_workspace_bytes(n, K), Y.device, ws)
-    _check(lib().exl3_encode_tiles(_ptr(Y), rows, cols, K, ctypes.c_float(scale), _ptr(codes),
-                                   _ptr(tile_cost), _ptr(ws), ws.numel() * ws.element_size(),
-                                   _stream(Y.device)))
+    _run("exl3_encode_tiles", Y.device, _ptr(Y), rows, cols, K, ctypes.c_float(scale), _ptr(codes),
+         _ptr(tile_cost), _ptr(ws), ws.numel() * ws.element_size())
     return (codes, tile_cost) if want_cost or tile_cost is not None else codes
 
 
@@ -274,9 +285,8 @@ def encode_rows(Y, K: int, scale: float = 1.0, codes=None, row_cost=None,
     if want_cost and row_cost is None:
         row_cost = torch.empty(n_rows, dtype=torch.float32, device=Y.device)
     ws = _workspace(encode_workspace_bytes(n_rows, K), Y.device, ws)
-    _check(lib().exl3_encode_rows(_ptr(Y), n_rows, T, K, ctypes.c_float(scale), _ptr(codes),
-                                  _ptr(row_cost), _ptr(ws), ws.numel() * ws.element_size(),
-                                  _stream(Y.device)))
+    _run("exl3_encode_rows", Y.device, _ptr(Y), n_rows, T, K, ctypes.c_float(scale), _ptr(codes),
+         _ptr(row_cost), _ptr(ws), ws.numel() * ws.element_size())
     return (codes, row_cost) if want_cost or row_cost is not None else codes
 
 
@@ -286,8 +296,7 @@ def decode_rows(codes, n_rows: int, T: int, K: int, scale: float = 1.0, out=None
     _need_cuda(codes, out)
     if out is None:
         out = torch.empty(n_rows, T, dtype=torch.float32, device=codes.device)
-    _check(lib().exl3_decode_rows(_ptr(codes), n_rows, T, K, ctypes.c_float(scale), _ptr(out),
-                                  _stream(codes.device)))
+    _run("exl3_decode_rows", codes.device, _ptr(codes), n_rows, T, K, ctypes.c_float(scale), _ptr(out))
     return out
 
 
@@ -297,8 +306,8 @@ def decode_tiles(codes, rows: int, cols: int, K: int, scale: float = 1.0, out=No
     _need_cuda(codes, out)
     if out is None:
         out = torch.empty(rows, cols, dtype=torch.float32, device=codes.device)
-    _check(lib().exl3_decode_tiles(_ptr(codes), rows, cols, K, ctypes.c_float(scale), _ptr(out),
-                                   _stream(codes.device)))
+    _run("exl3_decode_tiles", codes.device, _ptr(codes), rows, cols, K, ctypes.c_float(scale),
+         _ptr(out))
     return out
 
 
@@ -310,8 +319,8 @@ def mse(W, What, out=None, ws=None):
     if out is None:
         out = torch.empty((), dtype=torch.float64, device=W.device)
     ws = _workspace(mse_workspace_bytes(rows, cols), W.device, ws)
-    _check(lib().exl3_mse(_ptr(W), _dt(W), _ptr(What), rows, cols, _ptr(out), _ptr(ws),
-                          ws.numel() * ws.element_size(), _stream(W.device)))
+    _run("exl3_mse", W.device, _ptr(W), _dt(W), _ptr(What), rows, cols, _ptr(out), _ptr(ws),
+         ws.numel() * ws.element_size())
     return out
 
 
@@ -331,10 +340,9 @@ def quantize(W, su, sv, K: int, g: float = 1.0, codes=None, want_What: bool = Fa
     sigma = torch.empty((), dtype=torch.float64, device=dev)
     What = torch.empty(rows, cols, dtype=torch.float32, device=dev) if want_What else None
     ws = _workspace(quantize_workspace_bytes(rows, cols, K), dev, ws)
-    _check(lib().exl3_quantize(_ptr(W), _dt(W), rows, cols, _ptr(su), _ptr(sv), K,
-                               ctypes.c_double(g), _ptr(codes), _ptr(scale), _ptr(m), _ptr(sigma),
-                               _ptr(What), _ptr(ws), ws.numel() * ws.element_size(),
-                               _stream(dev)))
+    _run("exl3_quantize", dev, _ptr(W), _dt(W), rows, cols, _ptr(su), _ptr(sv), K, ctypes.c_double(g),
+         _ptr(codes), _ptr(scale), _ptr(m), _ptr(sigma), _ptr(What), _ptr(ws),
+         ws.numel() * ws.element_size())
     return dict(codes=codes, scale=scale, mse=m, sigma=sigma, What=What)
 
 
@@ -353,9 +361,8 @@ def scale_search(W, su, sv, K: int, want_history: bool = True, ws=None):
     scale = torch.empty((), dtype=torch.float32, device=dev)
     hist = torch.empty(54, dtype=torch.float64, device=dev) if want_history else None
     ws = _workspace(scale_search_workspace_bytes(rows, cols, K), dev, ws)
-    _check(lib().exl3_scale_search(_ptr(W), _dt(W), rows, cols, _ptr(su), _ptr(sv), K, _ptr(g),
-                                   _ptr(scale), _ptr(hist), _ptr(ws), ws.numel() * ws.element_size(),
-                                   _stream(dev)))
+    _run("exl3_scale_search", dev, _ptr(W), _dt(W), rows, cols, _ptr(su), _ptr(sv), K, _ptr(g),
+         _ptr(scale), _ptr(hist), _ptr(ws), ws.numel() * ws.element_size())
     return dict(g=g, scale=scale, history=None if hist is None else hist.view(27, 2))
 
 
@@ -376,9 +383,8 @@ def block_ldl(H, sigma_reg: float = 0.01, max_retries: int = 10, M=None, ws=None
         M = torch.empty(n, n, dtype=torch.float32, device=H.device)
     ws = _workspace(block_ldl_workspace_bytes(n), H.device, ws)
     retries = ctypes.c_int(-1)
-    _check(lib().exl3_block_ldl(_ptr(H), n, ctypes.c_double(sigma_reg), int(max_retries), _ptr(M),
-                                ctypes.byref(retries), _ptr(ws), ws.numel() * ws.element_size(),
-                                _stream(H.device)))
+    _run("exl3_block_ldl", H.device, _ptr(H), n, ctypes.c_double(sigma_reg), int(max_retries), _ptr(M),
+         ctypes.byref(retries), _ptr(ws), ws.numel() * ws.element_size())
     return M, retries.value
 
 
@@ -398,8 +404,8 @@ def ldlq(R, M, K: int, scale: float, want_q: bool = True, codes=None, ws=None):
         codes = torch.empty(rows // 16, cols // 16, 16 * K, dtype=torch.int16, device=dev)
     Q = torch.empty(rows, cols, dtype=torch.float32, device=dev) if want_q else None
     ws = _workspace(ldlq_workspace_bytes(rows, cols, K), dev, ws)
-    _check(lib().exl3_ldlq(_ptr(R), rows, cols, _ptr(M), K, ctypes.c_float(scale), _ptr(codes),
-                           _ptr(Q), _ptr(ws), ws.numel() * ws.element_size(), _stream(dev)))
+    _run("exl3_ldlq", dev, _ptr(R), rows, cols, _ptr(M), K, ctypes.c_float(scale), _ptr(codes), _ptr(Q),
+         _ptr(ws), ws.numel() * ws.element_size())
     return dict(codes=codes, Q=Q)
 
 
@@ -420,9 +426,8 @@ def regularize(W, h, sv, apply_out: int = -1, W_out=None, ws=None):
     sv_out = torch.empty(cols, dtype=torch.float32, device=dev)
     info = torch.empty(4, dtype=torch.float64, device=dev)
     ws = _workspace(regularize_workspace_bytes(rows, cols), dev, ws)
-    _check(lib().exl3_regularize(_ptr(W), _dt(W), rows, cols, _ptr(h), _ptr(sv), int(apply_out),
-                                 _ptr(W_out), _ptr(sv_out), _ptr(info), _ptr(ws),
-                                 ws.numel() * ws.element_size(), _stream(dev)))
+    _run("exl3_regularize", dev, _ptr(W), _dt(W), rows, cols, _ptr(h), _ptr(sv), int(apply_out),
+         _ptr(W_out), _ptr(sv_out), _ptr(info), _ptr(ws), ws.numel() * ws.element_size())
     return dict(W_out=W_out, sv_out=sv_out, info=info)
 
 
@@ -443,10 +448,9 @@ def gss_scale(W, su, sv, K: int, lo: float = 0.5, hi: float = 2.0, n_eval: int =
     m = torch.empty((), dtype=torch.float64, device=dev)
     hist = torch.empty(2 * n_eval, dtype=torch.float64, device=dev) if want_history else None
     ws = _workspace(gss_workspace_bytes(rows, cols, K), dev, ws)
-    _check(lib().exl3_gss_scale(_ptr(W), _dt(W), rows, cols, _ptr(su), _ptr(sv), K,
-                                ctypes.c_double(lo), ctypes.c_double(hi), int(n_eval),
-                                _ptr(best_codes), _ptr(scale), _ptr(g), _ptr(m), _ptr(hist),
-                                _ptr(ws), ws.numel() * ws.element_size(), _stream(dev)))
+    _run("exl3_gss_scale", dev, _ptr(W), _dt(W), rows, cols, _ptr(su), _ptr(sv), K, ctypes.c_double(lo),
+         ctypes.c_double(hi), int(n_eval), _ptr(best_codes), _ptr(scale), _ptr(g), _ptr(m),
+         _ptr(hist), _ptr(ws), ws.numel() * ws.element_size())
     return dict(codes=best_codes, scale=scale, g=g, mse=m, history=hist)
 
 
