@@ -326,7 +326,7 @@ template <typename TX, bool VEC, int MB> __global__ void __launch_bounds__(256, 
 // what it moves: 4096 tokens forward take 176 us so, 161 with the term in 16 bits in y.)
 // A block takes one tile and 512 outputs, 128 at a time; warp w the tokens 16 (w % 2) ..
 // and 32 of the outputs, whose sums go out in whole 32-byte sectors as they stand in the
-// registers.
+// registers.  Bound by these stores: 4096 x 4096, rank 16: 19 us, 3.4 TB/s written.
 template <typename TX> __global__ void __launch_bounds__(256) expand_kernel(const AdaptLaunch a, float *term) {
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ float downs[kTile];

@@ -379,6 +379,17 @@ namespace {
 
 // Tokens of a block, blocks of a cluster and shared memory; false when there are
 // too many tokens, or when the activations of a block do not fit it.
+//
+// Both sides, rotation and product in a replayed graph, us, this kernel / linear_product.cu:
+//   4096 -> 1024, K = 2     8 tokens 10.6 / 11.9   16: 12.1 / 12.0   32: 15.1 / 13.0
+//   4096 -> 4096, K = 3     8 tokens 14.4 / 14.7   16: 16.8 / 14.7   32: 32.0 / 16.6
+//   4096 -> 12288, K = 4    8 tokens 27.2 / 29.5   16: 30.0 / 29.8   32: 41.2 / 30.1
+//   12288 -> 4096, K = 1    8 tokens 24.6 / 26.4   16: 27.4 / 26.6   32: 60.7 / 29.3
+//   64 experts 2048 -> 1024, K = 2, even    8 rows each 67.0 / 69.3   16: 70.2 / 70.9   32: 78.3 / 73.7
+//     the same, skewed (largest 6 times)    8 rows each 53.8 / 54.4   16: 72.1 / 56.9   32: 108.5 / 60.8
+//   16 experts, K = 3, even                 8 rows each 19.5 / 22.8   16: 20.1 / 22.9   32: 22.8 / 23.4
+// So it wins up to 8 tokens, is about even at 16 and loses from 17 on, where a block has 32
+// token columns: the limits, 32 tokens and 16 rows an expert, are not where the sides cross.
 bool plan_few(const ProductLaunch &p, FewArgs &a, unsigned &grid, uint32_t &smem) {
     if (p.offsets ? p.T > 16 * (int64_t)p.E : p.T > kTok)
         return false;

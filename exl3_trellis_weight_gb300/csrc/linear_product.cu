@@ -28,8 +28,9 @@
 // the matrix instructions 512 for 256 tokens (1024 for a pair's 512), and shared memory
 // about 900 in a pair (writing and reading both operands); measured are 1000 a step, up
 // to 480 tokens in a pair, because the roles share the issue slots and the shared
-// memory.  4096 x 4096 x 4096, K = 2, in pairs: 110 us, 1.25 PFLOP/s; 333 tokens x 4096
-// x 12288, K = 4, in pairs: 48 us.
+// memory.  4096 x 4096 x 4096, K = 2, in pairs: 119 us with the rotation before it, and
+// the kernel alone 122 to 125 where it adds adapters' terms (64 MB more to read, which the
+// ends of its two rounds wait for); 1001 tokens x 4096 x 4096, K = 4, with terms: 48 us.
 //
 // With few tiles (decode), the sum is split over the `split` blocks of a
 // cluster; each leaves its partial sums in its shared memory and block r adds
@@ -654,7 +655,12 @@ exl3_status launch_product(const ProductLaunch &p, cudaStream_t s) {
     // pass behind the next tile's sums unless that needs both accumulators.  (333 tokens,
     // 4096 x 12288: 70 us alone in two rounds, 48 in pairs; 4096 tokens of 4096 x 4096 in
     // tiles of 480: 116 us, of 256: 153.)  The experts' tokens are not known here: pairs
-    // when an expert has more than 512 on average.
+    // when an expert has more than 512 on average.  (Pairs / alone, us with the rotation: 16
+    // experts 2048 -> 1024, K = 2, of 256 rows each 40.5 / 39.6, 400: 52.7 / 60.7, 600: 80.8 /
+    // 86.3, 1024: 115 / 124; skewed, 400 on average 81.9 / 63.2, 600: 93.7 / 88.6, 1024: 132 /
+    // 125.  8 experts 4096 -> 4096, K = 4, 400 each 115 / 155, 600: 206 / 219, 1024: 254 / 287;
+    // skewed, 400: 146 / 158, 600: 177 / 203, 1024: 292 / 317.  Below 256 alone is ahead, from
+    // there to 512 it goes by the rounds, which the host does not know.)
     int pair_n = 0;
     if (p.offsets) {
         pair_n = p.T > 512 * (int64_t)p.E ? 512 : 0;
