@@ -9,6 +9,7 @@ the shared library is missing or CUDA is unavailable, the calls raise.
 Entry points (same names as the C ABI, without the ``exl3_`` prefix):
   rotate, encode_tiles, decode_tiles, mse, quantize, gss_scale
   linear, linear_backward, expert_linear (products with coded matrices)
+  rms_norm, rms_norm_backward, quantize8, linear8 (what stands around them in a layer)
 plus the workspace queries.
 """
 from __future__ import annotations
@@ -24,18 +25,22 @@ __all__ = [
     "quantize", "gss_scale", "scale_search", "scale_search_workspace_bytes", "encode_workspace_bytes", "encode_workspace_min_bytes",
     "quantize_workspace_bytes", "gss_workspace_bytes", "mse_workspace_bytes",
     "supports_k", "rotate_last_kernel", "profile_enable", "profile_read", "wait_timeouts", "EXL3_F32", "EXL3_BF16", "EXL3_F16",
+    "EXL3_E4M3",
 ]
 
 # loaded with their first use (__getattr__): they need torch at import, which the rest
 # takes when it is called, so without torch they are no part of a star import
 _PRODUCTS = ("linear", "linear_backward", "expert_linear", "linear_workspace_bytes",
              "linear_backward_workspace_bytes", "expert_linear_workspace_bytes")
+_LAYER = ("rms_norm", "rms_norm_backward", "quantize8", "linear8", "rms_norm_backward_workspace_bytes",
+          "linear8_workspace_bytes")
 if importlib.util.find_spec("torch") is not None:
-    __all__ += _PRODUCTS
+    __all__ += _PRODUCTS + _LAYER
 
 EXL3_F32 = 0
 EXL3_BF16 = 1
 EXL3_F16 = 2
+EXL3_E4M3 = 3
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libexl3.so")
@@ -120,7 +125,15 @@ def lib():
         L.exl3_expert_linear_workspace_bytes.restype = sz
         L.exl3_expert_linear.argtypes = [P, i32, i64, i64, P, i32, P, i64, i64, i32, P, P, P, i32,
                                          P, i64, P, sz, P]
-        for name in ("exl3_linear", "exl3_linear_backward", "exl3_expert_linear", "exl3_regularize", "exl3_block_ldl", "exl3_ldlq", "exl3_scale_search", "exl3_encode_rows", "exl3_decode_rows", "exl3_profile_read", "exl3_wait_timeouts", "exl3_rotate", "exl3_encode_tiles", "exl3_decode_tiles", "exl3_mse",
+        L.exl3_rms_norm.argtypes = [P, i32, i64, i64, i64, P, i64, P, i32, f32, P, i64, P, i64, P, P, P]
+        L.exl3_rms_norm_backward_workspace_bytes.argtypes = [i64, i64]
+        L.exl3_rms_norm_backward_workspace_bytes.restype = sz
+        L.exl3_rms_norm_backward.argtypes = [P, i64, P, i64, i32, i64, i64, P, i32, f32, P, i64, P, i64, P, P, sz, P]
+        L.exl3_quantize8.argtypes = [P, i32, i64, i64, i64, i32, P, P, P]
+        L.exl3_linear8_workspace_bytes.argtypes = [i64, i64, i64, i32]
+        L.exl3_linear8_workspace_bytes.restype = sz
+        L.exl3_linear8.argtypes = [P, i32, i64, i64, P, i64, i64, P, P, i64, i64, i32, P, i32, i64, P, sz, P]
+        for name in ("exl3_rms_norm", "exl3_rms_norm_backward", "exl3_quantize8", "exl3_linear8", "exl3_linear", "exl3_linear_backward", "exl3_expert_linear", "exl3_regularize", "exl3_block_ldl", "exl3_ldlq", "exl3_scale_search", "exl3_encode_rows", "exl3_decode_rows", "exl3_profile_read", "exl3_wait_timeouts", "exl3_rotate", "exl3_encode_tiles", "exl3_decode_tiles", "exl3_mse",
                      "exl3_quantize", "exl3_gss_scale"):
             getattr(L, name).restype = i32
         _lib = L
@@ -455,9 +468,12 @@ def gss_scale(W, su, sv, K: int, lo: float = 0.5, hi: float = 2.0, n_eval: int =
 
 
 def __getattr__(name):
-    """The products with coded matrices load with their first use."""
+    """The products with coded matrices and what stands around them load with their first use."""
     if name in _PRODUCTS:
-        from . import products
-        value = globals()[name] = getattr(products, name)
-        return value
-    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+        from . import products as module
+    elif name in _LAYER:
+        from . import layer as module
+    else:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    value = globals()[name] = getattr(module, name)
+    return value

@@ -211,6 +211,8 @@ exl3_status launch_rotate_fwd_tma(const RotateLaunch &p, cudaStream_t s);
 exl3_status rot_take_wait_timeouts(unsigned int *n);
 // the same of the products with coded matrices (linear_product.cu)
 exl3_status product_take_wait_timeouts(unsigned int *n);
+// the same of the products in 8 bits (linear8.cu)
+exl3_status linear8_take_wait_timeouts(unsigned int *n);
 
 // grid-and-parabola scale search (scale_search.cu)
 struct GridSearchLaunch {

@@ -1,0 +1,536 @@
+// linear8.cu -- y = x W (or x W^T) with both in e4m3, x with a scale for each 128 inputs of
+// a token, W with one for each block of 128 x 128:
+//   y[t][f] = sum over blocks b of 128 inputs of  xs[t][b] ws[b][f / 128] sum_{k in b} x8[t][k] w8[k][f]
+//
+// The inner sums are whole steps of the tensor cores: 128 inputs are one row of a swizzled
+// operand and four instructions.  Their result leaves tensor memory after every step and is
+// added up in registers in binary32 under its scale, while the next steps' products run into
+// other columns of tensor memory.
+//
+// Two forms.  Few tokens (SWAP): the 128 rows of the instruction are outputs, tokens its
+// columns, and the blocks of a cluster share the inputs of a tile; bound by reading the
+// weights.  Many tokens: the rows are tokens, 128 or 256 outputs the columns, so that the
+// scale is one factor of a thread's whole row; bound by the tensor cores.  A weight matrix
+// is used as it lies, the operand's rows run along its inputs or along its outputs.
+//
+// Warps: accumulators to registers (four for each half of the columns), one that copies
+// tiles, one that issues the matrix instructions.
+#include "layer.cuh"
+#include "linear_rotate.cuh"
+#include "tc.cuh"
+#include "tensor_map.cuh"
+
+namespace exl3 {
+
+namespace {
+
+using namespace tc;
+
+__device__ unsigned int g_linear8_timeouts;
+
+struct Args8 {
+    const float *xs;
+    int64_t xs_t, xs_b;
+    const float *ws;
+    int ws_o, ws_k;          // steps between the scales of neighbouring outputs and inputs
+    int64_t T;
+    int n_out, blocks_k;     // outputs, blocks of 128 inputs
+    int split;               // blocks of a cluster
+    int tiles_t, tiles_f;    // tiles along tokens and outputs
+    void *y;
+    int dt;
+    int64_t y_stride;
+    bool behind;
+};
+
+// TN: columns of a tile (tokens with SWAP, else outputs); MN: W's rows run along its outputs
+template <int TN, bool SWAP, bool MN> struct Form {
+    static constexpr int kHalves = TN == 16 ? 1 : 2, kCols = TN / kHalves;     // columns of a result warp
+    static constexpr int kOutWarps = 4 * kHalves, kThreads8 = (kOutWarps + 2) * 32;
+    static constexpr int kCopy = kOutWarps, kIssue = kOutWarps + 1;            // warps
+    // results of a step in tensor memory: kAcc of them; what a block takes of it goes with
+    // what it takes of shared memory (128 columns with more than a quarter, 512 with all but
+    // 56 KB), so that blocks that fit an SM together never wait for each other's
+    static constexpr int kAcc = SWAP ? 128 / TN : 512 / TN, kTmem = SWAP ? 128 : 512;
+    static constexpr uint32_t kA = 16384, kB = TN * 128, kStage = kA + kB;
+    static constexpr int kStages = SWAP ? 4 : TN == 128 ? 6 : 4;
+    static constexpr uint32_t kSums = TN * 512;                                // split: the block's sums
+    static constexpr uint32_t kSmem = kStages * kStage + 1024;
+    static_assert(kSums <= kStages * kStage, "sums in the place of the stages");
+    static_assert(SWAP ? kSmem > 57 * 1024 : kSmem > 171 * 1024, "shared memory keeps tensor memory apart");
+};
+
+template <int COLS> __device__ __forceinline__ void tmem_alloc(uint32_t dst) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "n"(COLS) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+template <int COLS> __device__ __forceinline__ void tmem_free(uint32_t addr) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "n"(COLS));
+}
+
+// 16 columns of this warp's 32 lanes, asked for; they are there after the next tmem_wait
+__device__ __forceinline__ void tmem_ask16(uint32_t addr, uint32_t (&r)[16]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(addr));
+}
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+}
+
+// e4m3 operands, binary32 accumulators; a_mn, b_mn: the operand's rows run along M or N
+__device__ __forceinline__ uint32_t shape_e4m3(int m, int n, bool a_mn, bool b_mn) {
+    return 1u << 4 | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 | (uint32_t)(m >> 4) << 24;
+}
+__device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t shape, bool add) {
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "setp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(shape), "r"((uint32_t)add)
+                 : "memory");
+}
+
+// a tile of a tensor map; the innermost coordinate is a multiple of 128 bytes
+__device__ __forceinline__ void tile_load(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
+    asm volatile("cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+                 "l"(map), "r"(x), "r"(y), "r"(bar)
+                 : "memory");
+}
+
+// acc <- acc + f d for two neighbours
+__device__ __forceinline__ void add_scaled(float &a0, float &a1, float f0, float f1, uint32_t d0, uint32_t d1) {
+    asm("{\n\t.reg .b64 a, d, f;\n\t"
+        "mov.b64 a, {%0, %1};\n\t"
+        "mov.b64 f, {%2, %3};\n\t"
+        "mov.b64 d, {%4, %5};\n\t"
+        "fma.rn.f32x2 a, d, f, a;\n\t"
+        "mov.b64 {%0, %1}, a;\n\t}"
+        : "+f"(a0), "+f"(a1) : "f"(f0), "f"(f1), "r"(d0), "r"(d1));
+}
+
+__device__ __forceinline__ uint32_t pack_dt(int dt, float a, float b) {
+    return dt == EXL3_BF16 ? pack2<__nv_bfloat16>(a, b) : pack2<__half>(a, b);
+}
+
+template <int TN, bool SWAP, bool MN>
+__global__ void __launch_bounds__(Form<TN, SWAP, MN>::kThreads8, SWAP ? 2 : 1)
+    linear8_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ Args8 a) {
+    using F = Form<TN, SWAP, MN>;
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ __align__(8) unsigned long long bars[2 * F::kStages + 2 * F::kAcc + 1];
+    __shared__ __align__(16) float factors[SWAP ? F::kOutWarps : 1][2][SWAP ? F::kCols : 4];
+    __shared__ uint32_t tmem_at;
+    __shared__ int gave_up;
+    const uint32_t base = (saddr(smem_raw) + 1023u) & ~1023u;
+    const uint32_t bar0 = saddr(bars);
+    auto full = [&](uint32_t s) { return bar0 + 8u * s; };
+    auto empty = [&](uint32_t s) { return bar0 + 8u * (F::kStages + s); };
+    auto acc_full = [&](uint32_t d) { return bar0 + 8u * (2 * F::kStages + d); };
+    auto acc_empty = [&](uint32_t d) { return bar0 + 8u * (2 * F::kStages + F::kAcc + d); };
+    const uint32_t drained = bar0 + 8u * (2 * F::kStages + 2 * F::kAcc);
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    const int rank = a.split > 1 ? (int)(blockIdx.x % a.split) : 0;
+    unsigned int *const count = &g_linear8_timeouts;
+
+    if (tid == 0) {
+        for (int s = 0; s < F::kStages; s++) {
+            bar_init(full(s), 1);
+            bar_init(empty(s), 1);
+        }
+        for (int d = 0; d < F::kAcc; d++) {
+            bar_init(acc_full(d), 1);
+            bar_init(acc_empty(d), F::kOutWarps);
+        }
+        bar_init(drained, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        gave_up = 0;
+    }
+    if (warp == F::kIssue)
+        tmem_alloc<F::kTmem>(saddr(&tmem_at));
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = tmem_at;
+
+    // tiles of this block, and its share of the inputs; a tile's number counts tokens first,
+    // so that blocks running side by side share their weights
+    const int64_t tiles = (int64_t)a.tiles_t * a.tiles_f;
+    const int64_t it0 = blockIdx.x / a.split, dit = a.split > 1 ? tiles : gridDim.x;
+    const int k_lo = (int)((int64_t)a.blocks_k * rank / a.split), k_hi = (int)((int64_t)a.blocks_k * (rank + 1) / a.split);
+    const int steps = k_hi - k_lo;
+    constexpr int kRowsT = SWAP ? TN : 128, kRowsF = SWAP ? 128 : TN;          // tokens and outputs of a tile
+    auto t_of = [&](int64_t it) { return (it % a.tiles_t) * kRowsT; };
+    auto f_of = [&](int64_t it) { return (int)(it / a.tiles_t) * kRowsF; };
+    uint32_t issued = 0;                   // stages filled (of the thread that copies)
+
+    if (warp == F::kCopy) {
+        // ---- tiles of both operands, a stage for each 128 inputs ----
+        if (elect()) {
+            auto load_x = [&](uint32_t s, int64_t t0, int k) {
+                tile_load(base + s * F::kStage + (SWAP ? F::kA : 0u), &xmap, k * 128, (int)t0, full(s));
+            };
+            auto load_w = [&](uint32_t s, int f0, int k) {
+                const uint32_t to = base + s * F::kStage + (SWAP ? 0u : F::kA);
+#pragma unroll
+                for (int i = 0; i < kRowsF / 128; i++) {
+                    if (MN)
+                        tile_load(to + i * 16384u, &wmap, f0 + 128 * i, k * 128, full(s));
+                    else
+                        tile_load(to + i * 16384u, &wmap, k * 128, f0 + 128 * i, full(s));
+                }
+            };
+            // the weights of the first stages need not wait for the launch before this one
+            uint32_t ahead = 0;
+            if (a.behind && it0 < tiles) {
+                for (; ahead < F::kStages && (int)ahead < steps; ahead++) {
+                    bar_expect(full(ahead), F::kStage);
+                    load_w(ahead, f_of(it0), k_lo + (int)ahead);
+                }
+            }
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            uint32_t s = 0, phase = 1;     // (the phase before the first is over)
+            bool ok = true;
+            for (int64_t it = it0; ok && it < tiles; it += dit) {
+                const int64_t t0 = t_of(it);
+                const int f0 = f_of(it);
+                for (int k = k_lo; k < k_hi; k++) {
+                    if (!bar_wait(empty(s), phase, &gave_up, count)) {
+                        ok = false;
+                        break;
+                    }
+                    if (issued >= ahead) {
+                        bar_expect(full(s), F::kStage);
+                        load_w(s, f0, k);
+                    }
+                    load_x(s, t0, k);
+                    issued++;
+                    if (++s == F::kStages)
+                        s = 0, phase ^= 1;
+                }
+            }
+            if (gave_up) {
+                // nothing may be in flight when the block ends (a stage whose second copy was
+                // never asked for does not end: the wait is bounded, as its first copy is done by then)
+                const uint32_t most = issued > ahead ? issued : ahead;
+                for (uint32_t back = 1; back <= F::kStages && back <= most; back++)
+                    bar_drain(full((most - back) % F::kStages), ((most - back) / F::kStages) & 1);
+            }
+        }
+    } else if (warp == F::kIssue) {
+        // ---- matrix instructions ----
+        if (elect()) {
+            const bool a_mn = SWAP && MN, b_mn = !SWAP && MN;
+            const uint32_t shape = shape_e4m3(128, TN, a_mn, b_mn);
+            // 32 inputs on: 32 bytes of a row along K, or 32 rows
+            constexpr uint32_t kHopA = (SWAP && MN ? 4096u : 32u) >> 4, kHopB = (!SWAP && MN ? 4096u : 32u) >> 4;
+            uint32_t s = 0, s_phase = 0, d = 0, d_phase = 1;
+            for (int64_t it = it0; it < tiles && !gave_up; it += dit) {
+                for (int k = 0; k < steps; k++) {
+                    if (!bar_wait(acc_empty(d), d_phase, &gave_up, count) || !bar_wait(full(s), s_phase, &gave_up, count))
+                        break;
+                    fence_after();
+                    const uint64_t da = operand(base + s * F::kStage, 16, 1024);
+                    const uint64_t db = operand(base + s * F::kStage + F::kA, b_mn ? 16384 : 16, 1024);
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+                        mma_e4m3(tmem + d * TN, da + i * kHopA, db + i * kHopB, shape, i > 0);
+                    commit<false>(empty(s));
+                    commit<false>(acc_full(d));
+                    if (++s == F::kStages)
+                        s = 0, s_phase ^= 1;
+                    if (++d == F::kAcc)
+                        d = 0, d_phase ^= 1;
+                }
+            }
+            if (gave_up) {
+                commit<false>(drained);
+                bar_drain(drained, 0);
+            }
+        }
+    } else {
+        // ---- results ----
+        const int quarter = warp & 3, half = warp >> 2;
+        const int row = quarter * 32 + lane;             // of the tile: an output (SWAP) or a token
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        uint32_t d = 0, d_phase = 0;
+        bool ok = true;
+        for (int64_t it = it0; ok && it < tiles; it += dit) {
+            const int64_t t0 = t_of(it);
+            const int f0 = f_of(it);
+            // the factors of a step: of the thread's token, or of a column a lane
+            const int64_t t_mine = SWAP ? t0 + half * F::kCols + (lane % F::kCols) : t0 + row;
+            const bool have = t_mine < a.T;
+            const float *xs = a.xs + (have ? t_mine : 0) * a.xs_t + k_lo * a.xs_b;
+            const int fb = min(f0 + (SWAP ? 0 : half * F::kCols), a.n_out - 1) >> 7;
+            const float *ws = a.ws + (int64_t)fb * a.ws_o + (int64_t)k_lo * a.ws_k;
+            float acc[F::kCols];
+#pragma unroll
+            for (int c = 0; c < F::kCols; c++)
+                acc[c] = 0.0f;
+            auto factor = [&](int k) {
+                return have && k < steps ? __fmul_rn(__ldcg(xs + k * a.xs_b), __ldg(ws + (int64_t)k * a.ws_k)) : 0.0f;
+            };
+            float f_next = factor(0);
+            for (int k = 0; k < steps; k++) {
+                const float f = f_next;
+                f_next = factor(k + 1);
+                if (SWAP) {
+                    // (two places in turn: a step's reads are done before the barrier of the next)
+                    if (lane < F::kCols)
+                        factors[SWAP ? warp : 0][k & 1][lane] = f;
+                    __syncwarp();
+                }
+                ok = __all_sync(0xffffffffu, bar_wait(acc_full(d), d_phase, &gave_up, count));
+                if (!ok)
+                    break;
+                fence_after();
+                const uint32_t from = tmem + (uint32_t)(quarter * 32) * 65536u + d * TN + half * F::kCols;
+                uint32_t r[2][16];
+                tmem_ask16(from, r[0]);
+#pragma unroll
+                for (int c = 0; c < F::kCols; c += 16) {
+                    uint32_t(&now)[16] = r[(c >> 4) & 1];
+                    tmem_wait(now);
+                    if (c + 16 < F::kCols)
+                        tmem_ask16(from + c + 16, r[((c >> 4) + 1) & 1]);
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4) {
+                        float4 g = make_float4(f, f, f, f);
+                        if (SWAP)
+                            g = *reinterpret_cast<const float4 *>(&factors[SWAP ? warp : 0][k & 1][SWAP ? c + i : 0]);
+                        add_scaled(acc[c + i], acc[c + i + 1], g.x, g.y, now[i], now[i + 1]);
+                        add_scaled(acc[c + i + 2], acc[c + i + 3], g.z, g.w, now[i + 2], now[i + 3]);
+                    }
+                }
+                fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    bar_arrive(acc_empty(d));
+                if (++d == F::kAcc)
+                    d = 0, d_phase ^= 1;
+            }
+            if (!ok)
+                break;
+            if (a.split > 1) {
+                // every step's operands have been used: their place takes the sums, by column
+                float *const sums = reinterpret_cast<float *>(smem_raw + (base - saddr(smem_raw)));
+#pragma unroll
+                for (int c = 0; c < F::kCols; c++)
+                    sums[(half * F::kCols + c) * 128 + row] = acc[c];
+            } else if (SWAP) {
+                const int f = f0 + row;
+#pragma unroll
+                for (int c = 0; c < F::kCols; c++) {
+                    const int64_t t = t0 + half * F::kCols + c;
+                    if (f < a.n_out && t < a.T)
+                        reinterpret_cast<uint16_t *>(a.y)[t * a.y_stride + f] = (uint16_t)pack_dt(a.dt, acc[c], 0.0f);
+                }
+            } else if (have) {
+                uint16_t *y = reinterpret_cast<uint16_t *>(a.y) + t_mine * a.y_stride;
+                const bool wide = (((uintptr_t)a.y | (uintptr_t)(a.y_stride * 2)) & 15u) == 0;
+#pragma unroll
+                for (int c = 0; c < F::kCols; c += 8) {
+                    const int f = f0 + half * F::kCols + c;
+                    if (f < a.n_out) {     // (a multiple of 16)
+                        uint32_t q[4];
+#pragma unroll
+                        for (int i = 0; i < 4; i++)
+                            q[i] = pack_dt(a.dt, acc[c + 2 * i], acc[c + 2 * i + 1]);
+                        if (wide) {
+                            *reinterpret_cast<uint4 *>(y + f) = make_uint4(q[0], q[1], q[2], q[3]);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 8; i++)
+                                y[f + i] = (uint16_t)(q[i >> 1] >> (16 * (i & 1)));
+                        }
+                    }
+                }
+            }
+        }
+    }
+    __syncwarp();
+
+    if (a.split > 1) {
+        // the blocks' sums, added in block order: groups of 8 columns, 32 rows a warp
+        cluster_sync();
+        const int64_t t0 = t_of(it0);
+        const int f0 = f_of(it0);
+        const bool wide = (((uintptr_t)a.y | (uintptr_t)(a.y_stride * 2)) & 15u) == 0;
+        constexpr int kWarps8 = F::kThreads8 / 32;
+        if (SWAP) {
+            // a column is a token: a lane takes four outputs of it
+            for (int c = rank + warp * a.split; c < TN && t0 + c < a.T; c += kWarps8 * a.split) {
+                float4 v = {};
+                for (int b = 0; b < a.split; b++) {
+                    float4 u;
+                    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                 : "=f"(u.x), "=f"(u.y), "=f"(u.z), "=f"(u.w)
+                                 : "r"(at_block(base, b) + (uint32_t)(c * 128 + lane * 4) * 4u));
+                    v.x = __fadd_rn(v.x, u.x), v.y = __fadd_rn(v.y, u.y), v.z = __fadd_rn(v.z, u.z), v.w = __fadd_rn(v.w, u.w);
+                }
+                const int f = f0 + lane * 4;
+                if (f < a.n_out) {
+                    uint16_t *y = reinterpret_cast<uint16_t *>(a.y) + (t0 + c) * a.y_stride + f;
+                    const uint32_t q[2] = {pack_dt(a.dt, v.x, v.y), pack_dt(a.dt, v.z, v.w)};
+                    if (wide) {
+                        *reinterpret_cast<uint2 *>(y) = make_uint2(q[0], q[1]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; i++)
+                            y[i] = (uint16_t)(q[i >> 1] >> (16 * (i & 1)));
+                    }
+                }
+            }
+        } else {
+            // a column is an output: a lane takes eight of its token
+            for (int u = rank + warp * a.split; u < TN / 8 * 4; u += kWarps8 * a.split) {
+                const int c = u >> 2 << 3, row = (u & 3) * 32 + lane;
+                const int64_t t = t0 + row;
+                const int f = f0 + c;
+                if (t0 + (u & 3) * 32 >= a.T || f >= a.n_out)
+                    continue;
+                float v[8];
+#pragma unroll
+                for (int i = 0; i < 8; i++)
+                    v[i] = 0.0f;
+                for (int b = 0; b < a.split; b++) {
+                    const uint32_t from = at_block(base, b) + (uint32_t)(c * 128 + row) * 4u;
+#pragma unroll
+                    for (int i = 0; i < 8; i++) {
+                        float w;
+                        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(w) : "r"(from + i * 512u));
+                        v[i] = __fadd_rn(v[i], w);
+                    }
+                }
+                if (t < a.T) {
+                    uint16_t *y = reinterpret_cast<uint16_t *>(a.y) + t * a.y_stride + f;
+                    uint32_t q[4];
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+                        q[i] = pack_dt(a.dt, v[2 * i], v[2 * i + 1]);
+                    if (wide) {
+                        *reinterpret_cast<uint4 *>(y) = make_uint4(q[0], q[1], q[2], q[3]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; i++)
+                            y[i] = (uint16_t)(q[i >> 1] >> (16 * (i & 1)));
+                    }
+                }
+            }
+        }
+        cluster_sync();                    // no block ends while another may still read its sums
+    }
+    fence_before();
+    __syncthreads();
+    if (warp == F::kIssue) {
+        fence_after();
+        tmem_free<F::kTmem>(tmem);
+    }
+}
+
+// row-major [rows, cols] bytes; boxes of 128 columns, one swizzled row of an operand each
+bool encode_bytes(CUtensorMap *m, const void *ptr, int64_t rows, int64_t cols, int64_t pitch, int box_rows) {
+    const PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
+    if (!fn)
+        return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)pitch};
+    const cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+    const cuuint32_t each[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(ptr), dims, strides, box, each,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int TN, bool SWAP, bool MN> exl3_status launch_form8(const Linear8Launch &p, Args8 &a, cudaStream_t s) {
+    using F = Form<TN, SWAP, MN>;
+    constexpr int kRowsT = SWAP ? TN : 128, kRowsF = SWAP ? 128 : TN;
+    const int64_t sms = device_sm_count();
+    a.tiles_t = (int)((a.T + kRowsT - 1) / kRowsT);
+    a.tiles_f = (a.n_out + kRowsF - 1) / kRowsF;
+    const int64_t tiles = (int64_t)a.tiles_t * a.tiles_f, slots = SWAP ? 2 * sms : sms;
+    // blocks that would idle share the inputs of the tiles, two steps each at least
+    a.split = 1;
+    while (a.split < 8 && tiles * a.split * 2 <= slots && a.blocks_k >= a.split * 4)
+        a.split *= 2;
+    CUtensorMap xmap, wmap;
+    if (!encode_bytes(&xmap, p.x, p.T, p.transposed ? p.cols : p.rows, p.x_stride, kRowsT) ||
+        !encode_bytes(&wmap, p.w, p.rows, p.cols, p.cols, 128))
+        return set_error(EXL3_ERR_CUDA, "no tensor map for the operands");
+    cudaError_t e = allow_smem((const void *)linear8_kernel<TN, SWAP, MN>, F::kSmem);
+    if (e != cudaSuccess)
+        return cuda_check(e, "cudaFuncSetAttribute(8-bit product)");
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.split > 1 ? tiles * a.split : tiles < slots ? tiles : slots));
+    cfg.blockDim = dim3(F::kThreads8);
+    cfg.dynamicSmemBytes = F::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)a.split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.behind ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, linear8_kernel<TN, SWAP, MN>, xmap, wmap, a);
+    if (e != cudaSuccess)
+        return cuda_check(e, "8-bit product launch");
+    note_launch();
+    return cuda_check(cudaGetLastError(), "8-bit product launch");
+}
+
+template <bool MN> exl3_status launch_mn(const Linear8Launch &p, Args8 &a, cudaStream_t s) {
+    if (a.T <= 16)
+        return launch_form8<16, true, MN>(p, a, s);
+    if (a.T <= 32)
+        return launch_form8<32, true, MN>(p, a, s);
+    if (a.T <= 64)
+        return launch_form8<64, true, MN>(p, a, s);
+    const int64_t tiles = (a.T + 127) / 128 * ((a.n_out + 255) / 256);
+    return tiles >= device_sm_count() ? launch_form8<256, false, MN>(p, a, s) : launch_form8<128, false, MN>(p, a, s);
+}
+
+}  // namespace
+
+exl3_status launch_linear8(const Linear8Launch &p, cudaStream_t s) {
+    Args8 a = {};
+    const int64_t n_in = p.transposed ? p.cols : p.rows;
+    const int blocks_c = (int)((p.cols + 127) / 128);
+    a.xs = p.xs;
+    a.xs_t = p.xs_t;
+    a.xs_b = p.xs_b;
+    a.ws = p.ws;
+    a.ws_o = p.transposed ? blocks_c : 1;
+    a.ws_k = p.transposed ? 1 : blocks_c;
+    a.T = p.T;
+    a.n_out = (int)(p.transposed ? p.rows : p.cols);
+    a.blocks_k = (int)((n_in + 127) / 128);
+    a.y = p.y;
+    a.dt = p.dt;
+    a.y_stride = p.y_stride;
+    a.behind = p.behind;
+    return p.transposed ? launch_mn<false>(p, a, s) : launch_mn<true>(p, a, s);
+}
+
+exl3_status linear8_take_wait_timeouts(unsigned int *n) {
+    *n = 0;
+    unsigned int v = 0;
+    const unsigned int zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_linear8_timeouts, sizeof v);
+    if (e == cudaSuccess && v != 0)
+        e = cudaMemcpyToSymbol(g_linear8_timeouts, &zero, sizeof zero);
+    if (e != cudaSuccess)
+        return cuda_check(e, "wait timeout count");
+    *n = v;
+    return EXL3_OK;
+}
+
+}  // namespace exl3

@@ -1,61 +1,12 @@
 // linear_abi.cu -- entry points of the products with trellis-coded matrices
 // (exl3_linear, exl3_linear_backward, exl3_expert_linear in include/exl3.h):
 // argument checks, workspace layout, launch order.
+#include "abi_checks.cuh"
 #include "linear.cuh"
 
 using namespace exl3;
 
 namespace {
-
-constexpr size_t kAlign = 256;
-constexpr int64_t kMaxTokens = 1ll << 24;
-constexpr int64_t kMaxSide = 1ll << 16;
-
-bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
-
-exl3_status need(const void *p, const char *name, size_t al) {
-    if (!p)
-        return set_error(EXL3_ERR_INVALID_ARG, "%s is NULL", name);
-    if (!aligned(p, al))
-        return set_error(EXL3_ERR_INVALID_ARG, "%s is not %zu-byte aligned", name, al);
-    return EXL3_OK;
-}
-
-struct Rows {             // [T, n] activations or results of 2-byte elements
-    const void *p;
-    int64_t T, n, stride;
-    size_t bytes() const { return T > 0 ? (size_t)((T - 1) * stride + n) * 2 : 0; }
-};
-
-exl3_status check_rows(const Rows &r, const char *name) {
-    exl3_status st;
-    if (r.T == 0)
-        return EXL3_OK;
-    if ((st = need(r.p, name, 2)) != EXL3_OK) return st;
-    if (r.stride < r.n || r.stride > (1ll << 32))
-        return set_error(EXL3_ERR_INVALID_ARG, "%s: row stride %lld is not in [%lld, 2^32]", name,
-                         (long long)r.stride, (long long)r.n);
-    return EXL3_OK;
-}
-
-exl3_status check_apart(const Rows &out, const char *name, const void *p, size_t bytes, const char *other) {
-    const uintptr_t a = (uintptr_t)out.p, b = (uintptr_t)p;
-    if (p && out.T > 0 && bytes && a < b + bytes && b < a + out.bytes())
-        return set_error(EXL3_ERR_INVALID_ARG, "%s overlaps %s", name, other);
-    return EXL3_OK;
-}
-
-// the same for rows that may stand side by side with the result's: with one stride, rows
-// whose columns share no place modulo the stride never meet
-exl3_status check_apart(const Rows &out, const char *name, const Rows &r, const char *other) {
-    if (out.T > 1 && r.T > 1 && out.stride == r.stride) {
-        const int64_t step = out.stride * 2, between = (int64_t)((uintptr_t)r.p - (uintptr_t)out.p) % step;
-        const int64_t at = between < 0 ? between + step : between;
-        if (at >= out.n * 2 && at + r.n * 2 <= step)
-            return EXL3_OK;
-    }
-    return check_apart(out, name, r.p, r.bytes(), other);
-}
 
 struct Coded {
     const uint16_t *codes;
@@ -122,25 +73,6 @@ exl3_status check_read(const Rows &out, const char *name, const Coded &w, int E,
         return EXL3_OK;
     if ((st = check_apart(out, name, ad.A, factors * ad.inputs, "A")) != EXL3_OK) return st;
     return check_apart(out, name, ad.B, factors * ad.outputs, "B");
-}
-
-// workspace: bump allocation at 256-byte boundaries; with a null base it counts
-struct Carve {
-    unsigned char *p;
-    size_t used = 0;
-    template <typename T> T *take(size_t n) {
-        T *q = p ? reinterpret_cast<T *>(p + used) : nullptr;
-        used += align_up(n * sizeof(T), kAlign);
-        return q;
-    }
-};
-
-exl3_status check_ws(const void *ws, size_t have, size_t want) {
-    if (!ws || !aligned(ws, kAlign))
-        return set_error(EXL3_ERR_INVALID_ARG, "workspace must be non-NULL and 256-byte aligned");
-    if (have < want)
-        return set_error(EXL3_ERR_WORKSPACE, "workspace %zu bytes < %zu", have, want);
-    return EXL3_OK;
 }
 
 // up to here each token's adapter is multiplied on its own (rotation and coded product

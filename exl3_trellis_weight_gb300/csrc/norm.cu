@@ -1,0 +1,672 @@
+// norm.cu -- root-mean-square norms of rows, with the residual's addition before and
+// blocks in e4m3 behind them, their gradients, and the same blocks of any matrix.
+//
+//   h = rn(x + residual), s = 1 / sqrt(sum h^2 / n + eps), y = h s w
+//   with g = dy w:  dx = s g - h s^3 sum(g h) / n (+ dh),  dw = sum over rows of dy h s
+//
+// All of it is bound by memory: each row is read once, stays in registers (in the 16 bits
+// it came in) between its sum and its result, and the block of 128 that shares a scale lies
+// in half a warp.  A warp's unit is 256 neighbouring columns: lane l has columns 8l .. 8l + 7
+// of it where rows allow 16-byte accesses, and columns l, l + 32, ... where they do not, so
+// that a warp's accesses are whole sectors either way.
+#include "layer.cuh"
+
+namespace exl3 {
+
+namespace {
+
+constexpr int kUnitN = 256;
+
+// ---- eight values of a unit in the 16 bits of memory ------------------------------
+struct Eight {
+    uint32_t w[4];
+};
+
+template <bool VEC> __device__ __forceinline__ int column(int unit, int lane, int j) {
+    return unit * kUnitN + (VEC ? lane * 8 + j : lane + 32 * j);
+}
+
+template <typename T, bool VEC> __device__ __forceinline__ Eight load_eight(const T *row, int unit, int lane, int n) {
+    Eight e{};
+    if (VEC) {
+        const int c = column<true>(unit, lane, 0);
+        if (c < n) {
+            const uint4 q = *reinterpret_cast<const uint4 *>(row + c);
+            e.w[0] = q.x, e.w[1] = q.y, e.w[2] = q.z, e.w[3] = q.w;
+        }
+    } else {
+        const uint16_t *r = reinterpret_cast<const uint16_t *>(row);
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            const int c = column<false>(unit, lane, j);
+            if (c < n)
+                e.w[j >> 1] |= (uint32_t)r[c] << (16 * (j & 1));
+        }
+    }
+    return e;
+}
+
+template <typename T, bool VEC> __device__ __forceinline__ void store_eight(T *row, int unit, int lane, int n, const Eight &e) {
+    if (VEC) {
+        const int c = column<true>(unit, lane, 0);
+        if (c < n)
+            *reinterpret_cast<uint4 *>(row + c) = make_uint4(e.w[0], e.w[1], e.w[2], e.w[3]);
+    } else {
+        uint16_t *r = reinterpret_cast<uint16_t *>(row);
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            const int c = column<false>(unit, lane, j);
+            if (c < n)
+                r[c] = (uint16_t)(e.w[j >> 1] >> (16 * (j & 1)));
+        }
+    }
+}
+
+template <typename T> __device__ __forceinline__ void unpack_eight(const Eight &e, float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const float2 f = unpack2<T>(e.w[i]);
+        v[2 * i] = f.x, v[2 * i + 1] = f.y;
+    }
+}
+template <typename T> __device__ __forceinline__ Eight pack_eight(const float (&v)[8]) {
+    Eight e;
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+        e.w[i] = pack2<T>(v[2 * i], v[2 * i + 1]);
+    return e;
+}
+
+// the same from binary32, as the norm's weights may be, too
+template <typename T, bool VEC>
+__device__ __forceinline__ void load_weights(const void *w, bool wide, int unit, int lane, int n, float (&v)[8]) {
+    if (!wide) {
+        unpack_eight<T>(load_eight<T, VEC>(reinterpret_cast<const T *>(w), unit, lane, n), v);
+        return;
+    }
+    const float *f = reinterpret_cast<const float *>(w);
+    if (VEC) {
+        const int c = column<true>(unit, lane, 0);
+        float4 a = {}, b = {};
+        if (c < n)
+            a = reinterpret_cast<const float4 *>(f + c)[0], b = reinterpret_cast<const float4 *>(f + c)[1];
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            const int c = column<false>(unit, lane, j);
+            v[j] = c < n ? f[c] : 0.0f;
+        }
+    }
+}
+
+// ---- blocks of 128 ------------------------------------------------------------------
+// bits of the largest magnitude: as integers they order like the magnitudes, a NaN above all
+__device__ __forceinline__ uint32_t top_bits(uint32_t m, float v) { return max(m, __float_as_uint(v) & 0x7FFFFFFFu); }
+
+__device__ __forceinline__ void block_scale(uint32_t top, float &inv, float &scale) {
+    const float m = __uint_as_float(max(top, kLeast8));
+    inv = __fdiv_rn(kTop8, m);
+    scale = __fdiv_rn(m, kTop8);
+}
+
+// A unit's eight values of each lane to codes: two blocks of 128, each half a warp (VEC)
+// or half of every lane's values.  Outside of the row values are 0.
+template <bool VEC>
+__device__ __forceinline__ void encode_row(const float (&v)[8], uint8_t *codes, float *scale, int64_t hop, int unit, int lane,
+                                           int n) {
+    if (VEC) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            top = top_bits(top, v[j]);
+#pragma unroll
+        for (int d = 8; d; d >>= 1)
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+        float inv, sc;
+        block_scale(top, inv, sc);
+        const int c = column<true>(unit, lane, 0);
+        if (c < n) {
+            uint32_t q[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                q[i] = pack8(__fmul_rn(v[2 * i], inv), __fmul_rn(v[2 * i + 1], inv));
+            *reinterpret_cast<uint2 *>(codes + c) = make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
+            if ((lane & 15) == 0)
+                scale[(c >> 7) * hop] = sc;
+        }
+    } else {
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+                top = top_bits(top, v[4 * h + j]);
+            top = __reduce_max_sync(0xffffffffu, top);
+            float inv, sc;
+            block_scale(top, inv, sc);
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const int c = column<false>(unit, lane, 4 * h + j);
+                if (c < n)
+                    codes[c] = (uint8_t)pack8(__fmul_rn(v[4 * h + j], inv), 0.0f);
+            }
+            const int c0 = unit * kUnitN + 128 * h;
+            if (lane == 0 && c0 < n)
+                scale[(c0 >> 7) * hop] = sc;
+        }
+    }
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int d = 16; d; d >>= 1)
+        v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, d));
+    return v;
+}
+
+// A row whose sum of squares passes binary32's range (bfloat16's largest squares do) is
+// summed again with its values times 2^-75: the warps of a row take that turn together.
+constexpr float kDown = 0x1p-75f;
+__device__ __forceinline__ bool passed(float sum) { return !(sum <= 0x1.fffffep127f); }
+__device__ __forceinline__ void row_barrier(int sub, int wr) {
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + sub), "r"(wr * 32) : "memory");
+}
+
+// ---- the norm -------------------------------------------------------------------------
+// A row to `wr` warps, each VPT units of it; a block has one row or several.
+template <typename T, bool VEC, int VPT>
+__global__ void __launch_bounds__(1024) norm_kernel(const NormLaunch a, int wr) {
+    __shared__ float place[32];
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+    const int sub = warp / wr, wi = warp % wr, rows = (int)(blockDim.x >> 5) / wr;
+    const int64_t t = (int64_t)blockIdx.x * rows + sub;
+    const bool in = t < a.T;
+    Eight h[VPT];
+    float sum = 0.0f;
+    if (in) {
+        const T *x = reinterpret_cast<const T *>(a.x) + t * a.x_stride;
+        const T *r = reinterpret_cast<const T *>(a.residual) + t * a.r_stride;
+        Eight e[VPT];
+#pragma unroll
+        for (int k = 0; k < VPT; k++) {
+            h[k] = load_eight<T, VEC>(x, wi + k * wr, lane, a.n);
+            if (a.residual)
+                e[k] = load_eight<T, VEC>(r, wi + k * wr, lane, a.n);
+        }
+#pragma unroll
+        for (int k = 0; k < VPT; k++) {
+            float v[8];
+            unpack_eight<T>(h[k], v);
+            if (a.residual) {
+                float u[8];
+                unpack_eight<T>(e[k], u);
+#pragma unroll
+                for (int j = 0; j < 8; j++)
+                    v[j] = __fadd_rn(v[j], u[j]);
+                // what later layers read is what is normed: the rounded sum
+                h[k] = pack_eight<T>(v);
+                unpack_eight<T>(h[k], v);
+                store_eight<T, VEC>(reinterpret_cast<T *>(a.h) + t * a.h_stride, wi + k * wr, lane, a.n, h[k]);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                sum = __fmaf_rn(v[j], v[j], sum);
+        }
+    }
+    sum = warp_sum(sum);
+    if (wr > 1) {
+        if (lane == 0)
+            place[warp] = sum;
+        __syncthreads();
+        sum = warp_sum(lane < wr ? place[sub * wr + lane] : 0.0f);
+    }
+    if (!in)
+        return;
+    float down = 1.0f;
+    if (passed(sum)) {
+        down = kDown;
+        sum = 0.0f;
+#pragma unroll
+        for (int k = 0; k < VPT; k++) {
+            float v[8];
+            unpack_eight<T>(h[k], v);
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                sum = __fmaf_rn(__fmul_rn(v[j], kDown), __fmul_rn(v[j], kDown), sum);
+        }
+        sum = warp_sum(sum);
+        if (wr > 1) {
+            row_barrier(sub, wr);          // the first sums are read
+            if (lane == 0)
+                place[warp] = sum;
+            row_barrier(sub, wr);
+            sum = warp_sum(lane < wr ? place[sub * wr + lane] : 0.0f);
+        }
+    }
+    const float s = __frsqrt_rn(__fmaf_rn(__fmul_rn(a.eps, down), down, __fdiv_rn(sum, (float)a.n)));
+#pragma unroll
+    for (int k = 0; k < VPT; k++) {
+        const int unit = wi + k * wr;
+        float v[8], w[8];
+        unpack_eight<T>(h[k], v);
+        if (down != 1.0f) {
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                v[j] = __fmul_rn(v[j], kDown);
+        }
+        load_weights<T, VEC>(a.weight, a.w_dt == EXL3_F32, unit, lane, a.n, w);
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            v[j] = __fmul_rn(__fmul_rn(v[j], s), w[j]);
+        if (a.y)
+            store_eight<T, VEC>(reinterpret_cast<T *>(a.y) + t * a.y_stride, unit, lane, a.n, pack_eight<T>(v));
+        if (a.y8) {
+            if (VEC ? column<true>(unit, lane, 0) >= a.n : false) {
+#pragma unroll
+                for (int j = 0; j < 8; j++)
+                    v[j] = 0.0f;
+            } else if (!VEC) {
+#pragma unroll
+                for (int j = 0; j < 8; j++)
+                    v[j] = column<false>(unit, lane, j) < a.n ? v[j] : 0.0f;
+            }
+            encode_row<VEC>(v, a.y8 + t * a.n, a.scale + t, a.T, unit, lane, a.n);
+        }
+    }
+}
+
+// ---- its gradients ----------------------------------------------------------------------
+// Blocks stay and take rows in turn: a thread keeps its columns' part of dweight, in
+// registers up to two units and in shared memory beyond, where registers run out.
+template <typename T, bool VEC, int VPT>
+__global__ void __launch_bounds__(1024) norm_grad_kernel(const NormGradLaunch a, int wr) {
+    constexpr bool kRegs = VPT <= 2;
+    __shared__ float2 place[2][32];
+    extern __shared__ float dw_mem[];
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+    const int sub = warp / wr, wi = warp % wr, rows = (int)(blockDim.x >> 5) / wr;
+    const bool want = a.dweight != nullptr, wide = a.w_dt == EXL3_F32;
+    float dw[kRegs ? VPT : 1][8];
+    float *const mine = dw_mem + threadIdx.x;            // [unit][value][thread]
+    if (kRegs) {
+#pragma unroll
+        for (int k = 0; k < (kRegs ? VPT : 1); k++)
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                dw[k][j] = 0.0f;
+    } else if (want) {
+        for (int k = 0; k < VPT * 8; k++)
+            mine[k * blockDim.x] = 0.0f;
+    }
+    int turn = 0;
+    for (int64_t t0 = (int64_t)blockIdx.x * rows; t0 < a.T; t0 += (int64_t)gridDim.x * rows, turn ^= 1) {
+        const int64_t t = t0 + sub;
+        const bool in = t < a.T;
+        Eight eg[VPT], eh[VPT];
+        float hh = 0.0f, gh = 0.0f;
+        if (in) {
+            const T *dy = reinterpret_cast<const T *>(a.dy) + t * a.dy_stride;
+            const T *h = reinterpret_cast<const T *>(a.h) + t * a.h_stride;
+#pragma unroll
+            for (int k = 0; k < VPT; k++) {
+                eg[k] = load_eight<T, VEC>(dy, wi + k * wr, lane, a.n);
+                eh[k] = load_eight<T, VEC>(h, wi + k * wr, lane, a.n);
+            }
+#pragma unroll
+            for (int k = 0; k < VPT; k++) {
+                float g[8], v[8], w[8];
+                unpack_eight<T>(eg[k], g);
+                unpack_eight<T>(eh[k], v);
+                load_weights<T, VEC>(a.weight, wide, wi + k * wr, lane, a.n, w);
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                    hh = __fmaf_rn(v[j], v[j], hh);
+                    gh = __fmaf_rn(__fmul_rn(g[j], w[j]), v[j], gh);
+                }
+            }
+        }
+        hh = warp_sum(hh);
+        gh = warp_sum(gh);
+        if (wr > 1) {
+            // (two places in turn: a row's reads are done before the barrier of the next)
+            if (lane == 0)
+                place[turn][warp] = make_float2(hh, gh);
+            __syncthreads();
+            const float2 q = lane < wr ? place[turn][sub * wr + lane] : make_float2(0.0f, 0.0f);
+            hh = warp_sum(q.x);
+            gh = warp_sum(q.y);
+        }
+        if (!in)
+            continue;
+        float down = 1.0f;
+        if (passed(hh) || passed(fabsf(gh))) {
+            down = kDown;
+            hh = gh = 0.0f;
+#pragma unroll
+            for (int k = 0; k < VPT; k++) {
+                float g[8], v[8], w[8];
+                unpack_eight<T>(eg[k], g);
+                unpack_eight<T>(eh[k], v);
+                load_weights<T, VEC>(a.weight, wide, wi + k * wr, lane, a.n, w);
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                    const float q = __fmul_rn(v[j], kDown);
+                    hh = __fmaf_rn(q, q, hh);
+                    gh = __fmaf_rn(__fmul_rn(g[j], w[j]), q, gh);
+                }
+            }
+            hh = warp_sum(hh);
+            gh = warp_sum(gh);
+            if (wr > 1) {
+                row_barrier(sub, wr);      // the first sums are read
+                if (lane == 0)
+                    place[turn][warp] = make_float2(hh, gh);
+                row_barrier(sub, wr);
+                const float2 q = lane < wr ? place[turn][sub * wr + lane] : make_float2(0.0f, 0.0f);
+                hh = warp_sum(q.x);
+                gh = warp_sum(q.y);
+            }
+        }
+        // with h' = h down and s' = s / down:  dx = s (g - h' s'^2 sum(g h') / n)
+        const float s = __frsqrt_rn(__fmaf_rn(__fmul_rn(a.eps, down), down, __fdiv_rn(hh, (float)a.n)));
+        const float c = -__fmul_rn(__fmul_rn(s, s), __fdiv_rn(gh, (float)a.n)), sd = __fmul_rn(s, down);
+#pragma unroll
+        for (int k = 0; k < VPT; k++) {
+            const int unit = wi + k * wr;
+            float g[8], v[8], w[8];
+            unpack_eight<T>(eg[k], g);
+            unpack_eight<T>(eh[k], v);
+            load_weights<T, VEC>(a.weight, wide, unit, lane, a.n, w);
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                v[j] = __fmul_rn(v[j], down);
+            if (want) {
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                    const float p = __fmul_rn(v[j], s);
+                    if (kRegs)
+                        dw[kRegs ? k : 0][j] = __fmaf_rn(g[j], p, dw[kRegs ? k : 0][j]);
+                    else
+                        mine[(k * 8 + j) * blockDim.x] = __fmaf_rn(g[j], p, mine[(k * 8 + j) * blockDim.x]);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                v[j] = __fmul_rn(__fmaf_rn(v[j], c, __fmul_rn(g[j], w[j])), sd);
+            if (a.dh) {
+                unpack_eight<T>(load_eight<T, VEC>(reinterpret_cast<const T *>(a.dh) + t * a.dh_stride, unit, lane, a.n), g);
+#pragma unroll
+                for (int j = 0; j < 8; j++)
+                    v[j] = __fadd_rn(v[j], g[j]);
+            }
+            store_eight<T, VEC>(reinterpret_cast<T *>(a.dx) + t * a.dx_stride, unit, lane, a.n, pack_eight<T>(v));
+        }
+    }
+    if (!want)
+        return;
+    float *part = a.part + ((int64_t)blockIdx.x * rows + sub) * a.n;
+#pragma unroll
+    for (int k = 0; k < VPT; k++)
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            const int c = column<VEC>(wi + k * wr, lane, j);
+            if (c < a.n)
+                part[c] = kRegs ? dw[kRegs ? k : 0][j] : mine[(k * 8 + j) * blockDim.x];
+        }
+}
+
+// dweight: the partial rows of 32 columns, 32 threads to a column, in a fixed order
+template <typename T> __global__ void __launch_bounds__(1024) dweight_kernel(const float *part, int parts, int n, void *out, bool wide) {
+    __shared__ float place[32][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+    float s = 0.0f;
+    if (c < n)
+        for (int i = warp; i < parts; i += 32)
+            s = __fadd_rn(s, part[(int64_t)i * n + c]);
+    place[warp][lane] = s;
+    __syncthreads();
+    s = warp_sum(place[lane][warp]);
+    const int d = blockIdx.x * 32 + warp;
+    if (lane == 0 && d < n) {
+        if (wide)
+            reinterpret_cast<float *>(out)[d] = s;
+        else
+            reinterpret_cast<T *>(out)[d] = from_f32<T>(s);
+    }
+}
+
+// ---- blocks of any matrix ---------------------------------------------------------------
+template <typename T, bool VEC> __device__ __forceinline__ void load_values(const T *row, int unit, int lane, int n, float (&v)[8]) {
+    load_weights<__half, VEC>(row, true, unit, lane, n, v);
+}
+template <> __device__ __forceinline__ void load_values<__half, true>(const __half *row, int unit, int lane, int n, float (&v)[8]) {
+    unpack_eight<__half>(load_eight<__half, true>(row, unit, lane, n), v);
+}
+template <> __device__ __forceinline__ void load_values<__half, false>(const __half *row, int unit, int lane, int n, float (&v)[8]) {
+    unpack_eight<__half>(load_eight<__half, false>(row, unit, lane, n), v);
+}
+template <>
+__device__ __forceinline__ void load_values<__nv_bfloat16, true>(const __nv_bfloat16 *row, int unit, int lane, int n, float (&v)[8]) {
+    unpack_eight<__nv_bfloat16>(load_eight<__nv_bfloat16, true>(row, unit, lane, n), v);
+}
+template <>
+__device__ __forceinline__ void load_values<__nv_bfloat16, false>(const __nv_bfloat16 *row, int unit, int lane, int n, float (&v)[8]) {
+    unpack_eight<__nv_bfloat16>(load_eight<__nv_bfloat16, false>(row, unit, lane, n), v);
+}
+
+// 1 x 128: a warp takes one unit of one row after the other
+template <typename T, bool VEC> __global__ void __launch_bounds__(256) rows8_kernel(const Quantize8Launch a) {
+    // (a product behind this launch may load its weights; it waits for this kernel's end
+    // before it reads what is written here)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int lane = threadIdx.x & 31;
+    const int units = (int)((a.n + kUnitN - 1) / kUnitN);
+    const int64_t total = a.T * units, hop = (int64_t)gridDim.x * 8;
+    for (int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); i < total; i += hop) {
+        const int64_t t = i / units;
+        const int unit = (int)(i % units);
+        float v[8];
+        load_values<T, VEC>(reinterpret_cast<const T *>(a.x) + t * a.stride, unit, lane, (int)a.n, v);
+        encode_row<VEC>(v, a.codes + t * a.n, a.scale + t, a.T, unit, lane, (int)a.n);
+    }
+}
+
+// 128 x 128: eight warps to a block, two rows of it a warp at a time
+template <typename T, bool VEC> __global__ void __launch_bounds__(256) blocks8_kernel(const Quantize8Launch a) {
+    __shared__ uint32_t place[8];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int blocks_c = (int)((a.n + 127) / 128);
+    const int64_t r0 = (int64_t)(blockIdx.x / blocks_c) * 128;
+    const int c0 = (int)(blockIdx.x % blocks_c) * 128, cols = (int)min((int64_t)128, a.n - c0);
+    // (an "eighth" of the values: rows 2i, 2i + 1 of the block as one unit of 256)
+    float v[8][8];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        if (VEC) {
+            const int64_t r = r0 + 2 * (warp + 8 * i) + (lane >> 4);
+            load_values<T, true>(reinterpret_cast<const T *>(a.x) + r * a.stride + c0, 0, lane & 15, r < a.T ? cols : 0, v[i]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                const int64_t r = r0 + 2 * (warp + 8 * i) + (j >> 2);
+                const int c = lane + 32 * (j & 3);
+                v[i][j] = 0.0f;
+                if (r < a.T && c < cols) {
+                    const T *at = reinterpret_cast<const T *>(a.x) + r * a.stride + c0 + c;
+                    if constexpr (sizeof(T) == 4)
+                        v[i][j] = *at;
+                    else
+                        v[i][j] = to_f32<T>(*at);
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            top = top_bits(top, v[i][j]);
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (lane == 0)
+        place[warp] = top;
+    __syncthreads();
+    top = __reduce_max_sync(0xffffffffu, place[lane & 7]);
+    float inv, sc;
+    block_scale(top, inv, sc);
+    if (threadIdx.x == 0)
+        a.scale[blockIdx.x] = sc;
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        uint32_t q[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            q[j] = pack8(__fmul_rn(v[i][2 * j], inv), __fmul_rn(v[i][2 * j + 1], inv));
+        if (VEC) {
+            const int64_t r = r0 + 2 * (warp + 8 * i) + (lane >> 4);
+            const int c = (lane & 15) * 8;
+            if (r < a.T && c < cols)
+                *reinterpret_cast<uint2 *>(a.codes + r * a.n + c0 + c) = make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                const int64_t r = r0 + 2 * (warp + 8 * i) + (j >> 2);
+                const int c = lane + 32 * (j & 3);
+                if (r < a.T && c < cols)
+                    a.codes[r * a.n + c0 + c] = (uint8_t)(q[j >> 1] >> (8 * (j & 1)));
+            }
+        }
+    }
+}
+
+// ---- launches -----------------------------------------------------------------------------
+bool wide_rows(const void *p, int64_t stride, int size) { return ((uintptr_t)p & 15u) == 0 && stride * size % 16 == 0; }
+
+struct Shape {
+    int vpt, wr, rows;        // units of a warp, warps of a row, rows of a block
+};
+
+// Few rows: one unit a warp, for the shortest way through a row.  Many: eight warps to a
+// row, whose barriers cost less and whose loads are longer.
+Shape norm_shape(int64_t T, int64_t n, bool many) {
+    const int units = (int)((n + kUnitN - 1) / kUnitN), most = many ? 8 : 32;
+    Shape f;
+    f.vpt = units <= most ? 1 : units <= 2 * most ? 2 : 4;
+    f.wr = (units + f.vpt - 1) / f.vpt;
+    f.rows = many && f.wr < 8 ? 8 / f.wr : 1;
+    return f;
+}
+
+template <typename T, bool VEC> exl3_status norm_v(const NormLaunch &p, const Shape &f, cudaStream_t s) {
+    const unsigned grid = (unsigned)((p.T + f.rows - 1) / f.rows), block = (unsigned)(f.rows * f.wr * 32);
+    if (f.vpt == 1)
+        norm_kernel<T, VEC, 1><<<grid, block, 0, s>>>(p, f.wr);
+    else if (f.vpt == 2)
+        norm_kernel<T, VEC, 2><<<grid, block, 0, s>>>(p, f.wr);
+    else
+        norm_kernel<T, VEC, 4><<<grid, block, 0, s>>>(p, f.wr);
+    note_launch();
+    return cuda_check(cudaGetLastError(), "norm launch");
+}
+
+constexpr int kGradWarps = 32;                 // of an SM
+
+Shape grad_shape(int64_t n) {
+    const int units = (int)((n + kUnitN - 1) / kUnitN);
+    Shape f;
+    f.vpt = units <= 16 ? 1 : units <= 64 ? 2 : 4;
+    f.wr = (units + f.vpt - 1) / f.vpt;
+    f.rows = f.wr < 8 ? 8 / f.wr : 1;
+    return f;
+}
+unsigned grad_grid(int64_t T, const Shape &f) {
+    const int64_t per_sm = kGradWarps / (f.rows * f.wr) > 0 ? kGradWarps / (f.rows * f.wr) : 1;
+    const int64_t most = device_sm_count() * per_sm, want = (T + f.rows - 1) / f.rows;
+    return (unsigned)(want < most ? want : most);
+}
+
+template <typename T, bool VEC, int VPT> exl3_status norm_grad_k(const NormGradLaunch &p, const Shape &f, cudaStream_t s) {
+    const unsigned block = (unsigned)(f.rows * f.wr * 32), grid = grad_grid(p.T, f);
+    const size_t smem = VPT > 2 && p.dweight ? (size_t)VPT * 8 * block * sizeof(float) : 0;
+    if (smem) {
+        const cudaError_t e = allow_smem((const void *)norm_grad_kernel<T, VEC, VPT>, smem);
+        if (e != cudaSuccess)
+            return cuda_check(e, "cudaFuncSetAttribute(norm gradient)");
+    }
+    norm_grad_kernel<T, VEC, VPT><<<grid, block, smem, s>>>(p, f.wr);
+    note_launch();
+    return cuda_check(cudaGetLastError(), "norm gradient launch");
+}
+template <typename T> exl3_status norm_grad_t(const NormGradLaunch &p, bool vec, cudaStream_t s) {
+    const Shape f = grad_shape(p.n);
+    if (p.T) {
+        exl3_status st;
+        if (vec)
+            st = f.vpt == 1 ? norm_grad_k<T, true, 1>(p, f, s) : f.vpt == 2 ? norm_grad_k<T, true, 2>(p, f, s) : norm_grad_k<T, true, 4>(p, f, s);
+        else
+            st = f.vpt == 1 ? norm_grad_k<T, false, 1>(p, f, s) : f.vpt == 2 ? norm_grad_k<T, false, 2>(p, f, s) : norm_grad_k<T, false, 4>(p, f, s);
+        if (st != EXL3_OK)
+            return st;
+    }
+    if (!p.dweight)
+        return EXL3_OK;
+    const int parts = p.T ? (int)grad_grid(p.T, f) * f.rows : 0;
+    dweight_kernel<T><<<(unsigned)((p.n + 31) / 32), 1024, 0, s>>>(p.part, parts, p.n, p.dweight, p.w_dt == EXL3_F32);
+    note_launch();
+    return cuda_check(cudaGetLastError(), "norm weight gradient launch");
+}
+
+template <typename T> exl3_status quantize8_t(const Quantize8Launch &p, cudaStream_t s) {
+    const bool vec = wide_rows(p.x, p.stride, sizeof(T)) && p.n % 8 == 0 && ((uintptr_t)p.codes & 7u) == 0;
+    if (p.block_rows == 1) {
+        const int64_t warps = p.T * ((p.n + kUnitN - 1) / kUnitN), most = (int64_t)device_sm_count() * 8;
+        const unsigned grid = (unsigned)((warps + 7) / 8 < most ? (warps + 7) / 8 : most);
+        if (vec)
+            rows8_kernel<T, true><<<grid, 256, 0, s>>>(p);
+        else
+            rows8_kernel<T, false><<<grid, 256, 0, s>>>(p);
+    } else {
+        const unsigned grid = (unsigned)((p.n + 127) / 128 * ((p.T + 127) / 128));
+        if (vec)
+            blocks8_kernel<T, true><<<grid, 256, 0, s>>>(p);
+        else
+            blocks8_kernel<T, false><<<grid, 256, 0, s>>>(p);
+    }
+    note_launch();
+    return cuda_check(cudaGetLastError(), "8-bit blocks launch");
+}
+
+}  // namespace
+
+exl3_status launch_norm(const NormLaunch &p, cudaStream_t s) {
+    if (p.T == 0)
+        return EXL3_OK;
+    const int wsize = p.w_dt == EXL3_F32 ? 4 : 2;
+    const bool vec = p.n % 8 == 0 && wide_rows(p.x, p.x_stride, 2) && wide_rows(p.weight, p.n, wsize) &&
+                     (!p.residual || (wide_rows(p.residual, p.r_stride, 2) && wide_rows(p.h, p.h_stride, 2))) &&
+                     (!p.y || wide_rows(p.y, p.y_stride, 2)) && (!p.y8 || ((uintptr_t)p.y8 & 7u) == 0);
+    const Shape f = norm_shape(p.T, p.n, p.T > 2 * (int64_t)device_sm_count());
+    if (p.dt == EXL3_BF16)
+        return vec ? norm_v<__nv_bfloat16, true>(p, f, s) : norm_v<__nv_bfloat16, false>(p, f, s);
+    return vec ? norm_v<__half, true>(p, f, s) : norm_v<__half, false>(p, f, s);
+}
+
+int64_t norm_grad_parts(int64_t T, int64_t n) {
+    const Shape f = grad_shape(n);
+    return T ? (int64_t)grad_grid(T, f) * f.rows : 0;
+}
+
+exl3_status launch_norm_grad(const NormGradLaunch &p, cudaStream_t s) {
+    const int wsize = p.w_dt == EXL3_F32 ? 4 : 2;
+    const bool vec = p.n % 8 == 0 && wide_rows(p.dy, p.dy_stride, 2) && wide_rows(p.h, p.h_stride, 2) &&
+                     wide_rows(p.weight, p.n, wsize) && (!p.dh || wide_rows(p.dh, p.dh_stride, 2)) &&
+                     wide_rows(p.dx, p.dx_stride, 2);
+    return p.dt == EXL3_BF16 ? norm_grad_t<__nv_bfloat16>(p, vec, s) : norm_grad_t<__half>(p, vec, s);
+}
+
+exl3_status launch_quantize8(const Quantize8Launch &p, cudaStream_t s) {
+    if (p.T == 0)
+        return EXL3_OK;
+    return p.dt == EXL3_F32 ? quantize8_t<float>(p, s) : p.dt == EXL3_BF16 ? quantize8_t<__nv_bfloat16>(p, s) : quantize8_t<__half>(p, s);
+}
+
+}  // namespace exl3

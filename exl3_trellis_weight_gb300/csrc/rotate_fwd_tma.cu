@@ -32,12 +32,8 @@
 // `griddepcontrol.wait` holds every global access until that kernel has
 // completed, and each block allows the next kernel to launch once it has
 // started its last 128 x 128 block (4096 x 4096: 25.0 -> 22.4 us).
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
-#include <mutex>
-
 #include "common.cuh"
+#include "tensor_map.cuh"
 
 namespace exl3 {
 
@@ -293,24 +289,6 @@ __global__ void __launch_bounds__(kTmaThreads, 2)
 }  // namespace
 
 namespace {
-
-// cuTensorMapEncodeTiled, looked up once through the runtime (no link against
-// the driver library).
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-        else
-            (void)cudaGetLastError();
-    });
-    return fn;
-}
 
 // row-major [rows, cols] matrix, box of box_c columns x box_r rows
 bool encode_map(CUtensorMap *m, CUtensorMapDataType dt, uint32_t esize, const void *ptr, int64_t rows,

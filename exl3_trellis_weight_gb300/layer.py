@@ -1,0 +1,248 @@
+"""What stands around the products of a layer: root-mean-square norms with the
+residual's addition (``rms_norm``, ``rms_norm_backward``), blocks in 8 bits
+(``quantize8``) and products with them (``linear8``).  The same thin binding as
+``products``, whose helpers it uses."""
+from __future__ import annotations
+
+import torch
+
+from . import EXL3_BF16, EXL3_E4M3, EXL3_F16, EXL3_F32
+from .products import _call, _dense, _grad_on, _lib, _rows, _stream, _ws
+
+_DT = {torch.bfloat16: EXL3_BF16, torch.float16: EXL3_F16}
+_DT_X = {**_DT, torch.float32: EXL3_F32}
+_E4M3 = torch.float8_e4m3fn
+
+
+def rms_norm_backward_workspace_bytes(T: int, n: int) -> int:
+    return int(_lib().exl3_rms_norm_backward_workspace_bytes(T, n))
+
+
+def linear8_workspace_bytes(T: int, rows: int, cols: int, transposed: bool = False) -> int:
+    return int(_lib().exl3_linear8_workspace_bytes(T, rows, cols, int(transposed)))
+
+
+def _matrix(t, name, dtypes, columns=None, like=None):
+    """Row stride of a [T, columns] tensor of one of these types, in elements."""
+    shape = t.shape
+    if not t.is_cuda:
+        raise ValueError("all tensors must be CUDA tensors (no CPU fallback)")
+    if len(shape) != 2 or (columns is not None and shape[1] != columns):
+        raise ValueError(f"{name} must be [tokens, {'columns' if columns is None else columns}], got {tuple(shape)}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"unsupported dtype {t.dtype} of {name}")
+    if like is not None and (t.dtype != like.dtype or shape[0] != like.shape[0] or t.device != like.device):
+        raise ValueError(f"{name} must have the dtype, tokens and device of the activations")
+    row, column = t.stride()
+    if column != 1 and shape[0] and shape[1] > 1:
+        raise ValueError(f"{name}'s columns must be contiguous")
+    return row if shape[0] > 1 else shape[1]
+
+
+def _norm_weight(weight, n, x):
+    if weight.dtype is not torch.float32 and weight.dtype is not x.dtype:
+        raise ValueError(f"weight must be float32 or {x.dtype}, got {weight.dtype}")
+    return _dense(weight, "weight", weight.dtype, (n,), x.get_device()), _DT_X[weight.dtype]
+
+
+class _RmsNorm(torch.autograd.Function):
+    """``rms_norm`` with ``rms_norm_backward`` as its gradient: (y, h), or y without residual."""
+
+    @staticmethod
+    def forward(ctx, x, weight, residual, eps):
+        r = rms_norm(x, weight, eps, residual)
+        ctx.save_for_backward(x if residual is None else r["h"], weight)
+        ctx.eps = eps
+        ctx.set_materialize_grads(False)
+        return r["y"] if residual is None else (r["y"], r["h"])
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy, dh=None):
+        h, weight = ctx.saved_tensors
+        want_x, want_w, want_r, _ = ctx.needs_input_grad
+        if dy is None:
+            # only h was used
+            dx, dw = dh, torch.zeros_like(weight) if want_w and dh is not None else None
+        else:
+            g = rms_norm_backward(_rows(dy), h, weight, ctx.eps, dh=None if dh is None else _rows(dh), want_dweight=want_w)
+            dx, dw = g["dx"], g["dweight"]
+        return dx if want_x else None, dw, dx if want_r else None, None
+
+
+def rms_norm(x, weight, eps: float = 1e-6, residual=None, want_y: bool = True, want_y8: bool = False, h=None, out=None):
+    """exl3_rms_norm: h = x + residual (rounded to their dtype), y = h weight /
+    sqrt(mean(h^2) + eps) for each row.
+
+    x, residual [T, n] bfloat16 or float16 (rows may be strided), n up to 32768;
+    weight [n] of x's dtype or float32.  Returns dict(h, y, y8, scale): h with a
+    residual, y with ``want_y``, and with ``want_y8`` y in float8_e4m3fn [T, n]
+    with the scale of each 128 columns of a row [T, ceil(n / 128)] (what ``linear8``
+    takes); None otherwise.  h may be given as an output (x or residual itself, too),
+    ``out`` for y.  x, residual and weight get their gradients through y and h."""
+    xs = _matrix(x, "x", _DT)
+    T, n = x.shape
+    dev = x.device
+    pw, wdt = _norm_weight(weight, n, x)
+    rs = hs = ys = n
+    if residual is not None:
+        rs = _matrix(residual, "residual", _DT, n, like=x)
+    elif h is not None:
+        raise ValueError("h needs a residual (without one it is x)")
+    if not (want_y or want_y8):
+        raise ValueError("neither y nor y8 is wanted")
+    if out is not None and not want_y:
+        raise ValueError("out goes with want_y")
+    if _grad_on() and (x.requires_grad or weight.requires_grad or (residual is not None and residual.requires_grad)):
+        if want_y8:
+            raise ValueError("there is no gradient through y8 (torch.no_grad() lets it)")
+        if out is not None or h is not None:
+            raise ValueError("out and h do not go with inputs that want a gradient (torch.no_grad() lets them)")
+        r = _RmsNorm.apply(x, weight, residual, eps)
+        y, h = (r, None) if residual is None else r
+        return dict(h=h, y=y, y8=None, scale=None)
+    if residual is not None:
+        if h is None:
+            h = torch.empty(T, n, dtype=x.dtype, device=dev)
+        else:
+            hs = _matrix(h, "h", _DT, n, like=x)
+    y = y8 = scale = None
+    if want_y:
+        if out is None:
+            y = torch.empty(T, n, dtype=x.dtype, device=dev)
+        else:
+            y = out
+            ys = _matrix(out, "out", _DT, n, like=x)
+    if want_y8:
+        y8 = torch.empty(T, n, dtype=_E4M3, device=dev)
+        scale = torch.empty((n + 127) // 128, T, dtype=torch.float32, device=dev)
+    _call(_lib().exl3_rms_norm, dev.index, x.data_ptr(), _DT[x.dtype], T, n, xs,
+          None if residual is None else residual.data_ptr(), rs, pw, wdt, eps, None if h is None else h.data_ptr(), hs,
+          y.data_ptr() if want_y else None, ys, y8.data_ptr() if want_y8 else None,
+          scale.data_ptr() if want_y8 else None, _stream(dev.index))
+    return dict(h=h, y=y, y8=y8, scale=scale.t() if want_y8 else None)
+
+
+def rms_norm_backward(dy, h, weight, eps: float = 1e-6, dh=None, want_dweight: bool = True, dx=None, ws=None):
+    """exl3_rms_norm_backward: gradients of ``rms_norm``'s y for dy [T, n]; h is the
+    forward's h (x without a residual), dh the gradient of h's other uses or None.
+    Returns dict(dx, dweight): dx is the gradient of x and of the residual (dy or dh
+    itself may be given for it), dweight has weight's dtype (None without
+    ``want_dweight``)."""
+    gs = _matrix(dy, "dy", _DT)
+    T, n = dy.shape
+    dev = dy.device
+    hs = _matrix(h, "h", _DT, n, like=dy)
+    pw, wdt = _norm_weight(weight, n, dy)
+    ds = xs = n
+    if dh is not None:
+        ds = _matrix(dh, "dh", _DT, n, like=dy)
+    if dx is None:
+        dx = torch.empty(T, n, dtype=dy.dtype, device=dev)
+    else:
+        xs = _matrix(dx, "dx", _DT, n, like=dy)
+    L = _lib()
+    dw = pws = None
+    bytes_ = 0
+    if want_dweight:
+        dw = torch.empty(n, dtype=weight.dtype, device=dev)
+        ws = _ws(L.exl3_rms_norm_backward_workspace_bytes(T, n), dev, ws)
+        pws, bytes_ = ws.data_ptr(), ws.numel() * ws.element_size()
+    _call(L.exl3_rms_norm_backward, dev.index, dy.data_ptr(), gs, h.data_ptr(), hs, _DT[dy.dtype], T, n, pw, wdt, eps,
+          None if dh is None else dh.data_ptr(), ds, dx.data_ptr(), xs, None if dw is None else dw.data_ptr(), pws, bytes_,
+          _stream(dev.index))
+    return dict(dx=dx, dweight=dw)
+
+
+def quantize8(x, block_rows: int = 1):
+    """exl3_quantize8: x [T, n] (bfloat16, float16 or float32, rows may be strided)
+    -> (codes float8_e4m3fn [T, n], scale float32): codes times the scale of their
+    block of ``block_rows`` x 128 stand for x.  block_rows 1, for activations: scale
+    [T, ceil(n / 128)]; 128, for weights: [ceil(T / 128), ceil(n / 128)]."""
+    xs = _matrix(x, "x", _DT_X)
+    T, n = x.shape
+    dev = x.device
+    codes = torch.empty(T, n, dtype=_E4M3, device=dev)
+    nb = (n + 127) // 128
+    scale = torch.empty((nb, T) if block_rows == 1 else ((T + 127) // 128, nb), dtype=torch.float32, device=dev)
+    _call(_lib().exl3_quantize8, dev.index, x.data_ptr(), _DT_X[x.dtype], T, n, xs, block_rows, codes.data_ptr(),
+          scale.data_ptr(), _stream(dev.index))
+    return codes, scale.t() if block_rows == 1 else scale
+
+
+class _Linear8(torch.autograd.Function):
+    """``linear8`` with the call of the other transposition as its gradient."""
+
+    @staticmethod
+    def forward(ctx, x, w, w_scale, transposed, dtype, ws):
+        ctx.save_for_backward(w, w_scale)
+        ctx.transposed, ctx.dtype = transposed, x.dtype
+        return linear8(x, w, w_scale, transposed=transposed, dtype=dtype, ws=ws)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        w, w_scale = ctx.saved_tensors
+        return linear8(_rows(dy), w, w_scale, transposed=not ctx.transposed, dtype=ctx.dtype), *(None,) * 5
+
+
+def linear8(x, w, w_scale, x_scale=None, transposed: bool = False, dtype=None, out=None, ws=None):
+    """exl3_linear8: y = x W (transposed: x W^T), W in float8_e4m3fn [rows, cols] with
+    a float32 scale for each 128 x 128 [ceil(rows / 128), ceil(cols / 128)]; rows and
+    cols multiples of 16.
+
+    x [T, inputs] in float8_e4m3fn with ``x_scale`` [T, ceil(inputs / 128)] float32 (any
+    strides; rows of x 16-byte aligned), as ``rms_norm`` and ``quantize8`` leave them, or
+    in bfloat16 or float16, which are brought to that first.  Returns y [T, outputs] of
+    ``dtype`` (bfloat16 or float16; x's own if it is one of them, else bfloat16).  The
+    input gradient is the same call with ``transposed`` flipped, and what x in 16 bits
+    gets through autograd."""
+    if w.dim() != 2:
+        raise ValueError(f"w must be [rows, cols], got {tuple(w.shape)}")
+    rows, cols = w.shape
+    n_in, n_out = (cols, rows) if transposed else (rows, cols)
+    dev = x.device
+    index = dev.index if dev.type == "cuda" else -1
+    pw = _dense(w, "w", _E4M3, (rows, cols), index)
+    pws = _dense(w_scale, "w_scale", torch.float32, ((rows + 127) // 128, (cols + 127) // 128), index)
+    T = x.shape[0]
+    coded = x.dtype is _E4M3
+    L = _lib()
+    tr = 1 if transposed else 0
+    if coded:
+        xs, xdt = _matrix(x, "x", (_E4M3,), n_in), EXL3_E4M3
+        if x_scale is None:
+            raise ValueError("x in float8_e4m3fn needs x_scale")
+        if x_scale.dtype is not torch.float32 or x_scale.shape != (T, (n_in + 127) // 128) or x_scale.get_device() != index:
+            raise ValueError(f"x_scale must be torch.float32 {(T, (n_in + 127) // 128)} on x's device")
+        ps, (st, sb) = x_scale.data_ptr(), x_scale.stride()
+    else:
+        xs = _matrix(x, "x", _DT, n_in)
+        xdt = _DT[x.dtype]
+        if x_scale is not None:
+            raise ValueError("x_scale goes with x in float8_e4m3fn")
+        ps, st, sb = None, 0, 0
+    if dtype is None:
+        dtype = out.dtype if out is not None else torch.bfloat16 if coded else x.dtype
+    if dtype not in _DT:
+        raise ValueError(f"unsupported dtype {dtype} of y")
+    if _grad_on() and (x.requires_grad or w_scale.requires_grad or (x_scale is not None and x_scale.requires_grad)):
+        if w_scale.requires_grad or coded:
+            raise ValueError("there is a gradient only with respect to x in 16 bits (detach the scales)")
+        if out is not None:
+            raise ValueError("out does not go with inputs that want a gradient (torch.no_grad() lets it)")
+        return _Linear8.apply(x, w, w_scale, transposed, dtype, ws)
+    if out is None:
+        out = torch.empty(T, n_out, dtype=dtype, device=dev)
+        ys = n_out
+    else:
+        ys = _matrix(out, "out", (dtype,), n_out)
+        if out.shape[0] != T or out.device != dev:
+            raise ValueError("out must have the tokens and device of x")
+    pb, nb = None, 0
+    if not coded:
+        ws = _ws(L.exl3_linear8_workspace_bytes(T, rows, cols, tr), dev, ws)
+        pb, nb = ws.data_ptr(), ws.numel() * ws.element_size()
+    _call(L.exl3_linear8, index, x.data_ptr(), xdt, T, xs, ps, st, sb, pw, pws, rows, cols, tr, out.data_ptr(), _DT[dtype],
+          ys, pb, nb, _stream(index))
+    return out

@@ -71,8 +71,9 @@ typedef enum {
 } exl3_status;
 
 /* EXL3_F16 is a type of activations and adapters (exl3_linear and the entry
- * points beside it); weights are EXL3_F32 or EXL3_BF16. */
-typedef enum { EXL3_F32 = 0, EXL3_BF16 = 1, EXL3_F16 = 2 } exl3_dtype;
+ * points beside it); weights are EXL3_F32 or EXL3_BF16.  EXL3_E4M3 (8 bits, no
+ * infinities, largest value 448) is what exl3_linear8 multiplies. */
+typedef enum { EXL3_F32 = 0, EXL3_BF16 = 1, EXL3_F16 = 2, EXL3_E4M3 = 3 } exl3_dtype;
 
 /* Static string for a status code (never NULL). */
 EXL3_API const char *exl3_status_str(int status);
@@ -463,6 +464,86 @@ EXL3_API exl3_status exl3_expert_linear(const void *x, int dt, int64_t T, int64_
                                         const float *su, const float *sv, const float *scale,
                                         int transposed, void *y, int64_t y_stride, void *ws,
                                         size_t ws_bytes, void *stream);
+
+/*
+ * Root-mean-square norm of the rows of x, with the residual's addition before
+ * and blocks in 8 bits behind it:
+ *   h = x + residual, rounded to dt (h = x without a residual),
+ *   s = 1 / sqrt(sum h^2 / n + eps),  y = h s weight.
+ *   x, residual, h, y (device) [T, n] of dtype dt (EXL3_BF16 or EXL3_F16), rows
+ *     their stride apart, any 2-byte alignment (rows of 16-byte aligned strides
+ *     are read and written in wide accesses).  residual NULL: none, and h is not
+ *     written.  h may be x or residual itself (same address and stride), y may
+ *     be x itself; otherwise no output overlaps an input or another output.
+ *   weight (device) [n] of type w_dt: dt or EXL3_F32.  n in [1, 32768].
+ *   y may be NULL; y8 (device, uint8 [T][n], e4m3) and scale (device, fp32
+ *     [ceil(n/128)][T]) may both be NULL; y or y8 is there.
+ *   A block of 128 columns of a row (the last one may be shorter) whose largest
+ *   magnitude is m (2^-96 at least) holds e4m3(v fl(448 / m)), nearest, ties to
+ *   even, and the scale fl(m / 448); v is the value of y before its rounding.  An
+ *   infinity or a NaN in a row touches no other one; the codes times scale of a
+ *   block of y8 with such a value are all NaN.
+ * Arithmetic: binary32; sums in a fixed order for a given T, n and alignment.
+ */
+EXL3_API exl3_status exl3_rms_norm(const void *x, int dt, int64_t T, int64_t n, int64_t x_stride,
+                                   const void *residual, int64_t r_stride, const void *weight,
+                                   int w_dt, float eps, void *h, int64_t h_stride, void *y,
+                                   int64_t y_stride, uint8_t *y8, float *scale, void *stream);
+
+/*
+ * Gradients of exl3_rms_norm's y with respect to h and weight: with
+ * g = dy weight and s as there,
+ *   dx = s g - h s^3 sum(g h) / n  (+ dh, the gradient of h's other uses),
+ *   dweight = sum over rows of dy h s, rounded to w_dt once.
+ * x and residual both have the gradient dx.
+ *   dy, h, dh (NULL: none), dx (device) [T, n] of dtype dt, as in exl3_rms_norm;
+ *   dx may be dy or dh itself.  dweight (device, w_dt [n]) may be NULL.
+ *   ws: exl3_rms_norm_backward_workspace_bytes(T, n), needed with dweight.
+ */
+EXL3_API size_t exl3_rms_norm_backward_workspace_bytes(int64_t T, int64_t n);
+EXL3_API exl3_status exl3_rms_norm_backward(const void *dy, int64_t dy_stride, const void *h,
+                                            int64_t h_stride, int dt, int64_t T, int64_t n,
+                                            const void *weight, int w_dt, float eps, const void *dh,
+                                            int64_t dh_stride, void *dx, int64_t dx_stride,
+                                            void *dweight, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * A matrix in e4m3 with a scale for each block of block_rows x 128 (blocks at
+ * the ends may be smaller), as exl3_rms_norm writes it.
+ *   x (device) [T, n] of dtype dt (EXL3_F32, EXL3_BF16 or EXL3_F16), rows
+ *     x_stride elements apart; T up to 2^24, n up to 65536.
+ *   block_rows 1: scale fp32 [ceil(n/128)][T]; block_rows 128: scale fp32
+ *     [ceil(T/128)][ceil(n/128)].  codes uint8 [T][n].
+ */
+EXL3_API exl3_status exl3_quantize8(const void *x, int dt, int64_t T, int64_t n, int64_t x_stride,
+                                    int block_rows, uint8_t *codes, float *scale, void *stream);
+
+/*
+ * Product with a matrix in 8 bits: y = x W (transposed = 0) or x W^T, W in e4m3
+ * with a scale for each block of 128 x 128, x in e4m3 with a scale for each 128
+ * inputs of a token:
+ *   y[t][f] = sum_b x_scale[t][b] w_scale[block of b and f] sum_{k in b} x[t][k] W[k][f].
+ * The gradient of x is the same call on that of y with the other transposition.
+ *   x (device) [T, inputs], rows x_stride elements apart, of type x_dt:
+ *     EXL3_E4M3: x_scale (device, fp32) of token t and block b stands at
+ *       t * xs_t + b * xs_b; x 16-byte aligned, x_stride a multiple of 16.
+ *     EXL3_BF16, EXL3_F16: x is brought to e4m3 first, as by exl3_quantize8 with
+ *       block_rows 1; x_scale is NULL.
+ *   w (device, 16-byte aligned) uint8 [rows][cols]; w_scale (device) fp32
+ *     [ceil(rows/128)][ceil(cols/128)]; rows, cols multiples of 16 up to 65536.
+ *   y (device) [T, outputs] of type y_dt (EXL3_BF16 or EXL3_F16), rows y_stride
+ *     apart; it overlaps neither the inputs nor the workspace.
+ *   ws: exl3_linear8_workspace_bytes(...), needed with x in 16 bits.
+ * Arithmetic: products of a block of 128 inputs are summed by the tensor cores
+ * in binary32; blocks are scaled and added in binary32 in a fixed order for a
+ * given T, and rounded to y_dt once.
+ */
+EXL3_API size_t exl3_linear8_workspace_bytes(int64_t T, int64_t rows, int64_t cols, int transposed);
+EXL3_API exl3_status exl3_linear8(const void *x, int x_dt, int64_t T, int64_t x_stride,
+                                  const float *x_scale, int64_t xs_t, int64_t xs_b,
+                                  const uint8_t *w, const float *w_scale, int64_t rows,
+                                  int64_t cols, int transposed, void *y, int y_dt,
+                                  int64_t y_stride, void *ws, size_t ws_bytes, void *stream);
 
 /*
  * exl3_encode_tiles without a workspace, for callers that cannot allocate
