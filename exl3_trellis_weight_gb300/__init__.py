@@ -9,7 +9,7 @@ the shared library is missing or CUDA is unavailable, the calls raise.
 Entry points (same names as the C ABI, without the ``exl3_`` prefix):
   rotate, encode_tiles, decode_tiles, mse, quantize, gss_scale
   linear, linear_backward, expert_linear (products with coded matrices)
-  rms_norm, rms_norm_backward, quantize8, linear8 (what stands around them in a layer)
+  rms_norm, rms_norm_backward, quantize8, linear8, expert_layer (what stands around them)
 plus the workspace queries.
 """
 from __future__ import annotations
@@ -32,8 +32,8 @@ __all__ = [
 # takes when it is called, so without torch they are no part of a star import
 _PRODUCTS = ("linear", "linear_backward", "expert_linear", "linear_workspace_bytes",
              "linear_backward_workspace_bytes", "expert_linear_workspace_bytes")
-_LAYER = ("rms_norm", "rms_norm_backward", "quantize8", "linear8", "rms_norm_backward_workspace_bytes",
-          "linear8_workspace_bytes")
+_LAYER = ("rms_norm", "rms_norm_backward", "quantize8", "linear8", "expert_layer",
+          "rms_norm_backward_workspace_bytes", "linear8_workspace_bytes", "expert_layer_workspace_bytes")
 if importlib.util.find_spec("torch") is not None:
     __all__ += _PRODUCTS + _LAYER
 
@@ -133,7 +133,11 @@ def lib():
         L.exl3_linear8_workspace_bytes.argtypes = [i64, i64, i64, i32]
         L.exl3_linear8_workspace_bytes.restype = sz
         L.exl3_linear8.argtypes = [P, i32, i64, i64, P, i64, i64, P, P, i64, i64, i32, P, i32, i64, P, sz, P]
-        for name in ("exl3_rms_norm", "exl3_rms_norm_backward", "exl3_quantize8", "exl3_linear8", "exl3_linear", "exl3_linear_backward", "exl3_expert_linear", "exl3_regularize", "exl3_block_ldl", "exl3_ldlq", "exl3_scale_search", "exl3_encode_rows", "exl3_decode_rows", "exl3_profile_read", "exl3_wait_timeouts", "exl3_rotate", "exl3_encode_tiles", "exl3_decode_tiles", "exl3_mse",
+        L.exl3_expert_layer_workspace_bytes.argtypes = [i64, i64, i64, i32, i32]
+        L.exl3_expert_layer_workspace_bytes.restype = sz
+        L.exl3_expert_layer.argtypes = [P, i32, i64, i64, P, i32, P, P, i32, i32, i32, P, i64, i64, i32, i32, i32,
+                                        P, i64, P, sz, P]
+        for name in ("exl3_expert_layer", "exl3_rms_norm", "exl3_rms_norm_backward", "exl3_quantize8", "exl3_linear8", "exl3_linear", "exl3_linear_backward", "exl3_expert_linear", "exl3_regularize", "exl3_block_ldl", "exl3_ldlq", "exl3_scale_search", "exl3_encode_rows", "exl3_decode_rows", "exl3_profile_read", "exl3_wait_timeouts", "exl3_rotate", "exl3_encode_tiles", "exl3_decode_tiles", "exl3_mse",
                      "exl3_quantize", "exl3_gss_scale"):
             getattr(L, name).restype = i32
         _lib = L

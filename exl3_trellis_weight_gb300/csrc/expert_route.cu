@@ -1,0 +1,306 @@
+// expert_route.cu -- which tokens go to which experts, and what the first products read:
+//   logits = x R^T, p = softmax, the top_k largest of each token (of equals the first),
+//   pairs of token and expert sorted by expert into tiles of rows,
+//   z = (x . left) H of each pair for its gate and its up matrix.
+//
+// All of it is latency: a few hundred KB are read and little is computed, so the three
+// kernels start while the one before them ends.
+#include "layer.cuh"
+#include "linear_rotate.cuh"
+
+namespace exl3 {
+
+namespace {
+
+constexpr int kTogether = 4;               // tokens that share a reading of an expert's router row
+
+// ---- logits: a warp for an expert and four tokens ------------------------------------
+template <typename T, bool VEC> __device__ __forceinline__ void load_router(const void *r, bool wide, int64_t at, float (&v)[8]) {
+    if (!wide) {
+        load8<T, VEC>(reinterpret_cast<const T *>(r) + at, v);
+    } else {
+        const float *f = reinterpret_cast<const float *>(r) + at;
+        if (VEC) {
+            const float4 a = __ldg(reinterpret_cast<const float4 *>(f)), b = __ldg(reinterpret_cast<const float4 *>(f) + 1);
+            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                v[i] = f[i];
+        }
+    }
+}
+
+template <typename T, bool VEC> __global__ void __launch_bounds__(128) logits_kernel(const ExpertLaunch a) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int lane = threadIdx.x & 31;
+    const int64_t job = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    const int e = (int)(job % a.E);
+    const int64_t t0 = job / a.E * kTogether;
+    if (t0 >= a.T)
+        return;
+    const int n = (int)min((int64_t)kTogether, a.T - t0);
+    const T *x = reinterpret_cast<const T *>(a.x) + t0 * a.x_stride + lane * 8;
+    float sum[kTogether];
+#pragma unroll
+    for (int i = 0; i < kTogether; i++)
+        sum[i] = 0.0f;
+#pragma unroll 4
+    for (int k = 0; k < a.H; k += 256) {
+        if (k + lane * 8 < a.H) {          // (H is a multiple of 128)
+            float r[8];
+            load_router<T, VEC>(a.router, a.r_dt == EXL3_F32, (int64_t)e * a.H + k + lane * 8, r);
+#pragma unroll
+            for (int i = 0; i < kTogether; i++) {
+                if (i < n) {
+                    float v[8];
+                    load8<T, VEC>(x + i * a.x_stride + k, v);
+#pragma unroll
+                    for (int m = 0; m < 8; m++)
+                        sum[i] = __fmaf_rn(v[m], r[m], sum[i]);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kTogether; i++) {
+#pragma unroll
+        for (int d = 16; d; d >>= 1)
+            sum[i] = __fadd_rn(sum[i], __shfl_xor_sync(0xffffffffu, sum[i], d));
+        if (lane == 0 && i < n)
+            a.logits[(t0 + i) * a.E + e] = sum[i];
+    }
+}
+
+// ---- picks and the plan: one block ------------------------------------------------------
+// a float's bits, ordered as unsigned; any picks are valid experts, whatever the logits are
+__device__ __forceinline__ uint32_t order_of(float v) {
+    const uint32_t b = __float_as_uint(v);
+    return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+
+constexpr int kPlanThreads = 1024;
+
+template <bool ROUTE> __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const ExpertLaunch a) {
+    __shared__ int32_t count[kMaxExperts], first[kMaxExperts];
+    extern __shared__ uint32_t keys[];     // ROUTE: [warp][E]
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int n = (int)(a.T * a.top_k);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    for (int i = tid; i < a.E; i += kPlanThreads)
+        count[i] = 0;
+    for (int i = tid; i < a.rows; i += kPlanThreads)
+        a.pair_of[i] = -1;
+    for (int i = tid; i < a.T * (a.H / 128); i += kPlanThreads)
+        a.done[i] = 0;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (ROUTE) {
+        uint32_t *mine = keys + warp * a.E;
+        for (int64_t t = warp; t < a.T; t += kPlanThreads / 32) {
+            float top = -INFINITY, sum = 0.0f;
+            for (int e = lane; e < a.E; e += 32) {
+                const float v = __ldcg(a.logits + t * a.E + e);
+                mine[e] = order_of(v);
+                top = fmaxf(top, v);
+            }
+#pragma unroll
+            for (int d = 16; d; d >>= 1)
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            if (!a.normalize) {
+                for (int e = lane; e < a.E; e += 32)
+                    sum = __fadd_rn(sum, expf(__fsub_rn(__ldcg(a.logits + t * a.E + e), top)));
+#pragma unroll
+                for (int d = 16; d; d >>= 1)
+                    sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, d));
+            }
+            float p = 0.0f;                // of the lane's pick
+            int id = 0;
+            for (int j = 0; j < a.top_k; j++) {
+                uint32_t best = 0;
+                int at = a.E;
+                for (int e = lane; e < a.E; e += 32) {
+                    const uint32_t k = mine[e];
+                    if (k > best || at == a.E)
+                        best = k, at = e;
+                }
+                const uint32_t most = __reduce_max_sync(0xffffffffu, at < a.E ? best : 0u);
+                const int pick = (int)__reduce_min_sync(0xffffffffu, at < a.E && best == most ? (uint32_t)at : 0xFFFFu);
+                if (lane == (pick & 31))
+                    mine[pick] = 0;
+                if (lane == j)
+                    id = pick;
+                __syncwarp();
+            }
+            if (lane < a.top_k)
+                p = expf(__fsub_rn(__ldcg(a.logits + t * a.E + id), top));
+            if (a.normalize) {
+                sum = p;
+#pragma unroll
+                for (int d = 16; d; d >>= 1)
+                    sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, d));
+            }
+            if (lane < a.top_k) {
+                a.ids[t * a.top_k + lane] = id;
+                a.weights[t * a.top_k + lane] = __fdiv_rn(p, sum);
+            }
+        }
+    }
+    __syncthreads();
+    // how many pairs each expert has, and each token
+    for (int i = tid; i < n; i += kPlanThreads) {
+        const int e = a.ids[i];
+        if (e >= 0 && e < a.E)
+            atomicAdd(&count[e], 1);
+    }
+    for (int t = tid; t < a.T; t += kPlanThreads) {
+        int v = 0;
+        for (int j = 0; j < a.top_k; j++) {
+            const int e = a.ids[(int64_t)t * a.top_k + j];
+            v += e >= 0 && e < a.E;
+        }
+        a.valid[t] = v;
+        if (v == 0) {                      // no expert: the result is 0
+            uint16_t *y = reinterpret_cast<uint16_t *>(a.y) + (int64_t)t * a.y_stride;
+            for (int c = 0; c < a.H; c++)
+                y[c] = 0;
+        }
+    }
+    __syncthreads();
+    if (warp)
+        return;
+    // rows from multiples of 8 on, tiles of tile_n rows
+    int row = 0, tile = 0;
+    for (int e0 = 0; e0 < a.E; e0 += 32) {
+        const int e = e0 + lane, c = e < a.E ? count[e] : 0;
+        const int wide = (c + 7) & ~7, parts = (c + a.tile_n - 1) / a.tile_n;
+        int rs = wide, ts = parts;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int r = __shfl_up_sync(0xffffffffu, rs, d), t = __shfl_up_sync(0xffffffffu, ts, d);
+            if (lane >= d)
+                rs += r, ts += t;
+        }
+        if (e < a.E)
+            first[e] = row + rs - wide;
+        for (int i = 0; i < parts; i++)
+            a.tiles[tile + ts - parts + i] = make_int4(e, row + rs - wide + i * a.tile_n, min(a.tile_n, c - i * a.tile_n), 0);
+        row += __shfl_sync(0xffffffffu, rs, 31);
+        tile += __shfl_sync(0xffffffffu, ts, 31);
+    }
+    if (lane == 0)
+        *a.n_tiles = tile;
+    __syncwarp();
+    // the pairs in their order: the same plan each time
+    for (int p0 = 0; p0 < n; p0 += 32) {
+        const int p = p0 + lane, e = p < n ? a.ids[p] : -1;
+        const bool in = e >= 0 && e < a.E;
+        const uint32_t same = __match_any_sync(0xffffffffu, in ? e : -1);
+        int at = 0;
+        if (in) {
+            at = first[e] + __popc(same & ((1u << lane) - 1));
+            a.pair_of[at] = p;
+        }
+        __syncwarp();
+        if (in && (same >> lane) == 1u)    // the last of them
+            first[e] = at + 1;
+        __syncwarp();
+    }
+}
+
+// ---- rotated activations: a block for a row and one of its two matrices --------------------
+template <typename TX, bool VEC> __global__ void __launch_bounds__(1024) pairs_kernel(const ExpertLaunch a, int order) {
+    __shared__ float wmax[32];
+    extern __shared__ __align__(16) float parts[];
+    const int tid = threadIdx.x, warps = (int)(blockDim.x >> 5), lane = tid & 31;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // (what follows may read the plan at once: it is complete here)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int64_t row = blockIdx.x;
+    const int which = blockIdx.y;
+    const int p = __ldcg(a.pair_of + row);
+    if (p < 0)
+        return;
+    const int64_t t = p / a.top_k;
+    const int e = __ldcg(a.ids + p);
+    float *const part = parts + (tid >> 5) * (4 * kUnit);
+    const TX *x = reinterpret_cast<const TX *>(a.x) + t * a.x_stride + tid * 16;
+    const float *left = (which ? a.up.left : a.gate.left) + (size_t)e * a.H;
+    const int64_t NP = act_rows(a.rows);
+    float v[16], m = 0.0f;
+    for (int k = 0; k + tid * 16 < a.H; k += blockDim.x * 16) {
+        load16<TX, VEC>(x + k, v);
+        mul16(left + k + tid * 16, v);
+        m = max16(v, m);
+    }
+    m = block_max(m, wmax, warps);
+    float up, down;
+    row_scale(m, up, down);
+    if (tid == 0)
+        a.rscale[which][row] = down;
+    const bool one = (int)blockDim.x * 16 >= a.H;       // the values are still there
+    for (int k0 = 0; k0 < a.H; k0 += blockDim.x * 16) {
+        const int k = k0 + tid * 16;
+        const bool in = k < a.H;
+        if (!one && in) {
+            load16<TX, VEC>(x + k0, v);
+            mul16(left + k, v);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; i++)
+            v[i] = in ? __fmul_rn(v[i], up) : 0.0f;
+        rotate_out128(v, a.image[which], order, NP, row, k, in, part, lane);
+    }
+}
+
+template <typename... A> exl3_status start(void (*kernel)(A...), dim3 grid, unsigned block, size_t smem, bool early, cudaStream_t s, A... args) {
+    if (smem > 40 * 1024) {
+        const cudaError_t e = allow_smem((const void *)kernel, smem);
+        if (e != cudaSuccess)
+            return cuda_check(e, "cudaFuncSetAttribute(expert routing)");
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = early ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    if (e != cudaSuccess)
+        return cuda_check(e, "expert routing launch");
+    note_launch();
+    return cuda_check(cudaGetLastError(), "expert routing launch");
+}
+
+template <typename T> exl3_status route_t(const ExpertLaunch &p, cudaStream_t s) {
+    const bool vec = ((uintptr_t)p.x & 15u) == 0 && p.x_stride % 8 == 0;
+    exl3_status st;
+    if (p.router) {
+        const int64_t jobs = (p.T + kTogether - 1) / kTogether * p.E;
+        const bool both = vec && ((uintptr_t)p.router & 15u) == 0;
+        st = start(both ? logits_kernel<T, true> : logits_kernel<T, false>, dim3((unsigned)((jobs + 3) / 4)), 128, 0, false, s, p);
+        if (st != EXL3_OK)
+            return st;
+        st = start(plan_kernel<true>, dim3(1), kPlanThreads, (size_t)(kPlanThreads / 32) * p.E * 4, true, s, p);
+    } else {
+        st = start(plan_kernel<false>, dim3(1), kPlanThreads, 0, false, s, p);
+    }
+    if (st != EXL3_OK)
+        return st;
+    unsigned block = (unsigned)((p.H / 16 + 31) / 32 * 32);
+    block = block > 1024 ? 1024 : block;
+    return start(vec ? pairs_kernel<T, true> : pairs_kernel<T, false>, dim3((unsigned)p.rows, 2), block,
+                 (size_t)(block / 32) * 4 * kUnit * sizeof(float), true, s, p,
+                 !p.transposed || p.K == 3 ? 0 : p.K == 1 ? 2 : 1);
+}
+
+}  // namespace
+
+exl3_status launch_expert_route(const ExpertLaunch &p, cudaStream_t s) {
+    return p.dt == EXL3_BF16 ? route_t<__nv_bfloat16>(p, s) : route_t<__half>(p, s);
+}
+
+}  // namespace exl3

@@ -77,6 +77,59 @@ struct Linear8Launch {
 };
 exl3_status launch_linear8(const Linear8Launch &p, cudaStream_t s);
 
+// ---- expert layers (expert_route.cu, expert_up.cu, expert_down.cu) -------------------
+// y_t = sum_j w_tj (silu(x_t G_e) . (x_t U_e)) D_e, e = ids_tj the picks of token t.
+// A pair is a token and one of its picks, number t top_k + j.  Pairs are sorted by expert
+// into rows, an expert's from a multiple of 8 on (rows behind its last pair hold none).
+struct ExpertMatrix {
+    const uint32_t *codes;     // [E][rows/16][cols/16][8 K]
+    const float *left, *right; // [E][inputs], [E][outputs]
+    const float *scale;        // [E]
+};
+struct ExpertLaunch {
+    const void *x;             // [T, H]
+    int dt;
+    int64_t T, x_stride;
+    int H, F, E, top_k;
+    const void *router;        // [E, H] of type r_dt, or nullptr: ids and weights are given
+    int r_dt;
+    bool normalize;
+    ExpertMatrix gate, up, down;
+    int K, K_down, transposed;
+    void *y;                   // [T, H]
+    int64_t y_stride;
+    // workspace
+    float *logits;             // [T][E]
+    int32_t *ids;              // [T top_k]
+    float *weights;            // [T top_k]
+    int32_t *pair_of;          // [rows]: a row's pair, or -1
+    int4 *tiles;               // expert, first row and rows of each tile
+    int32_t *n_tiles;
+    int32_t *done;             // [T][H / 128]: pairs of a token that are finished
+    int32_t *valid;            // [T]: pairs of a token that have an expert
+    unsigned char *image[2];   // rotated activations of the rows for gate and up (act_rows(rows) x H)
+    float *rscale[2];          // [rows]
+    unsigned char *inner;      // rotated silu(.) . (.) of the rows (act_rows(rows) x F)
+    float *inner_scale;        // [rows][F / 128]: inner = image x scale, by blocks
+    float *part;               // [T top_k][H]: a pair's part of the result
+    int64_t rows;              // expert_rows(T, top_k, E)
+    int tile_n;                // rows of a tile
+};
+inline int64_t expert_rows(int64_t T, int top_k, int E) {
+    const int64_t n = T * top_k, used = n < E ? n : E;
+    return (n + 7 * used + 7) / 8 * 8;
+}
+// tiles, at most
+inline int64_t expert_tiles(int64_t T, int top_k, int E, int tile_n) {
+    const int64_t n = T * top_k, used = n < E ? n : E, most = used + n / tile_n;
+    return most < n ? most : n;
+}
+// rows of a tile for these sizes; 0 where a block's activations do not fit
+int expert_tile_n(int64_t T, int top_k, int E, int H, int F, int K, int K_down);
+exl3_status launch_expert_route(const ExpertLaunch &p, cudaStream_t s);
+exl3_status launch_expert_up(const ExpertLaunch &p, cudaStream_t s);
+exl3_status launch_expert_down(const ExpertLaunch &p, cudaStream_t s);
+
 // two values in e4m3, the first in the low byte; beyond 448 they become 448
 __device__ __forceinline__ uint32_t pack8(float a, float b) {
     uint16_t r;

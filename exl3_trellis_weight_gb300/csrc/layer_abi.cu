@@ -1,6 +1,6 @@
 // layer_abi.cu -- entry points of what stands around the coded products of a layer
-// (exl3_rms_norm, exl3_rms_norm_backward, exl3_quantize8, exl3_linear8 in
-// include/exl3.h): argument checks, workspace layout, launch order.
+// (exl3_rms_norm, exl3_rms_norm_backward, exl3_quantize8, exl3_linear8,
+// exl3_expert_layer in include/exl3.h): argument checks, workspace layout, launch order.
 #include "abi_checks.cuh"
 #include "layer.cuh"
 
@@ -58,6 +58,43 @@ struct Linear8Ws {
         bytes = c.used;
     }
 };
+
+constexpr int kMaxPicks = 32;
+constexpr int64_t kMaxLayerTokens = 256, kMaxPairs = 4096, kMaxLayerSide = 32768;
+
+bool layer_side(int64_t n) { return n > 0 && n % 128 == 0 && n <= kMaxLayerSide; }
+
+bool layer_ok(int64_t T, int64_t H, int64_t F, int E, int top_k) {
+    return T >= 0 && T <= kMaxLayerTokens && layer_side(H) && layer_side(F) && E >= 1 && E <= kMaxExperts && top_k >= 1 &&
+           top_k <= kMaxPicks && top_k <= E && T * top_k <= kMaxPairs;
+}
+
+// pointers of the workspace; the picks are in it unless they are given
+size_t carve_layer(ExpertLaunch &p, void *ws) {
+    Carve c{(unsigned char *)ws};
+    const int64_t n = p.T * p.top_k;
+    p.rows = expert_rows(p.T, p.top_k, p.E);
+    p.logits = c.take<float>((size_t)(p.T * p.E));
+    int32_t *ids = c.take<int32_t>((size_t)n);
+    float *weights = c.take<float>((size_t)n);
+    if (p.router || !p.ids) {
+        p.ids = ids;
+        p.weights = weights;
+    }
+    p.pair_of = c.take<int32_t>((size_t)p.rows);
+    p.tiles = c.take<int4>((size_t)expert_tiles(p.T, p.top_k, p.E, 8));
+    p.n_tiles = c.take<int32_t>(1);
+    p.done = c.take<int32_t>((size_t)(p.T * (p.H / 128)));
+    p.valid = c.take<int32_t>((size_t)p.T);
+    for (int w = 0; w < 2; w++) {
+        p.image[w] = c.take<unsigned char>((size_t)act_rows(p.rows) * p.H * 2);
+        p.rscale[w] = c.take<float>((size_t)p.rows);
+    }
+    p.inner = c.take<unsigned char>((size_t)act_rows(p.rows) * p.F * 2);
+    p.inner_scale = c.take<float>((size_t)(p.rows * (p.F / 128)));
+    p.part = c.take<float>((size_t)n * p.H);
+    return c.used;
+}
 
 }  // namespace
 
@@ -269,6 +306,112 @@ exl3_status exl3_linear8(const void *x, int x_dt, int64_t T, int64_t x_stride, c
     p.xs_b = T;
     p.behind = true;
     return launch_linear8(p, (cudaStream_t)stream);
+}
+
+size_t exl3_expert_layer_workspace_bytes(int64_t T, int64_t hidden, int64_t inner, int n_experts, int top_k) {
+    if (!layer_ok(T, hidden, inner, n_experts, top_k))
+        return 0;
+    ExpertLaunch p = {};
+    p.T = T;
+    p.H = (int)hidden;
+    p.F = (int)inner;
+    p.E = n_experts;
+    p.top_k = top_k;
+    return carve_layer(p, nullptr);
+}
+
+exl3_status exl3_expert_layer(const void *x, int dt, int64_t T, int64_t x_stride, const void *router, int r_dt,
+                              const int32_t *ids, const float *weights, int top_k, int normalize, int n_experts,
+                              const exl3_coded *experts, int64_t hidden, int64_t inner, int K, int K_down, int transposed,
+                              void *y, int64_t y_stride, void *ws, size_t ws_bytes, void *stream) {
+    exl3_status st;
+    if ((st = check_16bit(dt)) != EXL3_OK) return st;
+    if (n_experts < 1 || n_experts > kMaxExperts)
+        return set_error(EXL3_ERR_UNSUPPORTED, "%d experts: 1 to %d are supported", n_experts, kMaxExperts);
+    if (top_k < 1 || top_k > kMaxPicks || top_k > n_experts)
+        return set_error(EXL3_ERR_UNSUPPORTED, "%d picks of %d experts: 1 to %d are supported, no more than experts", top_k, n_experts, kMaxPicks);
+    if (T < 0 || T > kMaxLayerTokens || T * top_k > kMaxPairs)
+        return set_error(EXL3_ERR_UNSUPPORTED, "%lld tokens of %d picks: up to %lld tokens and %lld pairs are supported (exl3_expert_linear takes more)",
+                         (long long)T, top_k, (long long)kMaxLayerTokens, (long long)kMaxPairs);
+    if (!layer_side(hidden) || !layer_side(inner))
+        return set_error(EXL3_ERR_UNSUPPORTED, "hidden and inner must be multiples of 128 up to %lld, got %lld and %lld",
+                         (long long)kMaxLayerSide, (long long)hidden, (long long)inner);
+    if (!exl3_supports_k(K) || !exl3_supports_k(K_down))
+        return set_error(EXL3_ERR_UNSUPPORTED, "K=%d, K_down=%d is not supported", K, K_down);
+    if (!experts)
+        return set_error(EXL3_ERR_INVALID_ARG, "experts is NULL");
+    static const char *const names[3][4] = {{"gate codes", "gate su", "gate sv", "gate scale"},
+                                            {"up codes", "up su", "up sv", "up scale"},
+                                            {"down codes", "down su", "down sv", "down scale"}};
+    for (int m = 0; m < 3; m++) {
+        if ((st = need(experts[m].codes, names[m][0], 16)) != EXL3_OK) return st;
+        if ((st = need(experts[m].su, names[m][1], 16)) != EXL3_OK) return st;
+        if ((st = need(experts[m].sv, names[m][2], 16)) != EXL3_OK) return st;
+        if ((st = need(experts[m].scale, names[m][3], 4)) != EXL3_OK) return st;
+    }
+    if (router) {
+        if (r_dt != dt && r_dt != EXL3_F32)
+            return set_error(EXL3_ERR_INVALID_ARG, "router's dtype %d is neither x's nor EXL3_F32", r_dt);
+        if (!aligned(router, r_dt == EXL3_F32 ? 4 : 2))
+            return set_error(EXL3_ERR_INVALID_ARG, "router is not aligned");
+        if (ids || weights)
+            return set_error(EXL3_ERR_INVALID_ARG, "ids and weights do not go with a router");
+    } else if (T) {
+        if ((st = need(ids, "ids", 4)) != EXL3_OK) return st;
+        if ((st = need(weights, "weights", 4)) != EXL3_OK) return st;
+    }
+    const Rows xr{x, T, hidden, x_stride}, yr{y, T, hidden, y_stride};
+    if ((st = check_rows(xr, "x")) != EXL3_OK) return st;
+    if ((st = check_rows(yr, "y")) != EXL3_OK) return st;
+    if ((st = check_apart(yr, "y", xr, "x")) != EXL3_OK) return st;
+    for (int m = 0; m < 3; m++) {
+        const size_t n = (size_t)n_experts * 4, left = n * (m == 2 ? inner : hidden), right = n * (m == 2 ? hidden : inner);
+        const size_t bytes = (size_t)n_experts * hidden * inner * (m == 2 ? K_down : K) / 8;
+        if ((st = check_apart(yr, "y", experts[m].codes, bytes, names[m][0])) != EXL3_OK) return st;
+        if ((st = check_apart(yr, "y", experts[m].su, transposed ? right : left, names[m][1])) != EXL3_OK) return st;
+        if ((st = check_apart(yr, "y", experts[m].sv, transposed ? left : right, names[m][2])) != EXL3_OK) return st;
+        if ((st = check_apart(yr, "y", experts[m].scale, n, names[m][3])) != EXL3_OK) return st;
+    }
+    const size_t picks = (size_t)(T * top_k) * 4;
+    if ((st = check_apart(yr, "y", router, (size_t)n_experts * hidden * (r_dt == EXL3_F32 ? 4 : 2), "router")) != EXL3_OK) return st;
+    if ((st = check_apart(yr, "y", ids, picks, "ids")) != EXL3_OK) return st;
+    if ((st = check_apart(yr, "y", weights, picks, "weights")) != EXL3_OK) return st;
+    if (T == 0)
+        return EXL3_OK;
+    ExpertLaunch p = {};
+    p.x = x;
+    p.dt = dt;
+    p.T = T;
+    p.x_stride = x_stride;
+    p.H = (int)hidden;
+    p.F = (int)inner;
+    p.E = n_experts;
+    p.top_k = top_k;
+    p.router = router;
+    p.r_dt = r_dt;
+    p.normalize = normalize != 0;
+    ExpertMatrix *const to[3] = {&p.gate, &p.up, &p.down};
+    for (int m = 0; m < 3; m++) {
+        const exl3_coded &c = experts[m];
+        *to[m] = {reinterpret_cast<const uint32_t *>(c.codes), transposed ? c.sv : c.su, transposed ? c.su : c.sv, c.scale};
+    }
+    p.K = K;
+    p.K_down = K_down;
+    p.transposed = transposed ? 1 : 0;
+    p.y = y;
+    p.y_stride = y_stride;
+    p.ids = const_cast<int32_t *>(ids);            // (written only with a router)
+    p.weights = const_cast<float *>(weights);
+    const size_t want = carve_layer(p, ws);
+    if ((st = check_ws(ws, ws_bytes, want)) != EXL3_OK) return st;
+    if ((st = check_apart(yr, "y", ws, want, "the workspace")) != EXL3_OK) return st;
+    p.tile_n = expert_tile_n(T, top_k, n_experts, p.H, p.F, K, K_down);
+    if (!p.tile_n)
+        return set_error(EXL3_ERR_UNSUPPORTED, "%lld hidden and %lld inner channels do not fit a block", (long long)hidden, (long long)inner);
+    const cudaStream_t s = (cudaStream_t)stream;
+    if ((st = launch_expert_route(p, s)) != EXL3_OK) return st;
+    if ((st = launch_expert_up(p, s)) != EXL3_OK) return st;
+    return launch_expert_down(p, s);
 }
 
 }  // extern "C"

@@ -52,72 +52,6 @@ template <typename TX, bool VEC> __device__ __forceinline__ void shrink_rows(con
     }
 }
 
-// the largest of the block's m, in every thread; one barrier
-__device__ __forceinline__ float block_max(float m, float *place, int warps) {
-#pragma unroll
-    for (int d = 16; d; d >>= 1)
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    if ((threadIdx.x & 31) == 0)
-        place[threadIdx.x >> 5] = m;
-    __syncthreads();
-    m = (int)(threadIdx.x & 31) < warps ? place[threadIdx.x & 31] : 0.0f;
-#pragma unroll
-    for (int d = 16; d; d >>= 1)
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    return m;
-}
-
-// v: elements 16 s + i of a block of 128, s = lane % 8; writes v H in binary16.  Four
-// spans in registers, three after an exchange through the warp's part of shared memory
-// (shuffles, 48 a thread, made 4096 x 4096 22 us instead of 20.5): then lane s has, of each sixteen, the two
-// that stand at places 2s and 2s + 1.
-constexpr int kUnit = 144;                 // floats from one block of 128 to the next: other banks
-__device__ __forceinline__ void rotate_out128(float (&v)[16], const PrepLaunch &a, int64_t NP, int64_t t, int k, bool in,
-                                              float *part, int lane) {
-    const int s = lane & 7;
-    float *const unit = part + (lane >> 3) * kUnit;
-#pragma unroll
-    for (int i = 0; i < 16; i += 2) {
-        const float p = v[i], q = v[i + 1];
-        v[i] = __fadd_rn(p, q);
-        v[i + 1] = __fsub_rn(p, q);
-    }
-    span2<2>(v);
-    span2<4>(v);
-    span2<8>(v);
-    // float4 f of sixteen b at (4 b + f) ^ (b / 2): eight lanes cover all banks
-#pragma unroll
-    for (int f = 0; f < 4; f++)
-        *reinterpret_cast<float4 *>(unit + 4 * ((4 * s + f) ^ (s >> 1))) = make_float4(v[4 * f], v[4 * f + 1], v[4 * f + 2], v[4 * f + 3]);
-    __syncwarp();
-    if (a.order == 0) {
-#pragma unroll
-        for (int b = 0; b < 8; b++) {
-            const float2 w = *reinterpret_cast<const float2 *>(unit + 4 * ((4 * b + (s >> 1)) ^ (b >> 1)) + 2 * (s & 1));
-            v[2 * b] = w.x, v[2 * b + 1] = w.y;
-        }
-    } else {
-        // the inputs at places 2s and 2s + 1
-        const int j = s >> 1, h = s & 1;
-        const int i0 = a.order == 1 ? j + 8 * h : 2 * j + 8 * h, i1 = a.order == 1 ? i0 + 4 : i0 + 1;
-#pragma unroll
-        for (int b = 0; b < 8; b++) {
-            v[2 * b] = unit[4 * ((4 * b + (i0 >> 2)) ^ (b >> 1)) + (i0 & 3)];
-            v[2 * b + 1] = unit[4 * ((4 * b + (i1 >> 2)) ^ (b >> 1)) + (i1 & 3)];
-        }
-    }
-    __syncwarp();
-    span2<2>(v);
-    span2<4>(v);
-    span2<8>(v);
-    if (!in)
-        return;
-    const int k0 = k & ~127;
-#pragma unroll
-    for (int b = 0; b < 8; b++)
-        *reinterpret_cast<uint32_t *>(a.image + act_offset(NP, t, k0 + 16 * b + 2 * s)) = pack2<__half>(v[2 * b], v[2 * b + 1]);
-}
-
 // grid: (blocks of neighbouring rows, 1 + adapters' rows); block: a multiple of 32
 // threads, 16 inputs each.  ONE: a row fits one round of the block and stays in
 // registers, `left` too while the expert stays the same, and the next row is on its way.
@@ -216,7 +150,7 @@ __global__ void __launch_bounds__(1024) prep_kernel(const PrepLaunch a) {
 #pragma unroll
             for (int i = 0; i < 16; i += 2)
                 mul2(v[i], v[i + 1], up, up);
-            rotate_out128(v, a, NP, t, k, in, part, lane);
+            rotate_out128(v, a.image, a.order, NP, t, k, in, part, lane);
         }
     }
     // what follows waits for this kernel only: it may not end before those it runs beside.

@@ -1,13 +1,16 @@
 """What stands around the products of a layer: root-mean-square norms with the
 residual's addition (``rms_norm``, ``rms_norm_backward``), blocks in 8 bits
-(``quantize8``) and products with them (``linear8``).  The same thin binding as
-``products``, whose helpers it uses."""
+(``quantize8``) and products with them (``linear8``), and whole mixture-of-experts
+layers for a few tokens (``expert_layer``).  The same thin binding as ``products``,
+whose helpers it uses."""
 from __future__ import annotations
+
+import ctypes
 
 import torch
 
 from . import EXL3_BF16, EXL3_E4M3, EXL3_F16, EXL3_F32
-from .products import _call, _dense, _grad_on, _lib, _rows, _stream, _ws
+from .products import _activations, _call, _coded, _dense, _grad_on, _lib, _rows, _stream, _ws
 
 _DT = {torch.bfloat16: EXL3_BF16, torch.float16: EXL3_F16}
 _DT_X = {**_DT, torch.float32: EXL3_F32}
@@ -20,6 +23,10 @@ def rms_norm_backward_workspace_bytes(T: int, n: int) -> int:
 
 def linear8_workspace_bytes(T: int, rows: int, cols: int, transposed: bool = False) -> int:
     return int(_lib().exl3_linear8_workspace_bytes(T, rows, cols, int(transposed)))
+
+
+def expert_layer_workspace_bytes(T: int, hidden: int, inner: int, n_experts: int, top_k: int) -> int:
+    return int(_lib().exl3_expert_layer_workspace_bytes(T, hidden, inner, n_experts, top_k))
 
 
 def _matrix(t, name, dtypes, columns=None, like=None):
@@ -245,4 +252,64 @@ def linear8(x, w, w_scale, x_scale=None, transposed: bool = False, dtype=None, o
         pb, nb = ws.data_ptr(), ws.numel() * ws.element_size()
     _call(L.exl3_linear8, index, x.data_ptr(), xdt, T, xs, ps, st, sb, pw, pws, rows, cols, tr, out.data_ptr(), _DT[dtype],
           ys, pb, nb, _stream(index))
+    return out
+
+
+_Experts = ctypes.c_void_p * 12
+
+
+def expert_layer(x, gate, up, down, K: int, top_k: int, router=None, ids=None, weights=None, transposed: bool = False,
+                 K_down: int | None = None, normalize: bool = True, out=None, ws=None):
+    """exl3_expert_layer: a mixture-of-experts layer for a few tokens, y_t = sum over the
+    token's picks e of w_te (silu(x_t G_e) * (x_t U_e)) D_e.
+
+    x [T, hidden] bfloat16 or float16 (rows may be strided), T up to 256; gate, up, down
+    each (codes, su, sv, scale) of all experts as ``expert_linear`` takes them: G and U
+    [hidden, inner], D [inner, hidden] (transposed: the other way round, as torch keeps
+    them); K bits a weight, ``K_down`` for D where it differs.  Either ``router`` [experts,
+    hidden] of x's dtype or float32, from whose softmax the ``top_k`` largest are taken
+    (of equals the first; ``normalize``: divided by their sum), or ``ids`` int32 and
+    ``weights`` float32 [T, top_k] (an id that is no expert's is passed over).  Returns y
+    [T, hidden] of x's dtype.  For more tokens, and for gradients, there is
+    ``expert_linear``."""
+    dev = x.device
+    E = gate[0].shape[0]
+    H, F, *g = _coded(*gate[:3], K, gate[3], (E,), dev)
+    uh, uf, *u = _coded(*up[:3], K, up[3], (E,), dev)
+    kd = K if K_down is None else K_down
+    df, dh, *d = _coded(*down[:3], kd, down[3], (E,), dev)
+    if (uh, uf, dh, df) != (H, F, H, F):
+        raise ValueError(f"gate {(H, F)}, up {(uh, uf)} and down {(df, dh)} do not go together")
+    if transposed:
+        H, F = F, H
+    xs = _activations(x, "x", H)
+    T, index = x.shape[0], x.get_device()
+    pr = pi = pw = None
+    rdt = 0
+    if router is not None:
+        if ids is not None or weights is not None:
+            raise ValueError("ids and weights do not go with a router")
+        if router.dtype is not torch.float32 and router.dtype is not x.dtype:
+            raise ValueError(f"router must be float32 or {x.dtype}, got {router.dtype}")
+        pr, rdt = _dense(router, "router", router.dtype, (E, H), index), _DT_X[router.dtype]
+    else:
+        if ids is None or weights is None:
+            raise ValueError("a router, or ids and weights")
+        pi = _dense(ids, "ids", torch.int32, (T, top_k), index)
+        pw = _dense(weights, "weights", torch.float32, (T, top_k), index)
+    if _grad_on():
+        for name, t in (("x", x), ("router", router), ("weights", weights), *((n, t) for n, m in
+                        (("gate", gate), ("up", up), ("down", down)) for t in m[1:] if isinstance(t, torch.Tensor))):
+            if t is not None and t.requires_grad:
+                raise ValueError(f"there is no gradient with respect to {name} (torch.no_grad(); expert_linear has one)")
+    if out is None:
+        out = torch.empty(T, H, dtype=x.dtype, device=dev)
+        ys = H
+    else:
+        ys = _activations(out, "out", H, like=x)
+    L = _lib()
+    ws = _ws(L.exl3_expert_layer_workspace_bytes(T, H, F, E, top_k), dev, ws)
+    _call(L.exl3_expert_layer, dev.index, x.data_ptr(), _DT[x.dtype], T, xs, pr, rdt, pi, pw, top_k, 1 if normalize else 0, E,
+          _Experts(*g[:4], *u[:4], *d[:4]), H, F, K, kd, 1 if transposed else 0, out.data_ptr(), ys, ws.data_ptr(),
+          ws.numel() * ws.element_size(), _stream(dev.index))
     return out

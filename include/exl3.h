@@ -546,6 +546,46 @@ EXL3_API exl3_status exl3_linear8(const void *x, int x_dt, int64_t T, int64_t x_
                                   int64_t y_stride, void *ws, size_t ws_bytes, void *stream);
 
 /*
+ * A mixture-of-experts layer for a few tokens, its experts coded: with
+ * p = softmax(x R^T) and the top_k largest of each token (of equals the first),
+ *   y_t = sum_j w_tj (silu(x_t G_e) . (x_t U_e)) D_e,  e = ids_tj,
+ * w_tj = p_te / (sum of the picks' p) with normalize, else p_te.
+ *   x (device) [T, hidden], y [T, hidden] of dtype dt (EXL3_BF16 or EXL3_F16), rows
+ *     their stride apart, any 2-byte alignment.  T up to 256, T top_k up to 4096
+ *     (for more, exl3_expert_linear).
+ *   router (device) [n_experts, hidden] of type r_dt (dt or EXL3_F32); or NULL,
+ *     and ids (device) int32 [T, top_k], weights (device) fp32 [T, top_k] are the
+ *     picks: an id outside of [0, n_experts) is none, a token without any gets 0.
+ *     They are NULL with a router.
+ *   experts (host): the matrices G, U, D, each with codes (device, 16-byte aligned)
+ *     uint16 [n_experts][rows/16][cols/16][16 K], su fp32 [n_experts][rows], sv
+ *     [n_experts][cols], scale [n_experts], as exl3_expert_linear takes them.  G and U
+ *     are [hidden, inner], D is [inner, hidden] (transposed: [inner, hidden] and
+ *     [hidden, inner], multiplied as in exl3_linear).  K of G and U, K_down of D.
+ *   n_experts in [1, 1024], top_k in [1, 32], hidden and inner multiples of 128 up
+ *     to 32768 (what does not fit a block is EXL3_ERR_UNSUPPORTED).
+ *   y overlaps neither an input nor the workspace.
+ *   ws: exl3_expert_layer_workspace_bytes(...); 0 for sizes that are not supported.
+ * Arithmetic: logits, softmax and silu in binary32; products as in exl3_linear, the
+ * inner activations rounded to binary16 under a power of two for each 128 after
+ * D's rotation; a token's picks are added in binary32 in their order and rounded
+ * once.  Results are the same from run to run.  A token that holds an infinity
+ * or a NaN touches no other.
+ */
+typedef struct {
+    const uint16_t *codes;
+    const float *su, *sv, *scale;
+} exl3_coded;
+EXL3_API size_t exl3_expert_layer_workspace_bytes(int64_t T, int64_t hidden, int64_t inner,
+                                                  int n_experts, int top_k);
+EXL3_API exl3_status exl3_expert_layer(const void *x, int dt, int64_t T, int64_t x_stride,
+                                       const void *router, int r_dt, const int32_t *ids,
+                                       const float *weights, int top_k, int normalize,
+                                       int n_experts, const exl3_coded *experts, int64_t hidden,
+                                       int64_t inner, int K, int K_down, int transposed, void *y,
+                                       int64_t y_stride, void *ws, size_t ws_bytes, void *stream);
+
+/*
  * exl3_encode_tiles without a workspace, for callers that cannot allocate
  * device memory (no counterpart on the pages: an interface addition of this
  * library).  Such callers include plug-ins running inside an application that
