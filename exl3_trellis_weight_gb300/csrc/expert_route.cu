@@ -45,7 +45,7 @@ template <typename T, bool VEC> __global__ void __launch_bounds__(128) logits_ke
 #pragma unroll
     for (int i = 0; i < kTogether; i++)
         sum[i] = 0.0f;
-#pragma unroll 4
+#pragma unroll 8
     for (int k = 0; k < a.H; k += 256) {
         if (k + lane * 8 < a.H) {          // (H is a multiple of 128)
             float r[8];
@@ -79,28 +79,37 @@ __device__ __forceinline__ uint32_t order_of(float v) {
     return (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32;
+
+// shared memory behind the counts: ids, valid flags and, one after the other, the warps' keys
+// of the experts and their counts of them
+__host__ __device__ inline size_t plan_bytes(int64_t n, int E) { return (size_t)n * 4 + (size_t)kPlanWarps * E * 4; }
 
 template <bool ROUTE> __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const ExpertLaunch a) {
     __shared__ int32_t count[kMaxExperts], first[kMaxExperts];
-    extern __shared__ uint32_t keys[];     // ROUTE: [warp][E]
+    extern __shared__ int32_t plan_mem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int n = (int)(a.T * a.top_k);
+    const int n = (int)(a.T * a.top_k), T = (int)a.T;
+    int32_t *const ids = plan_mem;
+    uint32_t *const keys = reinterpret_cast<uint32_t *>(plan_mem + n) + warp * a.E;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    for (int i = tid; i < a.E; i += kPlanThreads)
-        count[i] = 0;
     for (int i = tid; i < a.rows; i += kPlanThreads)
         a.pair_of[i] = -1;
-    for (int i = tid; i < a.T * (a.H / 128); i += kPlanThreads)
+    for (int i = tid; i < T * (a.H / 128); i += kPlanThreads)
         a.done[i] = 0;
+    const int tiles = (int)expert_tiles(a.T, a.top_k, a.E, a.tile_n);
+    for (int i = tid; i < tiles * (a.F / 128); i += kPlanThreads)
+        a.up_done[i] = 0;
+    for (int i = tid; i < tiles * (a.H / 128); i += kPlanThreads)
+        a.down_done[i] = 0;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (ROUTE) {
-        uint32_t *mine = keys + warp * a.E;
-        for (int64_t t = warp; t < a.T; t += kPlanThreads / 32) {
+        for (int t = warp; t < T; t += kPlanWarps) {
+            const float *logits = a.logits + (int64_t)t * a.E;
             float top = -INFINITY, sum = 0.0f;
             for (int e = lane; e < a.E; e += 32) {
-                const float v = __ldcg(a.logits + t * a.E + e);
-                mine[e] = order_of(v);
+                const float v = __ldcg(logits + e);
+                keys[e] = order_of(v);
                 top = fmaxf(top, v);
             }
 #pragma unroll
@@ -108,31 +117,29 @@ template <bool ROUTE> __global__ void __launch_bounds__(kPlanThreads) plan_kerne
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
             if (!a.normalize) {
                 for (int e = lane; e < a.E; e += 32)
-                    sum = __fadd_rn(sum, expf(__fsub_rn(__ldcg(a.logits + t * a.E + e), top)));
+                    sum = __fadd_rn(sum, expf(__fsub_rn(__ldcg(logits + e), top)));
 #pragma unroll
                 for (int d = 16; d; d >>= 1)
                     sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, d));
             }
-            float p = 0.0f;                // of the lane's pick
-            int id = 0;
+            int id = 0;                    // the lane's pick
             for (int j = 0; j < a.top_k; j++) {
                 uint32_t best = 0;
                 int at = a.E;
                 for (int e = lane; e < a.E; e += 32) {
-                    const uint32_t k = mine[e];
+                    const uint32_t k = keys[e];
                     if (k > best || at == a.E)
                         best = k, at = e;
                 }
                 const uint32_t most = __reduce_max_sync(0xffffffffu, at < a.E ? best : 0u);
                 const int pick = (int)__reduce_min_sync(0xffffffffu, at < a.E && best == most ? (uint32_t)at : 0xFFFFu);
                 if (lane == (pick & 31))
-                    mine[pick] = 0;
+                    keys[pick] = 0;
                 if (lane == j)
                     id = pick;
                 __syncwarp();
             }
-            if (lane < a.top_k)
-                p = expf(__fsub_rn(__ldcg(a.logits + t * a.E + id), top));
+            const float p = lane < a.top_k ? expf(__fsub_rn(__ldcg(logits + id), top)) : 0.0f;
             if (a.normalize) {
                 sum = p;
 #pragma unroll
@@ -140,24 +147,45 @@ template <bool ROUTE> __global__ void __launch_bounds__(kPlanThreads) plan_kerne
                     sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, d));
             }
             if (lane < a.top_k) {
+                ids[t * a.top_k + lane] = id;
                 a.ids[t * a.top_k + lane] = id;
                 a.weights[t * a.top_k + lane] = __fdiv_rn(p, sum);
             }
         }
+    } else {
+        for (int i = tid; i < n; i += kPlanThreads) {
+            const int e = a.ids[i];
+            ids[i] = e >= 0 && e < a.E ? e : -1;
+        }
     }
     __syncthreads();
-    // how many pairs each expert has, and each token
-    for (int i = tid; i < n; i += kPlanThreads) {
-        const int e = a.ids[i];
-        if (e >= 0 && e < a.E)
-            atomicAdd(&count[e], 1);
-    }
-    for (int t = tid; t < a.T; t += kPlanThreads) {
-        int v = 0;
-        for (int j = 0; j < a.top_k; j++) {
-            const int e = a.ids[(int64_t)t * a.top_k + j];
-            v += e >= 0 && e < a.E;
+    // a warp counts the experts of its share of the pairs, and each pair's place among them
+    uint16_t *const seen = reinterpret_cast<uint16_t *>(plan_mem + n);          // [warp][E]
+    for (int i = tid; i < kPlanWarps * a.E; i += kPlanThreads)
+        seen[i] = 0;
+    __syncthreads();
+    constexpr int kMaxRounds = 4;                                               // 32 warps x 32 lanes x 4 pairs
+    const int rounds = (n + kPlanThreads - 1) / kPlanThreads;
+    uint16_t *const mine = seen + warp * a.E;
+    int place[kMaxRounds];
+#pragma unroll
+    for (int i = 0; i < kMaxRounds; i++) {
+        place[i] = 0;
+        if (i < rounds) {
+            const int p = (warp * rounds + i) * 32 + lane, e = p < n ? ids[p] : -1;
+            const uint32_t same = __match_any_sync(0xffffffffu, e);
+            if (e >= 0)
+                place[i] = mine[e] + __popc(same & ((1u << lane) - 1));
+            __syncwarp();
+            if (e >= 0 && (same >> lane) == 1u)                                 // the last of them
+                mine[e] = (uint16_t)(place[i] + 1);
+            __syncwarp();
         }
+    }
+    for (int t = tid; t < T; t += kPlanThreads) {
+        int v = 0;
+        for (int j = 0; j < a.top_k; j++)
+            v += ids[t * a.top_k + j] >= 0;
         a.valid[t] = v;
         if (v == 0) {                      // no expert: the result is 0
             uint16_t *y = reinterpret_cast<uint16_t *>(a.y) + (int64_t)t * a.y_stride;
@@ -166,44 +194,46 @@ template <bool ROUTE> __global__ void __launch_bounds__(kPlanThreads) plan_kerne
         }
     }
     __syncthreads();
-    if (warp)
-        return;
-    // rows from multiples of 8 on, tiles of tile_n rows
-    int row = 0, tile = 0;
-    for (int e0 = 0; e0 < a.E; e0 += 32) {
-        const int e = e0 + lane, c = e < a.E ? count[e] : 0;
-        const int wide = (c + 7) & ~7, parts = (c + a.tile_n - 1) / a.tile_n;
-        int rs = wide, ts = parts;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int r = __shfl_up_sync(0xffffffffu, rs, d), t = __shfl_up_sync(0xffffffffu, ts, d);
-            if (lane >= d)
-                rs += r, ts += t;
+    for (int e = tid; e < a.E; e += kPlanThreads) {
+        int c = 0;
+        for (int w = 0; w < kPlanWarps; w++) {
+            const int k = seen[w * a.E + e];
+            seen[w * a.E + e] = (uint16_t)c;
+            c += k;
         }
-        if (e < a.E)
-            first[e] = row + rs - wide;
-        for (int i = 0; i < parts; i++)
-            a.tiles[tile + ts - parts + i] = make_int4(e, row + rs - wide + i * a.tile_n, min(a.tile_n, c - i * a.tile_n), 0);
-        row += __shfl_sync(0xffffffffu, rs, 31);
-        tile += __shfl_sync(0xffffffffu, ts, 31);
+        count[e] = c;
     }
-    if (lane == 0)
-        *a.n_tiles = tile;
-    __syncwarp();
-    // the pairs in their order: the same plan each time
-    for (int p0 = 0; p0 < n; p0 += 32) {
-        const int p = p0 + lane, e = p < n ? a.ids[p] : -1;
-        const bool in = e >= 0 && e < a.E;
-        const uint32_t same = __match_any_sync(0xffffffffu, in ? e : -1);
-        int at = 0;
-        if (in) {
-            at = first[e] + __popc(same & ((1u << lane) - 1));
-            a.pair_of[at] = p;
+    __syncthreads();
+    if (warp == 0) {
+        // rows from multiples of 8 on, tiles of tile_n rows
+        int row = 0, tile = 0;
+        for (int e0 = 0; e0 < a.E; e0 += 32) {
+            const int e = e0 + lane, c = e < a.E ? count[e] : 0;
+            const int wide = (c + 7) & ~7, parts = (c + a.tile_n - 1) / a.tile_n;
+            int rs = wide, ts = parts;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int r = __shfl_up_sync(0xffffffffu, rs, d), t = __shfl_up_sync(0xffffffffu, ts, d);
+                if (lane >= d)
+                    rs += r, ts += t;
+            }
+            if (e < a.E)
+                first[e] = row + rs - wide;
+            for (int i = 0; i < parts; i++)
+                a.tiles[tile + ts - parts + i] = make_int4(e, row + rs - wide + i * a.tile_n, min(a.tile_n, c - i * a.tile_n), 0);
+            row += __shfl_sync(0xffffffffu, rs, 31);
+            tile += __shfl_sync(0xffffffffu, ts, 31);
         }
-        __syncwarp();
-        if (in && (same >> lane) == 1u)    // the last of them
-            first[e] = at + 1;
-        __syncwarp();
+        if (lane == 0)
+            *a.n_tiles = tile;
+    }
+    __syncthreads();
+    // the pairs in their order: the same plan each time
+#pragma unroll
+    for (int i = 0; i < kMaxRounds; i++) {
+        const int p = (warp * rounds + i) * 32 + lane;
+        if (i < rounds && p < n && ids[p] >= 0)
+            a.pair_of[first[ids[p]] + mine[ids[p]] + place[i]] = p;
     }
 }
 
@@ -284,9 +314,9 @@ template <typename T> exl3_status route_t(const ExpertLaunch &p, cudaStream_t s)
         st = start(both ? logits_kernel<T, true> : logits_kernel<T, false>, dim3((unsigned)((jobs + 3) / 4)), 128, 0, false, s, p);
         if (st != EXL3_OK)
             return st;
-        st = start(plan_kernel<true>, dim3(1), kPlanThreads, (size_t)(kPlanThreads / 32) * p.E * 4, true, s, p);
+        st = start(plan_kernel<true>, dim3(1), kPlanThreads, plan_bytes(p.T * p.top_k, p.E), true, s, p);
     } else {
-        st = start(plan_kernel<false>, dim3(1), kPlanThreads, 0, false, s, p);
+        st = start(plan_kernel<false>, dim3(1), kPlanThreads, plan_bytes(p.T * p.top_k, p.E), false, s, p);
     }
     if (st != EXL3_OK)
         return st;

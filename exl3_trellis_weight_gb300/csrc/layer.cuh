@@ -110,7 +110,9 @@ struct ExpertLaunch {
     unsigned char *image[2];   // rotated activations of the rows for gate and up (act_rows(rows) x H)
     float *rscale[2];          // [rows]
     unsigned char *inner;      // rotated silu(.) . (.) of the rows (act_rows(rows) x F)
-    float *inner_scale;        // [rows][F / 128]: inner = image x scale, by blocks
+    float *inner_scale;        // [F / 128][rows]: the powers of two of its blocks
+    float *sums;               // [2 blocks][2][tile_n][128]: of tiles that blocks share
+    int32_t *up_done, *down_done;      // [tiles][F / 128], [tiles][H / 128]: finished steps
     float *part;               // [T top_k][H]: a pair's part of the result
     int64_t rows;              // expert_rows(T, top_k, E)
     int tile_n;                // rows of a tile
@@ -120,15 +122,16 @@ inline int64_t expert_rows(int64_t T, int top_k, int E) {
     return (n + 7 * used + 7) / 8 * 8;
 }
 // tiles, at most
-inline int64_t expert_tiles(int64_t T, int top_k, int E, int tile_n) {
+__host__ __device__ inline int64_t expert_tiles(int64_t T, int top_k, int E, int tile_n) {
     const int64_t n = T * top_k, used = n < E ? n : E, most = used + n / tile_n;
     return most < n ? most : n;
 }
-// rows of a tile for these sizes; 0 where a block's activations do not fit
-int expert_tile_n(int64_t T, int top_k, int E, int H, int F, int K, int K_down);
+inline int expert_tile_n(int64_t T) { return T <= 8 ? 8 : T <= 16 ? 16 : 32; }
+inline int64_t expert_blocks() { return 2 * (int64_t)device_sm_count(); }
 exl3_status launch_expert_route(const ExpertLaunch &p, cudaStream_t s);
 exl3_status launch_expert_up(const ExpertLaunch &p, cudaStream_t s);
 exl3_status launch_expert_down(const ExpertLaunch &p, cudaStream_t s);
+exl3_status expert_down_take_wait_timeouts(unsigned int *n);
 
 // two values in e4m3, the first in the low byte; beyond 448 they become 448
 __device__ __forceinline__ uint32_t pack8(float a, float b) {

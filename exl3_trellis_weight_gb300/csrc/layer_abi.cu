@@ -82,7 +82,12 @@ size_t carve_layer(ExpertLaunch &p, void *ws) {
         p.weights = weights;
     }
     p.pair_of = c.take<int32_t>((size_t)p.rows);
-    p.tiles = c.take<int4>((size_t)expert_tiles(p.T, p.top_k, p.E, 8));
+    p.tile_n = expert_tile_n(p.T);
+    const size_t tiles = (size_t)expert_tiles(p.T, p.top_k, p.E, p.tile_n);
+    p.tiles = c.take<int4>(tiles);
+    p.up_done = c.take<int32_t>(tiles * (p.F / 128));
+    p.down_done = c.take<int32_t>(tiles * (p.H / 128));
+    p.sums = c.take<float>((size_t)expert_blocks() * 4 * p.tile_n * 128);
     p.n_tiles = c.take<int32_t>(1);
     p.done = c.take<int32_t>((size_t)(p.T * (p.H / 128)));
     p.valid = c.take<int32_t>((size_t)p.T);
@@ -405,9 +410,6 @@ exl3_status exl3_expert_layer(const void *x, int dt, int64_t T, int64_t x_stride
     const size_t want = carve_layer(p, ws);
     if ((st = check_ws(ws, ws_bytes, want)) != EXL3_OK) return st;
     if ((st = check_apart(yr, "y", ws, want, "the workspace")) != EXL3_OK) return st;
-    p.tile_n = expert_tile_n(T, top_k, n_experts, p.H, p.F, K, K_down);
-    if (!p.tile_n)
-        return set_error(EXL3_ERR_UNSUPPORTED, "%lld hidden and %lld inner channels do not fit a block", (long long)hidden, (long long)inner);
     const cudaStream_t s = (cudaStream_t)stream;
     if ((st = launch_expert_route(p, s)) != EXL3_OK) return st;
     if ((st = launch_expert_up(p, s)) != EXL3_OK) return st;

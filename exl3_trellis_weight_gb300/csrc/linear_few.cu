@@ -125,32 +125,21 @@ __global__ void __launch_bounds__(kThreadsF, 2) few_kernel(const __grid_constant
     const int blocks = rows_z / 8;         // blocks of 8 tokens that hold any
     const bool ok = __all_sync(0xffffffffu, bar_wait(full, 0, &gave_up, &g_few_timeouts));
     const Lane l = lane_of<K, TR>(g, j);
-    uint32_t tiles = ring;
+    Words tiles(ring, l);
+    uint32_t left = kTilesAhead;           // tiles up to the ring's end
     // token g's four inputs of tile i: 8 bytes of chunk 2 i + j / 2 of its row
     uint32_t z = base + (uint32_t)(q_lo >> 2) * (NB * 1024u) + (uint32_t)g * 128u + ((uint32_t)((j >> 1) ^ g) << 4) +
                  (uint32_t)(j & 1) * 8u;
     for (int q = q_lo; ok && q < q_hi; q += kAtOnce, z += NB * 1024u) {
         copy_wait<kTilesAhead / kAtOnce - 1>();
         __syncwarp();
-#pragma unroll
-        for (int i = 0; i < kAtOnce; i++) {
-            uint32_t f[4];
-            fragment<K, TR>(tiles + i * (32 * K), l, f);
-            const uint32_t row = z ^ (uint32_t)(i << 5);
-#pragma unroll
-            for (int b = 0; b < NB; b++) {
-                if (NB <= 2 || b < blocks) {
-                    uint32_t b0, b1;
-                    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(b0), "=r"(b1) : "r"(row + b * 1024u));
-                    mma16(acc[b], f, b0, b1);
-                }
-            }
-        }
+        four_tiles<K, TR, NB, 2>(tiles, l, z, blocks, acc);
         __syncwarp();                      // every lane has read the tiles that the next copies replace
         load_tiles(q + kTilesAhead);
-        tiles += kAtOnce * 32 * K;
-        if (tiles == ring + kTilesAhead * 32 * K)
-            tiles = ring;
+        left -= kAtOnce;
+        tiles.move(left ? kAtOnce * 32u * K : kAtOnce * 32u * K - kTilesAhead * 32u * K);
+        if (left == 0)
+            left = kTilesAhead;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
 

@@ -12,9 +12,10 @@ constexpr int kTilesAhead = 16;            // tiles in a warp's ring
 // PrepLaunch::order that lane_of wants: lane j's four inputs are places 4j .. 4j + 3 of 16
 inline int few_order(int K, bool transposed) { return !transposed || K == 3 ? 0 : K == 1 ? 2 : 1; }
 
-__device__ __forceinline__ uint32_t lds(uint32_t at) {
+// a word of shared memory, OFF bytes behind `at`
+template <int OFF> __device__ __forceinline__ uint32_t lds(uint32_t at) {
     uint32_t v;
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at));
+    asm volatile("ld.shared.b32 %0, [%1 + %2];" : "=r"(v) : "r"(at), "n"(OFF));
     return v;
 }
 // 16 bits of t, `B` bits before its end
@@ -56,44 +57,73 @@ template <int K, bool TR> __device__ __forceinline__ Lane lane_of(int g, int j) 
     return l;
 }
 
-// A fragment of one tile; `tile` is its codes' shared-memory address
-template <int K, bool TR> __device__ __forceinline__ void fragment(uint32_t tile, const Lane &l, uint32_t (&a)[4]) {
+// Where a lane's words lie in a warp's ring: the same distance from tile to tile, so that
+// the tiles of a group are told apart in the instructions (an address of its own for each
+// word made a tile 85 instructions instead of 70).
+struct Words {
+    uint32_t last, before, last1;
+    __device__ __forceinline__ Words(uint32_t tiles, const Lane &l) : last(tiles + l.last), before(tiles + l.before), last1(tiles + l.last1) {}
+    __device__ __forceinline__ void move(uint32_t by) { last += by, before += by, last1 += by; }
+};
+
+// A fragment of the tile OFF bytes on
+template <int K, bool TR, int OFF> __device__ __forceinline__ void fragment(const Words &at, const Lane &l, uint32_t (&a)[4]) {
     if constexpr (TR) {
         // rows g and g + 8 (4 K words on, where no word is the ring's first)
+        constexpr int NEXT = OFF + 16 * K;
+        const uint32_t w1[2] = {lds<OFF>(at.last), lds<NEXT>(at.last)};
+        const uint32_t w0[2] = {lds<OFF>(at.before), lds<NEXT - 4>(at.last)};
+        uint32_t w2[2] = {0u, 0u};
+        if constexpr (K == 4)
+            w2[0] = lds<OFF + 4>(at.last), w2[1] = lds<NEXT + 4>(at.last);
 #pragma unroll
         for (int h = 0; h < 2; h++) {
-            const uint32_t at = tile + l.last + 16 * K * h;
-            const uint32_t w1 = lds(at), w0 = h ? lds(at - 4) : lds(tile + l.before);
-            const uint32_t t = __funnelshift_r(w1, w0, l.sh);
+            const uint32_t t = __funnelshift_r(w1[h], w0[h], l.sh);
             if constexpr (K == 1) {        // inputs 2j, 2j + 1, 2j + 8, 2j + 9
                 const uint32_t u = t >> 1;
                 a[h] = levels2(cut<8>(u), cut<8>(t));
                 a[2 + h] = levels2(cut<0>(u), cut<0>(t));
             } else if constexpr (K == 2) { // inputs j, j + 4, j + 8, j + 12
-                const uint32_t u = __funnelshift_r(w1, w0, l.sh + 24);
+                const uint32_t u = __funnelshift_r(w1[h], w0[h], l.sh + 24);
                 a[h] = levels2(cut<0>(u), cut<16>(t));
                 a[2 + h] = levels2(cut<8>(t), cut<0>(t));
             } else if constexpr (K == 3) { // inputs 4j .. 4j + 3
                 a[h] = levels2(cut<9>(t), cut<6>(t));
                 a[2 + h] = levels2(cut<3>(t), cut<0>(t));
             } else {                       // inputs j, j + 4; j + 8, j + 12 end a word later
-                const uint32_t u = __funnelshift_r(lds(at + 4), w1, l.sh);
+                const uint32_t u = __funnelshift_r(w2[h], w1[h], l.sh);
                 a[h] = levels2(cut<16>(t), cut<0>(t));
                 a[2 + h] = levels2(cut<16>(u), cut<0>(u));
             }
         }
     } else {
-        // rows 4j .. 4j + 3; two outputs of each
-        uint32_t w[4][2];
+        // rows 4j .. 4j + 3; two outputs of each.  (Neighbouring rows share words up to K = 2.)
+        uint32_t w[4][2], t[4];
+        if constexpr (K == 1) {
+            const uint32_t q[3] = {lds<OFF>(at.before), lds<OFF>(at.last), lds<OFF + 4>(at.last)};
+#pragma unroll
+            for (int r = 0; r < 4; r++)
+                t[r] = __funnelshift_r(q[(r >> 1) + 1], q[r >> 1], l.sh - 16 * (r & 1));
+        } else if constexpr (K == 2) {
+            const uint32_t q[5] = {lds<OFF>(at.before), lds<OFF>(at.last), lds<OFF + 4>(at.last), lds<OFF + 8>(at.last), lds<OFF + 12>(at.last)};
+#pragma unroll
+            for (int r = 0; r < 4; r++)
+                t[r] = __funnelshift_r(q[r + 1], q[r], l.sh);
+        } else if constexpr (K == 3) {
+            t[0] = __funnelshift_r(lds<OFF>(at.last), lds<OFF>(at.before), l.sh);
+            t[1] = __funnelshift_r(lds<OFF>(at.last1), lds<OFF - 4>(at.last1), l.sh1);
+            t[2] = __funnelshift_r(lds<OFF + 12>(at.last), lds<OFF + 8>(at.last), l.sh);
+            t[3] = __funnelshift_r(lds<OFF + 12>(at.last1), lds<OFF + 8>(at.last1), l.sh1);
+        } else {
+            t[0] = __funnelshift_r(lds<OFF>(at.last), lds<OFF>(at.before), l.sh);
+            t[1] = __funnelshift_r(lds<OFF + 8>(at.last), lds<OFF + 4>(at.last), l.sh);
+            t[2] = __funnelshift_r(lds<OFF + 16>(at.last), lds<OFF + 12>(at.last), l.sh);
+            t[3] = __funnelshift_r(lds<OFF + 24>(at.last), lds<OFF + 20>(at.last), l.sh);
+        }
 #pragma unroll
         for (int r = 0; r < 4; r++) {
-            const bool odd3 = K == 3 && (r & 1);
-            const uint32_t at = tile + (odd3 ? l.last1 : l.last) + 4 * (K == 1 ? r >> 1 : K == 3 ? 3 * (r >> 1) : r * K / 2);
-            const bool first = r == 0 || (K == 1 && r == 1);
-            const uint32_t sh = K == 1 ? l.sh - 16 * (r & 1) : odd3 ? l.sh1 : l.sh;
-            const uint32_t t = __funnelshift_r(lds(at), first ? lds(tile + l.before) : lds(at - 4), sh);
-            w[r][0] = cut<K == 1 ? 8 : K == 2 ? 16 : K>(t);
-            w[r][1] = cut<0>(t);
+            w[r][0] = cut<K == 1 ? 8 : K == 2 ? 16 : K>(t[r]);
+            w[r][1] = cut<0>(t[r]);
         }
 #pragma unroll
         for (int h = 0; h < 2; h++) {
@@ -108,6 +138,25 @@ __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uin
                  "{%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// acc += the products of tiles I .. 3 of a group with their inputs at z: NB * 8 rows of 128
+// bytes; those of 8 rows from ANY on are left out where `blocks` says they hold none
+template <int K, bool TR, int NB, int ANY, int I = 0>
+__device__ __forceinline__ void four_tiles(const Words &at, const Lane &l, uint32_t z, int blocks, float (&acc)[NB][4]) {
+    uint32_t f[4];
+    fragment<K, TR, I * 32 * K>(at, l, f);
+    const uint32_t row = z ^ (uint32_t)(I << 5);
+#pragma unroll
+    for (int b = 0; b < NB; b++) {
+        if (b < ANY || b < blocks) {
+            uint32_t b0, b1;
+            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(b0), "=r"(b1) : "r"(row + b * 1024u));
+            mma16(acc[b], f, b0, b1);
+        }
+    }
+    if constexpr (I < 3)
+        four_tiles<K, TR, NB, ANY, I + 1>(at, l, z, blocks, acc);
 }
 
 }  // namespace exl3

@@ -563,7 +563,7 @@ EXL3_API exl3_status exl3_linear8(const void *x, int x_dt, int64_t T, int64_t x_
  *     are [hidden, inner], D is [inner, hidden] (transposed: [inner, hidden] and
  *     [hidden, inner], multiplied as in exl3_linear).  K of G and U, K_down of D.
  *   n_experts in [1, 1024], top_k in [1, 32], hidden and inner multiples of 128 up
- *     to 32768 (what does not fit a block is EXL3_ERR_UNSUPPORTED).
+ *     to 32768.
  *   y overlaps neither an input nor the workspace.
  *   ws: exl3_expert_layer_workspace_bytes(...); 0 for sizes that are not supported.
  * Arithmetic: logits, softmax and silu in binary32; products as in exl3_linear, the
