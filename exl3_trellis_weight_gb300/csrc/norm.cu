@@ -277,9 +277,10 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormLaunch a, int wr) 
 }
 
 // ---- its gradients ----------------------------------------------------------------------
-// Blocks stay and take rows in turn: a thread keeps its columns' part of dweight, in
-// registers up to two units and in shared memory beyond, where registers run out.
-template <typename T, bool VEC, int VPT>
+// Blocks stay and take rows in turn, the next row on its way while one is summed: a thread
+// keeps its columns' weights and part of dweight, in registers up to two units and in shared
+// memory beyond, where registers run out.
+template <typename T, bool VEC, int VPT, bool WAY>
 __global__ void __launch_bounds__(1024) norm_grad_kernel(const NormGradLaunch a, int wr) {
     constexpr bool kRegs = VPT <= 2;
     __shared__ float2 place[2][32];
@@ -299,31 +300,44 @@ __global__ void __launch_bounds__(1024) norm_grad_kernel(const NormGradLaunch a,
         for (int k = 0; k < VPT * 8; k++)
             mine[k * blockDim.x] = 0.0f;
     }
+    const T *const dy = reinterpret_cast<const T *>(a.dy), *const hs = reinterpret_cast<const T *>(a.h);
+    const T *const ds = reinterpret_cast<const T *>(a.dh);
+    const int64_t step = (int64_t)gridDim.x * rows;
+    Eight eg[VPT], eh[VPT], ed[VPT];
+    auto fetch = [&](int64_t t, Eight (&g)[VPT], Eight (&h)[VPT], Eight (&d)[VPT]) {
+#pragma unroll
+        for (int k = 0; k < VPT; k++) {
+            g[k] = h[k] = d[k] = Eight{};
+            if (t < a.T) {
+                g[k] = load_eight<T, VEC>(dy + t * a.dy_stride, wi + k * wr, lane, a.n);
+                h[k] = load_eight<T, VEC>(hs + t * a.h_stride, wi + k * wr, lane, a.n);
+                if (ds)
+                    d[k] = load_eight<T, VEC>(ds + t * a.dh_stride, wi + k * wr, lane, a.n);
+            }
+        }
+    };
+    if (WAY)
+        fetch((int64_t)blockIdx.x * rows + sub, eg, eh, ed);
     int turn = 0;
-    for (int64_t t0 = (int64_t)blockIdx.x * rows; t0 < a.T; t0 += (int64_t)gridDim.x * rows, turn ^= 1) {
+    for (int64_t t0 = (int64_t)blockIdx.x * rows; t0 < a.T; t0 += step, turn ^= 1) {
         const int64_t t = t0 + sub;
         const bool in = t < a.T;
-        Eight eg[VPT], eh[VPT];
+        Eight ng[WAY ? VPT : 1], nh[WAY ? VPT : 1], nd[WAY ? VPT : 1];
+        if constexpr (WAY)
+            fetch(t + step, ng, nh, nd);
+        else
+            fetch(t, eg, eh, ed);
         float hh = 0.0f, gh = 0.0f;
-        if (in) {
-            const T *dy = reinterpret_cast<const T *>(a.dy) + t * a.dy_stride;
-            const T *h = reinterpret_cast<const T *>(a.h) + t * a.h_stride;
 #pragma unroll
-            for (int k = 0; k < VPT; k++) {
-                eg[k] = load_eight<T, VEC>(dy, wi + k * wr, lane, a.n);
-                eh[k] = load_eight<T, VEC>(h, wi + k * wr, lane, a.n);
-            }
+        for (int k = 0; k < VPT; k++) {
+            float g[8], v[8], w[8];
+            unpack_eight<T>(eg[k], g);
+            unpack_eight<T>(eh[k], v);
+            load_weights<T, VEC>(a.weight, wide, wi + k * wr, lane, a.n, w);
 #pragma unroll
-            for (int k = 0; k < VPT; k++) {
-                float g[8], v[8], w[8];
-                unpack_eight<T>(eg[k], g);
-                unpack_eight<T>(eh[k], v);
-                load_weights<T, VEC>(a.weight, wide, wi + k * wr, lane, a.n, w);
-#pragma unroll
-                for (int j = 0; j < 8; j++) {
-                    hh = __fmaf_rn(v[j], v[j], hh);
-                    gh = __fmaf_rn(__fmul_rn(g[j], w[j]), v[j], gh);
-                }
+            for (int j = 0; j < 8; j++) {
+                hh = __fmaf_rn(v[j], v[j], hh);
+                gh = __fmaf_rn(__fmul_rn(g[j], w[j]), v[j], gh);
             }
         }
         hh = warp_sum(hh);
@@ -337,70 +351,75 @@ __global__ void __launch_bounds__(1024) norm_grad_kernel(const NormGradLaunch a,
             hh = warp_sum(q.x);
             gh = warp_sum(q.y);
         }
-        if (!in)
-            continue;
-        float down = 1.0f;
-        if (passed(hh) || passed(fabsf(gh))) {
-            down = kDown;
-            hh = gh = 0.0f;
+        if (in) {
+            float down = 1.0f;
+            if (passed(hh) || passed(fabsf(gh))) {
+                down = kDown;
+                hh = gh = 0.0f;
+#pragma unroll
+                for (int k = 0; k < VPT; k++) {
+                    float g[8], v[8], w[8];
+                    unpack_eight<T>(eg[k], g);
+                    unpack_eight<T>(eh[k], v);
+                    load_weights<T, VEC>(a.weight, wide, wi + k * wr, lane, a.n, w);
+#pragma unroll
+                    for (int j = 0; j < 8; j++) {
+                        const float q = __fmul_rn(v[j], kDown);
+                        hh = __fmaf_rn(q, q, hh);
+                        gh = __fmaf_rn(__fmul_rn(g[j], w[j]), q, gh);
+                    }
+                }
+                hh = warp_sum(hh);
+                gh = warp_sum(gh);
+                if (wr > 1) {
+                    row_barrier(sub, wr);  // the first sums are read
+                    if (lane == 0)
+                        place[turn][warp] = make_float2(hh, gh);
+                    row_barrier(sub, wr);
+                    const float2 q = lane < wr ? place[turn][sub * wr + lane] : make_float2(0.0f, 0.0f);
+                    hh = warp_sum(q.x);
+                    gh = warp_sum(q.y);
+                }
+            }
+            // with h' = h down and s' = s / down:  dx = s (g - h' s'^2 sum(g h') / n)
+            const float s = __frsqrt_rn(__fmaf_rn(__fmul_rn(a.eps, down), down, __fdiv_rn(hh, (float)a.n)));
+            const float c = -__fmul_rn(__fmul_rn(s, s), __fdiv_rn(gh, (float)a.n)), sd = __fmul_rn(s, down);
 #pragma unroll
             for (int k = 0; k < VPT; k++) {
+                const int unit = wi + k * wr;
                 float g[8], v[8], w[8];
                 unpack_eight<T>(eg[k], g);
                 unpack_eight<T>(eh[k], v);
-                load_weights<T, VEC>(a.weight, wide, wi + k * wr, lane, a.n, w);
-#pragma unroll
-                for (int j = 0; j < 8; j++) {
-                    const float q = __fmul_rn(v[j], kDown);
-                    hh = __fmaf_rn(q, q, hh);
-                    gh = __fmaf_rn(__fmul_rn(g[j], w[j]), q, gh);
-                }
-            }
-            hh = warp_sum(hh);
-            gh = warp_sum(gh);
-            if (wr > 1) {
-                row_barrier(sub, wr);      // the first sums are read
-                if (lane == 0)
-                    place[turn][warp] = make_float2(hh, gh);
-                row_barrier(sub, wr);
-                const float2 q = lane < wr ? place[turn][sub * wr + lane] : make_float2(0.0f, 0.0f);
-                hh = warp_sum(q.x);
-                gh = warp_sum(q.y);
-            }
-        }
-        // with h' = h down and s' = s / down:  dx = s (g - h' s'^2 sum(g h') / n)
-        const float s = __frsqrt_rn(__fmaf_rn(__fmul_rn(a.eps, down), down, __fdiv_rn(hh, (float)a.n)));
-        const float c = -__fmul_rn(__fmul_rn(s, s), __fdiv_rn(gh, (float)a.n)), sd = __fmul_rn(s, down);
-#pragma unroll
-        for (int k = 0; k < VPT; k++) {
-            const int unit = wi + k * wr;
-            float g[8], v[8], w[8];
-            unpack_eight<T>(eg[k], g);
-            unpack_eight<T>(eh[k], v);
-            load_weights<T, VEC>(a.weight, wide, unit, lane, a.n, w);
-#pragma unroll
-            for (int j = 0; j < 8; j++)
-                v[j] = __fmul_rn(v[j], down);
-            if (want) {
-#pragma unroll
-                for (int j = 0; j < 8; j++) {
-                    const float p = __fmul_rn(v[j], s);
-                    if (kRegs)
-                        dw[kRegs ? k : 0][j] = __fmaf_rn(g[j], p, dw[kRegs ? k : 0][j]);
-                    else
-                        mine[(k * 8 + j) * blockDim.x] = __fmaf_rn(g[j], p, mine[(k * 8 + j) * blockDim.x]);
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < 8; j++)
-                v[j] = __fmul_rn(__fmaf_rn(v[j], c, __fmul_rn(g[j], w[j])), sd);
-            if (a.dh) {
-                unpack_eight<T>(load_eight<T, VEC>(reinterpret_cast<const T *>(a.dh) + t * a.dh_stride, unit, lane, a.n), g);
+                load_weights<T, VEC>(a.weight, wide, unit, lane, a.n, w);
 #pragma unroll
                 for (int j = 0; j < 8; j++)
-                    v[j] = __fadd_rn(v[j], g[j]);
+                    v[j] = __fmul_rn(v[j], down);
+                if (want) {
+#pragma unroll
+                    for (int j = 0; j < 8; j++) {
+                        const float p = __fmul_rn(v[j], s);
+                        if (kRegs)
+                            dw[kRegs ? k : 0][j] = __fmaf_rn(g[j], p, dw[kRegs ? k : 0][j]);
+                        else
+                            mine[(k * 8 + j) * blockDim.x] = __fmaf_rn(g[j], p, mine[(k * 8 + j) * blockDim.x]);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 8; j++)
+                    v[j] = __fmul_rn(__fmaf_rn(v[j], c, __fmul_rn(g[j], w[j])), sd);
+                if (ds) {
+                    unpack_eight<T>(ed[k], g);
+#pragma unroll
+                    for (int j = 0; j < 8; j++)
+                        v[j] = __fadd_rn(v[j], g[j]);
+                }
+                store_eight<T, VEC>(reinterpret_cast<T *>(a.dx) + t * a.dx_stride, unit, lane, a.n, pack_eight<T>(v));
             }
-            store_eight<T, VEC>(reinterpret_cast<T *>(a.dx) + t * a.dx_stride, unit, lane, a.n, pack_eight<T>(v));
+        }
+        if constexpr (WAY) {
+#pragma unroll
+            for (int k = 0; k < VPT; k++)
+                eg[k] = ng[k], eh[k] = nh[k], ed[k] = nd[k];
         }
     }
     if (!want)
@@ -455,21 +474,32 @@ __device__ __forceinline__ void load_values<__nv_bfloat16, false>(const __nv_bfl
     unpack_eight<__nv_bfloat16>(load_eight<__nv_bfloat16, false>(row, unit, lane, n), v);
 }
 
-// 1 x 128: a warp takes one unit of one row after the other
+// 1 x 128: a warp takes four units, one behind the other
+constexpr int kUnitsWarp = 4;
 template <typename T, bool VEC> __global__ void __launch_bounds__(256) rows8_kernel(const Quantize8Launch a) {
     // (a product behind this launch may load its weights; it waits for this kernel's end
     // before it reads what is written here)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int lane = threadIdx.x & 31;
-    const int units = (int)((a.n + kUnitN - 1) / kUnitN);
-    const int64_t total = a.T * units, hop = (int64_t)gridDim.x * 8;
-    for (int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); i < total; i += hop) {
-        const int64_t t = i / units;
-        const int unit = (int)(i % units);
-        float v[8];
-        load_values<T, VEC>(reinterpret_cast<const T *>(a.x) + t * a.stride, unit, lane, (int)a.n, v);
-        encode_row<VEC>(v, a.codes + t * a.n, a.scale + t, a.T, unit, lane, (int)a.n);
+    const int lane = threadIdx.x & 31, n = (int)a.n;
+    const int units = (n + kUnitN - 1) / kUnitN;
+    const int64_t first = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * kUnitsWarp;
+    int64_t t[kUnitsWarp];
+    int unit[kUnitsWarp];
+    t[0] = first / units;
+    unit[0] = (int)(first - t[0] * units);
+#pragma unroll
+    for (int k = 1; k < kUnitsWarp; k++) {
+        const bool end = unit[k - 1] + 1 == units;
+        t[k] = t[k - 1] + end;
+        unit[k] = end ? 0 : unit[k - 1] + 1;
     }
+    float v[kUnitsWarp][8];
+#pragma unroll
+    for (int k = 0; k < kUnitsWarp; k++)
+        load_values<T, VEC>(reinterpret_cast<const T *>(a.x) + t[k] * a.stride, unit[k], lane, t[k] < a.T ? n : 0, v[k]);
+#pragma unroll
+    for (int k = 0; k < kUnitsWarp; k++)
+        encode_row<VEC>(v[k], a.codes + t[k] * n, a.scale + t[k], a.T, unit[k], lane, t[k] < a.T ? n : 0);
 }
 
 // 128 x 128: eight warps to a block, two rows of it a warp at a time
@@ -479,32 +509,60 @@ template <typename T, bool VEC> __global__ void __launch_bounds__(256) blocks8_k
     const int blocks_c = (int)((a.n + 127) / 128);
     const int64_t r0 = (int64_t)(blockIdx.x / blocks_c) * 128;
     const int c0 = (int)(blockIdx.x % blocks_c) * 128, cols = (int)min((int64_t)128, a.n - c0);
-    // (an "eighth" of the values: rows 2i, 2i + 1 of the block as one unit of 256)
-    float v[8][8];
-    uint32_t top = 0;
+    // (a unit of 256 values: rows 2i, 2i + 1 of the block.  They stay in the form they came in:
+    // as 64 numbers of binary32 they left room for three blocks an SM)
+    constexpr int kWords = sizeof(T) == 4 ? 8 : 4;
+    uint32_t raw[8][kWords];
+    auto values = [&](int i, float (&v)[8]) {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                v[j] = __uint_as_float(raw[i][j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const float2 f = unpack2<T>(raw[i][j]);
+                v[2 * j] = f.x, v[2 * j + 1] = f.y;
+            }
+        }
+    };
 #pragma unroll
     for (int i = 0; i < 8; i++) {
-        if (VEC) {
-            const int64_t r = r0 + 2 * (warp + 8 * i) + (lane >> 4);
-            load_values<T, true>(reinterpret_cast<const T *>(a.x) + r * a.stride + c0, 0, lane & 15, r < a.T ? cols : 0, v[i]);
+        const int64_t r = r0 + 2 * (warp + 8 * i) + (VEC ? lane >> 4 : 0);
+        const T *row = reinterpret_cast<const T *>(a.x) + r * a.stride + c0;
+        if constexpr (VEC) {
+            const int c = (lane & 15) * 8;
+            const bool in = r < a.T && c < cols;
+#pragma unroll
+            for (int j = 0; j < kWords; j += 4) {
+                uint4 q = make_uint4(0u, 0u, 0u, 0u);
+                if (in)
+                    q = *reinterpret_cast<const uint4 *>(reinterpret_cast<const char *>(row + c) + 4 * j);
+                raw[i][j] = q.x, raw[i][j + 1] = q.y, raw[i][j + 2] = q.z, raw[i][j + 3] = q.w;
+            }
         } else {
 #pragma unroll
             for (int j = 0; j < 8; j++) {
-                const int64_t r = r0 + 2 * (warp + 8 * i) + (j >> 2);
                 const int c = lane + 32 * (j & 3);
-                v[i][j] = 0.0f;
-                if (r < a.T && c < cols) {
-                    const T *at = reinterpret_cast<const T *>(a.x) + r * a.stride + c0 + c;
-                    if constexpr (sizeof(T) == 4)
-                        v[i][j] = *at;
-                    else
-                        v[i][j] = to_f32<T>(*at);
+                const bool in = r + (j >> 2) < a.T && c < cols;
+                const T *at = row + (j >> 2) * a.stride + c;
+                if constexpr (sizeof(T) == 4) {
+                    raw[i][j] = in ? *reinterpret_cast<const uint32_t *>(at) : 0u;
+                } else {
+                    const uint32_t w = in ? *reinterpret_cast<const uint16_t *>(at) : 0u;
+                    raw[i][j >> 1] = j & 1 ? raw[i][j >> 1] | w << 16 : w;
                 }
             }
         }
+    }
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        float v[8];
+        values(i, v);
 #pragma unroll
         for (int j = 0; j < 8; j++)
-            top = top_bits(top, v[i][j]);
+            top = top_bits(top, v[j]);
     }
     top = __reduce_max_sync(0xffffffffu, top);
     if (lane == 0)
@@ -517,10 +575,12 @@ template <typename T, bool VEC> __global__ void __launch_bounds__(256) blocks8_k
         a.scale[blockIdx.x] = sc;
 #pragma unroll
     for (int i = 0; i < 8; i++) {
+        float v[8];
+        values(i, v);
         uint32_t q[4];
 #pragma unroll
         for (int j = 0; j < 4; j++)
-            q[j] = pack8(__fmul_rn(v[i][2 * j], inv), __fmul_rn(v[i][2 * j + 1], inv));
+            q[j] = pack8(__fmul_rn(v[2 * j], inv), __fmul_rn(v[2 * j + 1], inv));
         if (VEC) {
             const int64_t r = r0 + 2 * (warp + 8 * i) + (lane >> 4);
             const int c = (lane & 15) * 8;
@@ -588,11 +648,11 @@ template <typename T, bool VEC, int VPT> exl3_status norm_grad_k(const NormGradL
     const unsigned block = (unsigned)(f.rows * f.wr * 32), grid = grad_grid(p.T, f);
     const size_t smem = VPT > 2 && p.dweight ? (size_t)VPT * 8 * block * sizeof(float) : 0;
     if (smem) {
-        const cudaError_t e = allow_smem((const void *)norm_grad_kernel<T, VEC, VPT>, smem);
+        const cudaError_t e = allow_smem((const void *)norm_grad_kernel<T, VEC, VPT, VPT == 1>, smem);
         if (e != cudaSuccess)
             return cuda_check(e, "cudaFuncSetAttribute(norm gradient)");
     }
-    norm_grad_kernel<T, VEC, VPT><<<grid, block, smem, s>>>(p, f.wr);
+    norm_grad_kernel<T, VEC, VPT, VPT == 1><<<grid, block, smem, s>>>(p, f.wr);
     note_launch();
     return cuda_check(cudaGetLastError(), "norm gradient launch");
 }
@@ -618,8 +678,8 @@ template <typename T> exl3_status norm_grad_t(const NormGradLaunch &p, bool vec,
 template <typename T> exl3_status quantize8_t(const Quantize8Launch &p, cudaStream_t s) {
     const bool vec = wide_rows(p.x, p.stride, sizeof(T)) && p.n % 8 == 0 && ((uintptr_t)p.codes & 7u) == 0;
     if (p.block_rows == 1) {
-        const int64_t warps = p.T * ((p.n + kUnitN - 1) / kUnitN), most = (int64_t)device_sm_count() * 8;
-        const unsigned grid = (unsigned)((warps + 7) / 8 < most ? (warps + 7) / 8 : most);
+        const int64_t units = p.T * ((p.n + kUnitN - 1) / kUnitN);
+        const unsigned grid = (unsigned)((units + 8 * kUnitsWarp - 1) / (8 * kUnitsWarp));
         if (vec)
             rows8_kernel<T, true><<<grid, 256, 0, s>>>(p);
         else

@@ -10,11 +10,26 @@ import ctypes
 import torch
 
 from . import EXL3_BF16, EXL3_E4M3, EXL3_F16, EXL3_F32
-from .products import _activations, _call, _coded, _dense, _grad_on, _lib, _rows, _stream, _ws
+from .products import _activations, _call, _coded, _current_device, _dense, _grad_on, _lib, _rows, _stream
+from .products import _ws as _given_ws
 
 _DT = {torch.bfloat16: EXL3_BF16, torch.float16: EXL3_F16}
 _DT_X = {**_DT, torch.float32: EXL3_F32}
 _E4M3 = torch.float8_e4m3fn
+
+# torch.empty_strided without the dispatcher, on the current device (two microseconds of
+# the seven that an allocation and a launch take)
+_strided = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
+
+
+def _new(shape, stride, dtype, dev):
+    if _strided is not None and _current_device() == dev.index:
+        return _strided(shape, stride, dtype)
+    return torch.empty_strided(shape, stride, dtype=dtype, device=dev)
+
+
+def _ws(need, dev, ws):
+    return _new((max(need, 256),), (1,), torch.uint8, dev) if ws is None else _given_ws(need, dev, ws)
 
 
 def rms_norm_backward_workspace_bytes(T: int, n: int) -> int:
@@ -110,24 +125,24 @@ def rms_norm(x, weight, eps: float = 1e-6, residual=None, want_y: bool = True, w
         return dict(h=h, y=y, y8=None, scale=None)
     if residual is not None:
         if h is None:
-            h = torch.empty(T, n, dtype=x.dtype, device=dev)
+            h = _new((T, n), (n, 1), x.dtype, dev)
         else:
             hs = _matrix(h, "h", _DT, n, like=x)
     y = y8 = scale = None
     if want_y:
         if out is None:
-            y = torch.empty(T, n, dtype=x.dtype, device=dev)
+            y = _new((T, n), (n, 1), x.dtype, dev)
         else:
             y = out
             ys = _matrix(out, "out", _DT, n, like=x)
     if want_y8:
-        y8 = torch.empty(T, n, dtype=_E4M3, device=dev)
-        scale = torch.empty((n + 127) // 128, T, dtype=torch.float32, device=dev)
+        y8 = _new((T, n), (n, 1), _E4M3, dev)
+        scale = _new((T, (n + 127) // 128), (1, T), torch.float32, dev)
     _call(_lib().exl3_rms_norm, dev.index, x.data_ptr(), _DT[x.dtype], T, n, xs,
           None if residual is None else residual.data_ptr(), rs, pw, wdt, eps, None if h is None else h.data_ptr(), hs,
           y.data_ptr() if want_y else None, ys, y8.data_ptr() if want_y8 else None,
           scale.data_ptr() if want_y8 else None, _stream(dev.index))
-    return dict(h=h, y=y, y8=y8, scale=scale.t() if want_y8 else None)
+    return dict(h=h, y=y, y8=y8, scale=scale)
 
 
 def rms_norm_backward(dy, h, weight, eps: float = 1e-6, dh=None, want_dweight: bool = True, dx=None, ws=None):
@@ -145,14 +160,14 @@ def rms_norm_backward(dy, h, weight, eps: float = 1e-6, dh=None, want_dweight: b
     if dh is not None:
         ds = _matrix(dh, "dh", _DT, n, like=dy)
     if dx is None:
-        dx = torch.empty(T, n, dtype=dy.dtype, device=dev)
+        dx = _new((T, n), (n, 1), dy.dtype, dev)
     else:
         xs = _matrix(dx, "dx", _DT, n, like=dy)
     L = _lib()
     dw = pws = None
     bytes_ = 0
     if want_dweight:
-        dw = torch.empty(n, dtype=weight.dtype, device=dev)
+        dw = _new((n,), (1,), weight.dtype, dev)
         ws = _ws(L.exl3_rms_norm_backward_workspace_bytes(T, n), dev, ws)
         pws, bytes_ = ws.data_ptr(), ws.numel() * ws.element_size()
     _call(L.exl3_rms_norm_backward, dev.index, dy.data_ptr(), gs, h.data_ptr(), hs, _DT[dy.dtype], T, n, pw, wdt, eps,
@@ -169,12 +184,15 @@ def quantize8(x, block_rows: int = 1):
     xs = _matrix(x, "x", _DT_X)
     T, n = x.shape
     dev = x.device
-    codes = torch.empty(T, n, dtype=_E4M3, device=dev)
+    codes = _new((T, n), (n, 1), _E4M3, dev)
     nb = (n + 127) // 128
-    scale = torch.empty((nb, T) if block_rows == 1 else ((T + 127) // 128, nb), dtype=torch.float32, device=dev)
+    if block_rows == 1:
+        scale = _new((T, nb), (1, T), torch.float32, dev)
+    else:
+        scale = _new(((T + 127) // 128, nb), (nb, 1), torch.float32, dev)
     _call(_lib().exl3_quantize8, dev.index, x.data_ptr(), _DT_X[x.dtype], T, n, xs, block_rows, codes.data_ptr(),
           scale.data_ptr(), _stream(dev.index))
-    return codes, scale.t() if block_rows == 1 else scale
+    return codes, scale
 
 
 class _Linear8(torch.autograd.Function):
@@ -240,7 +258,7 @@ def linear8(x, w, w_scale, x_scale=None, transposed: bool = False, dtype=None, o
             raise ValueError("out does not go with inputs that want a gradient (torch.no_grad() lets it)")
         return _Linear8.apply(x, w, w_scale, transposed, dtype, ws)
     if out is None:
-        out = torch.empty(T, n_out, dtype=dtype, device=dev)
+        out = _new((T, n_out), (n_out, 1), dtype, dev)
         ys = n_out
     else:
         ys = _matrix(out, "out", (dtype,), n_out)
@@ -303,7 +321,7 @@ def expert_layer(x, gate, up, down, K: int, top_k: int, router=None, ids=None, w
             if t is not None and t.requires_grad:
                 raise ValueError(f"there is no gradient with respect to {name} (torch.no_grad(); expert_linear has one)")
     if out is None:
-        out = torch.empty(T, H, dtype=x.dtype, device=dev)
+        out = _new((T, H), (H, 1), x.dtype, dev)
         ys = H
     else:
         ys = _activations(out, "out", H, like=x)
