@@ -28,9 +28,10 @@ struct DownArgs {
     void *y;
     int dt;
     int64_t y_stride;
+    bool two_parts;
 };
 
-template <int K, bool TR, int NB> struct DownOp {
+template <int K, bool TR, int RB, bool LO> struct DownOp {
     const DownArgs &a;
     int64_t hop, hop_f;       // bytes from tile to tile of codes along the inputs and the outputs
     __device__ __forceinline__ explicit DownOp(const DownArgs &a_) : a(a_) {
@@ -41,26 +42,30 @@ template <int K, bool TR, int NB> struct DownOp {
     __device__ __forceinline__ const char *codes(int, int e, int f0) const {
         return reinterpret_cast<const char *>(a.m.codes) + (int64_t)e * (a.H / 16) * (a.F / 16) * (32 * K) + f0 / 16 * hop_f;
     }
-    __device__ __forceinline__ uint32_t bytes(int rows) const { return 2u * (uint32_t)rows * 128u + (uint32_t)rows * 4u; }
+    __device__ __forceinline__ uint32_t bytes(int rows) const { return (LO ? 4u : 2u) * (uint32_t)rows * 128u + (uint32_t)rows * 4u; }
     __device__ __forceinline__ void load(uint32_t to, uint32_t bar, int row0, int k, int rows, int lane) const {
-        if (lane < 2)          // 64 inputs of the step
-            tc::bulk_load(to + lane * (NB * 1024u), a.inner + ((int64_t)(2 * k + lane) * act_rows(a.rows) + row0) * 128,
-                          (uint32_t)rows * 128u, bar);
-        else if (lane == 2)    // and the rows' scales of it
-            tc::bulk_load(to + 2 * (NB * 1024u), a.inner_scale + (int64_t)k * a.rows + row0, (uint32_t)rows * 4u, bar);
+        constexpr int kCopies = LO ? 4 : 2;
+        if (lane < kCopies) {              // 64 inputs of the step, and the part
+            const int64_t NP = act_rows(a.rows);
+            const int q = lane & 1, part = lane >> 1;
+            tc::bulk_load(to + (uint32_t)(q * (LO ? 2 : 1) + part) * (RB * 1024u),
+                          a.inner + part * (NP * a.F * 2) + ((int64_t)(2 * k + q) * NP + row0) * 128, (uint32_t)rows * 128u, bar);
+        } else if (lane == kCopies) {      // and the rows' scales of it
+            tc::bulk_load(to + kCopies * (RB * 1024u), a.inner_scale + (int64_t)k * a.rows + row0, (uint32_t)rows * 4u, bar);
+        }
     }
-    // right 2^-7 s, the rows' pairs (as bits) and weights
+    // right 2^-7 s, the rows' pairs and their tokens' numbers of pairs (as bits) and weights
     __device__ __forceinline__ float fetch(int tid, int e, int row0, int rows, int f0) const {
         if (tid < 128)
             return __fmul_rn(__ldg(a.m.right + (size_t)e * a.H + f0 + tid), __fmul_rn(__ldg(a.m.scale + e), 0x1p-7f));
         const int r = (tid - 128) & 63;
-        if (tid >= 256 || r >= rows)
+        if (tid >= 320 || r >= rows)
             return 0.0f;
         const int p = __ldcg(a.pair_of + row0 + r);
-        return tid < 192 ? __int_as_float(p) : __ldcg(a.weights + p);
+        return tid < 192 ? __int_as_float(p) : tid < 256 ? __ldcg(a.weights + p) : __int_as_float(__ldcg(a.valid + p / a.top_k));
     }
-    __device__ __forceinline__ void finish(float4 v, const float4 &w, const float *kept, int, int r, int f0, int lane) const {
-        v = mul4(mul4(rotate_row(add4(v, w), lane), reinterpret_cast<const float4 *>(kept)[lane]), kept[192 + r]);
+    __device__ __forceinline__ void finish(float4 v, const float4 &, const float *kept, int, int r, int f0, int lane) const {
+        v = mul4(mul4(rotate_row(v, lane), reinterpret_cast<const float4 *>(kept)[lane]), kept[192 + r]);
         const int p = __float_as_int(kept[128 + r]), t = p / a.top_k;
         float4 *part = reinterpret_cast<float4 *>(a.part + f0) + lane;
         const int64_t hop = a.H / 4;
@@ -69,7 +74,7 @@ template <int K, bool TR, int NB> struct DownOp {
         // the last of the token's pairs to come here
         int last = 0;
         if (lane == 0) {
-            const int pairs = __ldcg(a.valid + t);
+            const int pairs = __float_as_int(kept[256 + r]);
             __threadfence();
             last = atomicAdd(a.done + t * (a.H / 128) + f0 / 128, 1) + 1 == pairs ? pairs : 0;
             __threadfence();
@@ -78,7 +83,7 @@ template <int K, bool TR, int NB> struct DownOp {
         if (!last)
             return;
         v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
+#pragma unroll 8
         for (int j = 0; j < a.top_k; j++) {
             const int q = t * a.top_k + j;
             bool has = true;
@@ -100,13 +105,14 @@ template <int K, bool TR, int NB> struct DownOp {
     }
 };
 
-template <int K, bool TR, int NB> __global__ void __launch_bounds__(kExpertThreads, 2) down_kernel(const __grid_constant__ DownArgs a) {
-    run_share<K, TR, NB, false>(a.list, DownOp<K, TR, NB>(a), &g_down_timeouts);
+template <int K, bool TR, int RB, bool LO>
+__global__ void __launch_bounds__(kExpertThreads, 1) down_kernel(const __grid_constant__ DownArgs a) {
+    run_share<K, TR, RB, LO, false>(a.list, DownOp<K, TR, RB, LO>(a), &g_down_timeouts);
 }
 
-template <int K, bool TR, int NB> exl3_status launch_down_form(const DownArgs &a, unsigned grid, cudaStream_t s) {
-    constexpr uint32_t smem = ExpertForm<K, NB, false>::kSmem;
-    cudaError_t e = allow_smem((const void *)down_kernel<K, TR, NB>, smem);
+template <int K, bool TR, int RB, bool LO> exl3_status launch_down_form(const DownArgs &a, unsigned grid, cudaStream_t s) {
+    constexpr uint32_t smem = ExpertForm<K, RB, LO, false>::kSmem;
+    cudaError_t e = allow_smem((const void *)down_kernel<K, TR, RB, LO>, smem);
     if (e != cudaSuccess)
         return cuda_check(e, "cudaFuncSetAttribute(expert layer, down)");
     cudaLaunchConfig_t cfg = {};
@@ -119,7 +125,7 @@ template <int K, bool TR, int NB> exl3_status launch_down_form(const DownArgs &a
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, down_kernel<K, TR, NB>, a);
+    e = cudaLaunchKernelEx(&cfg, down_kernel<K, TR, RB, LO>, a);
     if (e != cudaSuccess)
         return cuda_check(e, "expert layer launch (down)");
     note_launch();
@@ -127,9 +133,11 @@ template <int K, bool TR, int NB> exl3_status launch_down_form(const DownArgs &a
 }
 
 template <int K, bool TR> exl3_status launch_down_n(const DownArgs &a, int tile_n, unsigned grid, cudaStream_t s) {
-    return tile_n == 8    ? launch_down_form<K, TR, 1>(a, grid, s)
-           : tile_n == 16 ? launch_down_form<K, TR, 2>(a, grid, s)
-                          : launch_down_form<K, TR, 4>(a, grid, s);
+    if (a.two_parts)
+        return tile_n == 8 ? launch_down_form<K, TR, 1, true>(a, grid, s) : launch_down_form<K, TR, 2, true>(a, grid, s);
+    return tile_n == 8    ? launch_down_form<K, TR, 1, false>(a, grid, s)
+           : tile_n == 16 ? launch_down_form<K, TR, 2, false>(a, grid, s)
+                          : launch_down_form<K, TR, 4, false>(a, grid, s);
 }
 template <int K> exl3_status launch_down_t(const DownArgs &a, bool tr, int tile_n, unsigned grid, cudaStream_t s) {
     return tr ? launch_down_n<K, true>(a, tile_n, grid, s) : launch_down_n<K, false>(a, tile_n, grid, s);
@@ -157,6 +165,7 @@ exl3_status launch_expert_down(const ExpertLaunch &p, cudaStream_t s) {
     a.y = p.y;
     a.dt = p.dt;
     a.y_stride = p.y_stride;
+    a.two_parts = p.dt == EXL3_F16;
     const unsigned grid = (unsigned)expert_blocks();
     switch (p.K_down) {
     case 1: return launch_down_t<1>(a, p.transposed, p.tile_n, grid, s);

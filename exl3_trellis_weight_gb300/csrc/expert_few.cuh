@@ -4,11 +4,17 @@
 //
 // The work is a list of steps: for each tile of rows, for each 128 outputs, each 128 inputs.
 // How many there are the host does not know (it goes by the picks), and the decoding that
-// bounds them cannot be shared, so the blocks - two to an SM, all there at once - take even
-// shares of the list, whatever it holds.  A tile's outputs that two blocks share are joined
-// in memory: each writes its sums, and the one that is last to come adds them in the order
-// of the list.  Codes and activations are asked for steps ahead, across the tiles, and what
-// the end of a tile needs at its beginning.
+// bounds them cannot be shared, so the blocks - one to an SM, all there at once - take even
+// shares of the list, whatever it holds.  A tile's outputs that blocks share are joined in
+// memory: each writes its sums, and the one that is last to come adds them in the order of
+// the list.  Codes and activations are asked for steps ahead, across the tiles.
+//
+// A block is four sets of eight warps, and a warp takes 128 inputs of its 16 outputs, eight
+// tiles, at a time; which set has which steps is below.  The sets are tied to each other by the
+// stages of the inputs.  With two blocks of half the warps to an SM the first was served
+// before the second, ended after two thirds of the time and left an SM's issue slots half empty
+// (64 tokens over 64 experts, 2048 / 1024, K = 2: 213 us instead of 190); 16 warps with all the
+// registers took 232.
 #pragma once
 
 #include "layer.cuh"
@@ -16,14 +22,14 @@
 
 namespace exl3 {
 
-constexpr int kExpertWarps = 16, kExpertThreads = kExpertWarps * 32;
+constexpr int kExpertWarps = 32, kExpertThreads = kExpertWarps * 32, kSets = 4;
 
 struct ExpertSteps {
     const int4 *tiles;        // expert, first row, rows
     const int32_t *n_tiles;
     int max_tiles;
     int nf, steps;            // 128 outputs and 128 inputs to a tile
-    float *part;              // [2 blocks][2][tile_n][128]: sums of tiles that blocks share
+    float *part;              // [blocks][2][matrices][rows of a tile][128]: sums of tiles that blocks share
     int32_t *done;            // [tiles][nf]: steps of it that are finished
 };
 
@@ -35,32 +41,6 @@ struct Shares {
     __device__ __forceinline__ int block_of(int step) const {
         const int wide = more * (each + 1);
         return step < wide ? step / (each + 1) : more + (step - wide) / each;     // (each > 0 behind `wide`)
-    }
-};
-
-// A warp's codes, GROUPS groups of four tiles a step (of the two that a step has), 16 tiles
-// ahead.  `left` groups follow at `src`, a step's `stride` bytes apart; then `next` is asked
-// for another run of them.
-template <int K, int GROUPS> struct CodeRing {
-    static constexpr int kLanes = 2 * K, kAtOnce = 4;         // lanes of a tile; tiles of a copy group
-    static constexpr int kAhead = kTilesAhead / kAtOnce;      // groups
-    static constexpr uint32_t kGroup = kAtOnce * 32 * K, kBytes = kAhead * kGroup;   // of a warp
-    static_assert(kLanes * kAtOnce <= 32 && kTilesAhead % kAtOnce == 0, "one copy group is one instruction");
-    uint32_t dst;             // of the next group
-    int left;
-    const char *src;
-
-    template <typename Run> __device__ __forceinline__ void next(uint32_t end, int64_t stride, bool mine, Run run) {
-        if (left == 0)
-            run(*this);
-        if (mine && left > 0)
-            tc::copy16(dst, src);
-        tc::copy_group();
-        src += stride;
-        left--;
-        dst += kGroup;
-        if (dst >= end)
-            dst -= kBytes;
     }
 };
 
@@ -101,57 +81,94 @@ __device__ __forceinline__ float4 rotate_row(float4 v, int lane) {
     return v;
 }
 
-// TWO: the warps' halves have a matrix each and all inputs of a step (gate and up), and the
-// halves' sums stay apart; otherwise each has half of a step's inputs, under the rows' scales
-// of that step, and the sums are added.
-template <int K, int NB, bool TWO> struct ExpertForm {
-    using Ring = CodeRing<K, TWO ? 2 : 1>;
-    // inputs of a step: [matrix][64 inputs][NB * 8 rows], and the rows' scales
-    static constexpr uint32_t kInputs = (TWO ? 2u : 1u) * 2u * NB * 1024u, kScales = TWO ? 0u : 256u, kZ = kInputs + kScales;
-    static constexpr int kStages = NB == 4 && TWO ? (K == 4 ? 2 : 3) : NB == 4 || TWO ? 4 : 6;
-    static constexpr uint32_t kRings = kExpertWarps * Ring::kBytes, kSums = 2u * NB * 8u * 512u;
-    static constexpr uint32_t kRingAt = kStages * kZ, kSumsAt = kRingAt + kRings;
+// A block's sums in shared memory, [set][row][33 float4] (the step from row to row spreads
+// a warp's fragments over all banks)
+constexpr int kSumRow = 132;
+__device__ __forceinline__ float4 set_sum(const float4 *sums, int set, int every, int rows, int row, int lane) {
+    float4 v = sums[(set * rows + row) * (kSumRow / 4) + lane];
+    for (set += every; set < kSets; set += every)
+        v = add4(v, sums[(set * rows + row) * (kSumRow / 4) + lane]);
+    return v;
+}
+
+// TWO: the sets have matrix set % 2 (gate and up) and every second step; otherwise every
+// fourth step, whose sums are added under the rows' scales of that step.
+// RB: a tile's blocks of 8 rows.  LO: activations are in two parts.
+template <int K, int RB, bool LO, bool TWO> struct ExpertForm {
+    static constexpr int kMatrices = TWO ? 2 : 1, kGroups = kSets / kMatrices, kRows = RB * 8;
+    // inputs of a step: [matrix][64 inputs][part][rows], and the rows' scales
+    static constexpr uint32_t kPanel = RB * (LO ? 2u : 1u) * 1024u, kInputs = kMatrices * 2u * kPanel;
+    static constexpr uint32_t kZ = kInputs + (TWO ? 0u : 128u);
+    // codes of a step of a warp, the ring of `kAhead` of them, and the stages of inputs: what
+    // shared memory has room for.  (A warp that is served first takes a step in a third of
+    // the latency of memory: two steps in the ring left 36 % of the issue slots empty.)
+    static constexpr uint32_t kCodes = 256u * K, kSums = kSets * kRows * kSumRow * 4u;
+    static constexpr uint32_t kRoom = 219u * 1024u - kSums;
+    static constexpr uint32_t ahead(int stages) {
+        const uint32_t n = (kRoom - stages * kZ) / (kExpertWarps * kCodes);
+        return n < 4u ? n : 4u;
+    }
+    static constexpr int kStages = ahead(4 * kGroups) >= 3u   ? 4 * kGroups
+                                   : ahead(3 * kGroups) >= 3u ? 3 * kGroups
+                                   : ahead(2 * kGroups) >= 3u ? 2 * kGroups
+                                                              : kGroups * 3 / 2;
+    static constexpr int kAhead = (int)ahead(kStages);
+    static constexpr uint32_t kRing = kAhead * kCodes;
+    static constexpr uint32_t kRingAt = kStages * kZ, kSumsAt = kRingAt + kExpertWarps * kRing;
     static constexpr uint32_t kSmem = kSumsAt + kSums + 1024u;
-    static_assert(kSmem <= 106 * 1024 && NB * 32 <= 256, "two blocks an SM, beside 6 KB of other variables");
+    static_assert(kAhead >= 3 && kSmem <= 220 * 1024 && kRows <= kExpertWarps, "beside 7 KB of other variables; a row a warp");
 };
+
+// One more of `all` to have come here; whether it was the last.  (What came before in the
+// others' order comes before what the last does next.)
+__device__ __forceinline__ uint32_t count_in(uint32_t at, uint32_t all) {
+    uint32_t n;
+    asm volatile("atom.acq_rel.cta.shared::cta.inc.u32 %0, [%1], %2;" : "=r"(n) : "r"(at), "r"(all - 1) : "memory");
+    return n == all - 1;
+}
 
 constexpr int kTable = 256;                // tiles that a block keeps the places of
 
 // One block's share of the list.  `op` has
-//   codes(half, e, f0): the first code of expert e's outputs f0 on
+//   codes(matrix, e, f0): the first code of expert e's outputs f0 on
 //   load(to, bar, row0, k, rows, lane): a warp's copies of a step's inputs, bytes(rows) in all
 //   fetch(tid, e, row0, rows, f0): a thread's part of the 512 numbers that finish() needs
-//   finish(x0, x1, kept, row0, r, f0, lane): a row's sums of both halves, by a warp
-template <int K, bool TR, int NB, bool TWO, typename Op>
+//   finish(x0, x1, kept, row0, r, f0, lane): a row's sums (of both matrices), by a warp
+template <int K, bool TR, int RB, bool LO, bool TWO, typename Op>
 __device__ __forceinline__ void run_share(const ExpertSteps &p, const Op &op, unsigned int *count) {
     using namespace tc;
-    using F = ExpertForm<K, NB, TWO>;
-    using Ring = typename F::Ring;
+    using F = ExpertForm<K, RB, LO, TWO>;
+    constexpr int G = F::kGroups, M = F::kMatrices, S = F::kStages;
     extern __shared__ unsigned char smem_raw[];
-    __shared__ __align__(8) unsigned long long bars[2 * F::kStages];
+    __shared__ __align__(8) unsigned long long bars[S + 2];
+    __shared__ uint32_t used[S], filled[S];                    // warps that are done with a stage; times it was asked for
     __shared__ int4 table[kTable];
-    __shared__ float kept[kExpertThreads];
-    __shared__ int gave_up, issued, last;
-    __shared__ int ahead[6];               // the next copies of inputs: share's step, its tile of outputs, step; rows
+    __shared__ __align__(16) float kept[512];
+    __shared__ int gave_up;
+    __shared__ int last[2];                // whether this block joins its first, its other shared tile
     const uint32_t base = (saddr(smem_raw) + 1023u) & ~1023u;
     unsigned char *const sb = smem_raw + (base - saddr(smem_raw));
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-    const int fw = warp & 7, half = warp >> 3, blocks = (int)gridDim.x, block = (int)blockIdx.x;
+    const int fw = warp & 7, set = warp >> 3, matrix = set % M, group = set / M;
+    const int blocks = (int)gridDim.x, block = (int)blockIdx.x;
     const uint32_t bar0 = saddr(bars);
     auto full = [&](int s) { return bar0 + 8u * (uint32_t)s; };
-    auto empty = [&](int s) { return bar0 + 8u * (uint32_t)(F::kStages + s); };
+    // the sums of a tile are there; have been read
+    const uint32_t sums_full = bar0 + 8u * S, sums_read = sums_full + 8u;
     // (the plan is complete: the launch before this one waited for it)
     const int nf = p.nf, steps = p.steps;
     const int n_tiles = __ldcg(p.n_tiles);
     if (tid < kTable && tid < p.max_tiles)
         table[tid] = __ldcg(p.tiles + tid);
     if (tid == 0) {
-        for (int s = 0; s < F::kStages; s++) {
+        for (int s = 0; s < S; s++) {
             bar_init(full(s), 1);
-            bar_init(empty(s), kExpertWarps);
+            used[s] = filled[s] = 0;
         }
+        bar_init(sums_full, kExpertWarps);
+        bar_init(sums_read, kExpertWarps);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        gave_up = issued = 0;
+        gave_up = last[0] = last[1] = 0;
     }
     const int all = n_tiles * nf * steps;
     const Shares shares(all, blocks);
@@ -169,186 +186,202 @@ __device__ __forceinline__ void run_share(const ExpertSteps &p, const Op &op, un
     }
     auto tile_of = [&](int it) { return table[it / nf - first]; };
 
-    // this warp's codes
-    const uint32_t ring0 = base + F::kRingAt + (uint32_t)warp * Ring::kBytes, ring1 = ring0 + Ring::kBytes;
-    const uint32_t lane16 = (uint32_t)lane * 16;
-    const bool mine = lane < Ring::kLanes * Ring::kAtOnce;
-    const int64_t along = (int64_t)fw * op.hop_f + (int64_t)((TWO ? 0 : half) * 4 + lane / Ring::kLanes) * op.hop + (lane % Ring::kLanes) * 16;
-    const int64_t stride = (TWO ? 4 : 8) * op.hop;
-    int ring_it = it0, ring_w = w0;        // where the next run begins
-    auto run = [&](Ring &r) {
-        const int k = ring_w - ring_it * steps, c = min(steps - k, w0 + n - ring_w);
-        if (c > 0) {
-            r.src = op.codes(half, tile_of(ring_it).x, ring_it % nf * 128) + along + (int64_t)k * 8 * op.hop;
-            r.left = c * (TWO ? 2 : 1);
-            ring_w += c;
-            ring_it++;
+    // this warp's codes: 16 K copies of 16 bytes a step
+    const uint32_t ring = base + F::kRingAt + (uint32_t)warp * F::kRing;
+    auto chunk = [&](int c) { return (int64_t)(c / (2 * K)) * op.hop + (c % (2 * K)) * 16; };
+    const int64_t along = (int64_t)fw * op.hop_f + chunk(lane), stride = 8 * G * op.hop;
+    const int more = (int)(chunk(lane + 32) - chunk(lane));
+    uint32_t dst = ring + (uint32_t)lane * 16;
+    int left = 0, run_it = it0, run_i = 0; // steps left at `src`; where the next run begins
+    const char *src = nullptr;
+    auto next_codes = [&]() {
+        while (left == 0 && run_i < n) {
+            const int k = w0 + run_i - run_it * steps, c = min(steps - k, n - run_i), skip = (group - run_i) & (G - 1);
+            if (skip < c) {
+                left = (c - skip + G - 1) / G;
+                src = op.codes(matrix, tile_of(run_it).x, run_it % nf * 128) + along + (int64_t)(k + skip) * 8 * op.hop;
+            }
+            run_i += c;
+            run_it++;
         }
+        if (left > 0) {
+            if (K > 1 || lane < 16)
+                copy16(dst, src);
+            if (K == 4 || (K == 3 && lane < 16))
+                copy16(dst + 512u, src + more);
+            src += stride;
+            left--;
+        }
+        copy_group();
+        dst += F::kCodes;
+        if (dst >= ring + F::kRing)
+            dst -= F::kRing;
     };
-    Ring ring;
-    ring.dst = ring0 + lane16;
-    ring.left = 0;
-    ring.src = nullptr;
 #pragma unroll 1
-    for (int i = 0; i < Ring::kAhead; i++)
-        ring.next(ring1, stride, mine, run);
-    if (tid == 0) {
-        ahead[0] = 0;
-        ahead[1] = it0;
-        ahead[2] = w0 - it0 * steps;
-        ahead[3] = tile_of(it0).y;
-        ahead[4] = (tile_of(it0).z + 7) & ~7;
-    }
+    for (int i = 0; i < F::kAhead; i++)
+        next_codes();
     __syncwarp();
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    // inputs of the next step to stage s, by warp 0
-    auto issue = [&](int s) {
-        const int k = ahead[2], row0 = ahead[3], rows = ahead[4];
-        if (lane == 0)
-            bar_expect(full(s), op.bytes(rows));
-        __syncwarp();
-        op.load(base + (uint32_t)s * F::kZ, full(s), row0, k, rows, lane);
+    // inputs of step i of the share, by a warp
+    auto issue = [&](int i) {
+        const int s = i % S, it = (w0 + i) / steps, k = w0 + i - it * steps;
+        const int4 t = tile_of(it);
+        const int rows = (t.z + 7) & ~7;
         if (lane == 0) {
-            issued = ++ahead[0];
-            if (k + 1 < steps) {
-                ahead[2] = k + 1;
-            } else if (issued < n) {
-                const int4 t = tile_of(++ahead[1]);
-                ahead[2] = 0;
-                ahead[3] = t.y;
-                ahead[4] = (t.z + 7) & ~7;
-            }
+            filled[s]++;
+            bar_expect(full(s), op.bytes(rows));
         }
         __syncwarp();
+        op.load(base + (uint32_t)s * F::kZ, full(s), t.y, k, rows, lane);
     };
-    if (warp == 0)
-        for (int i = 0; i < F::kStages && i < n; i++)
-            issue(i);
+    if (warp < S && warp < n)
+        issue(warp);
     const Lane l = lane_of<K, TR>(lane >> 2, lane & 3);
-    const uint32_t z_mine = base + lane_inputs(lane) + (TWO ? (uint32_t)half * 2u : (uint32_t)half) * (NB * 1024u);
-    Words codes(ring0, l);
-    int turn = Ring::kAhead;               // groups up to the ring's end
+    const uint32_t z_mine = base + lane_inputs(lane) + (uint32_t)matrix * (2u * F::kPanel);
+    Words codes(ring, l);
+    int turn = F::kAhead;                  // steps up to the ring's end
     float *const sums = reinterpret_cast<float *>(sb + F::kSumsAt);
-    int s = 0, it = it0;
-    uint32_t phase = 0;
+    // sums of a shared tile: of the block's first one, or its other
+    auto part_of = [&](int b, int which, int m) { return p.part + (int64_t)((b * 2 + which) * M + m) * (F::kRows * 128); };
     bool ok = true;
+    int it = it0;
+    uint32_t meet = 0;                     // parity of the sums' meetings
 #pragma unroll 1
     for (int i = 0; i < n; it++) {
-        const int k0 = w0 + i - it * steps, c = min(steps - k0, n - i);
+        const int k0 = w0 + i - it * steps, c = min(steps - k0, n - i), end = i + c;
         const bool own_first = i == 0;
         const int4 tl = tile_of(it);
         const int rows = tl.z, f0 = it % nf * 128, row_blocks = (rows + 7) / 8;
-        const float number = op.fetch(tid, tl.x, tl.y, rows, f0);
-        float acc[NB][4];
+        const float number = tid < 512 ? op.fetch(tid, tl.x, tl.y, rows, f0) : 0.0f;
+        float acc[RB][4];
 #pragma unroll
-        for (int b = 0; b < NB; b++)
+        for (int b = 0; b < RB; b++)
 #pragma unroll
             for (int j = 0; j < 4; j++)
                 acc[b][j] = 0.0f;
+        i += (group - i) & (G - 1);
 #pragma unroll 1
-        for (int end = i + c; i < end; i++) {
-            ok = ok && __all_sync(0xffffffffu, bar_wait(full(s), phase, &gave_up, count));
-            const uint32_t z = z_mine + (uint32_t)s * F::kZ;
-            float step[NB][4];
-            if (!TWO) {
-#pragma unroll
-                for (int b = 0; b < NB; b++)
-#pragma unroll
-                    for (int j = 0; j < 4; j++)
-                        step[b][j] = 0.0f;
-            }
-#pragma unroll 1
-            for (int g = 0; g < (TWO ? 2 : 1); g++) {
-                copy_wait<Ring::kAhead - 1>();
-                __syncwarp();
-                if (ok)
-                    four_tiles<K, TR, NB, 1>(codes, l, z + g * (NB * 1024u), row_blocks, TWO ? acc : step);
-                __syncwarp();              // every lane has read the tiles that the next copies replace
-                ring.next(ring1, stride, mine, run);
-                turn--;
-                codes.move(turn ? Ring::kGroup : Ring::kGroup - Ring::kBytes);
-                if (turn == 0)
-                    turn = Ring::kAhead;
-            }
-            if (!TWO) {
-                const float2 *scale = reinterpret_cast<const float2 *>(sb + (uint32_t)s * F::kZ + F::kInputs) + (lane & 3);
-#pragma unroll
-                for (int b = 0; b < NB; b++) {
-                    const float2 f = scale[4 * b];
-#pragma unroll
-                    for (int j = 0; j < 4; j++)
-                        acc[b][j] = __fmaf_rn(step[b][j], j & 1 ? f.y : f.x, acc[b][j]);
-                }
-            }
+        for (; i < end; i += G) {
+            const int s = i % S;
+            ok = ok && __all_sync(0xffffffffu, bar_wait(full(s), (uint32_t)(i / S) & 1, &gave_up, count));
+            copy_wait<F::kAhead - 1>();
             __syncwarp();
-            if (lane == 0)
-                bar_arrive(empty(s));
-            // the stage before this one is empty by now, or nearly
-            if (warp == 0 && i > 0 && i - 1 + F::kStages < n) {
-                const int before = s == 0 ? F::kStages - 1 : s - 1;
-                if (__all_sync(0xffffffffu, bar_wait(empty(before), s == 0 ? phase ^ 1 : phase, &gave_up, count)))
-                    issue(before);
-            }
-            if (++s == F::kStages)
-                s = 0, phase ^= 1;
-        }
-        // the sums meet in shared memory
-        kept[tid] = number;
-        if (c == steps) {
+            if (ok) {
+                const uint32_t z0 = z_mine + (uint32_t)s * F::kZ;
+                const uint32_t z[4] = {z0, z0 ^ 32u, z0 ^ 64u, z0 ^ 96u};
+                if constexpr (TWO) {
+                    eight_tiles<K, TR, RB, LO, F::kPanel>(codes, l, z, row_blocks, acc);
+                } else {
+                    float step[RB][4];
 #pragma unroll
-            for (int b = 0; b < NB; b++)
+                    for (int b = 0; b < RB; b++)
 #pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    const int o = sum_output<K, TR>(fw, lane, j);
-                    sums[(half * NB * 8 + sum_row(lane, b, j)) * 128 + 4 * out_at(o >> 2) + (o & 3)] = acc[b][j];
+                        for (int j = 0; j < 4; j++)
+                            step[b][j] = 0.0f;
+                    eight_tiles<K, TR, RB, LO, F::kPanel>(codes, l, z, row_blocks, step);
+                    const float2 *scale = reinterpret_cast<const float2 *>(sb + (uint32_t)s * F::kZ + F::kInputs) + (lane & 3);
+#pragma unroll
+                    for (int b = 0; b < RB; b++) {
+                        const float2 f = scale[4 * b];
+#pragma unroll
+                        for (int j = 0; j < 4; j++)
+                            acc[b][j] = __fmaf_rn(step[b][j], j & 1 ? f.y : f.x, acc[b][j]);
+                    }
                 }
+            }
+            __syncwarp();                  // every lane has read what the next copies replace
+            next_codes();
+            turn--;
+            codes.move(turn ? F::kCodes : F::kCodes - F::kRing);
+            if (turn == 0)
+                turn = F::kAhead;
+            // whoever is the last to be done with a stage asks for its next inputs (a warp that
+            // waited for the others instead was the last itself: a quarter of the time)
+            if (ok && i + S < n) {
+                uint32_t before = 0;
+                if (lane == 0)
+                    before = count_in(saddr(used + s), kExpertWarps / G);
+                if (__shfl_sync(0xffffffffu, before, 0) != 0u)
+                    issue(i + S);
+            }
+        }
+        i = end;
+        // the row that this warp finishes, from another set on at each tile
+        const int row = (warp + it * 8) % kExpertWarps;
+        // the sums meet in shared memory, once the rows of the tile before have been read
+        ok = ok && __all_sync(0xffffffffu, bar_wait(sums_read, meet ^ 1, &gave_up, count));
+        if (tid < 512)
+            kept[tid] = number;
+#pragma unroll
+        for (int b = 0; b < RB; b++)
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+                sums[(set * F::kRows + sum_row(lane, b, j)) * kSumRow + sum_output<K, TR>(fw, lane, j)] = acc[b][j];
+        __syncwarp();
+        if (lane == 0)
+            bar_arrive(sums_full);
+        const float4 *const from = reinterpret_cast<const float4 *>(sums);
+        if (c == steps) {
+            // (a warp without a row goes on)
+            if (row < rows) {
+                ok = ok && __all_sync(0xffffffffu, bar_wait(sums_full, meet, &gave_up, count));
+                if (ok)
+                    op.finish(set_sum(from, 0, M, F::kRows, row, lane), TWO ? set_sum(from, 1, M, F::kRows, row, lane) : float4{}, kept,
+                              tl.y, row, f0, lane);
+            }
         } else {
-            // of a share of the inputs: to memory, and the last to come adds all up
-            float *part = p.part + (int64_t)(block * 2 + (own_first ? 0 : 1)) * 2 * (NB * 8 * 128);
-#pragma unroll
-            for (int b = 0; b < NB; b++)
-#pragma unroll
-                for (int j = 0; j < 4; j++)
-                    if (sum_row(lane, b, j) < rows)
-                        __stcg(part + (half * NB * 8 + sum_row(lane, b, j)) * 128 + sum_output<K, TR>(fw, lane, j), acc[b][j]);
-            __threadfence();
+            // of a share of the inputs: to memory
+            ok = ok && __all_sync(0xffffffffu, bar_wait(sums_full, meet, &gave_up, count));
+            for (int q = warp; q < M * rows; q += kExpertWarps) {
+                const int m = q >= rows ? 1 : 0, r = q - m * rows;
+                __stcg(reinterpret_cast<float4 *>(part_of(block, own_first ? 0 : 1, m) + r * 128) + lane, set_sum(from, m, M, F::kRows, r, lane));
+            }
             __syncthreads();
             if (tid == 0) {
-                last = atomicAdd(p.done + it, c) + c == steps;
+                __threadfence();
+                last[own_first ? 0 : 1] = atomicAdd(p.done + it, c) + c == steps;
                 __threadfence();
             }
-            __syncthreads();
-            if (!last)
-                continue;                  // (`last` is written again behind another barrier)
-            const int from = it * steps, b_lo = shares.block_of(from), b_hi = shares.block_of(from + steps - 1);
-            for (int q = tid; q < 2 * rows * 32; q += kExpertThreads) {
-                const int h = q >= rows * 32 ? 1 : 0, r = (q >> 5) - h * rows, f = q & 31;
-                const float *at = p.part + (int64_t)((h * NB * 8 + r) * 128 + f * 4);
-                float4 sum = {};
-#pragma unroll 4
-                for (int b = b_lo; b <= b_hi; b++) {
-                    const int own = shares.first(b) >= from ? 0 : 1;
-                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(at + (int64_t)(b * 2 + own) * 2 * (NB * 8 * 128)));
-                    sum.x = __fadd_rn(sum.x, v.x), sum.y = __fadd_rn(sum.y, v.y);
-                    sum.z = __fadd_rn(sum.z, v.z), sum.w = __fadd_rn(sum.w, v.w);
-                }
-                reinterpret_cast<float4 *>(sums)[(h * NB * 8 + r) * 32 + out_at(f)] = sum;
-            }
         }
-        __syncthreads();
-#pragma unroll 1
-        for (int r = warp; r < rows; r += kExpertWarps) {
-            const float4 *at = reinterpret_cast<const float4 *>(sums) + r * 32 + out_at(lane);
-            op.finish(at[0], at[NB * 8 * 32], kept, tl.y, r, f0, lane);
-        }
-        __syncthreads();
+        __syncwarp();
+        if (lane == 0)
+            bar_arrive(sums_read);
+        meet ^= 1;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
+    // whose last share came from here, is added up: a row to a warp
+#pragma unroll 1
+    for (int which = 0; which < 2; which++) {
+        if (!last[which])
+            continue;
+        const int at = which ? it - 1 : it0, lo = at * steps, b_lo = shares.block_of(lo), b_hi = shares.block_of(lo + steps - 1);
+        const int4 tl = tile_of(at);
+        const int rows = tl.z, f0 = at % nf * 128;
+        const float number = tid < 512 ? op.fetch(tid, tl.x, tl.y, rows, f0) : 0.0f;
+        float4 v[M];
+#pragma unroll
+        for (int m = 0; m < M; m++)
+            v[m] = float4{};
+        if (warp < rows) {
+#pragma unroll 4
+            for (int b = b_lo; b <= b_hi; b++)
+#pragma unroll
+                for (int m = 0; m < M; m++)
+                    v[m] = add4(v[m], __ldcg(reinterpret_cast<const float4 *>(part_of(b, shares.first(b) >= lo ? 0 : 1, m) + warp * 128) + lane));
+        }
+        __syncthreads();
+        if (tid < 512)
+            kept[tid] = number;
+        __syncthreads();
+        if (warp < rows)
+            op.finish(v[0], v[M - 1], kept, tl.y, warp, f0, lane);
+    }
     if (gave_up && tid == 0)               // nothing may be in flight when the block ends
-        for (int i = max(0, issued - F::kStages); i < issued; i++)
-            bar_drain(full(i % F::kStages), (uint32_t)(i / F::kStages) & 1);
+        for (int i = 0; i < S; i++)
+            if (filled[i])
+                bar_drain(full(i), (filled[i] - 1) & 1);
 }
 
 }  // namespace exl3

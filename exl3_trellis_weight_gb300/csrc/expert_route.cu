@@ -238,6 +238,7 @@ template <bool ROUTE> __global__ void __launch_bounds__(kPlanThreads) plan_kerne
 }
 
 // ---- rotated activations: a block for a row and one of its two matrices --------------------
+// (x in binary16: its rotation is kept in two parts, see layer.cuh)
 template <typename TX, bool VEC> __global__ void __launch_bounds__(1024) pairs_kernel(const ExpertLaunch a, int order) {
     __shared__ float wmax[32];
     extern __shared__ __align__(16) float parts[];
@@ -278,7 +279,7 @@ template <typename TX, bool VEC> __global__ void __launch_bounds__(1024) pairs_k
 #pragma unroll
         for (int i = 0; i < 16; i++)
             v[i] = in ? __fmul_rn(v[i], up) : 0.0f;
-        rotate_out128(v, a.image[which], order, NP, row, k, in, part, lane);
+        rotate_out128<kTwoParts<TX>>(v, a.image[which], order, NP, row, k, in, part, lane, NP * a.H * 2);
     }
 }
 

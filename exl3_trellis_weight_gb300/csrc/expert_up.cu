@@ -24,11 +24,12 @@ struct UpArgs {
     int order;                // of 16 neighbouring inputs of D's product
     unsigned char *inner;
     float *inner_scale;       // [F / 128][rows]
+    bool two_parts;
 };
 
 __device__ __forceinline__ float silu(float v) { return __fdiv_rn(v, __fadd_rn(1.0f, expf(-v))); }
 
-template <int K, bool TR, int NB> struct UpOp {
+template <int K, bool TR, int RB, bool LO> struct UpOp {
     const UpArgs &a;
     int64_t hop, hop_f;       // bytes from tile to tile of codes along the inputs and the outputs
     __device__ __forceinline__ explicit UpOp(const UpArgs &a_) : a(a_) {
@@ -39,11 +40,14 @@ template <int K, bool TR, int NB> struct UpOp {
     __device__ __forceinline__ const char *codes(int half, int e, int f0) const {
         return reinterpret_cast<const char *>(a.m[half].codes) + (int64_t)e * (a.H / 16) * (a.F / 16) * (32 * K) + f0 / 16 * hop_f;
     }
-    __device__ __forceinline__ uint32_t bytes(int rows) const { return 4u * (uint32_t)rows * 128u; }
+    __device__ __forceinline__ uint32_t bytes(int rows) const { return (LO ? 8u : 4u) * (uint32_t)rows * 128u; }
     __device__ __forceinline__ void load(uint32_t to, uint32_t bar, int row0, int k, int rows, int lane) const {
-        if (lane < 4)          // matrix and 64 inputs of the step
-            tc::bulk_load(to + lane * (NB * 1024u), a.image[lane >> 1] + ((int64_t)(2 * k + (lane & 1)) * act_rows(a.rows) + row0) * 128,
-                          (uint32_t)rows * 128u, bar);
+        if (lane < (LO ? 8 : 4)) {         // matrix and 64 inputs of the step, and the part
+            const int64_t NP = act_rows(a.rows);
+            const int q = lane & 3, part = lane >> 2;
+            tc::bulk_load(to + (uint32_t)(q * (LO ? 2 : 1) + part) * (RB * 1024u),
+                          a.image[q >> 1] + part * (NP * a.H * 2) + ((int64_t)(2 * k + (q & 1)) * NP + row0) * 128, (uint32_t)rows * 128u, bar);
+        }
     }
     // right 2^-7 s of both matrices, D's left factors, the rows' scales of both images
     __device__ __forceinline__ float fetch(int tid, int e, int row0, int rows, int f0) const {
@@ -72,27 +76,34 @@ template <int K, bool TR, int NB> struct UpOp {
         if (lane == 0)
             a.inner_scale[(int64_t)(f0 / 128) * a.rows + row] = down;
         const int k = f0 + 4 * lane;
-        if (a.order == 0) {
-            *reinterpret_cast<uint2 *>(a.inner + act_offset(NP, row, k)) = make_uint2(pack2<__half>(g.x, g.y), pack2<__half>(g.z, g.w));
-        } else {
-            const float f[4] = {g.x, g.y, g.z, g.w};
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
-                const int q = (k & 15) + j;                           // of sixteen
-                const int to = a.order == 1 ? 4 * (q & 3) + (q >> 2) : 4 * ((q & 7) >> 1) + (q & 1) + 2 * (q >> 3);
-                *reinterpret_cast<__half *>(a.inner + act_offset(NP, row, (k & ~15) + to)) = __float2half_rn(f[j]);
+        for (int part = 0; part < (LO ? 2 : 1); part++) {
+            unsigned char *const inner = a.inner + part * (NP * a.F * 2);
+            const uint2 w = make_uint2(pack2<__half>(g.x, g.y), pack2<__half>(g.z, g.w));
+            if (a.order == 0) {
+                *reinterpret_cast<uint2 *>(inner + act_offset(NP, row, k)) = w;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    const int q = (k & 15) + j;                       // of sixteen
+                    const int to = a.order == 1 ? 4 * (q & 3) + (q >> 2) : 4 * ((q & 7) >> 1) + (q & 1) + 2 * (q >> 3);
+                    *reinterpret_cast<uint16_t *>(inner + act_offset(NP, row, (k & ~15) + to)) = (uint16_t)((j & 2 ? w.y : w.x) >> (16 * (j & 1)));
+                }
             }
+            const float2 p = unpack2<__half>(w.x), q = unpack2<__half>(w.y);
+            g = make_float4(__fsub_rn(g.x, p.x), __fsub_rn(g.y, p.y), __fsub_rn(g.z, q.x), __fsub_rn(g.w, q.y));
         }
     }
 };
 
-template <int K, bool TR, int NB> __global__ void __launch_bounds__(kExpertThreads, 2) up_kernel(const __grid_constant__ UpArgs a) {
-    run_share<K, TR, NB, true>(a.list, UpOp<K, TR, NB>(a), &g_up_timeouts);
+template <int K, bool TR, int RB, bool LO>
+__global__ void __launch_bounds__(kExpertThreads, 1) up_kernel(const __grid_constant__ UpArgs a) {
+    run_share<K, TR, RB, LO, true>(a.list, UpOp<K, TR, RB, LO>(a), &g_up_timeouts);
 }
 
-template <int K, bool TR, int NB> exl3_status launch_up_form(const UpArgs &a, unsigned grid, cudaStream_t s) {
-    constexpr uint32_t smem = ExpertForm<K, NB, true>::kSmem;
-    cudaError_t e = allow_smem((const void *)up_kernel<K, TR, NB>, smem);
+template <int K, bool TR, int RB, bool LO> exl3_status launch_up_form(const UpArgs &a, unsigned grid, cudaStream_t s) {
+    constexpr uint32_t smem = ExpertForm<K, RB, LO, true>::kSmem;
+    cudaError_t e = allow_smem((const void *)up_kernel<K, TR, RB, LO>, smem);
     if (e != cudaSuccess)
         return cuda_check(e, "cudaFuncSetAttribute(expert layer, up)");
     cudaLaunchConfig_t cfg = {};
@@ -105,7 +116,7 @@ template <int K, bool TR, int NB> exl3_status launch_up_form(const UpArgs &a, un
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, up_kernel<K, TR, NB>, a);
+    e = cudaLaunchKernelEx(&cfg, up_kernel<K, TR, RB, LO>, a);
     if (e != cudaSuccess)
         return cuda_check(e, "expert layer launch (up)");
     note_launch();
@@ -113,9 +124,11 @@ template <int K, bool TR, int NB> exl3_status launch_up_form(const UpArgs &a, un
 }
 
 template <int K, bool TR> exl3_status launch_up_n(const UpArgs &a, int tile_n, unsigned grid, cudaStream_t s) {
-    return tile_n == 8    ? launch_up_form<K, TR, 1>(a, grid, s)
-           : tile_n == 16 ? launch_up_form<K, TR, 2>(a, grid, s)
-                          : launch_up_form<K, TR, 4>(a, grid, s);
+    if (a.two_parts)
+        return tile_n == 8 ? launch_up_form<K, TR, 1, true>(a, grid, s) : launch_up_form<K, TR, 2, true>(a, grid, s);
+    return tile_n == 8    ? launch_up_form<K, TR, 1, false>(a, grid, s)
+           : tile_n == 16 ? launch_up_form<K, TR, 2, false>(a, grid, s)
+                          : launch_up_form<K, TR, 4, false>(a, grid, s);
 }
 template <int K> exl3_status launch_up_t(const UpArgs &a, bool tr, int tile_n, unsigned grid, cudaStream_t s) {
     return tr ? launch_up_n<K, true>(a, tile_n, grid, s) : launch_up_n<K, false>(a, tile_n, grid, s);
@@ -139,6 +152,7 @@ exl3_status launch_expert_up(const ExpertLaunch &p, cudaStream_t s) {
     a.order = few_order(p.K_down, p.transposed);
     a.inner = p.inner;
     a.inner_scale = p.inner_scale;
+    a.two_parts = p.dt == EXL3_F16;
     const unsigned grid = (unsigned)expert_blocks();
     switch (p.K) {
     case 1: return launch_up_t<1>(a, p.transposed, p.tile_n, grid, s);

@@ -107,11 +107,11 @@ struct ExpertLaunch {
     int32_t *n_tiles;
     int32_t *done;             // [T][H / 128]: pairs of a token that are finished
     int32_t *valid;            // [T]: pairs of a token that have an expert
-    unsigned char *image[2];   // rotated activations of the rows for gate and up (act_rows(rows) x H)
+    unsigned char *image[2];   // rotated activations of the rows for gate and up (act_rows(rows) x H), parts behind each other
     float *rscale[2];          // [rows]
-    unsigned char *inner;      // rotated silu(.) . (.) of the rows (act_rows(rows) x F)
+    unsigned char *inner;      // rotated silu(.) . (.) of the rows (act_rows(rows) x F), parts behind each other
     float *inner_scale;        // [F / 128][rows]: the powers of two of its blocks
-    float *sums;               // [2 blocks][2][tile_n][128]: of tiles that blocks share
+    float *sums;               // [blocks][2][2][tile_n][128]: of tiles that blocks share
     int32_t *up_done, *down_done;      // [tiles][F / 128], [tiles][H / 128]: finished steps
     float *part;               // [T top_k][H]: a pair's part of the result
     int64_t rows;              // expert_rows(T, top_k, E)
@@ -126,8 +126,15 @@ __host__ __device__ inline int64_t expert_tiles(int64_t T, int top_k, int E, int
     const int64_t n = T * top_k, used = n < E ? n : E, most = used + n / tile_n;
     return most < n ? most : n;
 }
-inline int expert_tile_n(int64_t T) { return T <= 8 ? 8 : T <= 16 ? 16 : 32; }
-inline int64_t expert_blocks() { return 2 * (int64_t)device_sm_count(); }
+// Rotated activations are multiplied in binary16.  One rounding to its 11 bits is an eighth of
+// what a result in bfloat16 loses anyway, but as much as one in binary16 does, and three of
+// them (x for both matrices, the inner activations) doubled its error: for those they are
+// kept in two parts, the second what the first leaves over, and multiplied twice.  The decoding
+// is shared, so that costs a tenth of the time.
+template <typename T> constexpr bool kTwoParts = false;
+template <> constexpr bool kTwoParts<__half> = true;
+inline int expert_tile_n(int64_t T, bool two_parts) { return T <= 8 ? 8 : T <= 16 || two_parts ? 16 : 32; }
+inline int64_t expert_blocks() { return device_sm_count(); }
 exl3_status launch_expert_route(const ExpertLaunch &p, cudaStream_t s);
 exl3_status launch_expert_up(const ExpertLaunch &p, cudaStream_t s);
 exl3_status launch_expert_down(const ExpertLaunch &p, cudaStream_t s);

@@ -159,4 +159,37 @@ __device__ __forceinline__ void four_tiles(const Words &at, const Lane &l, uint3
         four_tiles<K, TR, NB, ANY, I + 1>(at, l, z, blocks, acc);
 }
 
+// two neighbouring words of shared memory, OFF bytes behind `at`
+template <int OFF> __device__ __forceinline__ void lds2(uint32_t at, uint32_t &b0, uint32_t &b1) {
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2 + %3];" : "=r"(b0), "=r"(b1) : "r"(at), "n"(OFF));
+}
+
+// acc += the products of tiles I .. 7 of a step with their inputs: two panels of 64 inputs,
+// PANEL bytes apart, of RB * 8 rows of 128 bytes (LO: and as many of their remainders behind
+// them); z[i]: the lane's inputs of tiles i and 4 + i.  Those of 8 rows from the second on
+// are left out where `blocks` says they hold none.
+template <int K, bool TR, int RB, bool LO, int PANEL, int I = 0, int B = 0>
+__device__ __forceinline__ void tile_rows(const uint32_t (&f)[4], uint32_t z, int blocks, float (&acc)[RB][4]) {
+    if (B == 0 || B < blocks) {
+        constexpr int AT = (I >> 2) * PANEL + B * 1024;
+        uint32_t b0, b1;
+        lds2<AT>(z, b0, b1);
+        mma16(acc[B], f, b0, b1);
+        if constexpr (LO) {
+            lds2<AT + RB * 1024>(z, b0, b1);
+            mma16(acc[B], f, b0, b1);
+        }
+    }
+    if constexpr (B + 1 < RB)
+        tile_rows<K, TR, RB, LO, PANEL, I, B + 1>(f, z, blocks, acc);
+}
+template <int K, bool TR, int RB, bool LO, int PANEL, int I = 0>
+__device__ __forceinline__ void eight_tiles(const Words &at, const Lane &l, const uint32_t (&z)[4], int blocks, float (&acc)[RB][4]) {
+    uint32_t f[4];
+    fragment<K, TR, I * 32 * K>(at, l, f);
+    tile_rows<K, TR, RB, LO, PANEL, I>(f, z[I & 3], blocks, acc);
+    if constexpr (I < 7)
+        eight_tiles<K, TR, RB, LO, PANEL, I + 1>(at, l, z, blocks, acc);
+}
+
 }  // namespace exl3

@@ -169,10 +169,12 @@ __device__ __forceinline__ float block_max(float m, float *place, int warps) {
 // v: elements 16 s + i of a block of 128, s = lane % 8; writes v H in binary16.  Four
 // spans in registers, three after an exchange through the warp's part of shared memory
 // (shuffles, 48 a thread, made 4096 x 4096 22 us instead of 20.5): then lane s has, of each sixteen, the two
-// that stand at places 2s and 2s + 1.
+// that stand at places 2s and 2s + 1.  LO: what binary16 left of them goes to a second image,
+// `lo` bytes behind the first.
 constexpr int kUnit = 144;                 // floats from one block of 128 to the next: other banks
+template <bool LO = false>
 __device__ __forceinline__ void rotate_out128(float (&v)[16], unsigned char *image, int order, int64_t NP, int64_t t, int k,
-                                              bool in, float *part, int lane) {
+                                              bool in, float *part, int lane, int64_t lo = 0) {
     const int s = lane & 7;
     float *const unit = part + (lane >> 3) * kUnit;
 #pragma unroll
@@ -213,8 +215,15 @@ __device__ __forceinline__ void rotate_out128(float (&v)[16], unsigned char *ima
         return;
     const int k0 = k & ~127;
 #pragma unroll
-    for (int b = 0; b < 8; b++)
-        *reinterpret_cast<uint32_t *>(image + act_offset(NP, t, k0 + 16 * b + 2 * s)) = pack2<__half>(v[2 * b], v[2 * b + 1]);
+    for (int b = 0; b < 8; b++) {
+        const uint32_t w = pack2<__half>(v[2 * b], v[2 * b + 1]);
+        unsigned char *const to = image + act_offset(NP, t, k0 + 16 * b + 2 * s);
+        *reinterpret_cast<uint32_t *>(to) = w;
+        if constexpr (LO) {
+            const float2 f = unpack2<__half>(w);
+            *reinterpret_cast<uint32_t *>(to + lo) = pack2<__half>(__fsub_rn(v[2 * b], f.x), __fsub_rn(v[2 * b + 1], f.y));
+        }
+    }
 }
 
 }  // namespace exl3
