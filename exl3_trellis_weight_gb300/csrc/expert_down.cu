@@ -75,11 +75,10 @@ template <int K, bool TR, int RB, bool LO> struct DownOp {
         int last = 0;
         if (lane == 0) {
             const int pairs = __float_as_int(kept[256 + r]);
-            __threadfence();
-            last = atomicAdd(a.done + t * (a.H / 128) + f0 / 128, 1) + 1 == pairs ? pairs : 0;
-            __threadfence();
+            last = add_in(a.done + t * (a.H / 128) + f0 / 128, 1) + 1 == pairs ? pairs : 0;
         }
         last = __shfl_sync(0xffffffffu, last, 0);
+        __syncwarp();
         if (!last)
             return;
         v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);

@@ -127,6 +127,14 @@ __device__ __forceinline__ uint32_t count_in(uint32_t at, uint32_t all) {
     return n == all - 1;
 }
 
+// The same in memory: adds, and returns what was there.  (An atomic between two fences of
+// the whole device took longer.)
+__device__ __forceinline__ int add_in(int32_t *at, int n) {
+    int was;
+    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], %2;" : "=r"(was) : "l"(__cvta_generic_to_global(at)), "r"(n) : "memory");
+    return was;
+}
+
 constexpr int kTable = 256;                // tiles that a block keeps the places of
 
 // One block's share of the list.  `op` has
@@ -338,11 +346,8 @@ __device__ __forceinline__ void run_share(const ExpertSteps &p, const Op &op, un
                 __stcg(reinterpret_cast<float4 *>(part_of(block, own_first ? 0 : 1, m) + r * 128) + lane, set_sum(from, m, M, F::kRows, r, lane));
             }
             __syncthreads();
-            if (tid == 0) {
-                __threadfence();
-                last[own_first ? 0 : 1] = atomicAdd(p.done + it, c) + c == steps;
-                __threadfence();
-            }
+            if (tid == 0)
+                last[own_first ? 0 : 1] = add_in(p.done + it, c) + c == steps;
         }
         __syncwarp();
         if (lane == 0)

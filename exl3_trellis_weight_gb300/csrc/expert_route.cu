@@ -14,7 +14,7 @@ namespace {
 
 constexpr int kTogether = 4;               // tokens that share a reading of an expert's router row
 
-// ---- logits: a warp for an expert and four tokens ------------------------------------
+// ---- logits: a block for an expert and four tokens, its warps share the inputs ---------
 template <typename T, bool VEC> __device__ __forceinline__ void load_router(const void *r, bool wide, int64_t at, float (&v)[8]) {
     if (!wide) {
         load8<T, VEC>(reinterpret_cast<const T *>(r) + at, v);
@@ -31,44 +31,48 @@ template <typename T, bool VEC> __device__ __forceinline__ void load_router(cons
     }
 }
 
-template <typename T, bool VEC> __global__ void __launch_bounds__(128) logits_kernel(const ExpertLaunch a) {
+constexpr int kLogitWarps = 4;
+
+template <typename T, bool VEC> __global__ void __launch_bounds__(kLogitWarps * 32) logits_kernel(const ExpertLaunch a) {
+    __shared__ float place[kLogitWarps][kTogether];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int lane = threadIdx.x & 31;
-    const int64_t job = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int e = (int)(job % a.E);
-    const int64_t t0 = job / a.E * kTogether;
-    if (t0 >= a.T)
-        return;
-    const int n = (int)min((int64_t)kTogether, a.T - t0);
-    const T *x = reinterpret_cast<const T *>(a.x) + t0 * a.x_stride + lane * 8;
-    float sum[kTogether];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int e = (int)(blockIdx.x % (unsigned)a.E);
+    const int64_t t0 = (int64_t)(blockIdx.x / (unsigned)a.E) * kTogether;
+    // (behind the last token its numbers once more)
+    const T *x[kTogether];
 #pragma unroll
     for (int i = 0; i < kTogether; i++)
-        sum[i] = 0.0f;
-#pragma unroll 8
-    for (int k = 0; k < a.H; k += 256) {
-        if (k + lane * 8 < a.H) {          // (H is a multiple of 128)
-            float r[8];
-            load_router<T, VEC>(a.router, a.r_dt == EXL3_F32, (int64_t)e * a.H + k + lane * 8, r);
+        x[i] = reinterpret_cast<const T *>(a.x) + min(t0 + i, a.T - 1) * a.x_stride;
+    float sum[kTogether] = {};
+#pragma unroll 2
+    for (int k = (warp * 32 + lane) * 8; k < a.H; k += kLogitWarps * 256) {
+        float r[8], v[kTogether][8];
+        load_router<T, VEC>(a.router, a.r_dt == EXL3_F32, (int64_t)e * a.H + k, r);
 #pragma unroll
-            for (int i = 0; i < kTogether; i++) {
-                if (i < n) {
-                    float v[8];
-                    load8<T, VEC>(x + i * a.x_stride + k, v);
+        for (int i = 0; i < kTogether; i++)
+            load8<T, VEC>(x[i] + k, v[i]);
 #pragma unroll
-                    for (int m = 0; m < 8; m++)
-                        sum[i] = __fmaf_rn(v[m], r[m], sum[i]);
-                }
-            }
-        }
+        for (int i = 0; i < kTogether; i++)
+#pragma unroll
+            for (int m = 0; m < 8; m++)
+                sum[i] = __fmaf_rn(v[i][m], r[m], sum[i]);
     }
 #pragma unroll
     for (int i = 0; i < kTogether; i++) {
 #pragma unroll
         for (int d = 16; d; d >>= 1)
             sum[i] = __fadd_rn(sum[i], __shfl_xor_sync(0xffffffffu, sum[i], d));
-        if (lane == 0 && i < n)
-            a.logits[(t0 + i) * a.E + e] = sum[i];
+        if (lane == 0)
+            place[warp][i] = sum[i];
+    }
+    __syncthreads();
+    if (threadIdx.x < kTogether && t0 + threadIdx.x < a.T) {
+        float v = place[0][threadIdx.x];
+#pragma unroll
+        for (int w = 1; w < kLogitWarps; w++)
+            v = __fadd_rn(v, place[w][threadIdx.x]);
+        a.logits[(t0 + threadIdx.x) * a.E + e] = v;
     }
 }
 
@@ -123,18 +127,25 @@ template <bool ROUTE> __global__ void __launch_bounds__(kPlanThreads) plan_kerne
                     sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, d));
             }
             int id = 0;                    // the lane's pick
-            for (int j = 0; j < a.top_k; j++) {
-                uint32_t best = 0;
-                int at = a.E;
+            // the largest of a lane's own experts, found again only where one of them is picked
+            uint32_t best = 0;
+            int at = a.E;
+            auto own = [&]() {
+                best = 0, at = a.E;
                 for (int e = lane; e < a.E; e += 32) {
                     const uint32_t k = keys[e];
                     if (k > best || at == a.E)
                         best = k, at = e;
                 }
-                const uint32_t most = __reduce_max_sync(0xffffffffu, at < a.E ? best : 0u);
+            };
+            own();
+            for (int j = 0; j < a.top_k; j++) {
+                const uint32_t most = __reduce_max_sync(0xffffffffu, best);
                 const int pick = (int)__reduce_min_sync(0xffffffffu, at < a.E && best == most ? (uint32_t)at : 0xFFFFu);
-                if (lane == (pick & 31))
+                if (lane == (pick & 31)) {
                     keys[pick] = 0;
+                    own();
+                }
                 if (lane == j)
                     id = pick;
                 __syncwarp();
@@ -161,17 +172,17 @@ template <bool ROUTE> __global__ void __launch_bounds__(kPlanThreads) plan_kerne
     __syncthreads();
     // a warp counts the experts of its share of the pairs, and each pair's place among them
     uint16_t *const seen = reinterpret_cast<uint16_t *>(plan_mem + n);          // [warp][E]
-    for (int i = tid; i < kPlanWarps * a.E; i += kPlanThreads)
+    constexpr int kMaxRounds = 4;                                               // 32 warps x 32 lanes x 4 pairs
+    const int rounds = (n + kPlanThreads - 1) / kPlanThreads, shares = (n + 32 * rounds - 1) / (32 * rounds);
+    for (int i = tid; i < shares * a.E; i += kPlanThreads)
         seen[i] = 0;
     __syncthreads();
-    constexpr int kMaxRounds = 4;                                               // 32 warps x 32 lanes x 4 pairs
-    const int rounds = (n + kPlanThreads - 1) / kPlanThreads;
     uint16_t *const mine = seen + warp * a.E;
     int place[kMaxRounds];
 #pragma unroll
     for (int i = 0; i < kMaxRounds; i++) {
         place[i] = 0;
-        if (i < rounds) {
+        if (i < rounds && warp < shares) {
             const int p = (warp * rounds + i) * 32 + lane, e = p < n ? ids[p] : -1;
             const uint32_t same = __match_any_sync(0xffffffffu, e);
             if (e >= 0)
@@ -182,24 +193,30 @@ template <bool ROUTE> __global__ void __launch_bounds__(kPlanThreads) plan_kerne
             __syncwarp();
         }
     }
-    for (int t = tid; t < T; t += kPlanThreads) {
-        int v = 0;
-        for (int j = 0; j < a.top_k; j++)
-            v += ids[t * a.top_k + j] >= 0;
-        a.valid[t] = v;
+    for (int t = warp; t < T; t += kPlanWarps) {
+        const int v = __popc(__ballot_sync(0xffffffffu, lane < a.top_k && ids[t * a.top_k + min(lane, a.top_k - 1)] >= 0));
+        if (lane == 0)
+            a.valid[t] = v;
         if (v == 0) {                      // no expert: the result is 0
             uint16_t *y = reinterpret_cast<uint16_t *>(a.y) + (int64_t)t * a.y_stride;
-            for (int c = 0; c < a.H; c++)
+            for (int c = lane; c < a.H; c += 32)
                 y[c] = 0;
         }
     }
     __syncthreads();
     for (int e = tid; e < a.E; e += kPlanThreads) {
         int c = 0;
-        for (int w = 0; w < kPlanWarps; w++) {
-            const int k = seen[w * a.E + e];
-            seen[w * a.E + e] = (uint16_t)c;
-            c += k;
+        for (int w0 = 0; w0 < shares; w0 += 8) {
+            int k[8];
+#pragma unroll
+            for (int w = 0; w < 8; w++)
+                k[w] = w0 + w < shares ? seen[(w0 + w) * a.E + e] : 0;
+#pragma unroll
+            for (int w = 0; w < 8; w++) {
+                if (w0 + w < shares)
+                    seen[(w0 + w) * a.E + e] = (uint16_t)c;
+                c += k[w];
+            }
         }
         count[e] = c;
     }
@@ -310,9 +327,9 @@ template <typename T> exl3_status route_t(const ExpertLaunch &p, cudaStream_t s)
     const bool vec = ((uintptr_t)p.x & 15u) == 0 && p.x_stride % 8 == 0;
     exl3_status st;
     if (p.router) {
-        const int64_t jobs = (p.T + kTogether - 1) / kTogether * p.E;
+        const int64_t jobs = (p.T + kTogether - 1) / kTogether * p.E;          // (2^16 at most)
         const bool both = vec && ((uintptr_t)p.router & 15u) == 0;
-        st = start(both ? logits_kernel<T, true> : logits_kernel<T, false>, dim3((unsigned)((jobs + 3) / 4)), 128, 0, false, s, p);
+        st = start(both ? logits_kernel<T, true> : logits_kernel<T, false>, dim3((unsigned)jobs), kLogitWarps * 32, 0, false, s, p);
         if (st != EXL3_OK)
             return st;
         st = start(plan_kernel<true>, dim3(1), kPlanThreads, plan_bytes(p.T * p.top_k, p.E), true, s, p);

@@ -18,6 +18,10 @@ template <int OFF> __device__ __forceinline__ uint32_t lds(uint32_t at) {
     asm volatile("ld.shared.b32 %0, [%1 + %2];" : "=r"(v) : "r"(at), "n"(OFF));
     return v;
 }
+// two neighbouring words of shared memory, OFF bytes behind `at`
+template <int OFF> __device__ __forceinline__ void lds2(uint32_t at, uint32_t &b0, uint32_t &b1) {
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2 + %3];" : "=r"(b0), "=r"(b1) : "r"(at), "n"(OFF));
+}
 // 16 bits of t, `B` bits before its end
 template <int B> __device__ __forceinline__ uint32_t cut(uint32_t t) {
     if constexpr (B % 8 == 0)
@@ -99,13 +103,17 @@ template <int K, bool TR, int OFF> __device__ __forceinline__ void fragment(cons
     } else {
         // rows 4j .. 4j + 3; two outputs of each.  (Neighbouring rows share words up to K = 2.)
         uint32_t w[4][2], t[4];
+        // (up to K = 2 a lane's words from `last` on begin at K * 8 bytes times j)
         if constexpr (K == 1) {
-            const uint32_t q[3] = {lds<OFF>(at.before), lds<OFF>(at.last), lds<OFF + 4>(at.last)};
+            uint32_t q[3] = {lds<OFF>(at.before)};
+            lds2<OFF>(at.last, q[1], q[2]);
 #pragma unroll
             for (int r = 0; r < 4; r++)
                 t[r] = __funnelshift_r(q[(r >> 1) + 1], q[r >> 1], l.sh - 16 * (r & 1));
         } else if constexpr (K == 2) {
-            const uint32_t q[5] = {lds<OFF>(at.before), lds<OFF>(at.last), lds<OFF + 4>(at.last), lds<OFF + 8>(at.last), lds<OFF + 12>(at.last)};
+            uint32_t q[5] = {lds<OFF>(at.before)};
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4 + %5];"
+                         : "=r"(q[1]), "=r"(q[2]), "=r"(q[3]), "=r"(q[4]) : "r"(at.last), "n"(OFF));
 #pragma unroll
             for (int r = 0; r < 4; r++)
                 t[r] = __funnelshift_r(q[r + 1], q[r], l.sh);
@@ -157,11 +165,6 @@ __device__ __forceinline__ void four_tiles(const Words &at, const Lane &l, uint3
     }
     if constexpr (I < 3)
         four_tiles<K, TR, NB, ANY, I + 1>(at, l, z, blocks, acc);
-}
-
-// two neighbouring words of shared memory, OFF bytes behind `at`
-template <int OFF> __device__ __forceinline__ void lds2(uint32_t at, uint32_t &b0, uint32_t &b1) {
-    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2 + %3];" : "=r"(b0), "=r"(b1) : "r"(at), "n"(OFF));
 }
 
 // acc += the products of tiles I .. 7 of a step with their inputs: two panels of 64 inputs,
