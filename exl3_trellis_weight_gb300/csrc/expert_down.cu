@@ -2,8 +2,10 @@
 //
 // A step is 128 outputs and 128 inputs, half of them for each eight warps.  The inputs come
 // in binary16 under a power of two for each 128, so that a step's products are added to the
-// others under it.  A pair's part of the result goes to memory in binary32, and whoever
-// finishes the last pair of a token adds them up in the order of the picks.
+// others under it.  A pair's part of the result goes to memory in binary32, and a small
+// kernel behind adds a token's up in the order of the picks.  (The warp that finished a
+// token's last pair did that at first: the fence and the atomic that told it so stood
+// in the way of the next tile.)
 #include "expert_few.cuh"
 
 namespace exl3 {
@@ -17,17 +19,11 @@ struct DownArgs {
     ExpertMatrix m;
     const unsigned char *inner;
     const float *inner_scale;
-    const int32_t *pair_of, *valid;
-    const int32_t *ids;
+    const int32_t *pair_of;
     const float *weights;
-    int E, top_k;
     int64_t rows;
     int H, F;
     float *part;
-    int32_t *done;
-    void *y;
-    int dt;
-    int64_t y_stride;
     bool two_parts;
 };
 
@@ -54,55 +50,61 @@ template <int K, bool TR, int RB, bool LO> struct DownOp {
             tc::bulk_load(to + kCopies * (RB * 1024u), a.inner_scale + (int64_t)k * a.rows + row0, (uint32_t)rows * 4u, bar);
         }
     }
-    // right 2^-7 s, the rows' pairs and their tokens' numbers of pairs (as bits) and weights
+    // right 2^-7 s, the rows' pairs (as bits) and weights
     __device__ __forceinline__ float fetch(int tid, int e, int row0, int rows, int f0) const {
         if (tid < 128)
             return __fmul_rn(__ldg(a.m.right + (size_t)e * a.H + f0 + tid), __fmul_rn(__ldg(a.m.scale + e), 0x1p-7f));
         const int r = (tid - 128) & 63;
-        if (tid >= 320 || r >= rows)
+        if (tid >= 256 || r >= rows)
             return 0.0f;
         const int p = __ldcg(a.pair_of + row0 + r);
-        return tid < 192 ? __int_as_float(p) : tid < 256 ? __ldcg(a.weights + p) : __int_as_float(__ldcg(a.valid + p / a.top_k));
+        return tid < 192 ? __int_as_float(p) : __ldcg(a.weights + p);
     }
     __device__ __forceinline__ void finish(float4 v, const float4 &, const float *kept, int, int r, int f0, int lane) const {
         v = mul4(mul4(rotate_row(v, lane), reinterpret_cast<const float4 *>(kept)[lane]), kept[192 + r]);
-        const int p = __float_as_int(kept[128 + r]), t = p / a.top_k;
-        float4 *part = reinterpret_cast<float4 *>(a.part + f0) + lane;
-        const int64_t hop = a.H / 4;
-        __stcg(part + p * hop, v);
-        __syncwarp();
-        // the last of the token's pairs to come here
-        int last = 0;
-        if (lane == 0) {
-            const int pairs = __float_as_int(kept[256 + r]);
-            last = add_in(a.done + t * (a.H / 128) + f0 / 128, 1) + 1 == pairs ? pairs : 0;
-        }
-        last = __shfl_sync(0xffffffffu, last, 0);
-        __syncwarp();
-        if (!last)
-            return;
-        v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-        for (int j = 0; j < a.top_k; j++) {
-            const int q = t * a.top_k + j;
-            bool has = true;
-            if (last < a.top_k) {
-                const int id = __ldcg(a.ids + q);
-                has = id >= 0 && id < a.E;
-            }
-            if (has)
-                v = add4(v, __ldcg(part + q * hop));
-        }
-        uint16_t *y = reinterpret_cast<uint16_t *>(a.y) + (int64_t)t * a.y_stride + f0 + 4 * lane;
-        const uint2 q = a.dt == EXL3_BF16 ? make_uint2(pack2<__nv_bfloat16>(v.x, v.y), pack2<__nv_bfloat16>(v.z, v.w))
-                                          : make_uint2(pack2<__half>(v.x, v.y), pack2<__half>(v.z, v.w));
-        if ((((uintptr_t)a.y | (uintptr_t)(a.y_stride * 2)) & 7u) == 0) {
-            *reinterpret_cast<uint2 *>(y) = q;
-        } else {
-            y[0] = (uint16_t)q.x, y[1] = (uint16_t)(q.x >> 16), y[2] = (uint16_t)q.y, y[3] = (uint16_t)(q.y >> 16);
-        }
+        __stcg(reinterpret_cast<float4 *>(a.part + (int64_t)__float_as_int(kept[128 + r]) * a.H + f0) + lane, v);
     }
 };
+
+// ---- y_t, the sum of a token's parts: four columns a thread -------------------------------
+struct SumArgs {
+    const float *part;
+    const int32_t *ids;
+    int E, top_k, H;
+    void *y;
+    int64_t y_stride;
+};
+template <typename T> __global__ void __launch_bounds__(128) sum_kernel(const __grid_constant__ SumArgs a) {
+    const int t = (int)blockIdx.x, c = (int)(blockIdx.y * 128 + threadIdx.x) * 4;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (c >= a.H)
+        return;
+    float4 v = {};
+    const int64_t first = (int64_t)t * a.top_k;
+#pragma unroll 1
+    for (int j0 = 0; j0 < a.top_k; j0 += 8) {
+        // (all are asked for at once; what is no expert's is left out)
+        int id[8];
+        float4 u[8];
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            id[j] = __ldcg(a.ids + first + min(j0 + j, a.top_k - 1));
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            u[j] = __ldcg(reinterpret_cast<const float4 *>(a.part + (first + min(j0 + j, a.top_k - 1)) * a.H + c));
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            if (j0 + j < a.top_k && id[j] >= 0 && id[j] < a.E)
+                v = add4(v, u[j]);
+    }
+    uint16_t *y = reinterpret_cast<uint16_t *>(a.y) + t * a.y_stride + c;
+    const uint2 q = make_uint2(pack2<T>(v.x, v.y), pack2<T>(v.z, v.w));
+    if ((((uintptr_t)a.y | (uintptr_t)(a.y_stride * 2)) & 7u) == 0) {
+        *reinterpret_cast<uint2 *>(y) = q;
+    } else {
+        y[0] = (uint16_t)q.x, y[1] = (uint16_t)(q.x >> 16), y[2] = (uint16_t)q.y, y[3] = (uint16_t)(q.y >> 16);
+    }
+}
 
 template <int K, bool TR, int RB, bool LO>
 __global__ void __launch_bounds__(kExpertThreads, 1) down_kernel(const __grid_constant__ DownArgs a) {
@@ -151,27 +153,37 @@ exl3_status launch_expert_down(const ExpertLaunch &p, cudaStream_t s) {
     a.inner_scale = p.inner_scale;
     a.list = {p.tiles, p.n_tiles, (int)expert_tiles(p.T, p.top_k, p.E, p.tile_n), p.H / 128, p.F / 128, p.sums, p.down_done};
     a.pair_of = p.pair_of;
-    a.valid = p.valid;
-    a.ids = p.ids;
     a.weights = p.weights;
-    a.E = p.E;
-    a.top_k = p.top_k;
     a.rows = p.rows;
     a.H = p.H;
     a.F = p.F;
     a.part = p.part;
-    a.done = p.done;
-    a.y = p.y;
-    a.dt = p.dt;
-    a.y_stride = p.y_stride;
     a.two_parts = p.dt == EXL3_F16;
     const unsigned grid = (unsigned)expert_blocks();
+    exl3_status st;
     switch (p.K_down) {
-    case 1: return launch_down_t<1>(a, p.transposed, p.tile_n, grid, s);
-    case 2: return launch_down_t<2>(a, p.transposed, p.tile_n, grid, s);
-    case 3: return launch_down_t<3>(a, p.transposed, p.tile_n, grid, s);
-    default: return launch_down_t<4>(a, p.transposed, p.tile_n, grid, s);
+    case 1: st = launch_down_t<1>(a, p.transposed, p.tile_n, grid, s); break;
+    case 2: st = launch_down_t<2>(a, p.transposed, p.tile_n, grid, s); break;
+    case 3: st = launch_down_t<3>(a, p.transposed, p.tile_n, grid, s); break;
+    default: st = launch_down_t<4>(a, p.transposed, p.tile_n, grid, s);
     }
+    if (st != EXL3_OK)
+        return st;
+    const SumArgs q = {p.part, p.ids, p.E, p.top_k, p.H, p.y, p.y_stride};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)p.T, (unsigned)((p.H + 511) / 512));
+    cfg.blockDim = dim3(128);
+    cfg.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, p.dt == EXL3_BF16 ? sum_kernel<__nv_bfloat16> : sum_kernel<__half>, q);
+    if (e != cudaSuccess)
+        return cuda_check(e, "expert layer launch (sum)");
+    note_launch();
+    return cuda_check(cudaGetLastError(), "expert layer launch (sum)");
 }
 
 exl3_status expert_down_take_wait_timeouts(unsigned int *n) {

@@ -103,20 +103,21 @@ template <int K, int RB, bool LO, bool TWO> struct ExpertForm {
     // shared memory has room for.  (A warp that is served first takes a step in a third of
     // the latency of memory: two steps in the ring left 36 % of the issue slots empty.)
     static constexpr uint32_t kCodes = 256u * K, kSums = kSets * kRows * kSumRow * 4u;
-    static constexpr uint32_t kRoom = 219u * 1024u - kSums;
-    static constexpr uint32_t ahead(int stages) {
-        const uint32_t n = (kRoom - stages * kZ) / (kExpertWarps * kCodes);
-        return n < 4u ? n : 4u;
+    static constexpr uint32_t kRoom = 219u * 1024u;
+    static constexpr bool fits(int stages, int steps, int meetings) {
+        return stages * kZ + steps * kExpertWarps * kCodes + meetings * kSums <= kRoom;
     }
-    static constexpr int kStages = ahead(4 * kGroups) >= 3u   ? 4 * kGroups
-                                   : ahead(3 * kGroups) >= 3u ? 3 * kGroups
-                                   : ahead(2 * kGroups) >= 3u ? 2 * kGroups
-                                                              : kGroups * 3 / 2;
-    static constexpr int kAhead = (int)ahead(kStages);
+    // (two places for the sums: a tile's rows are read while the next tile's are written)
+    static constexpr int kMeet = fits(2 * kGroups, 3, 2) ? 2 : 1;
+    static constexpr int kStages = fits(4 * kGroups, 3, kMeet)   ? 4 * kGroups
+                                   : fits(3 * kGroups, 3, kMeet) ? 3 * kGroups
+                                   : fits(2 * kGroups, 3, kMeet) ? 2 * kGroups
+                                                                 : kGroups * 3 / 2;
+    static constexpr int kAhead = fits(kStages, 4, kMeet) ? 4 : 3;
     static constexpr uint32_t kRing = kAhead * kCodes;
     static constexpr uint32_t kRingAt = kStages * kZ, kSumsAt = kRingAt + kExpertWarps * kRing;
-    static constexpr uint32_t kSmem = kSumsAt + kSums + 1024u;
-    static_assert(kAhead >= 3 && kSmem <= 220 * 1024 && kRows <= kExpertWarps, "beside 7 KB of other variables; a row a warp");
+    static constexpr uint32_t kSmem = kSumsAt + kMeet * kSums + 1024u;
+    static_assert(fits(kStages, kAhead, kMeet) && kSmem <= 220 * 1024 && kRows <= kExpertWarps, "beside 7 KB of other variables, a row a warp");
 };
 
 // One more of `all` to have come here; whether it was the last.  (What came before in the
@@ -135,7 +136,7 @@ __device__ __forceinline__ int add_in(int32_t *at, int n) {
     return was;
 }
 
-constexpr int kTable = 256;                // tiles that a block keeps the places of
+constexpr int kTable = 128;                // tiles that a block keeps the places of
 
 // One block's share of the list.  `op` has
 //   codes(matrix, e, f0): the first code of expert e's outputs f0 on
@@ -146,13 +147,14 @@ template <int K, bool TR, int RB, bool LO, bool TWO, typename Op>
 __device__ __forceinline__ void run_share(const ExpertSteps &p, const Op &op, unsigned int *count) {
     using namespace tc;
     using F = ExpertForm<K, RB, LO, TWO>;
-    constexpr int G = F::kGroups, M = F::kMatrices, S = F::kStages;
+    constexpr int G = F::kGroups, M = F::kMatrices, S = F::kStages, B = F::kMeet;
     extern __shared__ unsigned char smem_raw[];
-    __shared__ __align__(8) unsigned long long bars[S + 2];
+    __shared__ __align__(8) unsigned long long bars[S + 2 * B];
     __shared__ uint32_t used[S], filled[S];                    // warps that are done with a stage; times it was asked for
     __shared__ int4 table[kTable];
-    __shared__ __align__(16) float kept[512];
+    __shared__ __align__(16) float kept[B][512];
     __shared__ int gave_up;
+    __shared__ int4 cursor[G];             // of a group: tile, outputs and step that follow in a stage it is done with
     __shared__ int last[2];                // whether this block joins its first, its other shared tile
     const uint32_t base = (saddr(smem_raw) + 1023u) & ~1023u;
     unsigned char *const sb = smem_raw + (base - saddr(smem_raw));
@@ -162,7 +164,8 @@ __device__ __forceinline__ void run_share(const ExpertSteps &p, const Op &op, un
     const uint32_t bar0 = saddr(bars);
     auto full = [&](int s) { return bar0 + 8u * (uint32_t)s; };
     // the sums of a tile are there; have been read
-    const uint32_t sums_full = bar0 + 8u * S, sums_read = sums_full + 8u;
+    auto sums_full = [&](int m) { return bar0 + 8u * (uint32_t)(S + m); };
+    auto sums_read = [&](int m) { return bar0 + 8u * (uint32_t)(S + B + m); };
     // (the plan is complete: the launch before this one waited for it)
     const int nf = p.nf, steps = p.steps;
     const int n_tiles = __ldcg(p.n_tiles);
@@ -173,8 +176,10 @@ __device__ __forceinline__ void run_share(const ExpertSteps &p, const Op &op, un
             bar_init(full(s), 1);
             used[s] = filled[s] = 0;
         }
-        bar_init(sums_full, kExpertWarps);
-        bar_init(sums_read, kExpertWarps);
+        for (int m = 0; m < B; m++) {
+            bar_init(sums_full(m), kExpertWarps);
+            bar_init(sums_read(m), kExpertWarps);
+        }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         gave_up = last[0] = last[1] = 0;
     }
@@ -192,7 +197,12 @@ __device__ __forceinline__ void run_share(const ExpertSteps &p, const Op &op, un
             table[tid] = __ldcg(p.tiles + first + tid);
         __syncthreads();
     }
-    auto tile_of = [&](int it) { return table[it / nf - first]; };
+    // the list from the share's first step on: 128 outputs of a tile of rows, and the next ones
+    const int tile0 = it0 / nf - first, out0 = it0 % nf, step0 = w0 - it0 * steps;
+    auto next_outputs = [&](int &tile, int &out) {
+        if (++out == nf)
+            out = 0, tile++;
+    };
 
     // this warp's codes: 16 K copies of 16 bytes a step
     const uint32_t ring = base + F::kRingAt + (uint32_t)warp * F::kRing;
@@ -200,17 +210,17 @@ __device__ __forceinline__ void run_share(const ExpertSteps &p, const Op &op, un
     const int64_t along = (int64_t)fw * op.hop_f + chunk(lane), stride = 8 * G * op.hop;
     const int more = (int)(chunk(lane + 32) - chunk(lane));
     uint32_t dst = ring + (uint32_t)lane * 16;
-    int left = 0, run_it = it0, run_i = 0; // steps left at `src`; where the next run begins
+    int left = 0, run_i = 0, run_tile = tile0, run_out = out0; // steps left at `src`; where the next run begins
     const char *src = nullptr;
     auto next_codes = [&]() {
         while (left == 0 && run_i < n) {
-            const int k = w0 + run_i - run_it * steps, c = min(steps - k, n - run_i), skip = (group - run_i) & (G - 1);
+            const int k = run_i == 0 ? step0 : 0, c = min(steps - k, n - run_i), skip = (group - run_i) & (G - 1);
             if (skip < c) {
                 left = (c - skip + G - 1) / G;
-                src = op.codes(matrix, tile_of(run_it).x, run_it % nf * 128) + along + (int64_t)(k + skip) * 8 * op.hop;
+                src = op.codes(matrix, table[run_tile].x, run_out * 128) + along + (int64_t)(k + skip) * 8 * op.hop;
             }
             run_i += c;
-            run_it++;
+            next_outputs(run_tile, run_out);
         }
         if (left > 0) {
             if (K > 1 || lane < 16)
@@ -231,36 +241,37 @@ __device__ __forceinline__ void run_share(const ExpertSteps &p, const Op &op, un
     __syncwarp();
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    // inputs of step i of the share, by a warp
-    auto issue = [&](int i) {
-        const int s = i % S, it = (w0 + i) / steps, k = w0 + i - it * steps;
-        const int4 t = tile_of(it);
-        const int rows = (t.z + 7) & ~7;
+    // inputs of step i of the share, which is step k of a tile, by a warp
+    auto issue = [&](int i, int tile, int k) {
+        const int s = i % S, rows = (table[tile].z + 7) & ~7;
         if (lane == 0) {
             filled[s]++;
             bar_expect(full(s), op.bytes(rows));
         }
         __syncwarp();
-        op.load(base + (uint32_t)s * F::kZ, full(s), t.y, k, rows, lane);
+        op.load(base + (uint32_t)s * F::kZ, full(s), table[tile].y, k, rows, lane);
     };
     if (warp < S && warp < n)
-        issue(warp);
+        issue(warp, (w0 + warp) / steps / nf - first, (w0 + warp) % steps);
+    if (tid < G) {
+        const int it = (w0 + S + tid) / steps;
+        cursor[tid] = make_int4(it / nf - first, it % nf, w0 + S + tid - it * steps, 0);
+    }
     const Lane l = lane_of<K, TR>(lane >> 2, lane & 3);
     const uint32_t z_mine = base + lane_inputs(lane) + (uint32_t)matrix * (2u * F::kPanel);
     Words codes(ring, l);
     int turn = F::kAhead;                  // steps up to the ring's end
-    float *const sums = reinterpret_cast<float *>(sb + F::kSumsAt);
     // sums of a shared tile: of the block's first one, or its other
     auto part_of = [&](int b, int which, int m) { return p.part + (int64_t)((b * 2 + which) * M + m) * (F::kRows * 128); };
+    __syncthreads();                       // (the cursors)
     bool ok = true;
-    int it = it0;
-    uint32_t meet = 0;                     // parity of the sums' meetings
+    int it = it0, tile = tile0, out = out0;
 #pragma unroll 1
-    for (int i = 0; i < n; it++) {
-        const int k0 = w0 + i - it * steps, c = min(steps - k0, n - i), end = i + c;
+    for (int i = 0; i < n; it++, next_outputs(tile, out)) {
         const bool own_first = i == 0;
-        const int4 tl = tile_of(it);
-        const int rows = tl.z, f0 = it % nf * 128, row_blocks = (rows + 7) / 8;
+        const int c = min(steps - (own_first ? step0 : 0), n - i), end = i + c;
+        const int4 tl = table[tile];
+        const int rows = tl.z, f0 = out * 128, row_blocks = (rows + 7) / 8;
         const float number = tid < 512 ? op.fetch(tid, tl.x, tl.y, rows, f0) : 0.0f;
         float acc[RB][4];
 #pragma unroll
@@ -310,17 +321,27 @@ __device__ __forceinline__ void run_share(const ExpertSteps &p, const Op &op, un
                 uint32_t before = 0;
                 if (lane == 0)
                     before = count_in(saddr(used + s), kExpertWarps / G);
-                if (__shfl_sync(0xffffffffu, before, 0) != 0u)
-                    issue(i + S);
+                if (__shfl_sync(0xffffffffu, before, 0) != 0u) {
+                    int4 at = cursor[group];
+                    issue(i + S, at.x, at.z);
+                    for (at.z += G; at.z >= steps; at.z -= steps)
+                        next_outputs(at.x, at.y);
+                    __syncwarp();
+                    if (lane == 0)
+                        cursor[group] = at;
+                }
             }
         }
         i = end;
         // the row that this warp finishes, from another set on at each tile
         const int row = (warp + it * 8) % kExpertWarps;
         // the sums meet in shared memory, once the rows of the tile before have been read
-        ok = ok && __all_sync(0xffffffffu, bar_wait(sums_read, meet ^ 1, &gave_up, count));
+        const int m_at = (it - it0) % B;
+        const uint32_t m_parity = (uint32_t)((it - it0) / B) & 1;
+        float *const sums = reinterpret_cast<float *>(sb + F::kSumsAt + m_at * F::kSums);
+        ok = ok && __all_sync(0xffffffffu, bar_wait(sums_read(m_at), m_parity ^ 1, &gave_up, count));
         if (tid < 512)
-            kept[tid] = number;
+            kept[m_at][tid] = number;
 #pragma unroll
         for (int b = 0; b < RB; b++)
 #pragma unroll
@@ -328,19 +349,19 @@ __device__ __forceinline__ void run_share(const ExpertSteps &p, const Op &op, un
                 sums[(set * F::kRows + sum_row(lane, b, j)) * kSumRow + sum_output<K, TR>(fw, lane, j)] = acc[b][j];
         __syncwarp();
         if (lane == 0)
-            bar_arrive(sums_full);
+            bar_arrive(sums_full(m_at));
         const float4 *const from = reinterpret_cast<const float4 *>(sums);
         if (c == steps) {
             // (a warp without a row goes on)
             if (row < rows) {
-                ok = ok && __all_sync(0xffffffffu, bar_wait(sums_full, meet, &gave_up, count));
+                ok = ok && __all_sync(0xffffffffu, bar_wait(sums_full(m_at), m_parity, &gave_up, count));
                 if (ok)
-                    op.finish(set_sum(from, 0, M, F::kRows, row, lane), TWO ? set_sum(from, 1, M, F::kRows, row, lane) : float4{}, kept,
+                    op.finish(set_sum(from, 0, M, F::kRows, row, lane), TWO ? set_sum(from, 1, M, F::kRows, row, lane) : float4{}, kept[m_at],
                               tl.y, row, f0, lane);
             }
         } else {
             // of a share of the inputs: to memory
-            ok = ok && __all_sync(0xffffffffu, bar_wait(sums_full, meet, &gave_up, count));
+            ok = ok && __all_sync(0xffffffffu, bar_wait(sums_full(m_at), m_parity, &gave_up, count));
             for (int q = warp; q < M * rows; q += kExpertWarps) {
                 const int m = q >= rows ? 1 : 0, r = q - m * rows;
                 __stcg(reinterpret_cast<float4 *>(part_of(block, own_first ? 0 : 1, m) + r * 128) + lane, set_sum(from, m, M, F::kRows, r, lane));
@@ -351,8 +372,7 @@ __device__ __forceinline__ void run_share(const ExpertSteps &p, const Op &op, un
         }
         __syncwarp();
         if (lane == 0)
-            bar_arrive(sums_read);
-        meet ^= 1;
+            bar_arrive(sums_read(m_at));
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
@@ -362,7 +382,7 @@ __device__ __forceinline__ void run_share(const ExpertSteps &p, const Op &op, un
         if (!last[which])
             continue;
         const int at = which ? it - 1 : it0, lo = at * steps, b_lo = shares.block_of(lo), b_hi = shares.block_of(lo + steps - 1);
-        const int4 tl = tile_of(at);
+        const int4 tl = table[at / nf - first];
         const int rows = tl.z, f0 = at % nf * 128;
         const float number = tid < 512 ? op.fetch(tid, tl.x, tl.y, rows, f0) : 0.0f;
         float4 v[M];
@@ -378,10 +398,10 @@ __device__ __forceinline__ void run_share(const ExpertSteps &p, const Op &op, un
         }
         __syncthreads();
         if (tid < 512)
-            kept[tid] = number;
+            kept[0][tid] = number;
         __syncthreads();
         if (warp < rows)
-            op.finish(v[0], v[M - 1], kept, tl.y, warp, f0, lane);
+            op.finish(v[0], v[M - 1], kept[0], tl.y, warp, f0, lane);
     }
     if (gave_up && tid == 0)               // nothing may be in flight when the block ends
         for (int i = 0; i < S; i++)

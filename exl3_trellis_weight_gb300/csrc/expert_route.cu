@@ -83,6 +83,8 @@ __device__ __forceinline__ uint32_t order_of(float v) {
     return (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
 
+__device__ __forceinline__ float value_of(uint32_t k) { return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k); }
+
 constexpr int kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32;
 
 // shared memory behind the counts: ids, valid flags and, one after the other, the warps' keys
@@ -99,8 +101,6 @@ template <bool ROUTE> __global__ void __launch_bounds__(kPlanThreads) plan_kerne
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     for (int i = tid; i < a.rows; i += kPlanThreads)
         a.pair_of[i] = -1;
-    for (int i = tid; i < T * (a.H / 128); i += kPlanThreads)
-        a.done[i] = 0;
     const int tiles = (int)expert_tiles(a.T, a.top_k, a.E, a.tile_n);
     for (int i = tid; i < tiles * (a.F / 128); i += kPlanThreads)
         a.up_done[i] = 0;
@@ -126,7 +126,8 @@ template <bool ROUTE> __global__ void __launch_bounds__(kPlanThreads) plan_kerne
                 for (int d = 16; d; d >>= 1)
                     sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, d));
             }
-            int id = 0;                    // the lane's pick
+            int id = 0;                    // the lane's pick, and its logit
+            float logit = 0.0f;
             // the largest of a lane's own experts, found again only where one of them is picked
             uint32_t best = 0;
             int at = a.E;
@@ -146,11 +147,13 @@ template <bool ROUTE> __global__ void __launch_bounds__(kPlanThreads) plan_kerne
                     keys[pick] = 0;
                     own();
                 }
-                if (lane == j)
+                if (lane == j) {
                     id = pick;
+                    logit = value_of(most);
+                }
                 __syncwarp();
             }
-            const float p = lane < a.top_k ? expf(__fsub_rn(__ldcg(logits + id), top)) : 0.0f;
+            const float p = lane < a.top_k ? expf(__fsub_rn(logit, top)) : 0.0f;
             if (a.normalize) {
                 sum = p;
 #pragma unroll
@@ -191,16 +194,6 @@ template <bool ROUTE> __global__ void __launch_bounds__(kPlanThreads) plan_kerne
             if (e >= 0 && (same >> lane) == 1u)                                 // the last of them
                 mine[e] = (uint16_t)(place[i] + 1);
             __syncwarp();
-        }
-    }
-    for (int t = warp; t < T; t += kPlanWarps) {
-        const int v = __popc(__ballot_sync(0xffffffffu, lane < a.top_k && ids[t * a.top_k + min(lane, a.top_k - 1)] >= 0));
-        if (lane == 0)
-            a.valid[t] = v;
-        if (v == 0) {                      // no expert: the result is 0
-            uint16_t *y = reinterpret_cast<uint16_t *>(a.y) + (int64_t)t * a.y_stride;
-            for (int c = lane; c < a.H; c += 32)
-                y[c] = 0;
         }
     }
     __syncthreads();

@@ -105,8 +105,6 @@ struct ExpertLaunch {
     int32_t *pair_of;          // [rows]: a row's pair, or -1
     int4 *tiles;               // expert, first row and rows of each tile
     int32_t *n_tiles;
-    int32_t *done;             // [T][H / 128]: pairs of a token that are finished
-    int32_t *valid;            // [T]: pairs of a token that have an expert
     unsigned char *image[2];   // rotated activations of the rows for gate and up (act_rows(rows) x H), parts behind each other
     float *rscale[2];          // [rows]
     unsigned char *inner;      // rotated silu(.) . (.) of the rows (act_rows(rows) x F), parts behind each other
@@ -133,7 +131,9 @@ __host__ __device__ inline int64_t expert_tiles(int64_t T, int top_k, int E, int
 // is shared, so that costs a tenth of the time.
 template <typename T> constexpr bool kTwoParts = false;
 template <> constexpr bool kTwoParts<__half> = true;
-inline int expert_tile_n(int64_t T, bool two_parts) { return T <= 8 ? 8 : T <= 16 || two_parts ? 16 : 32; }
+inline int expert_tile_n(int64_t T, int top_k, int E, bool two_parts) {
+    return T <= 8 || T * top_k <= 4 * (int64_t)E ? 8 : T <= 16 || two_parts || T * top_k <= 10 * (int64_t)E ? 16 : 32;
+}
 inline int64_t expert_blocks() { return device_sm_count(); }
 exl3_status launch_expert_route(const ExpertLaunch &p, cudaStream_t s);
 exl3_status launch_expert_up(const ExpertLaunch &p, cudaStream_t s);

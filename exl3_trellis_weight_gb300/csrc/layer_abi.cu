@@ -83,7 +83,7 @@ size_t carve_layer(ExpertLaunch &p, void *ws) {
     }
     p.pair_of = c.take<int32_t>((size_t)p.rows);
     // (the size is the same for both types of x)
-    const int least = expert_tile_n(p.T, true), most = expert_tile_n(p.T, false);
+    const int least = expert_tile_n(p.T, p.top_k, p.E, true), most = expert_tile_n(p.T, p.top_k, p.E, false);
     p.tile_n = p.dt == EXL3_F16 ? least : most;
     const size_t tiles = (size_t)expert_tiles(p.T, p.top_k, p.E, least);
     p.tiles = c.take<int4>(tiles);
@@ -91,8 +91,6 @@ size_t carve_layer(ExpertLaunch &p, void *ws) {
     p.down_done = c.take<int32_t>(tiles * (p.H / 128));
     p.sums = c.take<float>((size_t)expert_blocks() * 4 * most * 128);
     p.n_tiles = c.take<int32_t>(1);
-    p.done = c.take<int32_t>((size_t)(p.T * (p.H / 128)));
-    p.valid = c.take<int32_t>((size_t)p.T);
     for (int w = 0; w < 2; w++) {
         p.image[w] = c.take<unsigned char>((size_t)act_rows(p.rows) * p.H * 4);
         p.rscale[w] = c.take<float>((size_t)p.rows);
