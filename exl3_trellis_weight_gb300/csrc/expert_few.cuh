@@ -152,7 +152,7 @@ __device__ __forceinline__ void run_share(const ExpertSteps &p, const Op &op, un
     __shared__ __align__(8) unsigned long long bars[S + 2 * B];
     __shared__ uint32_t used[S], filled[S];                    // warps that are done with a stage; times it was asked for
     __shared__ int4 table[kTable];
-    __shared__ __align__(16) float kept[B][512];
+    __shared__ __align__(16) float kept[2][512];
     __shared__ int gave_up;
     __shared__ int4 cursor[G];             // of a group: tile, outputs and step that follow in a stage it is done with
     __shared__ int last[2];                // whether this block joins its first, its other shared tile
@@ -376,32 +376,36 @@ __device__ __forceinline__ void run_share(const ExpertSteps &p, const Op &op, un
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
-    // whose last share came from here, is added up: a row to a warp
+    // whose last share came from here, is added up: a row to a warp, both tiles at once where
+    // they have rows for half the warps at most
+    constexpr int kAtOnce = F::kRows <= kExpertWarps / 2 ? 2 : 1;
 #pragma unroll 1
-    for (int which = 0; which < 2; which++) {
-        if (!last[which])
+    for (int turn = 0; turn < 2; turn += kAtOnce) {
+        if (!last[turn] && !last[turn + kAtOnce - 1])
             continue;
+        const int which = kAtOnce == 2 ? warp / (kExpertWarps / 2) : turn, row = kAtOnce == 2 ? warp % (kExpertWarps / 2) : warp;
+        const int t = kAtOnce == 2 ? tid & 511 : tid;
         const int at = which ? it - 1 : it0, lo = at * steps, b_lo = shares.block_of(lo), b_hi = shares.block_of(lo + steps - 1);
         const int4 tl = table[at / nf - first];
-        const int rows = tl.z, f0 = at % nf * 128;
-        const float number = tid < 512 ? op.fetch(tid, tl.x, tl.y, rows, f0) : 0.0f;
+        const int rows = last[which] ? tl.z : 0, f0 = at % nf * 128;
+        const float number = t < 512 && rows ? op.fetch(t, tl.x, tl.y, rows, f0) : 0.0f;
         float4 v[M];
 #pragma unroll
         for (int m = 0; m < M; m++)
             v[m] = float4{};
-        if (warp < rows) {
+        if (row < rows) {
 #pragma unroll 4
             for (int b = b_lo; b <= b_hi; b++)
 #pragma unroll
                 for (int m = 0; m < M; m++)
-                    v[m] = add4(v[m], __ldcg(reinterpret_cast<const float4 *>(part_of(b, shares.first(b) >= lo ? 0 : 1, m) + warp * 128) + lane));
+                    v[m] = add4(v[m], __ldcg(reinterpret_cast<const float4 *>(part_of(b, shares.first(b) >= lo ? 0 : 1, m) + row * 128) + lane));
         }
         __syncthreads();
-        if (tid < 512)
-            kept[0][tid] = number;
+        if (t < 512)
+            kept[which][t] = number;
         __syncthreads();
-        if (warp < rows)
-            op.finish(v[0], v[M - 1], kept[0], tl.y, warp, f0, lane);
+        if (row < rows)
+            op.finish(v[0], v[M - 1], kept[which], tl.y, row, f0, lane);
     }
     if (gave_up && tid == 0)               // nothing may be in flight when the block ends
         for (int i = 0; i < S; i++)

@@ -77,10 +77,10 @@ template <typename T, bool VEC> __global__ void __launch_bounds__(kLogitWarps * 
 }
 
 // ---- picks and the plan: one block ------------------------------------------------------
-// a float's bits, ordered as unsigned; any picks are valid experts, whatever the logits are
+// a float's bits, ordered as unsigned, 1 at least; any picks are valid experts, whatever the logits are
 __device__ __forceinline__ uint32_t order_of(float v) {
     const uint32_t b = __float_as_uint(v);
-    return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+    return max((b & 0x80000000u) ? ~b : b | 0x80000000u, 1u);
 }
 
 __device__ __forceinline__ float value_of(uint32_t k) { return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k); }
@@ -90,6 +90,70 @@ constexpr int kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32;
 // shared memory behind the counts: ids, valid flags and, one after the other, the warps' keys
 // of the experts and their counts of them
 __host__ __device__ inline size_t plan_bytes(int64_t n, int E) { return (size_t)n * 4 + (size_t)kPlanWarps * E * 4; }
+
+// The picks of a token, by a warp: the largest keys, of equals the lowest expert; lane j has
+// the j-th and its key.  No key is 0 but one that has been picked.  Up to 32 R experts stay in
+// registers (in shared memory each pick took 380 cycles; counting for each expert how many
+// stand before it took longer still).
+struct Pick {
+    int e;
+    uint32_t key;
+};
+__device__ __forceinline__ int pick_of(uint32_t best, int at, uint32_t &most) {
+    most = __reduce_max_sync(0xffffffffu, best);
+    const uint32_t who = __ballot_sync(0xffffffffu, best == most);
+    if (__popc(who) == 1)
+        return __shfl_sync(0xffffffffu, at, __ffs(who) - 1);
+    return (int)__reduce_min_sync(0xffffffffu, best == most ? (uint32_t)at : 0xFFFFu);
+}
+template <int R> __device__ __forceinline__ Pick picks_few(const uint32_t *keys, int E, int top_k, int lane) {
+    uint32_t k[R];
+#pragma unroll
+    for (int i = 0; i < R; i++)
+        k[i] = lane + 32 * i < E ? keys[lane + 32 * i] : 0u;
+    Pick p = {0, 0u};
+    for (int j = 0; j < top_k; j++) {
+        uint32_t best = k[0], most;
+        int at = lane;
+#pragma unroll
+        for (int i = 1; i < R; i++)
+            if (k[i] > best)
+                best = k[i], at = lane + 32 * i;
+        const int e = pick_of(best, at, most);
+#pragma unroll
+        for (int i = 0; i < R; i++)
+            if (e == lane + 32 * i)
+                k[i] = 0u;
+        if (lane == j)
+            p = {e, most};
+    }
+    return p;
+}
+__device__ __forceinline__ Pick picks_many(uint32_t *keys, int E, int top_k, int lane) {
+    Pick p = {0, 0u};
+    uint32_t best = 0, most;
+    int at = 0;
+    auto own = [&]() {                     // (found again only where one of the lane's is picked)
+        best = 0;
+        for (int e = lane; e < E; e += 32) {
+            const uint32_t k = keys[e];
+            if (k > best)
+                best = k, at = e;
+        }
+    };
+    own();
+    for (int j = 0; j < top_k; j++) {
+        const int e = pick_of(best, at, most);
+        if (lane == (e & 31)) {
+            keys[e] = 0;
+            own();
+        }
+        if (lane == j)
+            p = {e, most};
+        __syncwarp();
+    }
+    return p;
+}
 
 template <bool ROUTE> __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const ExpertLaunch a) {
     __shared__ int32_t count[kMaxExperts], first[kMaxExperts];
@@ -126,34 +190,10 @@ template <bool ROUTE> __global__ void __launch_bounds__(kPlanThreads) plan_kerne
                 for (int d = 16; d; d >>= 1)
                     sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, d));
             }
-            int id = 0;                    // the lane's pick, and its logit
-            float logit = 0.0f;
-            // the largest of a lane's own experts, found again only where one of them is picked
-            uint32_t best = 0;
-            int at = a.E;
-            auto own = [&]() {
-                best = 0, at = a.E;
-                for (int e = lane; e < a.E; e += 32) {
-                    const uint32_t k = keys[e];
-                    if (k > best || at == a.E)
-                        best = k, at = e;
-                }
-            };
-            own();
-            for (int j = 0; j < a.top_k; j++) {
-                const uint32_t most = __reduce_max_sync(0xffffffffu, best);
-                const int pick = (int)__reduce_min_sync(0xffffffffu, at < a.E && best == most ? (uint32_t)at : 0xFFFFu);
-                if (lane == (pick & 31)) {
-                    keys[pick] = 0;
-                    own();
-                }
-                if (lane == j) {
-                    id = pick;
-                    logit = value_of(most);
-                }
-                __syncwarp();
-            }
-            const float p = lane < a.top_k ? expf(__fsub_rn(logit, top)) : 0.0f;
+            // (a lane reads back keys that it wrote itself)
+            const Pick pick = a.E <= 64 ? picks_few<2>(keys, a.E, a.top_k, lane) : picks_many(keys, a.E, a.top_k, lane);
+            const int id = pick.e;
+            const float p = lane < a.top_k ? expf(__fsub_rn(value_of(pick.key), top)) : 0.0f;
             if (a.normalize) {
                 sum = p;
 #pragma unroll
