@@ -14,7 +14,10 @@
 // is used as it lies, the operand's rows run along its inputs or along its outputs.
 //
 // Warps: accumulators to registers (four for each half of the columns), one that copies
-// tiles, one that issues the matrix instructions.
+// tiles, one that issues the matrix instructions, one that multiplies the scales of steps
+// ahead.  (When the warps with the accumulators fetched the scales themselves, a step ahead, and
+// each thread stored its row, 4096 tokens x 4096 x 12288 took 236 us: 41 of it waiting for
+// scales and 55 storing.)
 #include "layer.cuh"
 #include "linear_rotate.cuh"
 #include "tc.cuh"
@@ -33,7 +36,7 @@ struct Args8 {
     int64_t xs_t, xs_b;
     const float *ws;
     int ws_o, ws_k;          // steps between the scales of neighbouring outputs and inputs
-    int64_t T;
+    int T;
     int n_out, blocks_k;     // outputs, blocks of 128 inputs
     int split;               // blocks of a cluster
     int tiles_t, tiles_f;    // tiles along tokens and outputs
@@ -46,8 +49,8 @@ struct Args8 {
 // TN: columns of a tile (tokens with SWAP, else outputs); MN: W's rows run along its outputs
 template <int TN, bool SWAP, bool MN> struct Form {
     static constexpr int kHalves = TN == 16 ? 1 : 2, kCols = TN / kHalves;     // columns of a result warp
-    static constexpr int kOutWarps = 4 * kHalves, kThreads8 = (kOutWarps + 2) * 32;
-    static constexpr int kCopy = kOutWarps, kIssue = kOutWarps + 1;            // warps
+    static constexpr int kOutWarps = 4 * kHalves, kThreads8 = (kOutWarps + 3) * 32;
+    static constexpr int kCopy = kOutWarps, kIssue = kOutWarps + 1, kFactor = kOutWarps + 2;   // warps
     // results of a step in tensor memory: kAcc of them; what a block takes of it goes with
     // what it takes of shared memory (128 columns with more than a quarter, 512 with all but
     // 56 KB), so that blocks that fit an SM together never wait for each other's
@@ -55,9 +58,13 @@ template <int TN, bool SWAP, bool MN> struct Form {
     static constexpr uint32_t kA = 16384, kB = TN * 128, kStage = kA + kB;
     static constexpr int kStages = SWAP ? 4 : TN == 128 ? 6 : 4;
     static constexpr uint32_t kSums = TN * 512;                                // split: the block's sums
-    static constexpr uint32_t kSmem = kStages * kStage + 1024;
+    // factors of kFac steps, a product of scales for each token (SWAP) or token and 128 outputs;
+    // a place of 32 tokens x 32 outputs for each result warp on their way out
+    static constexpr int kFac = 8;
+    static constexpr uint32_t kFacAt = kStages * kStage, kOutAt = kFacAt + kFac * TN * 4;
+    static constexpr uint32_t kSmem = kOutAt + (SWAP ? 0u : kOutWarps * 2048u) + 1024;
     static_assert(kSums <= kStages * kStage, "sums in the place of the stages");
-    static_assert(SWAP ? kSmem > 57 * 1024 : kSmem > 171 * 1024, "shared memory keeps tensor memory apart");
+    static_assert(SWAP ? kSmem > 57 * 1024 && kSmem < 113 * 1024 : kSmem > 171 * 1024, "shared memory keeps tensor memory apart");
 };
 
 template <int COLS> __device__ __forceinline__ void tmem_alloc(uint32_t dst) {
@@ -123,8 +130,7 @@ __global__ void __launch_bounds__(Form<TN, SWAP, MN>::kThreads8, SWAP ? 2 : 1)
     linear8_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ Args8 a) {
     using F = Form<TN, SWAP, MN>;
     extern __shared__ unsigned char smem_raw[];
-    __shared__ __align__(8) unsigned long long bars[2 * F::kStages + 2 * F::kAcc + 1];
-    __shared__ __align__(16) float factors[SWAP ? F::kOutWarps : 1][2][SWAP ? F::kCols : 4];
+    __shared__ __align__(8) unsigned long long bars[2 * F::kStages + 2 * F::kAcc + 2 * F::kFac + 1];
     __shared__ uint32_t tmem_at;
     __shared__ int gave_up;
     const uint32_t base = (saddr(smem_raw) + 1023u) & ~1023u;
@@ -133,7 +139,11 @@ __global__ void __launch_bounds__(Form<TN, SWAP, MN>::kThreads8, SWAP ? 2 : 1)
     auto empty = [&](uint32_t s) { return bar0 + 8u * (F::kStages + s); };
     auto acc_full = [&](uint32_t d) { return bar0 + 8u * (2 * F::kStages + d); };
     auto acc_empty = [&](uint32_t d) { return bar0 + 8u * (2 * F::kStages + F::kAcc + d); };
-    const uint32_t drained = bar0 + 8u * (2 * F::kStages + 2 * F::kAcc);
+    auto fac_full = [&](uint32_t d) { return bar0 + 8u * (2 * F::kStages + 2 * F::kAcc + d); };
+    auto fac_empty = [&](uint32_t d) { return bar0 + 8u * (2 * F::kStages + 2 * F::kAcc + F::kFac + d); };
+    const uint32_t drained = bar0 + 8u * (2 * F::kStages + 2 * F::kAcc + 2 * F::kFac);
+    unsigned char *const sb = smem_raw + (base - saddr(smem_raw));
+    float *const factors = reinterpret_cast<float *>(sb + F::kFacAt);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int rank = a.split > 1 ? (int)(blockIdx.x % a.split) : 0;
     unsigned int *const count = &g_linear8_timeouts;
@@ -146,6 +156,10 @@ __global__ void __launch_bounds__(Form<TN, SWAP, MN>::kThreads8, SWAP ? 2 : 1)
         for (int d = 0; d < F::kAcc; d++) {
             bar_init(acc_full(d), 1);
             bar_init(acc_empty(d), F::kOutWarps);
+        }
+        for (int d = 0; d < F::kFac; d++) {
+            bar_init(fac_full(d), 1);
+            bar_init(fac_empty(d), F::kOutWarps);
         }
         bar_init(drained, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -160,20 +174,20 @@ __global__ void __launch_bounds__(Form<TN, SWAP, MN>::kThreads8, SWAP ? 2 : 1)
 
     // tiles of this block, and its share of the inputs; a tile's number counts tokens first,
     // so that blocks running side by side share their weights
-    const int64_t tiles = (int64_t)a.tiles_t * a.tiles_f;
-    const int64_t it0 = blockIdx.x / a.split, dit = a.split > 1 ? tiles : gridDim.x;
-    const int k_lo = (int)((int64_t)a.blocks_k * rank / a.split), k_hi = (int)((int64_t)a.blocks_k * (rank + 1) / a.split);
+    const int tiles = a.tiles_t * a.tiles_f;
+    const int it0 = (int)blockIdx.x / a.split, dit = a.split > 1 ? tiles : (int)gridDim.x;
+    const int k_lo = a.blocks_k * rank / a.split, k_hi = a.blocks_k * (rank + 1) / a.split;
     const int steps = k_hi - k_lo;
     constexpr int kRowsT = SWAP ? TN : 128, kRowsF = SWAP ? 128 : TN;          // tokens and outputs of a tile
-    auto t_of = [&](int64_t it) { return (it % a.tiles_t) * kRowsT; };
-    auto f_of = [&](int64_t it) { return (int)(it / a.tiles_t) * kRowsF; };
+    auto t_of = [&](int it) { return it % a.tiles_t * kRowsT; };     // (2^24 tokens at most)
+    auto f_of = [&](int it) { return it / a.tiles_t * kRowsF; };
     uint32_t issued = 0;                   // stages filled (of the thread that copies)
 
     if (warp == F::kCopy) {
         // ---- tiles of both operands, a stage for each 128 inputs ----
         if (elect()) {
-            auto load_x = [&](uint32_t s, int64_t t0, int k) {
-                tile_load(base + s * F::kStage + (SWAP ? F::kA : 0u), &xmap, k * 128, (int)t0, full(s));
+            auto load_x = [&](uint32_t s, int t0, int k) {
+                tile_load(base + s * F::kStage + (SWAP ? F::kA : 0u), &xmap, k * 128, t0, full(s));
             };
             auto load_w = [&](uint32_t s, int f0, int k) {
                 const uint32_t to = base + s * F::kStage + (SWAP ? 0u : F::kA);
@@ -196,8 +210,8 @@ __global__ void __launch_bounds__(Form<TN, SWAP, MN>::kThreads8, SWAP ? 2 : 1)
             asm volatile("griddepcontrol.wait;" ::: "memory");
             uint32_t s = 0, phase = 1;     // (the phase before the first is over)
             bool ok = true;
-            for (int64_t it = it0; ok && it < tiles; it += dit) {
-                const int64_t t0 = t_of(it);
+            for (int it = it0; ok && it < tiles; it += dit) {
+                const int t0 = t_of(it);
                 const int f0 = f_of(it);
                 for (int k = k_lo; k < k_hi; k++) {
                     if (!bar_wait(empty(s), phase, &gave_up, count)) {
@@ -230,7 +244,7 @@ __global__ void __launch_bounds__(Form<TN, SWAP, MN>::kThreads8, SWAP ? 2 : 1)
             // 32 inputs on: 32 bytes of a row along K, or 32 rows
             constexpr uint32_t kHopA = (SWAP && MN ? 4096u : 32u) >> 4, kHopB = (!SWAP && MN ? 4096u : 32u) >> 4;
             uint32_t s = 0, s_phase = 0, d = 0, d_phase = 1;
-            for (int64_t it = it0; it < tiles && !gave_up; it += dit) {
+            for (int it = it0; it < tiles && !gave_up; it += dit) {
                 for (int k = 0; k < steps; k++) {
                     if (!bar_wait(acc_empty(d), d_phase, &gave_up, count) || !bar_wait(full(s), s_phase, &gave_up, count))
                         break;
@@ -253,44 +267,80 @@ __global__ void __launch_bounds__(Form<TN, SWAP, MN>::kThreads8, SWAP ? 2 : 1)
                 bar_drain(drained, 0);
             }
         }
+    } else if (warp == F::kFactor) {
+        // ---- products of the scales: four steps on their way while four are written ----
+        constexpr int kEach = SWAP ? (TN + 31) / 32 : 4, kBlocks = SWAP ? 1 : TN / 128, kTogether = 4;
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        uint32_t s = 0, phase = 1;
+        bool ok = true;
+        for (int it = it0; ok && it < tiles; it += dit) {
+            const int t0 = t_of(it) + lane, f0 = f_of(it);
+            float x[kTogether][kEach], w[kTogether][kBlocks];
+            auto ask = [&](int k0) {
+#pragma unroll
+                for (int j = 0; j < kTogether; j++) {
+#pragma unroll
+                    for (int i = 0; i < kEach; i++)
+                        x[j][i] = k0 + j < steps && t0 + 32 * i < a.T && lane < TN
+                                      ? __ldcg(a.xs + (int64_t)(t0 + 32 * i) * a.xs_t + (k_lo + k0 + j) * a.xs_b) : 0.0f;
+#pragma unroll
+                    for (int b = 0; b < kBlocks; b++)
+                        w[j][b] = k0 + j < steps ? __ldg(a.ws + (int64_t)(min(f0 + 128 * b, a.n_out - 1) >> 7) * a.ws_o +
+                                                         (int64_t)(k_lo + k0 + j) * a.ws_k) : 0.0f;
+                }
+            };
+            ask(0);
+            for (int k0 = 0; ok && k0 < steps; k0 += kTogether) {
+                float f[kTogether][kBlocks][kEach];
+#pragma unroll
+                for (int j = 0; j < kTogether; j++)
+#pragma unroll
+                    for (int b = 0; b < kBlocks; b++)
+#pragma unroll
+                        for (int i = 0; i < kEach; i++)
+                            f[j][b][i] = __fmul_rn(x[j][i], w[j][b]);
+                ask(k0 + kTogether);
+#pragma unroll
+                for (int j = 0; j < kTogether; j++) {
+                    if (!ok || k0 + j >= steps)
+                        break;
+                    ok = __all_sync(0xffffffffu, bar_wait(fac_empty(s), phase, &gave_up, count));
+#pragma unroll
+                    for (int b = 0; b < kBlocks; b++)
+#pragma unroll
+                        for (int i = 0; i < kEach; i++)
+                            if (lane < TN)
+                                factors[s * TN + b * 128 + 32 * i + lane] = f[j][b][i];
+                    __syncwarp();
+                    if (lane == 0)
+                        bar_arrive(fac_full(s));
+                    if (++s == F::kFac)
+                        s = 0, phase ^= 1;
+                }
+            }
+        }
     } else {
         // ---- results ----
         const int quarter = warp & 3, half = warp >> 2;
         const int row = quarter * 32 + lane;             // of the tile: an output (SWAP) or a token
+        const float *const mine = factors + (SWAP ? half * F::kCols : half * F::kCols / 128 * 128 + row);
         asm volatile("griddepcontrol.wait;" ::: "memory");
-        uint32_t d = 0, d_phase = 0;
+        uint32_t d = 0, d_phase = 0, s = 0, s_phase = 0;
         bool ok = true;
-        for (int64_t it = it0; ok && it < tiles; it += dit) {
-            const int64_t t0 = t_of(it);
+        for (int it = it0; ok && it < tiles; it += dit) {
+            const int t0 = t_of(it);
             const int f0 = f_of(it);
-            // the factors of a step: of the thread's token, or of a column a lane
-            const int64_t t_mine = SWAP ? t0 + half * F::kCols + (lane % F::kCols) : t0 + row;
-            const bool have = t_mine < a.T;
-            const float *xs = a.xs + (have ? t_mine : 0) * a.xs_t + k_lo * a.xs_b;
-            const int fb = min(f0 + (SWAP ? 0 : half * F::kCols), a.n_out - 1) >> 7;
-            const float *ws = a.ws + (int64_t)fb * a.ws_o + (int64_t)k_lo * a.ws_k;
             float acc[F::kCols];
 #pragma unroll
             for (int c = 0; c < F::kCols; c++)
                 acc[c] = 0.0f;
-            auto factor = [&](int k) {
-                return have && k < steps ? __fmul_rn(__ldcg(xs + k * a.xs_b), __ldg(ws + (int64_t)k * a.ws_k)) : 0.0f;
-            };
-            float f_next = factor(0);
             for (int k = 0; k < steps; k++) {
-                const float f = f_next;
-                f_next = factor(k + 1);
-                if (SWAP) {
-                    // (two places in turn: a step's reads are done before the barrier of the next)
-                    if (lane < F::kCols)
-                        factors[SWAP ? warp : 0][k & 1][lane] = f;
-                    __syncwarp();
-                }
-                ok = __all_sync(0xffffffffu, bar_wait(acc_full(d), d_phase, &gave_up, count));
+                ok = __all_sync(0xffffffffu, bar_wait(fac_full(s), s_phase, &gave_up, count) && bar_wait(acc_full(d), d_phase, &gave_up, count));
                 if (!ok)
                     break;
                 fence_after();
                 const uint32_t from = tmem + (uint32_t)(quarter * 32) * 65536u + d * TN + half * F::kCols;
+                const float f = SWAP ? 0.0f : mine[s * TN];
                 uint32_t r[2][16];
                 tmem_ask16(from, r[0]);
 #pragma unroll
@@ -303,23 +353,27 @@ __global__ void __launch_bounds__(Form<TN, SWAP, MN>::kThreads8, SWAP ? 2 : 1)
                     for (int i = 0; i < 16; i += 4) {
                         float4 g = make_float4(f, f, f, f);
                         if (SWAP)
-                            g = *reinterpret_cast<const float4 *>(&factors[SWAP ? warp : 0][k & 1][SWAP ? c + i : 0]);
+                            g = *reinterpret_cast<const float4 *>(mine + s * TN + c + i);
                         add_scaled(acc[c + i], acc[c + i + 1], g.x, g.y, now[i], now[i + 1]);
                         add_scaled(acc[c + i + 2], acc[c + i + 3], g.z, g.w, now[i + 2], now[i + 3]);
                     }
                 }
                 fence_before();
                 __syncwarp();
-                if (lane == 0)
+                if (lane == 0) {
                     bar_arrive(acc_empty(d));
+                    bar_arrive(fac_empty(s));
+                }
                 if (++d == F::kAcc)
                     d = 0, d_phase ^= 1;
+                if (++s == F::kFac)
+                    s = 0, s_phase ^= 1;
             }
             if (!ok)
                 break;
             if (a.split > 1) {
                 // every step's operands have been used: their place takes the sums, by column
-                float *const sums = reinterpret_cast<float *>(smem_raw + (base - saddr(smem_raw)));
+                float *const sums = reinterpret_cast<float *>(sb);
 #pragma unroll
                 for (int c = 0; c < F::kCols; c++)
                     sums[(half * F::kCols + c) * 128 + row] = acc[c];
@@ -327,29 +381,42 @@ __global__ void __launch_bounds__(Form<TN, SWAP, MN>::kThreads8, SWAP ? 2 : 1)
                 const int f = f0 + row;
 #pragma unroll
                 for (int c = 0; c < F::kCols; c++) {
-                    const int64_t t = t0 + half * F::kCols + c;
+                    const int t = t0 + half * F::kCols + c;
                     if (f < a.n_out && t < a.T)
-                        reinterpret_cast<uint16_t *>(a.y)[t * a.y_stride + f] = (uint16_t)pack_dt(a.dt, acc[c], 0.0f);
+                        reinterpret_cast<uint16_t *>(a.y)[(int64_t)t * a.y_stride + f] = (uint16_t)pack_dt(a.dt, acc[c], 0.0f);
                 }
-            } else if (have) {
-                uint16_t *y = reinterpret_cast<uint16_t *>(a.y) + t_mine * a.y_stride;
+            } else {
+                // 32 outputs of the warp's 32 tokens at a time, through shared memory: eight of a
+                // token are 16 bytes, and a token's four such stand turned by its number
+                uint4 *const place = reinterpret_cast<uint4 *>(sb + F::kOutAt) + warp * 128;
                 const bool wide = (((uintptr_t)a.y | (uintptr_t)(a.y_stride * 2)) & 15u) == 0;
 #pragma unroll
-                for (int c = 0; c < F::kCols; c += 8) {
-                    const int f = f0 + half * F::kCols + c;
-                    if (f < a.n_out) {     // (a multiple of 16)
-                        uint32_t q[4];
+                for (int c = 0; c < F::kCols; c += 32) {
 #pragma unroll
-                        for (int i = 0; i < 4; i++)
-                            q[i] = pack_dt(a.dt, acc[c + 2 * i], acc[c + 2 * i + 1]);
-                        if (wide) {
-                            *reinterpret_cast<uint4 *>(y + f) = make_uint4(q[0], q[1], q[2], q[3]);
-                        } else {
+                    for (int u = 0; u < 4; u++) {
+                        const float *v = acc + c + 8 * u;
+                        place[lane * 4 + (u ^ ((lane >> 1) & 3))] =
+                            make_uint4(pack_dt(a.dt, v[0], v[1]), pack_dt(a.dt, v[2], v[3]), pack_dt(a.dt, v[4], v[5]), pack_dt(a.dt, v[6], v[7]));
+                    }
+                    __syncwarp();
+                    const int f = f0 + half * F::kCols + c + (lane & 3) * 8;
 #pragma unroll
-                            for (int i = 0; i < 8; i++)
-                                y[f + i] = (uint16_t)(q[i >> 1] >> (16 * (i & 1)));
+                    for (int j = 0; j < 4; j++) {
+                        const int r = (lane >> 2) + 8 * j, t = t0 + quarter * 32 + r;
+                        const uint4 q = place[r * 4 + ((lane & 3) ^ ((r >> 1) & 3))];
+                        if (t < a.T && f < a.n_out) {    // (a multiple of 16)
+                            uint16_t *y = reinterpret_cast<uint16_t *>(a.y) + (int64_t)t * a.y_stride + f;
+                            if (wide) {
+                                *reinterpret_cast<uint4 *>(y) = q;
+                            } else {
+                                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                                for (int i = 0; i < 8; i++)
+                                    y[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+                            }
                         }
                     }
+                    __syncwarp();
                 }
             }
         }
@@ -359,7 +426,7 @@ __global__ void __launch_bounds__(Form<TN, SWAP, MN>::kThreads8, SWAP ? 2 : 1)
     if (a.split > 1) {
         // the blocks' sums, added in block order: groups of 8 columns, 32 rows a warp
         cluster_sync();
-        const int64_t t0 = t_of(it0);
+        const int t0 = t_of(it0);
         const int f0 = f_of(it0);
         const bool wide = (((uintptr_t)a.y | (uintptr_t)(a.y_stride * 2)) & 15u) == 0;
         constexpr int kWarps8 = F::kThreads8 / 32;
@@ -376,7 +443,7 @@ __global__ void __launch_bounds__(Form<TN, SWAP, MN>::kThreads8, SWAP ? 2 : 1)
                 }
                 const int f = f0 + lane * 4;
                 if (f < a.n_out) {
-                    uint16_t *y = reinterpret_cast<uint16_t *>(a.y) + (t0 + c) * a.y_stride + f;
+                    uint16_t *y = reinterpret_cast<uint16_t *>(a.y) + (int64_t)(t0 + c) * a.y_stride + f;
                     const uint32_t q[2] = {pack_dt(a.dt, v.x, v.y), pack_dt(a.dt, v.z, v.w)};
                     if (wide) {
                         *reinterpret_cast<uint2 *>(y) = make_uint2(q[0], q[1]);
@@ -391,7 +458,7 @@ __global__ void __launch_bounds__(Form<TN, SWAP, MN>::kThreads8, SWAP ? 2 : 1)
             // a column is an output: a lane takes eight of its token
             for (int u = rank + warp * a.split; u < TN / 8 * 4; u += kWarps8 * a.split) {
                 const int c = u >> 2 << 3, row = (u & 3) * 32 + lane;
-                const int64_t t = t0 + row;
+                const int t = t0 + row;
                 const int f = f0 + c;
                 if (t0 + (u & 3) * 32 >= a.T || f >= a.n_out)
                     continue;
@@ -409,7 +476,7 @@ __global__ void __launch_bounds__(Form<TN, SWAP, MN>::kThreads8, SWAP ? 2 : 1)
                     }
                 }
                 if (t < a.T) {
-                    uint16_t *y = reinterpret_cast<uint16_t *>(a.y) + t * a.y_stride + f;
+                    uint16_t *y = reinterpret_cast<uint16_t *>(a.y) + (int64_t)t * a.y_stride + f;
                     uint32_t q[4];
 #pragma unroll
                     for (int i = 0; i < 4; i++)
@@ -452,7 +519,7 @@ template <int TN, bool SWAP, bool MN> exl3_status launch_form8(const Linear8Laun
     using F = Form<TN, SWAP, MN>;
     constexpr int kRowsT = SWAP ? TN : 128, kRowsF = SWAP ? 128 : TN;
     const int64_t sms = device_sm_count();
-    a.tiles_t = (int)((a.T + kRowsT - 1) / kRowsT);
+    a.tiles_t = (a.T + kRowsT - 1) / kRowsT;
     a.tiles_f = (a.n_out + kRowsF - 1) / kRowsF;
     const int64_t tiles = (int64_t)a.tiles_t * a.tiles_f, slots = SWAP ? 2 * sms : sms;
     // blocks that would idle share the inputs of the tiles, two steps each at least
@@ -494,7 +561,7 @@ template <bool MN> exl3_status launch_mn(const Linear8Launch &p, Args8 &a, cudaS
         return launch_form8<32, true, MN>(p, a, s);
     if (a.T <= 64)
         return launch_form8<64, true, MN>(p, a, s);
-    const int64_t tiles = (a.T + 127) / 128 * ((a.n_out + 255) / 256);
+    const int64_t tiles = (int64_t)((a.T + 127) / 128) * ((a.n_out + 255) / 256);
     return tiles >= device_sm_count() ? launch_form8<256, false, MN>(p, a, s) : launch_form8<128, false, MN>(p, a, s);
 }
 
@@ -510,7 +577,7 @@ exl3_status launch_linear8(const Linear8Launch &p, cudaStream_t s) {
     a.ws = p.ws;
     a.ws_o = p.transposed ? blocks_c : 1;
     a.ws_k = p.transposed ? 1 : blocks_c;
-    a.T = p.T;
+    a.T = (int)p.T;
     a.n_out = (int)(p.transposed ? p.rows : p.cols);
     a.blocks_k = (int)((n_in + 127) / 128);
     a.y = p.y;
