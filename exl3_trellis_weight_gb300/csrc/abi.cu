@@ -998,6 +998,8 @@ exl3_status exl3_wait_timeouts(unsigned int *count_out) {
     if (st == EXL3_OK)
         st = exl3::linear8_take_wait_timeouts(&r), n += r;
     if (st == EXL3_OK)
+        st = exl3::norm_take_wait_timeouts(&r), n += r;
+    if (st == EXL3_OK)
         st = exl3::expert_up_take_wait_timeouts(&r), n += r;
     if (count_out)
         *count_out = n;

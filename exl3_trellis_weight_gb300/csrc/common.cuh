@@ -213,6 +213,8 @@ exl3_status rot_take_wait_timeouts(unsigned int *n);
 exl3_status product_take_wait_timeouts(unsigned int *n);
 // the same of the products in 8 bits (linear8.cu)
 exl3_status linear8_take_wait_timeouts(unsigned int *n);
+// gradients of norms
+exl3_status norm_take_wait_timeouts(unsigned int *n);
 // the same of expert layers (expert_up.cu)
 exl3_status expert_up_take_wait_timeouts(unsigned int *n);
 

@@ -10,6 +10,7 @@
 // of it where rows allow 16-byte accesses, and columns l, l + 32, ... where they do not, so
 // that a warp's accesses are whole sectors either way.
 #include "layer.cuh"
+#include "tc.cuh"
 
 namespace exl3 {
 
@@ -167,7 +168,7 @@ __device__ __forceinline__ float warp_sum(float v) {
 
 // A row whose sum of squares passes binary32's range (bfloat16's largest squares do) is
 // summed again with its values times 2^-75: the warps of a row take that turn together.
-constexpr float kDown = 0x1p-75f;
+constexpr float kDown = 0x1p-75f, kDownG = 0x1p-100f;
 __device__ __forceinline__ bool passed(float sum) { return !(sum <= 0x1.fffffep127f); }
 __device__ __forceinline__ void row_barrier(int sub, int wr) {
     asm volatile("bar.sync %0, %1;" ::"r"(1 + sub), "r"(wr * 32) : "memory");
@@ -276,26 +277,81 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormLaunch a, int wr) 
     }
 }
 
+// Binary32 in pairs, each half rounded as the single operation would be: half the instructions,
+// which with 20 to a value bound the gradients as much as memory does.
+struct Pair {
+    float x, y;
+};
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    Pair d;
+    asm("{\n\t.reg .b64 a, b, c;\n\t"
+        "mov.b64 a, {%2, %3};\n\t"
+        "mov.b64 b, {%4, %5};\n\t"
+        "mov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 c, a, b, c;\n\t"
+        "mov.b64 {%0, %1}, c;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+    Pair d;
+    asm("{\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%2, %3};\n\t"
+        "mov.b64 b, {%4, %5};\n\t"
+        "mul.rn.f32x2 a, a, b;\n\t"
+        "mov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+    Pair d;
+    asm("{\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%2, %3};\n\t"
+        "mov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 a, a, b;\n\t"
+        "mov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+template <typename T> __device__ __forceinline__ void unpack_pairs(const Eight &e, Pair (&v)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const float2 f = unpack2<T>(e.w[i]);
+        v[i] = {f.x, f.y};
+    }
+}
+
 // ---- its gradients ----------------------------------------------------------------------
-// Blocks stay and take rows in turn, the next row on its way while one is summed: a thread
-// keeps its columns' weights and part of dweight, in registers up to two units and in shared
-// memory beyond, where registers run out.
-template <typename T, bool VEC, int VPT, bool WAY>
-__global__ void __launch_bounds__(1024) norm_grad_kernel(const NormGradLaunch a, int wr) {
+// Blocks stay and take rows in turn, the next rows on their way while one is summed: a thread
+// keeps its columns' part of dweight, in registers up to two units and in shared memory
+// beyond, where registers run out.
+// RING: whole rows are copied into stages of shared memory, `depth` of them ahead.  (One row
+// ahead in registers were 48 KB to an SM on their way: 8192 x 4096 took 66 us, 4.1 TB/s.)
+// WAY: the next row is asked for into registers.
+__device__ unsigned int g_norm_timeouts;
+constexpr int kMaxDepth = 8;
+
+template <typename T, bool VEC, int VPT, bool WAY, bool RING>
+__global__ void __launch_bounds__(RING ? 512 : 1024) norm_grad_kernel(const NormGradLaunch a, int wr, int depth) {
     constexpr bool kRegs = VPT <= 2;
     __shared__ float2 place[2][32];
-    extern __shared__ float dw_mem[];
+    __shared__ __align__(8) unsigned long long bars[RING ? kMaxDepth : 1];
+    __shared__ int gave_up;
+    extern __shared__ __align__(16) float dw_mem[];
+    // (the sum of dweight's parts waits for this kernel's end)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
     const int sub = warp / wr, wi = warp % wr, rows = (int)(blockDim.x >> 5) / wr;
     const bool want = a.dweight != nullptr, wide = a.w_dt == EXL3_F32;
-    float dw[kRegs ? VPT : 1][8];
+    Pair dw[kRegs ? VPT : 1][4];
+    const float inv_n = __fdiv_rn(1.0f, (float)a.n);
     float *const mine = dw_mem + threadIdx.x;            // [unit][value][thread]
     if (kRegs) {
 #pragma unroll
         for (int k = 0; k < (kRegs ? VPT : 1); k++)
 #pragma unroll
-            for (int j = 0; j < 8; j++)
-                dw[k][j] = 0.0f;
+            for (int j = 0; j < 4; j++)
+                dw[k][j] = {0.0f, 0.0f};
     } else if (want) {
         for (int k = 0; k < VPT * 8; k++)
             mine[k * blockDim.x] = 0.0f;
@@ -318,59 +374,134 @@ __global__ void __launch_bounds__(1024) norm_grad_kernel(const NormGradLaunch a,
     };
     if (WAY)
         fetch((int64_t)blockIdx.x * rows + sub, eg, eh, ed);
+    // stage: dy, h and dh of the block's rows, one behind the other
+    const uint32_t ring = tc::saddr(dw_mem), bar0 = tc::saddr(bars), row_bytes = (uint32_t)a.n * 2u;
+    const int ops = ds ? 3 : 2;
+    const uint32_t stage_bytes = (uint32_t)(ops * rows) * row_bytes;
+    auto issue = [&](int64_t t0, int s) {  // by a warp
+        if (t0 >= a.T)
+            return;
+        const int n = (int)min((int64_t)rows, a.T - t0);
+        if (lane == 0)
+            tc::bar_expect(bar0 + 8u * s, (uint32_t)(ops * n) * row_bytes);
+        __syncwarp();
+        const int op = lane / rows, r = lane % rows;
+        if (op < ops && r < n) {
+            const T *from = op == 0 ? dy + (t0 + r) * a.dy_stride : op == 1 ? hs + (t0 + r) * a.h_stride : ds + (t0 + r) * a.dh_stride;
+            tc::bulk_load(ring + s * stage_bytes + (uint32_t)(op * rows + r) * row_bytes, from, row_bytes, bar0 + 8u * s);
+        }
+        __syncwarp();
+    };
+    if constexpr (RING) {
+        if (threadIdx.x == 0) {
+            for (int s = 0; s < depth; s++)
+                tc::bar_init(bar0 + 8u * s, 1);
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+            gave_up = 0;
+        }
+        __syncthreads();
+        if (warp == 0)
+            for (int s = 0; s < depth; s++)
+                issue((int64_t)(blockIdx.x + (int64_t)s * gridDim.x) * rows, s);
+    }
+    int stage = 0;
+    uint32_t phase = 0;
     int turn = 0;
     for (int64_t t0 = (int64_t)blockIdx.x * rows; t0 < a.T; t0 += step, turn ^= 1) {
         const int64_t t = t0 + sub;
         const bool in = t < a.T;
+        float eps = a.eps;
         Eight ng[WAY ? VPT : 1], nh[WAY ? VPT : 1], nd[WAY ? VPT : 1];
-        if constexpr (WAY)
-            fetch(t + step, ng, nh, nd);
-        else
-            fetch(t, eg, eh, ed);
-        float hh = 0.0f, gh = 0.0f;
+        if constexpr (RING) {
+            tc::bar_wait(bar0 + 8u * stage, phase, &gave_up, &g_norm_timeouts);
+            const char *at = reinterpret_cast<const char *>(dw_mem) + stage * stage_bytes + sub * row_bytes;
 #pragma unroll
-        for (int k = 0; k < VPT; k++) {
-            float g[8], v[8], w[8];
-            unpack_eight<T>(eg[k], g);
-            unpack_eight<T>(eh[k], v);
+            for (int k = 0; k < VPT; k++) {
+                const int c = column<true>(wi + k * wr, lane, 0);
+                auto take = [&](int op) {
+                    Eight e{};
+                    if (in && c < a.n) {
+                        const uint4 q = *reinterpret_cast<const uint4 *>(at + (size_t)op * rows * row_bytes + 2 * c);
+                        e.w[0] = q.x, e.w[1] = q.y, e.w[2] = q.z, e.w[3] = q.w;
+                    }
+                    return e;
+                };
+                eg[k] = take(0);
+                eh[k] = take(1);
+                if (ds)
+                    ed[k] = take(2);
+            }
+        } else if constexpr (WAY) {
+            fetch(t + step, ng, nh, nd);
+        } else {
+            fetch(t, eg, eh, ed);
+        }
+        // dy, h and dy weight of a unit: they stay in registers where there are some, and are
+        // unpacked again for the results where there are not
+        constexpr bool kStay = VPT == 1 || RING;
+        struct Unit {
+            Pair g[4], v[4], gw[4];
+        } stay[kStay ? VPT : 1];
+        float hh, gh, dh = 1.0f, dg = 1.0f;                  // (powers of two, see below)
+        auto unit = [&](int k, Unit &u) {
+            unpack_pairs<T>(eg[k], u.g);
+            unpack_pairs<T>(eh[k], u.v);
+            float w[8];
             load_weights<T, VEC>(a.weight, wide, wi + k * wr, lane, a.n, w);
 #pragma unroll
-            for (int j = 0; j < 8; j++) {
-                hh = __fmaf_rn(v[j], v[j], hh);
-                gh = __fmaf_rn(__fmul_rn(g[j], w[j]), v[j], gh);
+            for (int j = 0; j < 4; j++)
+                u.gw[j] = mul2(u.g[j], {w[2 * j], w[2 * j + 1]});
+        };
+        auto down = [&](Unit &u) {
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                u.v[j] = mul2(u.v[j], {dh, dh});
+                u.gw[j] = mul2(u.gw[j], {dg, dg});
             }
-        }
-        hh = warp_sum(hh);
-        gh = warp_sum(gh);
+        };
+        auto sums = [&](bool first) {
+            Pair h2 = {0.0f, 0.0f}, g2 = {0.0f, 0.0f};
+#pragma unroll
+            for (int k = 0; k < VPT; k++) {
+                Unit &u = stay[kStay ? k : 0];
+                if (first || !kStay)
+                    unit(k, u);
+                if (!first)
+                    down(u);
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    h2 = fma2(u.v[j], u.v[j], h2);
+                    g2 = fma2(u.gw[j], u.v[j], g2);
+                }
+            }
+            hh = warp_sum(__fadd_rn(h2.x, h2.y));
+            gh = warp_sum(__fadd_rn(g2.x, g2.y));
+        };
+        sums(true);
         if (wr > 1) {
             // (two places in turn: a row's reads are done before the barrier of the next)
             if (lane == 0)
                 place[turn][warp] = make_float2(hh, gh);
             __syncthreads();
+            if (RING) {                    // (everyone has read the stage)
+                if (warp == 0)
+                    issue(t0 + depth * step, stage);
+                if (++stage == depth)
+                    stage = 0, phase ^= 1;
+            }
             const float2 q = lane < wr ? place[turn][sub * wr + lane] : make_float2(0.0f, 0.0f);
             hh = warp_sum(q.x);
             gh = warp_sum(q.y);
         }
         if (in) {
-            float down = 1.0f;
+            // beyond binary32's range: h and dy weight times powers of two, each as it needs
+            float back = 1.0f;
             if (passed(hh) || passed(fabsf(gh))) {
-                down = kDown;
-                hh = gh = 0.0f;
-#pragma unroll
-                for (int k = 0; k < VPT; k++) {
-                    float g[8], v[8], w[8];
-                    unpack_eight<T>(eg[k], g);
-                    unpack_eight<T>(eh[k], v);
-                    load_weights<T, VEC>(a.weight, wide, wi + k * wr, lane, a.n, w);
-#pragma unroll
-                    for (int j = 0; j < 8; j++) {
-                        const float q = __fmul_rn(v[j], kDown);
-                        hh = __fmaf_rn(q, q, hh);
-                        gh = __fmaf_rn(__fmul_rn(g[j], w[j]), q, gh);
-                    }
-                }
-                hh = warp_sum(hh);
-                gh = warp_sum(gh);
+                dh = passed(hh) ? kDown : 1.0f;
+                dg = passed(fabsf(gh)) ? kDownG : 1.0f;
+                back = __fdiv_rn(dh, dg);
+                eps = __fmul_rn(__fmul_rn(a.eps, dh), dh);
+                sums(false);
                 if (wr > 1) {
                     row_barrier(sub, wr);  // the first sums are read
                     if (lane == 0)
@@ -381,39 +512,46 @@ __global__ void __launch_bounds__(1024) norm_grad_kernel(const NormGradLaunch a,
                     gh = warp_sum(q.y);
                 }
             }
-            // with h' = h down and s' = s / down:  dx = s (g - h' s'^2 sum(g h') / n)
-            const float s = __frsqrt_rn(__fmaf_rn(__fmul_rn(a.eps, down), down, __fdiv_rn(hh, (float)a.n)));
-            const float c = -__fmul_rn(__fmul_rn(s, s), __fdiv_rn(gh, (float)a.n)), sd = __fmul_rn(s, down);
+            // with h' = h dh, g' = dy weight dg, s' = s / dh:  dx = s' dh / dg (g' - h' s'^2 sum(g' h') / n)
+            const float s = __frsqrt_rn(__fmaf_rn(hh, inv_n, eps));
+            const float c = -__fmul_rn(__fmul_rn(s, s), __fmul_rn(gh, inv_n)), sd = __fmul_rn(s, back);
 #pragma unroll
             for (int k = 0; k < VPT; k++) {
-                const int unit = wi + k * wr;
-                float g[8], v[8], w[8];
-                unpack_eight<T>(eg[k], g);
-                unpack_eight<T>(eh[k], v);
-                load_weights<T, VEC>(a.weight, wide, unit, lane, a.n, w);
-#pragma unroll
-                for (int j = 0; j < 8; j++)
-                    v[j] = __fmul_rn(v[j], down);
+                Unit &u = stay[kStay ? k : 0];
+                if (!kStay) {
+                    unit(k, u);
+                    if (back != 1.0f || dh != 1.0f)
+                        down(u);
+                }
                 if (want) {
 #pragma unroll
-                    for (int j = 0; j < 8; j++) {
-                        const float p = __fmul_rn(v[j], s);
-                        if (kRegs)
-                            dw[kRegs ? k : 0][j] = __fmaf_rn(g[j], p, dw[kRegs ? k : 0][j]);
-                        else
-                            mine[(k * 8 + j) * blockDim.x] = __fmaf_rn(g[j], p, mine[(k * 8 + j) * blockDim.x]);
+                    for (int j = 0; j < 4; j++) {
+                        const Pair p = mul2(u.v[j], {s, s});
+                        if (kRegs) {
+                            Pair &d = dw[kRegs ? k : 0][j];
+                            d = fma2(u.g[j], p, d);
+                        } else {
+                            float *d = mine + (k * 8 + 2 * j) * blockDim.x;
+                            d[0] = __fmaf_rn(u.g[j].x, p.x, d[0]);
+                            d[blockDim.x] = __fmaf_rn(u.g[j].y, p.y, d[blockDim.x]);
+                        }
                     }
                 }
+                Eight e;
+                Pair o[4];
 #pragma unroll
-                for (int j = 0; j < 8; j++)
-                    v[j] = __fmul_rn(__fmaf_rn(v[j], c, __fmul_rn(g[j], w[j])), sd);
+                for (int j = 0; j < 4; j++)
+                    o[j] = mul2(fma2(u.v[j], {c, c}, u.gw[j]), {sd, sd});
                 if (ds) {
-                    unpack_eight<T>(ed[k], g);
+                    unpack_pairs<T>(ed[k], u.g);
 #pragma unroll
-                    for (int j = 0; j < 8; j++)
-                        v[j] = __fadd_rn(v[j], g[j]);
+                    for (int j = 0; j < 4; j++)
+                        o[j] = add2(o[j], u.g[j]);
                 }
-                store_eight<T, VEC>(reinterpret_cast<T *>(a.dx) + t * a.dx_stride, unit, lane, a.n, pack_eight<T>(v));
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+                    e.w[j] = pack2<T>(o[j].x, o[j].y);
+                store_eight<T, VEC>(reinterpret_cast<T *>(a.dx) + t * a.dx_stride, wi + k * wr, lane, a.n, e);
             }
         }
         if constexpr (WAY) {
@@ -422,6 +560,9 @@ __global__ void __launch_bounds__(1024) norm_grad_kernel(const NormGradLaunch a,
                 eg[k] = ng[k], eh[k] = nh[k], ed[k] = nd[k];
         }
     }
+    if (RING && gave_up && threadIdx.x == 0)           // nothing may be in flight when the block ends
+        for (int s = 0; s < depth; s++)
+            tc::bar_drain(bar0 + 8u * s, phase ^ (s < stage));
     if (!want)
         return;
     float *part = a.part + ((int64_t)blockIdx.x * rows + sub) * a.n;
@@ -431,7 +572,7 @@ __global__ void __launch_bounds__(1024) norm_grad_kernel(const NormGradLaunch a,
         for (int j = 0; j < 8; j++) {
             const int c = column<VEC>(wi + k * wr, lane, j);
             if (c < a.n)
-                part[c] = kRegs ? dw[kRegs ? k : 0][j] : mine[(k * 8 + j) * blockDim.x];
+                part[c] = !kRegs ? mine[(k * 8 + j) * blockDim.x] : j & 1 ? dw[kRegs ? k : 0][j >> 1].y : dw[kRegs ? k : 0][j >> 1].x;
         }
 }
 
@@ -440,9 +581,12 @@ template <typename T> __global__ void __launch_bounds__(1024) dweight_kernel(con
     __shared__ float place[32][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     float s = 0.0f;
-    if (c < n)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (c < n) {
+#pragma unroll 8
         for (int i = warp; i < parts; i += 32)
-            s = __fadd_rn(s, part[(int64_t)i * n + c]);
+            s = __fadd_rn(s, __ldcg(part + (int64_t)i * n + c));
+    }
     place[warp][lane] = s;
     __syncthreads();
     s = warp_sum(place[lane][warp]);
@@ -628,49 +772,80 @@ template <typename T, bool VEC> exl3_status norm_v(const NormLaunch &p, const Sh
     return cuda_check(cudaGetLastError(), "norm launch");
 }
 
-constexpr int kGradWarps = 32;                 // of an SM
+// Warps of an SM (half of them with two units each, which take 117 registers), and how many
+// columns a ring of whole rows is for.
+constexpr int kGradWarps = 32, kRingFrom = 1024, kRingTo = 8192;
+constexpr uint32_t kRingRoom = 208 * 1024;     // of an SM
 
-Shape grad_shape(int64_t n) {
+struct GradShape : Shape {
+    int depth;                // 0: no ring
+    int per_sm;               // blocks
+};
+GradShape grad_shape(int64_t n, bool ring, bool with_dh) {
     const int units = (int)((n + kUnitN - 1) / kUnitN);
-    Shape f;
+    GradShape f;
     f.vpt = units <= 16 ? 1 : units <= 64 ? 2 : 4;
     f.wr = (units + f.vpt - 1) / f.vpt;
     f.rows = f.wr < 8 ? 8 / f.wr : 1;
+    f.per_sm = (ring && f.vpt == 2 ? kGradWarps / 2 : kGradWarps) / (f.rows * f.wr);
+    f.per_sm = f.per_sm > 0 ? f.per_sm : 1;
+    f.depth = 0;
+    if (ring) {
+        const uint32_t stage = (uint32_t)((with_dh ? 3 : 2) * f.rows * n * 2);
+        f.depth = (int)(kRingRoom / (f.per_sm * stage));
+        f.depth = f.depth > kMaxDepth ? kMaxDepth : f.depth;
+    }
     return f;
 }
-unsigned grad_grid(int64_t T, const Shape &f) {
-    const int64_t per_sm = kGradWarps / (f.rows * f.wr) > 0 ? kGradWarps / (f.rows * f.wr) : 1;
-    const int64_t most = device_sm_count() * per_sm, want = (T + f.rows - 1) / f.rows;
+unsigned grad_grid(int64_t T, const GradShape &f) {
+    const int64_t most = device_sm_count() * (int64_t)f.per_sm, want = (T + f.rows - 1) / f.rows;
     return (unsigned)(want < most ? want : most);
 }
+bool ring_size(int64_t n) { return n >= kRingFrom && n <= kRingTo && n % 8 == 0; }
 
-template <typename T, bool VEC, int VPT> exl3_status norm_grad_k(const NormGradLaunch &p, const Shape &f, cudaStream_t s) {
+template <typename T, bool VEC, int VPT, bool RING> exl3_status norm_grad_k(const NormGradLaunch &p, const GradShape &f, cudaStream_t s) {
     const unsigned block = (unsigned)(f.rows * f.wr * 32), grid = grad_grid(p.T, f);
-    const size_t smem = VPT > 2 && p.dweight ? (size_t)VPT * 8 * block * sizeof(float) : 0;
+    const size_t smem = RING ? (size_t)f.depth * (p.dh ? 3 : 2) * f.rows * p.n * 2
+                             : VPT > 2 && p.dweight ? (size_t)VPT * 8 * block * sizeof(float) : 0;
+    constexpr bool kWay = !RING && VPT == 1;
     if (smem) {
-        const cudaError_t e = allow_smem((const void *)norm_grad_kernel<T, VEC, VPT, VPT == 1>, smem);
+        const cudaError_t e = allow_smem((const void *)norm_grad_kernel<T, VEC, VPT, kWay, RING>, smem);
         if (e != cudaSuccess)
             return cuda_check(e, "cudaFuncSetAttribute(norm gradient)");
     }
-    norm_grad_kernel<T, VEC, VPT, VPT == 1><<<grid, block, smem, s>>>(p, f.wr);
+    norm_grad_kernel<T, VEC, VPT, kWay, RING><<<grid, block, smem, s>>>(p, f.wr, f.depth);
     note_launch();
     return cuda_check(cudaGetLastError(), "norm gradient launch");
 }
 template <typename T> exl3_status norm_grad_t(const NormGradLaunch &p, bool vec, cudaStream_t s) {
-    const Shape f = grad_shape(p.n);
+    const GradShape r = grad_shape(p.n, vec && ring_size(p.n), p.dh != nullptr);
+    const GradShape f = r.depth >= 2 ? r : grad_shape(p.n, false, false);
     if (p.T) {
         exl3_status st;
-        if (vec)
-            st = f.vpt == 1 ? norm_grad_k<T, true, 1>(p, f, s) : f.vpt == 2 ? norm_grad_k<T, true, 2>(p, f, s) : norm_grad_k<T, true, 4>(p, f, s);
+        if (f.depth)
+            st = f.vpt == 1 ? norm_grad_k<T, true, 1, true>(p, f, s) : norm_grad_k<T, true, 2, true>(p, f, s);
+        else if (vec)
+            st = f.vpt == 1 ? norm_grad_k<T, true, 1, false>(p, f, s) : f.vpt == 2 ? norm_grad_k<T, true, 2, false>(p, f, s) : norm_grad_k<T, true, 4, false>(p, f, s);
         else
-            st = f.vpt == 1 ? norm_grad_k<T, false, 1>(p, f, s) : f.vpt == 2 ? norm_grad_k<T, false, 2>(p, f, s) : norm_grad_k<T, false, 4>(p, f, s);
+            st = f.vpt == 1 ? norm_grad_k<T, false, 1, false>(p, f, s) : f.vpt == 2 ? norm_grad_k<T, false, 2, false>(p, f, s) : norm_grad_k<T, false, 4, false>(p, f, s);
         if (st != EXL3_OK)
             return st;
     }
     if (!p.dweight)
         return EXL3_OK;
     const int parts = p.T ? (int)grad_grid(p.T, f) * f.rows : 0;
-    dweight_kernel<T><<<(unsigned)((p.n + 31) / 32), 1024, 0, s>>>(p.part, parts, p.n, p.dweight, p.w_dt == EXL3_F32);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((p.n + 31) / 32));
+    cfg.blockDim = dim3(1024);
+    cfg.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = p.T ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, dweight_kernel<T>, (const float *)p.part, parts, p.n, p.dweight, p.w_dt == EXL3_F32);
+    if (e != cudaSuccess)
+        return cuda_check(e, "norm weight gradient launch");
     note_launch();
     return cuda_check(cudaGetLastError(), "norm weight gradient launch");
 }
@@ -711,8 +886,25 @@ exl3_status launch_norm(const NormLaunch &p, cudaStream_t s) {
 }
 
 int64_t norm_grad_parts(int64_t T, int64_t n) {
-    const Shape f = grad_shape(n);
-    return T ? (int64_t)grad_grid(T, f) * f.rows : 0;
+    if (T == 0)
+        return 0;
+    // (which form it is goes by alignment, too)
+    const GradShape f = grad_shape(n, false, false), r = grad_shape(n, ring_size(n), false);
+    const int64_t a = (int64_t)grad_grid(T, f) * f.rows, b = (int64_t)grad_grid(T, r) * r.rows;
+    return a > b ? a : b;
+}
+
+exl3_status norm_take_wait_timeouts(unsigned int *n) {
+    *n = 0;
+    unsigned int v = 0;
+    const unsigned int zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_norm_timeouts, sizeof v);
+    if (e == cudaSuccess && v != 0)
+        e = cudaMemcpyToSymbol(g_norm_timeouts, &zero, sizeof zero);
+    if (e != cudaSuccess)
+        return cuda_check(e, "wait timeout count");
+    *n = v;
+    return EXL3_OK;
 }
 
 exl3_status launch_norm_grad(const NormGradLaunch &p, cudaStream_t s) {
