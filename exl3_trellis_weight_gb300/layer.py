@@ -10,7 +10,7 @@ import ctypes
 import torch
 
 from . import EXL3_BF16, EXL3_E4M3, EXL3_F16, EXL3_F32
-from .products import _activations, _call, _coded, _current_device, _dense, _grad_on, _lib, _rows, _stream
+from .products import _activations, _call, _current_device, _dense, _grad_on, _lib, _rows, _stream
 from .products import _ws as _given_ws
 
 _DT = {torch.bfloat16: EXL3_BF16, torch.float16: EXL3_F16}
@@ -274,6 +274,7 @@ def linear8(x, w, w_scale, x_scale=None, transposed: bool = False, dtype=None, o
 
 
 _Experts = ctypes.c_void_p * 12
+_PARTS, _PART_DT = ("codes", "su", "sv", "scale"), (torch.int16, torch.float32, torch.float32, torch.float32)
 
 
 def expert_layer(x, gate, up, down, K: int, top_k: int, router=None, ids=None, weights=None, transposed: bool = False,
@@ -290,18 +291,29 @@ def expert_layer(x, gate, up, down, K: int, top_k: int, router=None, ids=None, w
     ``weights`` float32 [T, top_k] (an id that is no expert's is passed over).  Returns y
     [T, hidden] of x's dtype.  For more tokens, and for gradients, there is
     ``expert_linear``."""
-    dev = x.device
-    E = gate[0].shape[0]
-    H, F, *g = _coded(*gate[:3], K, gate[3], (E,), dev)
-    uh, uf, *u = _coded(*up[:3], K, up[3], (E,), dev)
+    dev, index = x.device, x.get_device()
+    gc = gate[0]
+    if gc.dim() != 4:
+        raise ValueError(f"gate codes must be [experts, rows/16, cols/16, 16K], got {tuple(gc.shape)}")
+    E, rows, cols, _ = gc.shape
     kd = K if K_down is None else K_down
-    df, dh, *d = _coded(*down[:3], kd, down[3], (E,), dev)
-    if (uh, uf, dh, df) != (H, F, H, F):
-        raise ValueError(f"gate {(H, F)}, up {(uh, uf)} and down {(df, dh)} do not go together")
-    if transposed:
-        H, F = F, H
+    at, made, grad = [], [], False
+    for name, m, r, c, k in (("gate", gate, rows, cols, K), ("up", up, rows, cols, K), ("down", down, cols, rows, kd)):
+        if m[0].shape[1:3] != (r, c):
+            raise ValueError(f"gate {(16 * rows, 16 * cols)} and {name} {tuple(16 * v for v in m[0].shape[1:3])} do not go together")
+        if not isinstance(m[3], torch.Tensor):
+            m = (*m[:3], torch.full((E,), float(m[3]), dtype=torch.float32, device=dev))
+            made.append(m)                 # (lives until the launch)
+        for t, what, dt, shape in zip(m, _PARTS, _PART_DT, ((E, r, c, 16 * k), (E, 16 * r), (E, 16 * c), (E,))):
+            if t.dtype is not dt or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+                _dense(t, f"{name} {what}", dt, shape, index)
+            at.append(t.data_ptr())
+            if t.requires_grad:
+                grad = True
+    H, F = (cols, rows) if transposed else (rows, cols)
+    H, F = 16 * H, 16 * F
     xs = _activations(x, "x", H)
-    T, index = x.shape[0], x.get_device()
+    T = x.shape[0]
     pr = pi = pw = None
     rdt = 0
     if router is not None:
@@ -315,11 +327,9 @@ def expert_layer(x, gate, up, down, K: int, top_k: int, router=None, ids=None, w
             raise ValueError("a router, or ids and weights")
         pi = _dense(ids, "ids", torch.int32, (T, top_k), index)
         pw = _dense(weights, "weights", torch.float32, (T, top_k), index)
-    if _grad_on():
-        for name, t in (("x", x), ("router", router), ("weights", weights), *((n, t) for n, m in
-                        (("gate", gate), ("up", up), ("down", down)) for t in m[1:] if isinstance(t, torch.Tensor))):
-            if t is not None and t.requires_grad:
-                raise ValueError(f"there is no gradient with respect to {name} (torch.no_grad(); expert_linear has one)")
+    if _grad_on() and (grad or x.requires_grad or (router is not None and router.requires_grad) or
+                       (weights is not None and weights.requires_grad)):
+        raise ValueError("there is no gradient through an expert layer (torch.no_grad() lets it; expert_linear has one)")
     if out is None:
         out = _new((T, H), (H, 1), x.dtype, dev)
         ys = H
@@ -328,6 +338,6 @@ def expert_layer(x, gate, up, down, K: int, top_k: int, router=None, ids=None, w
     L = _lib()
     ws = _ws(L.exl3_expert_layer_workspace_bytes(T, H, F, E, top_k), dev, ws)
     _call(L.exl3_expert_layer, dev.index, x.data_ptr(), _DT[x.dtype], T, xs, pr, rdt, pi, pw, top_k, 1 if normalize else 0, E,
-          _Experts(*g[:4], *u[:4], *d[:4]), H, F, K, kd, 1 if transposed else 0, out.data_ptr(), ys, ws.data_ptr(),
+          _Experts(*at), H, F, K, kd, 1 if transposed else 0, out.data_ptr(), ys, ws.data_ptr(),
           ws.numel() * ws.element_size(), _stream(dev.index))
     return out
