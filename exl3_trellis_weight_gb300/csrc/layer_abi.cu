@@ -32,8 +32,11 @@ exl3_status check_same_or_apart(const Rows &out, const char *name, const Rows &r
 
 bool norm_ok(int64_t T, int64_t n) { return T >= 0 && T <= kMaxTokens && n >= 1 && n <= kMaxNorm; }
 
-exl3_status check_norm(int dt, int64_t T, int64_t n, const void *weight, int w_dt) {
+exl3_status check_norm(int dt, int64_t T, int64_t n, const void *weight, int w_dt, float eps) {
     exl3_status st;
+    // (a normal number is above what the squares of a row lose below binary32's range)
+    if (!(eps >= 0x1p-126f && eps <= 0x1.fffffep127f))
+        return set_error(EXL3_ERR_INVALID_ARG, "eps = %g is not a positive normal number", (double)eps);
     if ((st = check_16bit(dt)) != EXL3_OK) return st;
     if ((st = check_tokens(T)) != EXL3_OK) return st;
     if (!norm_ok(T, n))
@@ -109,7 +112,7 @@ exl3_status exl3_rms_norm(const void *x, int dt, int64_t T, int64_t n, int64_t x
                           int64_t r_stride, const void *weight, int w_dt, float eps, void *h, int64_t h_stride, void *y,
                           int64_t y_stride, uint8_t *y8, float *scale, void *stream) {
     exl3_status st;
-    if ((st = check_norm(dt, T, n, weight, w_dt)) != EXL3_OK) return st;
+    if ((st = check_norm(dt, T, n, weight, w_dt, eps)) != EXL3_OK) return st;
     if (T == 0)
         return EXL3_OK;
     if (!y && !y8)
@@ -177,7 +180,7 @@ exl3_status exl3_rms_norm_backward(const void *dy, int64_t dy_stride, const void
                                    int64_t n, const void *weight, int w_dt, float eps, const void *dh, int64_t dh_stride,
                                    void *dx, int64_t dx_stride, void *dweight, void *ws, size_t ws_bytes, void *stream) {
     exl3_status st;
-    if ((st = check_norm(dt, T, n, weight, w_dt)) != EXL3_OK) return st;
+    if ((st = check_norm(dt, T, n, weight, w_dt, eps)) != EXL3_OK) return st;
     const size_t w_size = w_dt == EXL3_F32 ? 4 : 2, w_bytes = (size_t)n * w_size;
     const Rows dyr{dy, T, n, dy_stride}, hr{h, T, n, h_stride}, dhr{dh, dh ? T : 0, n, dh_stride}, dxr{dx, T, n, dx_stride};
     if ((st = check_rows(dyr, "dy")) != EXL3_OK) return st;

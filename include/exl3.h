@@ -475,7 +475,8 @@ EXL3_API exl3_status exl3_expert_linear(const void *x, int dt, int64_t T, int64_
  *     are read and written in wide accesses).  residual NULL: none, and h is not
  *     written.  h may be x or residual itself (same address and stride), y may
  *     be x itself; otherwise no output overlaps an input or another output.
- *   weight (device) [n] of type w_dt: dt or EXL3_F32.  n in [1, 32768].
+ *   weight (device) [n] of type w_dt: dt or EXL3_F32.  n in [1, 32768].  eps is a
+ *     positive normal number.
  *   y may be NULL; y8 (device, uint8 [T][n], e4m3) and scale (device, fp32
  *     [ceil(n/128)][T]) may both be NULL; y or y8 is there.
  *   A block of 128 columns of a row (the last one may be shorter) whose largest
