@@ -7,8 +7,9 @@
 // All of it is bound by memory: each row is read once, stays in registers (in the 16 bits
 // it came in) between its sum and its result, and the block of 128 that shares a scale lies
 // in half a warp.  A warp's unit is 256 neighbouring columns: lane l has columns 8l .. 8l + 7
-// of it where rows allow 16-byte accesses, and columns l, l + 32, ... where they do not, so
-// that a warp's accesses are whole sectors either way.
+// of it where rows allow 16-byte accesses (kWide), pairs 2l + 64i where they are whole pairs, and
+// columns l, l + 32, ... where they are not, so that a warp's accesses are whole sectors
+// each way.
 #include "layer.cuh"
 #include "tc.cuh"
 
@@ -17,29 +18,37 @@ namespace exl3 {
 namespace {
 
 constexpr int kUnitN = 256;
+constexpr int kSingle = 0, kWide = 1, kPairs = 2;      // VEC: a thread's accesses
 
 // ---- eight values of a unit in the 16 bits of memory ------------------------------
 struct Eight {
     uint32_t w[4];
 };
 
-template <bool VEC> __device__ __forceinline__ int column(int unit, int lane, int j) {
-    return unit * kUnitN + (VEC ? lane * 8 + j : lane + 32 * j);
+template <int VEC> __device__ __forceinline__ int column(int unit, int lane, int j) {
+    return unit * kUnitN + (VEC == kWide ? lane * 8 + j : VEC == kPairs ? 2 * lane + 64 * (j >> 1) + (j & 1) : lane + 32 * j);
 }
 
-template <typename T, bool VEC> __device__ __forceinline__ Eight load_eight(const T *row, int unit, int lane, int n) {
+template <typename T, int VEC> __device__ __forceinline__ Eight load_eight(const T *row, int unit, int lane, int n) {
     Eight e{};
-    if (VEC) {
-        const int c = column<true>(unit, lane, 0);
+    if (VEC == kWide) {
+        const int c = column<kWide>(unit, lane, 0);
         if (c < n) {
             const uint4 q = *reinterpret_cast<const uint4 *>(row + c);
             e.w[0] = q.x, e.w[1] = q.y, e.w[2] = q.z, e.w[3] = q.w;
+        }
+    } else if (VEC == kPairs) {
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int c = column<VEC>(unit, lane, 2 * i);
+            if (c < n)
+                e.w[i] = *reinterpret_cast<const uint32_t *>(row + c);
         }
     } else {
         const uint16_t *r = reinterpret_cast<const uint16_t *>(row);
 #pragma unroll
         for (int j = 0; j < 8; j++) {
-            const int c = column<false>(unit, lane, j);
+            const int c = column<VEC>(unit, lane, j);
             if (c < n)
                 e.w[j >> 1] |= (uint32_t)r[c] << (16 * (j & 1));
         }
@@ -47,16 +56,23 @@ template <typename T, bool VEC> __device__ __forceinline__ Eight load_eight(cons
     return e;
 }
 
-template <typename T, bool VEC> __device__ __forceinline__ void store_eight(T *row, int unit, int lane, int n, const Eight &e) {
-    if (VEC) {
-        const int c = column<true>(unit, lane, 0);
+template <typename T, int VEC> __device__ __forceinline__ void store_eight(T *row, int unit, int lane, int n, const Eight &e) {
+    if (VEC == kWide) {
+        const int c = column<kWide>(unit, lane, 0);
         if (c < n)
             *reinterpret_cast<uint4 *>(row + c) = make_uint4(e.w[0], e.w[1], e.w[2], e.w[3]);
+    } else if (VEC == kPairs) {
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int c = column<VEC>(unit, lane, 2 * i);
+            if (c < n)
+                *reinterpret_cast<uint32_t *>(row + c) = e.w[i];
+        }
     } else {
         uint16_t *r = reinterpret_cast<uint16_t *>(row);
 #pragma unroll
         for (int j = 0; j < 8; j++) {
-            const int c = column<false>(unit, lane, j);
+            const int c = column<VEC>(unit, lane, j);
             if (c < n)
                 r[c] = (uint16_t)(e.w[j >> 1] >> (16 * (j & 1)));
         }
@@ -79,15 +95,22 @@ template <typename T> __device__ __forceinline__ Eight pack_eight(const float (&
 }
 
 // the same from binary32, as the norm's weights may be, too
-template <typename T, bool VEC>
+template <typename T, int VEC>
 __device__ __forceinline__ void load_weights(const void *w, bool wide, int unit, int lane, int n, float (&v)[8]) {
     if (!wide) {
         unpack_eight<T>(load_eight<T, VEC>(reinterpret_cast<const T *>(w), unit, lane, n), v);
         return;
     }
     const float *f = reinterpret_cast<const float *>(w);
-    if (VEC) {
-        const int c = column<true>(unit, lane, 0);
+    if (VEC == kPairs) {
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int c = column<VEC>(unit, lane, 2 * i);
+            const float2 q = c < n ? *reinterpret_cast<const float2 *>(f + c) : make_float2(0.0f, 0.0f);
+            v[2 * i] = q.x, v[2 * i + 1] = q.y;
+        }
+    } else if (VEC == kWide) {
+        const int c = column<kWide>(unit, lane, 0);
         float4 a = {}, b = {};
         if (c < n)
             a = reinterpret_cast<const float4 *>(f + c)[0], b = reinterpret_cast<const float4 *>(f + c)[1];
@@ -95,7 +118,7 @@ __device__ __forceinline__ void load_weights(const void *w, bool wide, int unit,
     } else {
 #pragma unroll
         for (int j = 0; j < 8; j++) {
-            const int c = column<false>(unit, lane, j);
+            const int c = column<VEC>(unit, lane, j);
             v[j] = c < n ? f[c] : 0.0f;
         }
     }
@@ -113,10 +136,10 @@ __device__ __forceinline__ void block_scale(uint32_t top, float &inv, float &sca
 
 // A unit's eight values of each lane to codes: two blocks of 128, each half a warp (VEC)
 // or half of every lane's values.  Outside of the row values are 0.
-template <bool VEC>
+template <int VEC>
 __device__ __forceinline__ void encode_row(const float (&v)[8], uint8_t *codes, float *scale, int64_t hop, int unit, int lane,
                                            int n) {
-    if (VEC) {
+    if (VEC == kWide) {
         uint32_t top = 0;
 #pragma unroll
         for (int j = 0; j < 8; j++)
@@ -126,7 +149,7 @@ __device__ __forceinline__ void encode_row(const float (&v)[8], uint8_t *codes, 
             top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
         float inv, sc;
         block_scale(top, inv, sc);
-        const int c = column<true>(unit, lane, 0);
+        const int c = column<kWide>(unit, lane, 0);
         if (c < n) {
             uint32_t q[4];
 #pragma unroll
@@ -147,10 +170,15 @@ __device__ __forceinline__ void encode_row(const float (&v)[8], uint8_t *codes, 
             float inv, sc;
             block_scale(top, inv, sc);
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
-                const int c = column<false>(unit, lane, 4 * h + j);
-                if (c < n)
-                    codes[c] = (uint8_t)pack8(__fmul_rn(v[4 * h + j], inv), 0.0f);
+            for (int j = 0; j < 4; j += VEC == kPairs ? 2 : 1) {
+                const int c = column<VEC>(unit, lane, 4 * h + j);
+                const uint32_t q = pack8(__fmul_rn(v[4 * h + j], inv), __fmul_rn(v[4 * h + (j + 1) % 4], inv));
+                if (c < n) {
+                    if (VEC == kPairs)
+                        *reinterpret_cast<uint16_t *>(codes + c) = (uint16_t)q;
+                    else
+                        codes[c] = (uint8_t)q;
+                }
             }
             const int c0 = unit * kUnitN + 128 * h;
             if (lane == 0 && c0 < n)
@@ -176,7 +204,7 @@ __device__ __forceinline__ void row_barrier(int sub, int wr) {
 
 // ---- the norm -------------------------------------------------------------------------
 // A row to `wr` warps, each VPT units of it; a block has one row or several.
-template <typename T, bool VEC, int VPT>
+template <typename T, int VEC, int VPT>
 __global__ void __launch_bounds__(1024) norm_kernel(const NormLaunch a, int wr) {
     __shared__ float place[32];
     const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
@@ -263,14 +291,14 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormLaunch a, int wr) 
         if (a.y)
             store_eight<T, VEC>(reinterpret_cast<T *>(a.y) + t * a.y_stride, unit, lane, a.n, pack_eight<T>(v));
         if (a.y8) {
-            if (VEC ? column<true>(unit, lane, 0) >= a.n : false) {
+            if (VEC == kWide ? column<kWide>(unit, lane, 0) >= a.n : false) {
 #pragma unroll
                 for (int j = 0; j < 8; j++)
                     v[j] = 0.0f;
-            } else if (!VEC) {
+            } else if (VEC != kWide) {
 #pragma unroll
                 for (int j = 0; j < 8; j++)
-                    v[j] = column<false>(unit, lane, j) < a.n ? v[j] : 0.0f;
+                    v[j] = column<VEC>(unit, lane, j) < a.n ? v[j] : 0.0f;
             }
             encode_row<VEC>(v, a.y8 + t * a.n, a.scale + t, a.T, unit, lane, a.n);
         }
@@ -331,7 +359,7 @@ template <typename T> __device__ __forceinline__ void unpack_pairs(const Eight &
 __device__ unsigned int g_norm_timeouts;
 constexpr int kMaxDepth = 8;
 
-template <typename T, bool VEC, int VPT, bool WAY, bool RING>
+template <typename T, int VEC, int VPT, bool WAY, bool RING>
 __global__ void __launch_bounds__(RING ? 512 : 1024) norm_grad_kernel(const NormGradLaunch a, int wr, int depth) {
     constexpr bool kRegs = VPT <= 2;
     __shared__ float2 place[2][32];
@@ -417,7 +445,7 @@ __global__ void __launch_bounds__(RING ? 512 : 1024) norm_grad_kernel(const Norm
             const char *at = reinterpret_cast<const char *>(dw_mem) + stage * stage_bytes + sub * row_bytes;
 #pragma unroll
             for (int k = 0; k < VPT; k++) {
-                const int c = column<true>(wi + k * wr, lane, 0);
+                const int c = column<kWide>(wi + k * wr, lane, 0);
                 auto take = [&](int op) {
                     Eight e{};
                     if (in && c < a.n) {
@@ -600,27 +628,16 @@ template <typename T> __global__ void __launch_bounds__(1024) dweight_kernel(con
 }
 
 // ---- blocks of any matrix ---------------------------------------------------------------
-template <typename T, bool VEC> __device__ __forceinline__ void load_values(const T *row, int unit, int lane, int n, float (&v)[8]) {
-    load_weights<__half, VEC>(row, true, unit, lane, n, v);
-}
-template <> __device__ __forceinline__ void load_values<__half, true>(const __half *row, int unit, int lane, int n, float (&v)[8]) {
-    unpack_eight<__half>(load_eight<__half, true>(row, unit, lane, n), v);
-}
-template <> __device__ __forceinline__ void load_values<__half, false>(const __half *row, int unit, int lane, int n, float (&v)[8]) {
-    unpack_eight<__half>(load_eight<__half, false>(row, unit, lane, n), v);
-}
-template <>
-__device__ __forceinline__ void load_values<__nv_bfloat16, true>(const __nv_bfloat16 *row, int unit, int lane, int n, float (&v)[8]) {
-    unpack_eight<__nv_bfloat16>(load_eight<__nv_bfloat16, true>(row, unit, lane, n), v);
-}
-template <>
-__device__ __forceinline__ void load_values<__nv_bfloat16, false>(const __nv_bfloat16 *row, int unit, int lane, int n, float (&v)[8]) {
-    unpack_eight<__nv_bfloat16>(load_eight<__nv_bfloat16, false>(row, unit, lane, n), v);
+template <typename T, int VEC> __device__ __forceinline__ void load_values(const T *row, int unit, int lane, int n, float (&v)[8]) {
+    if constexpr (sizeof(T) == 4)
+        load_weights<__half, VEC>(row, true, unit, lane, n, v);
+    else
+        unpack_eight<T>(load_eight<T, VEC>(row, unit, lane, n), v);
 }
 
 // 1 x 128: a warp takes four units, one behind the other
 constexpr int kUnitsWarp = 4;
-template <typename T, bool VEC> __global__ void __launch_bounds__(256) rows8_kernel(const Quantize8Launch a) {
+template <typename T, int VEC> __global__ void __launch_bounds__(256) rows8_kernel(const Quantize8Launch a) {
     // (a product behind this launch may load its weights; it waits for this kernel's end
     // before it reads what is written here)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -647,7 +664,7 @@ template <typename T, bool VEC> __global__ void __launch_bounds__(256) rows8_ker
 }
 
 // 128 x 128: eight warps to a block, two rows of it a warp at a time
-template <typename T, bool VEC> __global__ void __launch_bounds__(256) blocks8_kernel(const Quantize8Launch a) {
+template <typename T, int VEC> __global__ void __launch_bounds__(256) blocks8_kernel(const Quantize8Launch a) {
     __shared__ uint32_t place[8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int blocks_c = (int)((a.n + 127) / 128);
@@ -743,7 +760,15 @@ template <typename T, bool VEC> __global__ void __launch_bounds__(256) blocks8_k
 }
 
 // ---- launches -----------------------------------------------------------------------------
-bool wide_rows(const void *p, int64_t stride, int size) { return ((uintptr_t)p & 15u) == 0 && stride * size % 16 == 0; }
+// rows whose elements, 8 or 2 at a time (see column), all stand at multiples of their size; the
+// narrowest of several arrays counts
+int access_of(const void *p, int64_t stride, int size, int64_t n, int best) {
+    if (!p)
+        return best;
+    auto fits = [&](int bytes) { return (uintptr_t)p % bytes == 0 && stride * size % bytes == 0; };
+    const int own = n % 8 == 0 && fits(size == 1 ? 8 : 16) ? kWide : n % 2 == 0 && fits(2 * size) ? kPairs : kSingle;
+    return own == kWide ? best : best == kWide || own == kSingle ? own : best;
+}
 
 struct Shape {
     int vpt, wr, rows;        // units of a warp, warps of a row, rows of a block
@@ -760,7 +785,7 @@ Shape norm_shape(int64_t T, int64_t n, bool many) {
     return f;
 }
 
-template <typename T, bool VEC> exl3_status norm_v(const NormLaunch &p, const Shape &f, cudaStream_t s) {
+template <typename T, int VEC> exl3_status norm_v(const NormLaunch &p, const Shape &f, cudaStream_t s) {
     const unsigned grid = (unsigned)((p.T + f.rows - 1) / f.rows), block = (unsigned)(f.rows * f.wr * 32);
     if (f.vpt == 1)
         norm_kernel<T, VEC, 1><<<grid, block, 0, s>>>(p, f.wr);
@@ -770,6 +795,10 @@ template <typename T, bool VEC> exl3_status norm_v(const NormLaunch &p, const Sh
         norm_kernel<T, VEC, 4><<<grid, block, 0, s>>>(p, f.wr);
     note_launch();
     return cuda_check(cudaGetLastError(), "norm launch");
+}
+
+template <typename T> exl3_status norm_t(const NormLaunch &p, int vec, const Shape &f, cudaStream_t s) {
+    return vec == kWide ? norm_v<T, kWide>(p, f, s) : vec == kPairs ? norm_v<T, kPairs>(p, f, s) : norm_v<T, kSingle>(p, f, s);
 }
 
 // Warps of an SM (half of them with two units each, which take 117 registers), and how many
@@ -803,7 +832,7 @@ unsigned grad_grid(int64_t T, const GradShape &f) {
 }
 bool ring_size(int64_t n) { return n >= kRingFrom && n <= kRingTo && n % 8 == 0; }
 
-template <typename T, bool VEC, int VPT, bool RING> exl3_status norm_grad_k(const NormGradLaunch &p, const GradShape &f, cudaStream_t s) {
+template <typename T, int VEC, int VPT, bool RING> exl3_status norm_grad_k(const NormGradLaunch &p, const GradShape &f, cudaStream_t s) {
     const unsigned block = (unsigned)(f.rows * f.wr * 32), grid = grad_grid(p.T, f);
     const size_t smem = RING ? (size_t)f.depth * (p.dh ? 3 : 2) * f.rows * p.n * 2
                              : VPT > 2 && p.dweight ? (size_t)VPT * 8 * block * sizeof(float) : 0;
@@ -817,17 +846,22 @@ template <typename T, bool VEC, int VPT, bool RING> exl3_status norm_grad_k(cons
     note_launch();
     return cuda_check(cudaGetLastError(), "norm gradient launch");
 }
-template <typename T> exl3_status norm_grad_t(const NormGradLaunch &p, bool vec, cudaStream_t s) {
-    const GradShape r = grad_shape(p.n, vec && ring_size(p.n), p.dh != nullptr);
+template <typename T, int VEC> exl3_status norm_grad_v(const NormGradLaunch &p, const GradShape &f, cudaStream_t s) {
+    return f.vpt == 1   ? norm_grad_k<T, VEC, 1, false>(p, f, s)
+           : f.vpt == 2 ? norm_grad_k<T, VEC, 2, false>(p, f, s)
+                        : norm_grad_k<T, VEC, 4, false>(p, f, s);
+}
+template <typename T> exl3_status norm_grad_t(const NormGradLaunch &p, int vec, cudaStream_t s) {
+    const GradShape r = grad_shape(p.n, vec == kWide && ring_size(p.n), p.dh != nullptr);
     const GradShape f = r.depth >= 2 ? r : grad_shape(p.n, false, false);
     if (p.T) {
         exl3_status st;
         if (f.depth)
-            st = f.vpt == 1 ? norm_grad_k<T, true, 1, true>(p, f, s) : norm_grad_k<T, true, 2, true>(p, f, s);
-        else if (vec)
-            st = f.vpt == 1 ? norm_grad_k<T, true, 1, false>(p, f, s) : f.vpt == 2 ? norm_grad_k<T, true, 2, false>(p, f, s) : norm_grad_k<T, true, 4, false>(p, f, s);
+            st = f.vpt == 1 ? norm_grad_k<T, kWide, 1, true>(p, f, s) : norm_grad_k<T, kWide, 2, true>(p, f, s);
         else
-            st = f.vpt == 1 ? norm_grad_k<T, false, 1, false>(p, f, s) : f.vpt == 2 ? norm_grad_k<T, false, 2, false>(p, f, s) : norm_grad_k<T, false, 4, false>(p, f, s);
+            st = vec == kWide    ? norm_grad_v<T, kWide>(p, f, s)
+                 : vec == kPairs ? norm_grad_v<T, kPairs>(p, f, s)
+                                 : norm_grad_v<T, kSingle>(p, f, s);
         if (st != EXL3_OK)
             return st;
     }
@@ -851,20 +885,22 @@ template <typename T> exl3_status norm_grad_t(const NormGradLaunch &p, bool vec,
 }
 
 template <typename T> exl3_status quantize8_t(const Quantize8Launch &p, cudaStream_t s) {
-    const bool vec = wide_rows(p.x, p.stride, sizeof(T)) && p.n % 8 == 0 && ((uintptr_t)p.codes & 7u) == 0;
+    const int vec = access_of(p.codes, p.n, 1, p.n, access_of(p.x, p.stride, sizeof(T), p.n, kWide));
     if (p.block_rows == 1) {
         const int64_t units = p.T * ((p.n + kUnitN - 1) / kUnitN);
         const unsigned grid = (unsigned)((units + 8 * kUnitsWarp - 1) / (8 * kUnitsWarp));
-        if (vec)
-            rows8_kernel<T, true><<<grid, 256, 0, s>>>(p);
+        if (vec == kWide)
+            rows8_kernel<T, kWide><<<grid, 256, 0, s>>>(p);
+        else if (vec == kPairs)
+            rows8_kernel<T, kPairs><<<grid, 256, 0, s>>>(p);
         else
-            rows8_kernel<T, false><<<grid, 256, 0, s>>>(p);
+            rows8_kernel<T, kSingle><<<grid, 256, 0, s>>>(p);
     } else {
         const unsigned grid = (unsigned)((p.n + 127) / 128 * ((p.T + 127) / 128));
-        if (vec)
-            blocks8_kernel<T, true><<<grid, 256, 0, s>>>(p);
+        if (vec == kWide)
+            blocks8_kernel<T, kWide><<<grid, 256, 0, s>>>(p);
         else
-            blocks8_kernel<T, false><<<grid, 256, 0, s>>>(p);
+            blocks8_kernel<T, kSingle><<<grid, 256, 0, s>>>(p);
     }
     note_launch();
     return cuda_check(cudaGetLastError(), "8-bit blocks launch");
@@ -875,14 +911,12 @@ template <typename T> exl3_status quantize8_t(const Quantize8Launch &p, cudaStre
 exl3_status launch_norm(const NormLaunch &p, cudaStream_t s) {
     if (p.T == 0)
         return EXL3_OK;
-    const int wsize = p.w_dt == EXL3_F32 ? 4 : 2;
-    const bool vec = p.n % 8 == 0 && wide_rows(p.x, p.x_stride, 2) && wide_rows(p.weight, p.n, wsize) &&
-                     (!p.residual || (wide_rows(p.residual, p.r_stride, 2) && wide_rows(p.h, p.h_stride, 2))) &&
-                     (!p.y || wide_rows(p.y, p.y_stride, 2)) && (!p.y8 || ((uintptr_t)p.y8 & 7u) == 0);
+    int vec = access_of(p.weight, p.n, p.w_dt == EXL3_F32 ? 4 : 2, p.n, access_of(p.x, p.x_stride, 2, p.n, kWide));
+    if (p.residual)
+        vec = access_of(p.h, p.h_stride, 2, p.n, access_of(p.residual, p.r_stride, 2, p.n, vec));
+    vec = access_of(p.y8, p.n, 1, p.n, access_of(p.y, p.y_stride, 2, p.n, vec));
     const Shape f = norm_shape(p.T, p.n, p.T > 2 * (int64_t)device_sm_count());
-    if (p.dt == EXL3_BF16)
-        return vec ? norm_v<__nv_bfloat16, true>(p, f, s) : norm_v<__nv_bfloat16, false>(p, f, s);
-    return vec ? norm_v<__half, true>(p, f, s) : norm_v<__half, false>(p, f, s);
+    return p.dt == EXL3_BF16 ? norm_t<__nv_bfloat16>(p, vec, f, s) : norm_t<__half>(p, vec, f, s);
 }
 
 int64_t norm_grad_parts(int64_t T, int64_t n) {
@@ -908,10 +942,9 @@ exl3_status norm_take_wait_timeouts(unsigned int *n) {
 }
 
 exl3_status launch_norm_grad(const NormGradLaunch &p, cudaStream_t s) {
-    const int wsize = p.w_dt == EXL3_F32 ? 4 : 2;
-    const bool vec = p.n % 8 == 0 && wide_rows(p.dy, p.dy_stride, 2) && wide_rows(p.h, p.h_stride, 2) &&
-                     wide_rows(p.weight, p.n, wsize) && (!p.dh || wide_rows(p.dh, p.dh_stride, 2)) &&
-                     wide_rows(p.dx, p.dx_stride, 2);
+    int vec = access_of(p.dy, p.dy_stride, 2, p.n, access_of(p.h, p.h_stride, 2, p.n, kWide));
+    vec = access_of(p.weight, p.n, p.w_dt == EXL3_F32 ? 4 : 2, p.n, vec);
+    vec = access_of(p.dh, p.dh_stride, 2, p.n, access_of(p.dx, p.dx_stride, 2, p.n, vec));
     return p.dt == EXL3_BF16 ? norm_grad_t<__nv_bfloat16>(p, vec, s) : norm_grad_t<__half>(p, vec, s);
 }
 
