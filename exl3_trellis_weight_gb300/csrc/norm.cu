@@ -774,14 +774,18 @@ struct Shape {
     int vpt, wr, rows;        // units of a warp, warps of a row, rows of a block
 };
 
-// Few rows: one unit a warp, for the shortest way through a row.  Many: eight warps to a
-// row, whose barriers cost less and whose loads are longer.
-Shape norm_shape(int64_t T, int64_t n, bool many) {
-    const int units = (int)((n + kUnitN - 1) / kUnitN), most = many ? 8 : 32;
+// As many units a warp, up to four, as leave 16 warps to an SM: its loads are longer and a row
+// meets in fewer warps.  (16384 x 4096 with four, two and one units a warp: 83, 90 and
+// 104 us; 16384 x 1024 with four and one: 27 and 39; 333 x 4096 with four and two: 7.2 and 6.2.)
+Shape norm_shape(int64_t T, int64_t n) {
+    const int units = (int)((n + kUnitN - 1) / kUnitN);
+    const int64_t sms = device_sm_count();
     Shape f;
-    f.vpt = units <= most ? 1 : units <= 2 * most ? 2 : 4;
+    f.vpt = 1;
+    while (f.vpt < 4 && (units > 32 * f.vpt || (units > f.vpt && T * ((units + 2 * f.vpt - 1) / (2 * f.vpt)) >= 16 * sms)))
+        f.vpt *= 2;
     f.wr = (units + f.vpt - 1) / f.vpt;
-    f.rows = many && f.wr < 8 ? 8 / f.wr : 1;
+    f.rows = T > 2 * sms && f.wr < 8 ? 8 / f.wr : 1;
     return f;
 }
 
@@ -915,7 +919,7 @@ exl3_status launch_norm(const NormLaunch &p, cudaStream_t s) {
     if (p.residual)
         vec = access_of(p.h, p.h_stride, 2, p.n, access_of(p.residual, p.r_stride, 2, p.n, vec));
     vec = access_of(p.y8, p.n, 1, p.n, access_of(p.y, p.y_stride, 2, p.n, vec));
-    const Shape f = norm_shape(p.T, p.n, p.T > 2 * (int64_t)device_sm_count());
+    const Shape f = norm_shape(p.T, p.n);
     return p.dt == EXL3_BF16 ? norm_t<__nv_bfloat16>(p, vec, f, s) : norm_t<__half>(p, vec, f, s);
 }
 
