@@ -354,13 +354,15 @@ template <typename T> __device__ __forceinline__ void unpack_pairs(const Eight &
 // keeps its columns' part of dweight, in registers up to two units and in shared memory
 // beyond, where registers run out.
 // RING: whole rows are copied into stages of shared memory, `depth` of them ahead.  (One row
-// ahead in registers were 48 KB to an SM on their way: 8192 x 4096 took 66 us, 4.1 TB/s.)
+// ahead in registers were 48 KB to an SM on their way: 8192 x 4096 took 66 us, 4.1 TB/s; now
+// 53, 5.1 TB/s, and 5 for the sum of dweight's parts, whose launch overlaps.  What is left
+// are the two meetings of a row's warps and 2.3 of 4 instructions a cycle.)
 // WAY: the next row is asked for into registers.
 __device__ unsigned int g_norm_timeouts;
 constexpr int kMaxDepth = 8;
 
 template <typename T, int VEC, int VPT, bool WAY, bool RING>
-__global__ void __launch_bounds__(RING ? 512 : 1024) norm_grad_kernel(const NormGradLaunch a, int wr, int depth) {
+__global__ void __launch_bounds__(RING ? 512 : 1024, RING && VPT == 1 ? 2 : 1) norm_grad_kernel(const NormGradLaunch a, int wr, int depth) {
     constexpr bool kRegs = VPT <= 2;
     __shared__ float2 place[2][32];
     __shared__ __align__(8) unsigned long long bars[RING ? kMaxDepth : 1];
@@ -480,22 +482,25 @@ __global__ void __launch_bounds__(RING ? 512 : 1024) norm_grad_kernel(const Norm
             for (int j = 0; j < 4; j++)
                 u.gw[j] = mul2(u.g[j], {w[2 * j], w[2 * j + 1]});
         };
-        auto down = [&](Unit &u) {
+        auto down = [&](Unit &u, float fh, float fg) {
 #pragma unroll
             for (int j = 0; j < 4; j++) {
-                u.v[j] = mul2(u.v[j], {dh, dh});
-                u.gw[j] = mul2(u.gw[j], {dg, dg});
+                u.v[j] = mul2(u.v[j], {fh, fh});
+                u.gw[j] = mul2(u.gw[j], {fg, fg});
             }
         };
-        auto sums = [&](bool first) {
+        // (of h times fh and dy weight times fg, beside what they have been multiplied by before)
+        auto sums = [&](bool first, float fh, float fg) {
             Pair h2 = {0.0f, 0.0f}, g2 = {0.0f, 0.0f};
+            dh = __fmul_rn(dh, fh);
+            dg = __fmul_rn(dg, fg);
 #pragma unroll
             for (int k = 0; k < VPT; k++) {
                 Unit &u = stay[kStay ? k : 0];
                 if (first || !kStay)
                     unit(k, u);
                 if (!first)
-                    down(u);
+                    down(u, kStay ? fh : dh, kStay ? fg : dg);
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
                     h2 = fma2(u.v[j], u.v[j], h2);
@@ -505,7 +510,7 @@ __global__ void __launch_bounds__(RING ? 512 : 1024) norm_grad_kernel(const Norm
             hh = warp_sum(__fadd_rn(h2.x, h2.y));
             gh = warp_sum(__fadd_rn(g2.x, g2.y));
         };
-        sums(true);
+        sums(true, 1.0f, 1.0f);
         if (wr > 1) {
             // (two places in turn: a row's reads are done before the barrier of the next)
             if (lane == 0)
@@ -522,23 +527,28 @@ __global__ void __launch_bounds__(RING ? 512 : 1024) norm_grad_kernel(const Norm
             gh = warp_sum(q.y);
         }
         if (in) {
-            // beyond binary32's range: h and dy weight times powers of two, each as it needs
+            // beyond binary32's range: h, and then dy weight if that was not enough, times powers of
+            // two (each at once as well, the products of small dy with large h were lost below)
             float back = 1.0f;
             if (passed(hh) || passed(fabsf(gh))) {
-                dh = passed(hh) ? kDown : 1.0f;
-                dg = passed(fabsf(gh)) ? kDownG : 1.0f;
+#pragma unroll 1
+                for (int again = 0; again < 2; again++) {
+                    const bool of_h = dh == 1.0f && passed(hh), of_g = dg == 1.0f && passed(fabsf(gh));
+                    if (!of_h && !of_g)
+                        break;
+                    sums(false, of_h ? kDown : 1.0f, of_h ? 1.0f : kDownG);
+                    if (wr > 1) {
+                        row_barrier(sub, wr);  // the sums before are read
+                        if (lane == 0)
+                            place[turn][warp] = make_float2(hh, gh);
+                        row_barrier(sub, wr);
+                        const float2 q = lane < wr ? place[turn][sub * wr + lane] : make_float2(0.0f, 0.0f);
+                        hh = warp_sum(q.x);
+                        gh = warp_sum(q.y);
+                    }
+                }
                 back = __fdiv_rn(dh, dg);
                 eps = __fmul_rn(__fmul_rn(a.eps, dh), dh);
-                sums(false);
-                if (wr > 1) {
-                    row_barrier(sub, wr);  // the first sums are read
-                    if (lane == 0)
-                        place[turn][warp] = make_float2(hh, gh);
-                    row_barrier(sub, wr);
-                    const float2 q = lane < wr ? place[turn][sub * wr + lane] : make_float2(0.0f, 0.0f);
-                    hh = warp_sum(q.x);
-                    gh = warp_sum(q.y);
-                }
             }
             // with h' = h dh, g' = dy weight dg, s' = s / dh:  dx = s' dh / dg (g' - h' s'^2 sum(g' h') / n)
             const float s = __frsqrt_rn(__fmaf_rn(hh, inv_n, eps));
@@ -548,8 +558,8 @@ __global__ void __launch_bounds__(RING ? 512 : 1024) norm_grad_kernel(const Norm
                 Unit &u = stay[kStay ? k : 0];
                 if (!kStay) {
                     unit(k, u);
-                    if (back != 1.0f || dh != 1.0f)
-                        down(u);
+                    if (dh != 1.0f || dg != 1.0f)
+                        down(u, dh, dg);
                 }
                 if (want) {
 #pragma unroll
@@ -817,7 +827,8 @@ struct GradShape : Shape {
 GradShape grad_shape(int64_t n, bool ring, bool with_dh) {
     const int units = (int)((n + kUnitN - 1) / kUnitN);
     GradShape f;
-    f.vpt = units <= 16 ? 1 : units <= 64 ? 2 : 4;
+    // (ring, 16384 x 4096: two units a warp 98 us, one 110; 1000 x 1024: 16.4 and 14.7)
+    f.vpt = ring ? (units <= 8 ? 1 : 2) : units <= 16 ? 1 : units <= 64 ? 2 : 4;
     f.wr = (units + f.vpt - 1) / f.vpt;
     f.rows = f.wr < 8 ? 8 / f.wr : 1;
     f.per_sm = (ring && f.vpt == 2 ? kGradWarps / 2 : kGradWarps) / (f.rows * f.wr);

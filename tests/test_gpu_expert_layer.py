@@ -142,6 +142,21 @@ def test_many_experts_and_picks(ex, T, dt):
     within(m.run(ex, x, 3, router=router, normalize=False), expected(m, x, *picks(x, router, 3, False), dt))
 
 
+def test_a_thousand_experts(ex):
+    g = gen(12)
+    m = Experts(g, 1024, 128, 128, 1, 1, False)
+    for T, top_k in ((2, 3), (40, 1)):
+        x, router = acts(g, T, 128, "bf16"), a_router(g, 1024, 128, torch.bfloat16)
+        within(m.run(ex, x, top_k, router=router), expected(m, x, *picks(x, router, top_k), "bf16"))
+    ids = torch.randint(0, 1024, (256, 16), generator=g, device=DEV, dtype=torch.int32)
+    w = torch.rand(256, 16, generator=g, device=DEV)
+    x = acts(g, 256, 128, "bf16")
+    y = m.run(ex, x, 16, ids=ids, weights=w)
+    part = m.run(ex, x[100:103], 16, ids=ids[100:103].contiguous(), weights=w[100:103].contiguous())
+    within(part, expected(m, x[100:103], ids[100:103], w[100:103], "bf16"))
+    assert float((y[100:103].float() - part.float()).norm()) <= 2.0 ** -7 * float(part.float().norm())
+
+
 @pytest.mark.parametrize("H,F,tr", [(17408, 128, False), (128, 16512, True), (4096, 1152, True)])
 def test_long_sides(ex, H, F, tr):
     g = gen(H)

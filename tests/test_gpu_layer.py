@@ -209,6 +209,28 @@ def test_norm_gradient(ex, T, n, dt, with_dh, wide, w32):
             assert torch.equal(over, got["dx"]) and torch.equal(r["dweight"], got["dweight"])
 
 
+@pytest.mark.parametrize("n", [300, 1001, 2048, 9000, 20000])
+def test_norm_gradient_of_large_rows(ex, n):
+    """Sums of squares and of products beyond binary32's range, one of them and both, among
+    ordinary rows: each row as exact as another."""
+    g = gen(n)
+    T = 9
+    h, dy = torch.randn(T, n, generator=g, device=DEV), torch.randn(T, n, generator=g, device=DEV)
+    h *= torch.tensor([1, 1e19, 1, 1e19, 1e-3, 1e30, 1e25, 1, 3e37], device=DEV)[:, None]
+    dy *= torch.tensor([1, 1, 1e36, 1e30, 1, 1e-10, 1e25, 1e20, 1], device=DEV)[:, None]
+    h, dy = h.bfloat16(), dy.bfloat16()
+    w = 0.5 + torch.rand(n, generator=g, device=DEV)
+    got = ex.rms_norm_backward(dy, h, w, 1e-6)
+    h64, g64 = h.double(), dy.double() * w.double()
+    _, s = norm64(h, w, 1e-6)
+    m = (g64 * h64).mean(1, keepdim=True)
+    dx = s * g64 - h64 * s.pow(3) * m
+    size = (s * g64).abs() + h64.abs() * s.pow(3) * (g64 * h64).abs().mean(1, keepdim=True)
+    within(got["dx"], dx, U["bf16"] * dx.abs() + 161 * F * size + 2.0 ** -133)
+    terms = dy.double() * h64 * s
+    within(got["dweight"], terms.sum(0), (61 + T / 16) * F * terms.abs().sum(0))
+
+
 def test_norm_gradient_against_differences(ex):
     """Along a direction: (f(h + d) - f(h - d)) / 2 in 64 bits of f = sum(dy . y); with d = 1e-4 of
     a unit row its own error is below 1e-7 of f's third derivatives, of the order of |dy| / rms^3."""
@@ -276,6 +298,30 @@ def test_blocks_bit_for_bit(ex, block, dt, T, n, wide):
     q = (b * inv[:, None, :, None]).clamp(-448, 448).view(R * block, N * 128)[:T, :n].to(E4M3)
     assert torch.equal(scale.cpu(), m / torch.full_like(m, 448.0))
     assert torch.equal(codes.cpu().view(torch.uint8), q.view(torch.uint8))
+
+
+@pytest.mark.parametrize("T,n", [(1, 2), (3, 130), (340, 1002), (5, 4100), (700, 2050), (310, 9010), (2, 20006)])
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_even_sizes(ex, T, n, dt):
+    """Rows of whole pairs that are no multiples of 16 bytes; the same from and into columns at even and
+    odd places of a wider buffer."""
+    test_norm(ex, T, n, dt, True, False, True)
+    test_norm(ex, T, n, dt, False, False, False)
+    test_norm_gradient(ex, T, n, dt, True, False, True)
+    test_norm_gradient(ex, T, n, dt, False, False, False)
+    for block in (1, 128):
+        test_blocks_bit_for_bit(ex, block, dt, T, n, False)
+    test_blocks_bit_for_bit(ex, 1, "fp32", T, n, False)
+    g = gen(n)
+    x, w = acts(g, T, n, dt), torch.rand(n, generator=g, device=DEV).to(DT[dt])
+    y, _ = norm64(x, w, 1e-6)
+    for at in (0, 1, 2, 8):
+        buf, out = (torch.full((T, n + 12), 3.0, dtype=DT[dt], device=DEV) for _ in range(2))
+        buf[:, at:at + n] = x
+        got = ex.rms_norm(buf[:, at:at + n], w, 1e-6, out=out[:, at:at + n], want_y8=True)
+        within(out[:, at:at + n], y, (U[dt] * (1 + 64 * F) + 32 * F) * y.abs() + TINY[dt])
+        assert bool((out[:, :at] == 3).all()) and bool((out[:, at + n:] == 3).all())
+        check_blocks(got["y8"], got["scale"], y, 32 * F)
 
 
 def weights8(g, rows, cols):

@@ -1,0 +1,122 @@
+"""The device that norms, 8-bit blocks and products and expert layers launch on (not gpu): that
+of their tensors, whichever one is current, and what a call refuses because it would lose a
+gradient.  The stand-ins are those of the coded products' test."""
+import contextlib
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from test_linear_device_host import Elsewhere, Library, Placed, placed  # noqa: E402
+
+BF16, E4M3 = torch.bfloat16, torch.float8_e4m3fn
+
+
+@pytest.fixture
+def layer(monkeypatch):
+    from exl3_trellis_weight_gb300 import layer, products
+    devices = [0]
+
+    @contextlib.contextmanager
+    def device(index):
+        devices.append(index if isinstance(index, int) else index.index)
+        yield
+        devices.pop()
+
+    def new(shape, stride, dtype, dev):
+        return torch.empty_strided(shape, stride, dtype=dtype).as_subclass(Placed if dev.index == 1 else Elsewhere)
+
+    monkeypatch.setattr(products, "_fn", Library(devices))
+    monkeypatch.setattr(products, "_current_device", lambda: devices[-1], raising=False)
+    for module in (products, layer):
+        monkeypatch.setattr(module, "_stream", lambda index: 1000 + index)
+    monkeypatch.setattr(layer, "_new", new)
+    monkeypatch.setattr(torch.cuda, "device", device)
+    layer.seen, layer.devices = products._fn.seen, devices
+    return layer
+
+
+def tensors(cls):
+    def t(*s, dtype=torch.float32):
+        return placed(*s, dtype=dtype, cls=cls)
+    up = t(3, 16, 8, 32, dtype=torch.int16), t(3, 256), t(3, 128), t(3)
+    down = t(3, 8, 16, 32, dtype=torch.int16), t(3, 128), t(3, 256), t(3)
+    return dict(x=t(2, 256, dtype=BF16), r=t(2, 256, dtype=BF16), w=t(256), w8=t(256, 128, dtype=E4M3), s8=t(2, 1), x8=t(2, 256, dtype=E4M3),
+                xs=t(2, 2), up=up, down=down, router=t(3, 256), ids=t(2, 1, dtype=torch.int32), pw=t(2, 1), ws=t(256, dtype=torch.uint8))
+
+
+def calls(m, v):
+    return {"rms_norm": lambda: m.rms_norm(v["x"], v["w"], residual=v["r"], want_y8=True),
+            "rms_norm_backward": lambda: m.rms_norm_backward(v["x"], v["r"], v["w"], ws=v["ws"]),
+            "quantize8": lambda: m.quantize8(v["x"]),
+            "linear8": lambda: m.linear8(v["x"], v["w8"], v["s8"], ws=v["ws"]),
+            "expert_layer": lambda: m.expert_layer(v["x"], v["up"], v["up"], v["down"], 2, 1, router=v["router"], ws=v["ws"])}
+
+
+@pytest.mark.parametrize("name", ["rms_norm", "rms_norm_backward", "quantize8", "linear8", "expert_layer"])
+def test_launches_on_the_device_of_the_tensors(layer, name):
+    for cls in (Placed, Elsewhere):
+        calls(layer, tensors(cls))[name]()
+        assert layer.seen == [("exl3_" + name, cls.where, 1000 + cls.where)]
+        assert layer.devices == [0]
+        layer.seen.clear()
+
+
+@pytest.mark.parametrize("name,key", [("rms_norm", "w"), ("rms_norm", "r"), ("rms_norm_backward", "r"), ("rms_norm_backward", "w"),
+                                      ("rms_norm_backward", "ws"), ("linear8", "w8"), ("linear8", "s8"), ("linear8", "ws"), ("expert_layer", "up"),
+                                      ("expert_layer", "down"), ("expert_layer", "router"), ("expert_layer", "ws"), ("expert_layer", "x")])
+def test_refuses_tensors_of_several_devices(layer, name, key):
+    v = tensors(Placed)
+    v[key] = tensors(Elsewhere)[key]
+    with pytest.raises(ValueError):
+        calls(layer, v)[name]()
+    assert not layer.seen
+
+
+def test_refuses_what_would_lose_a_gradient(layer):
+    v = tensors(Placed)
+
+    def wants(t):
+        return t.detach().clone().as_subclass(Placed).requires_grad_()
+
+    def norm(**kw):
+        return layer.rms_norm(**{**dict(x=v["x"], weight=v["w"], residual=v["r"]), **kw})
+
+    def product(**kw):
+        return layer.linear8(**{**dict(x=v["x"], w=v["w8"], w_scale=v["s8"], ws=v["ws"]), **kw})
+
+    def experts(**kw):
+        return layer.expert_layer(**{**dict(x=v["x"], gate=v["up"], up=v["up"], down=v["down"], K=2, top_k=1, router=v["router"], ws=v["ws"]), **kw})
+
+    def with_part(i):
+        return tuple(wants(t) if j == i else t for j, t in enumerate(v["up"]))
+
+    y = placed(2, 256, dtype=BF16)
+    given = dict(router=None, ids=v["ids"])
+    for call, bad in ((norm, dict(x=wants(v["x"]), want_y8=True)), (norm, dict(weight=wants(v["w"]), out=y)), (norm, dict(residual=wants(v["r"]), h=y)),
+                      (product, dict(w_scale=wants(v["s8"]))), (product, dict(x=wants(v["x"]), out=placed(2, 128, dtype=BF16))),
+                      (product, dict(x=v["x8"], x_scale=wants(v["xs"]))),
+                      (experts, dict(x=wants(v["x"]))), (experts, dict(router=wants(v["router"]))), (experts, dict(given, weights=wants(v["pw"]))),
+                      (experts, dict(gate=with_part(1))), (experts, dict(up=with_part(2))), (experts, dict(gate=with_part(3)))):
+        with pytest.raises(ValueError, match="gradient"):
+            call(**bad)
+        assert not layer.seen
+        with torch.no_grad():
+            call(**bad)
+        assert len(layer.seen) == 1
+        layer.seen.clear()
+
+
+def test_an_expert_scale_may_be_a_number(layer):
+    v = tensors(Placed)
+    new = torch.full
+
+    def full(shape, value, dtype, device):
+        return new(shape, value, dtype=dtype).as_subclass(Placed)
+
+    layer.torch.full, keep = full, layer.torch.full
+    try:
+        layer.expert_layer(v["x"], (*v["up"][:3], 0.5), v["up"], v["down"], 2, 1, router=v["router"], ws=v["ws"])
+    finally:
+        layer.torch.full = keep
+    assert len(layer.seen) == 1
