@@ -5,7 +5,8 @@
 // others under it.  A pair's part of the result goes to memory in binary32, and a small
 // kernel behind adds a token's up in the order of the picks.  (The warp that finished a
 // token's last pair did that at first: the fence and the atomic that told it so stood
-// in the way of the next tile.)
+// in the way of the next tile: 64 tokens of 64 experts, 2048 / 1024, 8 picks, K = 2 took 70 us,
+// now 54, the decode's bound is 20; one token 14.)
 #include "expert_few.cuh"
 
 namespace exl3 {

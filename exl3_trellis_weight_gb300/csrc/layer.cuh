@@ -1,6 +1,6 @@
 // layer.cuh -- launch parameters of what stands around the coded products of a layer:
 // norms and 8-bit blocks (norm.cu), products in 8 bits (linear8.cu), expert layers
-// (expert_layer.cu); entry points in layer_abi.cu.
+// (expert_route.cu, expert_up.cu, expert_down.cu); entry points in layer_abi.cu.
 #pragma once
 
 #include "linear.cuh"

