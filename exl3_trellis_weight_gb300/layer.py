@@ -22,14 +22,16 @@ _E4M3 = torch.float8_e4m3fn
 _strided = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
 
 
-def _new(shape, stride, dtype, dev):
-    if _strided is not None and _current_device() == dev.index:
-        return _strided(shape, stride, dtype)
-    return torch.empty_strided(shape, stride, dtype=dtype, device=dev)
+def _maker(index):
+    """make(shape, stride, dtype) -> an uninitialised tensor on CUDA device `index`."""
+    if _strided is not None and _current_device() == index:
+        return _strided
+    dev = torch.device("cuda", index) if index >= 0 else torch.device("cpu")
+    return lambda shape, stride, dtype: torch.empty_strided(shape, stride, dtype=dtype, device=dev)
 
 
-def _ws(need, dev, ws):
-    return _new((max(need, 256),), (1,), torch.uint8, dev) if ws is None else _given_ws(need, dev, ws)
+def _ws(need, dev, ws, make):
+    return make((need if need > 256 else 256,), (1,), torch.uint8) if ws is None else _given_ws(need, dev, ws)
 
 
 def rms_norm_backward_workspace_bytes(T: int, n: int) -> int:
@@ -59,6 +61,13 @@ def _matrix(t, name, dtypes, columns=None, like=None):
     if column != 1 and shape[0] and shape[1] > 1:
         raise ValueError(f"{name}'s columns must be contiguous")
     return row if shape[0] > 1 else shape[1]
+
+
+def _like(t, name, shape, x, index):
+    """Row stride of a tensor that has x's type, shape and device."""
+    if t.dtype is x.dtype and t.shape == shape and t.is_contiguous() and t.get_device() == index:
+        return shape[1]
+    return _matrix(t, name, _DT, shape[1], like=x)
 
 
 def _norm_weight(weight, n, x):
@@ -103,12 +112,12 @@ def rms_norm(x, weight, eps: float = 1e-6, residual=None, want_y: bool = True, w
     takes); None otherwise.  h may be given as an output (x or residual itself, too),
     ``out`` for y.  x, residual and weight get their gradients through y and h."""
     xs = _matrix(x, "x", _DT)
-    T, n = x.shape
-    dev = x.device
+    shape, index = x.shape, x.get_device()
+    T, n = shape
     pw, wdt = _norm_weight(weight, n, x)
     rs = hs = ys = n
     if residual is not None:
-        rs = _matrix(residual, "residual", _DT, n, like=x)
+        rs = _like(residual, "residual", shape, x, index)
     elif h is not None:
         raise ValueError("h needs a residual (without one it is x)")
     if not (want_y or want_y8):
@@ -123,25 +132,28 @@ def rms_norm(x, weight, eps: float = 1e-6, residual=None, want_y: bool = True, w
         r = _RmsNorm.apply(x, weight, residual, eps)
         y, h = (r, None) if residual is None else r
         return dict(h=h, y=y, y8=None, scale=None)
+    make = _maker(index)
     if residual is not None:
         if h is None:
-            h = _new((T, n), (n, 1), x.dtype, dev)
+            h = make((T, n), (n, 1), x.dtype)
         else:
-            hs = _matrix(h, "h", _DT, n, like=x)
-    y = y8 = scale = None
+            hs = _like(h, "h", shape, x, index)
+    y = y8 = scale = ph = py = pq = ps = None
     if want_y:
         if out is None:
-            y = _new((T, n), (n, 1), x.dtype, dev)
+            y = make((T, n), (n, 1), x.dtype)
         else:
             y = out
-            ys = _matrix(out, "out", _DT, n, like=x)
+            ys = _like(out, "out", shape, x, index)
+        py = y.data_ptr()
     if want_y8:
-        y8 = _new((T, n), (n, 1), _E4M3, dev)
-        scale = _new((T, (n + 127) // 128), (1, T), torch.float32, dev)
-    _call(_lib().exl3_rms_norm, dev.index, x.data_ptr(), _DT[x.dtype], T, n, xs,
-          None if residual is None else residual.data_ptr(), rs, pw, wdt, eps, None if h is None else h.data_ptr(), hs,
-          y.data_ptr() if want_y else None, ys, y8.data_ptr() if want_y8 else None,
-          scale.data_ptr() if want_y8 else None, _stream(dev.index))
+        y8 = make((T, n), (n, 1), _E4M3)
+        scale = make((T, (n + 127) // 128), (1, T), torch.float32)
+        pq, ps = y8.data_ptr(), scale.data_ptr()
+    if h is not None:
+        ph = h.data_ptr()
+    _call(_lib().exl3_rms_norm, index, x.data_ptr(), _DT[x.dtype], T, n, xs, None if residual is None else residual.data_ptr(),
+          rs, pw, wdt, eps, ph, hs, py, ys, pq, ps, _stream(index))
     return dict(h=h, y=y, y8=y8, scale=scale)
 
 
@@ -152,27 +164,27 @@ def rms_norm_backward(dy, h, weight, eps: float = 1e-6, dh=None, want_dweight: b
     itself may be given for it), dweight has weight's dtype (None without
     ``want_dweight``)."""
     gs = _matrix(dy, "dy", _DT)
-    T, n = dy.shape
-    dev = dy.device
-    hs = _matrix(h, "h", _DT, n, like=dy)
+    shape, index = dy.shape, dy.get_device()
+    T, n = shape
+    hs = _like(h, "h", shape, dy, index)
     pw, wdt = _norm_weight(weight, n, dy)
     ds = xs = n
     if dh is not None:
-        ds = _matrix(dh, "dh", _DT, n, like=dy)
+        ds = _like(dh, "dh", shape, dy, index)
+    make = _maker(index)
     if dx is None:
-        dx = _new((T, n), (n, 1), dy.dtype, dev)
+        dx = make((T, n), (n, 1), dy.dtype)
     else:
-        xs = _matrix(dx, "dx", _DT, n, like=dy)
+        xs = _like(dx, "dx", shape, dy, index)
     L = _lib()
-    dw = pws = None
+    dw = pd = pws = None
     bytes_ = 0
     if want_dweight:
-        dw = _new((n,), (1,), weight.dtype, dev)
-        ws = _ws(L.exl3_rms_norm_backward_workspace_bytes(T, n), dev, ws)
-        pws, bytes_ = ws.data_ptr(), ws.numel() * ws.element_size()
-    _call(L.exl3_rms_norm_backward, dev.index, dy.data_ptr(), gs, h.data_ptr(), hs, _DT[dy.dtype], T, n, pw, wdt, eps,
-          None if dh is None else dh.data_ptr(), ds, dx.data_ptr(), xs, None if dw is None else dw.data_ptr(), pws, bytes_,
-          _stream(dev.index))
+        dw = make((n,), (1,), weight.dtype)
+        ws = _ws(L.exl3_rms_norm_backward_workspace_bytes(T, n), dy.device, ws, make)
+        pd, pws, bytes_ = dw.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size()
+    _call(L.exl3_rms_norm_backward, index, dy.data_ptr(), gs, h.data_ptr(), hs, _DT[dy.dtype], T, n, pw, wdt, eps,
+          None if dh is None else dh.data_ptr(), ds, dx.data_ptr(), xs, pd, pws, bytes_, _stream(index))
     return dict(dx=dx, dweight=dw)
 
 
@@ -183,15 +195,16 @@ def quantize8(x, block_rows: int = 1):
     [T, ceil(n / 128)]; 128, for weights: [ceil(T / 128), ceil(n / 128)]."""
     xs = _matrix(x, "x", _DT_X)
     T, n = x.shape
-    dev = x.device
-    codes = _new((T, n), (n, 1), _E4M3, dev)
+    index = x.get_device()
+    make = _maker(index)
+    codes = make((T, n), (n, 1), _E4M3)
     nb = (n + 127) // 128
     if block_rows == 1:
-        scale = _new((T, nb), (1, T), torch.float32, dev)
+        scale = make((T, nb), (1, T), torch.float32)
     else:
-        scale = _new(((T + 127) // 128, nb), (nb, 1), torch.float32, dev)
-    _call(_lib().exl3_quantize8, dev.index, x.data_ptr(), _DT_X[x.dtype], T, n, xs, block_rows, codes.data_ptr(),
-          scale.data_ptr(), _stream(dev.index))
+        scale = make(((T + 127) // 128, nb), (nb, 1), torch.float32)
+    _call(_lib().exl3_quantize8, index, x.data_ptr(), _DT_X[x.dtype], T, n, xs, block_rows, codes.data_ptr(),
+          scale.data_ptr(), _stream(index))
     return codes, scale
 
 
@@ -226,8 +239,7 @@ def linear8(x, w, w_scale, x_scale=None, transposed: bool = False, dtype=None, o
         raise ValueError(f"w must be [rows, cols], got {tuple(w.shape)}")
     rows, cols = w.shape
     n_in, n_out = (cols, rows) if transposed else (rows, cols)
-    dev = x.device
-    index = dev.index if dev.type == "cuda" else -1
+    index = x.get_device()
     pw = _dense(w, "w", _E4M3, (rows, cols), index)
     pws = _dense(w_scale, "w_scale", torch.float32, ((rows + 127) // 128, (cols + 127) // 128), index)
     T = x.shape[0]
@@ -257,16 +269,17 @@ def linear8(x, w, w_scale, x_scale=None, transposed: bool = False, dtype=None, o
         if out is not None:
             raise ValueError("out does not go with inputs that want a gradient (torch.no_grad() lets it)")
         return _Linear8.apply(x, w, w_scale, transposed, dtype, ws)
+    make = _maker(index)
     if out is None:
-        out = _new((T, n_out), (n_out, 1), dtype, dev)
+        out = make((T, n_out), (n_out, 1), dtype)
         ys = n_out
     else:
         ys = _matrix(out, "out", (dtype,), n_out)
-        if out.shape[0] != T or out.device != dev:
+        if out.shape[0] != T or out.get_device() != index:
             raise ValueError("out must have the tokens and device of x")
     pb, nb = None, 0
     if not coded:
-        ws = _ws(L.exl3_linear8_workspace_bytes(T, rows, cols, tr), dev, ws)
+        ws = _ws(L.exl3_linear8_workspace_bytes(T, rows, cols, tr), x.device, ws, make)
         pb, nb = ws.data_ptr(), ws.numel() * ws.element_size()
     _call(L.exl3_linear8, index, x.data_ptr(), xdt, T, xs, ps, st, sb, pw, pws, rows, cols, tr, out.data_ptr(), _DT[dtype],
           ys, pb, nb, _stream(index))
@@ -274,7 +287,6 @@ def linear8(x, w, w_scale, x_scale=None, transposed: bool = False, dtype=None, o
 
 
 _Experts = ctypes.c_void_p * 12
-_PARTS, _PART_DT = ("codes", "su", "sv", "scale"), (torch.int16, torch.float32, torch.float32, torch.float32)
 
 
 def expert_layer(x, gate, up, down, K: int, top_k: int, router=None, ids=None, weights=None, transposed: bool = False,
@@ -291,7 +303,7 @@ def expert_layer(x, gate, up, down, K: int, top_k: int, router=None, ids=None, w
     ``weights`` float32 [T, top_k] (an id that is no expert's is passed over).  Returns y
     [T, hidden] of x's dtype.  For more tokens, and for gradients, there is
     ``expert_linear``."""
-    dev, index = x.device, x.get_device()
+    index = x.get_device()
     gc = gate[0]
     if gc.dim() != 4:
         raise ValueError(f"gate codes must be [experts, rows/16, cols/16, 16K], got {tuple(gc.shape)}")
@@ -302,14 +314,20 @@ def expert_layer(x, gate, up, down, K: int, top_k: int, router=None, ids=None, w
         if m[0].shape[1:3] != (r, c):
             raise ValueError(f"gate {(16 * rows, 16 * cols)} and {name} {tuple(16 * v for v in m[0].shape[1:3])} do not go together")
         if not isinstance(m[3], torch.Tensor):
-            m = (*m[:3], torch.full((E,), float(m[3]), dtype=torch.float32, device=dev))
+            m = (*m[:3], torch.full((E,), float(m[3]), dtype=torch.float32, device=x.device))
             made.append(m)                 # (lives until the launch)
-        for t, what, dt, shape in zip(m, _PARTS, _PART_DT, ((E, r, c, 16 * k), (E, 16 * r), (E, 16 * c), (E,))):
-            if t.dtype is not dt or t.shape != shape or t.get_device() != index or not t.is_contiguous():
-                _dense(t, f"{name} {what}", dt, shape, index)
-            at.append(t.data_ptr())
-            if t.requires_grad:
-                grad = True
+        codes, su, sv, scale = m
+        if not (codes.dtype is torch.int16 and codes.shape == (E, r, c, 16 * k) and codes.get_device() == index and codes.is_contiguous()):
+            _dense(codes, f"{name} codes", torch.int16, (E, r, c, 16 * k), index)
+        if not (su.dtype is torch.float32 and su.shape == (E, 16 * r) and su.get_device() == index and su.is_contiguous()):
+            _dense(su, f"{name} su", torch.float32, (E, 16 * r), index)
+        if not (sv.dtype is torch.float32 and sv.shape == (E, 16 * c) and sv.get_device() == index and sv.is_contiguous()):
+            _dense(sv, f"{name} sv", torch.float32, (E, 16 * c), index)
+        if not (scale.dtype is torch.float32 and scale.shape == (E,) and scale.get_device() == index and scale.is_contiguous()):
+            _dense(scale, f"{name} scale", torch.float32, (E,), index)
+        at += codes.data_ptr(), su.data_ptr(), sv.data_ptr(), scale.data_ptr()
+        if su.requires_grad or sv.requires_grad or scale.requires_grad:
+            grad = True
     H, F = (cols, rows) if transposed else (rows, cols)
     H, F = 16 * H, 16 * F
     xs = _activations(x, "x", H)
@@ -330,14 +348,15 @@ def expert_layer(x, gate, up, down, K: int, top_k: int, router=None, ids=None, w
     if _grad_on() and (grad or x.requires_grad or (router is not None and router.requires_grad) or
                        (weights is not None and weights.requires_grad)):
         raise ValueError("there is no gradient through an expert layer (torch.no_grad() lets it; expert_linear has one)")
+    make = _maker(index)
     if out is None:
-        out = _new((T, H), (H, 1), x.dtype, dev)
+        out = make((T, H), (H, 1), x.dtype)
         ys = H
     else:
         ys = _activations(out, "out", H, like=x)
     L = _lib()
-    ws = _ws(L.exl3_expert_layer_workspace_bytes(T, H, F, E, top_k), dev, ws)
-    _call(L.exl3_expert_layer, dev.index, x.data_ptr(), _DT[x.dtype], T, xs, pr, rdt, pi, pw, top_k, 1 if normalize else 0, E,
+    ws = _ws(L.exl3_expert_layer_workspace_bytes(T, H, F, E, top_k), x.device, ws, make)
+    _call(L.exl3_expert_layer, index, x.data_ptr(), _DT[x.dtype], T, xs, pr, rdt, pi, pw, top_k, 1 if normalize else 0, E,
           _Experts(*at), H, F, K, kd, 1 if transposed else 0, out.data_ptr(), ys, ws.data_ptr(),
-          ws.numel() * ws.element_size(), _stream(dev.index))
+          ws.numel() * ws.element_size(), _stream(index))
     return out

@@ -643,10 +643,11 @@ EXL3_API exl3_status exl3_profile_read(double *encode_ms, int64_t *encode_launch
                               int64_t *kernel_launches);
 
 /*
- * Device-side wait accounting (no counterpart on the pages).  Two kernels wait
- * on asynchronous arrivals: the forward rotation of bf16 weights waits for its
- * TMA tile loads, and the products with coded matrices (exl3_linear and the
- * entry points beside it) for their copies, operands and tensor-core results.
+ * Device-side wait accounting (no counterpart on the pages).  These kernels
+ * wait on asynchronous arrivals: the forward rotation of bf16 weights for its
+ * TMA tile loads, norm gradients for their rows, and the products (exl3_linear
+ * and the entry points beside it, exl3_linear8, exl3_expert_layer) for their
+ * copies, operands and tensor-core results.
  * Each such wait gives up after one second, after which the block issues
  * nothing further, waits (bounded) for what it already issued, and the
  * launch's results are void.  exl3_wait_timeouts synchronises the device,

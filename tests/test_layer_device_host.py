@@ -23,14 +23,14 @@ def layer(monkeypatch):
         yield
         devices.pop()
 
-    def new(shape, stride, dtype, dev):
-        return torch.empty_strided(shape, stride, dtype=dtype).as_subclass(Placed if dev.index == 1 else Elsewhere)
+    def maker(index):
+        return lambda shape, stride, dtype: torch.empty_strided(shape, stride, dtype=dtype).as_subclass(Placed if index == 1 else Elsewhere)
 
     monkeypatch.setattr(products, "_fn", Library(devices))
     monkeypatch.setattr(products, "_current_device", lambda: devices[-1], raising=False)
     for module in (products, layer):
         monkeypatch.setattr(module, "_stream", lambda index: 1000 + index)
-    monkeypatch.setattr(layer, "_new", new)
+    monkeypatch.setattr(layer, "_maker", maker)
     monkeypatch.setattr(torch.cuda, "device", device)
     layer.seen, layer.devices = products._fn.seen, devices
     return layer
