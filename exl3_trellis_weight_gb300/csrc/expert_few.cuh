@@ -30,7 +30,7 @@ struct ExpertSteps {
     int max_tiles;
     int nf, steps;            // 128 outputs and 128 inputs to a tile
     float *part;              // [blocks][2][matrices][rows of a tile][128]: sums of tiles that blocks share
-    int32_t *done;            // [tiles][nf]: steps of it that are finished
+    int32_t *done;            // [tiles][nf]: finished steps of it, of all rows and matrices
 };
 
 // `all` steps in even shares: block b begins at step first(b)
@@ -360,15 +360,19 @@ __device__ __forceinline__ void run_share(const ExpertSteps &p, const Op &op, un
                               tl.y, row, f0, lane);
             }
         } else {
-            // of a share of the inputs: to memory
-            ok = ok && __all_sync(0xffffffffu, bar_wait(sums_full(m_at), m_parity, &gave_up, count));
-            for (int q = warp; q < M * rows; q += kExpertWarps) {
+            // of a share of the inputs: to memory, a row of a matrix to a warp, and whichever row's
+            // last share comes from here says so (no meeting of the block: one to eight tokens
+            // gained 1 %)
+            if (row < M * rows)
+                ok = ok && __all_sync(0xffffffffu, bar_wait(sums_full(m_at), m_parity, &gave_up, count));
+#pragma unroll 1
+            for (int q = row; q < M * rows; q += kExpertWarps) {
                 const int m = q >= rows ? 1 : 0, r = q - m * rows;
                 __stcg(reinterpret_cast<float4 *>(part_of(block, own_first ? 0 : 1, m) + r * 128) + lane, set_sum(from, m, M, F::kRows, r, lane));
+                __syncwarp();
+                if (lane == 0 && add_in(p.done + it, c) + c == steps * M * rows)
+                    last[own_first ? 0 : 1] = 1;
             }
-            __syncthreads();
-            if (tid == 0)
-                last[own_first ? 0 : 1] = add_in(p.done + it, c) + c == steps;
         }
         __syncwarp();
         if (lane == 0)

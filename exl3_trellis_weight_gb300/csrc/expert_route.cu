@@ -86,11 +86,12 @@ __device__ __forceinline__ uint32_t order_of(float v) {
 
 __device__ __forceinline__ float value_of(uint32_t k) { return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k); }
 
-constexpr int kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32;
+// (threads of the plan; a few pairs are planned by fewer, whose barriers take less)
+constexpr int kPlanThreads = 1024, kPlanFew = 256;
 
-// shared memory behind the counts: ids, valid flags and, one after the other, the warps' keys
+// shared memory behind the counts: ids and, one after the other, the warps' keys
 // of the experts and their counts of them
-__host__ __device__ inline size_t plan_bytes(int64_t n, int E) { return (size_t)n * 4 + (size_t)kPlanWarps * E * 4; }
+inline size_t plan_bytes(int64_t n, int E, int threads) { return (size_t)n * 4 + (size_t)(threads / 32) * E * 4; }
 
 // The picks of a token, by a warp: the largest keys, of equals the lowest expert; lane j has
 // the j-th and its key.  No key is 0 but one that has been picked.  Up to 32 R experts stay in
@@ -156,7 +157,8 @@ __device__ __forceinline__ Pick picks_many(uint32_t *keys, int E, int top_k, int
     return p;
 }
 
-template <bool ROUTE> __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const ExpertLaunch a) {
+template <bool ROUTE, int THREADS> __global__ void __launch_bounds__(THREADS) plan_kernel(const ExpertLaunch a) {
+    constexpr int kPlanWarps = THREADS / 32;
     __shared__ int32_t count[kMaxExperts], first[kMaxExperts];
     extern __shared__ int32_t plan_mem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -164,12 +166,12 @@ template <bool ROUTE> __global__ void __launch_bounds__(kPlanThreads) plan_kerne
     int32_t *const ids = plan_mem;
     uint32_t *const keys = reinterpret_cast<uint32_t *>(plan_mem + n) + warp * a.E;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    for (int i = tid; i < a.rows; i += kPlanThreads)
+    for (int i = tid; i < a.rows; i += THREADS)
         a.pair_of[i] = -1;
     const int tiles = (int)expert_tiles(a.T, a.top_k, a.E, a.tile_n);
-    for (int i = tid; i < tiles * (a.F / 128); i += kPlanThreads)
+    for (int i = tid; i < tiles * (a.F / 128); i += THREADS)
         a.up_done[i] = 0;
-    for (int i = tid; i < tiles * (a.H / 128); i += kPlanThreads)
+    for (int i = tid; i < tiles * (a.H / 128); i += THREADS)
         a.down_done[i] = 0;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (ROUTE) {
@@ -208,7 +210,7 @@ template <bool ROUTE> __global__ void __launch_bounds__(kPlanThreads) plan_kerne
             }
         }
     } else {
-        for (int i = tid; i < n; i += kPlanThreads) {
+        for (int i = tid; i < n; i += THREADS) {
             const int e = a.ids[i];
             ids[i] = e >= 0 && e < a.E ? e : -1;
         }
@@ -217,8 +219,8 @@ template <bool ROUTE> __global__ void __launch_bounds__(kPlanThreads) plan_kerne
     // a warp counts the experts of its share of the pairs, and each pair's place among them
     uint16_t *const seen = reinterpret_cast<uint16_t *>(plan_mem + n);          // [warp][E]
     constexpr int kMaxRounds = 4;                                               // 32 warps x 32 lanes x 4 pairs
-    const int rounds = (n + kPlanThreads - 1) / kPlanThreads, shares = (n + 32 * rounds - 1) / (32 * rounds);
-    for (int i = tid; i < shares * a.E; i += kPlanThreads)
+    const int rounds = (n + THREADS - 1) / THREADS, shares = (n + 32 * rounds - 1) / (32 * rounds);
+    for (int i = tid; i < shares * a.E; i += THREADS)
         seen[i] = 0;
     __syncthreads();
     uint16_t *const mine = seen + warp * a.E;
@@ -238,7 +240,7 @@ template <bool ROUTE> __global__ void __launch_bounds__(kPlanThreads) plan_kerne
         }
     }
     __syncthreads();
-    for (int e = tid; e < a.E; e += kPlanThreads) {
+    for (int e = tid; e < a.E; e += THREADS) {
         int c = 0;
         for (int w0 = 0; w0 < shares; w0 += 8) {
             int k[8];
@@ -366,10 +368,12 @@ template <typename T> exl3_status route_t(const ExpertLaunch &p, cudaStream_t s)
         st = start(both ? logits_kernel<T, true> : logits_kernel<T, false>, dim3((unsigned)jobs), kLogitWarps * 32, 0, false, s, p);
         if (st != EXL3_OK)
             return st;
-        st = start(plan_kernel<true>, dim3(1), kPlanThreads, plan_bytes(p.T * p.top_k, p.E), true, s, p);
-    } else {
-        st = start(plan_kernel<false>, dim3(1), kPlanThreads, plan_bytes(p.T * p.top_k, p.E), false, s, p);
     }
+    const bool few = p.T * p.top_k <= kPlanFew;
+    const unsigned threads = few ? kPlanFew : kPlanThreads;
+    st = start(p.router ? (few ? plan_kernel<true, kPlanFew> : plan_kernel<true, kPlanThreads>)
+                        : (few ? plan_kernel<false, kPlanFew> : plan_kernel<false, kPlanThreads>),
+               dim3(1), threads, plan_bytes(p.T * p.top_k, p.E, (int)threads), p.router != nullptr, s, p);
     if (st != EXL3_OK)
         return st;
     unsigned block = (unsigned)((p.H / 16 + 31) / 32 * 32);

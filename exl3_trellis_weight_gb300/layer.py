@@ -106,7 +106,7 @@ def rms_norm(x, weight, eps: float = 1e-6, residual=None, want_y: bool = True, w
     sqrt(mean(h^2) + eps) for each row.
 
     x, residual [T, n] bfloat16 or float16 (rows may be strided), n up to 32768;
-    weight [n] of x's dtype or float32.  Returns dict(h, y, y8, scale): h with a
+    weight [n] of x's dtype or float32; eps a positive normal number.  Returns dict(h, y, y8, scale): h with a
     residual, y with ``want_y``, and with ``want_y8`` y in float8_e4m3fn [T, n]
     with the scale of each 128 columns of a row [T, ceil(n / 128)] (what ``linear8``
     takes); None otherwise.  h may be given as an output (x or residual itself, too),
