@@ -355,8 +355,8 @@ template <typename T> __device__ __forceinline__ void unpack_pairs(const Eight &
 // beyond, where registers run out.
 // RING: whole rows are copied into stages of shared memory, `depth` of them ahead.  (One row
 // ahead in registers were 48 KB to an SM on their way: 8192 x 4096 took 66 us, 4.1 TB/s; now
-// 53, 5.1 TB/s, and 5 for the sum of dweight's parts, whose launch overlaps.  What is left
-// are the two meetings of a row's warps and 2.3 of 4 instructions a cycle.)
+// 52, 5.2 TB/s, and 5 for the sum of dweight's parts, whose launch overlaps.  What is left
+// are the two meetings of a row's warps.)
 // WAY: the next row is asked for into registers.
 __device__ unsigned int g_norm_timeouts;
 constexpr int kMaxDepth = 8;
