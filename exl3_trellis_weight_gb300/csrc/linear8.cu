@@ -555,6 +555,9 @@ template <int TN, bool SWAP, bool MN> exl3_status launch_form8(const Linear8Laun
     return cuda_check(cudaGetLastError(), "8-bit product launch");
 }
 
+// Outputs are the instruction's rows up to 64 tokens: replayed graphs, us, 4096 x 4096, outputs / tokens as
+// rows: 17 tokens 10.3 / 12.4, 32 10.3 / 11.3, 64 12.3 / 12.2, 65 13.4 / 12.4.  256 outputs a tile where tiles
+// fill the SMs, else 128: 4096 tokens x 4096 x 12288 181 and 202, 2048 x 4096 x 4096 39 and 45.
 template <bool MN> exl3_status launch_mn(const Linear8Launch &p, Args8 &a, cudaStream_t s) {
     if (a.T <= 16)
         return launch_form8<16, true, MN>(p, a, s);

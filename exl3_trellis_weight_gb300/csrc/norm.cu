@@ -818,8 +818,11 @@ template <typename T> exl3_status norm_t(const NormLaunch &p, int vec, const Sha
 }
 
 // Warps of an SM (half of them with two units each, which take 117 registers), and how many
-// columns a ring of whole rows is for.
-constexpr int kGradWarps = 32, kRingFrom = 1024, kRingTo = 8192;
+// columns a ring of whole rows is for.  (8192 rows, with and without: 512 columns 24.0 and 26.6 us,
+// 1024 29 and 30, 2048 39 and 43, 8192 102 and 144.  A row of one warp has no meeting at which
+// its stage could be asked for again.)
+constexpr int kGradWarps = 32, kRingFrom = 512, kRingTo = 8192;
+static_assert(kRingFrom > kUnitN, "two warps to a row at least");
 constexpr uint32_t kRingRoom = 208 * 1024;     // of an SM
 
 struct GradShape : Shape {
