@@ -459,3 +459,89 @@ def test_in_a_graph_on_another_stream_and_without_tokens(ex):
     assert ex.linear8(e.to(E4M3), w8, ws, torch.empty(0, 4, device=DEV)).shape == (0, 768)
     b = ex.rms_norm_backward(e, e, w)
     assert b["dx"].shape == (0, n) and bool((b["dweight"] == 0).all())
+
+
+def test_threads_that_call_at_once(ex):
+    """Six host threads, each with its stream and sizes: the same results as alone."""
+    import threading
+    g = gen(21)
+    x = [acts(g, 64 + 100 * i, 512 + 128 * i, "bf16") for i in range(6)]
+    w = [torch.rand(512 + 128 * i, generator=g, device=DEV) for i in range(6)]
+    m = [ex.quantize8(torch.randn(512 + 128 * i, 640, generator=g, device=DEV), block_rows=128) for i in range(6)]
+
+    def work(i):
+        n = ex.rms_norm(x[i], w[i], want_y8=True)
+        b = ex.rms_norm_backward(x[i], x[i], w[i])
+        return n["y"], b["dx"], b["dweight"], ex.linear8(n["y8"], *m[i], n["scale"]), ex.linear8(x[i], *m[i])
+
+    want = [work(i) for i in range(6)]
+    torch.cuda.synchronize()
+    other = []
+
+    def run(i):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(10):
+                got = work(i)
+                s.synchronize()
+                if not all(torch.equal(a, b) for a, b in zip(got, want[i])):
+                    other.append(i)
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(6)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not other
+
+
+def test_a_captured_backward_pass(ex):
+    """Norm and 8-bit product with their gradients in a graph, replayed with other inputs."""
+    g = gen(22)
+    m = ex.quantize8(torch.randn(640, 256, generator=g, device=DEV), block_rows=128)
+    x, w = acts(g, 40, 640, "bf16").requires_grad_(), torch.rand(640, generator=g, device=DEV).requires_grad_()
+
+    def step():
+        y = ex.linear8(ex.rms_norm(x, w)["y"], *m)
+        return torch.autograd.grad(y, [x, w], torch.ones_like(y))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    with torch.no_grad():
+        x.copy_(acts(g, 40, 640, "bf16"))
+    graph.replay()
+    assert all(torch.equal(a, b) for a, b in zip(got, step()))
+
+
+def test_offsets_beyond_32_bits(ex):
+    """2.3e9 values: the first row, the last and the one across 2^31 are as exact as any."""
+    g = gen(23)
+    T, n = 140000, 16384
+    x = torch.empty(T, n, dtype=torch.bfloat16, device=DEV).normal_(generator=g)
+    w = torch.rand(n, generator=g, device=DEV)
+    m, ms = ex.quantize8(torch.randn(64, n, generator=g, device=DEV), block_rows=128)
+    at = [0, 2 ** 31 // n - 1, 2 ** 31 // n, T - 1]
+    r = ex.rms_norm(x, w, 1e-6, want_y8=True)
+    y, s = norm64(x[at], w, 1e-6)
+    within(r["y"][at], y, (U["bf16"] * (1 + 64 * F) + 32 * F) * y.abs())
+    check_blocks(r["y8"][at], r["scale"][at], y, 32 * F)
+    p = ex.linear8(r["y8"], m, ms, r["scale"], transposed=True)
+    ref, size = product64(r["y8"][at], r["scale"][at], m, ms, True)
+    within(p[at], ref, U["bf16"] * ref.abs() + 2.0 ** -17 * n / 5120 * size)
+    dy = r["y"]
+    del r, p
+    got = ex.rms_norm_backward(dy, x, w, 1e-6, want_dweight=False)["dx"]
+    h64, g64 = x[at].double(), dy[at].double() * w.double()
+    dx = s * g64 - h64 * s.pow(3) * (g64 * h64).mean(1, keepdim=True)
+    size = (s * g64).abs() + h64.abs() * s.pow(3) * (g64 * h64).abs().mean(1, keepdim=True)
+    within(got[at], dx, U["bf16"] * dx.abs() + 161 * F * size)
+    del got, dy
+    codes, scale = ex.quantize8(x, block_rows=128)
+    first = (T - 1) // 128 * 128
+    check_blocks(codes[first:], scale[first // 128:], x[first:].double(), 0.0, rows=128)
