@@ -17,12 +17,11 @@
 // 16 warps with all the registers took 232.
 #pragma once
 
+#include "expert_form.cuh"
 #include "layer.cuh"
 #include "linear_few.cuh"
 
 namespace exl3 {
-
-constexpr int kExpertWarps = 32, kExpertThreads = kExpertWarps * 32, kSets = 4;
 
 struct ExpertSteps {
     const int4 *tiles;        // expert, first row, rows
@@ -81,44 +80,13 @@ __device__ __forceinline__ float4 rotate_row(float4 v, int lane) {
     return v;
 }
 
-// A block's sums in shared memory, [set][row][33 float4] (the step from row to row spreads
-// a warp's fragments over all banks)
-constexpr int kSumRow = 132;
+// A block's sums in shared memory, [set][row][kSumRow floats]
 __device__ __forceinline__ float4 set_sum(const float4 *sums, int set, int every, int rows, int row, int lane) {
     float4 v = sums[(set * rows + row) * (kSumRow / 4) + lane];
     for (set += every; set < kSets; set += every)
         v = add4(v, sums[(set * rows + row) * (kSumRow / 4) + lane]);
     return v;
 }
-
-// TWO: the sets have matrix set % 2 (gate and up) and every second step; otherwise every
-// fourth step, whose sums are added under the rows' scales of that step.
-// RB: a tile's blocks of 8 rows.  LO: activations are in two parts.
-template <int K, int RB, bool LO, bool TWO> struct ExpertForm {
-    static constexpr int kMatrices = TWO ? 2 : 1, kGroups = kSets / kMatrices, kRows = RB * 8;
-    // inputs of a step: [matrix][64 inputs][part][rows], and the rows' scales
-    static constexpr uint32_t kPanel = RB * (LO ? 2u : 1u) * 1024u, kInputs = kMatrices * 2u * kPanel;
-    static constexpr uint32_t kZ = kInputs + (TWO ? 0u : 128u);
-    // codes of a step of a warp, the ring of `kAhead` of them, and the stages of inputs: what
-    // shared memory has room for.  (A warp that is served first takes a step in a third of
-    // the latency of memory: two steps in the ring left 36 % of the issue slots empty.)
-    static constexpr uint32_t kCodes = 256u * K, kSums = kSets * kRows * kSumRow * 4u;
-    static constexpr uint32_t kRoom = 219u * 1024u;
-    static constexpr bool fits(int stages, int steps, int meetings) {
-        return stages * kZ + steps * kExpertWarps * kCodes + meetings * kSums <= kRoom;
-    }
-    // (two places for the sums: a tile's rows are read while the next tile's are written)
-    static constexpr int kMeet = fits(2 * kGroups, 3, 2) ? 2 : 1;
-    static constexpr int kStages = fits(4 * kGroups, 3, kMeet)   ? 4 * kGroups
-                                   : fits(3 * kGroups, 3, kMeet) ? 3 * kGroups
-                                   : fits(2 * kGroups, 3, kMeet) ? 2 * kGroups
-                                                                 : kGroups * 3 / 2;
-    static constexpr int kAhead = fits(kStages, 4, kMeet) ? 4 : 3;
-    static constexpr uint32_t kRing = kAhead * kCodes;
-    static constexpr uint32_t kRingAt = kStages * kZ, kSumsAt = kRingAt + kExpertWarps * kRing;
-    static constexpr uint32_t kSmem = kSumsAt + kMeet * kSums + 1024u;
-    static_assert(fits(kStages, kAhead, kMeet) && kSmem <= 220 * 1024 && kRows <= kExpertWarps, "beside 7 KB of other variables, a row a warp");
-};
 
 // One more of `all` to have come here; whether it was the last.  (What came before in the
 // others' order comes before what the last does next.)
@@ -147,10 +115,10 @@ template <int K, bool TR, int RB, bool LO, bool TWO, typename Op>
 __device__ __forceinline__ void run_share(const ExpertSteps &p, const Op &op, unsigned int *count) {
     using namespace tc;
     using F = ExpertForm<K, RB, LO, TWO>;
-    constexpr int G = F::kGroups, M = F::kMatrices, S = F::kStages, B = F::kMeet;
+    constexpr int G = F::kGroups, M = F::kMatrices, S = F::kStages, L = F::kArrivals, B = F::kMeet;
     extern __shared__ unsigned char smem_raw[];
-    __shared__ __align__(8) unsigned long long bars[S + 2 * B];
-    __shared__ uint32_t used[S], filled[S];                    // warps that are done with a stage; times it was asked for
+    __shared__ __align__(8) unsigned long long bars[L + 2 * B];
+    __shared__ uint32_t used[S], filled[L];                    // warps that are done with a stage; times a barrier was armed
     __shared__ int4 table[kTable];
     __shared__ __align__(16) float kept[2][512];
     __shared__ int gave_up;
@@ -162,20 +130,22 @@ __device__ __forceinline__ void run_share(const ExpertSteps &p, const Op &op, un
     const int fw = warp & 7, set = warp >> 3, matrix = set % M, group = set / M;
     const int blocks = (int)gridDim.x, block = (int)blockIdx.x;
     const uint32_t bar0 = saddr(bars);
-    auto full = [&](int s) { return bar0 + 8u * (uint32_t)s; };
+    auto full = [&](int b) { return bar0 + 8u * (uint32_t)b; };
     // the sums of a tile are there; have been read
-    auto sums_full = [&](int m) { return bar0 + 8u * (uint32_t)(S + m); };
-    auto sums_read = [&](int m) { return bar0 + 8u * (uint32_t)(S + B + m); };
+    auto sums_full = [&](int m) { return bar0 + 8u * (uint32_t)(L + m); };
+    auto sums_read = [&](int m) { return bar0 + 8u * (uint32_t)(L + B + m); };
     // (the plan is complete: the launch before this one waited for it)
     const int nf = p.nf, steps = p.steps;
     const int n_tiles = __ldcg(p.n_tiles);
     if (tid < kTable && tid < p.max_tiles)
         table[tid] = __ldcg(p.tiles + tid);
     if (tid == 0) {
-        for (int s = 0; s < S; s++) {
-            bar_init(full(s), 1);
-            used[s] = filled[s] = 0;
+        for (int b = 0; b < L; b++) {
+            bar_init(full(b), 1);
+            filled[b] = 0;
         }
+        for (int s = 0; s < S; s++)
+            used[s] = 0;
         for (int m = 0; m < B; m++) {
             bar_init(sums_full(m), kExpertWarps);
             bar_init(sums_read(m), kExpertWarps);
@@ -243,13 +213,13 @@ __device__ __forceinline__ void run_share(const ExpertSteps &p, const Op &op, un
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // inputs of step i of the share, which is step k of a tile, by a warp
     auto issue = [&](int i, int tile, int k) {
-        const int s = i % S, rows = (table[tile].z + 7) & ~7;
+        const int s = F::stage(i), b = F::arrival(i), rows = (table[tile].z + 7) & ~7;
         if (lane == 0) {
-            filled[s]++;
-            bar_expect(full(s), op.bytes(rows));
+            filled[b]++;
+            bar_expect(full(b), op.bytes(rows));
         }
         __syncwarp();
-        op.load(base + (uint32_t)s * F::kZ, full(s), table[tile].y, k, rows, lane);
+        op.load(base + (uint32_t)s * F::kZ, full(b), table[tile].y, k, rows, lane);
     };
     if (warp < S && warp < n)
         issue(warp, (w0 + warp) / steps / nf - first, (w0 + warp) % steps);
@@ -282,8 +252,8 @@ __device__ __forceinline__ void run_share(const ExpertSteps &p, const Op &op, un
         i += (group - i) & (G - 1);
 #pragma unroll 1
         for (; i < end; i += G) {
-            const int s = i % S;
-            ok = ok && __all_sync(0xffffffffu, bar_wait(full(s), (uint32_t)(i / S) & 1, &gave_up, count));
+            const int s = F::stage(i);
+            ok = ok && __all_sync(0xffffffffu, bar_wait(full(F::arrival(i)), F::parity(i), &gave_up, count));
             copy_wait<F::kAhead - 1>();
             __syncwarp();
             if (ok) {
@@ -412,9 +382,9 @@ __device__ __forceinline__ void run_share(const ExpertSteps &p, const Op &op, un
             op.finish(v[0], v[M - 1], kept[which], tl.y, row, f0, lane);
     }
     if (gave_up && tid == 0)               // nothing may be in flight when the block ends
-        for (int i = 0; i < S; i++)
-            if (filled[i])
-                bar_drain(full(i), (filled[i] - 1) & 1);
+        for (int b = 0; b < L; b++)
+            if (filled[b])
+                bar_drain(full(b), (filled[b] - 1) & 1);
 }
 
 }  // namespace exl3
