@@ -380,7 +380,7 @@ template <typename T> exl3_status route_t(const ExpertLaunch &p, cudaStream_t s)
     block = block > 1024 ? 1024 : block;
     return start(vec ? pairs_kernel<T, true> : pairs_kernel<T, false>, dim3((unsigned)p.rows, 2), block,
                  (size_t)(block / 32) * 4 * kUnit * sizeof(float), true, s, p,
-                 !p.transposed || p.K == 3 ? 0 : p.K == 1 ? 2 : 1);
+                 few_order(p.K, p.transposed));
 }
 
 }  // namespace

@@ -87,7 +87,10 @@ struct ProductLaunch {
 exl3_status launch_product(const ProductLaunch &p, cudaStream_t s);
 // the same for few tokens (linear_few.cu)
 bool few_eligible(const ProductLaunch &p);
-int few_order(const ProductLaunch &p);     // PrepLaunch::order that it reads
+// PrepLaunch::order that the fragments of few tokens want (lane_of in linear_few.cuh): lane
+// j's four inputs are places 4j .. 4j + 3 of 16
+inline int few_order(int K, bool transposed) { return !transposed || K == 3 ? 0 : K == 1 ? 2 : 1; }
+int few_order(const ProductLaunch &p);
 exl3_status few_take_wait_timeouts(unsigned int *n);
 exl3_status launch_product_few(const ProductLaunch &p, cudaStream_t s);
 

@@ -9,9 +9,6 @@ namespace exl3 {
 
 constexpr int kTilesAhead = 16;            // tiles in a warp's ring
 
-// PrepLaunch::order that lane_of wants: lane j's four inputs are places 4j .. 4j + 3 of 16
-inline int few_order(int K, bool transposed) { return !transposed || K == 3 ? 0 : K == 1 ? 2 : 1; }
-
 // a word of shared memory, OFF bytes behind `at`
 template <int OFF> __device__ __forceinline__ uint32_t lds(uint32_t at) {
     uint32_t v;

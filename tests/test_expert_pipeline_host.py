@@ -5,6 +5,7 @@ The kernels' own header says how many stages and barriers each form has and whic
 which; the protocol around them (arm a barrier, copy, wait for a parity, count, ask for the next
 inputs) is played through in random orders, some warps and some loads far behind the others."""
 import os
+import re
 import shutil
 import subprocess
 
@@ -135,3 +136,13 @@ def test_every_warp_has_the_inputs_of_its_step(tmp_path):
     r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0, r.stdout
     assert r.stdout.startswith("40 forms")
+
+
+def test_the_order_of_inputs_stands_in_one_place():
+    """Which of 16 inputs a lane takes goes by K and the transposition: whoever stores inputs for the
+    fragments asks the same function."""
+    rule, places = re.compile(r"K\s*==\s*3\s*\?\s*0\s*:\s*(?:\w+\.)?K\s*==\s*1\s*\?\s*2\s*:\s*1"), []
+    for name in sorted(os.listdir(CSRC)):
+        with open(os.path.join(CSRC, name)) as f:
+            places += [name] * len(rule.findall(f.read()))
+    assert places == ["linear.cuh"]
