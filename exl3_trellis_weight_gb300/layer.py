@@ -192,8 +192,11 @@ def quantize8(x, block_rows: int = 1):
     """exl3_quantize8: x [T, n] (bfloat16, float16 or float32, rows may be strided)
     -> (codes float8_e4m3fn [T, n], scale float32): codes times the scale of their
     block of ``block_rows`` x 128 stand for x.  block_rows 1, for activations: scale
-    [T, ceil(n / 128)]; 128, for weights: [ceil(T / 128), ceil(n / 128)]."""
+    [T, ceil(n / 128)]; 128, for weights: [ceil(T / 128), ceil(n / 128)].  There is no
+    gradient through it: an x that wants one is refused (torch.no_grad() lets it)."""
     xs = _matrix(x, "x", _DT_X)
+    if _grad_on() and x.requires_grad:
+        raise ValueError("there is no gradient through 8-bit blocks (detach x, or torch.no_grad() lets it)")
     T, n = x.shape
     index = x.get_device()
     make = _maker(index)
@@ -234,7 +237,8 @@ def linear8(x, w, w_scale, x_scale=None, transposed: bool = False, dtype=None, o
     in bfloat16 or float16, which are brought to that first.  Returns y [T, outputs] of
     ``dtype`` (bfloat16 or float16; x's own if it is one of them, else bfloat16).  The
     input gradient is the same call with ``transposed`` flipped, and what x in 16 bits
-    gets through autograd."""
+    gets through autograd; w has none, so a w that wants one is refused (a Parameter does
+    unless it is made with requires_grad=False)."""
     if w.dim() != 2:
         raise ValueError(f"w must be [rows, cols], got {tuple(w.shape)}")
     rows, cols = w.shape
@@ -263,9 +267,9 @@ def linear8(x, w, w_scale, x_scale=None, transposed: bool = False, dtype=None, o
         dtype = out.dtype if out is not None else torch.bfloat16 if coded else x.dtype
     if dtype not in _DT:
         raise ValueError(f"unsupported dtype {dtype} of y")
-    if _grad_on() and (x.requires_grad or w_scale.requires_grad or (x_scale is not None and x_scale.requires_grad)):
-        if w_scale.requires_grad or coded:
-            raise ValueError("there is a gradient only with respect to x in 16 bits (detach the scales)")
+    if _grad_on() and (x.requires_grad or w.requires_grad or w_scale.requires_grad or (x_scale is not None and x_scale.requires_grad)):
+        if w.requires_grad or w_scale.requires_grad or coded:
+            raise ValueError("there is a gradient only with respect to x in 16 bits (detach w and the scales)")
         if out is not None:
             raise ValueError("out does not go with inputs that want a gradient (torch.no_grad() lets it)")
         return _Linear8.apply(x, w, w_scale, transposed, dtype, ws)

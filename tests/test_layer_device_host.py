@@ -120,3 +120,27 @@ def test_an_expert_scale_may_be_a_number(layer):
     finally:
         layer.torch.full = keep
     assert len(layer.seen) == 1
+
+
+def test_refuses_gradients_of_8_bit_blocks_and_matrices(layer):
+    """A torch.nn.Parameter in e4m3 wants a gradient unless told otherwise, and none comes to it."""
+    v = tensors(Placed)
+
+    def wants(t):
+        return t.detach().clone().as_subclass(Placed).requires_grad_()
+
+    for call in (lambda: layer.quantize8(wants(v["x"])), lambda: layer.quantize8(wants(v["w"][None]), block_rows=128),
+                 lambda: layer.linear8(v["x"], wants(v["w8"]), v["s8"], ws=v["ws"]),
+                 lambda: layer.linear8(wants(v["x"]), wants(v["w8"]), v["s8"], ws=v["ws"]),
+                 lambda: layer.linear8(v["x8"], wants(v["w8"]), v["s8"], v["xs"])):
+        with pytest.raises(ValueError, match="gradient"):
+            call()
+        assert not layer.seen
+        with torch.no_grad():
+            call()
+        assert len(layer.seen) == 1
+        layer.seen.clear()
+    # what wants none goes through, in either mode
+    layer.quantize8(v["x"])
+    layer.linear8(v["x"], torch.nn.Parameter(v["w8"].as_subclass(torch.Tensor), requires_grad=False).as_subclass(Placed), v["s8"], ws=v["ws"])
+    assert len(layer.seen) == 2
