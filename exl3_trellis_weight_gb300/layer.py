@@ -10,7 +10,8 @@ import ctypes
 import torch
 
 from . import EXL3_BF16, EXL3_E4M3, EXL3_F16, EXL3_F32
-from .products import _activations, _call, _current_device, _dense, _grad_on, _lib, _rows, _stream
+from .products import (_activations, _call, _current_device, _dense, _forward, _grad_on, _lib, _refuse_tangents, _rows,
+                       _stream)
 from .products import _ws as _given_ws
 
 _DT = {torch.bfloat16: EXL3_BF16, torch.float16: EXL3_F16}
@@ -124,6 +125,8 @@ def rms_norm(x, weight, eps: float = 1e-6, residual=None, want_y: bool = True, w
         raise ValueError("neither y nor y8 is wanted")
     if out is not None and not want_y:
         raise ValueError("out goes with want_y")
+    if _forward():
+        _refuse_tangents(x=x, weight=weight, residual=residual)
     if _grad_on() and (x.requires_grad or weight.requires_grad or (residual is not None and residual.requires_grad)):
         if want_y8:
             raise ValueError("there is no gradient through y8 (torch.no_grad() lets it)")
@@ -171,6 +174,8 @@ def rms_norm_backward(dy, h, weight, eps: float = 1e-6, dh=None, want_dweight: b
     ds = xs = n
     if dh is not None:
         ds = _like(dh, "dh", shape, dy, index)
+    if _forward():
+        _refuse_tangents(dy=dy, h=h, weight=weight, dh=dh)
     make = _maker(index)
     if dx is None:
         dx = make((T, n), (n, 1), dy.dtype)
@@ -195,6 +200,8 @@ def quantize8(x, block_rows: int = 1):
     [T, ceil(n / 128)]; 128, for weights: [ceil(T / 128), ceil(n / 128)].  There is no
     gradient through it: an x that wants one is refused (torch.no_grad() lets it)."""
     xs = _matrix(x, "x", _DT_X)
+    if _forward():
+        _refuse_tangents(x=x)
     if _grad_on() and x.requires_grad:
         raise ValueError("there is no gradient through 8-bit blocks (detach x, or torch.no_grad() lets it)")
     T, n = x.shape
@@ -267,6 +274,8 @@ def linear8(x, w, w_scale, x_scale=None, transposed: bool = False, dtype=None, o
         dtype = out.dtype if out is not None else torch.bfloat16 if coded else x.dtype
     if dtype not in _DT:
         raise ValueError(f"unsupported dtype {dtype} of y")
+    if _forward():
+        _refuse_tangents(x=x, w=w, w_scale=w_scale, x_scale=x_scale)
     if _grad_on() and (x.requires_grad or w.requires_grad or w_scale.requires_grad or (x_scale is not None and x_scale.requires_grad)):
         if w.requires_grad or w_scale.requires_grad or coded:
             raise ValueError("there is a gradient only with respect to x in 16 bits (detach w and the scales)")
@@ -349,6 +358,10 @@ def expert_layer(x, gate, up, down, K: int, top_k: int, router=None, ids=None, w
             raise ValueError("a router, or ids and weights")
         pi = _dense(ids, "ids", torch.int32, (T, top_k), index)
         pw = _dense(weights, "weights", torch.float32, (T, top_k), index)
+    if _forward():
+        _refuse_tangents(x=x, router=router, weights=weights)
+        for name, m in (("gate", gate), ("up", up), ("down", down)):
+            _refuse_tangents(**{f"{name} {part}": t for part, t in zip(("su", "sv", "scale"), m[1:])})
     if _grad_on() and (grad or x.requires_grad or (router is not None and router.requires_grad) or
                        (weights is not None and weights.requires_grad)):
         raise ValueError("there is no gradient through an expert layer (torch.no_grad() lets it; expert_linear has one)")

@@ -144,6 +144,19 @@ def _refuse_lost(out, **constants):
         raise ValueError("out does not go with inputs that want a gradient (torch.no_grad() lets it)")
 
 
+# whether forward-mode derivatives are on their way at all (a private name of torch's, read so
+# that a call outside of them pays nothing; without it every tensor is asked)
+def _forward():
+    return getattr(torch.autograd.forward_ad, "_current_level", 0) >= 0
+
+
+def _refuse_tangents(**inputs):
+    """Raises where a forward-mode derivative would be lost: the library reads addresses."""
+    for name, t in inputs.items():
+        if isinstance(t, torch.Tensor) and torch.autograd.forward_ad.unpack_dual(t).tangent is not None:
+            raise ValueError(f"there is no forward-mode derivative through {name} (only gradients)")
+
+
 def _rows(t):
     """t with rows as the library takes them (an expanded gradient has none)."""
     return t if t.shape[0] == 0 or (t.stride(1) == 1 and t.stride(0) >= t.shape[1]) else t.contiguous()
@@ -201,6 +214,8 @@ def linear(x, codes, su, sv, K: int, scale, transposed: bool = False, A=None, B=
     xs = _activations(x, "x", n_in)
     T = x.shape[0]
     pA, pB, pg, pslots, pranks, n, r = _adapters(A, B, gain, slots, ranks, n_in, n_out, x)
+    if _forward():
+        _refuse_tangents(x=x, su=su, sv=sv, scale=scale_, A=A, B=B, gain=gain)
     if _grad_on() and (x.requires_grad or su.requires_grad or sv.requires_grad or scale_.requires_grad or
                        (n and (A.requires_grad or B.requires_grad or gain.requires_grad))):
         _refuse_lost(out, su=su, sv=sv, scale=scale_, gain=gain)
@@ -229,6 +244,8 @@ def linear_backward(dy, x, codes, su, sv, K: int, scale, transposed: bool = Fals
     dys = _activations(dy, "dy", n_out)
     T = dy.shape[0]
     pA, pB, pg, pslots, pranks, n, r = _adapters(A, B, gain, slots, ranks, n_in, n_out, dy)
+    if _forward():
+        _refuse_tangents(dy=dy, x=x, su=su, sv=sv, scale=_keep, A=A, B=B, gain=gain)
     px, xs = None, n_in
     if n:
         if x is None:
@@ -267,6 +284,8 @@ def expert_linear(x, offsets, codes, su, sv, K: int, scale, transposed: bool = F
     xs = _activations(x, "x", n_in)
     T = x.shape[0]
     po = _dense(offsets, "offsets", torch.int32, (E + 1,), x.get_device())
+    if _forward():
+        _refuse_tangents(x=x, su=su, sv=sv, scale=scale_)
     if _grad_on() and (x.requires_grad or su.requires_grad or sv.requires_grad or scale_.requires_grad):
         _refuse_lost(out, su=su, sv=sv, scale=scale_)
         return _ExpertLinear.apply(x, offsets, codes, su, sv, K, scale_, transposed, ws)

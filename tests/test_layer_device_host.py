@@ -144,3 +144,60 @@ def test_refuses_gradients_of_8_bit_blocks_and_matrices(layer):
     layer.quantize8(v["x"])
     layer.linear8(v["x"], torch.nn.Parameter(v["w8"].as_subclass(torch.Tensor), requires_grad=False).as_subclass(Placed), v["s8"], ws=v["ws"])
     assert len(layer.seen) == 2
+
+
+def test_refuses_what_would_lose_a_tangent(layer):
+    """Forward-mode derivatives: a tensor that carries one does not want a gradient, so it has to be
+    asked.  The same calls go through outside of forward mode, and inside it without tangents."""
+    from torch.autograd import forward_ad as fw
+    from exl3_trellis_weight_gb300 import products
+    v = tensors(Placed)
+    one = dict(zip(("codes", "su", "sv", "scale"), (t[0] for t in v["up"])))
+    A, B, gain = placed(1, 4, 256, dtype=BF16), placed(1, 4, 128, dtype=BF16), placed(1)
+    slots, y, offsets = placed(2, dtype=torch.int32), placed(2, 128, dtype=BF16), placed(4, dtype=torch.int32)
+
+    def grouped(**kw):
+        m = dict(zip(("codes", "su", "sv", "scale"), v["up"]))
+        return products.expert_linear(**{**dict(x=v["x"], offsets=offsets, K=2, out=y, ws=v["ws"]), **m, **kw})
+
+    def linear(**kw):
+        return products.linear(**{**dict(x=v["x"], K=2, A=A, B=B, gain=gain, slots=slots, out=y, ws=v["ws"]), **one, **kw})
+
+    def backward(**kw):
+        a = dict(dy=y, x=v["x"], K=2, A=A, B=B, gain=gain, slots=slots, dx=placed(2, 256, dtype=BF16), ws=v["ws"])
+        return products.linear_backward(**{**a, **one, **kw})
+
+    def norm(**kw):
+        return layer.rms_norm(**{**dict(x=v["x"], weight=v["w"], residual=v["r"]), **kw})
+
+    def norm_backward(**kw):
+        return layer.rms_norm_backward(**{**dict(dy=v["x"], h=v["r"], weight=v["w"], dh=v["r"], ws=v["ws"]), **kw})
+
+    def product(**kw):
+        return layer.linear8(**{**dict(x=v["x"], w=v["w8"], w_scale=v["s8"], ws=v["ws"]), **kw})
+
+    def experts(**kw):
+        return layer.expert_layer(**{**dict(x=v["x"], gate=v["up"], up=v["up"], down=v["down"], K=2, top_k=1, router=v["router"], ws=v["ws"]), **kw})
+
+    def part(i):
+        return lambda d: tuple(d if j == i else t for j, t in enumerate(v["up"]))
+
+    given = dict(router=None, ids=v["ids"])
+    cases = [(norm, "x", v["x"]), (norm, "weight", v["w"]), (norm, "residual", v["r"]), (norm_backward, "dy", v["x"]), (norm_backward, "h", v["r"]),
+             (norm_backward, "weight", v["w"]), (norm_backward, "dh", v["r"]), (layer.quantize8, "x", v["x"]), (product, "x", v["x"]),
+             (product, "w_scale", v["s8"]), (experts, "x", v["x"]), (experts, "router", v["router"]), (linear, "x", v["x"]), (linear, "A", A),
+             (linear, "B", B), (linear, "gain", gain), (linear, "su", one["su"]), (linear, "scale", one["scale"]), (backward, "dy", y),
+             (backward, "x", v["x"]), (backward, "A", A), (grouped, "x", v["x"]), (grouped, "sv", v["up"][2])]
+    calls = [(lambda d, call=call, key=key: call(**{key: d}), t) for call, key, t in cases]
+    calls += [(lambda d: product(x=v["x8"], x_scale=d), v["xs"]), (lambda d: experts(**given, weights=d), v["pw"])]
+    calls += [(lambda d, i=i: experts(up=part(i)(d)), v["up"][i]) for i in (1, 2, 3)]
+    for call, t in calls:
+        with fw.dual_level():
+            for grad in (torch.enable_grad, torch.no_grad):
+                with grad(), pytest.raises(ValueError, match="forward-mode"):
+                    call(fw.make_dual(t, torch.ones_like(t)))
+            assert not layer.seen
+            call(t)
+        call(t)
+        assert len(layer.seen) == 2
+        layer.seen.clear()
