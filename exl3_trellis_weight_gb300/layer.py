@@ -10,8 +10,8 @@ import ctypes
 import torch
 
 from . import EXL3_BF16, EXL3_E4M3, EXL3_F16, EXL3_F32
-from .products import (_activations, _call, _current_device, _dense, _forward, _grad_on, _lib, _refuse_tangents, _rows,
-                       _stream)
+from .products import (_activations, _call, _current_device, _dense, _forward, _grad_on, _lib, _overwritten, _refuse_graph,
+                       _refuse_tangents, _rows, _stream)
 from .products import _ws as _given_ws
 
 _DT = {torch.bfloat16: EXL3_BF16, torch.float16: EXL3_F16}
@@ -136,11 +136,14 @@ def rms_norm(x, weight, eps: float = 1e-6, residual=None, want_y: bool = True, w
         y, h = (r, None) if residual is None else r
         return dict(h=h, y=y, y8=None, scale=None)
     make = _maker(index)
+    given = []
     if residual is not None:
         if h is None:
             h = make((T, n), (n, 1), x.dtype)
         else:
             hs = _like(h, "h", shape, x, index)
+            _refuse_graph(h, "h")
+            given.append(h)
     y = y8 = scale = ph = py = pq = ps = None
     if want_y:
         if out is None:
@@ -148,6 +151,8 @@ def rms_norm(x, weight, eps: float = 1e-6, residual=None, want_y: bool = True, w
         else:
             y = out
             ys = _like(out, "out", shape, x, index)
+            _refuse_graph(out, "out")
+            given.append(out)
         py = y.data_ptr()
     if want_y8:
         y8 = make((T, n), (n, 1), _E4M3)
@@ -157,6 +162,8 @@ def rms_norm(x, weight, eps: float = 1e-6, residual=None, want_y: bool = True, w
         ph = h.data_ptr()
     _call(_lib().exl3_rms_norm, index, x.data_ptr(), _DT[x.dtype], T, n, xs, None if residual is None else residual.data_ptr(),
           rs, pw, wdt, eps, ph, hs, py, ys, pq, ps, _stream(index))
+    if given:
+        _overwritten(given)
     return dict(h=h, y=y, y8=y8, scale=scale)
 
 
@@ -177,10 +184,12 @@ def rms_norm_backward(dy, h, weight, eps: float = 1e-6, dh=None, want_dweight: b
     if _forward():
         _refuse_tangents(dy=dy, h=h, weight=weight, dh=dh)
     make = _maker(index)
-    if dx is None:
-        dx = make((T, n), (n, 1), dy.dtype)
-    else:
+    given = dx is not None
+    if given:
         xs = _like(dx, "dx", shape, dy, index)
+        _refuse_graph(dx, "dx")
+    else:
+        dx = make((T, n), (n, 1), dy.dtype)
     L = _lib()
     dw = pd = pws = None
     bytes_ = 0
@@ -190,6 +199,8 @@ def rms_norm_backward(dy, h, weight, eps: float = 1e-6, dh=None, want_dweight: b
         pd, pws, bytes_ = dw.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size()
     _call(L.exl3_rms_norm_backward, index, dy.data_ptr(), gs, h.data_ptr(), hs, _DT[dy.dtype], T, n, pw, wdt, eps,
           None if dh is None else dh.data_ptr(), ds, dx.data_ptr(), xs, pd, pws, bytes_, _stream(index))
+    if given:
+        _overwritten(dx)
     return dict(dx=dx, dweight=dw)
 
 
@@ -283,19 +294,23 @@ def linear8(x, w, w_scale, x_scale=None, transposed: bool = False, dtype=None, o
             raise ValueError("out does not go with inputs that want a gradient (torch.no_grad() lets it)")
         return _Linear8.apply(x, w, w_scale, transposed, dtype, ws)
     make = _maker(index)
-    if out is None:
-        out = make((T, n_out), (n_out, 1), dtype)
-        ys = n_out
-    else:
+    given = out is not None
+    if given:
         ys = _matrix(out, "out", (dtype,), n_out)
         if out.shape[0] != T or out.get_device() != index:
             raise ValueError("out must have the tokens and device of x")
+        _refuse_graph(out, "out")
+    else:
+        out = make((T, n_out), (n_out, 1), dtype)
+        ys = n_out
     pb, nb = None, 0
     if not coded:
         ws = _ws(L.exl3_linear8_workspace_bytes(T, rows, cols, tr), x.device, ws, make)
         pb, nb = ws.data_ptr(), ws.numel() * ws.element_size()
     _call(L.exl3_linear8, index, x.data_ptr(), xdt, T, xs, ps, st, sb, pw, pws, rows, cols, tr, out.data_ptr(), _DT[dtype],
           ys, pb, nb, _stream(index))
+    if given:
+        _overwritten(out)
     return out
 
 
@@ -366,14 +381,18 @@ def expert_layer(x, gate, up, down, K: int, top_k: int, router=None, ids=None, w
                        (weights is not None and weights.requires_grad)):
         raise ValueError("there is no gradient through an expert layer (torch.no_grad() lets it; expert_linear has one)")
     make = _maker(index)
-    if out is None:
+    given = out is not None
+    if given:
+        ys = _activations(out, "out", H, like=x)
+        _refuse_graph(out, "out")
+    else:
         out = make((T, H), (H, 1), x.dtype)
         ys = H
-    else:
-        ys = _activations(out, "out", H, like=x)
     L = _lib()
     ws = _ws(L.exl3_expert_layer_workspace_bytes(T, H, F, E, top_k), x.device, ws, make)
     _call(L.exl3_expert_layer, index, x.data_ptr(), _DT[x.dtype], T, xs, pr, rdt, pi, pw, top_k, 1 if normalize else 0, E,
           _Experts(*at), H, F, K, kd, 1 if transposed else 0, out.data_ptr(), ys, ws.data_ptr(),
           ws.numel() * ws.element_size(), _stream(index))
+    if given:
+        _overwritten(out)
     return out

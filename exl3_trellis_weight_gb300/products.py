@@ -144,6 +144,17 @@ def _refuse_lost(out, **constants):
         raise ValueError("out does not go with inputs that want a gradient (torch.no_grad() lets it)")
 
 
+# Results go to addresses, which autograd does not see: a tensor given for one may not be part of a
+# graph of gradients (as with torch's own out=), and behind the call its version says that it was
+# overwritten, so that a backward pass that had saved it raises.
+_overwritten = torch.autograd.graph.increment_version
+
+
+def _refuse_graph(t, name):
+    if t.requires_grad and _grad_on():
+        raise ValueError(f"{name} wants a gradient, which would be lost (detach it, or torch.no_grad() lets it)")
+
+
 # whether forward-mode derivatives are on their way at all (a private name of torch's, read so
 # that a call outside of them pays nothing; without it every tensor is asked)
 def _forward():
@@ -220,16 +231,20 @@ def linear(x, codes, su, sv, K: int, scale, transposed: bool = False, A=None, B=
                        (n and (A.requires_grad or B.requires_grad or gain.requires_grad))):
         _refuse_lost(out, su=su, sv=sv, scale=scale_, gain=gain)
         return _Linear.apply(x, A, B, codes, su, sv, K, scale_, transposed, gain, slots, ranks, ws)
-    if out is None:
+    given = out is not None
+    if given:
+        ys = _activations(out, "out", n_out, like=x)
+        _refuse_graph(out, "out")
+    else:
         out = torch.empty(T, n_out, dtype=x.dtype, device=dev)
         ys = n_out
-    else:
-        ys = _activations(out, "out", n_out, like=x)
     L = _lib()
     tr = 1 if transposed else 0
     ws = _ws(L.exl3_linear_workspace_bytes(T, rows, cols, tr, n, r), dev, ws)
     _call(L.exl3_linear, dev.index, x.data_ptr(), _DT[x.dtype], T, xs, pc, rows, cols, K, pu, pv, ps, tr, pA, pB, pg,
           pslots, pranks, n, r, out.data_ptr(), ys, ws.data_ptr(), ws.numel() * ws.element_size(), _stream(dev.index))
+    if given:
+        _overwritten(out)
     return out
 
 
@@ -254,17 +269,21 @@ def linear_backward(dy, x, codes, su, sv, K: int, scale, transposed: bool = Fals
         px = x.data_ptr()
     dA = torch.empty_like(A) if n else None
     dB = torch.empty_like(B) if n else None
-    if dx is None:
+    given = dx is not None
+    if given:
+        dxs = _activations(dx, "dx", n_in, like=dy)
+        _refuse_graph(dx, "dx")
+    else:
         dx = torch.empty(T, n_in, dtype=dy.dtype, device=dev)
         dxs = n_in
-    else:
-        dxs = _activations(dx, "dx", n_in, like=dy)
     L = _lib()
     tr = 1 if transposed else 0
     ws = _ws(L.exl3_linear_backward_workspace_bytes(T, rows, cols, tr, n, r), dev, ws)
     _call(L.exl3_linear_backward, dev.index, dy.data_ptr(), dys, px, xs, _DT[dy.dtype], T, pc, rows, cols, K, pu, pv,
           ps, tr, pA, pB, pg, pslots, pranks, n, r, dx.data_ptr(), dxs, dA.data_ptr() if n else None,
           dB.data_ptr() if n else None, ws.data_ptr(), ws.numel() * ws.element_size(), _stream(dev.index))
+    if given:
+        _overwritten(dx)
     return dict(dx=dx, dA=dA, dB=dB)
 
 
@@ -289,14 +308,18 @@ def expert_linear(x, offsets, codes, su, sv, K: int, scale, transposed: bool = F
     if _grad_on() and (x.requires_grad or su.requires_grad or sv.requires_grad or scale_.requires_grad):
         _refuse_lost(out, su=su, sv=sv, scale=scale_)
         return _ExpertLinear.apply(x, offsets, codes, su, sv, K, scale_, transposed, ws)
-    if out is None:
+    given = out is not None
+    if given:
+        ys = _activations(out, "out", n_out, like=x)
+        _refuse_graph(out, "out")
+    else:
         out = torch.empty(T, n_out, dtype=x.dtype, device=dev)
         ys = n_out
-    else:
-        ys = _activations(out, "out", n_out, like=x)
     L = _lib()
     tr = 1 if transposed else 0
     ws = _ws(L.exl3_expert_linear_workspace_bytes(T, rows, cols, tr), dev, ws)
     _call(L.exl3_expert_linear, dev.index, x.data_ptr(), _DT[x.dtype], T, xs, po, E, pc, rows, cols, K, pu, pv, ps, tr,
           out.data_ptr(), ys, ws.data_ptr(), ws.numel() * ws.element_size(), _stream(dev.index))
+    if given:
+        _overwritten(out)
     return out

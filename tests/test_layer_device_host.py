@@ -201,3 +201,57 @@ def test_refuses_what_would_lose_a_tangent(layer):
         call(t)
         assert len(layer.seen) == 2
         layer.seen.clear()
+
+
+def outputs(layer):
+    """Each call with a tensor given for a result: (call, a tensor that it may be)."""
+    from exl3_trellis_weight_gb300 import products
+    v = tensors(Placed)
+    one, grouped = dict(zip(("codes", "su", "sv", "scale"), (t[0] for t in v["up"]))), dict(zip(("codes", "su", "sv", "scale"), v["up"]))
+    narrow, wide, ws = placed(2, 128, dtype=BF16), placed(2, 256, dtype=BF16), v["ws"]
+    offsets = placed(4, dtype=torch.int32)
+    return {"norm h": (lambda t: layer.rms_norm(v["x"], v["w"], residual=v["r"], h=t), wide),
+            "norm out": (lambda t: layer.rms_norm(v["x"], v["w"], residual=v["r"], out=t), wide),
+            "norm gradient dx": (lambda t: layer.rms_norm_backward(v["x"], v["r"], v["w"], dx=t, ws=ws), wide),
+            "8-bit product": (lambda t: layer.linear8(v["x"], v["w8"], v["s8"], out=t, ws=ws), narrow),
+            "experts": (lambda t: layer.expert_layer(v["x"], v["up"], v["up"], v["down"], 2, 1, router=v["router"], out=t, ws=ws), wide),
+            "linear": (lambda t: products.linear(v["x"], K=2, out=t, ws=ws, **one), narrow),
+            "linear gradient dx": (lambda t: products.linear_backward(narrow, None, K=2, dx=t, ws=ws, **one), wide),
+            "grouped": (lambda t: products.expert_linear(v["x"], offsets, K=2, out=t, ws=ws, **grouped), narrow)}
+
+
+@pytest.mark.parametrize("name", ["norm h", "norm out", "norm gradient dx", "8-bit product", "experts", "linear", "linear gradient dx", "grouped"])
+def test_autograd_hears_of_what_is_overwritten(layer, name):
+    call, like = outputs(layer)[name]
+    t = like.clone().as_subclass(Placed)
+    before = t._version
+    call(t)
+    assert t._version > before and len(layer.seen) == 1
+    # a backward pass that had saved it, or what it is a part of, raises
+    whole = torch.ones(like.shape[0], like.shape[1] + 8, dtype=BF16)
+    leaf = torch.ones_like(whole).requires_grad_()
+    loss = (leaf * whole).sum()
+    call(whole[:, :like.shape[1]].as_subclass(Placed))
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    # as an inference tensor it has no version, and needs none
+    with torch.inference_mode():
+        call(like.clone().as_subclass(Placed))
+    # part of a graph itself: refused, unless nobody wants gradients
+    layer.seen.clear()
+    bad = like.clone().as_subclass(Placed).requires_grad_()
+    with pytest.raises(ValueError, match="gradient"):
+        call(bad)
+    assert not layer.seen
+    with torch.no_grad():
+        call(bad)
+    assert len(layer.seen) == 1
+
+
+def test_a_refused_call_leaves_versions_alone(layer):
+    v = tensors(Placed)
+    t = placed(2, 256, dtype=BF16)
+    before = t._version
+    with pytest.raises(ValueError):
+        layer.rms_norm(v["x"], v["w"], residual=v["r"], h=t, out=placed(3, 256, dtype=BF16))
+    assert t._version == before
