@@ -1,6 +1,6 @@
 // expert_down.cu -- the last product of an expert layer and the sum over a token's experts.
 //
-// A step is 128 outputs and 128 inputs, half of them for each eight warps.  The inputs come
+// A step is 128 outputs and 128 inputs, and a set of eight warps takes it whole.  The inputs come
 // in binary16 under a power of two for each 128, so that a step's products are added to the
 // others under it.  A pair's part of the result goes to memory in binary32, and a small
 // kernel behind adds a token's up in the order of the picks.  (The warp that finished a

@@ -104,7 +104,9 @@ __device__ __forceinline__ int add_in(int32_t *at, int n) {
     return was;
 }
 
-constexpr int kTable = 128;                // tiles that a block keeps the places of
+// tiles that a block keeps the places of: all of them, or those of its share.  There are 1536 at
+// most (4096 pairs, 1024 experts), so that a share has part of 13 on 152 SMs, and of 128 on 13.
+constexpr int kTable = 128;
 
 // One block's share of the list.  `op` has
 //   codes(matrix, e, f0): the first code of expert e's outputs f0 on

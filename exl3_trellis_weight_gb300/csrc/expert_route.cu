@@ -32,6 +32,8 @@ template <typename T, bool VEC> __device__ __forceinline__ void load_router(cons
     }
 }
 
+// (the whole layer with 2, 4 and 8 warps, 64 experts 2048 / 1024: one token 39.3, 39.2 and 38.9 us, 8
+// tokens 98.9, 97.7 and 96.5, 128 tokens 206.7, 207.3 and 208.1)
 constexpr int kLogitWarps = 4;
 
 template <typename T, bool VEC> __global__ void __launch_bounds__(kLogitWarps * 32) logits_kernel(const ExpertLaunch a) {
@@ -86,7 +88,10 @@ __device__ __forceinline__ uint32_t order_of(float v) {
 
 __device__ __forceinline__ float value_of(uint32_t k) { return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k); }
 
-// (threads of the plan; a few pairs are planned by fewer, whose barriers take less)
+// (threads of the plan; a few pairs are planned by fewer, whose barriers take less.  The whole layer,
+// us, 256 threads and 1024: one token's 8 pairs 39.2 and 39.2, 7 tokens' 14 33.9 and 34.2, but 64
+// tokens' 128 35.1 and 31.3, 32 tokens' 256 145.1 and 141.6 - a warp picks for a token at a time -
+// 512 163.5 and 156.4, 1024 221.9 and 207.2)
 constexpr int kPlanThreads = 1024, kPlanFew = 256;
 
 // shared memory behind the counts: ids and, one after the other, the warps' keys

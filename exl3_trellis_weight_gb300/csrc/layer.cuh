@@ -131,6 +131,11 @@ __host__ __device__ inline int64_t expert_tiles(int64_t T, int top_k, int E, int
 // is shared, so that costs a tenth of the time.
 template <typename T> constexpr bool kTwoParts = false;
 template <> constexpr bool kTwoParts<__half> = true;
+// Rows of a tile, by the pairs that an expert has on average: larger tiles decode codes less often,
+// and each 8 rows cost a matrix instruction for 16 x 16 of them.  64 experts 2048 / 1024, 8 picks, K = 2,
+// us, 8 and 16 rows: 16 tokens 125 and 129, 32 tokens 143 and 146 (there the rule's borders are);
+// 16 and 32 rows: 64 tokens 160 and 169, 128 tokens 228 and 209, 256 tokens 380 and 312.  (32 rows in
+// two parts are not built: their inputs are as large as those of 64.)
 inline int expert_tile_n(int64_t T, int top_k, int E, bool two_parts) {
     return T <= 8 || T * top_k <= 4 * (int64_t)E ? 8 : T <= 16 || two_parts || T * top_k <= 10 * (int64_t)E ? 16 : 32;
 }

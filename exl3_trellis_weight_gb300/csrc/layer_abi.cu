@@ -62,6 +62,13 @@ struct Linear8Ws {
     }
 };
 
+// Up to 256 tokens.  A call, and the same of router, sort, three exl3_expert_linear and the sum (in
+// brackets the three products alone), replayed graphs, us, 64 experts 2048 / 1024, 8 picks, K = 2:
+//   tokens      64               128              192              256
+//   bfloat16    156 / 284 (196)  206 / 305 (208)  241 / 324 (215)  306 / 339 (219)
+//   float16     184 / 281 (194)  261 / 303 (205)  344 / 324 (216)  434 / 339 (220)
+// (K = 4: 172, 225, 263 and 331; 203, 287, 380 and 479.)  In float16 the parts are faster from about 170
+// tokens on here, where an expert has 20 rows; with more experts it is later.
 constexpr int kMaxPicks = 32;
 constexpr int64_t kMaxLayerTokens = 256, kMaxPairs = 4096, kMaxLayerSide = 32768;
 

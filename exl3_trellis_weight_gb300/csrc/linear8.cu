@@ -16,9 +16,12 @@
 // Warps: accumulators to registers (four for each half of the columns), one that copies
 // tiles, one that issues the matrix instructions, one that multiplies the scales of steps
 // ahead.  (When the warps with the accumulators fetched the scales themselves, a step ahead, and
-// each thread stored its row, 4096 tokens x 4096 x 12288 took 236 us, 41 of it waiting for
-// scales and 55 storing; now 181, 2270 TFLOP/s, where the way out of tensor memory after each step
-// is what the others wait for.)  One token: 14 us, 7.4 for the bytes at a copy's rate.
+// each thread stored its row, 4096 tokens x 4096 x 12288 took 236 us; now 181 to 191, 2160 to 2280
+// TFLOP/s, and 183 with W the other way round.  The tensor pipe is busy for half of the time, the issue
+// slots are not the limit: the steps wait for the result warps, which take each accumulator out of
+// tensor memory 16 columns at a time and store their rows between tiles.  Whether tensor memory's
+// rate or that order bounds them is not known.)  One token: 14 us, 7.4 for the bytes at a copy's
+// rate.
 #include "layer.cuh"
 #include "linear_rotate.cuh"
 #include "tc.cuh"
@@ -523,7 +526,10 @@ template <int TN, bool SWAP, bool MN> exl3_status launch_form8(const Linear8Laun
     a.tiles_t = (a.T + kRowsT - 1) / kRowsT;
     a.tiles_f = (a.n_out + kRowsF - 1) / kRowsF;
     const int64_t tiles = (int64_t)a.tiles_t * a.tiles_f, slots = SWAP ? 2 * sms : sms;
-    // blocks that would idle share the inputs of the tiles, two steps each at least
+    // blocks that would idle share the inputs of the tiles, two steps each at least (one or four at
+    // least are as fast: 512 -> 512 7.2, 6.7 and 6.7 us).  One token, replayed graphs, us, not split
+    // and 2, 4, 8 blocks to a tile, the rule's choice in brackets: 4096 -> 12288 17.8 (16.3) 15.8 18.5;
+    // 4096 -> 4096 13.3 10.8 8.8 (9.7); 12288 -> 4096 34.6 22.6 16.8 (15.5); 4096 -> 1024 12.7 10.3 8.2 (8.2)
     a.split = 1;
     while (a.split < 8 && tiles * a.split * 2 <= slots && a.blocks_k >= a.split * 4)
         a.split *= 2;

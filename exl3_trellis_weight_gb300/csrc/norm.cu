@@ -9,7 +9,9 @@
 // in half a warp.  A warp's unit is 256 neighbouring columns: lane l has columns 8l .. 8l + 7
 // of it where rows allow 16-byte accesses (kWide), pairs 2l + 64i where they are whole pairs, and
 // columns l, l + 32, ... where they are not, so that a warp's accesses are whole sectors
-// each way.  16384 x 4096 with a residual: 83 us, 6.4 TB/s (a copy: 6.8); one row: 5 us.
+// each way.  16384 x 4096 with a residual: 83 us, 6.4 TB/s (a copy: 6.8); one row: 5 us.  A row of
+// up to 256 columns is one warp with one load of each array on its way, and below that some of its lanes
+// load nothing: 131072 x 256 48 us (2.8 TB/s), 262144 x 128 85 (1.6).  8192 rows of 4096, 4098 and 4097 columns with a residual: 46, 54 and 84 us.
 #include "layer.cuh"
 #include "tc.cuh"
 
@@ -355,8 +357,9 @@ template <typename T> __device__ __forceinline__ void unpack_pairs(const Eight &
 // beyond, where registers run out.
 // RING: whole rows are copied into stages of shared memory, `depth` of them ahead.  (One row
 // ahead in registers were 48 KB to an SM on their way: 8192 x 4096 took 66 us, 4.1 TB/s; now
-// 52, 5.2 TB/s, and 5 for the sum of dweight's parts, whose launch overlaps.  What is left
-// are the two meetings of a row's warps.)
+// 52, 5.2 TB/s, and 5 for the sum of dweight's parts, whose launch overlaps.  In what is left a
+// row's wait for its copy, its sums, the meeting of its warps and its results follow one another,
+// with 16 warps to an SM to fill the gaps.)
 // WAY: the next row is asked for into registers.
 __device__ unsigned int g_norm_timeouts;
 constexpr int kMaxDepth = 8;
@@ -646,7 +649,10 @@ template <typename T, int VEC> __device__ __forceinline__ void load_values(const
 }
 
 // 1 x 128: a warp takes four units, one behind the other.  1001 x 12288: 10 us, of which 4 are any
-// kernel's ends and 5.5 the bytes at a copy's rate.
+// kernel's ends and 5.5 the bytes at a copy's rate; it runs in two and a half rounds of blocks, whose
+// 63 registers a thread (values in binary32) leave room for four to an SM.  Replayed graphs with 1, 2,
+// 4 and 8 units a warp: 8192 x 4096 26.7, 26.2, 24.7 and 30.2 us; 1001 x 12288 13.4, 13.1, 13.2 and 16.5;
+// 333 x 2000 4.1, 4.6, 5.1 and 6.2.
 constexpr int kUnitsWarp = 4;
 template <typename T, int VEC> __global__ void __launch_bounds__(256) rows8_kernel(const Quantize8Launch a) {
     // (a product behind this launch may load its weights; it waits for this kernel's end
